@@ -64,6 +64,7 @@ typedef enum {
 #define TRI_DEV_TIMEOUT 4         /* a bounded in-kernel wait gave up (~2 s)      */
 #define TRI_DEV_GROUP_NVALID 5    /* slices sharing a keep list differ in n_valid */
 #define TRI_DEV_BAD_BLOCK 6       /* a block table entry is outside [0, num_blocks) */
+#define TRI_DEV_BAD_QUERY 7       /* a sequence's n_new is outside [0, n_q]       */
 
 typedef enum { TRI_F32 = 0, TRI_BF16 = 1 } tri_dtype;
 
@@ -381,6 +382,83 @@ size_t tri_select_union_workspace_bytes(const tri_kv* kv, int32_t n_prompt, int3
 tri_status tri_select_union(const float* scores, const tri_kv* kv, int32_t n_prompt, int32_t n_recent,
                             int32_t budget, int32_t k_head, int32_t* keep_idx, float* final_scores, void* ws,
                             size_t ws_bytes, tri_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention over the cache, and eviction by the weight it gives.
+ * (The pages have no counterpart for these calls: they are the model's own use
+ * of the caches this library compresses.)
+ *
+ * A call covers one layer (`layer`) of every sequence. A sequence's n_new new
+ * tokens are the newest rows of its slices: their keys and values are in the
+ * cache already, and the query of token i sits at row r = n_valid - n_new + i
+ * of each slice of the layer (row counts may differ between heads, as they do
+ * after a per-head eviction). It sees row j when
+ *   j <= r and (window == 0, or j < n_sink, or j > r - window):
+ * everything before it, or the first n_sink rows and the newest `window`. With
+ * x_j = scale * (q . k_j) over the rows it sees,
+ *   lse = log sum_j e^(x_j),  out = sum_j e^(x_j - lse) v_j;
+ * a query that sees nothing (an empty slice, r < 0) gets out = 0, lse = -inf.
+ * Query head h * group + g reads KV head h. Rows a query does not see may hold
+ * anything, NaN and infinities included, except that V rows below n_valid
+ * must be finite for tri_attn_prefill (a weight of 0 multiplies them there).
+ *
+ * Keys are taken as cached, so they must be TRI_KEYS_POST_ROPE and q rotated
+ * in the same way (TRI_ERR_UNSUPPORTED otherwise). Sums, maxima and lse are
+ * fp32. Every result is deterministic.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  const void* q;         /* device [n_seq][n_q][n_kv_heads * group][head_dim] of the cache's
+                            type, 16-byte aligned; a token's heads are contiguous     */
+  int64_t seq_stride;    /* elements between sequences, and between tokens; x element */
+  int64_t token_stride;  /* size a multiple of 16 bytes                               */
+  const int32_t* n_new;  /* device [n_seq]: tokens of each sequence, 0 .. n_q, or NULL:
+                            n_q each. Outputs of tokens >= n_new are left as they were */
+  int32_t n_q;           /* tokens a sequence may have in this call, >= 1             */
+  int32_t group;         /* query heads per KV head, 1 .. 8                           */
+  int32_t layer;
+  int32_t n_sink;        /* first rows that stay visible next to a window, >= 0       */
+  int32_t window;        /* newest rows a query sees, its own included; 0: all rows   */
+  float scale;           /* > 0 and finite; usually head_dim^-1/2                     */
+} tri_queries;
+
+/* tri_attn_decode -- one new token per sequence (q->n_q == 1).
+ * out: device [n_seq][n_kv_heads * group][head_dim] of the cache's type, 16-byte
+ * aligned. lse: optional device [n_seq][n_kv_heads * group] fp32. mass:
+ * optional device [n_slices][n_cap] fp32 (all the cache's slices): the weight
+ * e^(x_j - lse) of every row a query sees is added to mass[slice][j], summed
+ * over the group's heads -- the accumulated attention weight tri_mass_evict
+ * ranks by; other entries are left as they were. ws: device scratch of
+ * tri_attn_decode_workspace_bytes(kv, group, mass != NULL) bytes, 16-byte
+ * aligned, no initial contents needed; calls that may overlap need one each.
+ * A slice with a fault (row count, block table, n_new) is skipped. */
+size_t tri_attn_decode_workspace_bytes(const tri_kv* kv, int32_t group, int32_t with_mass);
+tri_status tri_attn_decode(const tri_kv* kv, const tri_queries* q, void* out, float* lse, float* mass, void* ws,
+                           size_t ws_bytes, tri_stream_t stream);
+
+/* tri_attn_prefill -- a chunk of new tokens (a prompt, or the next part of
+ * one). out: device [n_seq][n_q][n_kv_heads * group][head_dim] of the cache's
+ * type, 16-byte aligned; lse: optional device [n_seq][n_q][n_kv_heads * group]
+ * fp32. bf16 caches: the weights are rounded to bf16 for their product with V
+ * (their sum is not). */
+tri_status tri_attn_prefill(const tri_kv* kv, const tri_queries* q, void* out, float* lse, tri_stream_t stream);
+
+/* tri_attn_mass -- the accumulated weight of every row under a chunk of
+ * queries: mass[slice][j] += sum over the tokens and the group's heads that see
+ * row j of e^(x_j - lse). lse: device fp32 as tri_attn_prefill wrote it,
+ * [n_seq][n_q][n_kv_heads * group] with lse_seq_stride elements between
+ * sequences (so q and lse may be the last n_q tokens of a longer chunk: an
+ * observation window). Rows nobody sees are left as they were. */
+tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* lse, int64_t lse_seq_stride, float* mass,
+                         tri_stream_t stream);
+
+/* tri_mass_evict -- eviction by accumulated weight: exactly tri_select_compact
+ * with scores = mass, and the masses moved with their rows: for j < n_keep,
+ * mass_out[s][j] <- mass[s][keep[j]], and the freed rows n_keep <= j < n_valid
+ * (the count before the call) get mass_out[s][j] = 0, so that rows cached there
+ * later start from nothing. mass, mass_out: device [n_slices][n_cap] fp32;
+ * mass_out may equal mass. kv->pos_out required. */
+tri_status tri_mass_evict(const float* mass, float* mass_out, const tri_kv* kv, int32_t n_prompt, int32_t n_recent,
+                          int32_t budget, int32_t* keep_idx, tri_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * tri_paged_blocks_used -- after a compaction of a paged cache: the blocks

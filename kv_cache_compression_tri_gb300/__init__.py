@@ -24,14 +24,15 @@ __all__ = [
     "compress", "compress_workspace_bytes", "score_heads", "score_heads_workspace_bytes",
     "select_topk_zmax", "select_union", "select_union_workspace_bytes", "rand_evict_scoped", "DRAW_PER_HEAD", "DRAW_PER_LAYER", "DRAW_PER_SEQUENCE",
     "launch_count", "ROPE_INTERLEAVED", "ROPE_HALF", "NORM_WEIGHTED", "NORM_UNWEIGHTED",
-    "DEV_OK", "DEV_NVALID_OVER_CAP", "DEV_NAN_SCORE", "DEV_BAD_KEEP",
+    "DEV_OK", "DEV_NVALID_OVER_CAP", "DEV_NAN_SCORE", "DEV_BAD_KEEP", "DEV_BAD_QUERY",
+    "attn_decode", "attn_decode_workspace_bytes", "attn_prefill", "attn_mass", "mass_evict",
 ]
 
 ROPE_INTERLEAVED, ROPE_HALF = 0, 1
 NORM_WEIGHTED, NORM_UNWEIGHTED = 0, 1
 F32, BF16 = 0, 1
-DEV_OK, DEV_NVALID_OVER_CAP, DEV_NAN_SCORE, DEV_BAD_KEEP, DEV_TIMEOUT, DEV_GROUP_NVALID, DEV_BAD_BLOCK = (
-    0, 1, 2, 3, 4, 5, 6)
+(DEV_OK, DEV_NVALID_OVER_CAP, DEV_NAN_SCORE, DEV_BAD_KEEP, DEV_TIMEOUT, DEV_GROUP_NVALID, DEV_BAD_BLOCK,
+ DEV_BAD_QUERY) = (0, 1, 2, 3, 4, 5, 6, 7)
 
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -58,6 +59,15 @@ class _TriKV(ctypes.Structure):
 class _TriCenters(ctypes.Structure):
     _fields_ = [("center", ctypes.c_void_p), ("mean_norm", ctypes.c_void_p),
                 ("mrl", ctypes.c_void_p)]
+
+
+class _TriQueries(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("seq_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+        ("n_new", ctypes.c_void_p), ("n_q", ctypes.c_int32), ("group", ctypes.c_int32),
+        ("layer", ctypes.c_int32), ("n_sink", ctypes.c_int32), ("window", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
 
 
 _lock = threading.Lock()
@@ -120,6 +130,17 @@ def load_library():
         lib.tri_select_compact.restype = ctypes.c_int
         lib.rand_evict_compact.argtypes = [kvp, u64, u32, ctypes.c_int, i32, i32, i32, vp, vp]
         lib.rand_evict_compact.restype = ctypes.c_int
+        qp = ctypes.POINTER(_TriQueries)
+        lib.tri_attn_decode_workspace_bytes.argtypes = [kvp, i32, i32]
+        lib.tri_attn_decode_workspace_bytes.restype = ctypes.c_size_t
+        lib.tri_attn_decode.argtypes = [kvp, qp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+        lib.tri_attn_decode.restype = ctypes.c_int
+        lib.tri_attn_prefill.argtypes = [kvp, qp, vp, vp, vp]
+        lib.tri_attn_prefill.restype = ctypes.c_int
+        lib.tri_attn_mass.argtypes = [kvp, qp, vp, i64, vp, vp]
+        lib.tri_attn_mass.restype = ctypes.c_int
+        lib.tri_mass_evict.argtypes = [vp, vp, kvp, i32, i32, i32, vp, vp]
+        lib.tri_mass_evict.restype = ctypes.c_int
         lib.tri_paged_blocks_used.argtypes = [kvp, vp, vp]
         lib.tri_paged_blocks_used.restype = ctypes.c_int
         lib.tri_selftest_wait_timeout.argtypes = [vp, u64, vp]
@@ -493,4 +514,106 @@ def select_union(scores: torch.Tensor, kv: KVCache, n_prompt: int, n_recent: int
     _check("tri_select_union", lib.tri_select_union(
         scores.data_ptr(), ctypes.byref(kvs), n_prompt, n_recent, budget, k_head, keep.data_ptr(),
         _ptr(final_scores), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return keep
+
+
+def _queries(kv, layer: int, q: torch.Tensor, n_new: torch.Tensor | None, scale: float | None, n_sink: int,
+             window: int) -> _TriQueries:
+    """q [n_seq, n_q, Hq, d] (any sequence and token strides) of the cache's type."""
+    n_seq, n_q, Hq, d = q.shape
+    H = kv.k.shape[2]
+    assert q.is_cuda and q.dtype == kv.k.dtype and d == kv.k.shape[4] and Hq % H == 0
+    assert q.stride(3) == 1 and (q.stride(2) == d or Hq == 1)
+    assert n_seq == (kv.n_seq if isinstance(kv, PagedKVCache) else kv.k.shape[0])
+    if n_new is not None:
+        assert n_new.is_cuda and n_new.dtype == torch.int32 and n_new.is_contiguous() and n_new.numel() == n_seq
+    return _TriQueries(q.data_ptr(), q.stride(0), q.stride(1), _ptr(n_new), n_q, Hq // H, layer, n_sink, window,
+                       d ** -0.5 if scale is None else scale)
+
+
+def _check_mass(kv, mass: torch.Tensor):
+    assert mass.is_cuda and mass.dtype == torch.float32 and mass.is_contiguous()
+    assert mass.numel() == kv.n_slices * kv.n_cap
+
+
+def attn_decode_workspace_bytes(kv, group: int, with_mass: bool = False) -> int:
+    kvs = kv._abi()
+    return int(load_library().tri_attn_decode_workspace_bytes(ctypes.byref(kvs), group, int(with_mass)))
+
+
+def attn_decode(kv, layer: int, q: torch.Tensor, out: torch.Tensor, n_new: torch.Tensor | None = None,
+                scale: float | None = None, n_sink: int = 0, window: int = 0, lse: torch.Tensor | None = None,
+                mass: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence, q [n_seq, Hq, d], over one layer
+    of a post-RoPE cache that already holds the token's row (tri_attn_decode):
+    out [n_seq, Hq, d]; lse [n_seq, Hq] fp32; mass [S, n_cap] fp32 gets every
+    row's weight added. window > 0: the first n_sink and newest `window` rows
+    only. n_new [n_seq] int32: 0 leaves a sequence out. scale: d ** -0.5."""
+    lib = load_library()
+    qs = _queries(kv, layer, q.unsqueeze(1), n_new, scale, n_sink, window)
+    assert out.is_cuda and out.is_contiguous() and out.shape == q.shape and out.dtype == q.dtype
+    if lse is not None:
+        assert lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == q.shape[0] * q.shape[1]
+    if mass is not None:
+        _check_mass(kv, mass)
+    kvs = kv._abi()
+    if workspace is None:
+        need = int(lib.tri_attn_decode_workspace_bytes(ctypes.byref(kvs), qs.group, int(mass is not None)))
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=kv.device)
+    assert workspace.is_cuda and workspace.is_contiguous()
+    _check("tri_attn_decode", lib.tri_attn_decode(ctypes.byref(kvs), ctypes.byref(qs), out.data_ptr(), _ptr(lse),
+                                                  _ptr(mass), workspace.data_ptr(),
+                                                  workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
+
+
+def attn_prefill(kv, layer: int, q: torch.Tensor, out: torch.Tensor, n_new: torch.Tensor | None = None,
+                 scale: float | None = None, n_sink: int = 0, window: int = 0, lse: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """Causal attention of a chunk of new tokens, q [n_seq, n_q, Hq, d] (any
+    sequence and token strides), over one layer of a post-RoPE cache whose
+    newest rows they are (tri_attn_prefill): out [n_seq, n_q, Hq, d]; lse
+    [n_seq, n_q, Hq] fp32. n_new [n_seq] int32: tokens of each sequence (rows of
+    out past them stay as they were)."""
+    lib = load_library()
+    qs = _queries(kv, layer, q, n_new, scale, n_sink, window)
+    assert out.is_cuda and out.is_contiguous() and out.shape == q.shape and out.dtype == q.dtype
+    if lse is not None:
+        assert lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == q.shape[:3]
+    kvs = kv._abi()
+    _check("tri_attn_prefill", lib.tri_attn_prefill(ctypes.byref(kvs), ctypes.byref(qs), out.data_ptr(), _ptr(lse),
+                                                    _stream(stream)))
+    return out
+
+
+def attn_mass(kv, layer: int, q: torch.Tensor, lse: torch.Tensor, mass: torch.Tensor,
+              n_new: torch.Tensor | None = None, scale: float | None = None, n_sink: int = 0, window: int = 0,
+              stream=None) -> torch.Tensor:
+    """Add to mass [S, n_cap] the weight every cached row of one layer gets from
+    a chunk of queries, q [n_seq, n_q, Hq, d] with their lse [n_seq, n_q, Hq] from
+    attn_prefill (tri_attn_mass). Both may be the last n_q tokens of a longer
+    chunk (q[:, -n:], lse[:, -n:]): an observation window."""
+    lib = load_library()
+    qs = _queries(kv, layer, q, n_new, scale, n_sink, window)
+    assert lse.is_cuda and lse.dtype == torch.float32 and lse.shape == q.shape[:3]
+    assert lse.stride(2) == 1 and (lse.stride(1) == q.shape[2] or q.shape[1] == 1)
+    _check_mass(kv, mass)
+    kvs = kv._abi()
+    _check("tri_attn_mass", lib.tri_attn_mass(ctypes.byref(kvs), ctypes.byref(qs), lse.data_ptr(), lse.stride(0),
+                                              mass.data_ptr(), _stream(stream)))
+    return mass
+
+
+def mass_evict(kv, mass: torch.Tensor, mass_out: torch.Tensor, n_prompt: int, n_recent: int, budget: int,
+               keep: torch.Tensor, stream=None) -> torch.Tensor:
+    """Eviction by accumulated attention weight (tri_mass_evict): select_compact
+    with mass [S, n_cap] as the scores, the masses moved with their rows into
+    mass_out (may be mass), the freed rows' masses set to 0."""
+    lib = load_library()
+    assert keep.dtype == torch.int32 and keep.is_contiguous() and keep.numel() == kv.n_slices * budget
+    _check_mass(kv, mass)
+    _check_mass(kv, mass_out)
+    kvs = kv._abi()
+    _check("tri_mass_evict", lib.tri_mass_evict(mass.data_ptr(), mass_out.data_ptr(), ctypes.byref(kvs), n_prompt,
+                                                n_recent, budget, keep.data_ptr(), _stream(stream)))
     return keep

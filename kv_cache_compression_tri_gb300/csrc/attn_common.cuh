@@ -1,0 +1,85 @@
+// attn_common.cuh -- parameters and row arithmetic shared by the attention
+// kernels (attn_decode.cu, attn_prefill.cu, attn_mass.cu).
+//
+// Rows are counted as the cache holds them: the query of the i-th of n_new
+// new tokens of a sequence sits at row r = n_valid - n_new + i of each of the
+// layer's slices, and sees row j when j <= r and (no window, or j < n_sink, or
+// j > r - window). The visible rows are therefore two runs, [0, s1) and
+// [w0, r], with w0 = max(0, r + 1 - window) and s1 = min(n_sink, w0).
+//
+// Logits are kept in base 2: x = scale * log2(e) * (q . k), so that a weight is
+// one ex2 and the log-sum is ln(2) * (m + log2(l)).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "tri_internal.cuh"
+
+namespace tri {
+
+namespace {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+constexpr float NEG_INF = -__builtin_huge_valf();
+
+// 2^x by the hardware's approximation (relative error about 2^-22; 2^-inf = 0).
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The runs of rows the query at row r sees (none for r < 0).
+struct Visible {
+  int s1;  // rows [0, s1)
+  int w0;  // and [w0, r]
+};
+__device__ __forceinline__ Visible visible_rows(int r, int n_sink, int window) {
+  if (r < 0) return {0, 0};
+  if (window == 0) return {0, 0};
+  const int w0 = max(0, r - window + 1);
+  return {min(n_sink, w0), w0};
+}
+
+// Slice index of (seq, layer, head).
+__device__ __forceinline__ int64_t slice_of(const AttnParams& p, int seq, int head) {
+  return (static_cast<int64_t>(seq) * p.n_layers + p.layer) * p.n_kv_heads + head;
+}
+
+// New tokens of a sequence, or -1 (reported) when the count is malformed.
+__device__ __forceinline__ int new_tokens(const AttnParams& p, int seq) {
+  const int n = p.n_new ? __ldg(p.n_new + seq) : p.n_q;
+  if (n < 0 || n > p.n_q) {
+    set_status(p.dev_status, TRI_DEV_BAD_QUERY);
+    return -1;
+  }
+  return n;
+}
+
+// 16 bytes of a row as fp32.
+__device__ __forceinline__ void widen(const uint4& w, float (&x)[8]) {
+  x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x);
+  x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
+  x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z);
+  x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
+}
+__device__ __forceinline__ void widen(const uint4& w, float (&x)[4]) {
+  x[0] = __uint_as_float(w.x);
+  x[1] = __uint_as_float(w.y);
+  x[2] = __uint_as_float(w.z);
+  x[3] = __uint_as_float(w.w);
+}
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+}  // namespace
+}  // namespace tri

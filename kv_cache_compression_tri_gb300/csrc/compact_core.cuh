@@ -206,12 +206,15 @@ struct CSmem {
 // and V rows through rings of NST tiles, the other warps the positions.
 // RO: the keep list is read-only for the whole kernel (else it was written
 // earlier in the same kernel).
-template <bool PAGED, int NTH, bool RO, int NST = CSTAGES>
+// MASS: the rows' accumulated weights (p.mass) are moved like the positions,
+// and those of the freed rows set to 0.
+template <bool PAGED, int NTH, bool RO, int NST = CSTAGES, bool MASS = false>
 __device__ __forceinline__ void compact_slice(const CompactParams& p, const CompactSmem<NST>& cs, int64_t s) {
   static_assert(NTH >= 128 && NTH % 32 == 0, "compaction CTA");
   __shared__ CSmem sm;
   const int t = threadIdx.x, lane = t & 31;
   const int32_t* keep = p.keep + s * static_cast<int64_t>(p.budget);
+  const int n_old = MASS ? p.n_valid[s] : 0;  // before the last lines set it
 
   if (t == 0) {
     sm.bad = 0;
@@ -322,6 +325,31 @@ __device__ __forceinline__ void compact_slice(const CompactParams& p, const Comp
       }
       asm volatile("bar.sync 1, %0;" ::"n"(PT) : "memory");
     }
+  }
+  if constexpr (MASS) {
+    const float* mass_in = p.mass + s * static_cast<int64_t>(p.n_cap);
+    float* mass_out = p.mass_out + s * static_cast<int64_t>(p.n_cap);
+    if (mass_in != mass_out) {
+      for (int j = pt; j < n_keep; j += PT) mass_out[j] = __ldg(mass_in + keep_at<RO>(keep, j));
+    } else {
+      for (int c0 = first; c0 < n_keep; c0 += PT * POS_PER_THREAD) {
+        float v[POS_PER_THREAD];
+#pragma unroll
+        for (int e = 0; e < POS_PER_THREAD; ++e) {
+          const int j = c0 + e * PT + pt;
+          v[e] = (j < n_keep) ? mass_in[keep_at<RO>(keep, j)] : 0.f;
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(PT) : "memory");
+#pragma unroll
+        for (int e = 0; e < POS_PER_THREAD; ++e) {
+          const int j = c0 + e * PT + pt;
+          if (j < n_keep) mass_out[j] = v[e];
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(PT) : "memory");
+      }
+    }
+    // only rows that were read above or lie past every source are cleared
+    for (int j = n_keep + pt; j < n_old; j += PT) mass_out[j] = 0.f;
   }
   if (pt == 0) p.n_valid[s] = n_keep;
 }

@@ -23,7 +23,7 @@ constexpr size_t fused_smem(bool paged) {
   return c > sizeof(SSmem) ? c : sizeof(SSmem);
 }
 
-template <class Src, bool PAGED>
+template <class Src, bool PAGED, bool MASS>
 __global__ void __launch_bounds__(NT, 3)
     select_compact_kernel(const __grid_constant__ SelectParams ps, const __grid_constant__ CompactParams pc) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -32,13 +32,13 @@ __global__ void __launch_bounds__(NT, 3)
   const int n = ps.n_valid[s];
   __syncthreads();  // the keep list is written; the selection's shared memory is free
   if (n > ps.n_cap || n < 0) return;  // the selection reported it and wrote no list
-  compact_slice<PAGED, NT, false>(pc, CompactSmem<CSTAGES>::packed(smem), s);
+  compact_slice<PAGED, NT, false, CSTAGES, MASS>(pc, CompactSmem<CSTAGES>::packed(smem), s);
 }
 
-template <class Src>
+template <class Src, bool MASS = false>
 cudaError_t launch_src_compact(const SelectParams& ps, const CompactParams& pc, int n_slices, cudaStream_t st) {
   const bool paged = pc.rows.table != nullptr;
-  auto kern = paged ? select_compact_kernel<Src, true> : select_compact_kernel<Src, false>;
+  auto kern = paged ? select_compact_kernel<Src, true, MASS> : select_compact_kernel<Src, false, MASS>;
   const size_t smem = fused_smem(paged);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -54,6 +54,11 @@ cudaError_t launch_select_compact(const SelectParams& ps, const CompactParams& p
   if (pc.row_bytes % 16 != 0 || pc.row_bytes < 128 || pc.row_bytes > CTILE) return cudaErrorInvalidValue;
   return random ? launch_src_compact<DrawKeys>(ps, pc, n_slices, st)
                 : launch_src_compact<ScoreKeys>(ps, pc, n_slices, st);
+}
+
+cudaError_t launch_mass_evict(const SelectParams& ps, const CompactParams& pc, int n_slices, cudaStream_t st) {
+  if (pc.row_bytes % 16 != 0 || pc.row_bytes < 128 || pc.row_bytes > CTILE) return cudaErrorInvalidValue;
+  return launch_src_compact<ScoreKeys, true>(ps, pc, n_slices, st);
 }
 
 }  // namespace tri

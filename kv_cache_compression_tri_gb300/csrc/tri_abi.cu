@@ -589,6 +589,147 @@ tri_status tri_select_union(const float* scores, const tri_kv* kv, int32_t n_pro
   return e == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
 }
 
+}  // extern "C"
+
+namespace tri {
+namespace {
+
+// Checks shared by the attention calls, and their parameter block.
+tri_status prepare_attn(const tri_kv* kv, const tri_queries* q, AttnParams& p) {
+  const tri_status st = check_kv(kv, true);
+  if (st != TRI_OK) return st;
+  if (kv->key_layout != TRI_KEYS_POST_ROPE) return TRI_ERR_UNSUPPORTED;
+  if (!q || !q->q || !aligned(q->q, 16)) return TRI_ERR_INVALID_ARG;
+  if (q->n_q < 1 || q->group < 1 || q->group > MAX_GROUP) return TRI_ERR_INVALID_ARG;
+  if (q->layer < 0 || q->layer >= kv->n_layers) return TRI_ERR_INVALID_ARG;
+  if (q->n_sink < 0 || q->window < 0) return TRI_ERR_INVALID_ARG;
+  if (!(q->scale > 0.f) || !std::isfinite(q->scale)) return TRI_ERR_INVALID_ARG;
+  if (q->n_new && !aligned(q->n_new, 4)) return TRI_ERR_INVALID_ARG;
+  const int e = elem_bytes(kv->dtype);
+  const int64_t token = static_cast<int64_t>(kv->n_kv_heads) * q->group * kv->head_dim;
+  if (q->seq_stride < 0 || (q->seq_stride * e) % 16 != 0 || (q->token_stride * e) % 16 != 0) return TRI_ERR_INVALID_ARG;
+  if (q->n_q > 1 && q->token_stride < token) return TRI_ERR_INVALID_ARG;
+  p = AttnParams{};
+  p.k = kv->k;
+  p.v = kv->v;
+  p.n_valid = kv->n_valid;
+  p.dev_status = kv->dev_status;
+  p.rows = row_map(kv);
+  p.n_cap = kv->n_cap;
+  p.n_seq = kv->n_seq;
+  p.n_layers = kv->n_layers;
+  p.n_kv_heads = kv->n_kv_heads;
+  p.layer = q->layer;
+  p.q = q->q;
+  p.q_seq = q->seq_stride;
+  p.q_token = q->token_stride;
+  p.n_new = q->n_new;
+  p.n_q = q->n_q;
+  p.group = q->group;
+  p.n_sink = q->n_sink;
+  p.window = q->window;
+  p.scale = q->scale;
+  return TRI_OK;
+}
+
+// Rows one new token can see at most: the launch's bound, the row counts being on the device.
+int max_visible(const tri_kv* kv, int32_t n_sink, int32_t window) {
+  if (window == 0) return kv->n_cap;
+  return static_cast<int>(std::min<int64_t>(kv->n_cap, static_cast<int64_t>(n_sink) + window));
+}
+
+// Workspace of tri_attn_decode: the splits' sums [slices][splits][group][d] f32,
+// their (m, l) [slices][splits][group], and for the masses the logits
+// [slices][group][n_cap] f32 (each part 16-byte aligned). A window only
+// shortens the rows, and with them the splits, so the bound is without one.
+struct DecodeWs {
+  size_t ml_off, logits_off, total;
+};
+DecodeWs decode_ws(const tri_kv* kv, int32_t group, int32_t n_split, bool with_mass) {
+  const size_t n = static_cast<size_t>(kv->n_seq) * kv->n_kv_heads;
+  DecodeWs w{};
+  w.ml_off = align16(n * n_split * group * kv->head_dim * sizeof(float));
+  w.logits_off = align16(w.ml_off + n * n_split * group * sizeof(float2));
+  w.total = w.logits_off + (with_mass ? align16(n * group * kv->n_cap * sizeof(float)) : 0);
+  return w;
+}
+
+}  // namespace
+}  // namespace tri
+
+extern "C" {
+
+size_t tri_attn_decode_workspace_bytes(const tri_kv* kv, int32_t group, int32_t with_mass) {
+  if (check_kv(kv, true) != TRI_OK || group < 1 || group > MAX_GROUP) return 0;
+  const int n = kv->n_seq * kv->n_kv_heads;
+  return decode_ws(kv, group, attn_decode_splits(n, kv->n_cap), with_mass != 0).total;
+}
+
+tri_status tri_attn_decode(const tri_kv* kv, const tri_queries* q, void* out, float* lse, float* mass, void* ws,
+                           size_t ws_bytes, tri_stream_t stream) {
+  TRI_CALL_RANGE();
+  AttnParams p;
+  const tri_status st = prepare_attn(kv, q, p);
+  if (st != TRI_OK) return st;
+  if (q->n_q != 1 || !out || !aligned(out, 16)) return TRI_ERR_INVALID_ARG;
+  if ((lse && !aligned(lse, 4)) || (mass && !aligned(mass, 4))) return TRI_ERR_INVALID_ARG;
+  const int n = kv->n_seq * kv->n_kv_heads;
+  p.n_split = attn_decode_splits(n, max_visible(kv, q->n_sink, q->window));
+  const DecodeWs w = decode_ws(kv, q->group, p.n_split, mass != nullptr);
+  if (!ws || !aligned(ws, 16) || ws_bytes < tri_attn_decode_workspace_bytes(kv, q->group, mass != nullptr))
+    return TRI_ERR_INVALID_ARG;
+  char* base = static_cast<char*>(ws);
+  p.part_o = reinterpret_cast<float*>(base);
+  p.part_ml = reinterpret_cast<float2*>(base + w.ml_off);
+  p.logits = mass ? reinterpret_cast<float*>(base + w.logits_off) : nullptr;
+  p.out = out;
+  p.lse = lse;
+  p.mass = mass;
+  return launch_attn_decode(p, kv->dtype, kv->head_dim, stream) == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
+}
+
+tri_status tri_attn_prefill(const tri_kv* kv, const tri_queries* q, void* out, float* lse, tri_stream_t stream) {
+  TRI_CALL_RANGE();
+  AttnParams p;
+  const tri_status st = prepare_attn(kv, q, p);
+  if (st != TRI_OK) return st;
+  if (!out || !aligned(out, 16) || (lse && !aligned(lse, 4))) return TRI_ERR_INVALID_ARG;
+  p.out = out;
+  p.lse = lse;
+  return launch_attn_prefill(p, kv->dtype, kv->head_dim, stream) == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
+}
+
+tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* lse, int64_t lse_seq_stride, float* mass,
+                         tri_stream_t stream) {
+  TRI_CALL_RANGE();
+  AttnParams p;
+  const tri_status st = prepare_attn(kv, q, p);
+  if (st != TRI_OK) return st;
+  if (!lse || !aligned(lse, 4) || !mass || !aligned(mass, 4)) return TRI_ERR_INVALID_ARG;
+  if (lse_seq_stride < 0) return TRI_ERR_INVALID_ARG;
+  p.lse_in = lse;
+  p.lse_seq = lse_seq_stride;
+  p.mass = mass;
+  return launch_attn_mass(p, kv->dtype, kv->head_dim, stream) == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
+}
+
+tri_status tri_mass_evict(const float* mass, float* mass_out, const tri_kv* kv, int32_t n_prompt, int32_t n_recent,
+                          int32_t budget, int32_t* keep_idx, tri_stream_t stream) {
+  TRI_CALL_RANGE();
+  tri_status st = check_kv(kv, true);
+  if (st != TRI_OK) return st;
+  if (!kv->pos_out || !mass || !aligned(mass, 4) || !mass_out || !aligned(mass_out, 4)) return TRI_ERR_INVALID_ARG;
+  if (!keep_idx || !aligned(keep_idx, 4)) return TRI_ERR_INVALID_ARG;
+  st = check_protect(n_prompt, n_recent, budget, kv->n_cap);
+  if (st != TRI_OK) return st;
+  CompactParams pc = compact_params(kv, keep_idx, budget);
+  pc.mass = mass;
+  pc.mass_out = mass_out;
+  const cudaError_t e = launch_mass_evict(select_params(mass, kv, n_prompt, n_recent, budget, keep_idx), pc,
+                                          static_cast<int>(slices_of(kv)), stream);
+  return e == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
+}
+
 tri_status tri_paged_blocks_used(const tri_kv* kv, int32_t* blocks_used, tri_stream_t stream) {
   TRI_CALL_RANGE();
   tri_status st = check_kv(kv, false);

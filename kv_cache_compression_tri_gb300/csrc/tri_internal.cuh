@@ -330,6 +330,35 @@ struct CompactParams {
   int32_t n_cap;
   int32_t budget;
   int32_t row_bytes;
+  // eviction by accumulated weight: [S][n_cap] masses, moved with the rows
+  const float* mass;
+  float* mass_out;
+};
+
+// Attention over one layer's slices (attn_common.cuh has the row arithmetic).
+struct AttnParams {
+  const void* k;
+  const void* v;
+  const int32_t* n_valid;  // [S]
+  int32_t* dev_status;
+  RowMap rows;  // where the K and V rows are
+  int32_t n_cap, n_seq, n_layers, n_kv_heads, layer;
+  const void* q;                   // [n_seq][n_q][n_kv_heads * group][head_dim]
+  int64_t q_seq, q_token;          // elements between sequences and tokens
+  const int32_t* n_new;            // [n_seq], or NULL: n_q
+  int32_t n_q, group;
+  int32_t n_sink, window;
+  float scale;                     // of q . k
+  void* out;                       // [n_seq][n_q][n_kv_heads * group][head_dim]
+  float* lse;                      // [n_seq][n_q][n_kv_heads * group], or NULL
+  const float* lse_in;             // the weights' log-sums (attn_mass)
+  int64_t lse_seq;                 // elements between its sequences
+  float* mass;                     // [S][n_cap], or NULL
+  // decode workspace
+  int32_t n_split;                 // CTAs per slice
+  float* part_o;                   // [layer slices][n_split][group][head_dim]: sums of 2^(x - m) v
+  float2* part_ml;                 // [layer slices][n_split][group]: m and sum of 2^(x - m); sum -1: skipped
+  float* logits;                   // [layer slices][group][n_cap], visible rows (mass only)
 };
 
 struct CalibParams {
@@ -403,5 +432,14 @@ cudaError_t launch_select_compact(const SelectParams& ps, const CompactParams& p
 cudaError_t launch_calibrate(const CalibParams& p, tri_dtype dt, int head_dim,
                              tri_rope_style style, int lh_count, cudaStream_t st);
 int calibrate_split_count(int lh_count, int64_t samples_per_lh);
+// One new token per sequence over the cache; CTAs per slice for it.
+int attn_decode_splits(int n_slices, int max_rows);
+cudaError_t launch_attn_decode(const AttnParams& p, tri_dtype dt, int head_dim, cudaStream_t st);
+// A chunk of new tokens over the cache.
+cudaError_t launch_attn_prefill(const AttnParams& p, tri_dtype dt, int head_dim, cudaStream_t st);
+// The weights a chunk of queries gives every row, added to the rows' masses.
+cudaError_t launch_attn_mass(const AttnParams& p, tri_dtype dt, int head_dim, cudaStream_t st);
+// Selection by mass, then compaction of K, V, positions and masses.
+cudaError_t launch_mass_evict(const SelectParams& ps, const CompactParams& pc, int n_slices, cudaStream_t st);
 
 }  // namespace tri
