@@ -3,12 +3,38 @@
 //
 // Per slice and query head g: x_j = scale * (q_g . k_j) over the visible rows,
 // out_g = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m). A slice's visible rows are
-// cut into n_split equal runs, one CTA each; a CTA keeps a running maximum m,
-// sum l and vector sum o per head (o and l rescaled when m grows), and writes
-// (m, l, o) to the workspace. The join takes the largest m of a head's runs and
-// adds the runs' l and o times 2^(m_run - m). Masses need every row's weight
-// under the final log-sum, so the logits of the first pass are kept in the
-// workspace and turned into weights by a third kernel.
+// cut into n_split runs, one CTA each; a run keeps a running maximum m, sum l and
+// vector sum o per head (o and l rescaled when m grows). The second kernel
+// joins: the largest m of a head's runs, and the runs' l and o times
+// 2^(m_run - m). Masses need every row's weight under the final log-sum, so the
+// first kernel leaves the logits in the workspace and the second turns them
+// into weights.
+//
+// Bound: K and V are read once, 4 G flop per 4 bytes of a bf16 row pair: HBM.
+//
+// bf16 rows (decode_tiles_kernel). At most 8 query heads share a row, so the
+// products are thin: one 16 x 8 x 16 warp MMA takes 16 rows against the
+// group's heads. (A tcgen05 MMA takes at least 64 rows of M, and its
+// operands and result would cross shared and tensor memory and two barriers
+// per tile for a product that is not what bounds the kernel.) Each warp owns a
+// ring of NST tiles of TK rows, filled with 16-byte asynchronous copies NST - 1
+// tiles ahead, so no CTA barrier stands in the loop and a row never sits in
+// registers while it is on its way. Rows out of sight are zero-filled by the
+// copy and never read. In shared memory the 16-byte chunk c of row r lies at
+// chunk c ^ (r & 7), so the eight rows of a matrix load hit eight different
+// groups of banks.
+//   S = K Q^T: A = 16 rows of K, B = the heads (registers, loaded once). A
+//   thread gets rows g, g + 8 and heads 2t, 2t + 1 (g = lane / 4, t = lane % 4);
+//   maxima and sums over rows are shuffles over g.
+//   O^T += V^T P^T: A = V transposed by the matrix load, B = the weights of 16
+//   rows, which a warp transpose turns from S's layout into B's. A head's
+//   column of O^T and of S sit in the same threads, so rescaling is local. The
+//   weights go in as a bf16 pair (p rounded, and the rest rounded): the product
+//   carries 16 bits of them, at the cost of eight more MMAs that the memory
+//   traffic hides.
+//
+// fp32 rows (decode_rows_kernel): 8 lanes per row on the CUDA cores, fp32
+// throughout (a tensor-core product would drop the rows to 10 bits).
 #include <cuda_runtime.h>
 
 #include "attn_common.cuh"
@@ -16,12 +42,7 @@
 namespace tri {
 namespace {
 
-constexpr int DT = 128;   // threads per CTA
-constexpr int LPR = 8;    // lanes per row
-constexpr int GROUPS = DT / LPR;
-
-// Row counts of the slice handled by this CTA; false: nothing to do. A slice
-// with a fault is reported and its partial sums marked (sum -1).
+// Row counts of a slice; false: nothing to do (faults are reported).
 struct Run {
   int64_t s;       // slice of the cache
   int n, seq, h;   // valid rows, sequence, KV head
@@ -45,17 +66,308 @@ __device__ __forceinline__ bool slice_run(const AttnParams& p, int ls, Run& r) {
   return true;
 }
 
-template <typename T, int D, int GP>
-__global__ void __launch_bounds__(DT) decode_partial_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int E = 16 / sizeof(T);       // elements per 16-byte chunk
-  constexpr int C = D / (E * LPR);        // chunks per lane
+// ---------------------------------------------------------------------------
+// bf16 rows
+// ---------------------------------------------------------------------------
+constexpr int NW = 4;  // warps per CTA
+
+template <int D>
+struct TileGeo {
+  static constexpr int TK = 2048 / D;         // rows per tile: 4 KB of K and of V
+  static constexpr int ROW = D * 2;           // bytes
+  static constexpr int CH = ROW / 16;         // 16-byte chunks per row
+  static constexpr int RPI = 32 / CH;         // rows per copy instruction of a warp
+  static constexpr int TILE = TK * ROW;       // bytes of one tensor's tile
+  static constexpr int NST = 3;
+  static constexpr int WARP_RING = NST * 2 * TILE;
+  static constexpr int SMEM = NW * WARP_RING;
+  static constexpr int SUB = TK / 16;         // 16-row steps of a tile
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  const int bytes = live ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The result of a head's element, or of its log-sum, from the sums of all its rows.
+template <typename T, int D>
+__device__ __forceinline__ void store_out(const AttnParams& p, const Run& r, int g, int e, float o, float l) {
+  const int64_t row = (static_cast<int64_t>(r.seq) * p.n_kv_heads + r.h) * p.group + g;
+  static_cast<T*>(p.out)[row * D + e] = from_f32<T>(l != 0.f ? o / l : 0.f);
+}
+__device__ __forceinline__ void store_lse(const AttnParams& p, const Run& r, int g, float m, float l) {
+  const int64_t row = (static_cast<int64_t>(r.seq) * p.n_kv_heads + r.h) * p.group + g;
+  if (p.lse) p.lse[row] = l != 0.f ? LN2 * (m + log2f(l)) : NEG_INF;
+}
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_constant__ AttnParams p) {
+  using G = TileGeo<D>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float sm_m[NW][8], sm_l[NW][8];
+  __shared__ int bad;
+  const int ls = blockIdx.x / p.n_split, split = blockIdx.x % p.n_split;
+  const int t = threadIdx.x, w = t >> 5, lane = t & 31, lg = lane >> 2, lt = lane & 3;
+  const int64_t pi = static_cast<int64_t>(blockIdx.x) * p.group;
+  pdl_launch();
+  Run r;
+  if (!slice_run(p, ls, r)) {
+    if (t < p.group) p.part_ml[pi + t] = make_float2(NEG_INF, -1.f);
+    return;
+  }
+  if (t == 0) bad = 0;
+
+  // the tiles that hold visible rows: [0, ta) and [tb, tn)
+  const int ta = (r.vis.s1 + G::TK - 1) / G::TK, tn = (r.n + G::TK - 1) / G::TK;
+  const int tb = max(ta, r.vis.w0 / G::TK);
+  const int tiles = ta + tn - tb;
+  const int u0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.n_split);
+  const int u1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.n_split);
+
+  // the heads' B fragments
+  uint32_t qf[D / 16][2];
+  {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) + r.seq * p.q_seq +
+                                                          (static_cast<int64_t>(r.h) * p.group + lg) * D);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      qf[ks][0] = lg < p.group ? __ldg(q + ks * 8 + lt) : 0u;
+      qf[ks][1] = lg < p.group ? __ldg(q + ks * 8 + lt + 4) : 0u;
+    }
+  }
+
+  const uint32_t ring = smem_addr(smem) + w * G::WARP_RING;
+  const int64_t base = p.rows.slice_base(r.s);
+  const int32_t* trow = p.rows.seq_table(r.s);
+  const int crow = lane / G::CH, cch = lane % G::CH;
+  bool blocks_ok = true;
+
+  auto row_of_tile = [&](int u) { return (u < ta ? u : u - ta + tb) * G::TK; };
+  // copy of tile u (of the slice's list) into stage st
+  auto fetch = [&](int u, int st) {
+    const int r0 = row_of_tile(u);
+    const uint32_t dk = ring + st * 2 * G::TILE, dv = dk + G::TILE;
+#pragma unroll
+    for (int s = 0; s < G::SUB; ++s) {
+      const int rs = r0 + 16 * s;
+      int64_t off;
+      bool in = rs < r.n;
+      if (PAGED) {
+        int blk = 0;
+        if (in) {
+          blk = __ldg(trow + (rs >> p.rows.block_shift));
+          if (blk < 0 || blk >= p.rows.num_blocks) {
+            // 16 rows that nobody sees may have no block any more
+            if (rs < r.vis.s1 || rs + 15 >= r.vis.w0) blocks_ok = false;
+            blk = 0;
+            in = false;
+          }
+        }
+        off = base + blk * p.rows.block_bytes + static_cast<int64_t>(rs & (p.rows.block_size - 1)) * G::ROW;
+      } else {
+        off = base + static_cast<int64_t>(rs) * G::ROW;
+      }
+#pragma unroll
+      for (int i = 0; i < 16 / G::RPI; ++i) {
+        const int rr = i * G::RPI + crow, j = rs + rr;
+        const bool live = in && j < r.n && (j < r.vis.s1 || j >= r.vis.w0);
+        const int64_t o = live ? off + rr * G::ROW + cch * 16 : 0;
+        const uint32_t d = (16 * s + rr) * G::ROW + ((cch ^ (rr & 7)) << 4);
+        cp_async16(dk + d, static_cast<const char*>(p.k) + o, live);
+        cp_async16(dv + d, static_cast<const char*>(p.v) + o, live);
+      }
+    }
+  };
+
+  float o[D / 16][4];
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
+  float m0 = NEG_INF, m1 = NEG_INF, l0 = 0.f, l1 = 0.f;  // heads 2 lt, 2 lt + 1
+  const float sl = p.scale * LOG2E;
+  float* logits = p.logits ? p.logits + static_cast<int64_t>(ls) * p.n_cap * p.group : nullptr;
+
+#pragma unroll
+  for (int i = 0; i < G::NST - 1; ++i) {
+    if (u0 + w + i * NW < u1) fetch(u0 + w + i * NW, i);
+    cp_async_commit();
+  }
+  int st = 0;
+  for (int u = u0 + w; u < u1; u += NW) {
+    {
+      const int nx = u + (G::NST - 1) * NW, ns = st == 0 ? G::NST - 1 : st - 1;
+      if (nx < u1) fetch(nx, ns);
+      cp_async_commit();
+    }
+    cp_async_wait<G::NST - 1>();
+    __syncwarp();
+    const int r0 = row_of_tile(u);
+    const bool inner = r0 + G::TK <= r.n && (r0 >= r.vis.w0 || r0 + G::TK <= r.vis.s1);
+    const uint32_t tk = ring + st * 2 * G::TILE, tv = tk + G::TILE;
+#pragma unroll
+    for (int s = 0; s < G::SUB; ++s) {
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      {
+        const int row = 16 * s + (lane & 15);
+        const uint32_t a = tk + row * G::ROW;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t kf[4];
+          ldsm4(a + (((2 * ks + (lane >> 4)) ^ (row & 7)) << 4), kf);
+          mma16816(x, kf, qf[ks][0], qf[ks][1]);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] *= sl;
+      const int ja = r0 + 16 * s + lg, jb = ja + 8;
+      if (!inner) {
+        if (!(ja < r.n && (ja < r.vis.s1 || ja >= r.vis.w0))) x[0] = x[1] = NEG_INF;
+        if (!(jb < r.n && (jb < r.vis.s1 || jb >= r.vis.w0))) x[2] = x[3] = NEG_INF;
+      }
+      if (logits) {  // (rows out of sight: their entries are not read)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int j = c < 2 ? ja : jb, g = 2 * lt + (c & 1);
+          if (g < p.group && j < r.n) logits[static_cast<int64_t>(j) * p.group + g] = x[c];
+        }
+      }
+      float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+#pragma unroll
+      for (int k = 4; k <= 16; k <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(FULL_MASK, mx0, k));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(FULL_MASK, mx1, k));
+      }
+      if (__any_sync(FULL_MASK, mx0 > m0 || mx1 > m1)) {
+        const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+        const float a0 = n0 == NEG_INF ? 1.f : fast_exp2(m0 - n0), a1 = n1 == NEG_INF ? 1.f : fast_exp2(m1 - n1);
+        m0 = n0;
+        m1 = n1;
+        l0 *= a0;
+        l1 *= a1;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          o[i][0] *= a0;
+          o[i][1] *= a1;
+          o[i][2] *= a0;
+          o[i][3] *= a1;
+        }
+      }
+      const float z0 = m0 == NEG_INF ? 0.f : m0, z1 = m1 == NEG_INF ? 0.f : m1;
+      const float e[4] = {fast_exp2(x[0] - z0), fast_exp2(x[1] - z1), fast_exp2(x[2] - z0), fast_exp2(x[3] - z1)};
+      l0 += e[0] + e[2];
+      l1 += e[1] + e[3];
+      const uint32_t ha = pack_bf16(e[0], e[1]), hb = pack_bf16(e[2], e[3]);
+      const uint32_t la = pack_bf16(e[0] - bf16_lo(ha), e[1] - bf16_hi(ha)), lb = pack_bf16(e[2] - bf16_lo(hb), e[3] - bf16_hi(hb));
+      const uint32_t b0 = transpose8(ha), b1 = transpose8(hb), c0 = transpose8(la), c1 = transpose8(lb);
+      const int row = 16 * s + (lane & 7) + ((lane >> 4) << 3);
+      const uint32_t a = tv + row * G::ROW;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t vf[4];
+        ldsm4_t(a + (((2 * i + ((lane >> 3) & 1)) ^ (row & 7)) << 4), vf);
+        mma16816(o[i], vf, b0, b1);
+        mma16816(o[i], vf, c0, c1);
+      }
+    }
+    __syncwarp();  // the stage may be refilled
+    st = st + 1 == G::NST ? 0 : st + 1;
+  }
+  cp_async_wait<0>();
+  if (PAGED && !blocks_ok) bad = 1;
+#pragma unroll
+  for (int k = 4; k <= 16; k <<= 1) {
+    l0 += __shfl_xor_sync(FULL_MASK, l0, k);
+    l1 += __shfl_xor_sync(FULL_MASK, l1, k);
+  }
+  if (lg == 0) {
+    sm_m[w][2 * lt] = m0;
+    sm_m[w][2 * lt + 1] = m1;
+    sm_l[w][2 * lt] = l0;
+    sm_l[w][2 * lt + 1] = l1;
+  }
+  __syncthreads();  // every ring is idle: the warps' vector sums go there
+  float* so = reinterpret_cast<float*>(smem);
+  constexpr int HS = D + 4;  // floats between heads: the four lt of a store hit different banks
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) so[(w * 8 + 2 * lt + (c & 1)) * HS + 16 * i + lg + (c >> 1) * 8] = o[i][c];
+  __syncthreads();
+  if (PAGED && bad) {
+    if (t == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
+    if (t < p.group) p.part_ml[pi + t] = make_float2(NEG_INF, -1.f);
+    return;
+  }
+  const bool direct = p.n_split == 1 && !p.mass;
+  for (int i = t; i < p.group * D; i += NW * 32) {
+    const int g = i / D, e = i % D;
+    float m = NEG_INF;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) m = fmaxf(m, sm_m[k][g]);
+    const float mu = m == NEG_INF ? 0.f : m;
+    float l = 0.f, acc = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const float a = fast_exp2(sm_m[k][g] - mu);
+      l = fmaf(sm_l[k][g], a, l);
+      acc = fmaf(so[(k * 8 + g) * HS + e], a, acc);
+    }
+    if (direct) {
+      store_out<__nv_bfloat16, D>(p, r, g, e, acc, l);
+      if (e == 0) store_lse(p, r, g, m, l);
+    } else {
+      p.part_o[(pi + g) * D + e] = acc;
+      if (e == 0) p.part_ml[pi + g] = make_float2(m, l);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// fp32 rows
+// ---------------------------------------------------------------------------
+constexpr int DT = 128;   // threads per CTA
+constexpr int LPR = 8;    // lanes per row
+constexpr int GROUPS = DT / LPR;
+
+template <int D, int GP>
+__global__ void __launch_bounds__(DT) decode_rows_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int E = 4;              // elements per 16-byte chunk
+  constexpr int C = D / (E * LPR);  // chunks per lane
   __shared__ float sq[GP][D];
   __shared__ float so[GROUPS][D];
   __shared__ float sm_m[GROUPS][GP], sm_l[GROUPS][GP];
   __shared__ int flag;
-  const int split = blockIdx.x, ls = blockIdx.y, t = threadIdx.x, G = p.group;
+  const int ls = blockIdx.x / p.n_split, split = blockIdx.x % p.n_split, t = threadIdx.x, G = p.group;
+  pdl_launch();
   Run r;
-  const int64_t pi = (static_cast<int64_t>(ls) * p.n_split + split) * G;
+  const int64_t pi = static_cast<int64_t>(blockIdx.x) * G;
   bool ok = slice_run(p, ls, r);
   int i0 = 0, i1 = 0;
   const int32_t* trow = p.rows.seq_table(r.s);
@@ -74,10 +386,10 @@ __global__ void __launch_bounds__(DT) decode_partial_kernel(const __grid_constan
     if (t < G) p.part_ml[pi + t] = make_float2(NEG_INF, -1.f);
     return;
   }
-  const T* q = static_cast<const T*>(p.q) + r.seq * p.q_seq + static_cast<int64_t>(r.h) * G * D;
+  const float* q = static_cast<const float*>(p.q) + r.seq * p.q_seq + static_cast<int64_t>(r.h) * G * D;
   for (int i = t; i < GP * D; i += DT) {
     const int g = i / D;
-    sq[g][i % D] = g < G ? to_f32(q[i]) * (p.scale * LOG2E) : 0.f;
+    sq[g][i % D] = g < G ? q[i] * (p.scale * LOG2E) : 0.f;
   }
   __syncthreads();
   const int rg = t / LPR, lane8 = t % LPR;
@@ -90,7 +402,7 @@ __global__ void __launch_bounds__(DT) decode_partial_kernel(const __grid_constan
     for (int e = 0; e < C * E; ++e) o[g][e] = 0.f;
   }
   const int64_t base = p.rows.slice_base(r.s);
-  float* logits = p.logits ? p.logits + static_cast<int64_t>(ls) * G * p.n_cap : nullptr;
+  float* logits = p.logits ? p.logits + static_cast<int64_t>(ls) * p.n_cap * G : nullptr;
   for (int i = i0 + rg; i - rg < i1; i += GROUPS) {
     const bool live = i < i1;
     const int j = i < r.vis.s1 ? i : i - r.vis.s1 + r.vis.w0;
@@ -117,20 +429,20 @@ __global__ void __launch_bounds__(DT) decode_partial_kernel(const __grid_constan
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
 #pragma unroll
-      for (int w = LPR / 2; w >= 1; w >>= 1) x[g] += __shfl_xor_sync(FULL_MASK, x[g], w);
+      for (int k = LPR / 2; k >= 1; k >>= 1) x[g] += __shfl_xor_sync(FULL_MASK, x[g], k);
       if (!live) x[g] = NEG_INF;
-      if (logits && live && lane8 == g % LPR && g < G) logits[static_cast<int64_t>(g) * p.n_cap + j] = x[g];
+      if (logits && live && lane8 == g % LPR && g < G) logits[static_cast<int64_t>(j) * G + g] = x[g];
       const float mn = fmaxf(m[g], x[g]);
       const float mu = mn == NEG_INF ? 0.f : mn;
-      const float a = fast_exp2(m[g] - mu), w = fast_exp2(x[g] - mu);
+      const float a = fast_exp2(m[g] - mu), e0 = fast_exp2(x[g] - mu);
       m[g] = mn;
-      l[g] = fmaf(l[g], a, w);
+      l[g] = fmaf(l[g], a, e0);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         float vx[E];
         widen(vw[c], vx);
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[g][c * E + e] = fmaf(o[g][c * E + e], a, w * vx[e]);
+        for (int e = 0; e < E; ++e) o[g][c * E + e] = fmaf(o[g][c * E + e], a, e0 * vx[e]);
       }
     }
   }
@@ -141,6 +453,7 @@ __global__ void __launch_bounds__(DT) decode_partial_kernel(const __grid_constan
       sm_l[rg][g] = l[g];
     }
   }
+  const bool direct = p.n_split == 1 && !p.mass;
 #pragma unroll
   for (int g = 0; g < GP; ++g) {
     if (g >= G) break;
@@ -154,111 +467,157 @@ __global__ void __launch_bounds__(DT) decode_partial_kernel(const __grid_constan
 #pragma unroll
       for (int e = 0; e < E; ++e) so[rg][(lane8 + LPR * c) * E + e] = o[g][c * E + e] * a;
     __syncthreads();
+    float sum_l = 0.f;
+    for (int u = 0; u < GROUPS; ++u) sum_l = fmaf(sm_l[u][g], fast_exp2(sm_m[u][g] - mu), sum_l);
     for (int e = t; e < D; e += DT) {
       float sum = 0.f;
       for (int u = 0; u < GROUPS; ++u) sum += so[u][e];
-      p.part_o[(pi + g) * D + e] = sum;
+      if (direct) store_out<float, D>(p, r, g, e, sum, sum_l);
+      else p.part_o[(pi + g) * D + e] = sum;
     }
     if (t == 0) {
-      float sum = 0.f;
-      for (int u = 0; u < GROUPS; ++u) sum = fmaf(sm_l[u][g], fast_exp2(sm_m[u][g] - mu), sum);
-      p.part_ml[pi + g] = make_float2(mx, sum);
+      if (direct) store_lse(p, r, g, mx, sum_l);
+      else p.part_ml[pi + g] = make_float2(mx, sum_l);
     }
   }
 }
 
-// Joined (m, l) of a head's runs; false: skipped.
-__device__ __forceinline__ bool join_ml(const AttnParams& p, int ls, int g, float& m, float& l) {
-  const float2* ml = p.part_ml + static_cast<int64_t>(ls) * p.n_split * p.group + g;
-  m = NEG_INF;
-  l = 0.f;
-  for (int i = 0; i < p.n_split; ++i) {
-    const float2 x = ml[static_cast<int64_t>(i) * p.group];
-    if (x.y < 0.f) return false;
-    m = fmaxf(m, x.x);
-  }
-  const float mu = m == NEG_INF ? 0.f : m;
-  for (int i = 0; i < p.n_split; ++i) {
-    const float2 x = ml[static_cast<int64_t>(i) * p.group];
-    l = fmaf(x.y, fast_exp2(x.x - mu), l);
-  }
-  return true;
-}
+// ---------------------------------------------------------------------------
+// join, and masses: CTA (slice, c) of `chunks` joins head c, and with masses
+// takes visible rows [c, c + 1) * JROWS: mass[j] += sum over the heads of
+// 2^(x_j - m) / l.
+// ---------------------------------------------------------------------------
+constexpr int JT = 128;
+constexpr int JROWS = 1024;
+constexpr int MAX_SPLIT = 128;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(D) decode_join_kernel(const __grid_constant__ AttnParams p) {
-  const int ls = blockIdx.x / p.group, g = blockIdx.x % p.group, t = threadIdx.x;
-  const int seq = ls / p.n_kv_heads, h = ls % p.n_kv_heads;
-  float m, l;
-  if (!join_ml(p, ls, g, m, l)) return;
-  const float mu = m == NEG_INF ? 0.f : m;
-  float o = 0.f;
-  for (int i = 0; i < p.n_split; ++i) {
-    const int64_t pi = (static_cast<int64_t>(ls) * p.n_split + i) * p.group + g;
-    o = fmaf(p.part_o[pi * D + t], fast_exp2(p.part_ml[pi].x - mu), o);
-  }
-  const int64_t row = (static_cast<int64_t>(seq) * p.n_kv_heads + h) * p.group + g;
-  static_cast<T*>(p.out)[row * D + t] = from_f32<T>(l != 0.f ? o / l : 0.f);
-  if (p.lse && t == 0) p.lse[row] = l != 0.f ? LN2 * (m + log2f(l)) : NEG_INF;
-}
-
-// mass[j] += sum over the heads of 2^(x_j - m) / l.
-__global__ void __launch_bounds__(256) decode_mass_kernel(const __grid_constant__ AttnParams p) {
-  __shared__ float lse2[MAX_GROUP];
+__global__ void __launch_bounds__(JT) decode_join_kernel(const __grid_constant__ AttnParams p, int chunks) {
+  __shared__ float lse2[MAX_GROUP], s_m[MAX_GROUP], s_l[MAX_GROUP];
   __shared__ int skip;
-  const int ls = blockIdx.y, t = threadIdx.x;
+  const int ls = blockIdx.x / chunks, c = blockIdx.x % chunks, t = threadIdx.x, G = p.group;
+  if (t == 0) skip = 0;
+  pdl_wait();
   Run r;
   if (!slice_run(p, ls, r)) return;
-  if (t == 0) skip = 0;
   __syncthreads();
-  if (t < p.group) {
-    float m, l;
-    if (!join_ml(p, ls, t, m, l)) skip = 1;
-    lse2[t] = m + log2f(l);
+  // (m, l) of the heads: a warp per head, lanes over the runs
+  const float2* ml = p.part_ml + static_cast<int64_t>(ls) * p.n_split * G;
+  for (int g = t >> 5; g < G; g += JT / 32) {
+    if (!p.mass && g != c) continue;
+    float m = NEG_INF, l = 0.f;
+    for (int i = t & 31; i < p.n_split; i += 32) {
+      const float2 x = ml[i * G + g];
+      if (x.y < 0.f) skip = 1;
+      m = fmaxf(m, x.x);
+    }
+#pragma unroll
+    for (int k = 16; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, k));
+    const float mu = m == NEG_INF ? 0.f : m;
+    for (int i = t & 31; i < p.n_split; i += 32) {
+      const float2 x = ml[i * G + g];
+      l = fmaf(x.y, fast_exp2(x.x - mu), l);
+    }
+#pragma unroll
+    for (int k = 16; k >= 1; k >>= 1) l += __shfl_xor_sync(FULL_MASK, l, k);
+    if ((t & 31) == 0) {
+      s_m[g] = mu;
+      s_l[g] = l;
+      lse2[g] = l != 0.f ? m + log2f(l) : -NEG_INF;  // (no weight at all: 2^(x - inf) = 0)
+    }
   }
   __syncthreads();
   if (skip) return;
-  const float* logits = p.logits + static_cast<int64_t>(ls) * p.group * p.n_cap;
+  if (c < G) {
+    const float* po = p.part_o + (static_cast<int64_t>(ls) * p.n_split * G + c) * D;
+    for (int e = t; e < D; e += JT) {
+      float o = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < p.n_split; ++i) o = fmaf(po[static_cast<int64_t>(i) * G * D + e], fast_exp2(ml[i * G + c].x - s_m[c]), o);
+      store_out<T, D>(p, r, c, e, o, s_l[c]);
+    }
+    if (t == 0) store_lse(p, r, c, s_m[c], s_l[c]);
+  }
+  if (!p.mass) return;
+  const float* logits = p.logits + static_cast<int64_t>(ls) * p.n_cap * G;
   float* mass = p.mass + r.s * p.n_cap;
-  for (int i = blockIdx.x * 256 + t; i < r.count; i += gridDim.x * 256) {
+  const int end = min(r.count, (c + 1) * JROWS);
+  for (int i = c * JROWS + t; i < end; i += JT) {
     const int j = i < r.vis.s1 ? i : i - r.vis.s1 + r.vis.w0;
-    float w = 0.f;
-    for (int g = 0; g < p.group; ++g) w += fast_exp2(logits[static_cast<int64_t>(g) * p.n_cap + j] - lse2[g]);
-    mass[j] += w;
+    float sum = 0.f;
+    for (int g = 0; g < G; ++g) sum += fast_exp2(logits[static_cast<int64_t>(j) * G + g] - lse2[g]);
+    mass[j] += sum;
   }
 }
 
 template <typename T, int D>
-cudaError_t launch_typed(const AttnParams& p, cudaStream_t st) {
-  const int n = p.n_seq * p.n_kv_heads;
-  const dim3 grid(static_cast<unsigned>(p.n_split), static_cast<unsigned>(n));
-  if (p.group == 1) decode_partial_kernel<T, D, 1><<<grid, DT, 0, st>>>(p);
-  else if (p.group == 2) decode_partial_kernel<T, D, 2><<<grid, DT, 0, st>>>(p);
-  else if (p.group <= 4) decode_partial_kernel<T, D, 4><<<grid, DT, 0, st>>>(p);
-  else decode_partial_kernel<T, D, 8><<<grid, DT, 0, st>>>(p);
-  note_launch();
-  cudaError_t e = cudaGetLastError();
+cudaError_t launch_join(const AttnParams& p, int max_rows, cudaStream_t st) {
+  const int chunks = p.mass ? max(p.group, (max_rows + JROWS - 1) / JROWS) : p.group;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.n_seq * p.n_kv_heads * chunks));
+  cfg.blockDim = dim3(JT);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D>, p, chunks);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+template <int D>
+cudaError_t launch_bf16(const AttnParams& p, int max_rows, cudaStream_t st) {
+  auto kern = p.rows.table ? decode_tiles_kernel<D, true> : decode_tiles_kernel<D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TileGeo<D>::SMEM);
   if (e != cudaSuccess) return e;
-  decode_join_kernel<T, D><<<static_cast<unsigned>(n * p.group), D, 0, st>>>(p);
+  kern<<<static_cast<unsigned>(p.n_seq * p.n_kv_heads * p.n_split), NW * 32, TileGeo<D>::SMEM, st>>>(p);
   note_launch();
   e = cudaGetLastError();
-  if (e != cudaSuccess || !p.mass) return e;
-  decode_mass_kernel<<<grid, 256, 0, st>>>(p);
+  if (e != cudaSuccess || (p.n_split == 1 && !p.mass)) return e;
+  return launch_join<__nv_bfloat16, D>(p, max_rows, st);
+}
+
+template <int D>
+cudaError_t launch_fp32(const AttnParams& p, int max_rows, cudaStream_t st) {
+  auto kern = p.group == 1 ? decode_rows_kernel<D, 1> : p.group == 2 ? decode_rows_kernel<D, 2>
+            : p.group <= 4 ? decode_rows_kernel<D, 4> : decode_rows_kernel<D, 8>;
+  kern<<<static_cast<unsigned>(p.n_seq * p.n_kv_heads * p.n_split), DT, 0, st>>>(p);
   note_launch();
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || (p.n_split == 1 && !p.mass)) return e;
+  return launch_join<float, D>(p, max_rows, st);
 }
 
 }  // namespace
 
-int attn_decode_splits(int n_slices, int max_rows) {
-  const int want = (152 * 8 + n_slices - 1) / n_slices;
-  const int most = (max_rows + 127) / 128;
-  return want < 1 ? 1 : (want < most ? want : most);
+int attn_decode_max_splits(int n_slices, int max_rows) {
+  const int fill = max(1, 152 * 8 / n_slices), most = (max_rows + 63) / 64;
+  return max(1, min(min(MAX_SPLIT, fill), most));
 }
 
-cudaError_t launch_attn_decode(const AttnParams& p, tri_dtype dt, int head_dim, cudaStream_t st) {
-  if (dt == TRI_BF16) return head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(p, st) : launch_typed<__nv_bfloat16, 128>(p, st);
-  return head_dim == 64 ? launch_typed<float, 64>(p, st) : launch_typed<float, 128>(p, st);
+// Runs per slice: the count that ends soonest when every slice holds max_rows,
+// SLOTS runs go at a time, and starting and joining a run costs about as long as
+// RUN_COST of its rows.
+int attn_decode_splits(int n_slices, int max_rows) {
+  constexpr int64_t SLOTS = 152 * 2, RUN_COST = 128;
+  const int most = attn_decode_max_splits(n_slices, max_rows);
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int s = 1; s <= most; ++s) {
+    const int64_t cost = (n_slices * static_cast<int64_t>(s) + SLOTS - 1) / SLOTS * ((max_rows + s - 1) / s + RUN_COST);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_attn_decode(const AttnParams& p, int max_rows, tri_dtype dt, int head_dim, cudaStream_t st) {
+  if (dt == TRI_BF16) return head_dim == 64 ? launch_bf16<64>(p, max_rows, st) : launch_bf16<128>(p, max_rows, st);
+  return head_dim == 64 ? launch_fp32<64>(p, max_rows, st) : launch_fp32<128>(p, max_rows, st);
 }
 
 }  // namespace tri

@@ -640,8 +640,8 @@ int max_visible(const tri_kv* kv, int32_t n_sink, int32_t window) {
 
 // Workspace of tri_attn_decode: the splits' sums [slices][splits][group][d] f32,
 // their (m, l) [slices][splits][group], and for the masses the logits
-// [slices][group][n_cap] f32 (each part 16-byte aligned). A window only
-// shortens the rows, and with them the splits, so the bound is without one.
+// [slices][n_cap][group] f32 (each part 16-byte aligned). The query allows for
+// the most runs any window may lead to.
 struct DecodeWs {
   size_t ml_off, logits_off, total;
 };
@@ -662,7 +662,7 @@ extern "C" {
 size_t tri_attn_decode_workspace_bytes(const tri_kv* kv, int32_t group, int32_t with_mass) {
   if (check_kv(kv, true) != TRI_OK || group < 1 || group > MAX_GROUP) return 0;
   const int n = kv->n_seq * kv->n_kv_heads;
-  return decode_ws(kv, group, attn_decode_splits(n, kv->n_cap), with_mass != 0).total;
+  return decode_ws(kv, group, attn_decode_max_splits(n, kv->n_cap), with_mass != 0).total;
 }
 
 tri_status tri_attn_decode(const tri_kv* kv, const tri_queries* q, void* out, float* lse, float* mass, void* ws,
@@ -673,8 +673,11 @@ tri_status tri_attn_decode(const tri_kv* kv, const tri_queries* q, void* out, fl
   if (st != TRI_OK) return st;
   if (q->n_q != 1 || !out || !aligned(out, 16)) return TRI_ERR_INVALID_ARG;
   if ((lse && !aligned(lse, 4)) || (mass && !aligned(mass, 4))) return TRI_ERR_INVALID_ARG;
-  const int n = kv->n_seq * kv->n_kv_heads;
-  p.n_split = attn_decode_splits(n, max_visible(kv, q->n_sink, q->window));
+  const int64_t n64 = static_cast<int64_t>(kv->n_seq) * kv->n_kv_heads;
+  if (n64 * std::max<int64_t>(q->group, kv->n_cap / 1024 + 1) > 0x7fffffff) return TRI_ERR_INVALID_ARG;
+  const int n = static_cast<int>(n64);
+  const int rows = max_visible(kv, q->n_sink, q->window);
+  p.n_split = attn_decode_splits(n, rows);
   const DecodeWs w = decode_ws(kv, q->group, p.n_split, mass != nullptr);
   if (!ws || !aligned(ws, 16) || ws_bytes < tri_attn_decode_workspace_bytes(kv, q->group, mass != nullptr))
     return TRI_ERR_INVALID_ARG;
@@ -685,7 +688,7 @@ tri_status tri_attn_decode(const tri_kv* kv, const tri_queries* q, void* out, fl
   p.out = out;
   p.lse = lse;
   p.mass = mass;
-  return launch_attn_decode(p, kv->dtype, kv->head_dim, stream) == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
+  return launch_attn_decode(p, rows, kv->dtype, kv->head_dim, stream) == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
 }
 
 tri_status tri_attn_prefill(const tri_kv* kv, const tri_queries* q, void* out, float* lse, tri_stream_t stream) {

@@ -358,7 +358,7 @@ struct AttnParams {
   int32_t n_split;                 // CTAs per slice
   float* part_o;                   // [layer slices][n_split][group][head_dim]: sums of 2^(x - m) v
   float2* part_ml;                 // [layer slices][n_split][group]: m and sum of 2^(x - m); sum -1: skipped
-  float* logits;                   // [layer slices][group][n_cap], visible rows (mass only)
+  float* logits;                   // [layer slices][n_cap][group], visible rows (mass only)
 };
 
 struct CalibParams {
@@ -433,8 +433,10 @@ cudaError_t launch_calibrate(const CalibParams& p, tri_dtype dt, int head_dim,
                              tri_rope_style style, int lh_count, cudaStream_t st);
 int calibrate_split_count(int lh_count, int64_t samples_per_lh);
 // One new token per sequence over the cache; CTAs per slice for it.
+// (and the most it may be, for the workspace: it grows with max_rows).
 int attn_decode_splits(int n_slices, int max_rows);
-cudaError_t launch_attn_decode(const AttnParams& p, tri_dtype dt, int head_dim, cudaStream_t st);
+int attn_decode_max_splits(int n_slices, int max_rows);
+cudaError_t launch_attn_decode(const AttnParams& p, int max_rows, tri_dtype dt, int head_dim, cudaStream_t st);
 // A chunk of new tokens over the cache.
 cudaError_t launch_attn_prefill(const AttnParams& p, tri_dtype dt, int head_dim, cudaStream_t st);
 // The weights a chunk of queries gives every row, added to the rows' masses.
