@@ -81,6 +81,8 @@ def lib_path() -> str:
 def load_library():
     """Load libtri.so (built in-tree by ``__graft_entry__.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -156,8 +158,9 @@ def _check(fn: str, status: int):
 
 
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -217,20 +220,21 @@ class KVCache:
         return self.k.device
 
     def _abi(self) -> _TriKV:
-        n_seq, L, H, n_cap, d = self.k.shape
-        assert self.k.is_cuda and self.k.dtype in _DTYPES
-        assert self.v.shape == self.k.shape and self.v.dtype == self.k.dtype
+        k, v = self.k, self.v
+        shape, strides, dtype = k.shape, k.stride(), k.dtype
+        n_seq, L, H, n_cap, d = shape
+        assert k.is_cuda and dtype in _DTYPES
+        assert v.shape == shape and v.dtype == dtype
         # rows contiguous, slices evenly strided
-        assert self.k.stride(4) == 1 and self.k.stride(3) == d
-        stride = self.k.stride(2)
-        assert self.k.stride(1) == H * stride and self.k.stride(0) == L * H * stride
-        assert tuple(self.v.stride()) == tuple(self.k.stride())
+        stride = strides[2]
+        assert strides == (L * H * stride, H * stride, stride, d, 1)
+        assert v.stride() == strides
         assert self.n_valid.dtype == torch.int32 and self.n_valid.numel() == n_seq * L * H
         for t in (self.pos, self.pos_out):
             if t is not None:
                 assert t.dtype == torch.int32 and t.is_contiguous() and t.numel() == n_seq * L * H * n_cap
-        return _TriKV(self.k.data_ptr(), self.v.data_ptr(), _ptr(self.pos), _ptr(self.pos_out),
-                      self.n_valid.data_ptr(), stride, n_seq, L, H, n_cap, d, _DTYPES[self.k.dtype],
+        return _TriKV(k.data_ptr(), v.data_ptr(), _ptr(self.pos), _ptr(self.pos_out),
+                      self.n_valid.data_ptr(), stride, n_seq, L, H, n_cap, d, _DTYPES[dtype],
                       _ptr(self.dev_status), 1 if self.post_rope else 0, None, 0, 0, 0, 0, 0)
 
 
@@ -268,21 +272,24 @@ class PagedKVCache:
         return self.k.device
 
     def _abi(self) -> _TriKV:
-        nb, L, H, bs, d = self.k.shape
-        assert self.k.is_cuda and self.k.dtype in _DTYPES
-        assert self.v.shape == self.k.shape and self.v.dtype == self.k.dtype
-        assert tuple(self.v.stride()) == tuple(self.k.stride())
-        assert self.k.stride(4) == 1 and self.k.stride(3) == d
-        assert self.block_table.dtype == torch.int32 and self.block_table.is_contiguous()
-        S, n_cap = self.n_slices, self.n_cap
+        k, v, table = self.k, self.v, self.block_table
+        shape, strides, dtype = k.shape, k.stride(), k.dtype
+        nb, L, H, bs, d = shape
+        assert k.is_cuda and dtype in _DTYPES
+        assert v.shape == shape and v.dtype == dtype
+        assert v.stride() == strides
+        assert strides[4] == 1 and strides[3] == d
+        assert table.dtype == torch.int32 and table.is_contiguous()
+        n_seq, blocks = table.shape
+        S, n_cap = n_seq * L * H, blocks * bs
         assert self.n_valid.dtype == torch.int32 and self.n_valid.numel() == S
         for t in (self.pos, self.pos_out):
             if t is not None:
                 assert t.dtype == torch.int32 and t.is_contiguous() and t.numel() == S * n_cap
-        return _TriKV(self.k.data_ptr(), self.v.data_ptr(), _ptr(self.pos), _ptr(self.pos_out),
-                      self.n_valid.data_ptr(), 0, self.n_seq, L, H, n_cap, d, _DTYPES[self.k.dtype],
-                      _ptr(self.dev_status), 1 if self.post_rope else 0, self.block_table.data_ptr(), bs, nb,
-                      self.k.stride(0), self.k.stride(1), self.k.stride(2))
+        return _TriKV(k.data_ptr(), v.data_ptr(), _ptr(self.pos), _ptr(self.pos_out),
+                      self.n_valid.data_ptr(), 0, n_seq, L, H, n_cap, d, _DTYPES[dtype],
+                      _ptr(self.dev_status), 1 if self.post_rope else 0, table.data_ptr(), bs, nb,
+                      strides[0], strides[1], strides[2])
 
 
 def paged_blocks_used(kv: PagedKVCache, out: torch.Tensor, stream=None) -> torch.Tensor:
@@ -517,23 +524,23 @@ def select_union(scores: torch.Tensor, kv: KVCache, n_prompt: int, n_recent: int
     return keep
 
 
-def _queries(kv, layer: int, q: torch.Tensor, n_new: torch.Tensor | None, scale: float | None, n_sink: int,
-             window: int) -> _TriQueries:
-    """q [n_seq, n_q, Hq, d] (any sequence and token strides) of the cache's type."""
-    n_seq, n_q, Hq, d = q.shape
-    H = kv.k.shape[2]
-    assert q.is_cuda and q.dtype == kv.k.dtype and d == kv.k.shape[4] and Hq % H == 0
-    assert q.stride(3) == 1 and (q.stride(2) == d or Hq == 1)
-    assert n_seq == (kv.n_seq if isinstance(kv, PagedKVCache) else kv.k.shape[0])
+def _queries(kvs: _TriKV, kv, layer: int, q: torch.Tensor, shape, strides, n_new: torch.Tensor | None,
+             scale: float | None, n_sink: int, window: int) -> _TriQueries:
+    """Queries of shape [n_seq, n_q, Hq, d] (any sequence and token strides) of the cache's type and device."""
+    n_seq, n_q, Hq, d = shape
+    dev = q.get_device()
+    assert dev == kv.k.get_device() == torch.cuda.current_device(), "cache and queries on the current device"
+    assert q.dtype == kv.k.dtype and d == kvs.head_dim and n_seq == kvs.n_seq and Hq % kvs.n_kv_heads == 0
+    assert strides[3] == 1 and (strides[2] == d or Hq == 1)
     if n_new is not None:
         assert n_new.is_cuda and n_new.dtype == torch.int32 and n_new.is_contiguous() and n_new.numel() == n_seq
-    return _TriQueries(q.data_ptr(), q.stride(0), q.stride(1), _ptr(n_new), n_q, Hq // H, layer, n_sink, window,
-                       d ** -0.5 if scale is None else scale)
+    return _TriQueries(q.data_ptr(), strides[0], strides[1], _ptr(n_new), n_q, Hq // kvs.n_kv_heads, layer, n_sink,
+                       window, d ** -0.5 if scale is None else scale)
 
 
-def _check_mass(kv, mass: torch.Tensor):
+def _check_mass(kvs: _TriKV, mass: torch.Tensor):
     assert mass.is_cuda and mass.dtype == torch.float32 and mass.is_contiguous()
-    assert mass.numel() == kv.n_slices * kv.n_cap
+    assert mass.numel() == kvs.n_seq * kvs.n_layers * kvs.n_kv_heads * kvs.n_cap
 
 
 def attn_decode_workspace_bytes(kv, group: int, with_mass: bool = False) -> int:
@@ -550,20 +557,22 @@ def attn_decode(kv, layer: int, q: torch.Tensor, out: torch.Tensor, n_new: torch
     row's weight added. window > 0: the first n_sink and newest `window` rows
     only. n_new [n_seq] int32: 0 leaves a sequence out. scale: d ** -0.5."""
     lib = load_library()
-    qs = _queries(kv, layer, q.unsqueeze(1), n_new, scale, n_sink, window)
-    assert out.is_cuda and out.is_contiguous() and out.shape == q.shape and out.dtype == q.dtype
-    if lse is not None:
-        assert lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == q.shape[0] * q.shape[1]
-    if mass is not None:
-        _check_mass(kv, mass)
     kvs = kv._abi()
+    shape, strides = q.shape, q.stride()
+    n_seq, Hq, d = shape
+    qs = _queries(kvs, kv, layer, q, (n_seq, 1, Hq, d), (strides[0], strides[0], strides[1], strides[2]), n_new, scale,
+                  n_sink, window)
+    assert out.is_cuda and out.is_contiguous() and out.shape == shape and out.dtype == q.dtype
+    if lse is not None:
+        assert lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == n_seq * Hq
+    if mass is not None:
+        _check_mass(kvs, mass)
     if workspace is None:
         need = int(lib.tri_attn_decode_workspace_bytes(ctypes.byref(kvs), qs.group, int(mass is not None)))
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=kv.device)
     assert workspace.is_cuda and workspace.is_contiguous()
     _check("tri_attn_decode", lib.tri_attn_decode(ctypes.byref(kvs), ctypes.byref(qs), out.data_ptr(), _ptr(lse),
-                                                  _ptr(mass), workspace.data_ptr(),
-                                                  workspace.numel() * workspace.element_size(), _stream(stream)))
+                                                  _ptr(mass), workspace.data_ptr(), workspace.nbytes, _stream(stream)))
     return out
 
 
@@ -576,11 +585,12 @@ def attn_prefill(kv, layer: int, q: torch.Tensor, out: torch.Tensor, n_new: torc
     [n_seq, n_q, Hq] fp32. n_new [n_seq] int32: tokens of each sequence (rows of
     out past them stay as they were)."""
     lib = load_library()
-    qs = _queries(kv, layer, q, n_new, scale, n_sink, window)
-    assert out.is_cuda and out.is_contiguous() and out.shape == q.shape and out.dtype == q.dtype
-    if lse is not None:
-        assert lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == q.shape[:3]
     kvs = kv._abi()
+    shape = q.shape
+    qs = _queries(kvs, kv, layer, q, shape, q.stride(), n_new, scale, n_sink, window)
+    assert out.is_cuda and out.is_contiguous() and out.shape == shape and out.dtype == q.dtype
+    if lse is not None:
+        assert lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == shape[:3]
     _check("tri_attn_prefill", lib.tri_attn_prefill(ctypes.byref(kvs), ctypes.byref(qs), out.data_ptr(), _ptr(lse),
                                                     _stream(stream)))
     return out
@@ -594,12 +604,13 @@ def attn_mass(kv, layer: int, q: torch.Tensor, lse: torch.Tensor, mass: torch.Te
     attn_prefill (tri_attn_mass). Both may be the last n_q tokens of a longer
     chunk (q[:, -n:], lse[:, -n:]): an observation window."""
     lib = load_library()
-    qs = _queries(kv, layer, q, n_new, scale, n_sink, window)
-    assert lse.is_cuda and lse.dtype == torch.float32 and lse.shape == q.shape[:3]
-    assert lse.stride(2) == 1 and (lse.stride(1) == q.shape[2] or q.shape[1] == 1)
-    _check_mass(kv, mass)
     kvs = kv._abi()
-    _check("tri_attn_mass", lib.tri_attn_mass(ctypes.byref(kvs), ctypes.byref(qs), lse.data_ptr(), lse.stride(0),
+    shape, ls = q.shape, lse.stride()
+    qs = _queries(kvs, kv, layer, q, shape, q.stride(), n_new, scale, n_sink, window)
+    assert lse.is_cuda and lse.dtype == torch.float32 and lse.shape == shape[:3]
+    assert ls[2] == 1 and (ls[1] == shape[2] or shape[1] == 1)
+    _check_mass(kvs, mass)
+    _check("tri_attn_mass", lib.tri_attn_mass(ctypes.byref(kvs), ctypes.byref(qs), lse.data_ptr(), ls[0],
                                               mass.data_ptr(), _stream(stream)))
     return mass
 
@@ -610,10 +621,10 @@ def mass_evict(kv, mass: torch.Tensor, mass_out: torch.Tensor, n_prompt: int, n_
     with mass [S, n_cap] as the scores, the masses moved with their rows into
     mass_out (may be mass), the freed rows' masses set to 0."""
     lib = load_library()
-    assert keep.dtype == torch.int32 and keep.is_contiguous() and keep.numel() == kv.n_slices * budget
-    _check_mass(kv, mass)
-    _check_mass(kv, mass_out)
     kvs = kv._abi()
+    assert keep.dtype == torch.int32 and keep.is_contiguous() and keep.numel() == kv.n_slices * budget
+    _check_mass(kvs, mass)
+    _check_mass(kvs, mass_out)
     _check("tri_mass_evict", lib.tri_mass_evict(mass.data_ptr(), mass_out.data_ptr(), ctypes.byref(kvs), n_prompt,
                                                 n_recent, budget, keep.data_ptr(), _stream(stream)))
     return keep

@@ -4,11 +4,17 @@
 // Per slice and query head g: x_j = scale * (q_g . k_j) over the visible rows,
 // out_g = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m). A slice's visible rows are
 // cut into n_split runs, one CTA each; a run keeps a running maximum m, sum l and
-// vector sum o per head (o and l rescaled when m grows). The second kernel
-// joins: the largest m of a head's runs, and the runs' l and o times
-// 2^(m_run - m). Masses need every row's weight under the final log-sum, so the
-// first kernel leaves the logits in the workspace and the second turns them
-// into weights.
+// vector sum o per head (o and l rescaled when m grows). Joining takes the
+// largest m of a head's runs, and the runs' l and o times 2^(m_run - m). Masses
+// need every row's weight under the final log-sum, so the logits are left in
+// the workspace and turned into weights after the join.
+//
+// Two ways to join. Up to MAX_CLUSTER runs of a slice form one thread-block
+// cluster: each run's sums stay in its shared memory, the CTAs read each
+// other's, each writes its share of the heads' elements and adds its own rows'
+// masses -- one launch. More runs (few slices, long rows) write their sums to
+// the workspace, and a second kernel, launched early and waiting for the first
+// on the device, joins them.
 //
 // Bound: K and V are read once, 4 G flop per 4 bytes of a bf16 row pair: HBM.
 //
@@ -70,6 +76,7 @@ __device__ __forceinline__ bool slice_run(const AttnParams& p, int ls, Run& r) {
 // bf16 rows
 // ---------------------------------------------------------------------------
 constexpr int NW = 4;  // warps per CTA
+constexpr int MAX_CLUSTER = 16;  // (above 8 a kernel has to allow for it; a GPC of this GPU holds 16 such CTAs)
 
 template <int D>
 struct TileGeo {
@@ -115,6 +122,28 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Barrier over the cluster's CTAs (over the CTA when it is alone).
+__device__ __forceinline__ void cluster_sync(int ns) {
+  if (ns == 1) {
+    __syncthreads();
+    return;
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// *p of CTA u of the cluster.
+__device__ __forceinline__ float cluster_ld(const float* p, int u, int ns) {
+  if (ns == 1) return *p;
+  float x;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(x) : "r"(smem_addr(p)), "r"(u) : "memory");
+  return x;
+}
+__device__ __forceinline__ float2 cluster_ld2(const float2* p, int u, int ns) {
+  const float* f = reinterpret_cast<const float*>(p);
+  return make_float2(cluster_ld(f, u, ns), cluster_ld(f + 1, u, ns));
+}
+
 // The result of a head's element, or of its log-sum, from the sums of all its rows.
 template <typename T, int D>
 __device__ __forceinline__ void store_out(const AttnParams& p, const Run& r, int g, int e, float o, float l) {
@@ -126,11 +155,73 @@ __device__ __forceinline__ void store_lse(const AttnParams& p, const Run& r, int
   if (p.lse) p.lse[row] = l != 0.f ? LN2 * (m + log2f(l)) : NEG_INF;
 }
 
+// A cluster's runs joined (p.n_split CTAs of NW * 32 threads): tot [group][D] and
+// ml [group] are each run's sums in its shared memory. This CTA's share of the
+// heads' elements is written, and the masses of its own rows: row_at(i), i in
+// [i0, i1), or -1.
+template <typename T, int D, class RowAt>
+__device__ __forceinline__ void join_cluster(const AttnParams& p, const Run& r, int ls, int split, const float* tot,
+                                             const float2* ml, int i0, int i1, RowAt row_at) {
+  __shared__ float s_m[MAX_GROUP], s_l[MAX_GROUP], s_a[MAX_CLUSTER][MAX_GROUP];
+  const int t = threadIdx.x, G = p.group, ns = p.n_split;
+  cluster_sync(ns);
+  for (int g = t >> 5; g < G; g += NW) {
+    // a lane per run
+    const int u = t & 31;
+    const float2 x = u < ns ? cluster_ld2(ml + g, u, ns) : make_float2(NEG_INF, 0.f);
+    float m = x.x, l = x.y;
+    const bool skip = __any_sync(FULL_MASK, l < 0.f);
+#pragma unroll
+    for (int k = 8; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, k));
+    m = m == NEG_INF ? 0.f : m;
+    const float a = fast_exp2(x.x - m);
+    l *= a;
+#pragma unroll
+    for (int k = 8; k >= 1; k >>= 1) l += __shfl_xor_sync(FULL_MASK, l, k);
+    if (u < ns) s_a[u][g] = a;
+    if (u == 0) {
+      s_m[g] = m;
+      s_l[g] = skip ? -1.f : l;
+    }
+  }
+  __syncthreads();
+  bool skip = false;
+  for (int g = 0; g < G; ++g) skip |= s_l[g] < 0.f;
+  if (!skip) {
+    for (int i = split * NW * 32 + t; i < G * D; i += ns * NW * 32) {
+      const int g = i / D, e = i % D;
+      float o = 0.f;
+      for (int u = 0; u < ns; ++u) o = fmaf(cluster_ld(tot + i, u, ns), s_a[u][g], o);
+      store_out<T, D>(p, r, g, e, o, s_l[g]);
+      if (e == 0) store_lse(p, r, g, s_m[g], s_l[g]);
+    }
+    if (p.mass) {
+      const float* logits = p.logits + static_cast<int64_t>(ls) * p.n_cap * G;
+      float* mass = p.mass + r.s * p.n_cap;
+      // (no weight at all: 2^(x - inf) = 0)
+      float lse2[MAX_GROUP];
+#pragma unroll
+      for (int g = 0; g < MAX_GROUP; ++g) lse2[g] = g < G && s_l[g] != 0.f ? s_m[g] + log2f(s_l[g]) : -NEG_INF;
+      for (int i = i0 + t; i < i1; i += NW * 32) {
+        const int j = row_at(i);
+        if (j < 0) continue;
+        float sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < MAX_GROUP; ++g)
+          if (g < G) sum += fast_exp2(logits[static_cast<int64_t>(j) * G + g] - lse2[g]);
+        mass[j] += sum;
+      }
+    }
+  }
+  cluster_sync(ns);  // a CTA's shared memory stays until the others have read it
+}
+
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_constant__ AttnParams p) {
   using G = TileGeo<D>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float sm_m[NW][8], sm_l[NW][8];
+  __shared__ float2 run_ml[MAX_GROUP];
   __shared__ int bad;
   const int ls = blockIdx.x / p.n_split, split = blockIdx.x % p.n_split;
   const int t = threadIdx.x, w = t >> 5, lane = t & 31, lg = lane >> 2, lt = lane & 3;
@@ -138,8 +229,8 @@ __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_cons
   pdl_launch();
   Run r;
   if (!slice_run(p, ls, r)) {
-    if (t < p.group) p.part_ml[pi + t] = make_float2(NEG_INF, -1.f);
-    return;
+    if (!p.join && t < p.group) p.part_ml[pi + t] = make_float2(NEG_INF, -1.f);
+    return;  // (every run of the slice does)
   }
   if (t == 0) bad = 0;
 
@@ -320,12 +411,9 @@ __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_cons
 #pragma unroll
     for (int c = 0; c < 4; ++c) so[(w * 8 + 2 * lt + (c & 1)) * HS + 16 * i + lg + (c >> 1) * 8] = o[i][c];
   __syncthreads();
-  if (PAGED && bad) {
-    if (t == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
-    if (t < p.group) p.part_ml[pi + t] = make_float2(NEG_INF, -1.f);
-    return;
-  }
-  const bool direct = p.n_split == 1 && !p.mass;
+  if (PAGED && bad && t == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
+  // the run's sums: over the warps, into `tot` (past them in shared memory)
+  float* tot = so + NW * 8 * HS;
   for (int i = t; i < p.group * D; i += NW * 32) {
     const int g = i / D, e = i % D;
     float m = NEG_INF;
@@ -339,20 +427,26 @@ __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_cons
       l = fmaf(sm_l[k][g], a, l);
       acc = fmaf(so[(k * 8 + g) * HS + e], a, acc);
     }
-    if (direct) {
-      store_out<__nv_bfloat16, D>(p, r, g, e, acc, l);
-      if (e == 0) store_lse(p, r, g, m, l);
+    if (PAGED && bad) l = -1.f;
+    if (p.join) {
+      tot[i] = acc;
+      if (e == 0) run_ml[g] = make_float2(m, l);
     } else {
       p.part_o[(pi + g) * D + e] = acc;
       if (e == 0) p.part_ml[pi + g] = make_float2(m, l);
     }
   }
+  if (p.join)
+    join_cluster<__nv_bfloat16, D>(p, r, ls, split, tot, run_ml, u0 * G::TK, u1 * G::TK, [&](int i) {
+      const int j = row_of_tile(i / G::TK) + i % G::TK;
+      return j < r.n && (j < r.vis.s1 || j >= r.vis.w0) ? j : -1;
+    });
 }
 
 // ---------------------------------------------------------------------------
 // fp32 rows
 // ---------------------------------------------------------------------------
-constexpr int DT = 128;   // threads per CTA
+constexpr int DT = NW * 32;  // threads per CTA
 constexpr int LPR = 8;    // lanes per row
 constexpr int GROUPS = DT / LPR;
 
@@ -363,28 +457,26 @@ __global__ void __launch_bounds__(DT) decode_rows_kernel(const __grid_constant__
   __shared__ float sq[GP][D];
   __shared__ float so[GROUPS][D];
   __shared__ float sm_m[GROUPS][GP], sm_l[GROUPS][GP];
+  __shared__ float tot[GP * D];
+  __shared__ float2 run_ml[GP];
   __shared__ int flag;
   const int ls = blockIdx.x / p.n_split, split = blockIdx.x % p.n_split, t = threadIdx.x, G = p.group;
   pdl_launch();
   Run r;
   const int64_t pi = static_cast<int64_t>(blockIdx.x) * G;
-  bool ok = slice_run(p, ls, r);
-  int i0 = 0, i1 = 0;
-  const int32_t* trow = p.rows.seq_table(r.s);
-  if (ok) {
-    i0 = static_cast<int>(static_cast<int64_t>(r.count) * split / p.n_split);
-    i1 = static_cast<int>(static_cast<int64_t>(r.count) * (split + 1) / p.n_split);
-    const int shift = r.vis.w0 - r.vis.s1;
-    bool blocks = p.rows.blocks_ok(trow, i0, min(i1, r.vis.s1), &flag);
-    blocks = p.rows.blocks_ok(trow, max(i0, r.vis.s1) + shift, i1 + shift, &flag) && blocks;
-    if (!blocks) {
-      if (t == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
-      ok = false;
-    }
+  if (!slice_run(p, ls, r)) {
+    if (!p.join && t < G) p.part_ml[pi + t] = make_float2(NEG_INF, -1.f);
+    return;  // (every run of the slice does)
   }
+  const int32_t* trow = p.rows.seq_table(r.s);
+  const int i0 = static_cast<int>(static_cast<int64_t>(r.count) * split / p.n_split);
+  int i1 = static_cast<int>(static_cast<int64_t>(r.count) * (split + 1) / p.n_split);
+  const int shift = r.vis.w0 - r.vis.s1;
+  bool ok = p.rows.blocks_ok(trow, i0, min(i1, r.vis.s1), &flag);
+  ok = p.rows.blocks_ok(trow, max(i0, r.vis.s1) + shift, i1 + shift, &flag) && ok;
   if (!ok) {
-    if (t < G) p.part_ml[pi + t] = make_float2(NEG_INF, -1.f);
-    return;
+    if (t == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
+    i1 = i0;  // nothing is read; the slice is skipped by the join
   }
   const float* q = static_cast<const float*>(p.q) + r.seq * p.q_seq + static_cast<int64_t>(r.h) * G * D;
   for (int i = t; i < GP * D; i += DT) {
@@ -453,7 +545,6 @@ __global__ void __launch_bounds__(DT) decode_rows_kernel(const __grid_constant__
       sm_l[rg][g] = l[g];
     }
   }
-  const bool direct = p.n_split == 1 && !p.mass;
 #pragma unroll
   for (int g = 0; g < GP; ++g) {
     if (g >= G) break;
@@ -467,19 +558,22 @@ __global__ void __launch_bounds__(DT) decode_rows_kernel(const __grid_constant__
 #pragma unroll
       for (int e = 0; e < E; ++e) so[rg][(lane8 + LPR * c) * E + e] = o[g][c * E + e] * a;
     __syncthreads();
-    float sum_l = 0.f;
-    for (int u = 0; u < GROUPS; ++u) sum_l = fmaf(sm_l[u][g], fast_exp2(sm_m[u][g] - mu), sum_l);
     for (int e = t; e < D; e += DT) {
       float sum = 0.f;
       for (int u = 0; u < GROUPS; ++u) sum += so[u][e];
-      if (direct) store_out<float, D>(p, r, g, e, sum, sum_l);
+      if (p.join) tot[g * D + e] = sum;
       else p.part_o[(pi + g) * D + e] = sum;
     }
     if (t == 0) {
-      if (direct) store_lse(p, r, g, mx, sum_l);
-      else p.part_ml[pi + g] = make_float2(mx, sum_l);
+      float sum = 0.f;
+      for (int u = 0; u < GROUPS; ++u) sum = fmaf(sm_l[u][g], fast_exp2(sm_m[u][g] - mu), sum);
+      const float2 x = make_float2(mx, ok ? sum : -1.f);
+      if (p.join) run_ml[g] = x;
+      else p.part_ml[pi + g] = x;
     }
   }
+  if (p.join)
+    join_cluster<float, D>(p, r, ls, split, tot, run_ml, i0, i1, [&](int i) { return i < r.vis.s1 ? i : i + shift; });
 }
 
 // ---------------------------------------------------------------------------
@@ -567,27 +661,52 @@ cudaError_t launch_join(const AttnParams& p, int max_rows, cudaStream_t st) {
   return e;
 }
 
+// The runs, as clusters of a slice's when they join there.
+template <class Kernel>
+cudaError_t launch_runs(Kernel kern, size_t smem, const AttnParams& p, cudaStream_t st) {
+  cudaError_t e;
+  if (smem > 48 * 1024) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  const unsigned ctas = static_cast<unsigned>(p.n_seq * p.n_kv_heads * p.n_split);
+  if (p.join && p.n_split > 1) {
+    if (p.n_split > 8) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(NW * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = static_cast<unsigned>(p.n_split);
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, p);
+  } else {
+    kern<<<ctas, NW * 32, smem, st>>>(p);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
 template <int D>
 cudaError_t launch_bf16(const AttnParams& p, int max_rows, cudaStream_t st) {
-  auto kern = p.rows.table ? decode_tiles_kernel<D, true> : decode_tiles_kernel<D, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TileGeo<D>::SMEM);
-  if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(p.n_seq * p.n_kv_heads * p.n_split), NW * 32, TileGeo<D>::SMEM, st>>>(p);
-  note_launch();
-  e = cudaGetLastError();
-  if (e != cudaSuccess || (p.n_split == 1 && !p.mass)) return e;
-  return launch_join<__nv_bfloat16, D>(p, max_rows, st);
+  const cudaError_t e = launch_runs(p.rows.table ? decode_tiles_kernel<D, true> : decode_tiles_kernel<D, false>,
+                                    TileGeo<D>::SMEM, p, st);
+  return e != cudaSuccess || p.join ? e : launch_join<__nv_bfloat16, D>(p, max_rows, st);
 }
 
 template <int D>
 cudaError_t launch_fp32(const AttnParams& p, int max_rows, cudaStream_t st) {
-  auto kern = p.group == 1 ? decode_rows_kernel<D, 1> : p.group == 2 ? decode_rows_kernel<D, 2>
-            : p.group <= 4 ? decode_rows_kernel<D, 4> : decode_rows_kernel<D, 8>;
-  kern<<<static_cast<unsigned>(p.n_seq * p.n_kv_heads * p.n_split), DT, 0, st>>>(p);
-  note_launch();
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || (p.n_split == 1 && !p.mass)) return e;
-  return launch_join<float, D>(p, max_rows, st);
+  const cudaError_t e = launch_runs(p.group == 1 ? decode_rows_kernel<D, 1> : p.group == 2 ? decode_rows_kernel<D, 2>
+                                    : p.group <= 4 ? decode_rows_kernel<D, 4> : decode_rows_kernel<D, 8>, 0, p, st);
+  return e != cudaSuccess || p.join ? e : launch_join<float, D>(p, max_rows, st);
 }
 
 }  // namespace
@@ -598,18 +717,21 @@ int attn_decode_max_splits(int n_slices, int max_rows) {
 }
 
 // Runs per slice: the count that ends soonest when every slice holds max_rows,
-// SLOTS runs go at a time, and starting and joining a run costs about as long as
-// RUN_COST of its rows.
-int attn_decode_splits(int n_slices, int max_rows) {
-  constexpr int64_t SLOTS = 152 * 2, RUN_COST = 128;
+// SLOTS runs go at a time, starting a run costs about as long as RUN_COST of
+// its rows, and a join by a second kernel as long as JOIN_COST. Clusters of 1,
+// 2, 4, 8 or 16.
+DecodePlan attn_decode_plan(int n_slices, int max_rows) {
+  constexpr int64_t SLOTS = 152 * 2, RUN_COST = 128, JOIN_COST = 160;
   const int most = attn_decode_max_splits(n_slices, max_rows);
-  int best = 1;
+  DecodePlan best{1, true};
   int64_t least = INT64_MAX;
   for (int s = 1; s <= most; ++s) {
-    const int64_t cost = (n_slices * static_cast<int64_t>(s) + SLOTS - 1) / SLOTS * ((max_rows + s - 1) / s + RUN_COST);
+    const bool join = s <= MAX_CLUSTER && (s & (s - 1)) == 0;
+    const int64_t cost = (n_slices * static_cast<int64_t>(s) + SLOTS - 1) / SLOTS * ((max_rows + s - 1) / s + RUN_COST) +
+                         (join ? 0 : JOIN_COST);
     if (cost < least) {
       least = cost;
-      best = s;
+      best = {s, join};
     }
   }
   return best;

@@ -355,7 +355,8 @@ struct AttnParams {
   int64_t lse_seq;                 // elements between its sequences
   float* mass;                     // [S][n_cap], or NULL
   // decode workspace
-  int32_t n_split;                 // CTAs per slice
+  int32_t n_split;                 // CTAs (runs of rows) per slice
+  int32_t join;                    // the runs of a slice are one cluster and join there
   float* part_o;                   // [layer slices][n_split][group][head_dim]: sums of 2^(x - m) v
   float2* part_ml;                 // [layer slices][n_split][group]: m and sum of 2^(x - m); sum -1: skipped
   float* logits;                   // [layer slices][n_cap][group], visible rows (mass only)
@@ -432,9 +433,13 @@ cudaError_t launch_select_compact(const SelectParams& ps, const CompactParams& p
 cudaError_t launch_calibrate(const CalibParams& p, tri_dtype dt, int head_dim,
                              tri_rope_style style, int lh_count, cudaStream_t st);
 int calibrate_split_count(int lh_count, int64_t samples_per_lh);
-// One new token per sequence over the cache; CTAs per slice for it.
-// (and the most it may be, for the workspace: it grows with max_rows).
-int attn_decode_splits(int n_slices, int max_rows);
+// One new token per sequence over the cache: runs per slice and whether a
+// cluster joins them; and the most runs, for the workspace (it grows with max_rows).
+struct DecodePlan {
+  int n_split;
+  bool join;
+};
+DecodePlan attn_decode_plan(int n_slices, int max_rows);
 int attn_decode_max_splits(int n_slices, int max_rows);
 cudaError_t launch_attn_decode(const AttnParams& p, int max_rows, tri_dtype dt, int head_dim, cudaStream_t st);
 // A chunk of new tokens over the cache.
