@@ -85,7 +85,7 @@ struct TileGeo {
   static constexpr int CH = ROW / 16;         // 16-byte chunks per row
   static constexpr int RPI = 32 / CH;         // rows per copy instruction of a warp
   static constexpr int TILE = TK * ROW;       // bytes of one tensor's tile
-  static constexpr int NST = 3;
+  static constexpr int NST = 2;
   static constexpr int WARP_RING = NST * 2 * TILE;
   static constexpr int SMEM = NW * WARP_RING;
   static constexpr int SUB = TK / 16;         // 16-row steps of a tile
@@ -155,6 +155,44 @@ __device__ __forceinline__ void store_lse(const AttnParams& p, const Run& r, int
   if (p.lse) p.lse[row] = l != 0.f ? LN2 * (m + log2f(l)) : NEG_INF;
 }
 
+// mass[j] += sum over the heads of 2^(x_j - m) / l for rows j = row_at(i), i in
+// [i0, i1) (-1: none), with the heads' joined m and l. A thread takes MASS_BATCH
+// rows at a time, all loads before the first store: one by one, the load of a
+// mass waits for the store before it (64 x 8 slices of up to 2176 rows: 66 us).
+constexpr int MASS_BATCH = 8;
+template <class RowAt>
+__device__ __forceinline__ void add_masses(const AttnParams& p, const Run& r, int ls, const float* m, const float* l,
+                                           int i0, int i1, RowAt row_at) {
+  const int G = p.group;
+  const float* logits = p.logits + static_cast<int64_t>(ls) * p.n_cap * G;
+  float* mass = p.mass + r.s * p.n_cap;
+  float lse2[MAX_GROUP];
+#pragma unroll
+  for (int g = 0; g < MAX_GROUP; ++g)  // (no weight at all: 2^(x - inf) = 0)
+    lse2[g] = g < G && l[g] != 0.f ? m[g] + log2f(l[g]) : -NEG_INF;
+  for (int i = i0 + static_cast<int>(threadIdx.x); i < i1; i += MASS_BATCH * NW * 32) {
+    int j[MASS_BATCH];
+    float old[MASS_BATCH], sum[MASS_BATCH];
+#pragma unroll
+    for (int b = 0; b < MASS_BATCH; ++b) {
+      const int ib = i + b * NW * 32;
+      j[b] = ib < i1 ? row_at(ib) : -1;
+      old[b] = j[b] >= 0 ? mass[j[b]] : 0.f;
+      sum[b] = 0.f;
+    }
+#pragma unroll
+    for (int g = 0; g < MAX_GROUP; ++g) {
+      if (g >= G) break;
+#pragma unroll
+      for (int b = 0; b < MASS_BATCH; ++b)
+        if (j[b] >= 0) sum[b] += fast_exp2(logits[static_cast<int64_t>(j[b]) * G + g] - lse2[g]);
+    }
+#pragma unroll
+    for (int b = 0; b < MASS_BATCH; ++b)
+      if (j[b] >= 0) mass[j[b]] = old[b] + sum[b];
+  }
+}
+
 // A cluster's runs joined (p.n_split CTAs of NW * 32 threads): tot [group][D] and
 // ml [group] are each run's sums in its shared memory. This CTA's share of the
 // heads' elements is written, and the masses of its own rows: row_at(i), i in
@@ -196,21 +234,7 @@ __device__ __forceinline__ void join_cluster(const AttnParams& p, const Run& r, 
       if (e == 0) store_lse(p, r, g, s_m[g], s_l[g]);
     }
     if (p.mass) {
-      const float* logits = p.logits + static_cast<int64_t>(ls) * p.n_cap * G;
-      float* mass = p.mass + r.s * p.n_cap;
-      // (no weight at all: 2^(x - inf) = 0)
-      float lse2[MAX_GROUP];
-#pragma unroll
-      for (int g = 0; g < MAX_GROUP; ++g) lse2[g] = g < G && s_l[g] != 0.f ? s_m[g] + log2f(s_l[g]) : -NEG_INF;
-      for (int i = i0 + t; i < i1; i += NW * 32) {
-        const int j = row_at(i);
-        if (j < 0) continue;
-        float sum = 0.f;
-#pragma unroll
-        for (int g = 0; g < MAX_GROUP; ++g)
-          if (g < G) sum += fast_exp2(logits[static_cast<int64_t>(j) * G + g] - lse2[g]);
-        mass[j] += sum;
-      }
+      add_masses(p, r, ls, s_m, s_l, i0, i1, row_at);
     }
   }
   cluster_sync(ns);  // a CTA's shared memory stays until the others have read it
@@ -581,13 +605,13 @@ __global__ void __launch_bounds__(DT) decode_rows_kernel(const __grid_constant__
 // takes visible rows [c, c + 1) * JROWS: mass[j] += sum over the heads of
 // 2^(x_j - m) / l.
 // ---------------------------------------------------------------------------
-constexpr int JT = 128;
+constexpr int JT = NW * 32;
 constexpr int JROWS = 1024;
 constexpr int MAX_SPLIT = 128;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(JT) decode_join_kernel(const __grid_constant__ AttnParams p, int chunks) {
-  __shared__ float lse2[MAX_GROUP], s_m[MAX_GROUP], s_l[MAX_GROUP];
+  __shared__ float s_m[MAX_GROUP], s_l[MAX_GROUP];
   __shared__ int skip;
   const int ls = blockIdx.x / chunks, c = blockIdx.x % chunks, t = threadIdx.x, G = p.group;
   if (t == 0) skip = 0;
@@ -617,7 +641,6 @@ __global__ void __launch_bounds__(JT) decode_join_kernel(const __grid_constant__
     if ((t & 31) == 0) {
       s_m[g] = mu;
       s_l[g] = l;
-      lse2[g] = l != 0.f ? m + log2f(l) : -NEG_INF;  // (no weight at all: 2^(x - inf) = 0)
     }
   }
   __syncthreads();
@@ -633,15 +656,8 @@ __global__ void __launch_bounds__(JT) decode_join_kernel(const __grid_constant__
     if (t == 0) store_lse(p, r, c, s_m[c], s_l[c]);
   }
   if (!p.mass) return;
-  const float* logits = p.logits + static_cast<int64_t>(ls) * p.n_cap * G;
-  float* mass = p.mass + r.s * p.n_cap;
-  const int end = min(r.count, (c + 1) * JROWS);
-  for (int i = c * JROWS + t; i < end; i += JT) {
-    const int j = i < r.vis.s1 ? i : i - r.vis.s1 + r.vis.w0;
-    float sum = 0.f;
-    for (int g = 0; g < G; ++g) sum += fast_exp2(logits[static_cast<int64_t>(j) * G + g] - lse2[g]);
-    mass[j] += sum;
-  }
+  add_masses(p, r, ls, s_m, s_l, c * JROWS, min(r.count, (c + 1) * JROWS),
+             [&](int i) { return i < r.vis.s1 ? i : i - r.vis.s1 + r.vis.w0; });
 }
 
 template <typename T, int D>
@@ -712,29 +728,39 @@ cudaError_t launch_fp32(const AttnParams& p, int max_rows, cudaStream_t st) {
 }  // namespace
 
 int attn_decode_max_splits(int n_slices, int max_rows) {
-  const int fill = max(1, 152 * 8 / n_slices), most = (max_rows + 63) / 64;
+  const int fill = max(MAX_CLUSTER, 608 / n_slices), most = (max_rows + 63) / 64;
   return max(1, min(min(MAX_SPLIT, fill), most));
 }
 
-// Runs per slice: the count that ends soonest when every slice holds max_rows,
-// SLOTS runs go at a time, starting a run costs about as long as RUN_COST of
-// its rows, and a join by a second kernel as long as JOIN_COST. Clusters of 1,
-// 2, 4, 8 or 16.
-DecodePlan attn_decode_plan(int n_slices, int max_rows) {
-  constexpr int64_t SLOTS = 152 * 2, RUN_COST = 128, JOIN_COST = 160;
-  const int most = attn_decode_max_splits(n_slices, max_rows);
-  DecodePlan best{1, true};
-  int64_t least = INT64_MAX;
-  for (int s = 1; s <= most; ++s) {
-    const bool join = s <= MAX_CLUSTER && (s & (s - 1)) == 0;
-    const int64_t cost = (n_slices * static_cast<int64_t>(s) + SLOTS - 1) / SLOTS * ((max_rows + s - 1) / s + RUN_COST) +
-                         (join ? 0 : JOIN_COST);
-    if (cost < least) {
-      least = cost;
-      best = {s, join};
-    }
+// Runs per slice, for slices of max_rows. Measured (us; bf16, d 128, group 4;
+// c: joined in a cluster, k: by a second kernel):
+//   slices x rows   1c    2c    4c    8c    16c   3k    6k    12k   19k   38k   76k
+//     8 x 2113     24.6  15.2  10.1   7.9   7.9  12.5   8.8   7.6   8.2   9.7    -
+//     8 x 32768   305.4 156.4  82.0  45.3  32.5 107.3  58.1  35.1  30.5  29.5  36.4
+//    32 x 8192     82.4  45.6  29.2  25.4  33.0  35.2  28.0  27.6  31.7  34.0  42.7
+//   128 x 8192     95.9  80.5  95.5  88.3 103.2  85.2  83.2  86.3  88.8  94.0    -
+//   256 x 2048     45.4  56.2  52.2  57.2  97.9  47.7  50.6  54.1  58.3    -     -
+// A run's start and end cost a few microseconds, so the best has as few runs as
+// fill the GPU once (`slots` of them) and no more: a cluster of the largest
+// power of two within that. Few slices of long rows need more runs than a
+// cluster holds; more slices than slots that leave the last wave part empty are
+// cut into a few runs (512 slices of 2048 rows, d 64, group 1, masses: 1c 62.9,
+// 3k 54.4). fp32 runs stream slower, so more of them are wanted.
+DecodePlan attn_decode_plan(int n_slices, int max_rows, tri_dtype dt, int group) {
+  const int64_t n = n_slices;
+  const int64_t slots = dt == TRI_BF16 ? 2 * 152 : group <= 2 ? 4 * 152 : 3 * 152;
+  int s = 1;
+  while (2 * s <= MAX_CLUSTER && n * 2 * s <= slots && max_rows >= 64 * 2 * s) s *= 2;
+  if (n * s * 3 <= slots * 2 && max_rows >= 512 * s) {
+    const int64_t k = min(min(slots / n, static_cast<int64_t>(max_rows / 384)), static_cast<int64_t>(MAX_SPLIT));
+    if (k > s) return {static_cast<int>(k), false};
   }
-  return best;
+  if (n > slots && max_rows >= 4 * 512) {
+    constexpr int64_t WAVE = 3 * 152;
+    for (int k = 1; k <= 4; ++k)
+      if (n * k * 5 >= (n * k + WAVE - 1) / WAVE * WAVE * 4) return {k, k == 1};
+  }
+  return {s, true};
 }
 
 cudaError_t launch_attn_decode(const AttnParams& p, int max_rows, tri_dtype dt, int head_dim, cudaStream_t st) {

@@ -1,12 +1,321 @@
 // attn_prefill.cu -- causal attention of a chunk of new tokens over the cache,
 // optionally windowed with first rows that stay visible.
+//
+// The group's query heads share a KV head's rows, so a query row is a (token,
+// head) pair and a tile packs 128 of them. Per pair of a query row and a cached
+// row it sees: 4 D flop and one exponential.
+//
+// bf16 rows (prefill_tc_kernel): tcgen05, one CTA per SM with two query tiles,
+// so that the tensor cores work on one tile while the other's weights are
+// formed. Roles:
+//   - the copy warp brings the cache's 128-row tiles of K and V, in turn, into a
+//     ring by TMA (a pool's blocks as boxes of a tile);
+//   - the MMA warp's elected thread issues, per tile of rows and query tile,
+//     O += P V for the previous weights and S = Q K^T for the next ones;
+//   - a warpgroup per query tile turns S into P: thread = query row = lane of
+//     tensor memory. P, rounded to bf16, takes S's place as the A operand of
+//     the product with V, so the weights never pass through shared memory.
+// Tensor memory: S/P of the two tiles 2 x 128 columns, O 2 x D columns.
+// The running maximum of a row is raised only when a tile exceeds it by more
+// than 8 (a factor of 256): O is then rescaled in tensor memory; until then
+// weights are up to 256, which costs no precision in a floating format. S of a
+// tile is complete only after the products with V issued before it, so the
+// warpgroup that has seen it may rescale O.
+// Tiles at the edge of what the rows see are masked by position; rows of V past
+// the last query's are set to zero in shared memory, whatever they hold.
+//
+// fp32 rows (prefill_kernel): CUDA cores, 64 x 64 tiles in shared memory.
 #include <cuda_runtime.h>
 
+#include "attn_tc.cuh"
 #include "attn_tile.cuh"
 
 namespace tri {
 namespace {
 
+// ---------------------------------------------------------------------------
+// bf16 rows
+// ---------------------------------------------------------------------------
+constexpr int PT = 384;  // copy warp, MMA warp, two idle, two warpgroups
+constexpr float RAISE = 8.f;
+
+template <int D>
+struct TcSmem {
+  static constexpr int TILE = D / 64 * TCOL;
+  static constexpr int NST = D == 128 ? 4 : 8;
+  static constexpr int RING = 2 * TILE;  // after the two query tiles
+  static constexpr int CTRL = RING + NST * TILE;
+  static constexpr int BYTES = CTRL + 512 + 1024;  // (1024: the tiles start on a multiple of it)
+};
+
+struct TcCtl {
+  uint64_t full[8], empty[8];          // ring stages
+  uint64_t q_ready[2];                 // the query tile is in shared memory
+  uint64_t s_full[2], p_ready[2];      // S complete; P written (and S read)
+  uint64_t o_done[2];                  // every product of the tile complete
+  uint64_t v_fix;                      // the last tile of V has landed, before its tail is cleared
+  uint32_t tmem;
+  int flag;
+};
+
+template <int D>
+__global__ void __launch_bounds__(PT, 1)
+    prefill_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap, int box_rows, int n_tiles) {
+  using L = TcSmem<D>;
+  extern __shared__ unsigned char raw[];
+  unsigned char* smem = raw + (-smem_addr(raw) & 1023u);
+  TcCtl& ctl = *reinterpret_cast<TcCtl*>(smem + L::CTRL);
+  const int t = threadIdx.x, w = t >> 5, lane = t & 31, G = p.group;
+  // the last tokens see the most rows: their tiles first
+  const int n_ls = p.n_seq * p.n_kv_heads;
+  const int ls = blockIdx.x % n_ls, tile = n_tiles - 1 - static_cast<int>(blockIdx.x) / n_ls;
+  Chunk c;
+  if (!chunk_of(p, ls, c)) return;
+  const int tpt = TROWS / G;  // tokens per query tile
+  const int tok0 = tile * 2 * tpt;
+  if (tok0 >= c.n_new) return;
+  const int toks0 = min(tpt, c.n_new - tok0), toks1 = min(tpt, c.n_new - tok0 - toks0);
+  const int nq = toks1 > 0 ? 2 : 1;
+  const int rf0 = c.r0 + tok0, rl0 = rf0 + toks0 - 1;
+  const int rf1 = rl0 + 1, rl1 = rl0 + toks1;  // (empty when nq is 1)
+  const int r_hi = rl1;
+  const int32_t* trow = p.rows.seq_table(c.s);
+  if (!chunk_blocks_ok(p, trow, rf0, r_hi, &ctl.flag)) return;
+  const TileList list = tiles_seen(p, rf0, r_hi);
+  const int n_list = list.count();
+  auto needed = [&](int q, int i) {
+    const int k0 = list.at(i) * TROWS;
+    return q == 0 ? tile_seen(p, k0, TROWS, rf0, rl0) : q < nq && tile_seen(p, k0, TROWS, rf1, rl1);
+  };
+
+  if (t == 0) {
+    for (int i = 0; i < L::NST; ++i) {
+      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.empty[i], 1);
+    }
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(&ctl.q_ready[q], 128);
+      mbar_init(&ctl.s_full[q], 1);
+      mbar_init(&ctl.p_ready[q], 128);
+      mbar_init(&ctl.o_done[q], 1);
+    }
+    mbar_init(&ctl.v_fix, 1);
+    mbar_init_fence();
+  }
+  if (w == 1) tmem_alloc(&ctl.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = ctl.tmem;
+  const uint32_t qa = smem_addr(smem), ring = qa + L::RING;
+  bool ok = true;
+
+  if (w == 0) {
+    // ---- copies: K and V tiles take the ring's stages in turn ----
+    int cnt = 0;
+    for (; cnt < 2 * n_list && ok; ++cnt) {
+      const int st = cnt % L::NST, k0 = list.at(cnt >> 1) * TROWS;
+      if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
+      if (!ok) break;
+      const bool is_v = cnt & 1;
+      const bool fix = is_v && k0 + TROWS - 1 > r_hi;
+      uint64_t* bar = fix ? &ctl.v_fix : &ctl.full[st];
+      if (lane == 0) mbar_arrive_expect_tx(bar, L::TILE);
+      __syncwarp();
+      load_tile<D>(ring + st * L::TILE, is_v ? &vmap : &kmap, p, box_rows, trow, c.seq, c.h, k0, c.n, bar, lane);
+      if (fix) {
+        ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.v_fix, 0));
+        if (!ok) break;
+        unsigned char* v = smem + L::RING + st * L::TILE;
+        for (int i = (r_hi + 1 - k0) * 8 + lane; i < TROWS * 8; i += 32)
+#pragma unroll
+          for (int a = 0; a < D / 64; ++a) *reinterpret_cast<uint4*>(v + a * TCOL + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.full[st]);
+      }
+    }
+    if (!ok && lane == 0) {
+      set_status(p.dev_status, TRI_DEV_TIMEOUT);
+      // let the copies in flight finish before shared memory is given up
+      for (int u = max(0, cnt - L::NST); u < cnt; ++u) (void)mbar_wait_bounded(&ctl.full[u % L::NST], (u / L::NST) & 1);
+    }
+  } else if (w == 1) {
+    // ---- MMAs ----
+    if (elect_one()) {
+      constexpr uint32_t IQK = bf16_idesc(TROWS, TROWS, false), IPV = bf16_idesc(TROWS, D, true);
+      bool begun[2] = {false, false};
+      int np[2] = {0, 0};  // weights taken so far
+      auto wait_stage = [&](int cnt) { return mbar_wait_bounded(&ctl.full[cnt % L::NST], (cnt / L::NST) & 1); };
+      auto issue_s = [&](int q, int i) {
+        umma_rows<D>(tm + q * 128, qa + q * L::TILE, ring + (2 * i) % L::NST * L::TILE, IQK);
+        umma_commit(&ctl.s_full[q]);
+      };
+      for (int q = 0; q < nq && ok; ++q) ok = mbar_wait_bounded(&ctl.q_ready[q], 0);
+      if (n_list > 0 && ok) {
+        ok = wait_stage(0);
+        tc_fence_after();
+        for (int q = 0; q < nq && ok; ++q)
+          if (needed(q, 0)) issue_s(q, 0);
+        umma_commit(&ctl.empty[0]);
+      }
+      for (int i = 0; i < n_list && ok; ++i) {
+        const bool more = i + 1 < n_list;
+        ok = wait_stage(2 * i + 1) && (!more || wait_stage(2 * i + 2));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t v = ring + (2 * i + 1) % L::NST * L::TILE;
+        for (int q = 0; q < nq; ++q) {
+          if (needed(q, i)) {
+            ok = mbar_wait_bounded(&ctl.p_ready[q], np[q] & 1);
+            if (!ok) break;
+            ++np[q];
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < TROWS / 16; ++k)
+              umma_ts(tm + 256 + q * 128, tm + q * 128 + k * 8, sw128_desc_mn(v + k * 2048), IPV, begun[q] || k > 0);
+            begun[q] = true;
+          }
+          if (more && needed(q, i + 1)) issue_s(q, i + 1);
+        }
+        if (!ok) break;
+        umma_commit(&ctl.empty[(2 * i + 1) % L::NST]);
+        if (more) umma_commit(&ctl.empty[(2 * i + 2) % L::NST]);
+      }
+      umma_commit(&ctl.o_done[0]);
+      umma_commit(&ctl.o_done[1]);
+      if (!ok) set_status(p.dev_status, TRI_DEV_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (w >= 4 && (w < 8 || nq == 2)) {
+    // ---- weights: warpgroup q, thread u = query row u of tile q ----
+    const int q = (w - 4) >> 2, u = (t - 128) & 127;
+    const int toks = q ? toks1 : toks0, rows = toks * G, rf = q ? rf1 : rf0, rl = q ? rl1 : rl0;
+    load_query_tile<D>(smem + q * L::TILE, p, c.seq, c.h, tok0 + q * tpt, rows, u);
+    fence_proxy_async_smem();
+    mbar_arrive(&ctl.q_ready[q]);
+    const uint32_t lanes = static_cast<uint32_t>((w & 3) * 32) << 16;
+    const uint32_t ts = tm + q * 128 + lanes, to = tm + 256 + q * 128 + lanes;
+    const int r = rf + u / G;
+    const float sl = p.scale * LOG2E;
+    float m = NEG_INF, l = 0.f;
+    int ns = 0;
+    for (int i = 0; i < n_list; ++i) {
+      if (!needed(q, i)) continue;
+      ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[q], ns & 1));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t x[128];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmem_ld32(ts + k * 32, x + k * 32);
+      tmem_wait_ld();
+      const int k0 = list.at(i) * TROWS;
+      const bool inner = k0 + TROWS - 1 <= rf && (p.window == 0 || k0 > rl - p.window || k0 + TROWS <= p.n_sink);
+      if (!inner) {
+        const int hi = r - k0;                                    // columns <= hi
+        const int lo = p.window ? max(r - p.window, -1) - k0 : -1;  // and > lo, or < sink
+        const int sink = p.window ? p.n_sink - k0 : 0;
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if (k > hi || (k <= lo && k >= sink)) x[k] = 0xff800000u;  // -inf
+      }
+      float mx = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+#pragma unroll
+      for (int k = 2; k < 128; k += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+      mx *= sl;
+      if (ns == 0) {
+        m = mx;
+      } else if (__any_sync(FULL_MASK, mx > m + RAISE)) {
+        const float mn = fmaxf(m, mx);
+        const float a = mn == NEG_INF ? 1.f : fast_exp2(m - mn);
+        m = mn;
+        l *= a;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t o[32];
+          tmem_ld32(to + k * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+          tmem_st32(to + k * 32, o);
+        }
+      }
+      const float mu = m == NEG_INF ? 0.f : m;
+      float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < 64; ++k) {
+        const float e0 = fast_exp2(fmaf(__uint_as_float(x[2 * k]), sl, -mu));
+        const float e1 = fast_exp2(fmaf(__uint_as_float(x[2 * k + 1]), sl, -mu));
+        l0 += e0;
+        l1 += e1;
+        x[k] = pack_bf16(e0, e1);
+      }
+      l += l0 + l1;
+      tmem_st32(ts, x);
+      tmem_st32(ts + 32, x + 32);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&ctl.p_ready[q]);
+      ++ns;
+    }
+    if (ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.o_done[q], 0));
+    if (!ok) {
+      if (lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
+    } else {
+      tc_fence_after();
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      const int64_t head = (static_cast<int64_t>(c.seq) * p.n_q + tok0 + q * tpt + u / G) * (p.n_kv_heads * G) + c.h * G + u % G;
+      uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + head * D);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t o[32];
+        if (ns > 0) {
+          tmem_ld32(to + k * 32, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (u < rows) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t y[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+              y[f] = pack_bf16(__uint_as_float(o[8 * e + 2 * f]) * inv, __uint_as_float(o[8 * e + 2 * f + 1]) * inv);
+            out[k * 4 + e] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+      if (p.lse && u < rows) p.lse[head] = l != 0.f ? LN2 * (m + log2f(l)) : NEG_INF;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (w == 1) tmem_dealloc(tm, 512);
+}
+
+template <int D>
+cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
+  CUtensorMap kmap, vmap;
+  const int box_rows = encode_rows(&kmap, p.k, p, D);
+  if (!box_rows || !encode_rows(&vmap, p.v, p, D)) return cudaErrorInvalidValue;
+  auto kern = prefill_tc_kernel<D>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D>::BYTES);
+  if (e != cudaSuccess) return e;
+  const int tokens = 2 * (TROWS / p.group), n_tiles = (p.n_q + tokens - 1) / tokens;
+  const int64_t ctas = static_cast<int64_t>(p.n_seq) * p.n_kv_heads * n_tiles;
+  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  kern<<<static_cast<unsigned>(ctas), PT, TcSmem<D>::BYTES, st>>>(p, kmap, vmap, box_rows, n_tiles);
+  note_launch();
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// fp32 rows
+// ---------------------------------------------------------------------------
 template <int D>
 struct PrefillSmem {
   float q[FM][D + 4];
@@ -119,7 +428,7 @@ cudaError_t launch_typed(const AttnParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attn_prefill(const AttnParams& p, tri_dtype dt, int head_dim, cudaStream_t st) {
-  if (dt == TRI_BF16) return head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(p, st) : launch_typed<__nv_bfloat16, 128>(p, st);
+  if (dt == TRI_BF16) return head_dim == 64 ? launch_tc<64>(p, st) : launch_tc<128>(p, st);
   return head_dim == 64 ? launch_typed<float, 64>(p, st) : launch_typed<float, 128>(p, st);
 }
 
