@@ -38,6 +38,7 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr int PT = 384;  // copy warp, MMA warp, two idle, two warpgroups
 constexpr float RAISE = 8.f;
+constexpr int REGS_LESS = 56, REGS_MORE = 216;
 
 template <int D>
 struct TcSmem {
@@ -111,7 +112,9 @@ __global__ void __launch_bounds__(PT, 1)
   const uint32_t qa = smem_addr(smem), ring = qa + L::RING;
   bool ok = true;
 
+  // registers: 128 * REGS_LESS + 256 * REGS_MORE <= 384 * 168
   if (w == 0) {
+    regs_less<REGS_LESS>();
     // ---- copies: K and V tiles take the ring's stages in turn ----
     int cnt = 0;
     for (; cnt < 2 * n_list && ok; ++cnt) {
@@ -142,6 +145,7 @@ __global__ void __launch_bounds__(PT, 1)
       for (int u = max(0, cnt - L::NST); u < cnt; ++u) (void)mbar_wait_bounded(&ctl.full[u % L::NST], (u / L::NST) & 1);
     }
   } else if (w == 1) {
+    regs_less<REGS_LESS>();
     // ---- MMAs ----
     if (elect_one()) {
       constexpr uint32_t IQK = bf16_idesc(TROWS, TROWS, false), IPV = bf16_idesc(TROWS, D, true);
@@ -188,7 +192,10 @@ __global__ void __launch_bounds__(PT, 1)
       if (!ok) set_status(p.dev_status, TRI_DEV_TIMEOUT);
     }
     __syncwarp();
-  } else if (w >= 4 && (w < 8 || nq == 2)) {
+  } else if (w < 4) {
+    regs_less<REGS_LESS>();
+  } else if (w < 8 || nq == 2) {
+    regs_more<REGS_MORE>();
     // ---- weights: warpgroup q, thread u = query row u of tile q ----
     const int q = (w - 4) >> 2, u = (t - 128) & 127;
     const int toks = q ? toks1 : toks0, rows = toks * G, rf = q ? rf1 : rf0, rl = q ? rl1 : rl0;
@@ -213,16 +220,23 @@ __global__ void __launch_bounds__(PT, 1)
       const int k0 = list.at(i) * TROWS;
       const bool inner = k0 + TROWS - 1 <= rf && (p.window == 0 || k0 > rl - p.window || k0 + TROWS <= p.n_sink);
       if (!inner) {
-        const int hi = r - k0;                                    // columns <= hi
-        const int lo = p.window ? max(r - p.window, -1) - k0 : -1;  // and > lo, or < sink
-        const int sink = p.window ? p.n_sink - k0 : 0;
 #pragma unroll
-        for (int k = 0; k < 128; ++k)
-          if (k > hi || (k <= lo && k >= sink)) x[k] = 0xff800000u;  // -inf
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t bits = seen_bits(p, r, k0, k);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(bits & (1u << e))) x[32 * k + e] = 0xff800000u;  // -inf
+        }
       }
-      float mx = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+      float mxs[4];  // (four chains)
 #pragma unroll
-      for (int k = 2; k < 128; k += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+      for (int k = 0; k < 4; ++k) {
+        mxs[k] = __uint_as_float(x[k]);
+#pragma unroll
+        for (int e = 4; e < 124; e += 8) mxs[k] = max3(mxs[k], __uint_as_float(x[e + k]), __uint_as_float(x[e + 4 + k]));
+        mxs[k] = fmaxf(mxs[k], __uint_as_float(x[124 + k]));
+      }
+      float mx = fmaxf(max3(mxs[0], mxs[1], mxs[2]), mxs[3]);
       mx *= sl;
       if (ns == 0) {
         m = mx;
@@ -242,16 +256,22 @@ __global__ void __launch_bounds__(PT, 1)
         }
       }
       const float mu = m == NEG_INF ? 0.f : m;
-      float l0 = 0.f, l1 = 0.f;
+      float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
-      for (int k = 0; k < 64; ++k) {
-        const float e0 = fast_exp2(fmaf(__uint_as_float(x[2 * k]), sl, -mu));
-        const float e1 = fast_exp2(fmaf(__uint_as_float(x[2 * k + 1]), sl, -mu));
-        l0 += e0;
-        l1 += e1;
+      for (int k = 0; k < 64; k += 2) {
+        float e0, e1, e2, e3;
+        fma2(e0, e1, __uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), sl, -mu);
+        fma2(e2, e3, __uint_as_float(x[2 * k + 2]), __uint_as_float(x[2 * k + 3]), sl, -mu);
+        e0 = fast_exp2(e0);
+        e1 = fast_exp2(e1);
+        e2 = fast_exp2(e2);
+        e3 = fast_exp2(e3);
+        add2(l0, l1, e0, e1);
+        add2(l2, l3, e2, e3);
         x[k] = pack_bf16(e0, e1);
+        x[k + 1] = pack_bf16(e2, e3);
       }
-      l += l0 + l1;
+      l += (l0 + l1) + (l2 + l3);
       tmem_st32(ts, x);
       tmem_st32(ts + 32, x + 32);
       tmem_wait_st();
