@@ -12,9 +12,13 @@
 //     ring by TMA (a pool's blocks as boxes of a tile);
 //   - the MMA warp's elected thread issues, per tile of rows and query tile,
 //     O += P V for the previous weights and S = Q K^T for the next ones;
-//   - a warpgroup per query tile turns S into P: thread = query row = lane of
-//     tensor memory. P, rounded to bf16, takes S's place as the A operand of
-//     the product with V, so the weights never pass through shared memory.
+//   - two warpgroups per query tile turn S into P: a thread has 64 of a query
+//     row's columns (row = lane of tensor memory), and two threads share their
+//     row's maximum through shared memory. (One thread per row measured 435
+//     instead of XXX us on the 8192-token prompt: the weights of one tile took
+//     longer than the products of the other.) P, rounded to bf16, takes S's
+//     place as the A operand of the product with V, so the weights never pass
+//     through shared memory.
 // Tensor memory: S/P of the two tiles 2 x 128 columns, O 2 x D columns.
 // The running maximum of a row is raised only when a tile exceeds it by more
 // than 8 (a factor of 256): O is then rescaled in tensor memory; until then
@@ -36,9 +40,9 @@ namespace {
 // ---------------------------------------------------------------------------
 // bf16 rows
 // ---------------------------------------------------------------------------
-constexpr int PT = 384;  // copy warp, MMA warp, two idle, two warpgroups
+constexpr int PT = 640;  // copy warp, MMA warp, two idle, four warpgroups
 constexpr float RAISE = 8.f;
-constexpr int REGS_LESS = 56, REGS_MORE = 216;
+constexpr int REGS_LESS = 56, REGS_MORE = 104;  // 128 * 56 + 512 * 104 <= 640 * 96
 
 template <int D>
 struct TcSmem {
@@ -46,7 +50,7 @@ struct TcSmem {
   static constexpr int NST = D == 128 ? 4 : 8;
   static constexpr int RING = 2 * TILE;  // after the two query tiles
   static constexpr int CTRL = RING + NST * TILE;
-  static constexpr int BYTES = CTRL + 512 + 1024;  // (1024: the tiles start on a multiple of it)
+  static constexpr int BYTES = CTRL + 4096 + 512 + 1024;  // (1024: the tiles start on a multiple of it)
 };
 
 struct TcCtl {
@@ -57,6 +61,7 @@ struct TcCtl {
   uint64_t v_fix;                      // the last tile of V has landed, before its tail is cleared
   uint32_t tmem;
   int flag;
+  float mx[2][2][2][TROWS];            // maxima: [tile parity][query tile][half][row]
 };
 
 template <int D>
@@ -96,9 +101,9 @@ __global__ void __launch_bounds__(PT, 1)
       mbar_init(&ctl.empty[i], 1);
     }
     for (int q = 0; q < 2; ++q) {
-      mbar_init(&ctl.q_ready[q], 128);
+      mbar_init(&ctl.q_ready[q], 256);
       mbar_init(&ctl.s_full[q], 1);
-      mbar_init(&ctl.p_ready[q], 128);
+      mbar_init(&ctl.p_ready[q], 256);
       mbar_init(&ctl.o_done[q], 1);
     }
     mbar_init(&ctl.v_fix, 1);
@@ -112,7 +117,6 @@ __global__ void __launch_bounds__(PT, 1)
   const uint32_t qa = smem_addr(smem), ring = qa + L::RING;
   bool ok = true;
 
-  // registers: 128 * REGS_LESS + 256 * REGS_MORE <= 384 * 168
   if (w == 0) {
     regs_less<REGS_LESS>();
     // ---- copies: K and V tiles take the ring's stages in turn ----
@@ -194,35 +198,37 @@ __global__ void __launch_bounds__(PT, 1)
     __syncwarp();
   } else if (w < 4) {
     regs_less<REGS_LESS>();
-  } else if (w < 8 || nq == 2) {
+  } else if (w < 12 || nq == 2) {
     regs_more<REGS_MORE>();
-    // ---- weights: warpgroup q, thread u = query row u of tile q ----
-    const int q = (w - 4) >> 2, u = (t - 128) & 127;
+    // ---- weights: thread u of a half = query row u of tile q, 64 columns ----
+    const int q = (w - 4) >> 3, half = ((w - 4) >> 2) & 1, u = t & 127;
     const int toks = q ? toks1 : toks0, rows = toks * G, rf = q ? rf1 : rf0, rl = q ? rl1 : rl0;
-    load_query_tile<D>(smem + q * L::TILE, p, c.seq, c.h, tok0 + q * tpt, rows, u);
+    load_query_tile<D, 256>(smem + q * L::TILE, p, c.seq, c.h, tok0 + q * tpt, rows, half * 128 + u);
     fence_proxy_async_smem();
     mbar_arrive(&ctl.q_ready[q]);
     const uint32_t lanes = static_cast<uint32_t>((w & 3) * 32) << 16;
-    const uint32_t ts = tm + q * 128 + lanes, to = tm + 256 + q * 128 + lanes;
+    const uint32_t ts = tm + q * 128 + lanes, to = tm + 256 + q * 128 + half * (D / 2) + lanes;
     const int r = rf + u / G;
+    const int pair = 1 + q * 4 + (w & 3);  // named barrier of the two warps of 32 rows
     const float sl = p.scale * LOG2E;
     float m = NEG_INF, l = 0.f;
     int ns = 0;
     for (int i = 0; i < n_list; ++i) {
       if (!needed(q, i)) continue;
-      ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[q], ns & 1));
-      if (!ok) break;
+      // (after a wait that gave up the loop runs on without waiting, since the
+      // two halves meet at barriers)
+      if (ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[q], ns & 1));
       tc_fence_after();
-      uint32_t x[128];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_ld32(ts + k * 32, x + k * 32);
+      uint32_t x[64];
+      tmem_ld32(ts + half * 64, x);
+      tmem_ld32(ts + half * 64 + 32, x + 32);
       tmem_wait_ld();
       const int k0 = list.at(i) * TROWS;
       const bool inner = k0 + TROWS - 1 <= rf && (p.window == 0 || k0 > rl - p.window || k0 + TROWS <= p.n_sink);
       if (!inner) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t bits = seen_bits(p, r, k0, k);
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t bits = seen_bits(p, r, k0, half * 2 + k);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (!(bits & (1u << e))) x[32 * k + e] = 0xff800000u;  // -inf
@@ -233,32 +239,37 @@ __global__ void __launch_bounds__(PT, 1)
       for (int k = 0; k < 4; ++k) {
         mxs[k] = __uint_as_float(x[k]);
 #pragma unroll
-        for (int e = 4; e < 124; e += 8) mxs[k] = max3(mxs[k], __uint_as_float(x[e + k]), __uint_as_float(x[e + 4 + k]));
-        mxs[k] = fmaxf(mxs[k], __uint_as_float(x[124 + k]));
+        for (int e = 4; e < 60; e += 8) mxs[k] = max3(mxs[k], __uint_as_float(x[e + k]), __uint_as_float(x[e + 4 + k]));
+        mxs[k] = fmaxf(mxs[k], __uint_as_float(x[60 + k]));
       }
       float mx = fmaxf(max3(mxs[0], mxs[1], mxs[2]), mxs[3]);
-      mx *= sl;
+      ctl.mx[ns & 1][q][half][u] = mx;
+      // after this both halves have read S, so either may store P over it
+      tc_fence_before();
+      asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+      tc_fence_after();
+      mx = fmaxf(mx, ctl.mx[ns & 1][q][half ^ 1][u]) * sl;
       if (ns == 0) {
         m = mx;
-      } else if (__any_sync(FULL_MASK, mx > m + RAISE)) {
+      } else if (__any_sync(FULL_MASK, mx > m + RAISE)) {  // (the same in both halves)
         const float mn = fmaxf(m, mx);
         const float a = mn == NEG_INF ? 1.f : fast_exp2(m - mn);
         m = mn;
         l *= a;
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          uint32_t o[32];
-          tmem_ld32(to + k * 32, o);
+        for (int k = 0; k < D / 16; ++k) {  // (few registers are left)
+          uint32_t o[8];
+          tmem_ld8(to + k * 8, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-          tmem_st32(to + k * 32, o);
+          for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+          tmem_st8(to + k * 8, o);
         }
       }
       const float mu = m == NEG_INF ? 0.f : m;
       float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
-      for (int k = 0; k < 64; k += 2) {
+      for (int k = 0; k < 32; k += 2) {
         float e0, e1, e2, e3;
         fma2(e0, e1, __uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), sl, -mu);
         fma2(e2, e3, __uint_as_float(x[2 * k + 2]), __uint_as_float(x[2 * k + 3]), sl, -mu);
@@ -272,23 +283,26 @@ __global__ void __launch_bounds__(PT, 1)
         x[k + 1] = pack_bf16(e2, e3);
       }
       l += (l0 + l1) + (l2 + l3);
-      tmem_st32(ts, x);
-      tmem_st32(ts + 32, x + 32);
+      tmem_st32(ts + half * 32, x);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&ctl.p_ready[q]);
       ++ns;
     }
     if (ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.o_done[q], 0));
+    ctl.mx[ns & 1][q][half][u] = l;
+    asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+    const float l_half = ctl.mx[ns & 1][q][half ^ 1][u];
+    l = half ? l_half + l : l + l_half;
     if (!ok) {
       if (lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
     } else {
       tc_fence_after();
       const float inv = l != 0.f ? 1.f / l : 0.f;
       const int64_t head = (static_cast<int64_t>(c.seq) * p.n_q + tok0 + q * tpt + u / G) * (p.n_kv_heads * G) + c.h * G + u % G;
-      uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + head * D);
+      uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + head * D + half * (D / 2));
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
+      for (int k = 0; k < D / 64; ++k) {
         uint32_t o[32];
         if (ns > 0) {
           tmem_ld32(to + k * 32, o);
@@ -308,7 +322,7 @@ __global__ void __launch_bounds__(PT, 1)
           }
         }
       }
-      if (p.lse && u < rows) p.lse[head] = l != 0.f ? LN2 * (m + log2f(l)) : NEG_INF;
+      if (p.lse && half == 0 && u < rows) p.lse[head] = l != 0.f ? LN2 * (m + log2f(l)) : NEG_INF;
     }
   }
   tc_fence_before();

@@ -89,12 +89,12 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
 }
 
 // Packed query rows of one tile (row u: token tok0 + u / group, head u % group;
-// zeros from `rows` on), swizzled, by the 128 threads `t` of a warpgroup.
-template <int D>
+// zeros from `rows` on), swizzled, by threads t of NT.
+template <int D, int NT>
 __device__ __forceinline__ void load_query_tile(unsigned char* dst, const AttnParams& p, int seq, int h, int tok0, int rows, int t) {
   constexpr int CH = D / 8;
 #pragma unroll 4
-  for (int i = t; i < TROWS * CH; i += 128) {
+  for (int i = t; i < TROWS * CH; i += NT) {
     const int u = i / CH, c = i % CH;
     uint4 w = make_uint4(0, 0, 0, 0);
     if (u < rows) {
@@ -161,6 +161,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
