@@ -56,7 +56,7 @@ struct TcSmem {
 struct TcCtl {
   uint64_t full[8], empty[8];          // ring stages
   uint64_t q_ready[2];                 // the query tile is in shared memory
-  uint64_t s_full[2], p_ready[2];      // S complete; P written (and S read)
+  uint64_t s_full[2], p_ready[2][2];   // S complete; the first and second columns of P written
   uint64_t o_done[2];                  // every product of the tile complete
   uint64_t v_fix;                      // the last tile of V has landed, before its tail is cleared
   uint32_t tmem;
@@ -103,7 +103,8 @@ __global__ void __launch_bounds__(PT, 1)
     for (int q = 0; q < 2; ++q) {
       mbar_init(&ctl.q_ready[q], 256);
       mbar_init(&ctl.s_full[q], 1);
-      mbar_init(&ctl.p_ready[q], 256);
+      mbar_init(&ctl.p_ready[q][0], 256);
+      mbar_init(&ctl.p_ready[q][1], 256);
       mbar_init(&ctl.o_done[q], 1);
     }
     mbar_init(&ctl.v_fix, 1);
@@ -176,14 +177,21 @@ __global__ void __launch_bounds__(PT, 1)
         const uint32_t v = ring + (2 * i + 1) % L::NST * L::TILE;
         for (int q = 0; q < nq; ++q) {
           if (needed(q, i)) {
-            ok = mbar_wait_bounded(&ctl.p_ready[q], np[q] & 1);
+            // P's columns 16 j .. 16 j + 15 of half h (rows 64 h + 16 j .. of V) sit at columns
+            // 64 h + 8 j; a part is two such steps of each half
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              if (ok) ok = mbar_wait_bounded(&ctl.p_ready[q][part], np[q] & 1);
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int h = k >> 1, j = 2 * part + (k & 1);
+                umma_ts(tm + 256 + q * 128, tm + q * 128 + h * 64 + j * 8, sw128_desc_mn(v + (h * 4 + j) * 2048), IPV, begun[q]);
+                begun[q] = true;
+              }
+            }
             if (!ok) break;
             ++np[q];
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < TROWS / 16; ++k)
-              umma_ts(tm + 256 + q * 128, tm + q * 128 + k * 8, sw128_desc_mn(v + k * 2048), IPV, begun[q] || k > 0);
-            begun[q] = true;
           }
           if (more && needed(q, i + 1)) issue_s(q, i + 1);
         }
@@ -244,10 +252,7 @@ __global__ void __launch_bounds__(PT, 1)
       }
       float mx = fmaxf(max3(mxs[0], mxs[1], mxs[2]), mxs[3]);
       ctl.mx[ns & 1][q][half][u] = mx;
-      // after this both halves have read S, so either may store P over it
-      tc_fence_before();
       asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
-      tc_fence_after();
       mx = fmaxf(mx, ctl.mx[ns & 1][q][half ^ 1][u]) * sl;
       if (ns == 0) {
         m = mx;
@@ -269,24 +274,27 @@ __global__ void __launch_bounds__(PT, 1)
       const float mu = m == NEG_INF ? 0.f : m;
       float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
-      for (int k = 0; k < 32; k += 2) {
-        float e0, e1, e2, e3;
-        fma2(e0, e1, __uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), sl, -mu);
-        fma2(e2, e3, __uint_as_float(x[2 * k + 2]), __uint_as_float(x[2 * k + 3]), sl, -mu);
-        e0 = fast_exp2(e0);
-        e1 = fast_exp2(e1);
-        e2 = fast_exp2(e2);
-        e3 = fast_exp2(e3);
-        add2(l0, l1, e0, e1);
-        add2(l2, l3, e2, e3);
-        x[k] = pack_bf16(e0, e1);
-        x[k + 1] = pack_bf16(e2, e3);
+      for (int part = 0; part < 2; ++part) {  // the products start on the first
+#pragma unroll
+        for (int k = part * 16; k < part * 16 + 16; k += 2) {
+          float e0, e1, e2, e3;
+          fma2(e0, e1, __uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), sl, -mu);
+          fma2(e2, e3, __uint_as_float(x[2 * k + 2]), __uint_as_float(x[2 * k + 3]), sl, -mu);
+          e0 = fast_exp2(e0);
+          e1 = fast_exp2(e1);
+          e2 = fast_exp2(e2);
+          e3 = fast_exp2(e3);
+          add2(l0, l1, e0, e1);
+          add2(l2, l3, e2, e3);
+          x[k] = pack_bf16(e0, e1);
+          x[k + 1] = pack_bf16(e2, e3);
+        }
+        tmem_st16(ts + half * 64 + part * 16, x + part * 16);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&ctl.p_ready[q][part]);
       }
       l += (l0 + l1) + (l2 + l3);
-      tmem_st32(ts + half * 32, x);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&ctl.p_ready[q]);
       ++ns;
     }
     if (ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.o_done[q], 0));
