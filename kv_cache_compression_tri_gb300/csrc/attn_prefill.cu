@@ -47,30 +47,31 @@ constexpr int REGS_LESS = 56, REGS_MORE = 104;  // 128 * 56 + 512 * 104 <= 640 *
 template <int D>
 struct TcSmem {
   static constexpr int TILE = D / 64 * TCOL;
-  static constexpr int NST = D == 128 ? 4 : 8;
+  static constexpr int NST = D == 128 ? 5 : 10;
   static constexpr int RING = 2 * TILE;  // after the two query tiles
   static constexpr int CTRL = RING + NST * TILE;
-  static constexpr int BYTES = CTRL + 4096 + 512 + 1024;  // (1024: the tiles start on a multiple of it)
+  static constexpr int BYTES = CTRL + 2560;
+  static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
 struct TcCtl {
-  uint64_t full[8], empty[8];          // ring stages
+  uint64_t full[12], empty[12];        // ring stages
   uint64_t q_ready[2];                 // the query tile is in shared memory
   uint64_t s_full[2], p_ready[2][2];   // S complete; the first and second columns of P written
   uint64_t o_done[2];                  // every product of the tile complete
   uint64_t v_fix;                      // the last tile of V has landed, before its tail is cleared
   uint32_t tmem;
   int flag;
-  float mx[2][2][2][TROWS];            // maxima: [tile parity][query tile][half][row]
+  float mx[2][2][TROWS];               // maxima: [query tile][half][row]
 };
+static_assert(sizeof(TcCtl) <= 2560, "control block");
 
 template <int D>
 __global__ void __launch_bounds__(PT, 1)
     prefill_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, int box_rows, int n_tiles) {
   using L = TcSmem<D>;
-  extern __shared__ unsigned char raw[];
-  unsigned char* smem = raw + (-smem_addr(raw) & 1023u);
+  extern __shared__ __align__(1024) unsigned char smem[];  // (the swizzle goes by address)
   TcCtl& ctl = *reinterpret_cast<TcCtl*>(smem + L::CTRL);
   const int t = threadIdx.x, w = t >> 5, lane = t & 31, G = p.group;
   // the last tokens see the most rows: their tiles first
@@ -101,10 +102,10 @@ __global__ void __launch_bounds__(PT, 1)
       mbar_init(&ctl.empty[i], 1);
     }
     for (int q = 0; q < 2; ++q) {
-      mbar_init(&ctl.q_ready[q], 256);
+      mbar_init(&ctl.q_ready[q], 8);  // (a warp arrives once)
       mbar_init(&ctl.s_full[q], 1);
-      mbar_init(&ctl.p_ready[q][0], 256);
-      mbar_init(&ctl.p_ready[q][1], 256);
+      mbar_init(&ctl.p_ready[q][0], 8);
+      mbar_init(&ctl.p_ready[q][1], 8);
       mbar_init(&ctl.o_done[q], 1);
     }
     mbar_init(&ctl.v_fix, 1);
@@ -213,7 +214,8 @@ __global__ void __launch_bounds__(PT, 1)
     const int toks = q ? toks1 : toks0, rows = toks * G, rf = q ? rf1 : rf0, rl = q ? rl1 : rl0;
     load_query_tile<D, 256>(smem + q * L::TILE, p, c.seq, c.h, tok0 + q * tpt, rows, half * 128 + u);
     fence_proxy_async_smem();
-    mbar_arrive(&ctl.q_ready[q]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl.q_ready[q]);
     const uint32_t lanes = static_cast<uint32_t>((w & 3) * 32) << 16;
     const uint32_t ts = tm + q * 128 + lanes, to = tm + 256 + q * 128 + half * (D / 2) + lanes;
     const int r = rf + u / G;
@@ -251,9 +253,11 @@ __global__ void __launch_bounds__(PT, 1)
         mxs[k] = fmaxf(mxs[k], __uint_as_float(x[60 + k]));
       }
       float mx = fmaxf(max3(mxs[0], mxs[1], mxs[2]), mxs[3]);
-      ctl.mx[ns & 1][q][half][u] = mx;
+      // (the partner has read the tile before's: S of this tile is issued after
+      // both halves' weights of that one)
+      ctl.mx[q][half][u] = mx;
       asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
-      mx = fmaxf(mx, ctl.mx[ns & 1][q][half ^ 1][u]) * sl;
+      mx = fmaxf(mx, ctl.mx[q][half ^ 1][u]) * sl;
       if (ns == 0) {
         m = mx;
       } else if (__any_sync(FULL_MASK, mx > m + RAISE)) {  // (the same in both halves)
@@ -292,15 +296,16 @@ __global__ void __launch_bounds__(PT, 1)
         tmem_st16(ts + half * 64 + part * 16, x + part * 16);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&ctl.p_ready[q][part]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.p_ready[q][part]);
       }
       l += (l0 + l1) + (l2 + l3);
       ++ns;
     }
     if (ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.o_done[q], 0));
-    ctl.mx[ns & 1][q][half][u] = l;
+    ctl.mx[q][half][u] = l;
     asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
-    const float l_half = ctl.mx[ns & 1][q][half ^ 1][u];
+    const float l_half = ctl.mx[q][half ^ 1][u];
     l = half ? l_half + l : l + l_half;
     if (!ok) {
       if (lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
