@@ -1,14 +1,575 @@
 // attn_mass.cu -- the accumulated weight of every cached row under a chunk of
 // queries: mass[j] += sum over the queries that see row j of e^(x_j - lse).
-// A CTA owns a run of cached rows and goes over the chunk's queries, so each
-// mass is summed by one thread row in a fixed order and written once.
+// A CTA owns cached rows and goes over the chunk's queries, so each mass is
+// summed in a fixed order and written once, without atomics.
+//
+// Per pair of a query row (token, head) and a cached row it sees: 2 D flop and
+// one exponential. Computed as S^T = K Q^T, cached rows on the lanes of tensor
+// memory: a thread owns a cached row, the weights of a query column need only
+// that column's lse, and the sum over queries is the thread's own.
+//
+// bf16 rows, tcgen05; a copy warp, an MMA warp, and four warpgroups that read S
+// from four 128-column buffers of tensor memory and add up the weights:
+//   - mass_few_kernel, at most FEW query tiles (an observation window): the
+//     queries stay in shared memory and the cache streams past them; bound by
+//     the keys' bytes. One CTA per SM takes an equal share of all slices' tiles,
+//     whatever the slices' lengths. A warpgroup takes every fourth tile of rows.
+//   - mass_many_kernel: two tiles of rows stay in shared memory and the query
+//     tiles stream past them. Under causality early rows are seen by many
+//     queries and late ones by few, so a CTA takes tile i and tile N - 1 - i. Two
+//     warpgroups per tile of rows take alternate query tiles.
+//
+// fp32 rows (mass_kernel): CUDA cores, 64 x 64 tiles in shared memory.
 #include <cuda_runtime.h>
 
+#include "attn_tc.cuh"
 #include "attn_tile.cuh"
 
 namespace tri {
 namespace {
 
+// ---------------------------------------------------------------------------
+// bf16 rows
+// ---------------------------------------------------------------------------
+constexpr int MT = 640;    // copy warp, MMA warp, two idle, four warpgroups
+constexpr int FEW = 2;     // query tiles that stay in shared memory
+constexpr int SLOTS = 16;  // lse rows kept by mass_few_kernel (see there)
+
+// Tensor map of the queries: (element, head, token, sequence), boxes of one
+// 64-element column of a packed tile.
+inline bool encode_queries(CUtensorMap* map, const AttnParams& p, int head_dim, Encode encode) {
+  const int64_t token = static_cast<int64_t>(p.n_kv_heads) * p.group * head_dim;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(p.n_kv_heads * p.group),
+                              static_cast<cuuint64_t>(p.n_q), static_cast<cuuint64_t>(p.q_seq ? p.n_seq : 1)};
+  // (strides of dimensions of one are never used)
+  const int64_t q_token = p.n_q > 1 ? p.q_token : token, q_seq = dims[3] > 1 ? p.q_seq : token * p.n_q;
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(q_token) * 2,
+                                 static_cast<cuuint64_t>(q_seq) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(TROWS / p.group), 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.q), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Query tile `qt` of (seq, h) into the tile at dst, by one thread that expected
+// the bytes of query_bytes<D>() on `bar`; rows past the tile's tokens are not written.
+template <int D>
+__device__ __forceinline__ uint32_t query_bytes(const AttnParams& p) {
+  return static_cast<uint32_t>(TROWS / p.group * p.group * D * 2);
+}
+template <int D>
+__device__ __forceinline__ void load_queries_tma(uint32_t dst, const CUtensorMap* map, const AttnParams& p, int seq, int h, int qt,
+                                                 uint64_t* bar) {
+#pragma unroll
+  for (int a = 0; a < D / 64; ++a)
+    tma_load4(dst + a * TCOL, map, 64 * a, h * p.group, qt * (TROWS / p.group), p.q_seq ? seq : 0, bar);
+}
+// -lse in base 2 of a query tile's rows (-inf, so no weight, past its tokens), by a warp.
+__device__ __forceinline__ void load_lse(float* nl, const AttnParams& p, const Chunk& c, int qt, int lane) {
+  const int tpt = TROWS / p.group;
+  for (int u = lane; u < TROWS; u += 32) {
+    const int tok = qt * tpt + u / p.group;
+    const bool live = u < tpt * p.group && tok < c.n_new;
+    nl[u] = live ? -LOG2E * p.lse_in[c.seq * p.lse_seq + static_cast<int64_t>(tok) * (p.n_kv_heads * p.group) +
+                                     c.h * p.group + u % p.group]
+                 : NEG_INF;
+  }
+}
+
+// Columns of query tile qt that see cached row j: [lo, hi).
+__device__ __forceinline__ void columns_seeing(const AttnParams& p, const Chunk& c, int qt, int j, int& lo, int& hi) {
+  const int tpt = TROWS / p.group, tok0 = qt * tpt, toks = min(tpt, c.n_new - tok0), rf = c.r0 + tok0;
+  lo = min(max(j - rf, 0), tpt) * p.group;
+  int end = toks;
+  if (p.window && j >= p.n_sink) end = static_cast<int>(min(static_cast<int64_t>(end), static_cast<int64_t>(j) + p.window - rf));
+  hi = max(end, 0) * p.group;
+}
+
+// Sum of the weights of this thread's cached row over 64 query columns (of a
+// tile's, from `first`) at ts, columns [lo, hi) only; `done` runs when S has
+// been read.
+template <class Done>
+__device__ __forceinline__ float row_weights(uint32_t ts, const float* nl, int first, float sl, bool all, int lo, int hi, Done done) {
+  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+  uint32_t x[64];
+  tmem_ld32(ts + first, x);
+  tmem_ld32(ts + first + 32, x + 32);
+  tmem_wait_ld();
+  done();
+  lo -= first;
+  hi -= first;
+#pragma unroll
+  for (int k = 0; k < 64; k += 4) {
+    const float4 n = *reinterpret_cast<const float4*>(nl + first + k);
+    float e0, e1, e2, e3;
+    fma2(e0, e1, __uint_as_float(x[k]), __uint_as_float(x[k + 1]), sl, n.x, n.y);
+    fma2(e2, e3, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]), sl, n.z, n.w);
+    e0 = fast_exp2(e0);
+    e1 = fast_exp2(e1);
+    e2 = fast_exp2(e2);
+    e3 = fast_exp2(e3);
+    if (!all) {  // (whatever those columns hold)
+      e0 = k >= lo && k < hi ? e0 : 0.f;
+      e1 = k + 1 >= lo && k + 1 < hi ? e1 : 0.f;
+      e2 = k + 2 >= lo && k + 2 < hi ? e2 : 0.f;
+      e3 = k + 3 >= lo && k + 3 < hi ? e3 : 0.f;
+    }
+    add2(s0, s1, e0, e1);
+    add2(s2, s3, e2, e3);
+  }
+  return (s0 + s1) + (s2 + s3);
+}
+
+// Whether every query row of tile qt sees every row of the cached tile at k0.
+__device__ __forceinline__ bool all_seen(const AttnParams& p, const Chunk& c, int qt, int k0) {
+  const int tpt = TROWS / p.group, tok0 = qt * tpt, rf = c.r0 + tok0, rl = rf + tpt - 1;
+  return tok0 + tpt <= c.n_new && k0 + TROWS - 1 <= rf &&
+         (p.window == 0 || k0 + TROWS <= p.n_sink || k0 > rl - p.window);
+}
+__device__ __forceinline__ bool any_seen(const AttnParams& p, const Chunk& c, int qt, int k0) {
+  const int tpt = TROWS / p.group, tok0 = qt * tpt;
+  if (tok0 >= c.n_new) return false;
+  const int rf = c.r0 + tok0, rl = rf + min(tpt, c.n_new - tok0) - 1;
+  return tile_seen(p, k0, TROWS, max(rf, 0), rl);
+}
+
+// Zeros in the rows of `tiles` query tiles that their boxes do not write.
+template <int D>
+__device__ __forceinline__ void clear_tails(unsigned char* q, int tiles, int group) {
+  const int first = TROWS / group * group;
+  for (int i = threadIdx.x; i < tiles * (D / 64) * (TROWS - first) * 8; i += MT) {
+    const int col = i / ((TROWS - first) * 8), rest = i % ((TROWS - first) * 8);
+    *reinterpret_cast<uint4*>(q + col * TCOL + first * 128 + rest * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+}
+
+template <int D>
+struct TcMass {
+  static constexpr int TILE = D / 64 * TCOL;
+  static constexpr int NST = D == 128 ? 4 : 8;
+  static constexpr int RING = FEW * TILE;  // after the resident tiles
+  static constexpr int CTRL = RING + NST * TILE;
+  static constexpr int BYTES = CTRL + 256 + SLOTS * FEW * TROWS * 4;
+  static_assert(BYTES <= 227 * 1024, "shared memory");
+};
+struct MassCtl {
+  uint64_t full[8], empty[8];     // ring stages
+  uint64_t res_full, res_free;    // the resident tiles have landed; are no longer read
+  uint64_t s_full[4], s_free[4];  // S complete; read
+  uint32_t tmem;
+  int flag;
+  int first_slice, first_tile;
+  float nl[SLOTS][FEW][TROWS];    // (mass_many_kernel: a row per ring stage)
+};
+static_assert(sizeof(MassCtl) <= 256 + SLOTS * FEW * TROWS * 4, "control block");
+
+template <int D>
+__global__ void __launch_bounds__(MT, 1)
+    mass_many_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap qmap, int box_rows) {
+  using L = TcMass<D>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  MassCtl& ctl = *reinterpret_cast<MassCtl*>(smem + L::CTRL);
+  const int t = threadIdx.x, w = t >> 5, lane = t & 31;
+  const int n_ls = p.n_seq * p.n_kv_heads, ls = blockIdx.x % n_ls, pair = blockIdx.x / n_ls;
+  Chunk c;
+  if (!chunk_of(p, ls, c)) return;
+  const int r_end = c.n - 1;
+  const int n_tiles = (c.n + TROWS - 1) / TROWS, other = n_tiles - 1 - pair;
+  if (pair > other) return;
+  const int nk = pair == other ? 1 : 2;
+  const int32_t* trow = p.rows.seq_table(c.s);
+  if (!chunk_blocks_ok(p, trow, c.r0, r_end, &ctl.flag)) return;
+  const int tpt = TROWS / p.group, n_qt = (c.n_new + tpt - 1) / tpt;
+  auto k_of = [&](int kt) { return (kt ? other : pair) * TROWS; };
+  auto needed = [&](int kt, int qt) { return kt < nk && any_seen(p, c, qt, k_of(kt)); };
+
+  if (t == 0) {
+    for (int i = 0; i < L::NST; ++i) {
+      mbar_init(&ctl.full[i], 2);    // the queries and their lse
+      mbar_init(&ctl.empty[i], 17);  // the MMAs and 16 warps
+    }
+    mbar_init(&ctl.res_full, 1);
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(&ctl.s_full[b], 1);
+      mbar_init(&ctl.s_free[b], 8);
+    }
+    mbar_init_fence();
+  }
+  clear_tails<D>(smem + L::RING, L::NST, p.group);
+  if (w == 1) tmem_alloc(&ctl.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = ctl.tmem, res = smem_addr(smem), ring = res + L::RING;
+  bool ok = true;
+
+  if (w == 0) {
+    if (lane == 0) mbar_arrive_expect_tx(&ctl.res_full, nk * L::TILE);
+    __syncwarp();
+    for (int kt = 0; kt < nk; ++kt)
+      load_tile<D>(res + kt * L::TILE, &kmap, p, box_rows, trow != nullptr, tile_block<D>(p, box_rows, trow, k_of(kt), c.n, lane),
+                   c.seq, c.h, k_of(kt), &ctl.res_full, lane);
+    int cnt = 0;
+    for (int qt = 0; qt < n_qt && ok; ++qt) {
+      if (!needed(0, qt) && !needed(1, qt)) continue;
+      const int st = cnt % L::NST;
+      if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&ctl.full[st], query_bytes<D>(p));
+        load_queries_tma<D>(ring + st * L::TILE, &qmap, p, c.seq, c.h, qt, &ctl.full[st]);
+      }
+      load_lse(&ctl.nl[0][0][0] + st * TROWS, p, c, qt, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.full[st]);
+      ++cnt;
+    }
+    if (!ok && lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
+    // copies in flight finish before shared memory is given up
+    (void)mbar_wait_bounded(&ctl.res_full, 0);
+    for (int u = max(0, cnt - L::NST); u < cnt; ++u) (void)mbar_wait_bounded(&ctl.full[u % L::NST], (u / L::NST) & 1);
+  } else if (w == 1) {
+    if (elect_one()) {
+      constexpr uint32_t IDESC = bf16_idesc(TROWS, TROWS, false);
+      int cnt = 0, pc[2] = {0, 0};
+      ok = mbar_wait_bounded(&ctl.res_full, 0);
+      for (int qt = 0; qt < n_qt && ok; ++qt) {
+        const bool need[2] = {needed(0, qt), needed(1, qt)};
+        if (!need[0] && !need[1]) continue;
+        const int st = cnt % L::NST;
+        ok = mbar_wait_bounded(&ctl.full[st], (cnt / L::NST) & 1);
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          if (!need[kt] || !ok) continue;
+          const int b = kt * 2 + (pc[kt] & 1);
+          if (pc[kt] >= 2) ok = mbar_wait_bounded(&ctl.s_free[b], ((pc[kt] >> 1) - 1) & 1);
+          if (!ok) continue;
+          tc_fence_after();
+          umma_rows<D>(tm + b * 128, res + kt * L::TILE, ring + st * L::TILE, IDESC);
+          umma_commit(&ctl.s_full[b]);
+          ++pc[kt];
+        }
+        if (!ok) break;
+        umma_commit(&ctl.empty[st]);
+        ++cnt;
+      }
+      if (!ok) set_status(p.dev_status, TRI_DEV_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (w >= 4) {
+    const int kt = (w - 4) >> 3, half = ((w - 4) >> 2) & 1, u = t & 127;
+    const uint32_t ts = tm + kt * 256 + (static_cast<uint32_t>((w & 3) * 32) << 16);
+    const int k0 = k_of(kt), j = k0 + u;
+    const float sl = p.scale * LOG2E;
+    float sum = 0.f;
+    int cnt = 0, pc = 0;
+    for (int qt = 0; qt < n_qt && ok; ++qt) {
+      const bool mine = needed(kt, qt);
+      if (!mine && !needed(kt ^ 1, qt)) continue;
+      const int st = cnt % L::NST;
+      ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.full[st], (cnt / L::NST) & 1));
+      if (!ok) break;
+      if (mine) {
+        const int b = kt * 2 + (pc & 1);
+        ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[b], (pc >> 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        const bool all = all_seen(p, c, qt, k0);
+        int lo = 0, hi = TROWS;
+        if (!all) columns_seeing(p, c, qt, j, lo, hi);
+        sum += row_weights(ts + (pc & 1) * 128, &ctl.nl[0][0][0] + st * TROWS, half * 64, sl, all, lo, hi, [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.s_free[b]);
+        });
+        ++pc;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.empty[st]);
+      ++cnt;
+    }
+    if (!ok && lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
+    ctl.nl[8 + kt * 2 + half][0][u] = sum;  // (the ring's lse rows are below)
+  }
+  tc_fence_before();
+  const bool fine = __syncthreads_and(ok);
+  tc_fence_after();
+  if (w == 1) tmem_dealloc(tm, 512);
+  if (fine && t < nk * TROWS) {
+    const int kt = t / TROWS, u = t % TROWS, j = k_of(kt) + u;
+    const float sum = ctl.nl[8 + 2 * kt][0][u] + ctl.nl[9 + 2 * kt][0][u];
+    if (j <= r_end && sum != 0.f) p.mass[c.s * p.n_cap + j] += sum;
+  }
+}
+
+// Tiles of rows of a slice that hold any (none of one with a bad count).
+__device__ __forceinline__ int tiles_of(const AttnParams& p, int ls) {
+  const int seq = ls / p.n_kv_heads;
+  const int n = p.n_valid[slice_of(p, seq, ls - seq * p.n_kv_heads)];
+  if (n >= 0 && n <= p.n_cap) return (n + TROWS - 1) / TROWS;
+  set_status(p.dev_status, TRI_DEV_NVALID_OVER_CAP);
+  return 0;
+}
+
+// Where the CTA's share of all tiles starts, and how many it has: (by the CTA;
+// sums of the slices before each thread's run of slices, then a walk).
+__device__ __forceinline__ int64_t my_share(const AttnParams& p, MassCtl& ctl) {
+  __shared__ int64_t warp_sum[MT / 32];
+  const int n_ls = p.n_seq * p.n_kv_heads, t = threadIdx.x;
+  const int per = (n_ls + MT - 1) / MT, s0 = min(n_ls, t * per), s1 = min(n_ls, s0 + per);
+  int64_t mine = 0;
+  for (int s = s0; s < s1; ++s) mine += tiles_of(p, s);
+  int64_t upto = mine;
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int64_t x = __shfl_up_sync(FULL_MASK, upto, k);
+    if ((t & 31) >= k) upto += x;
+  }
+  if ((t & 31) == 31) warp_sum[t >> 5] = upto;
+  __syncthreads();
+  int64_t total = 0;
+  for (int i = 0; i < MT / 32; ++i) {
+    if (i < (t >> 5)) upto += warp_sum[i];
+    total += warp_sum[i];
+  }
+  const int64_t x0 = total * blockIdx.x / gridDim.x, x1 = total * (blockIdx.x + 1) / gridDim.x;
+  int64_t base = upto - mine;
+  if (x0 >= base && x0 < upto) {
+    for (int s = s0; s < s1; ++s) {
+      const int n = tiles_of(p, s);
+      if (x0 < base + n) {
+        ctl.first_slice = s;
+        ctl.first_tile = static_cast<int>(x0 - base);
+        break;
+      }
+      base += n;
+    }
+  }
+  __syncthreads();
+  return x1 - x0;
+}
+
+// Every block that some query of the chunk sees rows of is in the pool (by a warp).
+__device__ __forceinline__ bool warp_blocks_ok(const AttnParams& p, const Chunk& c, int lane) {
+  const int32_t* trow = p.rows.seq_table(c.s);
+  if (!trow) return true;
+  const Visible first = visible_rows(max(c.r0, 0), p.n_sink, p.window);
+  const int s1 = visible_rows(c.n - 1, p.n_sink, p.window).s1;
+  bool ok = true;
+  for (int b = lane; b <= (c.n - 1) >> p.rows.block_shift; b += 32) {
+    const int r = b << p.rows.block_shift;
+    if (r >= s1 && r + p.rows.block_size <= first.w0) continue;
+    const int v = __ldg(trow + b);
+    ok = ok && v >= 0 && v < p.rows.num_blocks;
+  }
+  return __all_sync(FULL_MASK, ok);
+}
+
+// The queries of one (sequence, KV head) and a run of its tiles of rows: a
+// segment. Segments follow each other; every role walks them alike.
+//
+// The lse rows of segment g are in slot g % SLOTS. A warpgroup that still reads
+// them when segment g + SLOTS is loaded would have to be a tile more than 12
+// tiles behind the MMAs, and S's four buffers let it fall back by at most 8.
+template <int D>
+__global__ void __launch_bounds__(MT, 1)
+    mass_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
+                    const __grid_constant__ CUtensorMap qmap, int box_rows) {
+  using L = TcMass<D>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  MassCtl& ctl = *reinterpret_cast<MassCtl*>(smem + L::CTRL);
+  const int t = threadIdx.x, w = t >> 5, lane = t & 31;
+  const int64_t share = my_share(p, ctl);
+  if (share == 0) return;
+  const int tpt = TROWS / p.group;
+
+  if (t == 0) {
+    for (int i = 0; i < L::NST; ++i) {
+      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.empty[i], 1);
+    }
+    mbar_init(&ctl.res_full, 1);
+    mbar_init(&ctl.res_free, 1);
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(&ctl.s_full[b], 1);
+      mbar_init(&ctl.s_free[b], 4);
+    }
+    mbar_init_fence();
+  }
+  clear_tails<D>(smem, FEW, p.group);
+  if (w == 1) tmem_alloc(&ctl.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = ctl.tmem, res = smem_addr(smem), ring = res + L::RING;
+  bool ok = true;
+
+  // The walk, by a whole warp: body(segment, chunk, query tiles, cached tile k0) for every tile of the
+  // share that some query sees; next(segment, chunk, query tiles) before its first and
+  // last(segment) after its last one.
+  auto walk = [&](auto&& next, auto&& body, auto&& last) {
+    int ls = ctl.first_slice, i = ctl.first_tile, seg = 0;
+    for (int64_t left = share; left > 0 && ok; ++ls, i = 0) {
+      const int n = tiles_of(p, ls);
+      if (n == 0) continue;
+      const int end = static_cast<int>(min(static_cast<int64_t>(n), i + left));
+      left -= end - i;
+      Chunk c;
+      if (!chunk_of(p, ls, c)) continue;
+      if (!warp_blocks_ok(p, c, lane)) {
+        if (lane == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
+        continue;
+      }
+      const int n_qt = (c.n_new + tpt - 1) / tpt;
+      bool begun = false;
+      for (; i < end && ok; ++i) {
+        const int k0 = i * TROWS;
+        if (!tile_seen(p, k0, TROWS, max(c.r0, 0), c.n - 1)) continue;
+        if (!begun) next(seg, c, n_qt);
+        begun = true;
+        if (ok) body(seg, c, n_qt, k0);
+      }
+      if (begun && ok) {
+        last(seg);
+        ++seg;
+      }
+    }
+  };
+
+  if (w == 0) {
+    int cnt = 0, segs = 0;
+    int blk = 0, blk_row = -1;
+    const int32_t* blk_of = nullptr;  // the sequence and row that `blk` is for
+    walk(
+        [&](int seg, const Chunk& c, int n_qt) {
+          if (seg > 0) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.res_free, (seg - 1) & 1));
+          if (!ok) return;
+          for (int qt = 0; qt < n_qt; ++qt) load_lse(ctl.nl[seg % SLOTS][qt], p, c, qt, lane);
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&ctl.res_full, n_qt * query_bytes<D>(p));
+            for (int qt = 0; qt < n_qt; ++qt)
+              load_queries_tma<D>(res + qt * L::TILE, &qmap, p, c.seq, c.h, qt, &ctl.res_full);
+          }
+          segs = seg + 1;
+        },
+        [&](int, const Chunk& c, int, int k0) {
+          const int st = cnt % L::NST;
+          const int32_t* trow = p.rows.seq_table(c.s);
+          if (blk_row != k0 || blk_of != trow) blk = tile_block<D>(p, box_rows, trow, k0, c.n, lane);
+          // (the next tile's is on its way while this one waits for its stage)
+          blk_row = k0 + TROWS;
+          blk_of = trow;
+          const int blk_next = tile_block<D>(p, box_rows, trow, blk_row, c.n, lane);
+          if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
+          if (!ok) return;
+          if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], L::TILE);
+          __syncwarp();
+          load_tile<D>(ring + st * L::TILE, &kmap, p, box_rows, trow != nullptr, blk, c.seq, c.h, k0, &ctl.full[st], lane);
+          blk = blk_next;
+          ++cnt;
+        },
+        [](int) {});
+    if (!ok && lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
+    // copies in flight finish before shared memory is given up
+    if (segs) (void)mbar_wait_bounded(&ctl.res_full, (segs - 1) & 1);
+    for (int u = max(0, cnt - L::NST); u < cnt; ++u) (void)mbar_wait_bounded(&ctl.full[u % L::NST], (u / L::NST) & 1);
+  } else if (w == 1) {
+    // (lane 0 issues: what a commit covers is its own thread's MMAs)
+    constexpr uint32_t IDESC = bf16_idesc(TROWS, TROWS, false);
+    int cnt = 0;
+    uint32_t used = 0;  // 8 bits per buffer: uses so far, mod 256
+    walk([&](int seg, const Chunk&, int) { ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.res_full, seg & 1)); },
+         [&](int, const Chunk& c, int n_qt, int k0) {
+           const int st = cnt % L::NST, b = cnt & 3;
+           ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.full[st], (cnt / L::NST) & 1));
+           uint32_t n = (used >> (8 * b)) & 255u;
+           for (int qt = 0; qt < n_qt && ok; ++qt) {
+             if (!any_seen(p, c, qt, k0)) continue;
+             // (the phase before an mbarrier's first counts as complete)
+             ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_free[b], (n - 1) & 1));
+             if (!ok) break;
+             tc_fence_after();
+             if (lane == 0) {
+               umma_rows<D>(tm + b * 128, ring + st * L::TILE, res + qt * L::TILE, IDESC);
+               umma_commit(&ctl.s_full[b]);
+             }
+             __syncwarp();
+             ++n;
+           }
+           used = (used & ~(255u << (8 * b))) | ((n & 255u) << (8 * b));
+           if (ok && lane == 0) umma_commit(&ctl.empty[st]);
+           ++cnt;
+         },
+         [&](int) {
+           if (lane == 0) umma_commit(&ctl.res_free);
+         });
+    if (!ok && lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
+    __syncwarp();
+  } else if (w >= 4) {
+    const int b = (w - 4) >> 2, u = t & 127;
+    const uint32_t ts = tm + b * 128 + (static_cast<uint32_t>((w & 3) * 32) << 16);
+    const float sl = p.scale * LOG2E;
+    int cnt = 0, n = 0;
+    walk([](int, const Chunk&, int) {},
+         [&](int seg, const Chunk& c, int n_qt, int k0) {
+           if ((cnt++ & 3) != b) return;
+           const int j = k0 + u;
+           float* mass = p.mass + c.s * p.n_cap + j;
+           const float old = j < c.n ? *mass : 0.f;  // (on its way while the products run)
+           float sum = 0.f;
+           for (int qt = 0; qt < n_qt && ok; ++qt) {
+             if (!any_seen(p, c, qt, k0)) continue;
+             ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[b], n & 1));
+             if (!ok) break;
+             ++n;
+             tc_fence_after();
+             const bool all = all_seen(p, c, qt, k0);
+             int lo = 0, hi = TROWS;
+             if (!all) columns_seeing(p, c, qt, j, lo, hi);
+             sum += row_weights(ts, ctl.nl[seg % SLOTS][qt], 0, sl, all, lo, hi, [] {});
+             sum += row_weights(ts, ctl.nl[seg % SLOTS][qt], 64, sl, all, lo, hi, [&] {
+               tc_fence_before();
+               __syncwarp();
+               if (lane == 0) mbar_arrive(&ctl.s_free[b]);
+             });
+           }
+           if (ok && j < c.n && sum != 0.f) *mass = old + sum;
+         },
+         [](int) {});
+    if (!ok && lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (w == 1) tmem_dealloc(tm, 512);
+}
+
+template <int D>
+cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
+  CUtensorMap kmap, qmap;
+  const Encode encode = tensor_map_encode();
+  const int box_rows = encode ? encode_rows(&kmap, p.k, p, D, encode) : 0;
+  if (!box_rows || !encode_queries(&qmap, p, D, encode)) return cudaErrorInvalidValue;
+  const int tpt = TROWS / p.group, n_qt = (p.n_q + tpt - 1) / tpt;
+  const bool few = n_qt <= FEW;
+  auto kern = few ? mass_few_kernel<D> : mass_many_kernel<D>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcMass<D>::BYTES);
+  if (e != cudaSuccess) return e;
+  const int64_t n_ls = static_cast<int64_t>(p.n_seq) * p.n_kv_heads, tiles = (p.n_cap + TROWS - 1) / TROWS;
+  const int64_t ctas = few ? min(static_cast<int64_t>(SMS), n_ls * tiles) : n_ls * ((tiles + 1) / 2);
+  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  kern<<<static_cast<unsigned>(ctas), MT, TcMass<D>::BYTES, st>>>(p, kmap, qmap, box_rows);
+  note_launch();
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// fp32 rows
+// ---------------------------------------------------------------------------
 template <int D>
 struct MassSmem {
   float q[FM][D + 4];
@@ -85,7 +646,7 @@ cudaError_t launch_typed(const AttnParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attn_mass(const AttnParams& p, tri_dtype dt, int head_dim, cudaStream_t st) {
-  if (dt == TRI_BF16) return head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(p, st) : launch_typed<__nv_bfloat16, 128>(p, st);
+  if (dt == TRI_BF16) return head_dim == 64 ? launch_tc<64>(p, st) : launch_tc<128>(p, st);
   return head_dim == 64 ? launch_typed<float, 64>(p, st) : launch_typed<float, 128>(p, st);
 }
 

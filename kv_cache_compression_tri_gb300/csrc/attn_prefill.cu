@@ -123,8 +123,11 @@ __global__ void __launch_bounds__(PT, 1)
     regs_less<REGS_LESS>();
     // ---- copies: K and V tiles take the ring's stages in turn ----
     int cnt = 0;
+    int blk = n_list ? tile_block<D>(p, box_rows, trow, list.at(0) * TROWS, c.n, lane) : 0, blk_next = 0;
     for (; cnt < 2 * n_list && ok; ++cnt) {
       const int st = cnt % L::NST, k0 = list.at(cnt >> 1) * TROWS;
+      if (!(cnt & 1) && cnt + 2 < 2 * n_list)  // (on its way while this tile waits for its stage)
+        blk_next = tile_block<D>(p, box_rows, trow, list.at((cnt >> 1) + 1) * TROWS, c.n, lane);
       if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
       if (!ok) break;
       const bool is_v = cnt & 1;
@@ -132,7 +135,8 @@ __global__ void __launch_bounds__(PT, 1)
       uint64_t* bar = fix ? &ctl.v_fix : &ctl.full[st];
       if (lane == 0) mbar_arrive_expect_tx(bar, L::TILE);
       __syncwarp();
-      load_tile<D>(ring + st * L::TILE, is_v ? &vmap : &kmap, p, box_rows, trow, c.seq, c.h, k0, c.n, bar, lane);
+      load_tile<D>(ring + st * L::TILE, is_v ? &vmap : &kmap, p, box_rows, trow != nullptr, blk, c.seq, c.h, k0, bar, lane);
+      if (is_v) blk = blk_next;
       if (fix) {
         ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.v_fix, 0));
         if (!ok) break;
@@ -347,8 +351,9 @@ __global__ void __launch_bounds__(PT, 1)
 template <int D>
 cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
   CUtensorMap kmap, vmap;
-  const int box_rows = encode_rows(&kmap, p.k, p, D);
-  if (!box_rows || !encode_rows(&vmap, p.v, p, D)) return cudaErrorInvalidValue;
+  const Encode encode = tensor_map_encode();
+  const int box_rows = encode ? encode_rows(&kmap, p.k, p, D, encode) : 0;
+  if (!box_rows || !encode_rows(&vmap, p.v, p, D, encode)) return cudaErrorInvalidValue;
   auto kern = prefill_tc_kernel<D>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D>::BYTES);
   if (e != cudaSuccess) return e;

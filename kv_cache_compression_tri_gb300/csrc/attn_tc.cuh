@@ -24,13 +24,13 @@ namespace {
 constexpr int TROWS = 128;          // rows of a tile
 constexpr int TCOL = TROWS * 128;   // bytes of a 64-element column of it
 
-// Tensor map of one layer's K (or V) rows: (element, row, head, sequence) of
-// contiguous slices, (element, row of the block, head, block) of a pool. Boxes
-// of 64 elements by up to 128 rows. Returns the rows of a box, 0 on failure.
-inline int encode_rows(CUtensorMap* map, const void* pool, const AttnParams& p, int head_dim) {
-  typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+constexpr int SMS = 152;
+
+typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                           const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                           CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// The driver's encoder, or NULL.
+inline Encode tensor_map_encode() {
   static const Encode encode = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -39,7 +39,13 @@ inline int encode_rows(CUtensorMap* map, const void* pool, const AttnParams& p, 
       fn = nullptr;
     return reinterpret_cast<Encode>(fn);
   }();
-  if (!encode) return 0;
+  return encode;
+}
+
+// Tensor map of one layer's K (or V) rows: (element, row, head, sequence) of
+// contiguous slices, (element, row of the block, head, block) of a pool. Boxes
+// of 64 elements by up to 128 rows. Returns the rows of a box, 0 on failure.
+inline int encode_rows(CUtensorMap* map, const void* pool, const AttnParams& p, int head_dim, Encode encode) {
   const RowMap& m = p.rows;
   const bool paged = m.table != nullptr;
   const int64_t base = p.layer * (paged ? m.layer_bytes : p.n_kv_heads * m.slice_bytes);
@@ -65,27 +71,27 @@ __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
-// Cached rows [k0, k0 + 128) of slice (seq, h) into the tile at `dst`, by the
-// lanes of one warp after one of them expected D * 256 bytes on `bar`. Rows with
-// no block in the pool, or past the cache, read as zeros (the map's fill).
+// Block that holds a lane's box of the tile at row k0 (pools only): num_blocks,
+// which the map fills with zeros, where there is none.
 template <int D>
-__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, const AttnParams& p, int box_rows, const int32_t* trow,
-                                          int seq, int h, int k0, int n, uint64_t* bar, int lane) {
+__device__ __forceinline__ int tile_block(const AttnParams& p, int box_rows, const int32_t* trow, int k0, int n, int lane) {
+  const int i = lane / (D / 64), row = k0 + i * box_rows;
+  if (!trow || i >= TROWS / box_rows || row >= n) return p.rows.num_blocks;
+  const int blk = __ldg(trow + (row >> p.rows.block_shift));
+  return blk < 0 || blk > p.rows.num_blocks ? p.rows.num_blocks : blk;
+}
+// Cached rows [k0, k0 + 128) of slice (seq, h) into the tile at `dst`, by the
+// lanes of one warp after one of them expected D * 256 bytes on `bar`; blk as
+// tile_block gave it. Rows past the cache read as zeros too.
+template <int D>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, const AttnParams& p, int box_rows, bool paged, int blk,
+                                          int seq, int h, int k0, uint64_t* bar, int lane) {
   constexpr int COLS = D / 64;
-  const int boxes = TROWS / box_rows * COLS;
-  if (lane >= boxes) return;
+  if (lane >= TROWS / box_rows * COLS) return;
   const int col = lane % COLS, i = lane / COLS, row = k0 + i * box_rows;
   const uint32_t d = dst + col * TCOL + i * box_rows * 128;
-  if (!trow) {
-    tma_load4(d, map, 64 * col, row, h, seq, bar);
-    return;
-  }
-  int blk = p.rows.num_blocks;
-  if (row < n) {
-    blk = __ldg(trow + (row >> p.rows.block_shift));
-    if (blk < 0 || blk > p.rows.num_blocks) blk = p.rows.num_blocks;
-  }
-  tma_load4(d, map, 64 * col, row & (p.rows.block_size - 1), h, blk, bar);
+  if (paged) tma_load4(d, map, 64 * col, row & (p.rows.block_size - 1), h, blk, bar);
+  else tma_load4(d, map, 64 * col, row, h, seq, bar);
 }
 
 // Packed query rows of one tile (row u: token tok0 + u / group, head u % group;
@@ -182,6 +188,11 @@ __device__ __forceinline__ void fma2(float& x0, float& x1, float a0, float a1, f
   asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
       "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
       : "=f"(x0), "=f"(x1) : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void fma2(float& x0, float& x1, float a0, float a1, float b, float c0, float c1) {
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %6};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(x0), "=f"(x1) : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
 }
 __device__ __forceinline__ void add2(float& x0, float& x1, float a0, float a1) {
   asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%0, %1};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
