@@ -31,7 +31,7 @@ namespace {
 // ---------------------------------------------------------------------------
 // bf16 rows
 // ---------------------------------------------------------------------------
-constexpr int MT = 640;    // copy warp, MMA warp, two idle, four warpgroups
+constexpr int MT = 640;    // copy warp, MMA warp, lse warp, an idle one, four warpgroups
 constexpr int FEW = 2;     // query tiles that stay in shared memory
 constexpr int SLOTS = 16;  // lse rows kept by mass_few_kernel (see there)
 
@@ -65,21 +65,22 @@ __device__ __forceinline__ void load_queries_tma(uint32_t dst, const CUtensorMap
   for (int a = 0; a < D / 64; ++a)
     tma_load4(dst + a * TCOL, map, 64 * a, h * p.group, qt * (TROWS / p.group), p.q_seq ? seq : 0, bar);
 }
-// -lse in base 2 of a query tile's rows (-inf, so no weight, past its tokens), by a warp.
-__device__ __forceinline__ void load_lse(float* nl, const AttnParams& p, const Chunk& c, int qt, int lane) {
-  const int tpt = TROWS / p.group;
-  for (int u = lane; u < TROWS; u += 32) {
-    const int tok = qt * tpt + u / p.group;
+// -lse in base 2 of a query tile's rows (-inf, so no weight, past its tokens), by
+// a warp: row 32 k + lane in x[k].
+__device__ __forceinline__ void get_lse(float (&x)[TROWS / 32], const AttnParams& p, const Chunk& c, int tpt, int qt, int lane) {
+#pragma unroll
+  for (int k = 0; k < TROWS / 32; ++k) {
+    const int u = k * 32 + lane, tok = qt * tpt + u / p.group;
     const bool live = u < tpt * p.group && tok < c.n_new;
-    nl[u] = live ? -LOG2E * p.lse_in[c.seq * p.lse_seq + static_cast<int64_t>(tok) * (p.n_kv_heads * p.group) +
-                                     c.h * p.group + u % p.group]
-                 : NEG_INF;
+    x[k] = live ? -LOG2E * p.lse_in[c.seq * p.lse_seq + static_cast<int64_t>(tok) * (p.n_kv_heads * p.group) +
+                                    c.h * p.group + u % p.group]
+                : NEG_INF;
   }
 }
 
 // Columns of query tile qt that see cached row j: [lo, hi).
-__device__ __forceinline__ void columns_seeing(const AttnParams& p, const Chunk& c, int qt, int j, int& lo, int& hi) {
-  const int tpt = TROWS / p.group, tok0 = qt * tpt, toks = min(tpt, c.n_new - tok0), rf = c.r0 + tok0;
+__device__ __forceinline__ void columns_seeing(const AttnParams& p, const Chunk& c, int tpt, int qt, int j, int& lo, int& hi) {
+  const int tok0 = qt * tpt, toks = min(tpt, c.n_new - tok0), rf = c.r0 + tok0;
   lo = min(max(j - rf, 0), tpt) * p.group;
   int end = toks;
   if (p.window && j >= p.n_sink) end = static_cast<int>(min(static_cast<int64_t>(end), static_cast<int64_t>(j) + p.window - rf));
@@ -87,18 +88,17 @@ __device__ __forceinline__ void columns_seeing(const AttnParams& p, const Chunk&
 }
 
 // Sum of the weights of this thread's cached row over 64 query columns (of a
-// tile's, from `first`) at ts, columns [lo, hi) only; `done` runs when S has
-// been read.
-template <class Done>
-__device__ __forceinline__ float row_weights(uint32_t ts, const float* nl, int first, float sl, bool all, int lo, int hi, Done done) {
+// tile's, from `first`) at ts; `done` runs when S has been read. ALL: every
+// column counts, else columns [lo, hi) whatever the others hold. (Two loops: as
+// one with selects the 4096-token prompt took 189 us instead of YYY.)
+template <bool ALL, class Done>
+__device__ __forceinline__ float row_weights(uint32_t ts, const float* nl, int first, float sl, int lo, int hi, Done done) {
   float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
   uint32_t x[64];
   tmem_ld32(ts + first, x);
   tmem_ld32(ts + first + 32, x + 32);
   tmem_wait_ld();
   done();
-  lo -= first;
-  hi -= first;
 #pragma unroll
   for (int k = 0; k < 64; k += 4) {
     const float4 n = *reinterpret_cast<const float4*>(nl + first + k);
@@ -109,26 +109,31 @@ __device__ __forceinline__ float row_weights(uint32_t ts, const float* nl, int f
     e1 = fast_exp2(e1);
     e2 = fast_exp2(e2);
     e3 = fast_exp2(e3);
-    if (!all) {  // (whatever those columns hold)
-      e0 = k >= lo && k < hi ? e0 : 0.f;
-      e1 = k + 1 >= lo && k + 1 < hi ? e1 : 0.f;
-      e2 = k + 2 >= lo && k + 2 < hi ? e2 : 0.f;
-      e3 = k + 3 >= lo && k + 3 < hi ? e3 : 0.f;
+    if constexpr (!ALL) {
+      const unsigned c = first + k - lo, n_cols = hi > lo ? hi - lo : 0;
+      e0 = c < n_cols ? e0 : 0.f;
+      e1 = c + 1 < n_cols ? e1 : 0.f;
+      e2 = c + 2 < n_cols ? e2 : 0.f;
+      e3 = c + 3 < n_cols ? e3 : 0.f;
     }
     add2(s0, s1, e0, e1);
     add2(s2, s3, e2, e3);
   }
   return (s0 + s1) + (s2 + s3);
 }
+template <class Done>
+__device__ __forceinline__ float row_weights(uint32_t ts, const float* nl, int first, float sl, bool all, int lo, int hi, Done done) {
+  return all ? row_weights<true>(ts, nl, first, sl, 0, 0, done) : row_weights<false>(ts, nl, first, sl, lo, hi, done);
+}
 
 // Whether every query row of tile qt sees every row of the cached tile at k0.
-__device__ __forceinline__ bool all_seen(const AttnParams& p, const Chunk& c, int qt, int k0) {
-  const int tpt = TROWS / p.group, tok0 = qt * tpt, rf = c.r0 + tok0, rl = rf + tpt - 1;
+__device__ __forceinline__ bool all_seen(const AttnParams& p, const Chunk& c, int tpt, int qt, int k0) {
+  const int tok0 = qt * tpt, rf = c.r0 + tok0, rl = rf + tpt - 1;
   return tok0 + tpt <= c.n_new && k0 + TROWS - 1 <= rf &&
          (p.window == 0 || k0 + TROWS <= p.n_sink || k0 > rl - p.window);
 }
-__device__ __forceinline__ bool any_seen(const AttnParams& p, const Chunk& c, int qt, int k0) {
-  const int tpt = TROWS / p.group, tok0 = qt * tpt;
+__device__ __forceinline__ bool any_seen(const AttnParams& p, const Chunk& c, int tpt, int qt, int k0) {
+  const int tok0 = qt * tpt;
   if (tok0 >= c.n_new) return false;
   const int rf = c.r0 + tok0, rl = rf + min(tpt, c.n_new - tok0) - 1;
   return tile_seen(p, k0, TROWS, max(rf, 0), rl);
@@ -184,7 +189,7 @@ __global__ void __launch_bounds__(MT, 1)
   if (!chunk_blocks_ok(p, trow, c.r0, r_end, &ctl.flag)) return;
   const int tpt = TROWS / p.group, n_qt = (c.n_new + tpt - 1) / tpt;
   auto k_of = [&](int kt) { return (kt ? other : pair) * TROWS; };
-  auto needed = [&](int kt, int qt) { return kt < nk && any_seen(p, c, qt, k_of(kt)); };
+  auto needed = [&](int kt, int qt) { return kt < nk && any_seen(p, c, tpt, qt, k_of(kt)); };
 
   if (t == 0) {
     for (int i = 0; i < L::NST; ++i) {
@@ -222,15 +227,38 @@ __global__ void __launch_bounds__(MT, 1)
         mbar_arrive_expect_tx(&ctl.full[st], query_bytes<D>(p));
         load_queries_tma<D>(ring + st * L::TILE, &qmap, p, c.seq, c.h, qt, &ctl.full[st]);
       }
-      load_lse(&ctl.nl[0][0][0] + st * TROWS, p, c, qt, lane);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.full[st]);
       ++cnt;
     }
     if (!ok && lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
     // copies in flight finish before shared memory is given up
     (void)mbar_wait_bounded(&ctl.res_full, 0);
     for (int u = max(0, cnt - L::NST); u < cnt; ++u) (void)mbar_wait_bounded(&ctl.full[u % L::NST], (u / L::NST) & 1);
+  } else if (w == 2) {
+    // ---- lse, each tile's loaded before the stage of the one before is free ----
+    int cnt = 0;
+    bool any = false;
+    float nl[TROWS / 32];
+    auto store = [&] {
+      const int st = cnt % L::NST;
+      if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
+#pragma unroll
+      for (int k = 0; k < TROWS / 32; ++k) (&ctl.nl[0][0][0])[st * TROWS + k * 32 + lane] = nl[k];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.full[st]);
+      ++cnt;
+    };
+    for (int qt = 0; qt < n_qt && ok; ++qt) {
+      if (!needed(0, qt) && !needed(1, qt)) continue;
+      float next[TROWS / 32];
+      get_lse(next, p, c, tpt, qt, lane);
+      if (any) store();
+      any = true;
+#pragma unroll
+      for (int k = 0; k < TROWS / 32; ++k) nl[k] = next[k];
+    }
+    if (any && ok) store();
+    if (!ok && lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
   } else if (w == 1) {
     if (elect_one()) {
       constexpr uint32_t IDESC = bf16_idesc(TROWS, TROWS, false);
@@ -277,9 +305,9 @@ __global__ void __launch_bounds__(MT, 1)
         ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[b], (pc >> 1) & 1));
         if (!ok) break;
         tc_fence_after();
-        const bool all = all_seen(p, c, qt, k0);
+        const bool all = all_seen(p, c, tpt, qt, k0);
         int lo = 0, hi = TROWS;
-        if (!all) columns_seeing(p, c, qt, j, lo, hi);
+        if (!all) columns_seeing(p, c, tpt, qt, j, lo, hi);
         sum += row_weights(ts + (pc & 1) * 128, &ctl.nl[0][0][0] + st * TROWS, half * 64, sl, all, lo, hi, [&] {
           tc_fence_before();
           __syncwarp();
@@ -447,7 +475,12 @@ __global__ void __launch_bounds__(MT, 1)
         [&](int seg, const Chunk& c, int n_qt) {
           if (seg > 0) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.res_free, (seg - 1) & 1));
           if (!ok) return;
-          for (int qt = 0; qt < n_qt; ++qt) load_lse(ctl.nl[seg % SLOTS][qt], p, c, qt, lane);
+          for (int qt = 0; qt < n_qt; ++qt) {
+            float x[TROWS / 32];
+            get_lse(x, p, c, tpt, qt, lane);
+#pragma unroll
+            for (int k = 0; k < TROWS / 32; ++k) ctl.nl[seg % SLOTS][qt][k * 32 + lane] = x[k];
+          }
           __syncwarp();
           if (lane == 0) {
             mbar_arrive_expect_tx(&ctl.res_full, n_qt * query_bytes<D>(p));
@@ -488,7 +521,7 @@ __global__ void __launch_bounds__(MT, 1)
            ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.full[st], (cnt / L::NST) & 1));
            uint32_t n = (used >> (8 * b)) & 255u;
            for (int qt = 0; qt < n_qt && ok; ++qt) {
-             if (!any_seen(p, c, qt, k0)) continue;
+             if (!any_seen(p, c, tpt, qt, k0)) continue;
              // (the phase before an mbarrier's first counts as complete)
              ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_free[b], (n - 1) & 1));
              if (!ok) break;
@@ -522,14 +555,14 @@ __global__ void __launch_bounds__(MT, 1)
            const float old = j < c.n ? *mass : 0.f;  // (on its way while the products run)
            float sum = 0.f;
            for (int qt = 0; qt < n_qt && ok; ++qt) {
-             if (!any_seen(p, c, qt, k0)) continue;
+             if (!any_seen(p, c, tpt, qt, k0)) continue;
              ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[b], n & 1));
              if (!ok) break;
              ++n;
              tc_fence_after();
-             const bool all = all_seen(p, c, qt, k0);
+             const bool all = all_seen(p, c, tpt, qt, k0);
              int lo = 0, hi = TROWS;
-             if (!all) columns_seeing(p, c, qt, j, lo, hi);
+             if (!all) columns_seeing(p, c, tpt, qt, j, lo, hi);
              sum += row_weights(ts, ctl.nl[seg % SLOTS][qt], 0, sl, all, lo, hi, [] {});
              sum += row_weights(ts, ctl.nl[seg % SLOTS][qt], 64, sl, all, lo, hi, [&] {
                tc_fence_before();
