@@ -5,27 +5,29 @@
 // head) pair and a tile packs 128 of them. Per pair of a query row and a cached
 // row it sees: 4 D flop and one exponential.
 //
-// bf16 rows (prefill_tc_kernel): tcgen05, one CTA per SM with two query tiles,
-// so that the tensor cores work on one tile while the other's weights are
-// formed. Roles:
+// bf16 rows (prefill_tc_kernel): tcgen05, one CTA per SM with two query tiles.
+// A step takes 64 cached rows: S = Q K^T (128 x 64), weights P from S, O += P V.
+// One step is a chain -- eight MMAs and their completion 1056 clocks, then the
+// weights, then a signal back, about 250 clocks -- several times longer than
+// its MMAs run, so two steps of each query tile are in flight, each in its own
+// buffer of tensor memory. (With one 128-row step per query tile in flight the
+// 8192-token prompt took 419 us at 55% of the tensor cores' cycles.) Roles:
 //   - the copy warp brings the cache's 128-row tiles of K and V, in turn, into a
 //     ring by TMA (a pool's blocks as boxes of a tile);
-//   - the MMA warp's elected thread issues, per tile of rows and query tile,
-//     O += P V for the previous weights and S = Q K^T for the next ones;
-//   - two warpgroups per query tile turn S into P: a thread has 64 of a query
+//   - an MMA warp per query tile: one thread issues, step by step, the product
+//     with V once the weights are ready and the S of the step after next (issuing
+//     blocks for as long as the MMAs run);
+//   - two warpgroups per query tile turn S into P: a thread has 32 of a query
 //     row's columns (row = lane of tensor memory), and two threads share their
-//     row's maximum through shared memory. (One thread per row measured 435
-//     instead of XXX us on the 8192-token prompt: the weights of one tile took
-//     longer than the products of the other.) P, rounded to bf16, takes S's
-//     place as the A operand of the product with V, so the weights never pass
-//     through shared memory.
-// Tensor memory: S/P of the two tiles 2 x 128 columns, O 2 x D columns.
-// The running maximum of a row is raised only when a tile exceeds it by more
-// than 8 (a factor of 256): O is then rescaled in tensor memory; until then
-// weights are up to 256, which costs no precision in a floating format. S of a
-// tile is complete only after the products with V issued before it, so the
-// warpgroup that has seen it may rescale O.
-// Tiles at the edge of what the rows see are masked by position; rows of V past
+//     row's maximum through shared memory. P, rounded to bf16, takes its part of
+//     S's place as the A operand of the product with V, so the weights never
+//     pass through shared memory.
+// Tensor memory: per query tile 2 x 64 columns of S/P and D columns of O.
+// The running maximum of a row is raised only when a step exceeds it by more
+// than 8 (a factor of 256): O is then rescaled in tensor memory, once the
+// products before have completed; until then weights are up to 256, which costs
+// no precision in a floating format.
+// Steps at the edge of what the rows see are masked by position; rows of V past
 // the last query's are set to zero in shared memory, whatever they hold.
 //
 // fp32 rows (prefill_kernel): CUDA cores, 64 x 64 tiles in shared memory.
@@ -40,31 +42,30 @@ namespace {
 // ---------------------------------------------------------------------------
 // bf16 rows
 // ---------------------------------------------------------------------------
-constexpr int PT = 640;  // copy warp, MMA warp, two idle, four warpgroups
+constexpr int PT = 640;      // copy warp, two MMA warps, an idle one, four warpgroups
+constexpr int STEP = 64;     // cached rows of a step
 constexpr float RAISE = 8.f;
-constexpr int REGS_LESS = 56, REGS_MORE = 104;  // 128 * 56 + 512 * 104 <= 640 * 96
 
 template <int D>
 struct TcSmem {
   static constexpr int TILE = D / 64 * TCOL;
-  static constexpr int NST = D == 128 ? 5 : 10;
+  static constexpr int NST = D == 128 ? 4 : 8;
   static constexpr int RING = 2 * TILE;  // after the two query tiles
   static constexpr int CTRL = RING + NST * TILE;
-  static constexpr int BYTES = CTRL + 2560;
+  static constexpr int BYTES = CTRL + 4608;
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
 struct TcCtl {
-  uint64_t full[12], empty[12];        // ring stages
-  uint64_t q_ready[2];                 // the query tile is in shared memory
-  uint64_t s_full[2], p_ready[2][2];   // S complete; the first and second columns of P written
-  uint64_t o_done[2];                  // every product of the tile complete
-  uint64_t v_fix;                      // the last tile of V has landed, before its tail is cleared
+  uint64_t full[8], empty[8];                           // ring stages
+  uint64_t q_ready[2];                                  // the query tile is in shared memory
+  uint64_t s_full[2][2], p_ready[2][2], o_ready[2][2];  // [query tile][half of a tile of rows]: S complete; P written; its product complete
+  uint64_t v_fix;                                       // the last tile of V has landed, before its tail is cleared
   uint32_t tmem;
   int flag;
-  float mx[2][2][TROWS];               // maxima: [query tile][half][row]
+  float mx[2][2][2][TROWS];                             // maxima: [step parity][query tile][half][row]
 };
-static_assert(sizeof(TcCtl) <= 2560, "control block");
+static_assert(sizeof(TcCtl) <= 4608, "control block");
 
 template <int D>
 __global__ void __launch_bounds__(PT, 1)
@@ -73,7 +74,9 @@ __global__ void __launch_bounds__(PT, 1)
   using L = TcSmem<D>;
   extern __shared__ __align__(1024) unsigned char smem[];  // (the swizzle goes by address)
   TcCtl& ctl = *reinterpret_cast<TcCtl*>(smem + L::CTRL);
-  const int t = threadIdx.x, w = t >> 5, lane = t & 31, G = p.group;
+  // (values that the MMA warps use come through a shuffle, so that the compiler
+  // knows them to be the same in a warp and keeps them in uniform registers)
+  const int t = threadIdx.x, w = __shfl_sync(FULL_MASK, t >> 5, 0), lane = t & 31, G = p.group;
   // the last tokens see the most rows: their tiles first
   const int n_ls = p.n_seq * p.n_kv_heads;
   const int ls = blockIdx.x % n_ls, tile = n_tiles - 1 - static_cast<int>(blockIdx.x) / n_ls;
@@ -90,23 +93,33 @@ __global__ void __launch_bounds__(PT, 1)
   const int32_t* trow = p.rows.seq_table(c.s);
   if (!chunk_blocks_ok(p, trow, rf0, r_hi, &ctl.flag)) return;
   const TileList list = tiles_seen(p, rf0, r_hi);
-  const int n_list = list.count();
-  auto needed = [&](int q, int i) {
-    const int k0 = list.at(i) * TROWS;
-    return q == 0 ? tile_seen(p, k0, TROWS, rf0, rl0) : q < nq && tile_seen(p, k0, TROWS, rf1, rl1);
+  const int n_list = __shfl_sync(FULL_MASK, list.count(), 0);
+  // the tiles of the list that query tile q needs: [0, a) and [f, e)
+  struct Range {
+    int a, f, e;
+    __device__ bool has(int i) const { return i < a || (i >= f && i < e); }
+  };
+  auto range_of = [&](int q) {
+    const int rf = q ? rf1 : rf0, rl = q ? rl1 : rl0;
+    Range r;
+    r.a = rl < 0 ? 0 : min(list.a, rl / TROWS + 1);
+    r.f = p.window ? list.a + max(0, max(0, rf - p.window + 1) / TROWS - list.b) : 0;
+    r.e = rl < 0 ? 0 : list.a + max(0, rl / TROWS + 1 - list.b);
+    return Range{__shfl_sync(FULL_MASK, r.a, 0), __shfl_sync(FULL_MASK, r.f, 0), __shfl_sync(FULL_MASK, r.e, 0)};
   };
 
   if (t == 0) {
     for (int i = 0; i < L::NST; ++i) {
       mbar_init(&ctl.full[i], 1);
-      mbar_init(&ctl.empty[i], 1);
+      mbar_init(&ctl.empty[i], nq);
     }
     for (int q = 0; q < 2; ++q) {
       mbar_init(&ctl.q_ready[q], 8);  // (a warp arrives once)
-      mbar_init(&ctl.s_full[q], 1);
-      mbar_init(&ctl.p_ready[q][0], 8);
-      mbar_init(&ctl.p_ready[q][1], 8);
-      mbar_init(&ctl.o_done[q], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&ctl.s_full[q][b], 1);
+        mbar_init(&ctl.p_ready[q][b], 8);
+        mbar_init(&ctl.o_ready[q][b], 1);
+      }
     }
     mbar_init(&ctl.v_fix, 1);
     mbar_init_fence();
@@ -115,12 +128,13 @@ __global__ void __launch_bounds__(PT, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tm = ctl.tmem;
+  const uint32_t tm = __shfl_sync(FULL_MASK, ctl.tmem, 0);
+  auto s_col = [&](int q, int b) { return tm + (q * 2 + b) * STEP; };
+  auto o_col = [&](int q) { return tm + 256 + q * 128; };
   const uint32_t qa = smem_addr(smem), ring = qa + L::RING;
   bool ok = true;
 
   if (w == 0) {
-    regs_less<REGS_LESS>();
     // ---- copies: K and V tiles take the ring's stages in turn ----
     int cnt = 0;
     int blk = n_list ? tile_block<D>(p, box_rows, trow, list.at(0) * TROWS, c.n, lane) : 0, blk_next = 0;
@@ -154,66 +168,64 @@ __global__ void __launch_bounds__(PT, 1)
       // let the copies in flight finish before shared memory is given up
       for (int u = max(0, cnt - L::NST); u < cnt; ++u) (void)mbar_wait_bounded(&ctl.full[u % L::NST], (u / L::NST) & 1);
     }
-  } else if (w == 1) {
-    regs_less<REGS_LESS>();
-    // ---- MMAs ----
-    if (elect_one()) {
-      constexpr uint32_t IQK = bf16_idesc(TROWS, TROWS, false), IPV = bf16_idesc(TROWS, D, true);
-      bool begun[2] = {false, false};
-      int np[2] = {0, 0};  // weights taken so far
-      auto wait_stage = [&](int cnt) { return mbar_wait_bounded(&ctl.full[cnt % L::NST], (cnt / L::NST) & 1); };
-      auto issue_s = [&](int q, int i) {
-        umma_rows<D>(tm + q * 128, qa + q * L::TILE, ring + (2 * i) % L::NST * L::TILE, IQK);
-        umma_commit(&ctl.s_full[q]);
+  } else if (w < 3) {
+    // ---- MMAs of query tile w - 1 ----
+    const int q = w - 1;
+    const Range need = range_of(q);
+    if (q < nq && elect_one()) {
+      constexpr uint32_t IQK = bf16_idesc(TROWS, STEP, false), IPV = bf16_idesc(TROWS, D, true);
+      constexpr uint64_t STAGE = L::TILE >> 4;  // (descriptors count 16 bytes)
+      const uint64_t dq = sw128_desc(qa + q * L::TILE), dk = sw128_desc(ring), dv = sw128_desc_mn(ring);
+      const uint32_t to = o_col(q);
+      auto issue_s = [&](uint32_t at, int b) {
+        const uint64_t ds = dk + at * STAGE + b * (STEP * 8);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t off = (k >> 2) * (TCOL >> 4) + (k & 3) * 2;
+          umma_f16(s_col(q, b), dq + off, ds + off, IQK, k > 0);
+        }
+        umma_commit(&ctl.s_full[q][b]);
       };
-      for (int q = 0; q < nq && ok; ++q) ok = mbar_wait_bounded(&ctl.q_ready[q], 0);
+      uint32_t n = 0;  // tiles done
+      ok = mbar_wait_bounded(&ctl.q_ready[q], 0);
       if (n_list > 0 && ok) {
-        ok = wait_stage(0);
+        ok = mbar_wait_bounded(&ctl.full[0], 0);
         tc_fence_after();
-        for (int q = 0; q < nq && ok; ++q)
-          if (needed(q, 0)) issue_s(q, 0);
+        if (ok && need.has(0)) {
+          issue_s(0, 0);
+          issue_s(0, 1);
+        }
         umma_commit(&ctl.empty[0]);
       }
       for (int i = 0; i < n_list && ok; ++i) {
-        const bool more = i + 1 < n_list;
-        ok = wait_stage(2 * i + 1) && (!more || wait_stage(2 * i + 2));
+        const bool now = need.has(i), more = i + 1 < n_list, next = more && need.has(i + 1);
+        const uint32_t cv = 2 * i + 1, sv = cv % L::NST, sk = (cv + 1) % L::NST;
+        ok = mbar_wait_bounded(&ctl.full[sv], (cv / L::NST) & 1);
+        if (ok && more) ok = mbar_wait_bounded(&ctl.full[sk], ((cv + 1) / L::NST) & 1);
         if (!ok) break;
-        tc_fence_after();
-        const uint32_t v = ring + (2 * i + 1) % L::NST * L::TILE;
-        for (int q = 0; q < nq; ++q) {
-          if (needed(q, i)) {
-            // P's columns 16 j .. 16 j + 15 of half h (rows 64 h + 16 j .. of V) sit at columns
-            // 64 h + 8 j; a part is two such steps of each half
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              if (ok) ok = mbar_wait_bounded(&ctl.p_ready[q][part], np[q] & 1);
-              tc_fence_after();
+        for (int b = 0; b < 2; ++b) {
+          if (now) {
+            ok = ok && mbar_wait_bounded(&ctl.p_ready[q][b], n & 1);
+            tc_fence_after();
+            // P's rows 16 j .. 16 j + 15 of the step sit at columns 32 (j / 2) + 8 (j % 2) of its buffer
+            const uint64_t ds = dv + sv * STAGE + b * (STEP * 8);
+            umma_ts(to, s_col(q, b), ds, IPV, n > 0 || b > 0);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int h = k >> 1, j = 2 * part + (k & 1);
-                umma_ts(tm + 256 + q * 128, tm + q * 128 + h * 64 + j * 8, sw128_desc_mn(v + (h * 4 + j) * 2048), IPV, begun[q]);
-                begun[q] = true;
-              }
-            }
-            if (!ok) break;
-            ++np[q];
+            for (int j = 1; j < STEP / 16; ++j) umma_ts(to, s_col(q, b) + (j >> 1) * 32 + (j & 1) * 8, ds + j * 128, IPV, true);
+            umma_commit(&ctl.o_ready[q][b]);
           }
-          if (more && needed(q, i + 1)) issue_s(q, i + 1);
+          if (next) issue_s(sk, b);
         }
-        if (!ok) break;
-        umma_commit(&ctl.empty[(2 * i + 1) % L::NST]);
-        if (more) umma_commit(&ctl.empty[(2 * i + 2) % L::NST]);
+        n += now;
+        umma_commit(&ctl.empty[sv]);
+        if (more) umma_commit(&ctl.empty[sk]);
       }
-      umma_commit(&ctl.o_done[0]);
-      umma_commit(&ctl.o_done[1]);
       if (!ok) set_status(p.dev_status, TRI_DEV_TIMEOUT);
     }
     __syncwarp();
-  } else if (w < 4) {
-    regs_less<REGS_LESS>();
-  } else if (w < 12 || nq == 2) {
-    regs_more<REGS_MORE>();
-    // ---- weights: thread u of a half = query row u of tile q, 64 columns ----
+  } else if (w >= 4 && (w < 12 || nq == 2)) {
+    // ---- weights: thread u of a half = query row u of tile q, 32 columns of a step ----
     const int q = (w - 4) >> 3, half = ((w - 4) >> 2) & 1, u = t & 127;
     const int toks = q ? toks1 : toks0, rows = toks * G, rf = q ? rf1 : rf0, rl = q ? rl1 : rl0;
     load_query_tile<D, 256>(smem + q * L::TILE, p, c.seq, c.h, tok0 + q * tpt, rows, half * 128 + u);
@@ -221,107 +233,107 @@ __global__ void __launch_bounds__(PT, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&ctl.q_ready[q]);
     const uint32_t lanes = static_cast<uint32_t>((w & 3) * 32) << 16;
-    const uint32_t ts = tm + q * 128 + lanes, to = tm + 256 + q * 128 + half * (D / 2) + lanes;
+    const uint32_t to = o_col(q) + half * (D / 2) + lanes;
     const int r = rf + u / G;
     const int pair = 1 + q * 4 + (w & 3);  // named barrier of the two warps of 32 rows
     const float sl = p.scale * LOG2E;
     float m = NEG_INF, l = 0.f;
-    int ns = 0;
-    for (int i = 0; i < n_list; ++i) {
-      if (!needed(q, i)) continue;
+    const Range need = range_of(q);
+    int n = 0;  // steps done
+    // The products of the steps before n are complete. (Those before n - 1 are: S of
+    // step n was issued after them.)
+    auto wait_products = [&] {
+      if (n > 0 && ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.o_ready[q][(n - 1) & 1], ((n - 1) >> 1) & 1));
+      tc_fence_after();
+    };
+    for (int step = 0; step < 2 * n_list; ++step) {
+      if (!need.has(step >> 1)) continue;
+      const int b = step & 1;
+      const uint32_t ts = s_col(q, b) + half * 32 + lanes;
       // (after a wait that gave up the loop runs on without waiting, since the
       // two halves meet at barriers)
-      if (ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[q], ns & 1));
+      if (ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[q][b], (n >> 1) & 1));
       tc_fence_after();
-      uint32_t x[64];
-      tmem_ld32(ts + half * 64, x);
-      tmem_ld32(ts + half * 64 + 32, x + 32);
+      uint32_t x[32];
+      tmem_ld32(ts, x);
       tmem_wait_ld();
-      const int k0 = list.at(i) * TROWS;
-      const bool inner = k0 + TROWS - 1 <= rf && (p.window == 0 || k0 > rl - p.window || k0 + TROWS <= p.n_sink);
+      const int k0 = list.at(step >> 1) * TROWS + b * STEP;
+      const bool inner = k0 + STEP - 1 <= rf && (p.window == 0 || k0 > rl - p.window || k0 + STEP <= p.n_sink);
       if (!inner) {
+        const uint32_t bits = seen_bits(p, r, k0, half);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t bits = seen_bits(p, r, k0, half * 2 + k);
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!(bits & (1u << e))) x[32 * k + e] = 0xff800000u;  // -inf
-        }
+        for (int e = 0; e < 32; ++e)
+          if (!(bits & (1u << e))) x[e] = 0xff800000u;  // -inf
       }
       float mxs[4];  // (four chains)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         mxs[k] = __uint_as_float(x[k]);
 #pragma unroll
-        for (int e = 4; e < 60; e += 8) mxs[k] = max3(mxs[k], __uint_as_float(x[e + k]), __uint_as_float(x[e + 4 + k]));
-        mxs[k] = fmaxf(mxs[k], __uint_as_float(x[60 + k]));
+        for (int e = 4; e < 28; e += 8) mxs[k] = max3(mxs[k], __uint_as_float(x[e + k]), __uint_as_float(x[e + 4 + k]));
+        mxs[k] = fmaxf(mxs[k], __uint_as_float(x[28 + k]));
       }
       float mx = fmaxf(max3(mxs[0], mxs[1], mxs[2]), mxs[3]);
-      // (the partner has read the tile before's: S of this tile is issued after
-      // both halves' weights of that one)
-      ctl.mx[q][half][u] = mx;
+      ctl.mx[n & 1][q][half][u] = mx;
       asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
-      mx = fmaxf(mx, ctl.mx[q][half ^ 1][u]) * sl;
-      if (ns == 0) {
+      mx = fmaxf(mx, ctl.mx[n & 1][q][half ^ 1][u]) * sl;
+      if (n == 0) {
         m = mx;
       } else if (__any_sync(FULL_MASK, mx > m + RAISE)) {  // (the same in both halves)
         const float mn = fmaxf(m, mx);
         const float a = mn == NEG_INF ? 1.f : fast_exp2(m - mn);
         m = mn;
         l *= a;
+        wait_products();
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {  // (few registers are left)
-          uint32_t o[8];
-          tmem_ld8(to + k * 8, o);
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t o[16];
+          tmem_ld16(to + k * 16, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-          tmem_st8(to + k * 8, o);
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+          tmem_st16(to + k * 16, o);
         }
       }
       const float mu = m == NEG_INF ? 0.f : m;
       float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {  // the products start on the first
-#pragma unroll
-        for (int k = part * 16; k < part * 16 + 16; k += 2) {
-          float e0, e1, e2, e3;
-          fma2(e0, e1, __uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), sl, -mu);
-          fma2(e2, e3, __uint_as_float(x[2 * k + 2]), __uint_as_float(x[2 * k + 3]), sl, -mu);
-          e0 = fast_exp2(e0);
-          e1 = fast_exp2(e1);
-          e2 = fast_exp2(e2);
-          e3 = fast_exp2(e3);
-          add2(l0, l1, e0, e1);
-          add2(l2, l3, e2, e3);
-          x[k] = pack_bf16(e0, e1);
-          x[k + 1] = pack_bf16(e2, e3);
-        }
-        tmem_st16(ts + half * 64 + part * 16, x + part * 16);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.p_ready[q][part]);
+      for (int k = 0; k < 16; k += 2) {
+        float e0, e1, e2, e3;
+        fma2(e0, e1, __uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), sl, -mu);
+        fma2(e2, e3, __uint_as_float(x[2 * k + 2]), __uint_as_float(x[2 * k + 3]), sl, -mu);
+        e0 = fast_exp2(e0);
+        e1 = fast_exp2(e1);
+        e2 = fast_exp2(e2);
+        e3 = fast_exp2(e3);
+        add2(l0, l1, e0, e1);
+        add2(l2, l3, e2, e3);
+        x[k] = pack_bf16(e0, e1);
+        x[k + 1] = pack_bf16(e2, e3);
       }
       l += (l0 + l1) + (l2 + l3);
-      ++ns;
+      tmem_st16(ts, x);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.p_ready[q][b]);
+      ++n;
     }
-    if (ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.o_done[q], 0));
-    ctl.mx[q][half][u] = l;
+    wait_products();
+    ctl.mx[n & 1][q][half][u] = l;
     asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
-    const float l_half = ctl.mx[q][half ^ 1][u];
+    const float l_half = ctl.mx[n & 1][q][half ^ 1][u];
     l = half ? l_half + l : l + l_half;
     if (!ok) {
       if (lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
     } else {
-      tc_fence_after();
       const float inv = l != 0.f ? 1.f / l : 0.f;
       const int64_t head = (static_cast<int64_t>(c.seq) * p.n_q + tok0 + q * tpt + u / G) * (p.n_kv_heads * G) + c.h * G + u % G;
       uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + head * D + half * (D / 2));
 #pragma unroll
       for (int k = 0; k < D / 64; ++k) {
         uint32_t o[32];
-        if (ns > 0) {
+        if (n > 0) {
           tmem_ld32(to + k * 32, o);
           tmem_wait_ld();
         } else {
