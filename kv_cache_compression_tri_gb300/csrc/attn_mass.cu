@@ -31,7 +31,7 @@ namespace {
 // ---------------------------------------------------------------------------
 // bf16 rows
 // ---------------------------------------------------------------------------
-constexpr int MT = 640;    // copy warp, MMA warp, lse warp, an idle one, four warpgroups
+constexpr int MT = 640;    // copy warp, MMA warp, lse warp, second MMA warp, four warpgroups
 constexpr int FEW = 2;     // query tiles that stay in shared memory
 constexpr int SLOTS = 16;  // lse rows kept by mass_few_kernel (see there)
 
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(MT, 1)
   using L = TcMass<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
   MassCtl& ctl = *reinterpret_cast<MassCtl*>(smem + L::CTRL);
-  const int t = threadIdx.x, w = t >> 5, lane = t & 31;
+  const int t = threadIdx.x, w = __shfl_sync(FULL_MASK, t >> 5, 0), lane = t & 31;
   const int n_ls = p.n_seq * p.n_kv_heads, ls = blockIdx.x % n_ls, pair = blockIdx.x / n_ls;
   Chunk c;
   if (!chunk_of(p, ls, c)) return;
@@ -187,14 +187,33 @@ __global__ void __launch_bounds__(MT, 1)
   const int nk = pair == other ? 1 : 2;
   const int32_t* trow = p.rows.seq_table(c.s);
   if (!chunk_blocks_ok(p, trow, c.r0, r_end, &ctl.flag)) return;
-  const int tpt = TROWS / p.group, n_qt = (c.n_new + tpt - 1) / tpt;
+  const int tpt = TROWS / p.group, n_qt = __shfl_sync(FULL_MASK, (c.n_new + tpt - 1) / tpt, 0);
   auto k_of = [&](int kt) { return (kt ? other : pair) * TROWS; };
-  auto needed = [&](int kt, int qt) { return kt < nk && any_seen(p, c, tpt, qt, k_of(kt)); };
+  // the query tiles that see any row of tile kt: [lo, hi) (uniform values, see prefill_tc_kernel)
+  struct Range {
+    int lo, hi;
+    __device__ bool has(int i) const { return i >= lo && i < hi; }
+  };
+  auto range_of = [&](int kt) {
+    Range r{0, 0};
+    if (kt < nk) {
+      // tokens from the tile's first row on, and with a window up to its last row + window - 1
+      const int k0 = k_of(kt);
+      r.lo = max(0, k0 - c.r0) / tpt;
+      r.hi = n_qt;
+      if (p.window && k0 >= p.n_sink) {
+        const int64_t last = static_cast<int64_t>(k0) + TROWS - 1 + p.window - 1 - c.r0;
+        r.hi = static_cast<int>(min(static_cast<int64_t>(n_qt), last < 0 ? 0 : last / tpt + 1));
+      }
+    }
+    return Range{__shfl_sync(FULL_MASK, r.lo, 0), __shfl_sync(FULL_MASK, r.hi, 0)};
+  };
+  const Range need0 = range_of(0), need1 = range_of(1);
 
   if (t == 0) {
     for (int i = 0; i < L::NST; ++i) {
       mbar_init(&ctl.full[i], 2);    // the queries and their lse
-      mbar_init(&ctl.empty[i], 17);  // the MMAs and 16 warps
+      mbar_init(&ctl.empty[i], 18);  // two threads' MMAs and 16 warps
     }
     mbar_init(&ctl.res_full, 1);
     for (int b = 0; b < 4; ++b) {
@@ -208,7 +227,7 @@ __global__ void __launch_bounds__(MT, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tm = ctl.tmem, res = smem_addr(smem), ring = res + L::RING;
+  const uint32_t tm = __shfl_sync(FULL_MASK, ctl.tmem, 0), res = smem_addr(smem), ring = res + L::RING;
   bool ok = true;
 
   if (w == 0) {
@@ -219,7 +238,7 @@ __global__ void __launch_bounds__(MT, 1)
                    c.seq, c.h, k_of(kt), &ctl.res_full, lane);
     int cnt = 0;
     for (int qt = 0; qt < n_qt && ok; ++qt) {
-      if (!needed(0, qt) && !needed(1, qt)) continue;
+      if (!need0.has(qt) && !need1.has(qt)) continue;
       const int st = cnt % L::NST;
       if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
       if (!ok) break;
@@ -235,50 +254,80 @@ __global__ void __launch_bounds__(MT, 1)
     (void)mbar_wait_bounded(&ctl.res_full, 0);
     for (int u = max(0, cnt - L::NST); u < cnt; ++u) (void)mbar_wait_bounded(&ctl.full[u % L::NST], (u / L::NST) & 1);
   } else if (w == 2) {
-    // ---- lse, each tile's loaded before the stage of the one before is free ----
-    int cnt = 0;
-    bool any = false;
-    float nl[TROWS / 32];
-    auto store = [&] {
-      const int st = cnt % L::NST;
+    // ---- lse: a tile's is loaded two tiles before it is stored (two register sets in turn) ----
+    const int per_tile = tpt * p.n_kv_heads * p.group;
+    const float* src[TROWS / 32];
+    int tok[TROWS / 32];  // within a tile; n_new: none
+#pragma unroll
+    for (int k = 0; k < TROWS / 32; ++k) {
+      const int u = k * 32 + lane;
+      tok[k] = u < tpt * p.group ? u / p.group : c.n_new;
+      src[k] = p.lse_in + c.seq * p.lse_seq + static_cast<int64_t>(u / p.group) * (p.n_kv_heads * p.group) + c.h * p.group + u % p.group;
+    }
+    auto next = [&](int qt) {
+      while (qt < n_qt && !need0.has(qt) && !need1.has(qt)) ++qt;
+      return qt;
+    };
+    auto get = [&](float (&x)[TROWS / 32], int qt) {
+#pragma unroll
+      for (int k = 0; k < TROWS / 32; ++k)
+        x[k] = qt < n_qt && qt * tpt + tok[k] < c.n_new ? __ldg(src[k] + static_cast<int64_t>(qt) * per_tile) : -NEG_INF;
+    };
+    uint32_t cnt = 0;
+    auto store = [&](const float (&x)[TROWS / 32]) {
+      const uint32_t st = cnt % L::NST;
       if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
 #pragma unroll
-      for (int k = 0; k < TROWS / 32; ++k) (&ctl.nl[0][0][0])[st * TROWS + k * 32 + lane] = nl[k];
+      for (int k = 0; k < TROWS / 32; ++k) (&ctl.nl[0][0][0])[st * TROWS + k * 32 + lane] = -LOG2E * x[k];
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.full[st]);
       ++cnt;
     };
-    for (int qt = 0; qt < n_qt && ok; ++qt) {
-      if (!needed(0, qt) && !needed(1, qt)) continue;
-      float next[TROWS / 32];
-      get_lse(next, p, c, tpt, qt, lane);
-      if (any) store();
-      any = true;
-#pragma unroll
-      for (int k = 0; k < TROWS / 32; ++k) nl[k] = next[k];
+    float xa[TROWS / 32], xb[TROWS / 32];
+    int qa = next(0), qb = next(qa + 1);
+    get(xa, qa);
+    get(xb, qb);
+    while (qa < n_qt && ok) {
+      store(xa);
+      qa = next(qb + 1);
+      get(xa, qa);
+      if (qb >= n_qt || !ok) break;
+      store(xb);
+      qb = next(qa + 1);
+      get(xb, qb);
     }
-    if (any && ok) store();
     if (!ok && lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
-  } else if (w == 1) {
+  } else if (w < 4) {
+    // ---- MMAs: products w == 1 ? 0, 2, .. : 1, 3, .. ----
+    const int par = w == 1 ? 0 : 1;
     if (elect_one()) {
       constexpr uint32_t IDESC = bf16_idesc(TROWS, TROWS, false);
-      int cnt = 0, pc[2] = {0, 0};
+      constexpr uint64_t STAGE = L::TILE >> 4;  // (descriptors count 16 bytes)
+      const uint64_t dk = sw128_desc(res), dr = sw128_desc(ring);
+      uint32_t cnt = 0, n = 0;  // stages taken, products counted
       ok = mbar_wait_bounded(&ctl.res_full, 0);
       for (int qt = 0; qt < n_qt && ok; ++qt) {
-        const bool need[2] = {needed(0, qt), needed(1, qt)};
+        const bool need[2] = {need0.has(qt), need1.has(qt)};
         if (!need[0] && !need[1]) continue;
-        const int st = cnt % L::NST;
+        const uint32_t st = cnt % L::NST;
         ok = mbar_wait_bounded(&ctl.full[st], (cnt / L::NST) & 1);
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
           if (!need[kt] || !ok) continue;
-          const int b = kt * 2 + (pc[kt] & 1);
-          if (pc[kt] >= 2) ok = mbar_wait_bounded(&ctl.s_free[b], ((pc[kt] >> 1) - 1) & 1);
-          if (!ok) continue;
-          tc_fence_after();
-          umma_rows<D>(tm + b * 128, res + kt * L::TILE, ring + st * L::TILE, IDESC);
-          umma_commit(&ctl.s_full[b]);
-          ++pc[kt];
+          if ((n & 1) == par) {
+            const uint32_t b = n & 3;
+            // (the phase before an mbarrier's first counts as complete)
+            ok = mbar_wait_bounded(&ctl.s_free[b], ((n >> 2) + 1) & 1);
+            if (!ok) continue;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint64_t off = (k >> 2) * (TCOL >> 4) + (k & 3) * 2;
+              umma_f16(tm + b * 128, dk + kt * STAGE + off, dr + st * STAGE + off, IDESC, k > 0);
+            }
+            umma_commit(&ctl.s_full[b]);
+          }
+          ++n;
         }
         if (!ok) break;
         umma_commit(&ctl.empty[st]);
@@ -287,40 +336,46 @@ __global__ void __launch_bounds__(MT, 1)
       if (!ok) set_status(p.dev_status, TRI_DEV_TIMEOUT);
     }
     __syncwarp();
-  } else if (w >= 4) {
-    const int kt = (w - 4) >> 3, half = ((w - 4) >> 2) & 1, u = t & 127;
-    const uint32_t ts = tm + kt * 256 + (static_cast<uint32_t>((w & 3) * 32) << 16);
-    const int k0 = k_of(kt), j = k0 + u;
+  } else {
+    // ---- weights: pair `par` takes products of its parity, a thread 64 columns of a row ----
+    const int par = (w - 4) >> 3, half = ((w - 4) >> 2) & 1, u = t & 127;
+    const uint32_t lanes = static_cast<uint32_t>((w & 3) * 32) << 16;
     const float sl = p.scale * LOG2E;
-    float sum = 0.f;
-    int cnt = 0, pc = 0;
+    float sums[2] = {0.f, 0.f};
+    uint32_t cnt = 0, n = 0;
     for (int qt = 0; qt < n_qt && ok; ++qt) {
-      const bool mine = needed(kt, qt);
-      if (!mine && !needed(kt ^ 1, qt)) continue;
-      const int st = cnt % L::NST;
+      const bool need[2] = {need0.has(qt), need1.has(qt)};
+      if (!need[0] && !need[1]) continue;
+      const uint32_t st = cnt % L::NST;
       ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.full[st], (cnt / L::NST) & 1));
-      if (!ok) break;
-      if (mine) {
-        const int b = kt * 2 + (pc & 1);
-        ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[b], (pc >> 1) & 1));
-        if (!ok) break;
-        tc_fence_after();
-        const bool all = all_seen(p, c, tpt, qt, k0);
-        int lo = 0, hi = TROWS;
-        if (!all) columns_seeing(p, c, tpt, qt, j, lo, hi);
-        sum += row_weights(ts + (pc & 1) * 128, &ctl.nl[0][0][0] + st * TROWS, half * 64, sl, all, lo, hi, [&] {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.s_free[b]);
-        });
-        ++pc;
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        if (!need[kt] || !ok) continue;
+        if ((n & 1) == par) {
+          const uint32_t b = n & 3;
+          ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[b], (n >> 2) & 1));
+          if (!ok) continue;
+          tc_fence_after();
+          const int k0 = k_of(kt);
+          const bool all = all_seen(p, c, tpt, qt, k0);
+          int lo = 0, hi = TROWS;
+          if (!all) columns_seeing(p, c, tpt, qt, k0 + u, lo, hi);
+          sums[kt] += row_weights(tm + b * 128 + lanes, &ctl.nl[0][0][0] + st * TROWS, half * 64, sl, all, lo, hi, [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.s_free[b]);
+          });
+        }
+        ++n;
       }
+      if (!ok) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.empty[st]);
       ++cnt;
     }
     if (!ok && lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
-    ctl.nl[8 + kt * 2 + half][0][u] = sum;  // (the ring's lse rows are below)
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) ctl.nl[8 + kt * 4 + par * 2 + half][0][u] = sums[kt];  // (the ring's lse rows are below)
   }
   tc_fence_before();
   const bool fine = __syncthreads_and(ok);
@@ -328,7 +383,8 @@ __global__ void __launch_bounds__(MT, 1)
   if (w == 1) tmem_dealloc(tm, 512);
   if (fine && t < nk * TROWS) {
     const int kt = t / TROWS, u = t % TROWS, j = k_of(kt) + u;
-    const float sum = ctl.nl[8 + 2 * kt][0][u] + ctl.nl[9 + 2 * kt][0][u];
+    const float(*part)[FEW][TROWS] = ctl.nl + 8 + kt * 4;
+    const float sum = (part[0][0][u] + part[1][0][u]) + (part[2][0][u] + part[3][0][u]);
     if (j <= r_end && sum != 0.f) p.mass[c.s * p.n_cap + j] += sum;
   }
 }
