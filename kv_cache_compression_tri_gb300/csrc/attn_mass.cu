@@ -90,7 +90,8 @@ __device__ __forceinline__ void columns_seeing(const AttnParams& p, const Chunk&
 // Sum of the weights of this thread's cached row over 64 query columns (of a
 // tile's, from `first`) at ts; `done` runs when S has been read. ALL: every
 // column counts, else columns [lo, hi) whatever the others hold. (Two loops: as
-// one with selects the 4096-token prompt took 189 us instead of YYY.)
+// one with selects the 4096-token prompt took 189 us
+// where this took 164.)
 template <bool ALL, class Done>
 __device__ __forceinline__ float row_weights(uint32_t ts, const float* nl, int first, float sl, int lo, int hi, Done done) {
   float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(MT, 1)
   using L = TcMass<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
   MassCtl& ctl = *reinterpret_cast<MassCtl*>(smem + L::CTRL);
-  const int t = threadIdx.x, w = t >> 5, lane = t & 31;
+  const int t = threadIdx.x, w = __shfl_sync(FULL_MASK, t >> 5, 0), lane = t & 31;
   const int64_t share = my_share(p, ctl);
   if (share == 0) return;
   const int tpt = TROWS / p.group;
@@ -488,45 +489,41 @@ __global__ void __launch_bounds__(MT, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tm = ctl.tmem, res = smem_addr(smem), ring = res + L::RING;
+  const uint32_t tm = __shfl_sync(FULL_MASK, ctl.tmem, 0), res = smem_addr(smem), ring = res + L::RING;
   bool ok = true;
 
-  // The walk, by a whole warp: body(segment, chunk, query tiles, cached tile k0) for every tile of the
-  // share that some query sees; next(segment, chunk, query tiles) before its first and
-  // last(segment) after its last one.
+  // The walk, by a whole warp: body(segment, chunk, query tiles, cached tile k0) for
+  // every tile of the share that some query sees; next(segment, chunk, query tiles)
+  // before its first and last(segment) after its last one.
   auto walk = [&](auto&& next, auto&& body, auto&& last) {
-    int ls = ctl.first_slice, i = ctl.first_tile, seg = 0;
-    for (int64_t left = share; left > 0 && ok; ++ls, i = 0) {
+    int ls = ctl.first_slice, first = ctl.first_tile, seg = 0;
+    for (int64_t left = share; left > 0 && ok; ++ls, first = 0) {
       const int n = tiles_of(p, ls);
       if (n == 0) continue;
-      const int end = static_cast<int>(min(static_cast<int64_t>(n), i + left));
-      left -= end - i;
+      const int end = static_cast<int>(min(static_cast<int64_t>(n), first + left));
+      left -= end - first;
       Chunk c;
       if (!chunk_of(p, ls, c)) continue;
       if (!warp_blocks_ok(p, c, lane)) {
         if (lane == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
         continue;
       }
-      const int n_qt = (c.n_new + tpt - 1) / tpt;
-      bool begun = false;
-      for (; i < end && ok; ++i) {
-        const int k0 = i * TROWS;
-        if (!tile_seen(p, k0, TROWS, max(c.r0, 0), c.n - 1)) continue;
-        if (!begun) next(seg, c, n_qt);
-        begun = true;
-        if (ok) body(seg, c, n_qt, k0);
-      }
-      if (begun && ok) {
-        last(seg);
-        ++seg;
-      }
+      const TileList list = tiles_seen(p, max(c.r0, 0), c.n - 1);
+      const int a = min(end, list.a), b = max(first, list.b), e = min(end, list.e);
+      if (first >= a && b >= e) continue;
+      const int n_qt = __shfl_sync(FULL_MASK, (c.n_new + tpt - 1) / tpt, 0);
+      next(seg, c, n_qt);
+      for (int i = first; i < a && ok; ++i) body(seg, c, n_qt, i * TROWS);
+      for (int i = b; i < e && ok; ++i) body(seg, c, n_qt, i * TROWS);
+      if (ok) last(seg);
+      ++seg;
     }
   };
 
   if (w == 0) {
     int cnt = 0, segs = 0;
-    int blk = 0, blk_row = -1;
-    const int32_t* blk_of = nullptr;  // the sequence and row that `blk` is for
+    const int32_t* trow = nullptr;
+    int blk = 0, blk_row = -1;  // (of the row it is for)
     walk(
         [&](int seg, const Chunk& c, int n_qt) {
           if (seg > 0) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.res_free, (seg - 1) & 1));
@@ -544,14 +541,14 @@ __global__ void __launch_bounds__(MT, 1)
               load_queries_tma<D>(res + qt * L::TILE, &qmap, p, c.seq, c.h, qt, &ctl.res_full);
           }
           segs = seg + 1;
+          trow = p.rows.seq_table(c.s);
+          blk_row = -1;
         },
         [&](int, const Chunk& c, int, int k0) {
           const int st = cnt % L::NST;
-          const int32_t* trow = p.rows.seq_table(c.s);
-          if (blk_row != k0 || blk_of != trow) blk = tile_block<D>(p, box_rows, trow, k0, c.n, lane);
+          if (blk_row != k0) blk = tile_block<D>(p, box_rows, trow, k0, c.n, lane);
           // (the next tile's is on its way while this one waits for its stage)
           blk_row = k0 + TROWS;
-          blk_of = trow;
           const int blk_next = tile_block<D>(p, box_rows, trow, blk_row, c.n, lane);
           if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
           if (!ok) return;
@@ -569,6 +566,8 @@ __global__ void __launch_bounds__(MT, 1)
   } else if (w == 1) {
     // (lane 0 issues: what a commit covers is its own thread's MMAs)
     constexpr uint32_t IDESC = bf16_idesc(TROWS, TROWS, false);
+    constexpr uint64_t STAGE = L::TILE >> 4;  // (descriptors count 16 bytes)
+    const uint64_t dq = sw128_desc(res), dr = sw128_desc(ring);
     int cnt = 0;
     uint32_t used = 0;  // 8 bits per buffer: uses so far, mod 256
     walk([&](int seg, const Chunk&, int) { ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.res_full, seg & 1)); },
@@ -583,7 +582,11 @@ __global__ void __launch_bounds__(MT, 1)
              if (!ok) break;
              tc_fence_after();
              if (lane == 0) {
-               umma_rows<D>(tm + b * 128, ring + st * L::TILE, res + qt * L::TILE, IDESC);
+#pragma unroll
+               for (int k = 0; k < D / 16; ++k) {
+                 const uint64_t off = (k >> 2) * (TCOL >> 4) + (k & 3) * 2;
+                 umma_f16(tm + b * 128, dr + st * STAGE + off, dq + qt * STAGE + off, IDESC, k > 0);
+               }
                umma_commit(&ctl.s_full[b]);
              }
              __syncwarp();
