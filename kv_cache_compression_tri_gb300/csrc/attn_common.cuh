@@ -72,6 +72,34 @@ __device__ __forceinline__ void widen(const uint4& w, float (&x)[4]) {
   x[3] = __uint_as_float(w.w);
 }
 
+// Barrier over the cluster's CTAs (over the CTA when it is alone).
+__device__ __forceinline__ void cluster_sync(int ns) {
+  if (ns == 1) {
+    __syncthreads();
+    return;
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// *p of CTA u of the cluster.
+__device__ __forceinline__ float cluster_ld(const float* p, int u, int ns) {
+  if (ns == 1) return *p;
+  float x;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(x) : "r"(smem_addr(p)), "r"(u) : "memory");
+  return x;
+}
+__device__ __forceinline__ float2 cluster_ld2(const float2* p, int u, int ns) {
+  const float* f = reinterpret_cast<const float*>(p);
+  return make_float2(cluster_ld(f, u, ns), cluster_ld(f + 1, u, ns));
+}
+__device__ __forceinline__ float4 cluster_ld4(const float4* p, int u) {
+  float4 x;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(smem_addr(p)), "r"(u) : "memory");
+  return x;
+}
+
 // (lo, hi) rounded to bf16, lo in the low half.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;

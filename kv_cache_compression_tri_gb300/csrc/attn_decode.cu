@@ -122,28 +122,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Barrier over the cluster's CTAs (over the CTA when it is alone).
-__device__ __forceinline__ void cluster_sync(int ns) {
-  if (ns == 1) {
-    __syncthreads();
-    return;
-  }
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// *p of CTA u of the cluster.
-__device__ __forceinline__ float cluster_ld(const float* p, int u, int ns) {
-  if (ns == 1) return *p;
-  float x;
-  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-               : "=f"(x) : "r"(smem_addr(p)), "r"(u) : "memory");
-  return x;
-}
-__device__ __forceinline__ float2 cluster_ld2(const float2* p, int u, int ns) {
-  const float* f = reinterpret_cast<const float*>(p);
-  return make_float2(cluster_ld(f, u, ns), cluster_ld(f + 1, u, ns));
-}
-
 // The result of a head's element, or of its log-sum, from the sums of all its rows.
 template <typename T, int D>
 __device__ __forceinline__ void store_out(const AttnParams& p, const Run& r, int g, int e, float o, float l) {

@@ -27,6 +27,11 @@
 // than 8 (a factor of 256): O is then rescaled in tensor memory, once the
 // products before have completed; until then weights are up to 256, which costs
 // no precision in a floating format.
+// A few CTAs' worth of queries (a follow-up question on a long cache) would leave
+// most SMs idle: then a cluster of CTAs shares a pair of query tiles, each takes a
+// run of the cached rows, and they join through their shared memories. The
+// tensor cores are not what bounds such a call, so the weights go in as a bf16 pair
+// (p rounded, and the rest rounded) instead of rounded once.
 // Steps at the edge of what the rows see are masked by position; rows of V past
 // the last query's are set to zero in shared memory, whatever they hold.
 //
@@ -67,11 +72,12 @@ struct TcCtl {
 };
 static_assert(sizeof(TcCtl) <= 4608, "control block");
 
-template <int D>
+template <int D, bool FEW_CTAS>
 __global__ void __launch_bounds__(PT, 1)
     prefill_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
-                      const __grid_constant__ CUtensorMap vmap, int box_rows, int n_tiles) {
+                      const __grid_constant__ CUtensorMap vmap, int box_rows, int n_tiles, int cluster) {
   using L = TcSmem<D>;
+  const int splits = FEW_CTAS ? cluster : 1;
   extern __shared__ __align__(1024) unsigned char smem[];  // (the swizzle goes by address)
   TcCtl& ctl = *reinterpret_cast<TcCtl*>(smem + L::CTRL);
   // (values that the MMA warps use come through a shuffle, so that the compiler
@@ -79,9 +85,10 @@ __global__ void __launch_bounds__(PT, 1)
   const int t = threadIdx.x, w = __shfl_sync(FULL_MASK, t >> 5, 0), lane = t & 31, G = p.group;
   // the last tokens see the most rows: their tiles first
   const int n_ls = p.n_seq * p.n_kv_heads;
-  const int ls = blockIdx.x % n_ls, tile = n_tiles - 1 - static_cast<int>(blockIdx.x) / n_ls;
+  const int unit = static_cast<int>(blockIdx.x) / splits, rank = static_cast<int>(blockIdx.x) % splits;
+  const int ls = unit % n_ls, tile = n_tiles - 1 - unit / n_ls;
   Chunk c;
-  if (!chunk_of(p, ls, c)) return;
+  if (!chunk_of(p, ls, c)) return;  // (all returns here are a whole cluster's)
   const int tpt = TROWS / G;  // tokens per query tile
   const int tok0 = tile * 2 * tpt;
   if (tok0 >= c.n_new) return;
@@ -93,8 +100,10 @@ __global__ void __launch_bounds__(PT, 1)
   const int32_t* trow = p.rows.seq_table(c.s);
   if (!chunk_blocks_ok(p, trow, rf0, r_hi, &ctl.flag)) return;
   const TileList list = tiles_seen(p, rf0, r_hi);
-  const int n_list = __shfl_sync(FULL_MASK, list.count(), 0);
-  // the tiles of the list that query tile q needs: [0, a) and [f, e)
+  // this CTA's run of the list: tiles first .. first + n_list - 1
+  const int first = __shfl_sync(FULL_MASK, list.count() * rank / splits, 0);
+  const int n_list = __shfl_sync(FULL_MASK, list.count() * (rank + 1) / splits - first, 0);
+  // the tiles of the run that query tile q needs: [0, a) and [f, e)
   struct Range {
     int a, f, e;
     __device__ bool has(int i) const { return i < a || (i >= f && i < e); }
@@ -105,8 +114,10 @@ __global__ void __launch_bounds__(PT, 1)
     r.a = rl < 0 ? 0 : min(list.a, rl / TROWS + 1);
     r.f = p.window ? list.a + max(0, max(0, rf - p.window + 1) / TROWS - list.b) : 0;
     r.e = rl < 0 ? 0 : list.a + max(0, rl / TROWS + 1 - list.b);
-    return Range{__shfl_sync(FULL_MASK, r.a, 0), __shfl_sync(FULL_MASK, r.f, 0), __shfl_sync(FULL_MASK, r.e, 0)};
+    return Range{__shfl_sync(FULL_MASK, r.a - first, 0), __shfl_sync(FULL_MASK, r.f - first, 0),
+                 __shfl_sync(FULL_MASK, r.e - first, 0)};
   };
+  auto tile_row = [&](int i) { return list.at(first + i) * TROWS; };
 
   if (t == 0) {
     for (int i = 0; i < L::NST; ++i) {
@@ -133,15 +144,17 @@ __global__ void __launch_bounds__(PT, 1)
   auto o_col = [&](int q) { return tm + 256 + q * 128; };
   const uint32_t qa = smem_addr(smem), ring = qa + L::RING;
   bool ok = true;
+  float m = NEG_INF, l = 0.f;  // (weights' threads: running maximum and sum; steps done)
+  int n = 0;
 
   if (w == 0) {
     // ---- copies: K and V tiles take the ring's stages in turn ----
     int cnt = 0;
-    int blk = n_list ? tile_block<D>(p, box_rows, trow, list.at(0) * TROWS, c.n, lane) : 0, blk_next = 0;
+    int blk = n_list ? tile_block<D>(p, box_rows, trow, tile_row(0), c.n, lane) : 0, blk_next = 0;
     for (; cnt < 2 * n_list && ok; ++cnt) {
-      const int st = cnt % L::NST, k0 = list.at(cnt >> 1) * TROWS;
+      const int st = cnt % L::NST, k0 = tile_row(cnt >> 1);
       if (!(cnt & 1) && cnt + 2 < 2 * n_list)  // (on its way while this tile waits for its stage)
-        blk_next = tile_block<D>(p, box_rows, trow, list.at((cnt >> 1) + 1) * TROWS, c.n, lane);
+        blk_next = tile_block<D>(p, box_rows, trow, tile_row((cnt >> 1) + 1), c.n, lane);
       if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
       if (!ok) break;
       const bool is_v = cnt & 1;
@@ -186,7 +199,7 @@ __global__ void __launch_bounds__(PT, 1)
         }
         umma_commit(&ctl.s_full[q][b]);
       };
-      uint32_t n = 0;  // tiles done
+      uint32_t done = 0;  // tiles
       ok = mbar_wait_bounded(&ctl.q_ready[q], 0);
       if (n_list > 0 && ok) {
         ok = mbar_wait_bounded(&ctl.full[0], 0);
@@ -206,18 +219,22 @@ __global__ void __launch_bounds__(PT, 1)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           if (now) {
-            ok = ok && mbar_wait_bounded(&ctl.p_ready[q][b], n & 1);
+            ok = ok && mbar_wait_bounded(&ctl.p_ready[q][b], done & 1);
             tc_fence_after();
             // P's rows 16 j .. 16 j + 15 of the step sit at columns 32 (j / 2) + 8 (j % 2) of its buffer
             const uint64_t ds = dv + sv * STAGE + b * (STEP * 8);
-            umma_ts(to, s_col(q, b), ds, IPV, n > 0 || b > 0);
+            umma_ts(to, s_col(q, b), ds, IPV, done > 0 || b > 0);
 #pragma unroll
             for (int j = 1; j < STEP / 16; ++j) umma_ts(to, s_col(q, b) + (j >> 1) * 32 + (j & 1) * 8, ds + j * 128, IPV, true);
+            if constexpr (FEW_CTAS) {  // the pair's second half, 16 columns on
+#pragma unroll
+              for (int j = 0; j < STEP / 16; ++j) umma_ts(to, s_col(q, b) + 16 + (j >> 1) * 32 + (j & 1) * 8, ds + j * 128, IPV, true);
+            }
             umma_commit(&ctl.o_ready[q][b]);
           }
           if (next) issue_s(sk, b);
         }
-        n += now;
+        done += now;
         umma_commit(&ctl.empty[sv]);
         if (more) umma_commit(&ctl.empty[sk]);
       }
@@ -237,10 +254,8 @@ __global__ void __launch_bounds__(PT, 1)
     const int r = rf + u / G;
     const int pair = 1 + q * 4 + (w & 3);  // named barrier of the two warps of 32 rows
     const float sl = p.scale * LOG2E;
-    float m = NEG_INF, l = 0.f;
     const Range need = range_of(q);
-    int n = 0;  // steps done
-    // The products of the steps before n are complete. (Those before n - 1 are: S of
+    // n: steps done. The products of the steps before n are complete. (Those before n - 1 are: S of
     // step n was issued after them.)
     auto wait_products = [&] {
       if (n > 0 && ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.o_ready[q][(n - 1) & 1], ((n - 1) >> 1) & 1));
@@ -257,7 +272,7 @@ __global__ void __launch_bounds__(PT, 1)
       uint32_t x[32];
       tmem_ld32(ts, x);
       tmem_wait_ld();
-      const int k0 = list.at(step >> 1) * TROWS + b * STEP;
+      const int k0 = tile_row(step >> 1) + b * STEP;
       const bool inner = k0 + STEP - 1 <= rf && (p.window == 0 || k0 > rl - p.window || k0 + STEP <= p.n_sink);
       if (!inner) {
         const uint32_t bits = seen_bits(p, r, k0, half);
@@ -308,11 +323,29 @@ __global__ void __launch_bounds__(PT, 1)
         e3 = fast_exp2(e3);
         add2(l0, l1, e0, e1);
         add2(l2, l3, e2, e3);
-        x[k] = pack_bf16(e0, e1);
-        x[k + 1] = pack_bf16(e2, e3);
+        const uint32_t p0 = pack_bf16(e0, e1), p1 = pack_bf16(e2, e3);
+        if constexpr (FEW_CTAS) {  // and what the rounding left
+          x[2 * k + 2] = pack_bf16(e2 - bf16_lo(p1), e3 - bf16_hi(p1));
+          x[2 * k] = pack_bf16(e0 - bf16_lo(p0), e1 - bf16_hi(p0));
+          x[2 * k + 1] = p0;
+          x[2 * k + 3] = p1;
+        } else {
+          x[k] = p0;
+          x[k + 1] = p1;
+        }
       }
       l += (l0 + l1) + (l2 + l3);
-      tmem_st16(ts, x);
+      if constexpr (FEW_CTAS) {
+        uint32_t y[32];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          y[k] = x[2 * k + 1];
+          y[16 + k] = x[2 * k];
+        }
+        tmem_st32(ts, y);
+      } else {
+        tmem_st16(ts, x);
+      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -326,7 +359,7 @@ __global__ void __launch_bounds__(PT, 1)
     l = half ? l_half + l : l + l_half;
     if (!ok) {
       if (lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
-    } else {
+    } else if (!FEW_CTAS) {
       const float inv = l != 0.f ? 1.f / l : 0.f;
       const int64_t head = (static_cast<int64_t>(c.seq) * p.n_q + tok0 + q * tpt + u / G) * (p.n_kv_heads * G) + c.h * G + u % G;
       uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + head * D + half * (D / 2));
@@ -355,8 +388,66 @@ __global__ void __launch_bounds__(PT, 1)
     }
   }
   tc_fence_before();
-  __syncthreads();
+  __syncthreads();  // (nothing uses the tiles in shared memory any more)
   tc_fence_after();
+  if constexpr (FEW_CTAS) {
+    // ---- join: every CTA's sums go to its shared memory, and each joins its share of rows ----
+    constexpr int RS = D + 4;  // floats of a row (16-byte stores of neighbouring rows in other banks)
+    static_assert(2 * TROWS * RS * 4 <= L::CTRL, "the rows' sums");
+    float* so = reinterpret_cast<float*>(smem);
+    float* sm = &ctl.mx[0][0][0][0];  // m and l of 256 rows
+    if (w >= 4 && (w < 12 || nq == 2)) {
+      const int q = (w - 4) >> 3, half = ((w - 4) >> 2) & 1, u = t & 127, row = q * TROWS + u;
+      const uint32_t to = o_col(q) + half * (D / 2) + (static_cast<uint32_t>((w & 3) * 32) << 16);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t o[16];
+        if (n > 0) {
+          tmem_ld16(to + k * 16, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<uint4*>(so + row * RS + half * (D / 2) + k * 16 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      }
+      if (half == 0) {
+        sm[row] = m;
+        sm[256 + row] = ok ? l : -1.f;
+      }
+    }
+    cluster_sync(splits);
+    const int n_rows = 2 * TROWS / splits;
+    for (int i = t; i < n_rows * (D / 4); i += PT) {
+      const int row = rank * n_rows + i / (D / 4), e = i % (D / 4) * 4, q = row >> 7, u = row & 127;
+      if (u >= (q ? toks1 : toks0) * G) continue;
+      float mj = NEG_INF;
+      for (int k = 0; k < splits; ++k) mj = fmaxf(mj, cluster_ld(sm + row, k, splits));
+      const float mu = mj == NEG_INF ? 0.f : mj;
+      float lj = 0.f;
+      bool skip = false;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < splits; ++k) {
+        const float a = fast_exp2(cluster_ld(sm + row, k, splits) - mu), lk = cluster_ld(sm + 256 + row, k, splits);
+        const float4 x = cluster_ld4(reinterpret_cast<const float4*>(so + row * RS + e), k);
+        skip |= lk < 0.f;
+        lj = fmaf(lk, a, lj);
+        o.x = fmaf(x.x, a, o.x);
+        o.y = fmaf(x.y, a, o.y);
+        o.z = fmaf(x.z, a, o.z);
+        o.w = fmaf(x.w, a, o.w);
+      }
+      if (skip) continue;
+      const float inv = lj != 0.f ? 1.f / lj : 0.f;
+      const int64_t head = (static_cast<int64_t>(c.seq) * p.n_q + tok0 + q * tpt + u / G) * (p.n_kv_heads * G) + c.h * G + u % G;
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + head * D + e) =
+          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+      if (p.lse && e == 0) p.lse[head] = lj != 0.f ? LN2 * (mj + log2f(lj)) : NEG_INF;
+    }
+    cluster_sync(splits);  // a CTA's shared memory stays until the others have read it
+  }
   if (w == 1) tmem_dealloc(tm, 512);
 }
 
@@ -366,15 +457,33 @@ cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
   const Encode encode = tensor_map_encode();
   const int box_rows = encode ? encode_rows(&kmap, p.k, p, D, encode) : 0;
   if (!box_rows || !encode_rows(&vmap, p.v, p, D, encode)) return cudaErrorInvalidValue;
-  auto kern = prefill_tc_kernel<D>;
+  
+  const int tokens = 2 * (TROWS / p.group), n_tiles = (p.n_q + tokens - 1) / tokens;
+  const int64_t units = static_cast<int64_t>(p.n_seq) * p.n_kv_heads * n_tiles;
+  if (units > 0x7fffffff) return cudaErrorInvalidValue;
+  // CTAs per pair of query tiles: as many as the SMs have room for, with two tiles of rows each at least
+  int64_t rows = p.n_cap;
+  if (p.window) rows = min(rows, static_cast<int64_t>(p.window) + tokens + p.n_sink);
+  const bool few = units * 2 <= SMS;
+  int splits = 1;
+  while (few && splits < 8 && units * splits * 2 <= SMS && rows >= 2 * splits * 2 * TROWS) splits *= 2;
+  auto kern = few ? prefill_tc_kernel<D, true> : prefill_tc_kernel<D, false>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D>::BYTES);
   if (e != cudaSuccess) return e;
-  const int tokens = 2 * (TROWS / p.group), n_tiles = (p.n_q + tokens - 1) / tokens;
-  const int64_t ctas = static_cast<int64_t>(p.n_seq) * p.n_kv_heads * n_tiles;
-  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  kern<<<static_cast<unsigned>(ctas), PT, TcSmem<D>::BYTES, st>>>(p, kmap, vmap, box_rows, n_tiles);
-  note_launch();
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * splits));
+  cfg.blockDim = dim3(PT);
+  cfg.dynamicSmemBytes = TcSmem<D>::BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(splits);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = splits > 1;
+  const cudaError_t r = cudaLaunchKernelEx(&cfg, kern, p, kmap, vmap, box_rows, n_tiles, splits);
+  if (r == cudaSuccess) note_launch();
+  return r;
 }
 
 // ---------------------------------------------------------------------------
