@@ -93,7 +93,8 @@ __device__ __forceinline__ float2 cluster_ld2(const float2* p, int u, int ns) {
   const float* f = reinterpret_cast<const float*>(p);
   return make_float2(cluster_ld(f, u, ns), cluster_ld(f + 1, u, ns));
 }
-__device__ __forceinline__ float4 cluster_ld4(const float4* p, int u) {
+__device__ __forceinline__ float4 cluster_ld4(const float4* p, int u, int ns) {
+  if (ns == 1) return *p;
   float4 x;
   asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
                : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(smem_addr(p)), "r"(u) : "memory");

@@ -47,15 +47,16 @@ namespace {
 // ---------------------------------------------------------------------------
 // bf16 rows
 // ---------------------------------------------------------------------------
-constexpr int PT = 640;      // copy warp, two MMA warps, an idle one, four warpgroups
 constexpr int STEP = 64;     // cached rows of a step
 constexpr float RAISE = 8.f;
 
-template <int D>
+template <int D, int NQ>
 struct TcSmem {
   static constexpr int TILE = D / 64 * TCOL;
-  static constexpr int NST = D == 128 ? 4 : 8;
-  static constexpr int RING = 2 * TILE;  // after the two query tiles
+  static constexpr int THREADS = 128 + NQ * 256;  // copy warp, two MMA warps, an idle one, two warpgroups per query tile
+  static constexpr int NST = D == 128 ? 4 : 5;
+  static constexpr int RING = NQ * TILE;  // after the query tiles
+  static constexpr int TMEM = NQ * 256;   // columns: per query tile 2 x 64 of S/P and up to 128 of O
   static constexpr int CTRL = RING + NST * TILE;
   static constexpr int BYTES = CTRL + 4608;
   static_assert(BYTES <= 227 * 1024, "shared memory");
@@ -67,16 +68,66 @@ struct TcCtl {
   uint64_t s_full[2][2], p_ready[2][2], o_ready[2][2];  // [query tile][half of a tile of rows]: S complete; P written; its product complete
   uint64_t v_fix;                                       // the last tile of V has landed, before its tail is cleared
   uint32_t tmem;
-  int flag;
+  int flag;                                             // a bad table entry
   float mx[2][2][2][TROWS];                             // maxima: [step parity][query tile][half][row]
 };
 static_assert(sizeof(TcCtl) <= 4608, "control block");
 
-template <int D, bool FEW_CTAS>
-__global__ void __launch_bounds__(PT, 1)
+__device__ __forceinline__ float max_of(const uint32_t (&x)[32]) {
+  float m[4];  // (four chains)
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    m[k] = __uint_as_float(x[k]);
+#pragma unroll
+    for (int e = 4; e < 28; e += 8) m[k] = max3(m[k], __uint_as_float(x[e + k]), __uint_as_float(x[e + 4 + k]));
+    m[k] = fmaxf(m[k], __uint_as_float(x[28 + k]));
+  }
+  return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+}
+// N columns of this thread's row of O, times a.
+template <int N>
+__device__ __forceinline__ void scale_o(uint32_t to, float a) {
+#pragma unroll
+  for (int k = 0; k < N / 16; ++k) {
+    uint32_t o[16];
+    tmem_ld16(to + k * 16, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+    tmem_st16(to + k * 16, o);
+  }
+}
+// Weights 2^(x sl - mu) of 32 columns, rounded to bf16 (hi), with PAIR also what the
+// rounding left (lo); returns their fp32 sum.
+template <bool PAIR>
+__device__ __forceinline__ float weights_of(const uint32_t (&x)[32], float sl, float mu, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
+  float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; k += 2) {
+    float e0, e1, e2, e3;
+    fma2(e0, e1, __uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), sl, -mu);
+    fma2(e2, e3, __uint_as_float(x[2 * k + 2]), __uint_as_float(x[2 * k + 3]), sl, -mu);
+    e0 = fast_exp2(e0);
+    e1 = fast_exp2(e1);
+    e2 = fast_exp2(e2);
+    e3 = fast_exp2(e3);
+    add2(l0, l1, e0, e1);
+    add2(l2, l3, e2, e3);
+    hi[k] = pack_bf16(e0, e1);
+    hi[k + 1] = pack_bf16(e2, e3);
+    if constexpr (PAIR) {
+      lo[k] = pack_bf16(e0 - bf16_lo(hi[k]), e1 - bf16_hi(hi[k]));
+      lo[k + 1] = pack_bf16(e2 - bf16_lo(hi[k + 1]), e3 - bf16_hi(hi[k + 1]));
+    }
+  }
+  return (l0 + l1) + (l2 + l3);
+}
+
+template <int D, int NQ, bool FEW_CTAS>
+__global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
     prefill_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, int box_rows, int n_tiles, int cluster) {
-  using L = TcSmem<D>;
+  using L = TcSmem<D, NQ>;
   const int splits = FEW_CTAS ? cluster : 1;
   extern __shared__ __align__(1024) unsigned char smem[];  // (the swizzle goes by address)
   TcCtl& ctl = *reinterpret_cast<TcCtl*>(smem + L::CTRL);
@@ -90,15 +141,14 @@ __global__ void __launch_bounds__(PT, 1)
   Chunk c;
   if (!chunk_of(p, ls, c)) return;  // (all returns here are a whole cluster's)
   const int tpt = TROWS / G;  // tokens per query tile
-  const int tok0 = tile * 2 * tpt;
+  const int tok0 = tile * NQ * tpt;
   if (tok0 >= c.n_new) return;
-  const int toks0 = min(tpt, c.n_new - tok0), toks1 = min(tpt, c.n_new - tok0 - toks0);
+  const int toks0 = min(tpt, c.n_new - tok0), toks1 = NQ == 2 ? min(tpt, c.n_new - tok0 - toks0) : 0;
   const int nq = toks1 > 0 ? 2 : 1;
   const int rf0 = c.r0 + tok0, rl0 = rf0 + toks0 - 1;
   const int rf1 = rl0 + 1, rl1 = rl0 + toks1;  // (empty when nq is 1)
   const int r_hi = rl1;
   const int32_t* trow = p.rows.seq_table(c.s);
-  if (!chunk_blocks_ok(p, trow, rf0, r_hi, &ctl.flag)) return;
   const TileList list = tiles_seen(p, rf0, r_hi);
   // this CTA's run of the list: tiles first .. first + n_list - 1
   const int first = __shfl_sync(FULL_MASK, list.count() * rank / splits, 0);
@@ -133,15 +183,16 @@ __global__ void __launch_bounds__(PT, 1)
       }
     }
     mbar_init(&ctl.v_fix, 1);
+    ctl.flag = 0;
     mbar_init_fence();
   }
-  if (w == 1) tmem_alloc(&ctl.tmem, 512);
+  if (w == 1) tmem_alloc(&ctl.tmem, L::TMEM);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = __shfl_sync(FULL_MASK, ctl.tmem, 0);
   auto s_col = [&](int q, int b) { return tm + (q * 2 + b) * STEP; };
-  auto o_col = [&](int q) { return tm + 256 + q * 128; };
+  auto o_col = [&](int q) { return tm + (NQ + q) * 128; };
   const uint32_t qa = smem_addr(smem), ring = qa + L::RING;
   bool ok = true;
   float m = NEG_INF, l = 0.f;  // (weights' threads: running maximum and sum; steps done)
@@ -149,17 +200,29 @@ __global__ void __launch_bounds__(PT, 1)
 
   if (w == 0) {
     // ---- copies: K and V tiles take the ring's stages in turn ----
+    // (a pool's tables are checked as they are read: with a bad entry for rows that some
+    // query sees, the query tiles are left out)
     int cnt = 0;
-    int blk = n_list ? tile_block<D>(p, box_rows, trow, tile_row(0), c.n, lane) : 0, blk_next = 0;
+    bool blocks_ok = true;
+    const int see0 = visible_rows(max(rf0, 0), p.n_sink, p.window).w0, see1 = visible_rows(max(r_hi, 0), p.n_sink, p.window).s1;
+    auto block_of = [&](int k0) {
+      if (!trow) return 0;
+      const int blk = tile_block<D>(p, box_rows, trow, k0, c.n, lane), row = k0 + lane / (D / 64) * box_rows;
+      if (blk == p.rows.num_blocks && row < k0 + TROWS && row <= r_hi && (row < see1 || row + box_rows > see0)) blocks_ok = false;
+      return blk;
+    };
+    int blk = n_list ? block_of(tile_row(0)) : 0, blk_next = 0;
     for (; cnt < 2 * n_list && ok; ++cnt) {
       const int st = cnt % L::NST, k0 = tile_row(cnt >> 1);
       if (!(cnt & 1) && cnt + 2 < 2 * n_list)  // (on its way while this tile waits for its stage)
-        blk_next = tile_block<D>(p, box_rows, trow, tile_row((cnt >> 1) + 1), c.n, lane);
+        blk_next = block_of(tile_row((cnt >> 1) + 1));
       if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
       if (!ok) break;
       const bool is_v = cnt & 1;
       const bool fix = is_v && k0 + TROWS - 1 > r_hi;
       uint64_t* bar = fix ? &ctl.v_fix : &ctl.full[st];
+      if (!blocks_ok) ctl.flag = 1;
+      __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(bar, L::TILE);
       __syncwarp();
       load_tile<D>(ring + st * L::TILE, is_v ? &vmap : &kmap, p, box_rows, trow != nullptr, blk, c.seq, c.h, k0, bar, lane);
@@ -176,6 +239,7 @@ __global__ void __launch_bounds__(PT, 1)
         if (lane == 0) mbar_arrive(&ctl.full[st]);
       }
     }
+    if (!blocks_ok) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
     if (!ok && lane == 0) {
       set_status(p.dev_status, TRI_DEV_TIMEOUT);
       // let the copies in flight finish before shared memory is given up
@@ -280,15 +344,7 @@ __global__ void __launch_bounds__(PT, 1)
         for (int e = 0; e < 32; ++e)
           if (!(bits & (1u << e))) x[e] = 0xff800000u;  // -inf
       }
-      float mxs[4];  // (four chains)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        mxs[k] = __uint_as_float(x[k]);
-#pragma unroll
-        for (int e = 4; e < 28; e += 8) mxs[k] = max3(mxs[k], __uint_as_float(x[e + k]), __uint_as_float(x[e + 4 + k]));
-        mxs[k] = fmaxf(mxs[k], __uint_as_float(x[28 + k]));
-      }
-      float mx = fmaxf(max3(mxs[0], mxs[1], mxs[2]), mxs[3]);
+      float mx = max_of(x);
       ctl.mx[n & 1][q][half][u] = mx;
       asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
       mx = fmaxf(mx, ctl.mx[n & 1][q][half ^ 1][u]) * sl;
@@ -300,52 +356,13 @@ __global__ void __launch_bounds__(PT, 1)
         m = mn;
         l *= a;
         wait_products();
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          uint32_t o[16];
-          tmem_ld16(to + k * 16, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-          tmem_st16(to + k * 16, o);
-        }
+        scale_o<D / 2>(to, a);
       }
       const float mu = m == NEG_INF ? 0.f : m;
-      float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-#pragma unroll
-      for (int k = 0; k < 16; k += 2) {
-        float e0, e1, e2, e3;
-        fma2(e0, e1, __uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), sl, -mu);
-        fma2(e2, e3, __uint_as_float(x[2 * k + 2]), __uint_as_float(x[2 * k + 3]), sl, -mu);
-        e0 = fast_exp2(e0);
-        e1 = fast_exp2(e1);
-        e2 = fast_exp2(e2);
-        e3 = fast_exp2(e3);
-        add2(l0, l1, e0, e1);
-        add2(l2, l3, e2, e3);
-        const uint32_t p0 = pack_bf16(e0, e1), p1 = pack_bf16(e2, e3);
-        if constexpr (FEW_CTAS) {  // and what the rounding left
-          x[2 * k + 2] = pack_bf16(e2 - bf16_lo(p1), e3 - bf16_hi(p1));
-          x[2 * k] = pack_bf16(e0 - bf16_lo(p0), e1 - bf16_hi(p0));
-          x[2 * k + 1] = p0;
-          x[2 * k + 3] = p1;
-        } else {
-          x[k] = p0;
-          x[k + 1] = p1;
-        }
-      }
-      l += (l0 + l1) + (l2 + l3);
-      if constexpr (FEW_CTAS) {
-        uint32_t y[32];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          y[k] = x[2 * k + 1];
-          y[16 + k] = x[2 * k];
-        }
-        tmem_st32(ts, y);
-      } else {
-        tmem_st16(ts, x);
-      }
+      uint32_t hi[16], lo[16];
+      l += weights_of<FEW_CTAS>(x, sl, mu, hi, lo);
+      tmem_st16(ts, hi);
+      if constexpr (FEW_CTAS) tmem_st16(ts + 16, lo);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -359,7 +376,7 @@ __global__ void __launch_bounds__(PT, 1)
     l = half ? l_half + l : l + l_half;
     if (!ok) {
       if (lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
-    } else if (!FEW_CTAS) {
+    } else if (!FEW_CTAS && !ctl.flag) {
       const float inv = l != 0.f ? 1.f / l : 0.f;
       const int64_t head = (static_cast<int64_t>(c.seq) * p.n_q + tok0 + q * tpt + u / G) * (p.n_kv_heads * G) + c.h * G + u % G;
       uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + head * D + half * (D / 2));
@@ -393,7 +410,7 @@ __global__ void __launch_bounds__(PT, 1)
   if constexpr (FEW_CTAS) {
     // ---- join: every CTA's sums go to its shared memory, and each joins its share of rows ----
     constexpr int RS = D + 4;  // floats of a row (16-byte stores of neighbouring rows in other banks)
-    static_assert(2 * TROWS * RS * 4 <= L::CTRL, "the rows' sums");
+    static_assert(NQ * TROWS * RS * 4 <= L::CTRL, "the rows' sums");
     float* so = reinterpret_cast<float*>(smem);
     float* sm = &ctl.mx[0][0][0][0];  // m and l of 256 rows
     if (w >= 4 && (w < 12 || nq == 2)) {
@@ -415,12 +432,12 @@ __global__ void __launch_bounds__(PT, 1)
       }
       if (half == 0) {
         sm[row] = m;
-        sm[256 + row] = ok ? l : -1.f;
+        sm[256 + row] = ok && !ctl.flag ? l : -1.f;
       }
     }
     cluster_sync(splits);
-    const int n_rows = 2 * TROWS / splits;
-    for (int i = t; i < n_rows * (D / 4); i += PT) {
+    const int n_rows = NQ * TROWS / splits;
+    for (int i = t; i < n_rows * (D / 4); i += L::THREADS) {
       const int row = rank * n_rows + i / (D / 4), e = i % (D / 4) * 4, q = row >> 7, u = row & 127;
       if (u >= (q ? toks1 : toks0) * G) continue;
       float mj = NEG_INF;
@@ -431,7 +448,7 @@ __global__ void __launch_bounds__(PT, 1)
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int k = 0; k < splits; ++k) {
         const float a = fast_exp2(cluster_ld(sm + row, k, splits) - mu), lk = cluster_ld(sm + 256 + row, k, splits);
-        const float4 x = cluster_ld4(reinterpret_cast<const float4*>(so + row * RS + e), k);
+        const float4 x = cluster_ld4(reinterpret_cast<const float4*>(so + row * RS + e), k, splits);
         skip |= lk < 0.f;
         lj = fmaf(lk, a, lj);
         o.x = fmaf(x.x, a, o.x);
@@ -448,7 +465,7 @@ __global__ void __launch_bounds__(PT, 1)
     }
     cluster_sync(splits);  // a CTA's shared memory stays until the others have read it
   }
-  if (w == 1) tmem_dealloc(tm, 512);
+  if (w == 1) tmem_dealloc(tm, L::TMEM);
 }
 
 template <int D>
@@ -457,8 +474,11 @@ cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
   const Encode encode = tensor_map_encode();
   const int box_rows = encode ? encode_rows(&kmap, p.k, p, D, encode) : 0;
   if (!box_rows || !encode_rows(&vmap, p.v, p, D, encode)) return cudaErrorInvalidValue;
-  
-  const int tokens = 2 * (TROWS / p.group), n_tiles = (p.n_q + tokens - 1) / tokens;
+  // one or two query tiles per CTA: at d 64 two CTAs with a tile each fit an SM, and one's
+  // start and end hide behind the other's work (8 padded prompts of up to 4096 tokens, sinks
+  // and a window of 1000: 189 us, with two tiles per CTA 199)
+  constexpr int NQ = D == 128 ? 2 : 1;
+  const int tokens = NQ * (TROWS / p.group), n_tiles = (p.n_q + tokens - 1) / tokens;
   const int64_t units = static_cast<int64_t>(p.n_seq) * p.n_kv_heads * n_tiles;
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
   // CTAs per pair of query tiles: as many as the SMs have room for, with two tiles of rows each at least
@@ -467,13 +487,13 @@ cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
   const bool few = units * 2 <= SMS;
   int splits = 1;
   while (few && splits < 8 && units * splits * 2 <= SMS && rows >= 2 * splits * 2 * TROWS) splits *= 2;
-  auto kern = few ? prefill_tc_kernel<D, true> : prefill_tc_kernel<D, false>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D>::BYTES);
+  auto kern = few ? prefill_tc_kernel<D, NQ, true> : prefill_tc_kernel<D, NQ, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D, NQ>::BYTES);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(units * splits));
-  cfg.blockDim = dim3(PT);
-  cfg.dynamicSmemBytes = TcSmem<D>::BYTES;
+  cfg.blockDim = dim3(TcSmem<D, NQ>::THREADS);
+  cfg.dynamicSmemBytes = TcSmem<D, NQ>::BYTES;
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
