@@ -39,8 +39,8 @@
 //   carries 16 bits of them, at the cost of eight more MMAs that the memory
 //   traffic hides.
 //
-// fp32 rows (decode_rows_kernel): 8 lanes per row on the CUDA cores, fp32
-// throughout (a tensor-core product would drop the rows to 10 bits).
+// fp32 rows (decode_rows_kernel): the same rings, 8 lanes per row on the CUDA
+// cores, fp32 throughout (a tensor-core product would drop the rows to 10 bits).
 #include <cuda_runtime.h>
 
 #include "attn_common.cuh"
@@ -78,17 +78,17 @@ __device__ __forceinline__ bool slice_run(const AttnParams& p, int ls, Run& r) {
 constexpr int NW = 4;  // warps per CTA
 constexpr int MAX_CLUSTER = 16;  // (above 8 a kernel has to allow for it; a GPC of this GPU holds 16 such CTAs)
 
-template <int D>
+template <typename T, int D>
 struct TileGeo {
-  static constexpr int TK = 2048 / D;         // rows per tile: 4 KB of K and of V
-  static constexpr int ROW = D * 2;           // bytes
+  static constexpr int ROW = D * static_cast<int>(sizeof(T));  // bytes
+  static constexpr int TK = 4096 / ROW;       // rows per tile: 4 KB of K and of V
   static constexpr int CH = ROW / 16;         // 16-byte chunks per row
   static constexpr int RPI = 32 / CH;         // rows per copy instruction of a warp
   static constexpr int TILE = TK * ROW;       // bytes of one tensor's tile
   static constexpr int NST = 2;
   static constexpr int WARP_RING = NST * 2 * TILE;
   static constexpr int SMEM = NW * WARP_RING;
-  static constexpr int SUB = TK / 16;         // 16-row steps of a tile
+  static constexpr int RUN = TK < 16 ? TK : 16;  // rows of a tile that lie in one block of any pool
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
@@ -218,9 +218,66 @@ __device__ __forceinline__ void join_cluster(const AttnParams& p, const Run& r, 
   cluster_sync(ns);  // a CTA's shared memory stays until the others have read it
 }
 
+// The tiles that hold visible rows of a slice, [0, ta) and [tb, tn), and a run's
+// share of them: numbers u0 .. u1 - 1 of the list.
+template <typename T, int D>
+struct Tiles {
+  int ta, tb, u0, u1;
+  __device__ __forceinline__ Tiles(const AttnParams& p, const Run& r, int split) {
+    constexpr int TK = TileGeo<T, D>::TK;
+    const int tn = (r.n + TK - 1) / TK;
+    ta = (r.vis.s1 + TK - 1) / TK;
+    tb = max(ta, r.vis.w0 / TK);
+    const int64_t tiles = ta + tn - tb;
+    u0 = static_cast<int>(tiles * split / p.n_split);
+    u1 = static_cast<int>(tiles * (split + 1) / p.n_split);
+  }
+  __device__ __forceinline__ int row(int u) const { return (u < ta ? u : u - ta + tb) * TileGeo<T, D>::TK; }
+};
+
+// Copies of tile u of a slice's list to `dst` (K, then V) by a warp.
+template <typename T, int D, bool PAGED>
+__device__ __forceinline__ void fetch_tile(const AttnParams& p, const Run& r, const Tiles<T, D>& tl, int u, uint32_t dst, int lane,
+                                           bool& blocks_ok) {
+  using G = TileGeo<T, D>;
+  const int crow = lane / G::CH, cch = lane % G::CH, r0 = tl.row(u);
+  const int64_t base = p.rows.slice_base(r.s);
+#pragma unroll
+  for (int s = 0; s < G::TK / G::RUN; ++s) {
+    const int rs = r0 + G::RUN * s;
+    int64_t off;
+    bool in = rs < r.n;
+    if (PAGED) {
+      int blk = 0;
+      if (in) {
+        blk = __ldg(p.rows.seq_table(r.s) + (rs >> p.rows.block_shift));
+        if (blk < 0 || blk >= p.rows.num_blocks) {
+          // rows that nobody sees may have no block any more
+          if (rs < r.vis.s1 || rs + G::RUN - 1 >= r.vis.w0) blocks_ok = false;
+          blk = 0;
+          in = false;
+        }
+      }
+      off = base + blk * p.rows.block_bytes + static_cast<int64_t>(rs & (p.rows.block_size - 1)) * G::ROW;
+    } else {
+      off = base + static_cast<int64_t>(rs) * G::ROW;
+    }
+#pragma unroll
+    for (int i = 0; i < G::RUN / G::RPI; ++i) {
+      const int rr = i * G::RPI + crow, j = rs + rr;
+      const bool live = in && j < r.n && (j < r.vis.s1 || j >= r.vis.w0);
+      const int64_t o = live ? off + rr * G::ROW + cch * 16 : 0;
+      const uint32_t d = (G::RUN * s + rr) * G::ROW + ((cch ^ (rr & 7)) << 4);
+      cp_async16(dst + d, static_cast<const char*>(p.k) + o, live);
+      cp_async16(dst + G::TILE + d, static_cast<const char*>(p.v) + o, live);
+    }
+  }
+}
+
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_constant__ AttnParams p) {
-  using G = TileGeo<D>;
+  using T = __nv_bfloat16;
+  using G = TileGeo<T, D>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float sm_m[NW][8], sm_l[NW][8];
   __shared__ float2 run_ml[MAX_GROUP];
@@ -236,12 +293,7 @@ __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_cons
   }
   if (t == 0) bad = 0;
 
-  // the tiles that hold visible rows: [0, ta) and [tb, tn)
-  const int ta = (r.vis.s1 + G::TK - 1) / G::TK, tn = (r.n + G::TK - 1) / G::TK;
-  const int tb = max(ta, r.vis.w0 / G::TK);
-  const int tiles = ta + tn - tb;
-  const int u0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.n_split);
-  const int u1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.n_split);
+  const Tiles<T, D> tl(p, r, split);
 
   // the heads' B fragments
   uint32_t qf[D / 16][2];
@@ -256,47 +308,8 @@ __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_cons
   }
 
   const uint32_t ring = smem_addr(smem) + w * G::WARP_RING;
-  const int64_t base = p.rows.slice_base(r.s);
-  const int32_t* trow = p.rows.seq_table(r.s);
-  const int crow = lane / G::CH, cch = lane % G::CH;
   bool blocks_ok = true;
-
-  auto row_of_tile = [&](int u) { return (u < ta ? u : u - ta + tb) * G::TK; };
-  // copy of tile u (of the slice's list) into stage st
-  auto fetch = [&](int u, int st) {
-    const int r0 = row_of_tile(u);
-    const uint32_t dk = ring + st * 2 * G::TILE, dv = dk + G::TILE;
-#pragma unroll
-    for (int s = 0; s < G::SUB; ++s) {
-      const int rs = r0 + 16 * s;
-      int64_t off;
-      bool in = rs < r.n;
-      if (PAGED) {
-        int blk = 0;
-        if (in) {
-          blk = __ldg(trow + (rs >> p.rows.block_shift));
-          if (blk < 0 || blk >= p.rows.num_blocks) {
-            // 16 rows that nobody sees may have no block any more
-            if (rs < r.vis.s1 || rs + 15 >= r.vis.w0) blocks_ok = false;
-            blk = 0;
-            in = false;
-          }
-        }
-        off = base + blk * p.rows.block_bytes + static_cast<int64_t>(rs & (p.rows.block_size - 1)) * G::ROW;
-      } else {
-        off = base + static_cast<int64_t>(rs) * G::ROW;
-      }
-#pragma unroll
-      for (int i = 0; i < 16 / G::RPI; ++i) {
-        const int rr = i * G::RPI + crow, j = rs + rr;
-        const bool live = in && j < r.n && (j < r.vis.s1 || j >= r.vis.w0);
-        const int64_t o = live ? off + rr * G::ROW + cch * 16 : 0;
-        const uint32_t d = (16 * s + rr) * G::ROW + ((cch ^ (rr & 7)) << 4);
-        cp_async16(dk + d, static_cast<const char*>(p.k) + o, live);
-        cp_async16(dv + d, static_cast<const char*>(p.v) + o, live);
-      }
-    }
-  };
+  auto fetch = [&](int u, int st) { fetch_tile<T, D, PAGED>(p, r, tl, u, ring + st * 2 * G::TILE, lane, blocks_ok); };
 
   float o[D / 16][4];
 #pragma unroll
@@ -309,23 +322,23 @@ __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_cons
 
 #pragma unroll
   for (int i = 0; i < G::NST - 1; ++i) {
-    if (u0 + w + i * NW < u1) fetch(u0 + w + i * NW, i);
+    if (tl.u0 + w + i * NW < tl.u1) fetch(tl.u0 + w + i * NW, i);
     cp_async_commit();
   }
   int st = 0;
-  for (int u = u0 + w; u < u1; u += NW) {
+  for (int u = tl.u0 + w; u < tl.u1; u += NW) {
     {
       const int nx = u + (G::NST - 1) * NW, ns = st == 0 ? G::NST - 1 : st - 1;
-      if (nx < u1) fetch(nx, ns);
+      if (nx < tl.u1) fetch(nx, ns);
       cp_async_commit();
     }
     cp_async_wait<G::NST - 1>();
     __syncwarp();
-    const int r0 = row_of_tile(u);
+    const int r0 = tl.row(u);
     const bool inner = r0 + G::TK <= r.n && (r0 >= r.vis.w0 || r0 + G::TK <= r.vis.s1);
     const uint32_t tk = ring + st * 2 * G::TILE, tv = tk + G::TILE;
 #pragma unroll
-    for (int s = 0; s < G::SUB; ++s) {
+    for (int s = 0; s < G::TK / 16; ++s) {
       float x[4] = {0.f, 0.f, 0.f, 0.f};
       {
         const int row = 16 * s + (lane & 15);
@@ -439,8 +452,8 @@ __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_cons
     }
   }
   if (p.join)
-    join_cluster<__nv_bfloat16, D>(p, r, ls, split, tot, run_ml, u0 * G::TK, u1 * G::TK, [&](int i) {
-      const int j = row_of_tile(i / G::TK) + i % G::TK;
+    join_cluster<__nv_bfloat16, D>(p, r, ls, split, tot, run_ml, tl.u0 * G::TK, tl.u1 * G::TK, [&](int i) {
+      const int j = tl.row(i / G::TK) + i % G::TK;
       return j < r.n && (j < r.vis.s1 || j >= r.vis.w0) ? j : -1;
     });
 }
@@ -452,17 +465,19 @@ constexpr int DT = NW * 32;  // threads per CTA
 constexpr int LPR = 8;    // lanes per row
 constexpr int GROUPS = DT / LPR;
 
-template <int D, int GP>
+template <int D, int GP, bool PAGED>
 __global__ void __launch_bounds__(DT) decode_rows_kernel(const __grid_constant__ AttnParams p) {
+  using T = float;
+  using Geo = TileGeo<T, D>;
   constexpr int E = 4;              // elements per 16-byte chunk
   constexpr int C = D / (E * LPR);  // chunks per lane
+  extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float sq[GP][D];
-  __shared__ float so[GROUPS][D];
   __shared__ float sm_m[GROUPS][GP], sm_l[GROUPS][GP];
-  __shared__ float tot[GP * D];
   __shared__ float2 run_ml[GP];
-  __shared__ int flag;
+  __shared__ int bad;
   const int ls = blockIdx.x / p.n_split, split = blockIdx.x % p.n_split, t = threadIdx.x, G = p.group;
+  const int w = t >> 5, lane = t & 31;
   pdl_launch();
   Run r;
   const int64_t pi = static_cast<int64_t>(blockIdx.x) * G;
@@ -470,15 +485,16 @@ __global__ void __launch_bounds__(DT) decode_rows_kernel(const __grid_constant__
     if (!p.join && t < G) p.part_ml[pi + t] = make_float2(NEG_INF, -1.f);
     return;  // (every run of the slice does)
   }
-  const int32_t* trow = p.rows.seq_table(r.s);
-  const int i0 = static_cast<int>(static_cast<int64_t>(r.count) * split / p.n_split);
-  int i1 = static_cast<int>(static_cast<int64_t>(r.count) * (split + 1) / p.n_split);
-  const int shift = r.vis.w0 - r.vis.s1;
-  bool ok = p.rows.blocks_ok(trow, i0, min(i1, r.vis.s1), &flag);
-  ok = p.rows.blocks_ok(trow, max(i0, r.vis.s1) + shift, i1 + shift, &flag) && ok;
-  if (!ok) {
-    if (t == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
-    i1 = i0;  // nothing is read; the slice is skipped by the join
+  if (t == 0) bad = 0;
+  const Tiles<T, D> tl(p, r, split);
+  const uint32_t ring = smem_addr(smem) + w * Geo::WARP_RING;
+  const unsigned char* ring_p = smem + w * Geo::WARP_RING;
+  bool ok = true;
+  auto fetch = [&](int u, int st) { fetch_tile<T, D, PAGED>(p, r, tl, u, ring + st * 2 * Geo::TILE, lane, ok); };
+#pragma unroll
+  for (int i = 0; i < Geo::NST - 1; ++i) {
+    if (tl.u0 + w + i * NW < tl.u1) fetch(tl.u0 + w + i * NW, i);
+    cp_async_commit();
   }
   const float* q = static_cast<const float*>(p.q) + r.seq * p.q_seq + static_cast<int64_t>(r.h) * G * D;
   for (int i = t; i < GP * D; i += DT) {
@@ -487,6 +503,15 @@ __global__ void __launch_bounds__(DT) decode_rows_kernel(const __grid_constant__
   }
   __syncthreads();
   const int rg = t / LPR, lane8 = t % LPR;
+  // up to four heads' queries stay in registers (with more, they and o do not fit)
+  constexpr bool Q_REGS = GP <= 4;
+  float4 qr[Q_REGS ? GP : 1][C];
+  if constexpr (Q_REGS) {
+#pragma unroll
+    for (int g = 0; g < GP; ++g)
+#pragma unroll
+      for (int c = 0; c < C; ++c) qr[g][c] = *reinterpret_cast<const float4*>(&sq[g][(lane8 + LPR * c) * E]);
+  }
   float m[GP], l[GP], o[GP][C * E];
 #pragma unroll
   for (int g = 0; g < GP; ++g) {
@@ -495,51 +520,75 @@ __global__ void __launch_bounds__(DT) decode_rows_kernel(const __grid_constant__
 #pragma unroll
     for (int e = 0; e < C * E; ++e) o[g][e] = 0.f;
   }
-  const int64_t base = p.rows.slice_base(r.s);
   float* logits = p.logits ? p.logits + static_cast<int64_t>(ls) * p.n_cap * G : nullptr;
-  for (int i = i0 + rg; i - rg < i1; i += GROUPS) {
-    const bool live = i < i1;
-    const int j = i < r.vis.s1 ? i : i - r.vis.s1 + r.vis.w0;
-    const int64_t off = live ? p.rows.row(base, trow, j) : 0;
-    float x[GP];
-#pragma unroll
-    for (int g = 0; g < GP; ++g) x[g] = 0.f;
-    uint4 vw[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      uint4 kw = make_uint4(0, 0, 0, 0);
-      vw[c] = kw;
-      if (live) {
-        kw = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.k) + off) + lane8 + LPR * c);
-        vw[c] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.v) + off) + lane8 + LPR * c);
-      }
-      float kx[E];
-      widen(kw, kx);
-#pragma unroll
-      for (int g = 0; g < GP; ++g)
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[g] = fmaf(sq[g][(lane8 + LPR * c) * E + e], kx[e], x[g]);
+  int st = 0;
+  for (int u = tl.u0 + w; u < tl.u1; u += NW) {
+    {
+      const int nx = u + (Geo::NST - 1) * NW, ns = st == 0 ? Geo::NST - 1 : st - 1;
+      if (nx < tl.u1) fetch(nx, ns);
+      cp_async_commit();
     }
+    cp_async_wait<Geo::NST - 1>();
+    __syncwarp();
+    const int r0 = tl.row(u);
+#pragma unroll 1
+    for (int s = 0; s < Geo::TK; s += 32 / LPR) {
+      const int row = s + lane / LPR, j = r0 + row;
+      const bool live = j < r.n && (j < r.vis.s1 || j >= r.vis.w0);
+      const unsigned char* kp = ring_p + st * 2 * Geo::TILE + row * Geo::ROW;
+      float x[GP];
 #pragma unroll
-    for (int g = 0; g < GP; ++g) {
-#pragma unroll
-      for (int k = LPR / 2; k >= 1; k >>= 1) x[g] += __shfl_xor_sync(FULL_MASK, x[g], k);
-      if (!live) x[g] = NEG_INF;
-      if (logits && live && lane8 == g % LPR && g < G) logits[static_cast<int64_t>(j) * G + g] = x[g];
-      const float mn = fmaxf(m[g], x[g]);
-      const float mu = mn == NEG_INF ? 0.f : mn;
-      const float a = fast_exp2(m[g] - mu), e0 = fast_exp2(x[g] - mu);
-      m[g] = mn;
-      l[g] = fmaf(l[g], a, e0);
+      for (int g = 0; g < GP; ++g) x[g] = 0.f;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        float vx[E];
-        widen(vw[c], vx);
+        const float4 kx = *reinterpret_cast<const float4*>(kp + (((lane8 + LPR * c) ^ (row & 7)) << 4));
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[g][c * E + e] = fmaf(o[g][c * E + e], a, e0 * vx[e]);
+        for (int g = 0; g < GP; ++g) {
+          const float4 qx = Q_REGS ? qr[Q_REGS ? g : 0][c] : *reinterpret_cast<const float4*>(&sq[g][(lane8 + LPR * c) * E]);
+          x[g] = fmaf(qx.x, kx.x, x[g]);
+          x[g] = fmaf(qx.y, kx.y, x[g]);
+          x[g] = fmaf(qx.z, kx.z, x[g]);
+          x[g] = fmaf(qx.w, kx.w, x[g]);
+        }
+      }
+      float wgt[GP];
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+#pragma unroll
+        for (int k = LPR / 2; k >= 1; k >>= 1) x[g] += __shfl_xor_sync(FULL_MASK, x[g], k);
+        if (!live) x[g] = NEG_INF;
+        if (logits && live && lane8 == g % LPR && g < G) logits[static_cast<int64_t>(j) * G + g] = x[g];
+        if (x[g] > m[g]) {  // (the 8 lanes of a row agree)
+          const float a = fast_exp2(m[g] - x[g]);
+          m[g] = x[g];
+          l[g] *= a;
+#pragma unroll
+          for (int e = 0; e < C * E; ++e) o[g][e] *= a;
+        }
+        wgt[g] = fast_exp2(x[g] - (m[g] == NEG_INF ? 0.f : m[g]));
+        l[g] += wgt[g];
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const float4 vx = *reinterpret_cast<const float4*>(kp + Geo::TILE + (((lane8 + LPR * c) ^ (row & 7)) << 4));
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+          o[g][c * E] = fmaf(wgt[g], vx.x, o[g][c * E]);
+          o[g][c * E + 1] = fmaf(wgt[g], vx.y, o[g][c * E + 1]);
+          o[g][c * E + 2] = fmaf(wgt[g], vx.z, o[g][c * E + 2]);
+          o[g][c * E + 3] = fmaf(wgt[g], vx.w, o[g][c * E + 3]);
+        }
       }
     }
+    __syncwarp();  // the stage may be refilled
+    st = st + 1 == Geo::NST ? 0 : st + 1;
   }
+  cp_async_wait<0>();
+  if (PAGED && !ok) bad = 1;
+  __syncthreads();  // every ring is idle: the row groups' sums go there
+  float(*so)[D] = reinterpret_cast<float(*)[D]>(smem);
+  float* tot = reinterpret_cast<float*>(smem) + GROUPS * D;
+  if (PAGED && bad && t == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
   if (lane8 == 0) {
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
@@ -569,13 +618,16 @@ __global__ void __launch_bounds__(DT) decode_rows_kernel(const __grid_constant__
     if (t == 0) {
       float sum = 0.f;
       for (int u = 0; u < GROUPS; ++u) sum = fmaf(sm_l[u][g], fast_exp2(sm_m[u][g] - mu), sum);
-      const float2 x = make_float2(mx, ok ? sum : -1.f);
+      const float2 x = make_float2(mx, PAGED && bad ? -1.f : sum);
       if (p.join) run_ml[g] = x;
       else p.part_ml[pi + g] = x;
     }
   }
   if (p.join)
-    join_cluster<float, D>(p, r, ls, split, tot, run_ml, i0, i1, [&](int i) { return i < r.vis.s1 ? i : i + shift; });
+    join_cluster<float, D>(p, r, ls, split, tot, run_ml, tl.u0 * Geo::TK, tl.u1 * Geo::TK, [&](int i) {
+      const int j = tl.row(i / Geo::TK) + i % Geo::TK;
+      return j < r.n && (j < r.vis.s1 || j >= r.vis.w0) ? j : -1;
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -692,14 +744,19 @@ cudaError_t launch_runs(Kernel kern, size_t smem, const AttnParams& p, cudaStrea
 template <int D>
 cudaError_t launch_bf16(const AttnParams& p, int max_rows, cudaStream_t st) {
   const cudaError_t e = launch_runs(p.rows.table ? decode_tiles_kernel<D, true> : decode_tiles_kernel<D, false>,
-                                    TileGeo<D>::SMEM, p, st);
+                                    TileGeo<__nv_bfloat16, D>::SMEM, p, st);
   return e != cudaSuccess || p.join ? e : launch_join<__nv_bfloat16, D>(p, max_rows, st);
+}
+
+template <int D, int GP>
+cudaError_t launch_fp32_group(const AttnParams& p, cudaStream_t st) {
+  return launch_runs(p.rows.table ? decode_rows_kernel<D, GP, true> : decode_rows_kernel<D, GP, false>, TileGeo<float, D>::SMEM, p, st);
 }
 
 template <int D>
 cudaError_t launch_fp32(const AttnParams& p, int max_rows, cudaStream_t st) {
-  const cudaError_t e = launch_runs(p.group == 1 ? decode_rows_kernel<D, 1> : p.group == 2 ? decode_rows_kernel<D, 2>
-                                    : p.group <= 4 ? decode_rows_kernel<D, 4> : decode_rows_kernel<D, 8>, 0, p, st);
+  const cudaError_t e = p.group == 1 ? launch_fp32_group<D, 1>(p, st) : p.group == 2 ? launch_fp32_group<D, 2>(p, st)
+                      : p.group <= 4 ? launch_fp32_group<D, 4>(p, st) : launch_fp32_group<D, 8>(p, st);
   return e != cudaSuccess || p.join ? e : launch_join<float, D>(p, max_rows, st);
 }
 
@@ -718,15 +775,17 @@ int attn_decode_max_splits(int n_slices, int max_rows) {
 //    32 x 8192     82.4  45.6  29.2  25.4  33.0  35.2  28.0  27.6  31.7  34.0  42.7
 //   128 x 8192     95.9  80.5  95.5  88.3 103.2  85.2  83.2  86.3  88.8  94.0    -
 //   256 x 2048     45.4  56.2  52.2  57.2  97.9  47.7  50.6  54.1  58.3    -     -
+// and fp32, group 1:
+//    64 x 2048     50.2  30.6  25.2  31.8  38.0  28.8  26.9  27.6  30.7  36.5    -
+//   128 x 8192    194.8 152.8 185.6 160.2 171.5 161.5 153.8 156.2 158.1 160.7    -
 // A run's start and end cost a few microseconds, so the best has as few runs as
 // fill the GPU once (`slots` of them) and no more: a cluster of the largest
 // power of two within that. Few slices of long rows need more runs than a
 // cluster holds; more slices than slots that leave the last wave part empty are
 // cut into a few runs (512 slices of 2048 rows, d 64, group 1, masses: 1c 62.9,
-// 3k 54.4). fp32 runs stream slower, so more of them are wanted.
-DecodePlan attn_decode_plan(int n_slices, int max_rows, tri_dtype dt, int group) {
-  const int64_t n = n_slices;
-  const int64_t slots = dt == TRI_BF16 ? 2 * 152 : group <= 2 ? 4 * 152 : 3 * 152;
+// 3k 54.4).
+DecodePlan attn_decode_plan(int n_slices, int max_rows) {
+  const int64_t n = n_slices, slots = 2 * 152;
   int s = 1;
   while (2 * s <= MAX_CLUSTER && n * 2 * s <= slots && max_rows >= 64 * 2 * s) s *= 2;
   if (n * s * 3 <= slots * 2 && max_rows >= 512 * s) {

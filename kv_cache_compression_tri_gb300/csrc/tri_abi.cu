@@ -677,7 +677,7 @@ tri_status tri_attn_decode(const tri_kv* kv, const tri_queries* q, void* out, fl
   if (n64 * std::max<int64_t>(q->group, kv->n_cap / 1024 + 1) > 0x7fffffff) return TRI_ERR_INVALID_ARG;
   const int n = static_cast<int>(n64);
   const int rows = max_visible(kv, q->n_sink, q->window);
-  const DecodePlan plan = attn_decode_plan(n, rows, kv->dtype, q->group);
+  const DecodePlan plan = attn_decode_plan(n, rows);
   p.n_split = plan.n_split;
   p.join = plan.join;
   const DecodeWs w = decode_ws(kv, q->group, p.n_split, mass != nullptr);

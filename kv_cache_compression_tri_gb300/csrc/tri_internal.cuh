@@ -439,7 +439,7 @@ struct DecodePlan {
   int n_split;
   bool join;
 };
-DecodePlan attn_decode_plan(int n_slices, int max_rows, tri_dtype dt, int group);
+DecodePlan attn_decode_plan(int n_slices, int max_rows);
 int attn_decode_max_splits(int n_slices, int max_rows);
 cudaError_t launch_attn_decode(const AttnParams& p, int max_rows, tri_dtype dt, int head_dim, cudaStream_t st);
 // A chunk of new tokens over the cache.
