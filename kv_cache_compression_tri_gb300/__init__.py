@@ -570,6 +570,8 @@ def attn_decode(kv, layer: int, q: torch.Tensor, out: torch.Tensor, n_new: torch
     if workspace is None:
         need = int(lib.tri_attn_decode_workspace_bytes(ctypes.byref(kvs), qs.group, int(mass is not None)))
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=kv.device)
+        if stream is not None:
+            workspace.record_stream(stream)  # not handed out again before the call has run
     assert workspace.is_cuda and workspace.is_contiguous()
     _check("tri_attn_decode", lib.tri_attn_decode(ctypes.byref(kvs), ctypes.byref(qs), out.data_ptr(), _ptr(lse),
                                                   _ptr(mass), workspace.data_ptr(), workspace.nbytes, _stream(stream)))
@@ -622,6 +624,7 @@ def mass_evict(kv, mass: torch.Tensor, mass_out: torch.Tensor, n_prompt: int, n_
     mass_out (may be mass), the freed rows' masses set to 0."""
     lib = load_library()
     kvs = kv._abi()
+    assert kv.k.get_device() == mass.get_device() == mass_out.get_device() == torch.cuda.current_device()
     assert keep.dtype == torch.int32 and keep.is_contiguous() and keep.numel() == kv.n_slices * budget
     _check_mass(kvs, mass)
     _check_mass(kvs, mass_out)

@@ -223,7 +223,11 @@ __device__ __forceinline__ void join_cluster(const AttnParams& p, const Run& r, 
 template <typename T, int D>
 struct Tiles {
   int ta, tb, u0, u1;
+  int64_t base;         // of the slice's rows, and its table (kept: they take divisions)
+  const int32_t* trow;
   __device__ __forceinline__ Tiles(const AttnParams& p, const Run& r, int split) {
+    base = p.rows.slice_base(r.s);
+    trow = p.rows.seq_table(r.s);
     constexpr int TK = TileGeo<T, D>::TK;
     const int tn = (r.n + TK - 1) / TK;
     ta = (r.vis.s1 + TK - 1) / TK;
@@ -241,7 +245,6 @@ __device__ __forceinline__ void fetch_tile(const AttnParams& p, const Run& r, co
                                            bool& blocks_ok) {
   using G = TileGeo<T, D>;
   const int crow = lane / G::CH, cch = lane % G::CH, r0 = tl.row(u);
-  const int64_t base = p.rows.slice_base(r.s);
 #pragma unroll
   for (int s = 0; s < G::TK / G::RUN; ++s) {
     const int rs = r0 + G::RUN * s;
@@ -250,7 +253,7 @@ __device__ __forceinline__ void fetch_tile(const AttnParams& p, const Run& r, co
     if (PAGED) {
       int blk = 0;
       if (in) {
-        blk = __ldg(p.rows.seq_table(r.s) + (rs >> p.rows.block_shift));
+        blk = __ldg(tl.trow + (rs >> p.rows.block_shift));
         if (blk < 0 || blk >= p.rows.num_blocks) {
           // rows that nobody sees may have no block any more
           if (rs < r.vis.s1 || rs + G::RUN - 1 >= r.vis.w0) blocks_ok = false;
@@ -258,9 +261,9 @@ __device__ __forceinline__ void fetch_tile(const AttnParams& p, const Run& r, co
           in = false;
         }
       }
-      off = base + blk * p.rows.block_bytes + static_cast<int64_t>(rs & (p.rows.block_size - 1)) * G::ROW;
+      off = tl.base + blk * p.rows.block_bytes + static_cast<int64_t>(rs & (p.rows.block_size - 1)) * G::ROW;
     } else {
-      off = base + static_cast<int64_t>(rs) * G::ROW;
+      off = tl.base + static_cast<int64_t>(rs) * G::ROW;
     }
 #pragma unroll
     for (int i = 0; i < G::RUN / G::RPI; ++i) {

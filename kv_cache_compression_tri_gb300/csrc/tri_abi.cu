@@ -674,7 +674,7 @@ tri_status tri_attn_decode(const tri_kv* kv, const tri_queries* q, void* out, fl
   if (q->n_q != 1 || !out || !aligned(out, 16)) return TRI_ERR_INVALID_ARG;
   if ((lse && !aligned(lse, 4)) || (mass && !aligned(mass, 4))) return TRI_ERR_INVALID_ARG;
   const int64_t n64 = static_cast<int64_t>(kv->n_seq) * kv->n_kv_heads;
-  if (n64 * std::max<int64_t>(q->group, kv->n_cap / 1024 + 1) > 0x7fffffff) return TRI_ERR_INVALID_ARG;
+  if (n64 * std::max<int64_t>(16, kv->n_cap / 1024 + 1) > 0x7fffffff) return TRI_ERR_INVALID_ARG;
   const int n = static_cast<int>(n64);
   const int rows = max_visible(kv, q->n_sink, q->window);
   const DecodePlan plan = attn_decode_plan(n, rows);

@@ -382,6 +382,203 @@ def test_serving_run(block):
     check_prefill(c, G, [16, 5], layer=layer)
 
 
+def test_prefill_sequences_left_out_and_scale():
+    check_prefill(Case([[50, 60], [33, 200], [0, 4]], 128, torch.bfloat16), 3, [0, 33, 4], n_q=40, scale=0.2)
+    check_prefill(Case([[50, 60], [33, 200], [0, 4]], 64, torch.float32), 2, [20, 0, 4], n_q=30, scale=0.2)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_many_tiles(d):
+    """More query tiles than the GPU has SMs for in one go: the kernel with several CTAs' worth of work per SM (few queries
+    go through another), sampled against the definition."""
+    B, H, G, n_new, n = 8, 8, 2, 300, 700
+    c = Case([[n] * H] * B, d, torch.bfloat16, L=1)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q = torch.randn(B, n_new, H * G, d, generator=g, device="cuda").to(torch.bfloat16)
+    out, lse = torch.empty_like(q), torch.empty(B, n_new, H * G, device="cuda")
+    for n_sink, window in ((0, 0), (4, 150)):
+        tri.attn_prefill(c.kv, 0, q, out, n_sink=n_sink, window=window, lse=lse)
+        mass0 = torch.rand(B * H, c.n_cap, generator=g, device="cuda")
+        mass = mass0.clone()
+        tri.attn_mass(c.kv, 0, q, lse, mass, n_sink=n_sink, window=window)
+        c.ok()
+        qn, on, ln, mn = f64(q), f64(out), f64(lse), f64(mass) - f64(mass0)
+        for b, h in ((0, 0), (3, 5), (7, 7)):
+            k, v = c.rows(b, 0, h)
+            total = np.zeros(n)
+            for i in range(n_new):
+                for gq in range(G):
+                    r, hq = n - n_new + i, h * G + gq
+                    o, l, w = attend(qn[b, i, hq], k, v, r, d ** -0.5, n_sink, window)
+                    to, tl, _ = _bounds(qn[b, i, hq], k, v, r, d ** -0.5, w, o, l, n_sink, window, torch.bfloat16, 2.0 ** -8)
+                    assert np.all(np.abs(on[b, i, hq] - o) <= to) and abs(ln[b, i, hq] - l) <= tl
+                    total += w
+            # (mass0 < 1 is added in fp32: half a step of the sum, and the weights' own error, see check_prefill)
+            assert np.all(np.abs(mn[b * H + h, :n] - total) <= 1e-4 * total + 2.0 ** -23 * (total + 1))
+
+
+@pytest.mark.parametrize("n_q", [64, 65, 130])
+def test_mass_of_more_queries_than_stay_resident(n_q):
+    # group 4: 32 tokens to a query tile; two tiles stay in shared memory, more stream past the rows
+    check_prefill(Case([[n_q + 40, 300]], 128, torch.bfloat16, L=1, block=16), 4, [n_q], layer=0)
+    check_prefill(Case([[n_q + 200, n_q + 1]], 64, torch.bfloat16, L=1), 4, [n_q], layer=0, n_sink=3, window=50)
+
+
+@pytest.mark.parametrize("layout", ["blh", "lbh"])
+def test_pool_layouts(layout):
+    """A pool whose layers are outermost (a view with other strides) gives the same bits."""
+    c = Case([[70, 33], [100, 129]], 128, torch.bfloat16, L=3, block=32)
+    if layout == "lbh":
+        for name in ("k", "v"):
+            x = getattr(c.kv, name)
+            setattr(c.kv, name, x.permute(1, 0, 2, 3, 4).contiguous().permute(1, 0, 2, 3, 4))
+    check_decode(c, 4, layer=2, with_mass=True)
+    check_prefill(c, 2, [33, 40], layer=2)
+
+
+def test_queries_broadcast_over_sequences():
+    c = Case([[70, 33], [100, 129], [5, 6]], 64, torch.bfloat16)
+    one = torch.randn(1, 5, 6, 64, device="cuda").to(torch.bfloat16)
+    out, ref = torch.zeros(3, 5, 6, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, 5, 6, 64, dtype=torch.bfloat16, device="cuda")
+    lse, lse_ref = torch.zeros(3, 5, 6, device="cuda"), torch.zeros(3, 5, 6, device="cuda")
+    m, m_ref = torch.zeros(12, c.n_cap, device="cuda"), torch.zeros(12, c.n_cap, device="cuda")
+    q = one.expand(3, 5, 6, 64)
+    tri.attn_prefill(c.kv, 0, q, out, lse=lse)
+    tri.attn_prefill(c.kv, 0, q.contiguous(), ref, lse=lse_ref)
+    tri.attn_mass(c.kv, 0, q, lse, m)
+    tri.attn_mass(c.kv, 0, q.contiguous(), lse, m_ref)
+    c.ok()
+    assert torch.equal(out, ref) and torch.equal(lse, lse_ref) and torch.equal(m, m_ref)
+    d, d_ref = torch.zeros(3, 6, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, 6, 64, dtype=torch.bfloat16, device="cuda")
+    tri.attn_decode(c.kv, 0, q[:, 0], d)
+    tri.attn_decode(c.kv, 0, q[:, 0].contiguous(), d_ref)
+    c.ok()
+    assert torch.equal(d, d_ref)
+
+
+@pytest.mark.parametrize("lens", [[[900, 1500], [40, 2000]], [[30000, 20001]]])
+def test_captured_calls_follow_the_cache(lens):
+    """A captured step replayed after the cache grew equals the eager calls, bit for bit, on a stream of its own."""
+    c = Case(lens, 128, torch.bfloat16, L=1, n_cap=max(map(max, lens)) + 40)
+    G, B = 4, len(lens)
+    S = B * 2
+    c.kv.k.nan_to_num_(0.5)
+    c.kv.v.nan_to_num_(0.25)
+    q = torch.randn(B, 9, 8, 128, device="cuda").to(torch.bfloat16)
+    nn = torch.full((B,), 9, dtype=torch.int32, device="cuda")
+    ws = torch.empty(tri.attn_decode_workspace_bytes(c.kv, G, True), dtype=torch.uint8, device="cuda")
+
+    def bufs():
+        return (torch.zeros(B, 8, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(B, 9, 8, 128, dtype=torch.bfloat16, device="cuda"),
+                torch.zeros(B, 9, 8, device="cuda"), torch.zeros(S, c.n_cap, device="cuda"))
+
+    def step(d, o, l, m):
+        tri.attn_prefill(c.kv, 0, q, o, n_new=nn, lse=l, n_sink=4, window=500)
+        tri.attn_mass(c.kv, 0, q, l, m, n_new=nn, n_sink=4, window=500)
+        tri.attn_decode(c.kv, 0, q[:, 0], d, mass=m, workspace=ws)
+
+    captured, eager = bufs(), bufs()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(*bufs())
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step(*captured)
+    torch.cuda.synchronize()
+    for b in captured:
+        b.zero_()
+    for grow in (0, 7, 20):
+        c.kv.n_valid += grow
+        nn.fill_(9 - grow // 7)
+        graph.replay()
+        torch.cuda.synchronize()
+        step(*eager)
+        torch.cuda.synchronize()
+        for x, y in zip(captured, eager):
+            assert torch.equal(x, y)
+    assert int(c.status.item()) == 0
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its workspace, do not disturb each other."""
+    cases = [Case([[3000, 4000]] * 4, 128, torch.bfloat16, L=1, seed=i) for i in range(2)]
+    for c in cases:
+        c.kv.k.nan_to_num_(0.5)
+        c.kv.v.nan_to_num_(0.25)
+    q = torch.randn(4, 40, 8, 128, device="cuda").to(torch.bfloat16)
+
+    def run(c, stream, ws):
+        o, l = torch.zeros(4, 40, 8, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 40, 8, device="cuda")
+        m, d = torch.zeros(8, c.n_cap, device="cuda"), torch.zeros(4, 8, 128, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        return (o, l, m, d), lambda: (tri.attn_prefill(c.kv, 0, q, o, lse=l, stream=stream), tri.attn_mass(c.kv, 0, q, l, m, stream=stream),
+                                      tri.attn_decode(c.kv, 0, q[:, 3], d, mass=m, workspace=ws, stream=stream))
+
+    ref = []
+    for c in cases:
+        bufs, go = run(c, torch.cuda.current_stream(), None)
+        go()
+        torch.cuda.synchronize()
+        ref.append(bufs)
+    streams = [torch.cuda.Stream() for _ in cases]
+    ws = [torch.empty(tri.attn_decode_workspace_bytes(c.kv, 4, True), dtype=torch.uint8, device="cuda") for c in cases]
+    for _ in range(3):
+        got = [run(c, s, w) for c, s, w in zip(cases, streams, ws)]
+        for _, go in got:
+            go()
+        torch.cuda.synchronize()
+        for (bufs, _), want in zip(got, ref):
+            for x, y in zip(bufs, want):
+                assert torch.equal(x, y)
+
+
+def test_calls_repeat_bit_for_bit():
+    c = Case([[3000, 129], [64, 5000]], 64, torch.bfloat16, L=1, block=64)
+    q = torch.randn(2, 70, 6, 64, device="cuda").to(torch.bfloat16)
+    first = None
+    for _ in range(3):
+        o, l = torch.zeros_like(q), torch.zeros(2, 70, 6, device="cuda")
+        m, d = torch.zeros(4, c.n_cap, device="cuda"), torch.zeros(2, 6, 64, dtype=torch.bfloat16, device="cuda")
+        tri.attn_prefill(c.kv, 0, q, o, lse=l, n_new=torch.tensor([70, 64], dtype=torch.int32, device="cuda"))
+        tri.attn_mass(c.kv, 0, q, l, m, n_new=torch.tensor([70, 64], dtype=torch.int32, device="cuda"))
+        tri.attn_decode(c.kv, 0, q[:, 0], d, mass=m)
+        c.ok()
+        got = (o, l, m, d)
+        first = first or got
+        for x, y in zip(got, first):
+            assert torch.equal(x, y)
+
+
+def test_neighbours_are_left_alone():
+    """Guard bytes around every output and after the workspace, rows and slices of other layers."""
+    c = Case([[130, 40], [64, 100]], 128, torch.bfloat16, L=2)
+    def guarded(*shape, dtype):
+        n = int(np.prod(shape)) * torch.tensor([], dtype=dtype).element_size()
+        buf = torch.full((256 + n + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+        return buf, buf[256:256 + n].view(dtype).view(shape)
+    q = torch.randn(2, 33, 8, 128, device="cuda").to(torch.bfloat16)
+    ob, o = guarded(2, 33, 8, 128, dtype=torch.bfloat16)
+    lb, l = guarded(2, 33, 8, dtype=torch.float32)
+    mb, m = guarded(8, c.n_cap, dtype=torch.float32)
+    db, d = guarded(2, 8, 128, dtype=torch.bfloat16)
+    m.zero_()
+    k0, v0, nv0 = c.kv.k.clone(), c.kv.v.clone(), c.kv.n_valid.clone()
+    tri.attn_prefill(c.kv, 1, q, o, lse=l)
+    tri.attn_mass(c.kv, 1, q, l, m)
+    tri.attn_decode(c.kv, 1, q[:, 0], d, mass=m)
+    c.ok()
+    for buf in (ob, lb, mb, db):
+        assert bool((buf[:256] == 0xA5).all()) and bool((buf[-256:] == 0xA5).all())
+    mm = m.view(2, 2, 2, -1)
+    assert bool((mm[:, 0] == 0).all())  # layer 0's slices
+    for b in range(2):
+        for h in range(2):
+            assert bool((mm[b, 1, h, int(c.lens[b, h]):] == 0).all())
+    assert torch.equal(c.kv.k.view(torch.int16), k0.view(torch.int16)) and torch.equal(c.kv.v.view(torch.int16), v0.view(torch.int16))
+    assert torch.equal(c.kv.n_valid, nv0)
+
+
 def test_faults_are_reported_and_skipped():
     def fresh(**kw):
         return Case([[40, 50], [30, 60]], 64, torch.bfloat16, L=1, **kw)
