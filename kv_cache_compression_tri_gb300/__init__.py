@@ -534,8 +534,9 @@ def _queries(kvs: _TriKV, kv, layer: int, q: torch.Tensor, shape, strides, n_new
     assert strides[3] == 1 and (strides[2] == d or Hq == 1)
     if n_new is not None:
         assert n_new.is_cuda and n_new.dtype == torch.int32 and n_new.is_contiguous() and n_new.numel() == n_seq
-    return _TriQueries(q.data_ptr(), strides[0], strides[1], _ptr(n_new), n_q, Hq // kvs.n_kv_heads, layer, n_sink,
-                       window, d ** -0.5 if scale is None else scale)
+    # (the stride of a dimension of one may be anything)
+    return _TriQueries(q.data_ptr(), strides[0] if n_seq > 1 else 0, strides[1] if n_q > 1 else Hq * d, _ptr(n_new), n_q,
+                       Hq // kvs.n_kv_heads, layer, n_sink, window, d ** -0.5 if scale is None else scale)
 
 
 def _check_mass(kvs: _TriKV, mass: torch.Tensor):

@@ -49,6 +49,7 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr int STEP = 64;     // cached rows of a step
 constexpr float RAISE = 8.f;
+constexpr int MAX_SPLITS = 8;  // CTAs that share query tiles
 
 template <int D, int NQ>
 struct TcSmem {
@@ -437,31 +438,56 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
     }
     cluster_sync(splits);
     const int n_rows = NQ * TROWS / splits;
-    for (int i = t; i < n_rows * (D / 4); i += L::THREADS) {
-      const int row = rank * n_rows + i / (D / 4), e = i % (D / 4) * 4, q = row >> 7, u = row & 127;
-      if (u >= (q ? toks1 : toks0) * G) continue;
-      float mj = NEG_INF;
-      for (int k = 0; k < splits; ++k) mj = fmaxf(mj, cluster_ld(sm + row, k, splits));
-      const float mu = mj == NEG_INF ? 0.f : mj;
-      float lj = 0.f;
-      bool skip = false;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < splits; ++k) {
-        const float a = fast_exp2(cluster_ld(sm + row, k, splits) - mu), lk = cluster_ld(sm + 256 + row, k, splits);
-        const float4 x = cluster_ld4(reinterpret_cast<const float4*>(so + row * RS + e), k, splits);
-        skip |= lk < 0.f;
-        lj = fmaf(lk, a, lj);
-        o.x = fmaf(x.x, a, o.x);
-        o.y = fmaf(x.y, a, o.y);
-        o.z = fmaf(x.z, a, o.z);
-        o.w = fmaf(x.w, a, o.w);
+    // the factors of a row's sums, 2^(m_k - m) / l, by a thread per row (-1: left out)
+    float* factor = sm + 512;
+    auto live = [&](int row) { return (row & 127) < (row >= TROWS ? toks1 : toks0) * G; };
+    auto out_row = [&](int row) {
+      return (static_cast<int64_t>(c.seq) * p.n_q + tok0 + (row >> 7) * tpt + (row & 127) / G) * (p.n_kv_heads * G) + c.h * G +
+             (row & 127) % G;
+    };
+    if (t < n_rows) {
+      const int row = rank * n_rows + t;
+      float mk[MAX_SPLITS], lk[MAX_SPLITS], mj = NEG_INF, lj = 0.f;
+#pragma unroll
+      for (int k = 0; k < MAX_SPLITS; ++k) {
+        mk[k] = k < splits ? cluster_ld(sm + row, k, splits) : NEG_INF;
+        lk[k] = k < splits ? cluster_ld(sm + 256 + row, k, splits) : 0.f;
+        mj = fmaxf(mj, mk[k]);
       }
-      if (skip) continue;
+      const float mu = mj == NEG_INF ? 0.f : mj;
+      bool skip = false;
+#pragma unroll
+      for (int k = 0; k < MAX_SPLITS; ++k) {
+        skip |= lk[k] < 0.f;
+        mk[k] = fast_exp2(mk[k] - mu);
+        lj = fmaf(lk[k], mk[k], lj);
+      }
       const float inv = lj != 0.f ? 1.f / lj : 0.f;
-      const int64_t head = (static_cast<int64_t>(c.seq) * p.n_q + tok0 + q * tpt + u / G) * (p.n_kv_heads * G) + c.h * G + u % G;
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + head * D + e) =
-          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-      if (p.lse && e == 0) p.lse[head] = lj != 0.f ? LN2 * (mj + log2f(lj)) : NEG_INF;
+#pragma unroll
+      for (int k = 0; k < MAX_SPLITS; ++k)
+        if (k < splits) factor[k * n_rows + t] = skip ? -1.f : mk[k] * inv;
+      if (p.lse && !skip && live(row)) p.lse[out_row(row)] = lj != 0.f ? LN2 * (mj + log2f(lj)) : NEG_INF;
+    }
+    __syncthreads();
+    for (int i = t; i < n_rows * (D / 4); i += L::THREADS) {
+      const int r_own = i / (D / 4), row = rank * n_rows + r_own, e = i % (D / 4) * 4;
+      if (!live(row) || factor[r_own] < 0.f) continue;
+      float4 x[MAX_SPLITS];
+#pragma unroll
+      for (int k = 0; k < MAX_SPLITS; ++k)
+        if (k < splits) x[k] = cluster_ld4(reinterpret_cast<const float4*>(so + row * RS + e), k, splits);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < MAX_SPLITS; ++k) {
+        if (k >= splits) break;
+        const float a = factor[k * n_rows + r_own];
+        o.x = fmaf(x[k].x, a, o.x);
+        o.y = fmaf(x[k].y, a, o.y);
+        o.z = fmaf(x[k].z, a, o.z);
+        o.w = fmaf(x[k].w, a, o.w);
+      }
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + out_row(row) * D + e) =
+          make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
     }
     cluster_sync(splits);  // a CTA's shared memory stays until the others have read it
   }
@@ -486,7 +512,7 @@ cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
   if (p.window) rows = min(rows, static_cast<int64_t>(p.window) + tokens + p.n_sink);
   const bool few = units * 2 <= SMS;
   int splits = 1;
-  while (few && splits < 8 && units * splits * 2 <= SMS && rows >= 2 * splits * 2 * TROWS) splits *= 2;
+  while (few && splits < MAX_SPLITS && units * splits * 2 <= SMS && rows >= 2 * splits * 2 * TROWS) splits *= 2;
   auto kern = few ? prefill_tc_kernel<D, NQ, true> : prefill_tc_kernel<D, NQ, false>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D, NQ>::BYTES);
   if (e != cudaSuccess) return e;
