@@ -72,6 +72,15 @@ __device__ __forceinline__ void widen(const uint4& w, float (&x)[4]) {
   x[3] = __uint_as_float(w.w);
 }
 
+// 16 bytes global -> shared, zeros when not live; groups of a thread's copies.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  const int bytes = live ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Barrier over the cluster's CTAs (over the CTA when it is alone).
 __device__ __forceinline__ void cluster_sync(int ns) {
   if (ns == 1) {

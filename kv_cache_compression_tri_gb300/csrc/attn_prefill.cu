@@ -310,7 +310,7 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
     // ---- weights: thread u of a half = query row u of tile q, 32 columns of a step ----
     const int q = (w - 4) >> 3, half = ((w - 4) >> 2) & 1, u = t & 127;
     const int toks = q ? toks1 : toks0, rows = toks * G, rf = q ? rf1 : rf0, rl = q ? rl1 : rl0;
-    load_query_tile<D, 256>(smem + q * L::TILE, p, c.seq, c.h, tok0 + q * tpt, rows, half * 128 + u);
+    load_query_tile<D, 256>(qa + q * L::TILE, p, c.seq, c.h, tok0 + q * tpt, rows, half * 128 + u);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&ctl.q_ready[q]);
@@ -371,6 +371,8 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
       ++n;
     }
     wait_products();
+    // (without a step nothing has waited for the other warps' copies of the query tile)
+    if (n == 0 && ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.q_ready[q], 0));
     ctl.mx[n & 1][q][half][u] = l;
     asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
     const float l_half = ctl.mx[n & 1][q][half ^ 1][u];
@@ -379,8 +381,17 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
       if (lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
     } else if (!FEW_CTAS && !ctl.flag) {
       const float inv = l != 0.f ? 1.f / l : 0.f;
-      const int64_t head = (static_cast<int64_t>(c.seq) * p.n_q + tok0 + q * tpt + u / G) * (p.n_kv_heads * G) + c.h * G + u % G;
-      uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + head * D + half * (D / 2));
+      // The rows go out through the query tile, which no product reads any more (the last
+      // product's completion is that of every MMA of the query tile): stored
+      // by the thread that holds them, each warp's 32 rows then leave as whole 16-byte
+      // chunks of D bytes a row (a thread storing its own row touches 32 bytes of memory
+      // for each 16 it writes).
+      unsigned char* stage = smem + q * L::TILE;
+      constexpr int CHUNKS = D / 16;  // of a thread's half row
+      auto chunk_at = [&](int row, int k) {
+        const int ch = half * CHUNKS + k;
+        return reinterpret_cast<uint4*>(stage + (ch >> 3) * TCOL + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+      };
 #pragma unroll
       for (int k = 0; k < D / 64; ++k) {
         uint32_t o[32];
@@ -391,17 +402,27 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
-        if (u < rows) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t y[4];
+        for (int e = 0; e < 4; ++e) {
+          uint32_t y[4];
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
-              y[f] = pack_bf16(__uint_as_float(o[8 * e + 2 * f]) * inv, __uint_as_float(o[8 * e + 2 * f + 1]) * inv);
-            out[k * 4 + e] = make_uint4(y[0], y[1], y[2], y[3]);
-          }
+          for (int f = 0; f < 4; ++f)
+            y[f] = pack_bf16(__uint_as_float(o[8 * e + 2 * f]) * inv, __uint_as_float(o[8 * e + 2 * f + 1]) * inv);
+          *chunk_at(u, k * 4 + e) = make_uint4(y[0], y[1], y[2], y[3]);
         }
       }
+      __syncwarp();
+      auto head_of = [&](int row) {
+        const int tok = row / G;
+        return (static_cast<int64_t>(c.seq) * p.n_q + tok0 + q * tpt + tok) * (p.n_kv_heads * G) + c.h * G + row - tok * G;
+      };
+#pragma unroll
+      for (int i = 0; i < CHUNKS; ++i) {
+        const int row = (w & 3) * 32 + i * (32 / CHUNKS) + lane / CHUNKS, k = lane % CHUNKS;
+        if (row < rows)
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + head_of(row) * D + (half * CHUNKS + k) * 8) = *chunk_at(row, k);
+      }
+      const int64_t head = head_of(u);
       if (p.lse && half == 0 && u < rows) p.lse[head] = l != 0.f ? LN2 * (m + log2f(l)) : NEG_INF;
     }
   }

@@ -95,22 +95,29 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
 }
 
 // Packed query rows of one tile (row u: token tok0 + u / group, head u % group;
-// zeros from `rows` on), swizzled, by threads t of NT.
+// zeros from `rows` on), swizzled, by threads t of NT, as 16-byte asynchronous
+// copies that have landed on return. (Through registers, with a division per
+// row, a tile took 4 us of its CTA's time.)
 template <int D, int NT>
-__device__ __forceinline__ void load_query_tile(unsigned char* dst, const AttnParams& p, int seq, int h, int tok0, int rows, int t) {
-  constexpr int CH = D / 8;
-#pragma unroll 4
-  for (int i = t; i < TROWS * CH; i += NT) {
-    const int u = i / CH, c = i % CH;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (u < rows) {
-      const int tok = tok0 + u / p.group, g = u % p.group;
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + seq * p.q_seq + tok * p.q_token +
-                               (static_cast<int64_t>(h) * p.group + g) * D;
-      w = __ldg(reinterpret_cast<const uint4*>(q) + c);
+__device__ __forceinline__ void load_query_tile(uint32_t dst, const AttnParams& p, int seq, int h, int tok0, int rows, int t) {
+  constexpr int CH = D / 8, STEP = NT / CH;
+  const int G = p.group, c = t % CH, dt = STEP / G, dg = STEP - dt * G;
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + seq * p.q_seq + tok0 * p.q_token + static_cast<int64_t>(h) * G * D;
+  int u = t / CH, tok = u / G, g = u - tok * G;
+#pragma unroll
+  for (int i = 0; i < TROWS / STEP; ++i) {
+    const bool live = u < rows;
+    cp_async16(dst + (c >> 3) * TCOL + u * 128 + (((c & 7) ^ (u & 7)) << 4), live ? q + tok * p.q_token + g * D + c * 8 : q, live);
+    u += STEP;
+    tok += dt;
+    g += dg;
+    if (g >= G) {
+      g -= G;
+      ++tok;
     }
-    *reinterpret_cast<uint4*>(dst + (c >> 3) * TCOL + u * 128 + (((c & 7) ^ (u & 7)) << 4)) = w;
   }
+  cp_async_commit();
+  cp_async_wait<0>();
 }
 
 // kind::f16 with bf16 operands (bits 7-9 and 10-12 = 1), fp32 accumulation; bit

@@ -623,3 +623,17 @@ def test_faults_are_reported_and_skipped():
         assert st == tri.DEV_BAD_QUERY
         if o is not None:
             assert bool((o[1] == 9.0).all()) and bool((o[0] != 9.0).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_tiles_that_see_nothing(d):
+    """Whole query tiles before the first cached row, in the kernel for many queries and the one for few."""
+    for B, H, n_new in ((10, 8, 300), (1, 1, 300)):
+        c = Case([[0] * H] * (B - 1) + [[7] * H], d, torch.bfloat16, L=1)
+        q = torch.randn(B, n_new, H * 2, d, device="cuda").to(torch.bfloat16)
+        out, lse = torch.full_like(q, 9.0), torch.zeros(B, n_new, H * 2, device="cuda")
+        tri.attn_prefill(c.kv, 0, q, out, lse=lse)
+        c.ok()
+        assert bool((out[:-1] == 0).all()) and bool((lse[:-1] == float("-inf")).all())
+        assert bool((out[-1, :-7] == 0).all()) and bool((lse[-1, :-7] == float("-inf")).all())
+        assert bool((out[-1, -7:].float().abs().amax(-1) > 0).all()) and bool(torch.isfinite(lse[-1, -7:]).all())
