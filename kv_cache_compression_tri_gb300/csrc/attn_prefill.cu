@@ -154,19 +154,16 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
   // this CTA's run of the list: tiles first .. first + n_list - 1
   const int first = __shfl_sync(FULL_MASK, list.count() * rank / splits, 0);
   const int n_list = __shfl_sync(FULL_MASK, list.count() * (rank + 1) / splits - first, 0);
-  // the tiles of the run that query tile q needs: [0, a) and [f, e)
-  struct Range {
+  // the steps (row / 64) that some row of query tile q sees: below e, and below a or from f on
+  struct Steps {
     int a, f, e;
-    __device__ bool has(int i) const { return i < a || (i >= f && i < e); }
+    __device__ bool has(int x) const { return x < e && (x < a || x >= f); }
   };
-  auto range_of = [&](int q) {
+  auto steps_of = [&](int q) {
     const int rf = q ? rf1 : rf0, rl = q ? rl1 : rl0;
-    Range r;
-    r.a = rl < 0 ? 0 : min(list.a, rl / TROWS + 1);
-    r.f = p.window ? list.a + max(0, max(0, rf - p.window + 1) / TROWS - list.b) : 0;
-    r.e = rl < 0 ? 0 : list.a + max(0, rl / TROWS + 1 - list.b);
-    return Range{__shfl_sync(FULL_MASK, r.a - first, 0), __shfl_sync(FULL_MASK, r.f - first, 0),
-                 __shfl_sync(FULL_MASK, r.e - first, 0)};
+    const int a = p.window ? (min(p.n_sink, max(rl + 1, 0)) + STEP - 1) / STEP : 0;
+    const int f = p.window ? max(0, rf - p.window + 1) / STEP : 0;
+    return Steps{__shfl_sync(FULL_MASK, a, 0), __shfl_sync(FULL_MASK, f, 0), __shfl_sync(FULL_MASK, rl < 0 ? 0 : rl / STEP + 1, 0)};
   };
   auto tile_row = [&](int i) { return list.at(first + i) * TROWS; };
 
@@ -249,7 +246,7 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
   } else if (w < 3) {
     // ---- MMAs of query tile w - 1 ----
     const int q = w - 1;
-    const Range need = range_of(q);
+    const Steps need = steps_of(q);
     if (q < nq && elect_one()) {
       constexpr uint32_t IQK = bf16_idesc(TROWS, STEP, false), IPV = bf16_idesc(TROWS, D, true);
       constexpr uint64_t STAGE = L::TILE >> 4;  // (descriptors count 16 bytes)
@@ -264,31 +261,32 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
         }
         umma_commit(&ctl.s_full[q][b]);
       };
-      uint32_t done = 0;  // tiles
+      uint32_t use[2] = {0, 0};  // products of each buffer
+      auto step_of = [&](int i) { return 2 * list.at(first + i); };
       ok = mbar_wait_bounded(&ctl.q_ready[q], 0);
       if (n_list > 0 && ok) {
         ok = mbar_wait_bounded(&ctl.full[0], 0);
         tc_fence_after();
-        if (ok && need.has(0)) {
-          issue_s(0, 0);
-          issue_s(0, 1);
-        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          if (ok && need.has(step_of(0) + b)) issue_s(0, b);
         umma_commit(&ctl.empty[0]);
       }
       for (int i = 0; i < n_list && ok; ++i) {
-        const bool now = need.has(i), more = i + 1 < n_list, next = more && need.has(i + 1);
+        const bool more = i + 1 < n_list;
+        const int x = step_of(i), xn = more ? step_of(i + 1) : need.e;
         const uint32_t cv = 2 * i + 1, sv = cv % L::NST, sk = (cv + 1) % L::NST;
         ok = mbar_wait_bounded(&ctl.full[sv], (cv / L::NST) & 1);
         if (ok && more) ok = mbar_wait_bounded(&ctl.full[sk], ((cv + 1) / L::NST) & 1);
         if (!ok) break;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          if (now) {
-            ok = ok && mbar_wait_bounded(&ctl.p_ready[q][b], done & 1);
+          if (need.has(x + b)) {
+            ok = ok && mbar_wait_bounded(&ctl.p_ready[q][b], use[b] & 1);
             tc_fence_after();
             // P's rows 16 j .. 16 j + 15 of the step sit at columns 32 (j / 2) + 8 (j % 2) of its buffer
             const uint64_t ds = dv + sv * STAGE + b * (STEP * 8);
-            umma_ts(to, s_col(q, b), ds, IPV, done > 0 || b > 0);
+            umma_ts(to, s_col(q, b), ds, IPV, use[0] + use[1] > 0);
 #pragma unroll
             for (int j = 1; j < STEP / 16; ++j) umma_ts(to, s_col(q, b) + (j >> 1) * 32 + (j & 1) * 8, ds + j * 128, IPV, true);
             if constexpr (FEW_CTAS) {  // the pair's second half, 16 columns on
@@ -296,10 +294,10 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
               for (int j = 0; j < STEP / 16; ++j) umma_ts(to, s_col(q, b) + 16 + (j >> 1) * 32 + (j & 1) * 8, ds + j * 128, IPV, true);
             }
             umma_commit(&ctl.o_ready[q][b]);
+            ++use[b];
           }
-          if (next) issue_s(sk, b);
+          if (need.has(xn + b)) issue_s(sk, b);
         }
-        done += now;
         umma_commit(&ctl.empty[sv]);
         if (more) umma_commit(&ctl.empty[sk]);
       }
@@ -319,20 +317,23 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
     const int r = rf + u / G;
     const int pair = 1 + q * 4 + (w & 3);  // named barrier of the two warps of 32 rows
     const float sl = p.scale * LOG2E;
-    const Range need = range_of(q);
-    // n: steps done. The products of the steps before n are complete. (Those before n - 1 are: S of
-    // step n was issued after them.)
+    const Steps need = steps_of(q);
+    uint32_t par = 0;         // bit b: parity of buffer b's next use
+    int last = 0;             // the last step's buffer, and the parity of that use
+    uint32_t last_par = 0;
+    // The products of all steps before are complete. (Those before the last one are: S of
+    // this step was issued after them.)
     auto wait_products = [&] {
-      if (n > 0 && ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.o_ready[q][(n - 1) & 1], ((n - 1) >> 1) & 1));
+      if (n > 0 && ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.o_ready[q][last], last_par));
       tc_fence_after();
     };
     for (int step = 0; step < 2 * n_list; ++step) {
-      if (!need.has(step >> 1)) continue;
       const int b = step & 1;
+      if (!need.has(2 * list.at(first + (step >> 1)) + b)) continue;
       const uint32_t ts = s_col(q, b) + half * 32 + lanes;
       // (after a wait that gave up the loop runs on without waiting, since the
       // two halves meet at barriers)
-      if (ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[q][b], (n >> 1) & 1));
+      if (ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[q][b], (par >> b) & 1));
       tc_fence_after();
       uint32_t x[32];
       tmem_ld32(ts, x);
@@ -368,6 +369,9 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.p_ready[q][b]);
+      last = b;
+      last_par = (par >> b) & 1;
+      par ^= 1u << b;
       ++n;
     }
     wait_products();
