@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(MT, 1)
     mbar_init(&ctl.res_full, 1);
     for (int b = 0; b < 4; ++b) {
       mbar_init(&ctl.s_full[b], 1);
-      mbar_init(&ctl.s_free[b], 8);
+      mbar_init(&ctl.s_free[b], 4);
     }
     mbar_init_fence();
   }
@@ -338,9 +338,10 @@ __global__ void __launch_bounds__(MT, 1)
     }
     __syncwarp();
   } else {
-    // ---- weights: pair `par` takes products of its parity, a thread 64 columns of a row ----
-    const int par = (w - 4) >> 3, half = ((w - 4) >> 2) & 1, u = t & 127;
-    const uint32_t lanes = static_cast<uint32_t>((w & 3) * 32) << 16;
+    // ---- weights: warpgroup g takes products g, g + 4, .., which are in buffer g ----
+    const uint32_t g = (w - 4) >> 2;
+    const int u = t & 127;
+    const uint32_t ts = tm + g * 128 + (static_cast<uint32_t>((w & 3) * 32) << 16);
     const float sl = p.scale * LOG2E;
     float sums[2] = {0.f, 0.f};
     uint32_t cnt = 0, n = 0;
@@ -352,19 +353,20 @@ __global__ void __launch_bounds__(MT, 1)
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
         if (!need[kt] || !ok) continue;
-        if ((n & 1) == par) {
-          const uint32_t b = n & 3;
-          ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[b], (n >> 2) & 1));
+        if ((n & 3) == g) {
+          ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[g], (n >> 2) & 1));
           if (!ok) continue;
           tc_fence_after();
           const int k0 = k_of(kt);
           const bool all = all_seen(p, c, tpt, qt, k0);
           int lo = 0, hi = TROWS;
           if (!all) columns_seeing(p, c, tpt, qt, k0 + u, lo, hi);
-          sums[kt] += row_weights(tm + b * 128 + lanes, &ctl.nl[0][0][0] + st * TROWS, half * 64, sl, all, lo, hi, [&] {
+          const float* nl = &ctl.nl[0][0][0] + st * TROWS;
+          sums[kt] += row_weights(ts, nl, 0, sl, all, lo, hi, [] {});
+          sums[kt] += row_weights(ts, nl, 64, sl, all, lo, hi, [&] {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.s_free[b]);
+            if (lane == 0) mbar_arrive(&ctl.s_free[g]);
           });
         }
         ++n;
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(MT, 1)
     }
     if (!ok && lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) ctl.nl[8 + kt * 4 + par * 2 + half][0][u] = sums[kt];  // (the ring's lse rows are below)
+    for (int kt = 0; kt < 2; ++kt) ctl.nl[8 + kt * 4 + g][0][u] = sums[kt];  // (the ring's lse rows are below)
   }
   tc_fence_before();
   const bool fine = __syncthreads_and(ok);
