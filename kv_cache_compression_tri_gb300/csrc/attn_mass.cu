@@ -34,6 +34,7 @@ namespace {
 constexpr int MT = 640;    // copy warp, MMA warp, lse warp, second MMA warp, four warpgroups
 constexpr int FEW = 2;     // query tiles that stay in shared memory
 constexpr int SLOTS = 16;  // lse rows kept by mass_few_kernel (see there)
+constexpr int LSE_ROWS = 16;  // and by mass_many_kernel
 
 // Tensor map of the queries: (element, head, token, sequence), boxes of one
 // 64-element column of a packed tile.
@@ -167,7 +168,7 @@ struct MassCtl {
   uint32_t tmem;
   int flag;
   int first_slice, first_tile;
-  float nl[SLOTS][FEW][TROWS];    // (mass_many_kernel: a row per ring stage)
+  float nl[SLOTS][FEW][TROWS];    // -lse, base 2 (mass_many_kernel: LSE_ROWS rows, then the rows' sums)
 };
 static_assert(sizeof(MassCtl) <= 256 + SLOTS * FEW * TROWS * 4, "control block");
 
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(MT, 1)
   if (t == 0) {
     for (int i = 0; i < L::NST; ++i) {
       mbar_init(&ctl.full[i], 2);    // the queries and their lse
-      mbar_init(&ctl.empty[i], 18);  // two threads' MMAs and 16 warps
+      mbar_init(&ctl.empty[i], 2);   // two threads' MMAs
     }
     mbar_init(&ctl.res_full, 1);
     for (int b = 0; b < 4; ++b) {
@@ -256,6 +257,10 @@ __global__ void __launch_bounds__(MT, 1)
     for (int u = max(0, cnt - L::NST); u < cnt; ++u) (void)mbar_wait_bounded(&ctl.full[u % L::NST], (u / L::NST) & 1);
   } else if (w == 2) {
     // ---- lse: a tile's is loaded two tiles before it is stored (two register sets in turn) ----
+    // Tile i's is in row i % LSE_ROWS, overwritten for tile i + 16 once the products of tile
+    // i + 16 - NST are done, at least eight after those of tile i. Product p + 8 goes to p's
+    // buffer and waits until its warpgroup has read product p + 4, so is done with p.
+    static_assert(LSE_ROWS - L::NST >= 8, "lse rows");
     const int per_tile = tpt * p.n_kv_heads * p.group;
     const float* src[TROWS / 32];
     int tok[TROWS / 32];  // within a tile; n_new: none
@@ -279,7 +284,7 @@ __global__ void __launch_bounds__(MT, 1)
       const uint32_t st = cnt % L::NST;
       if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
 #pragma unroll
-      for (int k = 0; k < TROWS / 32; ++k) (&ctl.nl[0][0][0])[st * TROWS + k * 32 + lane] = -LOG2E * x[k];
+      for (int k = 0; k < TROWS / 32; ++k) (&ctl.nl[0][0][0])[cnt % LSE_ROWS * TROWS + k * 32 + lane] = -LOG2E * x[k];
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.full[st]);
       ++cnt;
@@ -348,12 +353,11 @@ __global__ void __launch_bounds__(MT, 1)
     for (int qt = 0; qt < n_qt && ok; ++qt) {
       const bool need[2] = {need0.has(qt), need1.has(qt)};
       if (!need[0] && !need[1]) continue;
-      const uint32_t st = cnt % L::NST;
-      ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.full[st], (cnt / L::NST) & 1));
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
         if (!need[kt] || !ok) continue;
         if ((n & 3) == g) {
+          // (the product was issued once the tile's lse were there too)
           ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.s_full[g], (n >> 2) & 1));
           if (!ok) continue;
           tc_fence_after();
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(MT, 1)
           const bool all = all_seen(p, c, tpt, qt, k0);
           int lo = 0, hi = TROWS;
           if (!all) columns_seeing(p, c, tpt, qt, k0 + u, lo, hi);
-          const float* nl = &ctl.nl[0][0][0] + st * TROWS;
+          const float* nl = &ctl.nl[0][0][0] + cnt % LSE_ROWS * TROWS;
           sums[kt] += row_weights(ts, nl, 0, sl, all, lo, hi, [] {});
           sums[kt] += row_weights(ts, nl, 64, sl, all, lo, hi, [&] {
             tc_fence_before();
@@ -371,9 +375,6 @@ __global__ void __launch_bounds__(MT, 1)
         }
         ++n;
       }
-      if (!ok) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.empty[st]);
       ++cnt;
     }
     if (!ok && lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
