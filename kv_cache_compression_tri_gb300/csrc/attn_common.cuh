@@ -58,20 +58,6 @@ __device__ __forceinline__ int new_tokens(const AttnParams& p, int seq) {
   return n;
 }
 
-// 16 bytes of a row as fp32.
-__device__ __forceinline__ void widen(const uint4& w, float (&x)[8]) {
-  x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x);
-  x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
-  x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z);
-  x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
-}
-__device__ __forceinline__ void widen(const uint4& w, float (&x)[4]) {
-  x[0] = __uint_as_float(w.x);
-  x[1] = __uint_as_float(w.y);
-  x[2] = __uint_as_float(w.z);
-  x[3] = __uint_as_float(w.w);
-}
-
 // 16 bytes global -> shared, zeros when not live; groups of a thread's copies.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
   const int bytes = live ? 16 : 0;
@@ -117,8 +103,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <typename T>
 __device__ __forceinline__ T from_f32(float x);
 template <>

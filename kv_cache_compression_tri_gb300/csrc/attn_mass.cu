@@ -674,7 +674,7 @@ struct MassSmem {
   int flag;
 };
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(FT) mass_kernel(const __grid_constant__ AttnParams p, int n_tiles) {
   extern __shared__ __align__(16) unsigned char raw[];
   MassSmem<D>& sm = *reinterpret_cast<MassSmem<D>*>(raw);
@@ -691,14 +691,14 @@ __global__ void __launch_bounds__(FT) mass_kernel(const __grid_constant__ AttnPa
     if (t == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
     return;
   }
-  load_rows<T, D>(p, p.k, base, trow, k0, last, sm.k);
+  load_rows<D>(p, p.k, base, trow, k0, last, sm.k);
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
   const int tpt = FM / G;
   for (int tok0 = 0; tok0 < c.n_new; tok0 += tpt) {
     const int toks = min(tpt, c.n_new - tok0), rows = toks * G, r_first = c.r0 + tok0;
     if (!tile_seen(p, k0, FN, max(r_first, 0), r_first + toks - 1)) continue;
     __syncthreads();
-    load_queries<T, D>(p, c, tok0, rows, sm.q);
+    load_queries<D>(p, c, tok0, rows, sm.q);
     if (t < rows)
       sm.lse2[t] = LOG2E * p.lse_in[c.seq * p.lse_seq + static_cast<int64_t>(tok0 + t / G) * (p.n_kv_heads * G) + c.h * G + t % G];
     __syncthreads();
@@ -724,9 +724,9 @@ __global__ void __launch_bounds__(FT) mass_kernel(const __grid_constant__ AttnPa
   }
 }
 
-template <typename T, int D>
-cudaError_t launch_typed(const AttnParams& p, cudaStream_t st) {
-  auto kern = mass_kernel<T, D>;
+template <int D>
+cudaError_t launch_fp32(const AttnParams& p, cudaStream_t st) {
+  auto kern = mass_kernel<D>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(MassSmem<D>)));
   if (e != cudaSuccess) return e;
@@ -742,7 +742,7 @@ cudaError_t launch_typed(const AttnParams& p, cudaStream_t st) {
 
 cudaError_t launch_attn_mass(const AttnParams& p, tri_dtype dt, int head_dim, cudaStream_t st) {
   if (dt == TRI_BF16) return head_dim == 64 ? launch_tc<64>(p, st) : launch_tc<128>(p, st);
-  return head_dim == 64 ? launch_typed<float, 64>(p, st) : launch_typed<float, 128>(p, st);
+  return head_dim == 64 ? launch_fp32<64>(p, st) : launch_fp32<128>(p, st);
 }
 
 }  // namespace tri

@@ -569,7 +569,7 @@ struct PrefillSmem {
   int flag;
 };
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(FT) prefill_kernel(const __grid_constant__ AttnParams p, int n_tiles) {
   extern __shared__ __align__(16) unsigned char raw[];
   PrefillSmem<D>& sm = *reinterpret_cast<PrefillSmem<D>*>(raw);
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(FT) prefill_kernel(const __grid_constant__ Att
   const int64_t base = p.rows.slice_base(c.s);
   const int32_t* trow = p.rows.seq_table(c.s);
   if (!chunk_blocks_ok(p, trow, r_first, r_last, &sm.flag)) return;
-  load_queries<T, D>(p, c, tok0, rows, sm.q);
+  load_queries<D>(p, c, tok0, rows, sm.q);
   float m[4], l[4], o[4][D / 16];
   int r[4];
 #pragma unroll
@@ -599,8 +599,8 @@ __global__ void __launch_bounds__(FT) prefill_kernel(const __grid_constant__ Att
   for (int k0 = 0; k0 <= r_last; k0 += FN) {
     if (!tile_seen(p, k0, FN, r_first, r_last)) continue;
     __syncthreads();
-    load_rows<T, D>(p, p.k, base, trow, k0, r_last, sm.k);
-    load_rows<T, D>(p, p.v, base, trow, k0, r_last, sm.v);
+    load_rows<D>(p, p.k, base, trow, k0, r_last, sm.k);
+    load_rows<D>(p, p.v, base, trow, k0, r_last, sm.v);
     __syncthreads();
     float x[4][4];
     tile_logits<D>(sm.q, sm.k, ty, tx, x);
@@ -650,14 +650,14 @@ __global__ void __launch_bounds__(FT) prefill_kernel(const __grid_constant__ Att
     const int64_t head = (static_cast<int64_t>(c.seq) * p.n_q + tok0 + u / G) * (p.n_kv_heads * G) + c.h * G + u % G;
     const float inv = l[a] != 0.f ? 1.f / l[a] : 0.f;
 #pragma unroll
-    for (int e = 0; e < D / 16; ++e) static_cast<T*>(p.out)[head * D + tx + 16 * e] = from_f32<T>(o[a][e] * inv);
+    for (int e = 0; e < D / 16; ++e) static_cast<float*>(p.out)[head * D + tx + 16 * e] = o[a][e] * inv;
     if (p.lse && tx == 0) p.lse[head] = l[a] != 0.f ? LN2 * (m[a] + log2f(l[a])) : NEG_INF;
   }
 }
 
-template <typename T, int D>
-cudaError_t launch_typed(const AttnParams& p, cudaStream_t st) {
-  auto kern = prefill_kernel<T, D>;
+template <int D>
+cudaError_t launch_fp32(const AttnParams& p, cudaStream_t st) {
+  auto kern = prefill_kernel<D>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(PrefillSmem<D>)));
   if (e != cudaSuccess) return e;
@@ -673,7 +673,7 @@ cudaError_t launch_typed(const AttnParams& p, cudaStream_t st) {
 
 cudaError_t launch_attn_prefill(const AttnParams& p, tri_dtype dt, int head_dim, cudaStream_t st) {
   if (dt == TRI_BF16) return head_dim == 64 ? launch_tc<64>(p, st) : launch_tc<128>(p, st);
-  return head_dim == 64 ? launch_typed<float, 64>(p, st) : launch_typed<float, 128>(p, st);
+  return head_dim == 64 ? launch_fp32<64>(p, st) : launch_fp32<128>(p, st);
 }
 
 }  // namespace tri

@@ -1,5 +1,5 @@
-// attn_tile.cuh -- the CUDA-core forms of attention over a chunk of queries:
-// tiles of 64 packed query rows (tokens x the group's heads) by 64 cached rows
+// attn_tile.cuh -- the CUDA-core forms (fp32 caches) of attention over a chunk of
+// queries: tiles of 64 packed query rows (tokens x the group's heads) by 64 cached rows
 // in fp32 shared memory, 4 x 4 logits per thread.
 #pragma once
 
@@ -56,39 +56,34 @@ __device__ __forceinline__ bool chunk_blocks_ok(const AttnParams& p, const int32
 }
 
 // Packed rows [0, FM) of queries: row u is token tok0 + u / group, head u % group.
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void load_queries(const AttnParams& p, const Chunk& c, int tok0, int rows, float (*sq)[D + 4]) {
-  constexpr int E = 16 / sizeof(T), C = D / E;
+  constexpr int C = D / 4;
   for (int i = threadIdx.x; i < FM * C; i += FT) {
     const int u = i / C, ch = i % C;
-    uint4 w = make_uint4(0, 0, 0, 0);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (u < rows) {
       const int tok = tok0 + u / p.group, g = u % p.group;
-      const T* q = static_cast<const T*>(p.q) + c.seq * p.q_seq + tok * p.q_token +
-                   (static_cast<int64_t>(c.h) * p.group + g) * D;
-      w = __ldg(reinterpret_cast<const uint4*>(q) + ch);
+      const float* q = static_cast<const float*>(p.q) + c.seq * p.q_seq + tok * p.q_token +
+                       (static_cast<int64_t>(c.h) * p.group + g) * D;
+      x = __ldg(reinterpret_cast<const float4*>(q) + ch);
     }
-    float x[E];
-    widen(w, x);
-#pragma unroll
-    for (int e = 0; e < E; ++e) sq[u][ch * E + e] = x[e] * (p.scale * LOG2E);
+    const float sl = p.scale * LOG2E;
+    *reinterpret_cast<float4*>(&sq[u][ch * 4]) = make_float4(x.x * sl, x.y * sl, x.z * sl, x.w * sl);
   }
 }
 
 // Cached rows [k0, k0 + FN) of K or V; rows past `last` are zeros.
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void load_rows(const AttnParams& p, const void* pool, int64_t base, const int32_t* trow, int k0,
                                           int last, float (*dst)[D + 4]) {
-  constexpr int E = 16 / sizeof(T), C = D / E;
+  constexpr int C = D / 4;
   for (int i = threadIdx.x; i < FN * C; i += FT) {
     const int u = i / C, ch = i % C;
-    uint4 w = make_uint4(0, 0, 0, 0);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (k0 + u <= last)
-      w = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(pool) + p.rows.row(base, trow, k0 + u)) + ch);
-    float x[E];
-    widen(w, x);
-#pragma unroll
-    for (int e = 0; e < E; ++e) dst[u][ch * E + e] = x[e];
+      x = __ldg(reinterpret_cast<const float4*>(static_cast<const char*>(pool) + p.rows.row(base, trow, k0 + u)) + ch);
+    *reinterpret_cast<float4*>(&dst[u][ch * 4]) = x;
   }
 }
 
