@@ -43,14 +43,14 @@ constexpr size_t CRING_BYTES = CSTAGES * CTILE;
 constexpr size_t COMPACT_SMEM = 2 * CRING_BYTES + 2 * CSTAGES * sizeof(uint64_t);
 
 // Where a compaction CTA keeps its shared state: the K and V rings (NST
-// tiles each, V's right after K's), 2 NST mbarriers, and for a paged cache
+// tiles of TB bytes each, V's right after K's), 2 NST mbarriers, and for a paged cache
 // the copy of CTAB table entries.
-template <int NST>
+template <int NST, int TB = CTILE>
 struct CompactSmem {
   unsigned char* rings;
   uint64_t* bars;
   int32_t* ctab;
-  static constexpr size_t RING = static_cast<size_t>(NST) * CTILE;  // one tensor's
+  static constexpr size_t RING = static_cast<size_t>(NST) * TB;  // one tensor's
   static constexpr size_t BARS = 2 * NST * sizeof(uint64_t);
   // the standalone kernels' layout: rings, then mbarriers, then the table
   __device__ static CompactSmem packed(unsigned char* smem) {
@@ -73,9 +73,9 @@ __device__ __forceinline__ int keep_at(const int32_t* keep, int j) {
 }
 
 // Rows [first, n_keep) of one tensor of one slice, moved by one warp
-// through a ring of NST tiles of CTILE bytes (see the file comment).
+// through a ring of NST tiles of TB bytes (see the file comment).
 // Row r of the slice is at pool + rows.row(sbase, trow, r).
-template <bool PAGED, bool RO, int NST>
+template <bool PAGED, bool RO, int NST, int TB>
 __device__ __forceinline__ void move_rows(char* pool, const RowMap& rows, int64_t sbase, const int32_t* trow,
                                           const int32_t* ctab, int cb0, unsigned char* ring, uint64_t* full,
                                           const int32_t* keep, int first, int n_keep, int rb, int lane,
@@ -87,7 +87,7 @@ __device__ __forceinline__ void move_rows(char* pool, const RowMap& rows, int64_
     const int64_t blk = (i < CTAB) ? ctab[i] : __ldg(trow + (r >> rows.block_shift));
     return sbase + blk * rows.block_bytes + static_cast<int64_t>(r & (rows.block_size - 1)) * rows.row_bytes;
   };
-  const int TR = CTILE / rb;  // rows per tile
+  const int TR = TB / rb;  // rows per tile
   const int u_first = first / TR;
   const int ntiles = (n_keep - 1) / TR - u_first + 1;
   if (lane == 0) {
@@ -105,7 +105,7 @@ __device__ __forceinline__ void move_rows(char* pool, const RowMap& rows, int64_
   // Each lane copies rows lo_j + lane + 32 r of a tile (r < RPL); the byte
   // offsets of their sources (keep entry, and block for a paged cache) are
   // resolved one tile ahead so no gather waits on them.
-  constexpr int RPL = CTILE / 128 / 32;  // most rows a lane copies per tile (2)
+  constexpr int RPL = TB / 128 / 32;  // most rows a lane copies per tile (2)
   int64_t knext[RPL];
   auto load_keep = [&](int k, int64_t (&kv)[RPL]) {
     int lo_j, hi_j, t0;
@@ -138,7 +138,7 @@ __device__ __forceinline__ void move_rows(char* pool, const RowMap& rows, int64_
       if (valid && !cont) {
         const unsigned after = (lane == 31) ? 0u : (runs >> (lane + 1));  // continuations after this lane
         const int len = 1 + (__ffs(~after) - 1);
-        bulk_g2s(ring + st * CTILE + (j - t0) * rb, pool + kv[r], static_cast<uint32_t>(len * rb), &full[st]);
+        bulk_g2s(ring + st * TB + (j - t0) * rb, pool + kv[r], static_cast<uint32_t>(len * rb), &full[st]);
       }
     }
   };
@@ -162,12 +162,12 @@ __device__ __forceinline__ void move_rows(char* pool, const RowMap& rows, int64_
       int lo_j, hi_j, t0;
       rows_of(k, lo_j, hi_j, t0);
       if (!PAGED) {
-        bulk_s2g(pool + sbase + static_cast<int64_t>(lo_j) * rb, ring + st * CTILE + (lo_j - t0) * rb,
+        bulk_s2g(pool + sbase + static_cast<int64_t>(lo_j) * rb, ring + st * TB + (lo_j - t0) * rb,
                  static_cast<uint32_t>((hi_j - lo_j) * rb));
       } else {
         for (int j = lo_j; j < hi_j;) {
           const int run = rows.run(j, hi_j - j);
-          bulk_s2g(pool + paged_row(j), ring + st * CTILE + (j - t0) * rb, static_cast<uint32_t>(run * rb));
+          bulk_s2g(pool + paged_row(j), ring + st * TB + (j - t0) * rb, static_cast<uint32_t>(run * rb));
           j += run;
         }
       }
@@ -208,8 +208,8 @@ struct CSmem {
 // earlier in the same kernel).
 // MASS: the rows' accumulated weights (p.mass) are moved like the positions,
 // and those of the freed rows set to 0.
-template <bool PAGED, int NTH, bool RO, int NST = CSTAGES, bool MASS = false>
-__device__ __forceinline__ void compact_slice(const CompactParams& p, const CompactSmem<NST>& cs, int64_t s) {
+template <bool PAGED, int NTH, bool RO, int NST = CSTAGES, bool MASS = false, int TB = CTILE>
+__device__ __forceinline__ void compact_slice(const CompactParams& p, const CompactSmem<NST, TB>& cs, int64_t s) {
   static_assert(NTH >= 128 && NTH % 32 == 0, "compaction CTA");
   __shared__ CSmem sm;
   const int t = threadIdx.x, lane = t & 31;
@@ -292,7 +292,7 @@ __device__ __forceinline__ void compact_slice(const CompactParams& p, const Comp
   if (wid < 2) {
     // warp 0 moves the K rows, warp 1 the V rows, each through its own ring
     if (first < n_keep)
-      move_rows<PAGED, RO, NST>(wid == 0 ? p.k : p.v, p.rows, sbase, trow, ctab, cb0, cs.rings + wid * cs.RING,
+      move_rows<PAGED, RO, NST, TB>(wid == 0 ? p.k : p.v, p.rows, sbase, trow, ctab, cb0, cs.rings + wid * cs.RING,
                                 cs.bars + wid * NST, keep, first, n_keep, p.row_bytes, lane, p.dev_status);
     return;
   }
