@@ -637,3 +637,33 @@ def test_prefill_tiles_that_see_nothing(d):
         assert bool((out[:-1] == 0).all()) and bool((lse[:-1] == float("-inf")).all())
         assert bool((out[-1, :-7] == 0).all()) and bool((lse[-1, :-7] == float("-inf")).all())
         assert bool((out[-1, -7:].float().abs().amax(-1) > 0).all()) and bool(torch.isfinite(lse[-1, -7:]).all())
+
+
+@pytest.mark.parametrize("B,L,H,n,budget", [(2, 1, 8, 5000, 4300), (2, 1, 8, 5000, 700), (10, 2, 8, 700, 600), (1, 1, 1, 9000, 8999)])
+@pytest.mark.parametrize("block", [0, 32])
+@pytest.mark.parametrize("d,dtype", [(64, torch.bfloat16), (128, torch.float32)])
+def test_mass_evict_moves_what_select_compact_moves(B, L, H, n, budget, block, d, dtype):
+    """Few and many slices (they take different tiles) and rows over many tiles, against tri_select_compact bit for bit."""
+    res = []
+    for own in (False, True):
+        c = Case([[n - 3 * h for h in range(H)]] * B, d, dtype, L=L, block=block, seed=3)
+        S = B * L * H
+        mass = torch.exp(2 * torch.randn(S, c.n_cap, generator=c.g, device="cuda"))
+        keep = torch.zeros(S, budget, dtype=torch.int32, device="cuda")
+        if own:
+            out = torch.full_like(mass, 5.0)
+            tri.mass_evict(c.kv, mass, out, 20, 30, budget, keep)
+            c.ok()
+            k = keep.clamp(min=0).long()
+            kept, old = (keep >= 0).sum(1, keepdim=True), torch.tensor([n - 3 * h for h in range(H)] * (B * L), device="cuda")[:, None]
+            j = torch.arange(c.n_cap, device="cuda")[None]
+            want = torch.where(j < old, 0.0, 5.0)
+            want = torch.where(j < kept, torch.nn.functional.pad(mass.gather(1, k), (0, c.n_cap - budget)), want)
+            assert torch.equal(out, want)
+        else:
+            tri.select_compact(mass, c.kv, 20, 30, budget, keep)
+            c.ok()
+        bits = torch.int16 if dtype == torch.bfloat16 else torch.int32
+        res.append((keep, c.kv.n_valid.clone(), c.kv.pos_out.clone(), c.kv.k.view(bits).clone(), c.kv.v.view(bits).clone()))
+    for x, y in zip(*res):
+        assert torch.equal(x, y)
