@@ -456,7 +456,7 @@ tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* ls
  * mass_out[s][j] <- mass[s][keep[j]], and the freed rows n_keep <= j < n_valid
  * (the count before the call) get mass_out[s][j] = 0, so that rows cached there
  * later start from nothing. mass, mass_out: device [n_slices][n_cap] fp32;
- * mass_out may equal mass. kv->pos_out required. */
+ * mass_out is mass or does not overlap it. kv->pos_out required. */
 tri_status tri_mass_evict(const float* mass, float* mass_out, const tri_kv* kv, int32_t n_prompt, int32_t n_recent,
                           int32_t budget, int32_t* keep_idx, tri_stream_t stream);
 

@@ -622,7 +622,7 @@ def mass_evict(kv, mass: torch.Tensor, mass_out: torch.Tensor, n_prompt: int, n_
                keep: torch.Tensor, stream=None) -> torch.Tensor:
     """Eviction by accumulated attention weight (tri_mass_evict): select_compact
     with mass [S, n_cap] as the scores, the masses moved with their rows into
-    mass_out (may be mass), the freed rows' masses set to 0."""
+    mass_out (mass itself or apart from it), the freed rows' masses set to 0."""
     lib = load_library()
     kvs = kv._abi()
     assert kv.k.get_device() == mass.get_device() == mass_out.get_device() == torch.cuda.current_device()

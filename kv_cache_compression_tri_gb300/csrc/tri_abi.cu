@@ -725,6 +725,10 @@ tri_status tri_mass_evict(const float* mass, float* mass_out, const tri_kv* kv, 
   if (st != TRI_OK) return st;
   if (!kv->pos_out || !mass || !aligned(mass, 4) || !mass_out || !aligned(mass_out, 4)) return TRI_ERR_INVALID_ARG;
   if (!keep_idx || !aligned(keep_idx, 4)) return TRI_ERR_INVALID_ARG;
+  // in place, or apart: one slice's masses must not land on another's before it has read them
+  const uintptr_t m0 = reinterpret_cast<uintptr_t>(mass), m1 = reinterpret_cast<uintptr_t>(mass_out);
+  if (m0 != m1 && (m0 < m1 ? m1 - m0 : m0 - m1) / sizeof(float) < static_cast<uint64_t>(slices_of(kv)) * kv->n_cap)
+    return TRI_ERR_INVALID_ARG;
   st = check_protect(n_prompt, n_recent, budget, kv->n_cap);
   if (st != TRI_OK) return st;
   CompactParams pc = compact_params(kv, keep_idx, budget);

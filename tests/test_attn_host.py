@@ -112,6 +112,15 @@ def test_mass_evict_rejects_bad_args(lib):  # noqa: F811
     assert call(kv=_kv(head_dim=96)) == UNSUPPORTED
 
 
+def test_mass_evict_rejects_masses_that_overlap(lib):  # noqa: F811
+    kv = _kv()
+    nbytes = kv.n_seq * kv.n_layers * kv.n_kv_heads * kv.n_cap * 4
+    call = lambda m0, m1: lib.tri_mass_evict(m0, m1, ctypes.byref(kv), 0, 0, 64, 0x50000, None)
+    for off in (4, 4 * kv.n_cap, nbytes - 4):
+        assert call(0x1000000, 0x1000000 + off) == INVALID
+        assert call(0x1000000 + off, 0x1000000) == INVALID
+
+
 def test_definitions_by_hand():
     # rows seen by row 9 with two sinks and a window of three
     assert visible(9, 12, 2, 3).nonzero()[0].tolist() == [0, 1, 7, 8, 9]
