@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(FT) mass_kernel(const __grid_constant__ AttnPa
     if (t == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
     return;
   }
-  load_rows<D>(p, p.k, base, trow, k0, last, sm.k);
+  load_rows<D>(p, p.k, base, trow, k0, 0, k0, last, sm.k);
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
   const int tpt = FM / G;
   for (int tok0 = 0; tok0 < c.n_new; tok0 += tpt) {

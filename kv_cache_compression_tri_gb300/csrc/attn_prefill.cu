@@ -585,6 +585,7 @@ __global__ void __launch_bounds__(FT) prefill_kernel(const __grid_constant__ Att
   const int64_t base = p.rows.slice_base(c.s);
   const int32_t* trow = p.rows.seq_table(c.s);
   if (!chunk_blocks_ok(p, trow, r_first, r_last, &sm.flag)) return;
+  const int s1 = visible_rows(max(r_last, 0), p.n_sink, p.window).s1, w0 = visible_rows(max(r_first, 0), p.n_sink, p.window).w0;
   load_queries<D>(p, c, tok0, rows, sm.q);
   float m[4], l[4], o[4][D / 16];
   int r[4];
@@ -599,8 +600,8 @@ __global__ void __launch_bounds__(FT) prefill_kernel(const __grid_constant__ Att
   for (int k0 = 0; k0 <= r_last; k0 += FN) {
     if (!tile_seen(p, k0, FN, r_first, r_last)) continue;
     __syncthreads();
-    load_rows<D>(p, p.k, base, trow, k0, r_last, sm.k);
-    load_rows<D>(p, p.v, base, trow, k0, r_last, sm.v);
+    load_rows<D>(p, p.k, base, trow, k0, s1, w0, r_last, sm.k);
+    load_rows<D>(p, p.v, base, trow, k0, s1, w0, r_last, sm.v);
     __syncthreads();
     float x[4][4];
     tile_logits<D>(sm.q, sm.k, ty, tx, x);

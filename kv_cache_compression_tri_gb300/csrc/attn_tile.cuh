@@ -73,16 +73,18 @@ __device__ __forceinline__ void load_queries(const AttnParams& p, const Chunk& c
   }
 }
 
-// Cached rows [k0, k0 + FN) of K or V; rows past `last` are zeros.
+// Cached rows [k0, k0 + FN) of K or V: those in [0, s1) and [w0, last], which are the rows that
+// chunk_blocks_ok checked the table for; zeros for the others, which are not read.
 template <int D>
 __device__ __forceinline__ void load_rows(const AttnParams& p, const void* pool, int64_t base, const int32_t* trow, int k0,
-                                          int last, float (*dst)[D + 4]) {
+                                          int s1, int w0, int last, float (*dst)[D + 4]) {
   constexpr int C = D / 4;
   for (int i = threadIdx.x; i < FN * C; i += FT) {
     const int u = i / C, ch = i % C;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (k0 + u <= last)
-      x = __ldg(reinterpret_cast<const float4*>(static_cast<const char*>(pool) + p.rows.row(base, trow, k0 + u)) + ch);
+    const int j = k0 + u;
+    if (j <= last && (j < s1 || j >= w0))
+      x = __ldg(reinterpret_cast<const float4*>(static_cast<const char*>(pool) + p.rows.row(base, trow, j)) + ch);
     *reinterpret_cast<float4*>(&dst[u][ch * 4]) = x;
   }
 }

@@ -1,0 +1,78 @@
+"""Attention at its edges: table entries of rows out of sight, windows in both
+types, queries before the first row, faults, memory orders of pools and
+queries, workspaces. Definitions and tolerances are test_gpu_attn.py's; where a
+call may not change its result at all, its bits are compared."""
+import numpy as np
+import pytest
+import torch
+
+import kv_cache_compression_tri_gb300 as tri
+from attn_oracle import visible
+from test_gpu_attn import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    tri.load_library()
+
+
+def hide(c, n_new, n_sink, window, what):
+    """Point every table entry whose rows no query of its sequence sees at a block of the pool that holds NaN
+    (what = "nan") or nowhere (a number). Returns how many there were."""
+    table = c.kv.block_table
+    bs = c.kv.k.shape[3]
+    if what == "nan":
+        what = min(set(range(c.kv.k.shape[0])) - set(table.flatten().tolist()))
+        assert bool(c.kv.k[what].isnan().all()) and bool(c.kv.v[what].isnan().all())
+    new, count = table.clone(), 0
+    for b in range(c.B):
+        seen = np.zeros(c.n_cap, dtype=bool)
+        for h in range(c.H):
+            n = int(c.lens[b, h])
+            for r in range(n - n_new[b], n):
+                seen |= visible(r, c.n_cap, n_sink, window)
+        for i in range(table.shape[1]):
+            if not seen[i * bs:(i + 1) * bs].any():
+                new[b, i] = what
+                count += 1
+    c.kv.block_table = new
+    return count
+
+
+def chunk_bufs(c, G, n_q, seed=2):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q = torch.randn(c.B, n_q, c.H * G, c.d, generator=g, device="cuda").to(c.dtype)
+    return q, torch.full_like(q, 9.0), torch.full((c.B, n_q, c.H * G), 9.0, device="cuda")
+
+
+# (row counts, new tokens, sinks, window): few queries and many, edges inside a tile of rows, heads of different lengths
+HIDDEN = [
+    ([[314, 314]], [64], 4, 90),
+    ([[700, 333], [512, 640]], [70, 1], 4, 90),
+    ([[700, 333], [512, 640]], [70, 1], 0, 17),
+    ([[900, 1100]], [200], 130, 65),
+    ([[1500] * 4] * 5, [300] * 5, 4, 200),
+]
+
+
+@pytest.mark.parametrize("lens,n_new,n_sink,window", HIDDEN)
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("what", ["nan", -1, 1 << 20])
+def test_prefill_fp32_blocks_out_of_sight(lens, n_new, n_sink, window, block, d, what):
+    c = Case(lens, d, torch.float32, L=1, block=block)
+    nn = torch.tensor(n_new, dtype=torch.int32, device="cuda")
+    res = []
+    for hidden in (False, True):
+        if hidden:
+            assert hide(c, n_new, n_sink, window, what) > 0
+        q, out, lse = chunk_bufs(c, 2, max(n_new))
+        tri.attn_prefill(c.kv, 0, q, out, n_new=nn, n_sink=n_sink, window=window, lse=lse)
+        c.ok()
+        res.append((out, lse))
+    for x, y in zip(*res):
+        assert torch.equal(x, y)
