@@ -687,11 +687,10 @@ __global__ void __launch_bounds__(FT) mass_kernel(const __grid_constant__ AttnPa
   const int64_t base = p.rows.slice_base(c.s);
   const int32_t* trow = p.rows.seq_table(c.s);
   const int last = min(k0 + FN - 1, r_end);
-  if (!p.rows.blocks_ok(trow, k0, last + 1, &sm.flag)) {
-    if (t == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
-    return;
-  }
-  load_rows<D>(p, p.k, base, trow, k0, 0, k0, last, sm.k);
+  // (with a bad entry for rows that some query sees the whole slice is left out, by each of its CTAs)
+  if (!chunk_blocks_ok(p, trow, c.r0, r_end, &sm.flag)) return;
+  const int s1 = visible_rows(max(r_end, 0), p.n_sink, p.window).s1, w0 = visible_rows(max(c.r0, 0), p.n_sink, p.window).w0;
+  load_rows<D>(p, p.k, base, trow, k0, s1, w0, last, sm.k);
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
   const int tpt = FM / G;
   for (int tok0 = 0; tok0 < c.n_new; tok0 += tpt) {

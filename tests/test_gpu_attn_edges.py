@@ -76,3 +76,43 @@ def test_prefill_fp32_blocks_out_of_sight(lens, n_new, n_sink, window, block, d,
         res.append((out, lse))
     for x, y in zip(*res):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("lens,n_new,n_sink,window", HIDDEN)
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("what", ["nan", -1, 1 << 20])
+def test_mass_blocks_out_of_sight(lens, n_new, n_sink, window, block, dtype, what):
+    c = Case(lens, 128, dtype, L=1, block=block)
+    nn = torch.tensor(n_new, dtype=torch.int32, device="cuda")
+    q, out, lse = chunk_bufs(c, 2, max(n_new))
+    tri.attn_prefill(c.kv, 0, q, out, n_new=nn, n_sink=n_sink, window=window, lse=lse)
+    res = []
+    for hidden in (False, True):
+        if hidden:
+            assert hide(c, n_new, n_sink, window, what) > 0
+        mass = torch.zeros(c.B * c.H, c.n_cap, device="cuda")
+        tri.attn_mass(c.kv, 0, q, lse, mass, n_new=nn, n_sink=n_sink, window=window)
+        c.ok()
+        res.append(mass)
+    assert torch.equal(*res)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n_new", [5, 200])
+def test_mass_of_a_slice_with_a_bad_block_stays(dtype, n_new):
+    """A bad entry for rows that a query sees leaves the masses of the whole slice as they were, and no other's."""
+    c = Case([[300, 400], [330, 310]], 128, dtype, L=1, block=32)
+    q, out, lse = chunk_bufs(c, 2, n_new)
+    tri.attn_prefill(c.kv, 0, q, out, lse=lse)
+    good = torch.zeros(4, c.n_cap, device="cuda")
+    tri.attn_mass(c.kv, 0, q, lse, good, n_sink=4, window=100)
+    c.ok()
+    c.kv.block_table[0, 11] = -1  # rows 352 .. 383 of sequence 0: its head 0 holds 300 rows, head 1 400
+    mass = torch.zeros_like(good)
+    tri.attn_mass(c.kv, 0, q, lse, mass, n_sink=4, window=100)
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == tri.DEV_BAD_BLOCK
+    assert bool((mass[1] == 0).all())
+    for s in (0, 2, 3):
+        assert torch.equal(mass[s], good[s]) and bool((mass[s] > 0).any())
