@@ -162,7 +162,7 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
   auto steps_of = [&](int q) {
     const int rf = q ? rf1 : rf0, rl = q ? rl1 : rl0;
     const int a = p.window ? (min(p.n_sink, max(rl + 1, 0)) + STEP - 1) / STEP : 0;
-    const int f = p.window ? max(0, rf - p.window + 1) / STEP : 0;
+    const int f = p.window ? max(0, max(rf, 0) - p.window + 1) / STEP : 0;
     return Steps{__shfl_sync(FULL_MASK, a, 0), __shfl_sync(FULL_MASK, f, 0), __shfl_sync(FULL_MASK, rl < 0 ? 0 : rl / STEP + 1, 0)};
   };
   auto tile_row = [&](int i) { return list.at(first + i) * TROWS; };

@@ -205,7 +205,7 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnParams& p, int r, int k0
   return upto & (~below(r + 1 - p.window - c0) | below(p.n_sink - c0));
 }
 
-// The 128-row tiles of the cache that rows r_lo .. r_hi see: [0, a) and [b, e).
+// The 128-row tiles of the cache that rows r_lo (it may be negative) .. r_hi see: [0, a) and [b, e).
 struct TileList {
   int a, b, e;
   __device__ __forceinline__ int count() const { return a + e - b; }
@@ -217,7 +217,7 @@ __device__ __forceinline__ TileList tiles_seen(const AttnParams& p, int r_lo, in
   t.e = r_hi / TROWS + 1;
   if (p.window == 0) return {0, 0, t.e};
   t.a = (min(p.n_sink, r_hi + 1) + TROWS - 1) / TROWS;
-  t.b = max(t.a, max(0, r_lo - p.window + 1) / TROWS);
+  t.b = max(t.a, max(0, max(r_lo, 0) - p.window + 1) / TROWS);
   if (t.b > t.e) t.b = t.e;
   return t;
 }

@@ -34,10 +34,11 @@ __device__ __forceinline__ bool chunk_of(const AttnParams& p, int ls, Chunk& c) 
   return c.n_new > 0;
 }
 
-// Whether any query of rows r_first .. r_last sees a row of [k0, k0 + len).
+// Whether any query of rows r_first .. r_last sees a row of [k0, k0 + len)
+// (r_first may be negative: the first query that sees anything is at row 0 then).
 __device__ __forceinline__ bool tile_seen(const AttnParams& p, int k0, int len, int r_first, int r_last) {
   if (k0 > r_last) return false;
-  return p.window == 0 || k0 < p.n_sink || k0 + len - 1 > r_first - p.window;
+  return p.window == 0 || k0 < p.n_sink || k0 + len - 1 > max(r_first, 0) - p.window;
 }
 
 __device__ __forceinline__ bool sees(const AttnParams& p, int r, int j) {

@@ -627,7 +627,9 @@ tri_status prepare_attn(const tri_kv* kv, const tri_queries* q, AttnParams& p) {
   p.n_q = q->n_q;
   p.group = q->group;
   p.n_sink = q->n_sink;
-  p.window = q->window;
+  // (no query sees more than n_cap rows, so a window of that many or more is none; the kernels
+  // subtract the window from rows)
+  p.window = q->window < kv->n_cap ? q->window : 0;
   p.scale = q->scale;
   return TRI_OK;
 }

@@ -8,7 +8,7 @@ import torch
 
 import kv_cache_compression_tri_gb300 as tri
 from attn_oracle import visible
-from test_gpu_attn import Case
+from test_gpu_attn import Case, check_decode, check_prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +116,21 @@ def test_mass_of_a_slice_with_a_bad_block_stays(dtype, n_new):
     assert bool((mass[1] == 0).all())
     for s in (0, 2, 3):
         assert torch.equal(mass[s], good[s]) and bool((mass[s] > 0).any())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n_sink,window", [(0, 1), (0, 6), (2, 3), (0, 1 << 30), (4, (1 << 31) - 1), ((1 << 31) - 1, (1 << 31) - 1),
+                                           ((1 << 31) - 1, 4)])
+def test_windows_and_queries_before_the_first_row(dtype, n_sink, window):
+    """Heads that hold fewer rows than there are new tokens, under every size of window."""
+    check_prefill(Case([[5, 40], [0, 30]], 64, dtype, L=1), 2, [30, 30], layer=0, n_sink=n_sink, window=window)
+    check_prefill(Case([[3, 160]], 128, dtype, L=1, block=16), 4, [150], layer=0, n_sink=n_sink, window=window)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("window", [76, 77, 78, 1 << 30, (1 << 31) - 1])
+def test_windows_about_the_capacity(dtype, window):
+    """77 rows fit a slice: a window of as many or more is none."""
+    c = Case([[77, 70]], 64, dtype, L=1, n_cap=77)
+    check_decode(c, 3, layer=0, n_sink=1, window=window, with_mass=True)
+    check_prefill(c, 3, [60], layer=0, n_sink=1, window=window)
