@@ -276,7 +276,6 @@ __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_cons
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float sm_m[NW][8], sm_l[NW][8];
   __shared__ float2 run_ml[MAX_GROUP];
-  __shared__ int bad;
   const int ls = blockIdx.x / p.n_split, split = blockIdx.x % p.n_split;
   const int t = threadIdx.x, w = t >> 5, lane = t & 31, lg = lane >> 2, lt = lane & 3;
   const int64_t pi = static_cast<int64_t>(blockIdx.x) * p.group;
@@ -286,8 +285,6 @@ __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_cons
     if (!p.join && t < p.group) p.part_ml[pi + t] = make_float2(NEG_INF, -1.f);
     return;  // (every run of the slice does)
   }
-  if (t == 0) bad = 0;
-
   const Tiles<T, D> tl(p, r, split);
 
   // the heads' B fragments
@@ -401,7 +398,6 @@ __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_cons
     st = st + 1 == G::NST ? 0 : st + 1;
   }
   cp_async_wait<0>();
-  if (PAGED && !blocks_ok) bad = 1;
 #pragma unroll
   for (int k = 4; k <= 16; k <<= 1) {
     l0 += __shfl_xor_sync(FULL_MASK, l0, k);
@@ -413,7 +409,8 @@ __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_cons
     sm_l[w][2 * lt] = l0;
     sm_l[w][2 * lt + 1] = l1;
   }
-  __syncthreads();  // every ring is idle: the warps' vector sums go there
+  // every ring is idle: the warps' vector sums go there
+  const bool bad = __syncthreads_or(PAGED && !blocks_ok);
   float* so = reinterpret_cast<float*>(smem);
   constexpr int HS = D + 4;  // floats between heads: the four lt of a store hit different banks
 #pragma unroll
@@ -470,7 +467,6 @@ __global__ void __launch_bounds__(DT) decode_rows_kernel(const __grid_constant__
   __shared__ float sq[GP][D];
   __shared__ float sm_m[GROUPS][GP], sm_l[GROUPS][GP];
   __shared__ float2 run_ml[GP];
-  __shared__ int bad;
   const int ls = blockIdx.x / p.n_split, split = blockIdx.x % p.n_split, t = threadIdx.x, G = p.group;
   const int w = t >> 5, lane = t & 31;
   pdl_launch();
@@ -480,7 +476,6 @@ __global__ void __launch_bounds__(DT) decode_rows_kernel(const __grid_constant__
     if (!p.join && t < G) p.part_ml[pi + t] = make_float2(NEG_INF, -1.f);
     return;  // (every run of the slice does)
   }
-  if (t == 0) bad = 0;
   const Tiles<T, D> tl(p, r, split);
   const uint32_t ring = smem_addr(smem) + w * Geo::WARP_RING;
   const unsigned char* ring_p = smem + w * Geo::WARP_RING;
@@ -579,8 +574,7 @@ __global__ void __launch_bounds__(DT) decode_rows_kernel(const __grid_constant__
     st = st + 1 == Geo::NST ? 0 : st + 1;
   }
   cp_async_wait<0>();
-  if (PAGED && !ok) bad = 1;
-  __syncthreads();  // every ring is idle: the row groups' sums go there
+  const bool bad = __syncthreads_or(PAGED && !ok);  // every ring is idle: the row groups' sums go there
   float(*so)[D] = reinterpret_cast<float(*)[D]>(smem);
   float* tot = reinterpret_cast<float*>(smem) + GROUPS * D;
   if (PAGED && bad && t == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);

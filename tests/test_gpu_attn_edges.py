@@ -134,3 +134,36 @@ def test_windows_about_the_capacity(dtype, window):
     c = Case([[77, 70]], 64, dtype, L=1, n_cap=77)
     check_decode(c, 3, layer=0, n_sink=1, window=window, with_mass=True)
     check_prefill(c, 3, [60], layer=0, n_sink=1, window=window)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,n_cap", [(150, 160), (1500, 1504), (12000, 12000)])
+def test_decode_reports_a_bad_block_wherever_it_is(dtype, n, n_cap):
+    """Every run, every warp and the first and last tile of a slice may be the one that meets the bad entry: the slice
+    is left out and reported, sequence by sequence, and the others are not touched by it."""
+    B = 6
+    c = Case([[n, n - 20]] * B, 64, dtype, L=1, block=16, n_cap=n_cap)
+    q = torch.randn(B, 4, 64, generator=c.g, device="cuda").to(dtype)
+
+    def run():
+        out, lse = torch.full_like(q, 9.0), torch.full((B, 4), 9.0, device="cuda")
+        mass = torch.zeros(2 * B, c.n_cap, device="cuda")
+        c.status.zero_()
+        tri.attn_decode(c.kv, 0, q, out, lse=lse, mass=mass)
+        torch.cuda.synchronize()
+        return int(c.status.item()), out, lse, mass
+
+    st, *good = run()
+    assert st == 0
+    table = c.kv.block_table.clone()
+    last = (n - 21) // 16  # head 1's last block
+    for i in sorted({*range(0, min(last, 24) + 1), last - 1, last, *range(0, last, max(1, last // 20))}):
+        b = i % B
+        c.kv.block_table = table.clone()
+        c.kv.block_table[b, i] = -1 if i % 2 else c.kv.k.shape[0]
+        st, *got = run()
+        assert st == tri.DEV_BAD_BLOCK, i
+        for x, y in zip(got, good):
+            x, y = x.view(B, -1), y.view(B, -1)
+            assert torch.equal(x[torch.arange(B) != b], y[torch.arange(B) != b])
+            assert bool((x[b] == (0.0 if x.shape[1] == 2 * c.n_cap else 9.0)).all()), i
