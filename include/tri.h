@@ -401,6 +401,8 @@ tri_status tri_select_union(const float* scores, const tri_kv* kv, int32_t n_pro
  * Query head h * group + g reads KV head h. Rows a query does not see may hold
  * anything, NaN and infinities included, except that V rows below n_valid
  * must be finite for tri_attn_prefill (a weight of 0 multiplies them there).
+ * A pool's blocks that no query of a sequence sees may be gone: their table
+ * entries may be anything, and no row of such a block is read into a result.
  *
  * Keys are taken as cached, so they must be TRI_KEYS_POST_ROPE and q rotated
  * in the same way (TRI_ERR_UNSUPPORTED otherwise). Sums, maxima and lse are
@@ -439,7 +441,10 @@ tri_status tri_attn_decode(const tri_kv* kv, const tri_queries* q, void* out, fl
  * one). out: device [n_seq][n_q][n_kv_heads * group][head_dim] of the cache's
  * type, 16-byte aligned; lse: optional device [n_seq][n_q][n_kv_heads * group]
  * fp32. bf16 caches: the weights are rounded to bf16 for their product with V
- * (their sum is not). */
+ * (their sum is not). A sequence with a fault in its row count or n_new is
+ * skipped. The queries that see a row of a bad table entry are left out, with
+ * the tokens next to them: tokens go in tiles of 128 / group from token 0 on
+ * (fp32: 64 / group), and a tile is written or left out as a whole. */
 tri_status tri_attn_prefill(const tri_kv* kv, const tri_queries* q, void* out, float* lse, tri_stream_t stream);
 
 /* tri_attn_mass -- the accumulated weight of every row under a chunk of
@@ -447,7 +452,8 @@ tri_status tri_attn_prefill(const tri_kv* kv, const tri_queries* q, void* out, f
  * row j of e^(x_j - lse). lse: device fp32 as tri_attn_prefill wrote it,
  * [n_seq][n_q][n_kv_heads * group] with lse_seq_stride elements between
  * sequences (so q and lse may be the last n_q tokens of a longer chunk: an
- * observation window). Rows nobody sees are left as they were. */
+ * observation window). Rows nobody sees are left as they were. A slice with a
+ * fault (row count, n_new, a block that some query sees) is skipped. */
 tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* lse, int64_t lse_seq_stride, float* mass,
                          tri_stream_t stream);
 

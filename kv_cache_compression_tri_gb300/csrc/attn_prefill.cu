@@ -69,7 +69,7 @@ struct TcCtl {
   uint64_t s_full[2][2], p_ready[2][2], o_ready[2][2];  // [query tile][half of a tile of rows]: S complete; P written; its product complete
   uint64_t v_fix;                                       // the last tile of V has landed, before its tail is cleared
   uint32_t tmem;
-  int flag;                                             // a bad table entry
+  int flag[2];                                          // a bad table entry for rows that the query tile sees
   float mx[2][2][2][TROWS];                             // maxima: [step parity][query tile][half][row]
 };
 static_assert(sizeof(TcCtl) <= 4608, "control block");
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
       }
     }
     mbar_init(&ctl.v_fix, 1);
-    ctl.flag = 0;
+    ctl.flag[0] = ctl.flag[1] = 0;
     mbar_init_fence();
   }
   if (w == 1) tmem_alloc(&ctl.tmem, L::TMEM);
@@ -198,15 +198,28 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
 
   if (w == 0) {
     // ---- copies: K and V tiles take the ring's stages in turn ----
-    // (a pool's tables are checked as they are read: with a bad entry for rows that some
-    // query sees, the query tiles are left out)
+    // (A pool's tables are checked as they are read: a query tile with a bad entry for rows
+    // that it sees is left out. Its flag is set before the rows are brought, and by no other
+    // rows, so a query tile that is done with its rows reads it settled. Boxes that no query
+    // sees are zeros: they may have no block any more.)
     int cnt = 0;
-    bool blocks_ok = true;
-    const int see0 = visible_rows(max(rf0, 0), p.n_sink, p.window).w0, see1 = visible_rows(max(r_hi, 0), p.n_sink, p.window).s1;
+    uint32_t bad = 0;  // bit q
+    int see0[NQ], see1[NQ];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      see0[q] = visible_rows(max(q ? rf1 : rf0, 0), p.n_sink, p.window).w0;
+      see1[q] = visible_rows(max(q ? rl1 : rl0, 0), p.n_sink, p.window).s1;
+    }
     auto block_of = [&](int k0) {
       if (!trow) return 0;
-      const int blk = tile_block<D>(p, box_rows, trow, k0, c.n, lane), row = k0 + lane / (D / 64) * box_rows;
-      if (blk == p.rows.num_blocks && row < k0 + TROWS && row <= r_hi && (row < see1 || row + box_rows > see0)) blocks_ok = false;
+      const int row = k0 + lane / (D / 64) * box_rows;
+      uint32_t seen = 0;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+        if (q < nq && row <= (q ? rl1 : rl0) && (row < see1[q] || row + box_rows > see0[q])) seen |= 1u << q;
+      if (!seen || row >= k0 + TROWS) return p.rows.num_blocks;
+      const int blk = tile_block<D>(p, box_rows, trow, k0, c.n, lane);
+      if (blk == p.rows.num_blocks) bad |= seen;
       return blk;
     };
     int blk = n_list ? block_of(tile_row(0)) : 0, blk_next = 0;
@@ -219,7 +232,8 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
       const bool is_v = cnt & 1;
       const bool fix = is_v && k0 + TROWS - 1 > r_hi;
       uint64_t* bar = fix ? &ctl.v_fix : &ctl.full[st];
-      if (!blocks_ok) ctl.flag = 1;
+      if (bad & 1) ctl.flag[0] = 1;
+      if (bad & 2) ctl.flag[1] = 1;
       __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(bar, L::TILE);
       __syncwarp();
@@ -237,7 +251,7 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
         if (lane == 0) mbar_arrive(&ctl.full[st]);
       }
     }
-    if (!blocks_ok) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
+    if (bad) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
     if (!ok && lane == 0) {
       set_status(p.dev_status, TRI_DEV_TIMEOUT);
       // let the copies in flight finish before shared memory is given up
@@ -383,7 +397,7 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
     l = half ? l_half + l : l + l_half;
     if (!ok) {
       if (lane == 0) set_status(p.dev_status, TRI_DEV_TIMEOUT);
-    } else if (!FEW_CTAS && !ctl.flag) {
+    } else if (!FEW_CTAS && !ctl.flag[q]) {
       const float inv = l != 0.f ? 1.f / l : 0.f;
       // The rows go out through the query tile, which no product reads any more (the last
       // product's completion is that of every MMA of the query tile): stored
@@ -458,7 +472,7 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
       }
       if (half == 0) {
         sm[row] = m;
-        sm[256 + row] = ok && !ctl.flag ? l : -1.f;
+        sm[256 + row] = ok && !ctl.flag[q] ? l : -1.f;
       }
     }
     cluster_sync(splits);

@@ -167,3 +167,56 @@ def test_decode_reports_a_bad_block_wherever_it_is(dtype, n, n_cap):
             x, y = x.view(B, -1), y.view(B, -1)
             assert torch.equal(x[torch.arange(B) != b], y[torch.arange(B) != b])
             assert bool((x[b] == (0.0 if x.shape[1] == 2 * c.n_cap else 9.0)).all()), i
+
+
+@pytest.mark.parametrize("lens,n_new,n_sink,window", HIDDEN)
+@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("what", ["nan", -1, 1 << 20])
+def test_prefill_bf16_blocks_out_of_sight(lens, n_new, n_sink, window, block, d, what):
+    c = Case(lens, d, torch.bfloat16, L=1, block=block)
+    nn = torch.tensor(n_new, dtype=torch.int32, device="cuda")
+    res = []
+    for hidden in (False, True):
+        if hidden:
+            assert hide(c, n_new, n_sink, window, what) > 0
+        q, out, lse = chunk_bufs(c, 2, max(n_new))
+        tri.attn_prefill(c.kv, 0, q, out, n_new=nn, n_sink=n_sink, window=window, lse=lse)
+        c.ok()
+        res.append((out, lse))
+    for x, y in zip(*res):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads", [1, 80])  # few query tiles, and more than the GPU has room for at once
+@pytest.mark.parametrize("n_sink,window", [(0, 0), (4, 50)])
+def test_prefill_leaves_out_the_tiles_that_see_a_bad_block(dtype, d, heads, n_sink, window):
+    G, n_new, n, bs = 4, 128, 300, 16
+    per = (128 if dtype == torch.bfloat16 else 64) // G
+    c = Case([[n] * heads], d, dtype, L=1, block=bs)
+    q = torch.randn(1, n_new, heads * G, d, generator=c.g, device="cuda").to(dtype)
+
+    def run():
+        c.status.zero_()
+        out, lse = torch.full_like(q, 9.0), torch.full((1, n_new, heads * G), 9.0, device="cuda")
+        tri.attn_prefill(c.kv, 0, q, out, n_sink=n_sink, window=window, lse=lse)
+        torch.cuda.synchronize()
+        return int(c.status.item()), out, lse
+
+    st, good, good_lse = run()
+    assert st == 0
+    table = c.kv.block_table.clone()
+    for i in range((n + bs - 1) // bs):
+        c.kv.block_table = table.clone()
+        c.kv.block_table[0, i] = -1 if i % 2 else 1 << 20
+        hit = np.zeros(n_new, dtype=bool)
+        for t0 in range(0, n_new, per):
+            hit[t0:t0 + per] = any(visible(n - n_new + t, n, n_sink, window)[i * bs:(i + 1) * bs].any() for t in range(t0, t0 + per))
+        for _ in range(3):
+            st, out, lse = run()
+            assert st == (tri.DEV_BAD_BLOCK if hit.any() else 0), i
+            h = torch.from_numpy(hit).cuda()
+            assert bool((out[:, h] == 9.0).all()) and bool((lse[:, h] == 9.0).all()), i
+            assert torch.equal(out[:, ~h], good[:, ~h]) and torch.equal(lse[:, ~h], good_lse[:, ~h]), i
