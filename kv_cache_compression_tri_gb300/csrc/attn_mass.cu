@@ -172,10 +172,10 @@ struct MassCtl {
 };
 static_assert(sizeof(MassCtl) <= 256 + SLOTS * FEW * TROWS * 4, "control block");
 
-template <int D>
+template <int D, bool MAPS>
 __global__ void __launch_bounds__(MT, 1)
     mass_many_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
-                     const __grid_constant__ CUtensorMap qmap, int box_rows) {
+                     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ RowNumbers rn) {
   using L = TcMass<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
   MassCtl& ctl = *reinterpret_cast<MassCtl*>(smem + L::CTRL);
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(MT, 1)
       mbar_init(&ctl.full[i], 2);    // the queries and their lse
       mbar_init(&ctl.empty[i], 2);   // two threads' MMAs
     }
-    mbar_init(&ctl.res_full, 1);
+    mbar_init(&ctl.res_full, nk);
     for (int b = 0; b < 4; ++b) {
       mbar_init(&ctl.s_full[b], 1);
       mbar_init(&ctl.s_free[b], 4);
@@ -233,11 +233,12 @@ __global__ void __launch_bounds__(MT, 1)
   bool ok = true;
 
   if (w == 0) {
-    if (lane == 0) mbar_arrive_expect_tx(&ctl.res_full, nk * L::TILE);
-    __syncwarp();
-    for (int kt = 0; kt < nk; ++kt)
-      load_tile<D>(res + kt * L::TILE, &kmap, p, box_rows, trow != nullptr, tile_block<D>(p, box_rows, trow, k_of(kt), c.n, lane),
-                   c.seq, c.h, k_of(kt), &ctl.res_full, lane);
+    const LaneBox<D> box(rn, lane);
+    for (int kt = 0; kt < nk; ++kt) {
+      const int blk = tile_block<D>(p, rn.box_rows, trow, c.seq, k_of(kt), c.n, lane);
+      load_tile<D, MAPS>(res + kt * L::TILE, &kmap, p.k, p, rn, box, box_place<D, MAPS>(rn, box, blk, c.h, k_of(kt)), c.seq, c.h, k_of(kt),
+                         &ctl.res_full, lane);
+    }
     int cnt = 0;
     for (int qt = 0; qt < n_qt && ok; ++qt) {
       if (!need0.has(qt) && !need1.has(qt)) continue;
@@ -462,10 +463,10 @@ __device__ __forceinline__ bool warp_blocks_ok(const AttnParams& p, const Chunk&
 // The lse rows of segment g are in slot g % SLOTS. A warpgroup that still reads
 // them when segment g + SLOTS is loaded would have to be a tile more than 12
 // tiles behind the MMAs, and S's four buffers let it fall back by at most 8.
-template <int D>
+template <int D, bool MAPS>
 __global__ void __launch_bounds__(MT, 1)
     mass_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
-                    const __grid_constant__ CUtensorMap qmap, int box_rows) {
+                    const __grid_constant__ CUtensorMap qmap, const __grid_constant__ RowNumbers rn) {
   using L = TcMass<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
   MassCtl& ctl = *reinterpret_cast<MassCtl*>(smem + L::CTRL);
@@ -527,6 +528,7 @@ __global__ void __launch_bounds__(MT, 1)
     int cnt = 0, segs = 0;
     const int32_t* trow = nullptr;
     int blk = 0, blk_row = -1;  // (of the row it is for)
+    const LaneBox<D> box(rn, lane);
     walk(
         [&](int seg, const Chunk& c, int n_qt) {
           if (seg > 0) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.res_free, (seg - 1) & 1));
@@ -549,15 +551,14 @@ __global__ void __launch_bounds__(MT, 1)
         },
         [&](int, const Chunk& c, int, int k0) {
           const int st = cnt % L::NST;
-          if (blk_row != k0) blk = tile_block<D>(p, box_rows, trow, k0, c.n, lane);
+          if (blk_row != k0) blk = tile_block<D>(p, rn.box_rows, trow, c.seq, k0, c.n, lane);
+          const int place = box_place<D, MAPS>(rn, box, blk, c.h, k0);
           // (the next tile's is on its way while this one waits for its stage)
           blk_row = k0 + TROWS;
-          const int blk_next = tile_block<D>(p, box_rows, trow, blk_row, c.n, lane);
+          const int blk_next = tile_block<D>(p, rn.box_rows, trow, c.seq, blk_row, c.n, lane);
           if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
           if (!ok) return;
-          if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], L::TILE);
-          __syncwarp();
-          load_tile<D>(ring + st * L::TILE, &kmap, p, box_rows, trow != nullptr, blk, c.seq, c.h, k0, &ctl.full[st], lane);
+          load_tile<D, MAPS>(ring + st * L::TILE, &kmap, p.k, p, rn, box, place, c.seq, c.h, k0, &ctl.full[st], lane);
           blk = blk_next;
           ++cnt;
         },
@@ -645,19 +646,21 @@ __global__ void __launch_bounds__(MT, 1)
 
 template <int D>
 cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
-  CUtensorMap kmap, qmap;
+  CUtensorMap kmap{}, qmap;
+  const RowNumbers rn = row_numbers(p);
   const Encode encode = tensor_map_encode();
-  const int box_rows = encode ? encode_rows(&kmap, p.k, p, D, encode) : 0;
-  if (!box_rows || !encode_queries(&qmap, p, D, encode)) return cudaErrorInvalidValue;
+  if (!encode || (rn.maps && !encode_rows(&kmap, p.k, p, D, rn, encode)) || !encode_queries(&qmap, p, D, encode))
+    return cudaErrorInvalidValue;
   const int tpt = TROWS / p.group, n_qt = (p.n_q + tpt - 1) / tpt;
   const bool few = n_qt <= FEW;
-  auto kern = few ? mass_few_kernel<D> : mass_many_kernel<D>;
+  auto kern = rn.maps ? (few ? mass_few_kernel<D, true> : mass_many_kernel<D, true>)
+                      : (few ? mass_few_kernel<D, false> : mass_many_kernel<D, false>);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcMass<D>::BYTES);
   if (e != cudaSuccess) return e;
   const int64_t n_ls = static_cast<int64_t>(p.n_seq) * p.n_kv_heads, tiles = (p.n_cap + TROWS - 1) / TROWS;
   const int64_t ctas = few ? min(static_cast<int64_t>(SMS), n_ls * tiles) : n_ls * ((tiles + 1) / 2);
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  kern<<<static_cast<unsigned>(ctas), MT, TcMass<D>::BYTES, st>>>(p, kmap, qmap, box_rows);
+  kern<<<static_cast<unsigned>(ctas), MT, TcMass<D>::BYTES, st>>>(p, kmap, qmap, rn);
   note_launch();
   return cudaGetLastError();
 }

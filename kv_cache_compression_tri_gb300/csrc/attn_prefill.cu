@@ -124,10 +124,10 @@ __device__ __forceinline__ float weights_of(const uint32_t (&x)[32], float sl, f
   return (l0 + l1) + (l2 + l3);
 }
 
-template <int D, int NQ, bool FEW_CTAS>
+template <int D, int NQ, bool FEW_CTAS, bool MAPS>
 __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
     prefill_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
-                      const __grid_constant__ CUtensorMap vmap, int box_rows, int n_tiles, int cluster) {
+                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ RowNumbers rn, int n_tiles, int cluster) {
   using L = TcSmem<D, NQ>;
   const int splits = FEW_CTAS ? cluster : 1;
   extern __shared__ __align__(1024) unsigned char smem[];  // (the swizzle goes by address)
@@ -211,18 +211,20 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
       see1[q] = visible_rows(max(q ? rl1 : rl0, 0), p.n_sink, p.window).s1;
     }
     auto block_of = [&](int k0) {
-      if (!trow) return 0;
-      const int row = k0 + lane / (D / 64) * box_rows;
+      if (!trow) return c.seq;
+      const int row = k0 + lane / (D / 64) * rn.box_rows;
       uint32_t seen = 0;
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
-        if (q < nq && row <= (q ? rl1 : rl0) && (row < see1[q] || row + box_rows > see0[q])) seen |= 1u << q;
+        if (q < nq && row <= (q ? rl1 : rl0) && (row < see1[q] || row + rn.box_rows > see0[q])) seen |= 1u << q;
       if (!seen || row >= k0 + TROWS) return p.rows.num_blocks;
-      const int blk = tile_block<D>(p, box_rows, trow, k0, c.n, lane);
+      const int blk = tile_block<D>(p, rn.box_rows, trow, c.seq, k0, c.n, lane);
       if (blk == p.rows.num_blocks) bad |= seen;
       return blk;
     };
-    int blk = n_list ? block_of(tile_row(0)) : 0, blk_next = 0;
+    const LaneBox<D> box(rn, lane);
+    auto place_of = [&](int blk, int k0) { return box_place<D, MAPS>(rn, box, blk, c.h, k0); };
+    int place = n_list ? place_of(block_of(tile_row(0)), tile_row(0)) : 0, blk_next = 0;
     for (; cnt < 2 * n_list && ok; ++cnt) {
       const int st = cnt % L::NST, k0 = tile_row(cnt >> 1);
       if (!(cnt & 1) && cnt + 2 < 2 * n_list)  // (on its way while this tile waits for its stage)
@@ -235,10 +237,8 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
       if (bad & 1) ctl.flag[0] = 1;
       if (bad & 2) ctl.flag[1] = 1;
       __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(bar, L::TILE);
-      __syncwarp();
-      load_tile<D>(ring + st * L::TILE, is_v ? &vmap : &kmap, p, box_rows, trow != nullptr, blk, c.seq, c.h, k0, bar, lane);
-      if (is_v) blk = blk_next;
+      load_tile<D, MAPS>(ring + st * L::TILE, is_v ? &vmap : &kmap, is_v ? p.v : p.k, p, rn, box, place, c.seq, c.h, k0, bar, lane);
+      if (is_v && cnt + 1 < 2 * n_list) place = place_of(blk_next, tile_row((cnt >> 1) + 1));
       if (fix) {
         ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.v_fix, 0));
         if (!ok) break;
@@ -535,10 +535,11 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
 
 template <int D>
 cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
-  CUtensorMap kmap, vmap;
-  const Encode encode = tensor_map_encode();
-  const int box_rows = encode ? encode_rows(&kmap, p.k, p, D, encode) : 0;
-  if (!box_rows || !encode_rows(&vmap, p.v, p, D, encode)) return cudaErrorInvalidValue;
+  CUtensorMap kmap{}, vmap{};
+  const RowNumbers rn = row_numbers(p);
+  const Encode encode = rn.maps ? tensor_map_encode() : nullptr;
+  if (rn.maps && (!encode || !encode_rows(&kmap, p.k, p, D, rn, encode) || !encode_rows(&vmap, p.v, p, D, rn, encode)))
+    return cudaErrorInvalidValue;
   // one or two query tiles per CTA: at d 64 two CTAs with a tile each fit an SM, and one's
   // start and end hide behind the other's work (8 padded prompts of up to 4096 tokens, sinks
   // and a window of 1000: 189 us, with two tiles per CTA 199)
@@ -552,7 +553,8 @@ cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
   const bool few = units * 2 <= SMS;
   int splits = 1;
   while (few && splits < MAX_SPLITS && units * splits * 2 <= SMS && rows >= 2 * splits * 2 * TROWS) splits *= 2;
-  auto kern = few ? prefill_tc_kernel<D, NQ, true> : prefill_tc_kernel<D, NQ, false>;
+  auto kern = rn.maps ? (few ? prefill_tc_kernel<D, NQ, true, true> : prefill_tc_kernel<D, NQ, false, true>)
+                      : (few ? prefill_tc_kernel<D, NQ, true, false> : prefill_tc_kernel<D, NQ, false, false>);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D, NQ>::BYTES);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -566,7 +568,7 @@ cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = splits > 1;
-  const cudaError_t r = cudaLaunchKernelEx(&cfg, kern, p, kmap, vmap, box_rows, n_tiles, splits);
+  const cudaError_t r = cudaLaunchKernelEx(&cfg, kern, p, kmap, vmap, rn, n_tiles, splits);
   if (r == cudaSuccess) note_launch();
   return r;
 }

@@ -42,27 +42,57 @@ inline Encode tensor_map_encode() {
   return encode;
 }
 
-// Tensor map of one layer's K (or V) rows: (element, row, head, sequence) of
-// contiguous slices, (element, row of the block, head, block) of a pool. Boxes
-// of 64 elements by up to 128 rows. Returns the rows of a box, 0 on failure.
-inline int encode_rows(CUtensorMap* map, const void* pool, const AttnParams& p, int head_dim, Encode encode) {
+// Where a layer's rows are, for the copy warps. Blocks (of a pool) or sequences, and heads,
+// are multiples of a row apart in any order the strides give, so a row of the pool has one
+// number and the tensor map is (element, row): two strides never have to fit into each
+// other, which a map of more dimensions would ask of them (each of its strides is
+// documented as a multiple of the one before). Strides that are not whole rows have no
+// such map; their rows are brought by 16-byte copies of the copy warp.
+struct RowNumbers {
+  int box_rows;                 // rows of a box: 128, or a smaller block
+  int maps;                     // whether there are tensor maps
+  int head_rows, outer_rows;    // rows from head to head, from block (or sequence) to the next
+  int none, row_mask;           // the number of no block (or sequence); row & row_mask is its place in the block
+  int count;                    // rows of the map; one past its last row reads as zeros
+};
+inline RowNumbers row_numbers(const AttnParams& p) {
   const RowMap& m = p.rows;
   const bool paged = m.table != nullptr;
-  const int64_t base = p.layer * (paged ? m.layer_bytes : p.n_kv_heads * m.slice_bytes);
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(paged ? m.block_size : p.n_cap),
-                              static_cast<cuuint64_t>(p.n_kv_heads), static_cast<cuuint64_t>(paged ? m.num_blocks : p.n_seq)};
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(m.row_bytes), static_cast<cuuint64_t>(paged ? m.head_bytes : m.slice_bytes),
-                           static_cast<cuuint64_t>(paged ? m.block_bytes : m.lh_count * m.slice_bytes)};
-  if (dims[3] == 1 && strides[2] < strides[1]) strides[2] = strides[1];  // (never used)
-  const int rows = paged && m.block_size < TROWS ? m.block_size : TROWS;
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1};
-  const cuuint32_t step[4] = {1, 1, 1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, static_cast<char*>(const_cast<void*>(pool)) + base, dims,
-                            strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? rows : 0;
+  const int64_t head = p.n_kv_heads > 1 ? (paged ? m.head_bytes : m.slice_bytes) : 0;
+  const int64_t n_outer = paged ? m.num_blocks : p.n_seq;
+  const int64_t outer = n_outer > 1 ? (paged ? m.block_bytes : m.lh_count * m.slice_bytes) : 0;
+  RowNumbers r{};
+  r.none = paged ? m.num_blocks : -1;
+  r.row_mask = paged ? m.block_size - 1 : 0x7fffffff;
+  r.box_rows = paged && m.block_size < TROWS ? m.block_size : TROWS;
+  if (head % m.row_bytes || outer % m.row_bytes) return r;
+  const int64_t count = ((p.n_kv_heads - 1) * head + (n_outer - 1) * outer) / m.row_bytes + (paged ? m.block_size : p.n_cap);
+  if (count > 0x7fffffff - 2 * TROWS) return r;  // (coordinates are 32 bits)
+  r.maps = 1;
+  r.head_rows = static_cast<int>(head / m.row_bytes);
+  r.outer_rows = static_cast<int>(outer / m.row_bytes);
+  r.count = static_cast<int>(count);
+  return r;
+}
+// The tensor map of one layer's K (or V) rows, boxes of 64 elements by box_rows rows.
+inline bool encode_rows(CUtensorMap* map, const void* pool, const AttnParams& p, int head_dim, const RowNumbers& r, Encode encode) {
+  const RowMap& m = p.rows;
+  const int64_t base = p.layer * (m.table ? m.layer_bytes : p.n_kv_heads * m.slice_bytes);
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(r.count)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(m.row_bytes)};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(r.box_rows)};
+  const cuuint32_t step[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, static_cast<char*>(const_cast<void*>(pool)) + base, dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+__device__ __forceinline__ void tma_load2(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
 __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
@@ -71,27 +101,68 @@ __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
-// Block that holds a lane's box of the tile at row k0 (pools only): num_blocks,
-// which the map fills with zeros, where there is none.
+// The block that holds a lane's box of the tile at row k0 of sequence `seq` (num_blocks, which
+// reads as zeros, where there is none), or for contiguous slices the sequence.
 template <int D>
-__device__ __forceinline__ int tile_block(const AttnParams& p, int box_rows, const int32_t* trow, int k0, int n, int lane) {
+__device__ __forceinline__ int tile_block(const AttnParams& p, int box_rows, const int32_t* trow, int seq, int k0, int n, int lane) {
+  if (!trow) return seq;
   const int i = lane / (D / 64), row = k0 + i * box_rows;
-  if (!trow || i >= TROWS / box_rows || row >= n) return p.rows.num_blocks;
+  if (i >= TROWS / box_rows || row >= n) return p.rows.num_blocks;
   const int blk = __ldg(trow + (row >> p.rows.block_shift));
   return blk < 0 || blk > p.rows.num_blocks ? p.rows.num_blocks : blk;
 }
-// Cached rows [k0, k0 + 128) of slice (seq, h) into the tile at `dst`, by the
-// lanes of one warp after one of them expected D * 256 bytes on `bar`; blk as
-// tile_block gave it. Rows past the cache read as zeros too.
+// A lane's box of a tile: 64 elements from `x` on of the rows from `row` on, at `off` in the tile.
 template <int D>
-__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, const AttnParams& p, int box_rows, bool paged, int blk,
-                                          int seq, int h, int k0, uint64_t* bar, int lane) {
-  constexpr int COLS = D / 64;
-  if (lane >= TROWS / box_rows * COLS) return;
-  const int col = lane % COLS, i = lane / COLS, row = k0 + i * box_rows;
-  const uint32_t d = dst + col * TCOL + i * box_rows * 128;
-  if (paged) tma_load4(d, map, 64 * col, row & (p.rows.block_size - 1), h, blk, bar);
-  else tma_load4(d, map, 64 * col, row, h, seq, bar);
+struct LaneBox {
+  int x, row;
+  uint32_t off;
+  bool live;
+  __device__ __forceinline__ LaneBox(const RowNumbers& rn, int lane) {
+    constexpr int COLS = D / 64;
+    x = lane % COLS * 64;
+    row = lane / COLS * rn.box_rows;
+    off = lane % COLS * TCOL + row * 128;
+    live = row < TROWS;
+  }
+};
+// Where a lane's box of the tile at row k0 of head h is: with maps its first row's number, else
+// the block (as tile_block gave it). Worked out before the wait for a ring stage: after it, the
+// dozen instructions are on the chain from a stage set free to its next rows (32 queries over 16
+// caches of up to 32768 rows: 170 us, before it 164).
+template <int D, bool MAPS>
+__device__ __forceinline__ int box_place(const RowNumbers& rn, const LaneBox<D>& box, int blk, int h, int k0) {
+  if (!MAPS) return blk;
+  return blk == rn.none ? rn.count : blk * rn.outer_rows + h * rn.head_rows + ((k0 + box.row) & rn.row_mask);
+}
+// Cached rows [k0, k0 + 128) of slice (seq, h) of K or V into the tile at `dst`, by one warp,
+// arriving once on `bar`. Rows past the slice hold zeros or another slice's rows. (MAPS by
+// template: with both ways in one kernel an 8192-token prompt took 390 us for 376.)
+template <int D, bool MAPS>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, const void* pool, const AttnParams& p, const RowNumbers& rn,
+                                          const LaneBox<D>& box, int place, int seq, int h, int k0, uint64_t* bar, int lane) {
+  if constexpr (MAPS) {
+    if (lane == 0) mbar_arrive_expect_tx(bar, D * 256);
+    __syncwarp();
+    if (box.live) tma_load2(dst + box.off, map, box.x, place, bar);
+  } else {
+    constexpr int COLS = D / 64, CH = D / 8;
+    const bool paged = p.rows.paged();
+    const char* base = static_cast<const char*>(pool) + p.rows.slice_base(slice_of(p, seq, h));
+#pragma unroll 4
+    for (int i = lane; i < TROWS * CH; i += 32) {
+      const int u = i / CH, ch = i % CH, row = k0 + u;
+      const int blk = __shfl_sync(FULL_MASK, place, u / rn.box_rows * COLS);  // (from the lane of row u's box)
+      const bool live = paged ? blk < p.rows.num_blocks : row < p.n_cap;
+      const int64_t off = paged ? blk * p.rows.block_bytes + static_cast<int64_t>(row & (p.rows.block_size - 1)) * p.rows.row_bytes
+                                : static_cast<int64_t>(row) * p.rows.row_bytes;
+      cp_async16(dst + (ch >> 3) * TCOL + u * 128 + (((ch & 7) ^ (u & 7)) << 4), base + (live ? off + ch * 16 : 0), live);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  }
 }
 
 // Packed query rows of one tile (row u: token tok0 + u / group, head u % group;

@@ -220,3 +220,71 @@ def test_prefill_leaves_out_the_tiles_that_see_a_bad_block(dtype, d, heads, n_si
             h = torch.from_numpy(hit).cuda()
             assert bool((out[:, h] == 9.0).all()) and bool((lse[:, h] == 9.0).all()), i
             assert torch.equal(out[:, ~h], good[:, ~h]) and torch.equal(lse[:, ~h], good_lse[:, ~h]), i
+
+
+def strided(x, order, pad):
+    """x in memory with its dimensions in `order`, `pad` elements of NaN after each slice of the second innermost dimension
+    outwards (so strides grow by pad), as a view of x's shape."""
+    dims = [x.shape[i] for i in order]
+    strides, step = [0] * 5, 1
+    for k in reversed(range(5)):
+        strides[order[k]] = step
+        step *= dims[k]
+        if k == 3:
+            step += pad
+    buf = torch.full((step,), float("nan"), dtype=x.dtype, device=x.device)
+    view = buf.as_strided(x.shape, strides)
+    view.copy_(x)
+    return view
+
+
+def same_results(c, G, n_new, change, **kw):
+    """Decode, prompt attention and masses of layer 0 before and after `change` laid the cache or the queries out anew."""
+    res = []
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q0 = torch.randn(c.B, n_new, c.H * G, c.d, generator=g, device="cuda").to(c.dtype)
+    nn = torch.tensor([n_new - 3 * b for b in range(c.B)], dtype=torch.int32, device="cuda")
+    for again in (False, True):
+        q = change(q0) if again else q0
+        out, lse = torch.full_like(q0, 9.0), torch.full((c.B, n_new, c.H * G), 9.0, device="cuda")
+        mass = torch.zeros(c.B * c.L * c.H, c.n_cap, device="cuda")
+        dec = torch.full((c.B, c.H * G, c.d), 9.0, dtype=c.dtype, device="cuda")
+        tri.attn_prefill(c.kv, 0, q, out, n_new=nn, lse=lse, **kw)
+        tri.attn_mass(c.kv, 0, q, lse, mass, n_new=nn, **kw)
+        tri.attn_decode(c.kv, 0, q[:, 0], dec, mass=mass, **kw)
+        c.ok()
+        assert bool((mass.sum(1) > 0).any())
+        res.append((out, lse, mass, dec))
+    for x, y in zip(*res):
+        assert torch.equal(x, y)
+
+
+# blocks, layers, heads, rows, elements: heads outermost, blocks innermost, layers outermost, and blocks that do not follow
+# each other at whole slices or whole rows
+@pytest.mark.parametrize("order", [(0, 1, 2, 3, 4), (2, 0, 1, 3, 4), (2, 1, 0, 3, 4), (1, 0, 2, 3, 4), (1, 2, 0, 3, 4)])
+@pytest.mark.parametrize("pad", ["none", "row", "16 bytes"])
+@pytest.mark.parametrize("d,dtype", [(128, torch.bfloat16), (64, torch.bfloat16), (64, torch.float32)])
+def test_pools_in_any_order(order, pad, d, dtype):
+    for lens, G, n_new, block in (([[300, 270]] * 3, 4, 60, 16), ([[250] * 8] * 4, 3, 240, 256)):
+        c = Case(lens, d, dtype, L=2, block=block)
+
+        def change(q):
+            n = {"none": 0, "row": d, "16 bytes": 16 // q.element_size()}[pad]
+            c.kv.k, c.kv.v = strided(c.kv.k, order, n), strided(c.kv.v, order, n)
+            return q
+
+        same_results(c, G, n_new, change, n_sink=4, window=120)
+
+
+@pytest.mark.parametrize("pad", ["row", "16 bytes"])
+@pytest.mark.parametrize("d,dtype", [(128, torch.bfloat16), (64, torch.bfloat16), (64, torch.float32)])
+def test_slices_at_any_stride(pad, d, dtype):
+    for lens, G, n_new in (([[300, 270]] * 3, 4, 60), ([[250] * 8] * 4, 3, 240)):
+        c = Case(lens, d, dtype, L=2)
+
+        def change(q):
+            n = {"row": d, "16 bytes": 16 // q.element_size()}[pad]
+            c.kv.k, c.kv.v = strided(c.kv.k, (0, 1, 2, 3, 4), n), strided(c.kv.v, (0, 1, 2, 3, 4), n)
+            return q
+
+        same_results(c, G, n_new, change)
