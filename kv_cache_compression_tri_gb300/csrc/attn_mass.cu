@@ -36,35 +36,77 @@ constexpr int FEW = 2;     // query tiles that stay in shared memory
 constexpr int SLOTS = 16;  // lse rows kept by mass_few_kernel (see there)
 constexpr int LSE_ROWS = 16;  // and by mass_many_kernel
 
-// Tensor map of the queries: (element, head, token, sequence), boxes of one
-// 64-element column of a packed tile.
-inline bool encode_queries(CUtensorMap* map, const AttnParams& p, int head_dim, Encode encode) {
-  const int64_t token = static_cast<int64_t>(p.n_kv_heads) * p.group * head_dim;
+// Which tensor map the queries have. A map asks each stride to be a multiple of the one
+// before it that holds the dimension between them, so tokens lie inside sequences or
+// sequences inside tokens; queries at other strides are brought by 16-byte copies.
+enum QueryOrder { Q_COPIED, Q_TOKENS_INSIDE, Q_SEQUENCES_INSIDE };
+struct QueryDims {
+  QueryOrder order;
+  int64_t inner, outer;  // elements between tokens, or sequences: those of the inner dimension first
+};
+inline QueryDims query_dims(const AttnParams& p, int head_dim) {
+  const int64_t token = static_cast<int64_t>(p.n_kv_heads) * p.group * head_dim, seqs = p.q_seq ? p.n_seq : 1;
+  auto fits = [](int64_t outer, int64_t inner, int64_t n) { return outer % inner == 0 && outer / inner >= n; };
+  if (p.n_q == 1 || seqs == 1) {  // (strides of dimensions of one are never used)
+    const int64_t only = p.n_q > 1 ? p.q_token : seqs > 1 ? p.q_seq : token;
+    if (!fits(only, head_dim, p.n_kv_heads * p.group)) return {Q_COPIED, 0, 0};
+    return {Q_TOKENS_INSIDE, only, only * p.n_q};
+  }
+  if (fits(p.q_token, head_dim, p.n_kv_heads * p.group) && fits(p.q_seq, p.q_token, p.n_q)) return {Q_TOKENS_INSIDE, p.q_token, p.q_seq};
+  if (fits(p.q_seq, head_dim, p.n_kv_heads * p.group) && fits(p.q_token, p.q_seq, seqs)) return {Q_SEQUENCES_INSIDE, p.q_seq, p.q_token};
+  return {Q_COPIED, 0, 0};
+}
+// Tensor map of the queries: (element, head, token, sequence) or (element, head, sequence,
+// token), boxes of one 64-element column of a packed tile.
+inline bool encode_queries(CUtensorMap* map, const AttnParams& p, int head_dim, const QueryDims& q, Encode encode) {
+  const bool tokens_inside = q.order == Q_TOKENS_INSIDE;
+  const cuuint64_t seqs = static_cast<cuuint64_t>(p.q_seq ? p.n_seq : 1), tokens = static_cast<cuuint64_t>(p.n_q);
+  const cuuint32_t box_tokens = static_cast<cuuint32_t>(TROWS / p.group);
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(p.n_kv_heads * p.group),
-                              static_cast<cuuint64_t>(p.n_q), static_cast<cuuint64_t>(p.q_seq ? p.n_seq : 1)};
-  // (strides of dimensions of one are never used)
-  const int64_t q_token = p.n_q > 1 ? p.q_token : token, q_seq = dims[3] > 1 ? p.q_seq : token * p.n_q;
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(q_token) * 2,
-                                 static_cast<cuuint64_t>(q_seq) * 2};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(TROWS / p.group), 1};
+                              tokens_inside ? tokens : seqs, tokens_inside ? seqs : tokens};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(q.inner) * 2,
+                                 static_cast<cuuint64_t>(q.outer) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.group), tokens_inside ? box_tokens : 1, tokens_inside ? 1 : box_tokens};
   const cuuint32_t step[4] = {1, 1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.q), dims, strides, box, step,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Query tile `qt` of (seq, h) into the tile at dst, by one thread that expected
-// the bytes of query_bytes<D>() on `bar`; rows past the tile's tokens are not written.
-template <int D>
-__device__ __forceinline__ uint32_t query_bytes(const AttnParams& p) {
-  return static_cast<uint32_t>(TROWS / p.group * p.group * D * 2);
-}
-template <int D>
-__device__ __forceinline__ void load_queries_tma(uint32_t dst, const CUtensorMap* map, const AttnParams& p, int seq, int h, int qt,
-                                                 uint64_t* bar) {
+// Query tiles [qt, qt + n) of a chunk into the tiles at dst, by one warp, arriving once on
+// `bar`. By maps, rows past a tile's tokens are not written.
+template <int D, bool QMAPS>
+__device__ __forceinline__ void load_queries_tc(uint32_t dst, const CUtensorMap* map, bool tokens_inside, const AttnParams& p, const Chunk& c,
+                                                int qt, int n, uint64_t* bar, int lane) {
+  const int tpt = TROWS / p.group;
+  if constexpr (QMAPS) {
+    if (lane == 0) {
+      const int seq = p.q_seq ? c.seq : 0;
+      mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * tpt * p.group * D * 2));
+      for (int i = 0; i < n; ++i) {
+        const int tok = (qt + i) * tpt;
 #pragma unroll
-  for (int a = 0; a < D / 64; ++a)
-    tma_load4(dst + a * TCOL, map, 64 * a, h * p.group, qt * (TROWS / p.group), p.q_seq ? seq : 0, bar);
+        for (int a = 0; a < D / 64; ++a)
+          tma_load4(dst + (i * (D / 64) + a) * TCOL, map, 64 * a, c.h * p.group, tokens_inside ? tok : seq, tokens_inside ? seq : tok, bar);
+      }
+    }
+  } else {
+    constexpr int CH = D / 8;
+    const int G = p.group;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + c.seq * p.q_seq + static_cast<int64_t>(c.h) * G * D;
+#pragma unroll 4
+    for (int i = lane; i < n * TROWS * CH; i += 32) {
+      const int ch = i % CH, u = i / CH % TROWS, tile = i / (TROWS * CH), tok = (qt + tile) * tpt + u / G;
+      const bool live = u < tpt * G && tok < c.n_new;
+      cp_async16(dst + (tile * (D / 64) + (ch >> 3)) * TCOL + u * 128 + (((ch & 7) ^ (u & 7)) << 4),
+                 live ? q + tok * p.q_token + u % G * D + ch * 8 : q, live);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  }
 }
 // -lse in base 2 of a query tile's rows (-inf, so no weight, past its tokens), by
 // a warp: row 32 k + lane in x[k].
@@ -172,10 +214,10 @@ struct MassCtl {
 };
 static_assert(sizeof(MassCtl) <= 256 + SLOTS * FEW * TROWS * 4, "control block");
 
-template <int D, bool MAPS>
+template <int D, bool MAPS, bool QMAPS>
 __global__ void __launch_bounds__(MT, 1)
     mass_many_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
-                     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ RowNumbers rn) {
+                     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ RowNumbers rn, bool tokens_inside) {
   using L = TcMass<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
   MassCtl& ctl = *reinterpret_cast<MassCtl*>(smem + L::CTRL);
@@ -245,10 +287,7 @@ __global__ void __launch_bounds__(MT, 1)
       const int st = cnt % L::NST;
       if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
       if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&ctl.full[st], query_bytes<D>(p));
-        load_queries_tma<D>(ring + st * L::TILE, &qmap, p, c.seq, c.h, qt, &ctl.full[st]);
-      }
+      load_queries_tc<D, QMAPS>(ring + st * L::TILE, &qmap, tokens_inside, p, c, qt, 1, &ctl.full[st], lane);
       __syncwarp();
       ++cnt;
     }
@@ -463,10 +502,10 @@ __device__ __forceinline__ bool warp_blocks_ok(const AttnParams& p, const Chunk&
 // The lse rows of segment g are in slot g % SLOTS. A warpgroup that still reads
 // them when segment g + SLOTS is loaded would have to be a tile more than 12
 // tiles behind the MMAs, and S's four buffers let it fall back by at most 8.
-template <int D, bool MAPS>
+template <int D, bool MAPS, bool QMAPS>
 __global__ void __launch_bounds__(MT, 1)
     mass_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
-                    const __grid_constant__ CUtensorMap qmap, const __grid_constant__ RowNumbers rn) {
+                    const __grid_constant__ CUtensorMap qmap, const __grid_constant__ RowNumbers rn, bool tokens_inside) {
   using L = TcMass<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
   MassCtl& ctl = *reinterpret_cast<MassCtl*>(smem + L::CTRL);
@@ -540,11 +579,7 @@ __global__ void __launch_bounds__(MT, 1)
             for (int k = 0; k < TROWS / 32; ++k) ctl.nl[seg % SLOTS][qt][k * 32 + lane] = x[k];
           }
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&ctl.res_full, n_qt * query_bytes<D>(p));
-            for (int qt = 0; qt < n_qt; ++qt)
-              load_queries_tma<D>(res + qt * L::TILE, &qmap, p, c.seq, c.h, qt, &ctl.res_full);
-          }
+          load_queries_tc<D, QMAPS>(res, &qmap, tokens_inside, p, c, 0, n_qt, &ctl.res_full, lane);
           segs = seg + 1;
           trow = p.rows.seq_table(c.s);
           blk_row = -1;
@@ -646,21 +681,24 @@ __global__ void __launch_bounds__(MT, 1)
 
 template <int D>
 cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
-  CUtensorMap kmap{}, qmap;
+  CUtensorMap kmap{}, qmap{};
   const RowNumbers rn = row_numbers(p);
-  const Encode encode = tensor_map_encode();
-  if (!encode || (rn.maps && !encode_rows(&kmap, p.k, p, D, rn, encode)) || !encode_queries(&qmap, p, D, encode))
+  const QueryDims qd = query_dims(p, D);
+  const bool qmaps = rn.maps && qd.order != Q_COPIED;
+  const Encode encode = rn.maps ? tensor_map_encode() : nullptr;
+  if (rn.maps && (!encode || !encode_rows(&kmap, p.k, p, D, rn, encode) || (qmaps && !encode_queries(&qmap, p, D, qd, encode))))
     return cudaErrorInvalidValue;
   const int tpt = TROWS / p.group, n_qt = (p.n_q + tpt - 1) / tpt;
   const bool few = n_qt <= FEW;
-  auto kern = rn.maps ? (few ? mass_few_kernel<D, true> : mass_many_kernel<D, true>)
-                      : (few ? mass_few_kernel<D, false> : mass_many_kernel<D, false>);
+  auto kern = qmaps     ? (few ? mass_few_kernel<D, true, true> : mass_many_kernel<D, true, true>)
+              : rn.maps ? (few ? mass_few_kernel<D, true, false> : mass_many_kernel<D, true, false>)
+                        : (few ? mass_few_kernel<D, false, false> : mass_many_kernel<D, false, false>);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcMass<D>::BYTES);
   if (e != cudaSuccess) return e;
   const int64_t n_ls = static_cast<int64_t>(p.n_seq) * p.n_kv_heads, tiles = (p.n_cap + TROWS - 1) / TROWS;
   const int64_t ctas = few ? min(static_cast<int64_t>(SMS), n_ls * tiles) : n_ls * ((tiles + 1) / 2);
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  kern<<<static_cast<unsigned>(ctas), MT, TcMass<D>::BYTES, st>>>(p, kmap, qmap, rn);
+  kern<<<static_cast<unsigned>(ctas), MT, TcMass<D>::BYTES, st>>>(p, kmap, qmap, rn, qd.order == Q_TOKENS_INSIDE);
   note_launch();
   return cudaGetLastError();
 }

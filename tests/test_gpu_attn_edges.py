@@ -288,3 +288,68 @@ def test_slices_at_any_stride(pad, d, dtype):
             return q
 
         same_results(c, G, n_new, change)
+
+
+# strides between sequences and tokens in units of a token's heads, and elements more
+QUERIES = [
+    (lambda B, T: (1, B), 0, 0),  # sequences inside tokens
+    (lambda B, T: (2, 2 * B), 0, 0),
+    (lambda B, T: (T, 1), 64, 0),  # sequences that are not whole tokens apart
+    (lambda B, T: (T, 1), 8, 0),
+    (lambda B, T: (2 * T, 2), 0, 8),  # tokens that are not whole rows apart
+    (lambda B, T: (1, B + 1), 8, 8),
+    (lambda B, T: (5, 1), 0, 0),  # sequences that share tokens
+]
+
+
+@pytest.mark.parametrize("case", range(len(QUERIES)))
+@pytest.mark.parametrize("d,dtype", [(128, torch.bfloat16), (64, torch.bfloat16), (64, torch.float32)])
+def test_queries_at_any_stride(case, d, dtype):
+    units, seq_more, token_more = QUERIES[case]
+    for lens, G, n_new in (([[300, 270]] * 3, 4, 60), ([[250] * 8] * 4, 3, 240), ([[70, 80]] * 3, 2, 10)):
+        c = Case(lens, d, dtype, L=1)
+
+        def change(q):
+            B, T, Hq, _ = q.shape
+            us, ut = units(B, T)
+            ss, st = us * Hq * d + seq_more, ut * Hq * d + token_more
+            if (us, ut) == (2 * T, 2):
+                ss = us * (Hq * d + token_more) + seq_more
+            buf = torch.full(((B - 1) * ss + (T - 1) * st + Hq * d,), float("nan"), dtype=q.dtype, device="cuda")
+            view = buf.as_strided(q.shape, (ss, st, d, 1))
+            if case == len(QUERIES) - 1:
+                buf.copy_(torch.randn(buf.shape, generator=c.g, device="cuda"))
+            else:
+                view.copy_(q)
+            return view
+
+        if case == len(QUERIES) - 1:
+            same_queries(c, G, n_new, change(torch.empty(c.B, n_new, c.H * G, d, dtype=dtype, device="cuda")))
+        else:
+            same_results(c, G, n_new, change)
+            same_results(c, G, n_new, change, n_sink=4, window=50)
+
+
+def same_queries(c, G, n_new, q):
+    """Queries in memory of any kind give what their copy gives."""
+    res = []
+    for x in (q.contiguous(), q):
+        out, lse = torch.empty(x.shape, dtype=x.dtype, device="cuda"), torch.empty(x.shape[:3], device="cuda")
+        mass = torch.zeros(c.B * c.L * c.H, c.n_cap, device="cuda")
+        dec = torch.empty(c.B, c.H * G, c.d, dtype=c.dtype, device="cuda")
+        tri.attn_prefill(c.kv, 0, x, out, lse=lse)
+        tri.attn_mass(c.kv, 0, x, lse, mass)
+        tri.attn_decode(c.kv, 0, x[:, 0], dec, mass=mass)
+        c.ok()
+        res.append((out, lse, mass, dec))
+    for x, y in zip(*res):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_query_of_each_sequence(d):
+    """One token per sequence, sequences at any stride, through the calls for chunks."""
+    c = Case([[300, 270], [5, 0], [129, 128]], d, torch.bfloat16, L=1)
+    for more in (0, 8, 6 * d):
+        buf = torch.randn(3 * (6 * d + more), generator=c.g, device="cuda").to(torch.bfloat16)
+        same_queries(c, 3, 1, buf.as_strided((3, 1, 6, d), (6 * d + more, 6 * d, d, 1)))
