@@ -163,6 +163,19 @@ def _stream(stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    """Memory for a call on `stream` (None: the current one), from that stream's own: the current
+    stream's may still be in use there, and be handed out there again before the call has run."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(nbytes: int, device, stream=None) -> torch.Tensor:
+    return _empty(max(nbytes, 16), torch.uint8, device, stream)
+
+
 def _ptr(t: torch.Tensor | None) -> int | None:
     if t is None:
         return None
@@ -328,11 +341,13 @@ def calibrate_centers(q: torch.Tensor, group: int, style: int = ROPE_INTERLEAVED
     assert q.is_cuda and q.is_contiguous() and q.dtype in _DTYPES
     H, F = Hq // group, d // 2
     if out is None:
-        out = Centers(torch.empty(L * H, F, 2, device=q.device), torch.empty(L * H, F, device=q.device),
-                      torch.empty(L * H, F, device=q.device))
+        out = Centers(*(_empty(shape, torch.float32, q.device, stream) for shape in ((L * H, F, 2), (L * H, F), (L * H, F))))
+        if stream is not None:  # read on the current stream later on
+            for t in (out.center, out.mean_norm, out.mrl):
+                t.record_stream(torch.cuda.current_stream())
     ws_bytes = calibrate_workspace_bytes(L, Hq, group, d, n_tok)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(ws_bytes, q.device, stream)
     assert workspace.numel() >= ws_bytes
     _check("tri_calibrate_centers", lib.tri_calibrate_centers(
         q.data_ptr(), _DTYPES[q.dtype], L, Hq, group, d, n_tok, style, out._abi(),
@@ -443,7 +458,7 @@ def compress(kv: KVCache, centers: Centers, rope_theta: float, offsets, p_cur: t
     kvs, cs = kv._abi(), centers._abi()
     need = int(lib.tri_compress_workspace_bytes(ctypes.byref(kvs)))
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=kv.device)
+        workspace = _scratch(need, kv.device, stream)
     assert workspace.numel() >= need
     _check("tri_compress", lib.tri_compress(ctypes.byref(kvs), ctypes.byref(cs), float(rope_theta), style,
                                             norm_mode, ctypes.cast(offs, ctypes.c_void_p), len(offsets),
@@ -472,7 +487,7 @@ def score_heads(kv: KVCache, centers: Centers, group: int, rope_theta: float, of
     kvs, cs = kv._abi(), centers._abi()
     need = int(lib.tri_score_heads_workspace_bytes(ctypes.byref(kvs), group))
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=kv.device)
+        workspace = _scratch(need, kv.device, stream)
     assert workspace.numel() >= need
     _check("tri_score_heads", lib.tri_score_heads(
         ctypes.byref(kvs), ctypes.byref(cs), group, float(rope_theta), style, norm_mode,
@@ -514,7 +529,7 @@ def select_union(scores: torch.Tensor, kv: KVCache, n_prompt: int, n_recent: int
     kvs = kv._abi()
     need = int(lib.tri_select_union_workspace_bytes(ctypes.byref(kvs), n_prompt, n_recent, k_head))
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=kv.device)
+        workspace = _scratch(need, kv.device, stream)
     assert workspace.numel() >= need
     if final_scores is not None:
         assert final_scores.dtype == torch.float32 and final_scores.is_contiguous()
@@ -570,9 +585,7 @@ def attn_decode(kv, layer: int, q: torch.Tensor, out: torch.Tensor, n_new: torch
         _check_mass(kvs, mass)
     if workspace is None:
         need = int(lib.tri_attn_decode_workspace_bytes(ctypes.byref(kvs), qs.group, int(mass is not None)))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=kv.device)
-        if stream is not None:
-            workspace.record_stream(stream)  # not handed out again before the call has run
+        workspace = _scratch(need, kv.device, stream)
     assert workspace.is_cuda and workspace.is_contiguous()
     _check("tri_attn_decode", lib.tri_attn_decode(ctypes.byref(kvs), ctypes.byref(qs), out.data_ptr(), _ptr(lse),
                                                   _ptr(mass), workspace.data_ptr(), workspace.nbytes, _stream(stream)))

@@ -353,3 +353,30 @@ def test_one_query_of_each_sequence(d):
     for more in (0, 8, 6 * d):
         buf = torch.randn(3 * (6 * d + more), generator=c.g, device="cuda").to(torch.bfloat16)
         same_queries(c, 3, 1, buf.as_strided((3, 1, 6, d), (6 * d + more, 6 * d, d, 1)))
+
+
+def test_default_workspaces_are_the_streams_own():
+    """A call on a stream other than the current one, with no workspace given: its scratch may not be memory that the
+    current stream's pending work still writes."""
+    c = Case([[30000, 20001]], 128, torch.bfloat16, L=1)
+    q = torch.randn(1, 8, 128, generator=c.g, device="cuda").to(torch.bfloat16)
+    want, want_m = torch.empty_like(q), torch.zeros(2, c.n_cap, device="cuda")
+    tri.attn_decode(c.kv, 0, q, want, mass=want_m)
+    need = tri.attn_decode_workspace_bytes(c.kv, 4, True)
+    side, busy = torch.cuda.Stream(), torch.randn(8192, 8192, device="cuda").to(torch.bfloat16)
+    product = torch.empty_like(busy)
+    outs = [(torch.empty_like(q), torch.zeros(2, c.n_cap, device="cuda")) for _ in range(20)]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    scratch = torch.empty(need, dtype=torch.uint8, device="cuda")  # the workspace's size, in use on the current stream ...
+    for _ in range(40):  # (the host is ahead of the GPU from here on)
+        torch.mm(busy, busy, out=product)
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(2000):
+        scratch.fill_(255)
+    del scratch  # ... and still to be written when its memory is free to the current stream's next tensor
+    for out, mass in outs:
+        tri.attn_decode(c.kv, 0, q, out, mass=mass, stream=side)
+    torch.cuda.synchronize()
+    for out, mass in outs:
+        assert torch.equal(out, want) and torch.equal(mass, want_m)
