@@ -380,3 +380,52 @@ def test_default_workspaces_are_the_streams_own():
     torch.cuda.synchronize()
     for out, mass in outs:
         assert torch.equal(out, want) and torch.equal(mass, want_m)
+
+
+@pytest.mark.parametrize("n_sink,window", [(0, 1), (0, 33), (4, 1), (4, 60), (70, 65), (1000, 3)])
+@pytest.mark.parametrize("block", [0, 16, 64])
+@pytest.mark.parametrize("d,dtype", [(64, torch.float32), (128, torch.float32), (64, torch.bfloat16)])
+def test_prefill_and_mass_sinks_and_window(n_sink, window, block, d, dtype):
+    check_prefill(Case([[200, 150], [70, 90]], d, dtype, L=1, block=block), 3, [66, 20], layer=0, n_sink=n_sink, window=window)
+
+
+@pytest.mark.parametrize("block", [0, 64])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_offsets_past_32_bits(block, dtype):
+    """The last slices of a cache of more than 4 GB each of K and V give what a cache of those slices alone gives."""
+    H, n, d, G = 2, 300, 128, 4
+    c = Case([[n, n - 7]], d, dtype, L=1, block=block)
+    per = c.n_cap
+    elem = 2 if dtype == torch.bfloat16 else 4
+    slices = (1 << 32) // (per * d * elem) + 50
+    if block:
+        nb, blocks = c.kv.k.shape[0], slices * per // (block * H)
+        big = [torch.empty(blocks, 1, H, block, d, dtype=dtype, device="cuda") for _ in range(2)]
+        for x, y in zip(big, (c.kv.k, c.kv.v)):
+            x[blocks - nb:] = y
+        kv = tri.PagedKVCache(*big, c.kv.block_table + (blocks - nb), c.kv.n_valid, c.kv.pos, c.kv.pos_out, c.status, post_rope=True)
+        layer = 0
+    else:
+        L = slices // H
+        big = [torch.empty(1, L, H, per, d, dtype=dtype, device="cuda") for _ in range(2)]
+        for x, y in zip(big, (c.kv.k, c.kv.v)):
+            x[:, L - 1:] = y
+        nv = torch.zeros(L * H, dtype=torch.int32, device="cuda")
+        nv[-H:] = c.kv.n_valid
+        kv = tri.KVCache(*big, nv, None, None, c.status, post_rope=True)
+        layer = L - 1
+    assert big[0].numel() * elem > 1 << 32
+    q = torch.randn(1, 70, H * G, d, generator=c.g, device="cuda").to(dtype)
+    res = []
+    for cache, lay in ((c.kv, 0), (kv, layer)):
+        out, lse = torch.empty_like(q), torch.empty(1, 70, H * G, device="cuda")
+        mass = torch.zeros(cache.n_slices, per, device="cuda")
+        dec = torch.empty(1, H * G, d, dtype=dtype, device="cuda")
+        tri.attn_prefill(cache, lay, q, out, lse=lse)
+        tri.attn_mass(cache, lay, q, lse, mass)
+        tri.attn_mass(cache, lay, q[:, -8:], lse[:, -8:], mass)
+        tri.attn_decode(cache, lay, q[:, 69], dec, mass=mass)
+        c.ok()
+        res.append((out, lse, mass[-H:], dec))
+    for x, y in zip(*res):
+        assert torch.equal(x, y)
