@@ -403,6 +403,7 @@ tri_status tri_select_union(const float* scores, const tri_kv* kv, int32_t n_pro
  * must be finite for tri_attn_prefill (a weight of 0 multiplies them there).
  * A pool's blocks that no query of a sequence sees may be gone: their table
  * entries may be anything, and no row of such a block is read into a result.
+ * An infinite V element of a row that a query sees gives infinity or NaN.
  *
  * Keys are taken as cached, so they must be TRI_KEYS_POST_ROPE and q rotated
  * in the same way (TRI_ERR_UNSUPPORTED otherwise). Sums, maxima and lse are
@@ -441,7 +442,9 @@ tri_status tri_attn_decode(const tri_kv* kv, const tri_queries* q, void* out, fl
  * one). out: device [n_seq][n_q][n_kv_heads * group][head_dim] of the cache's
  * type, 16-byte aligned; lse: optional device [n_seq][n_q][n_kv_heads * group]
  * fp32. bf16 caches: the weights are rounded to bf16 for their product with V
- * (their sum is not). A sequence with a fault in its row count or n_new is
+ * (their sum is not), or to a pair of bf16 in calls of so few query tiles that
+ * the product is not what they wait for: the same tokens in a larger call may
+ * differ by that rounding. A sequence with a fault in its row count or n_new is
  * skipped. The queries that see a row of a bad table entry are left out, with
  * the tokens next to them: tokens go in tiles of 128 / group from token 0 on
  * (fp32: 64 / group), and a tile is written or left out as a whole. */

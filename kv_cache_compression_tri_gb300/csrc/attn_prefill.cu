@@ -31,7 +31,10 @@
 // most SMs idle: then a cluster of CTAs shares a pair of query tiles, each takes a
 // run of the cached rows, and they join through their shared memories. The
 // tensor cores are not what bounds such a call, so the weights go in as a bf16 pair
-// (p rounded, and the rest rounded) instead of rounded once.
+// (p rounded, and the rest rounded) instead of rounded once. In a large call the pair would
+// cost a third of the time (8192-token prompt 380 -> 505 us, 8 prompts at d 64 with a window 175
+// -> 206) for an rms error of 1.11e-4 instead of 1.47e-4, of which the output's own bf16
+// rounding is 1.11e-4: there p is rounded once.
 // Steps at the edge of what the rows see are masked by position; rows of V past
 // the last query's are set to zero in shared memory, whatever they hold.
 //
