@@ -36,10 +36,12 @@ constexpr int FEW = 2;     // query tiles that stay in shared memory
 constexpr int SLOTS = 16;  // lse rows kept by mass_few_kernel (see there)
 constexpr int LSE_ROWS = 16;  // and by mass_many_kernel
 
-// Which tensor map the queries have. A map asks each stride to be a multiple of the one
-// before it that holds the dimension between them, so tokens lie inside sequences or
-// sequences inside tokens; queries at other strides are brought by 16-byte copies.
-enum QueryOrder { Q_COPIED, Q_TOKENS_INSIDE, Q_SEQUENCES_INSIDE };
+// Which tensor maps the queries have. A map asks each stride to be a multiple of the one
+// before it that holds the dimension between them, so (element, head, token, sequence) has
+// tokens inside sequences, or the other way round, and a box of it is a column of a packed
+// tile. Queries at other strides are rows by number, a box for each token's heads (weights of a
+// 4096-token prompt: 298 us, by columns 76; a warp issues the boxes one lane at a time).
+enum QueryOrder { Q_ROWS, Q_TOKENS_INSIDE, Q_SEQUENCES_INSIDE };
 struct QueryDims {
   QueryOrder order;
   int64_t inner, outer;  // elements between tokens, or sequences: those of the inner dimension first
@@ -49,16 +51,14 @@ inline QueryDims query_dims(const AttnParams& p, int head_dim) {
   auto fits = [](int64_t outer, int64_t inner, int64_t n) { return outer % inner == 0 && outer / inner >= n; };
   if (p.n_q == 1 || seqs == 1) {  // (strides of dimensions of one are never used)
     const int64_t only = p.n_q > 1 ? p.q_token : seqs > 1 ? p.q_seq : token;
-    if (!fits(only, head_dim, p.n_kv_heads * p.group)) return {Q_COPIED, 0, 0};
+    if (!fits(only, head_dim, p.n_kv_heads * p.group)) return {Q_ROWS, 0, 0};
     return {Q_TOKENS_INSIDE, only, only * p.n_q};
   }
   if (fits(p.q_token, head_dim, p.n_kv_heads * p.group) && fits(p.q_seq, p.q_token, p.n_q)) return {Q_TOKENS_INSIDE, p.q_token, p.q_seq};
   if (fits(p.q_seq, head_dim, p.n_kv_heads * p.group) && fits(p.q_token, p.q_seq, seqs)) return {Q_SEQUENCES_INSIDE, p.q_seq, p.q_token};
-  return {Q_COPIED, 0, 0};
+  return {Q_ROWS, 0, 0};
 }
-// Tensor map of the queries: (element, head, token, sequence) or (element, head, sequence,
-// token), boxes of one 64-element column of a packed tile.
-inline bool encode_queries(CUtensorMap* map, const AttnParams& p, int head_dim, const QueryDims& q, Encode encode) {
+inline bool encode_queries(RowMaps<false>& map, const AttnParams& p, int head_dim, const QueryDims& q, Encode encode) {
   const bool tokens_inside = q.order == Q_TOKENS_INSIDE;
   const cuuint64_t seqs = static_cast<cuuint64_t>(p.q_seq ? p.n_seq : 1), tokens = static_cast<cuuint64_t>(p.n_q);
   const cuuint32_t box_tokens = static_cast<cuuint32_t>(TROWS / p.group);
@@ -68,44 +68,41 @@ inline bool encode_queries(CUtensorMap* map, const AttnParams& p, int head_dim, 
                                  static_cast<cuuint64_t>(q.outer) * 2};
   const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.group), tokens_inside ? box_tokens : 1, tokens_inside ? 1 : box_tokens};
   const cuuint32_t step[4] = {1, 1, 1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.q), dims, strides, box, step,
+  return encode(&map.m[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.q), dims, strides, box, step,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+inline bool encode_queries(RowMaps<true>& maps, const AttnParams& p, int head_dim, const QueryDims&, Encode encode) {
+  const int64_t elements = (p.n_seq - 1) * p.q_seq + (p.n_q - 1) * p.q_token + static_cast<int64_t>(p.n_kv_heads) * p.group * head_dim;
+  return encode_row_maps(maps, p.q, elements * 2, head_dim, p.group, encode);
+}
 
 // Query tiles [qt, qt + n) of a chunk into the tiles at dst, by one warp, arriving once on
-// `bar`. By maps, rows past a tile's tokens are not written.
-template <int D, bool QMAPS>
-__device__ __forceinline__ void load_queries_tc(uint32_t dst, const CUtensorMap* map, bool tokens_inside, const AttnParams& p, const Chunk& c,
-                                                int qt, int n, uint64_t* bar, int lane) {
-  const int tpt = TROWS / p.group;
-  if constexpr (QMAPS) {
-    if (lane == 0) {
-      const int seq = p.q_seq ? c.seq : 0;
-      mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * tpt * p.group * D * 2));
-      for (int i = 0; i < n; ++i) {
-        const int tok = (qt + i) * tpt;
-#pragma unroll
-        for (int a = 0; a < D / 64; ++a)
-          tma_load4(dst + (i * (D / 64) + a) * TCOL, map, 64 * a, c.h * p.group, tokens_inside ? tok : seq, tokens_inside ? seq : tok, bar);
-      }
-    }
-  } else {
-    constexpr int CH = D / 8;
-    const int G = p.group;
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + c.seq * p.q_seq + static_cast<int64_t>(c.h) * G * D;
-#pragma unroll 4
-    for (int i = lane; i < n * TROWS * CH; i += 32) {
-      const int ch = i % CH, u = i / CH % TROWS, tile = i / (TROWS * CH), tok = (qt + tile) * tpt + u / G;
-      const bool live = u < tpt * G && tok < c.n_new;
-      cp_async16(dst + (tile * (D / 64) + (ch >> 3)) * TCOL + u * 128 + (((ch & 7) ^ (u & 7)) << 4),
-                 live ? q + tok * p.q_token + u % G * D + ch * 8 : q, live);
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    fence_proxy_async_smem();
+// `bar`. Rows past the tokens of a tile's box, or of the chunk, are not written.
+template <int D, bool QROWS>
+__device__ __forceinline__ void load_queries_tma(uint32_t dst, const RowMaps<QROWS>& maps, bool tokens_inside, const AttnParams& p, const Chunk& c,
+                                                 int qt, int n, uint64_t* bar, int lane) {
+  constexpr int COLS = D / 64;
+  const int tpt = TROWS / p.group, tok0 = qt * tpt;
+  if constexpr (QROWS) {
+    const int toks = min(n * tpt, c.n_new - tok0);
+    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(toks * p.group * D * 2));
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
+    for (int i = lane; i < toks * COLS; i += 32) {
+      const int col = i % COLS, tok = i / COLS, tile = tok / tpt;
+      const int64_t at = (c.seq * p.q_seq + (tok0 + tok) * p.q_token) / 8 + c.h * p.group * (D / 8);  // 16-byte units
+      tma_load2(dst + (tile * COLS + col) * TCOL + (tok - tile * tpt) * p.group * 128, &maps.m[at % (D / 8)], 64 * col,
+                static_cast<int>(at / (D / 8)), bar);
+    }
+  } else if (lane == 0) {
+    const int seq = p.q_seq ? c.seq : 0;
+    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * tpt * p.group * D * 2));
+    for (int i = 0; i < n; ++i) {
+      const int tok = tok0 + i * tpt;
+#pragma unroll
+      for (int a = 0; a < COLS; ++a)
+        tma_load4(dst + (i * COLS + a) * TCOL, &maps.m[0], 64 * a, c.h * p.group, tokens_inside ? tok : seq, tokens_inside ? seq : tok, bar);
+    }
   }
 }
 // -lse in base 2 of a query tile's rows (-inf, so no weight, past its tokens), by
@@ -214,10 +211,10 @@ struct MassCtl {
 };
 static_assert(sizeof(MassCtl) <= 256 + SLOTS * FEW * TROWS * 4, "control block");
 
-template <int D, bool MAPS, bool QMAPS>
+template <int D, bool ODD, bool QROWS>
 __global__ void __launch_bounds__(MT, 1)
-    mass_many_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
-                     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ RowNumbers rn, bool tokens_inside) {
+    mass_many_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ RowMaps<ODD> kmap,
+                     const __grid_constant__ RowMaps<QROWS> qmap, const __grid_constant__ RowNumbers rn, bool tokens_inside) {
   using L = TcMass<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
   MassCtl& ctl = *reinterpret_cast<MassCtl*>(smem + L::CTRL);
@@ -278,8 +275,7 @@ __global__ void __launch_bounds__(MT, 1)
     const LaneBox<D> box(rn, lane);
     for (int kt = 0; kt < nk; ++kt) {
       const int blk = tile_block<D>(p, rn.box_rows, trow, c.seq, k_of(kt), c.n, lane);
-      load_tile<D, MAPS>(res + kt * L::TILE, &kmap, p.k, p, rn, box, box_place<D, MAPS>(rn, box, blk, c.h, k_of(kt)), c.seq, c.h, k_of(kt),
-                         &ctl.res_full, lane);
+      load_tile<D, ODD>(res + kt * L::TILE, kmap, box, box_place<D, ODD>(rn, box, blk, c.h, k_of(kt)), &ctl.res_full, lane);
     }
     int cnt = 0;
     for (int qt = 0; qt < n_qt && ok; ++qt) {
@@ -287,7 +283,7 @@ __global__ void __launch_bounds__(MT, 1)
       const int st = cnt % L::NST;
       if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
       if (!ok) break;
-      load_queries_tc<D, QMAPS>(ring + st * L::TILE, &qmap, tokens_inside, p, c, qt, 1, &ctl.full[st], lane);
+      load_queries_tma<D, QROWS>(ring + st * L::TILE, qmap, tokens_inside, p, c, qt, 1, &ctl.full[st], lane);
       __syncwarp();
       ++cnt;
     }
@@ -502,10 +498,10 @@ __device__ __forceinline__ bool warp_blocks_ok(const AttnParams& p, const Chunk&
 // The lse rows of segment g are in slot g % SLOTS. A warpgroup that still reads
 // them when segment g + SLOTS is loaded would have to be a tile more than 12
 // tiles behind the MMAs, and S's four buffers let it fall back by at most 8.
-template <int D, bool MAPS, bool QMAPS>
+template <int D, bool ODD, bool QROWS>
 __global__ void __launch_bounds__(MT, 1)
-    mass_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
-                    const __grid_constant__ CUtensorMap qmap, const __grid_constant__ RowNumbers rn, bool tokens_inside) {
+    mass_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ RowMaps<ODD> kmap,
+                    const __grid_constant__ RowMaps<QROWS> qmap, const __grid_constant__ RowNumbers rn, bool tokens_inside) {
   using L = TcMass<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
   MassCtl& ctl = *reinterpret_cast<MassCtl*>(smem + L::CTRL);
@@ -579,7 +575,7 @@ __global__ void __launch_bounds__(MT, 1)
             for (int k = 0; k < TROWS / 32; ++k) ctl.nl[seg % SLOTS][qt][k * 32 + lane] = x[k];
           }
           __syncwarp();
-          load_queries_tc<D, QMAPS>(res, &qmap, tokens_inside, p, c, 0, n_qt, &ctl.res_full, lane);
+          load_queries_tma<D, QROWS>(res, qmap, tokens_inside, p, c, 0, n_qt, &ctl.res_full, lane);
           segs = seg + 1;
           trow = p.rows.seq_table(c.s);
           blk_row = -1;
@@ -587,13 +583,13 @@ __global__ void __launch_bounds__(MT, 1)
         [&](int, const Chunk& c, int, int k0) {
           const int st = cnt % L::NST;
           if (blk_row != k0) blk = tile_block<D>(p, rn.box_rows, trow, c.seq, k0, c.n, lane);
-          const int place = box_place<D, MAPS>(rn, box, blk, c.h, k0);
+          const Place place = box_place<D, ODD>(rn, box, blk, c.h, k0);
           // (the next tile's is on its way while this one waits for its stage)
           blk_row = k0 + TROWS;
           const int blk_next = tile_block<D>(p, rn.box_rows, trow, c.seq, blk_row, c.n, lane);
           if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
           if (!ok) return;
-          load_tile<D, MAPS>(ring + st * L::TILE, &kmap, p.k, p, rn, box, place, c.seq, c.h, k0, &ctl.full[st], lane);
+          load_tile<D, ODD>(ring + st * L::TILE, kmap, box, place, &ctl.full[st], lane);
           blk = blk_next;
           ++cnt;
         },
@@ -679,20 +675,15 @@ __global__ void __launch_bounds__(MT, 1)
   if (w == 1) tmem_dealloc(tm, 512);
 }
 
-template <int D>
-cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
-  CUtensorMap kmap{}, qmap{};
-  const RowNumbers rn = row_numbers(p);
-  const QueryDims qd = query_dims(p, D);
-  const bool qmaps = rn.maps && qd.order != Q_COPIED;
-  const Encode encode = rn.maps ? tensor_map_encode() : nullptr;
-  if (rn.maps && (!encode || !encode_rows(&kmap, p.k, p, D, rn, encode) || (qmaps && !encode_queries(&qmap, p, D, qd, encode))))
-    return cudaErrorInvalidValue;
+template <int D, bool ODD, bool QROWS>
+cudaError_t launch_tc(const AttnParams& p, const RowNumbers& rn, const QueryDims& qd, cudaStream_t st) {
+  RowMaps<ODD> kmap;
+  RowMaps<QROWS> qmap;
+  const Encode encode = tensor_map_encode();
+  if (!encode || !encode_rows(kmap, p.k, p, D, rn, encode) || !encode_queries(qmap, p, D, qd, encode)) return cudaErrorInvalidValue;
   const int tpt = TROWS / p.group, n_qt = (p.n_q + tpt - 1) / tpt;
   const bool few = n_qt <= FEW;
-  auto kern = qmaps     ? (few ? mass_few_kernel<D, true, true> : mass_many_kernel<D, true, true>)
-              : rn.maps ? (few ? mass_few_kernel<D, true, false> : mass_many_kernel<D, true, false>)
-                        : (few ? mass_few_kernel<D, false, false> : mass_many_kernel<D, false, false>);
+  auto kern = few ? mass_few_kernel<D, ODD, QROWS> : mass_many_kernel<D, ODD, QROWS>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcMass<D>::BYTES);
   if (e != cudaSuccess) return e;
   const int64_t n_ls = static_cast<int64_t>(p.n_seq) * p.n_kv_heads, tiles = (p.n_cap + TROWS - 1) / TROWS;
@@ -701,6 +692,18 @@ cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
   kern<<<static_cast<unsigned>(ctas), MT, TcMass<D>::BYTES, st>>>(p, kmap, qmap, rn, qd.order == Q_TOKENS_INSIDE);
   note_launch();
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_bf16(const AttnParams& p, cudaStream_t st) {
+  RowNumbers rn{};
+  if (!row_numbers(p, rn)) return cudaErrorNotSupported;
+  const QueryDims qd = query_dims(p, D);
+  if (qd.order == Q_ROWS) {
+    if ((p.n_seq - 1) * p.q_seq + (p.n_q - 1) * p.q_token > static_cast<int64_t>(0x7fffffff - 2 * TROWS) * D) return cudaErrorNotSupported;
+    return rn.odd ? launch_tc<D, true, true>(p, rn, qd, st) : launch_tc<D, false, true>(p, rn, qd, st);
+  }
+  return rn.odd ? launch_tc<D, true, false>(p, rn, qd, st) : launch_tc<D, false, false>(p, rn, qd, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -781,7 +784,7 @@ cudaError_t launch_fp32(const AttnParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attn_mass(const AttnParams& p, tri_dtype dt, int head_dim, cudaStream_t st) {
-  if (dt == TRI_BF16) return head_dim == 64 ? launch_tc<64>(p, st) : launch_tc<128>(p, st);
+  if (dt == TRI_BF16) return head_dim == 64 ? launch_bf16<64>(p, st) : launch_bf16<128>(p, st);
   return head_dim == 64 ? launch_fp32<64>(p, st) : launch_fp32<128>(p, st);
 }
 

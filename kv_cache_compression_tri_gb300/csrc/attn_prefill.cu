@@ -127,10 +127,10 @@ __device__ __forceinline__ float weights_of(const uint32_t (&x)[32], float sl, f
   return (l0 + l1) + (l2 + l3);
 }
 
-template <int D, int NQ, bool FEW_CTAS, bool MAPS>
+template <int D, int NQ, bool FEW_CTAS, bool ODD>
 __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
-    prefill_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
-                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ RowNumbers rn, int n_tiles, int cluster) {
+    prefill_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ RowMaps<ODD> kmap,
+                      const __grid_constant__ RowMaps<ODD> vmap, const __grid_constant__ RowNumbers rn, int n_tiles, int cluster) {
   using L = TcSmem<D, NQ>;
   const int splits = FEW_CTAS ? cluster : 1;
   extern __shared__ __align__(1024) unsigned char smem[];  // (the swizzle goes by address)
@@ -226,8 +226,9 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
       return blk;
     };
     const LaneBox<D> box(rn, lane);
-    auto place_of = [&](int blk, int k0) { return box_place<D, MAPS>(rn, box, blk, c.h, k0); };
-    int place = n_list ? place_of(block_of(tile_row(0)), tile_row(0)) : 0, blk_next = 0;
+    auto place_of = [&](int blk, int k0) { return box_place<D, ODD>(rn, box, blk, c.h, k0); };
+    int blk_next = n_list ? block_of(tile_row(0)) : 0;
+    Place place = n_list ? place_of(blk_next, tile_row(0)) : Place{0, 0};
     for (; cnt < 2 * n_list && ok; ++cnt) {
       const int st = cnt % L::NST, k0 = tile_row(cnt >> 1);
       if (!(cnt & 1) && cnt + 2 < 2 * n_list)  // (on its way while this tile waits for its stage)
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
       if (bad & 1) ctl.flag[0] = 1;
       if (bad & 2) ctl.flag[1] = 1;
       __syncwarp();
-      load_tile<D, MAPS>(ring + st * L::TILE, is_v ? &vmap : &kmap, is_v ? p.v : p.k, p, rn, box, place, c.seq, c.h, k0, bar, lane);
+      load_tile<D, ODD>(ring + st * L::TILE, is_v ? vmap : kmap, box, place, bar, lane);
       if (is_v && cnt + 1 < 2 * n_list) place = place_of(blk_next, tile_row((cnt >> 1) + 1));
       if (fix) {
         ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.v_fix, 0));
@@ -536,13 +537,11 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
   if (w == 1) tmem_dealloc(tm, L::TMEM);
 }
 
-template <int D>
-cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
-  CUtensorMap kmap{}, vmap{};
-  const RowNumbers rn = row_numbers(p);
-  const Encode encode = rn.maps ? tensor_map_encode() : nullptr;
-  if (rn.maps && (!encode || !encode_rows(&kmap, p.k, p, D, rn, encode) || !encode_rows(&vmap, p.v, p, D, rn, encode)))
-    return cudaErrorInvalidValue;
+template <int D, bool ODD>
+cudaError_t launch_tc(const AttnParams& p, const RowNumbers& rn, cudaStream_t st) {
+  RowMaps<ODD> kmap, vmap;
+  const Encode encode = tensor_map_encode();
+  if (!encode || !encode_rows(kmap, p.k, p, D, rn, encode) || !encode_rows(vmap, p.v, p, D, rn, encode)) return cudaErrorInvalidValue;
   // one or two query tiles per CTA: at d 64 two CTAs with a tile each fit an SM, and one's
   // start and end hide behind the other's work (8 padded prompts of up to 4096 tokens, sinks
   // and a window of 1000: 189 us, with two tiles per CTA 199)
@@ -556,8 +555,7 @@ cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
   const bool few = units * 2 <= SMS;
   int splits = 1;
   while (few && splits < MAX_SPLITS && units * splits * 2 <= SMS && rows >= 2 * splits * 2 * TROWS) splits *= 2;
-  auto kern = rn.maps ? (few ? prefill_tc_kernel<D, NQ, true, true> : prefill_tc_kernel<D, NQ, false, true>)
-                      : (few ? prefill_tc_kernel<D, NQ, true, false> : prefill_tc_kernel<D, NQ, false, false>);
+  auto kern = few ? prefill_tc_kernel<D, NQ, true, ODD> : prefill_tc_kernel<D, NQ, false, ODD>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D, NQ>::BYTES);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -692,7 +690,12 @@ cudaError_t launch_fp32(const AttnParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attn_prefill(const AttnParams& p, tri_dtype dt, int head_dim, cudaStream_t st) {
-  if (dt == TRI_BF16) return head_dim == 64 ? launch_tc<64>(p, st) : launch_tc<128>(p, st);
+  if (dt == TRI_BF16) {
+    RowNumbers rn{};
+    if (!row_numbers(p, rn)) return cudaErrorNotSupported;
+    if (head_dim == 64) return rn.odd ? launch_tc<64, true>(p, rn, st) : launch_tc<64, false>(p, rn, st);
+    return rn.odd ? launch_tc<128, true>(p, rn, st) : launch_tc<128, false>(p, rn, st);
+  }
   return head_dim == 64 ? launch_fp32<64>(p, st) : launch_fp32<128>(p, st);
 }
 

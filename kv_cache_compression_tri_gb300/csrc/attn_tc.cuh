@@ -15,6 +15,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "attn_common.cuh"
 #include "umma.cuh"
 
@@ -42,49 +44,67 @@ inline Encode tensor_map_encode() {
   return encode;
 }
 
-// Where a layer's rows are, for the copy warps. Blocks (of a pool) or sequences, and heads,
-// are multiples of a row apart in any order the strides give, so a row of the pool has one
-// number and the tensor map is (element, row): two strides never have to fit into each
-// other, which a map of more dimensions would ask of them (each of its strides is
-// documented as a multiple of the one before). Strides that are not whole rows have no
-// such map; their rows are brought by 16-byte copies of the copy warp.
-struct RowNumbers {
-  int box_rows;                 // rows of a box: 128, or a smaller block
-  int maps;                     // whether there are tensor maps
-  int head_rows, outer_rows;    // rows from head to head, from block (or sequence) to the next
-  int none, row_mask;           // the number of no block (or sequence); row & row_mask is its place in the block
-  int count;                    // rows of the map; one past its last row reads as zeros
+// Where a layer's rows are, for the copy warps. Blocks (of a pool) or sequences, and heads, lie
+// in any order and at any strides of whole 16 bytes. A tensor map of them as dimensions would
+// ask each stride to be a multiple of the one before (so it is documented), so the maps are
+// (element, row): a row's number is its offset divided by its size. Where strides are not
+// whole rows (ODD) there is a map for each remainder, from the remainder on.
+constexpr int MAX_ROW_MAPS = 16;  // 256-byte rows at offsets of whole 16 bytes
+template <bool ODD>
+struct RowMaps {
+  CUtensorMap m[ODD ? MAX_ROW_MAPS : 1];
 };
-inline RowNumbers row_numbers(const AttnParams& p) {
+struct RowNumbers {
+  int box_rows;          // rows of a box: 128, or a smaller block
+  int odd;               // whether strides are not whole rows
+  int head, outer;       // from head to head, from block (or sequence) to the next: rows, if odd 16-byte units
+  int none, row_mask;    // the number of no block (or sequence); row & row_mask is its place in the block
+  int count;             // rows of the (first) map; one past its last row reads as zeros
+};
+// false: more rows, or 16-byte units between slices, than a coordinate can number.
+inline bool row_numbers(const AttnParams& p, RowNumbers& r) {
   const RowMap& m = p.rows;
   const bool paged = m.table != nullptr;
-  const int64_t head = p.n_kv_heads > 1 ? (paged ? m.head_bytes : m.slice_bytes) : 0;
   const int64_t n_outer = paged ? m.num_blocks : p.n_seq;
+  const int64_t head = p.n_kv_heads > 1 ? (paged ? m.head_bytes : m.slice_bytes) : 0;
   const int64_t outer = n_outer > 1 ? (paged ? m.block_bytes : m.lh_count * m.slice_bytes) : 0;
-  RowNumbers r{};
+  const int64_t count = ((p.n_kv_heads - 1) * head + (n_outer - 1) * outer) / m.row_bytes + (paged ? m.block_size : p.n_cap);
+  r.odd = head % m.row_bytes != 0 || outer % m.row_bytes != 0;
+  const int64_t unit = r.odd ? 16 : m.row_bytes;
+  if (count > 0x7fffffff - 2 * TROWS || head / unit > 0x7fffffff || outer / unit > 0x7fffffff) return false;
   r.none = paged ? m.num_blocks : -1;
   r.row_mask = paged ? m.block_size - 1 : 0x7fffffff;
   r.box_rows = paged && m.block_size < TROWS ? m.block_size : TROWS;
-  if (head % m.row_bytes || outer % m.row_bytes) return r;
-  const int64_t count = ((p.n_kv_heads - 1) * head + (n_outer - 1) * outer) / m.row_bytes + (paged ? m.block_size : p.n_cap);
-  if (count > 0x7fffffff - 2 * TROWS) return r;  // (coordinates are 32 bits)
-  r.maps = 1;
-  r.head_rows = static_cast<int>(head / m.row_bytes);
-  r.outer_rows = static_cast<int>(outer / m.row_bytes);
+  r.head = static_cast<int>(head / unit);
+  r.outer = static_cast<int>(outer / unit);
   r.count = static_cast<int>(count);
-  return r;
+  return true;
 }
-// The tensor map of one layer's K (or V) rows, boxes of 64 elements by box_rows rows.
-inline bool encode_rows(CUtensorMap* map, const void* pool, const AttnParams& p, int head_dim, const RowNumbers& r, Encode encode) {
+// The tensor maps of `bytes` of rows from `base` on, boxes of 64 elements by box_rows rows.
+template <bool ODD>
+inline bool encode_row_maps(RowMaps<ODD>& maps, const void* base, int64_t bytes, int head_dim, int box_rows, Encode encode) {
+  const int row_bytes = head_dim * 2;
+  for (int i = 0; i < (ODD ? row_bytes / 16 : 1); ++i) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(std::max<int64_t>((bytes - 16 * i) / row_bytes, 1))};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t step[2] = {1, 1};
+    if (encode(&maps.m[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, static_cast<char*>(const_cast<void*>(base)) + 16 * i, dims, strides, box,
+               step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  }
+  return true;
+}
+// Those of one layer's K (or V).
+template <bool ODD>
+inline bool encode_rows(RowMaps<ODD>& maps, const void* pool, const AttnParams& p, int head_dim, const RowNumbers& r, Encode encode) {
   const RowMap& m = p.rows;
   const int64_t base = p.layer * (m.table ? m.layer_bytes : p.n_kv_heads * m.slice_bytes);
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(r.count)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(m.row_bytes)};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(r.box_rows)};
-  const cuuint32_t step[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, static_cast<char*>(const_cast<void*>(pool)) + base, dims, strides, box, step,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const int64_t n_outer = m.table ? m.num_blocks : p.n_seq, unit = ODD ? 16 : m.row_bytes;
+  const int64_t bytes = ((p.n_kv_heads - 1) * static_cast<int64_t>(r.head) + (n_outer - 1) * r.outer) * unit +
+                        static_cast<int64_t>(m.table ? m.block_size : p.n_cap) * m.row_bytes;
+  return encode_row_maps(maps, static_cast<const char*>(pool) + base, bytes, head_dim, r.box_rows, encode);
 }
 
 __device__ __forceinline__ void tma_load2(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
@@ -125,44 +145,31 @@ struct LaneBox {
     live = row < TROWS;
   }
 };
-// Where a lane's box of the tile at row k0 of head h is: with maps its first row's number, else
-// the block (as tile_block gave it). Worked out before the wait for a ring stage: after it, the
-// dozen instructions are on the chain from a stage set free to its next rows (32 queries over 16
+// Where a lane's box of the tile at row k0 of head h is (blk as tile_block gave it): a row's
+// number, and of which map. Worked out before the wait for a ring stage: after it, the dozen
+// instructions are on the chain from a stage set free to its next rows (32 queries over 16
 // caches of up to 32768 rows: 170 us, before it 164).
-template <int D, bool MAPS>
-__device__ __forceinline__ int box_place(const RowNumbers& rn, const LaneBox<D>& box, int blk, int h, int k0) {
-  if (!MAPS) return blk;
-  return blk == rn.none ? rn.count : blk * rn.outer_rows + h * rn.head_rows + ((k0 + box.row) & rn.row_mask);
-}
-// Cached rows [k0, k0 + 128) of slice (seq, h) of K or V into the tile at `dst`, by one warp,
-// arriving once on `bar`. Rows past the slice hold zeros or another slice's rows. (MAPS by
-// template: with both ways in one kernel an 8192-token prompt took 390 us for 376.)
-template <int D, bool MAPS>
-__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, const void* pool, const AttnParams& p, const RowNumbers& rn,
-                                          const LaneBox<D>& box, int place, int seq, int h, int k0, uint64_t* bar, int lane) {
-  if constexpr (MAPS) {
-    if (lane == 0) mbar_arrive_expect_tx(bar, D * 256);
-    __syncwarp();
-    if (box.live) tma_load2(dst + box.off, map, box.x, place, bar);
+struct Place {
+  int row, map;
+};
+template <int D, bool ODD>
+__device__ __forceinline__ Place box_place(const RowNumbers& rn, const LaneBox<D>& box, int blk, int h, int k0) {
+  const int row = (k0 + box.row) & rn.row_mask;
+  if constexpr (ODD) {
+    constexpr int UNITS = D / 8;  // 16-byte units of a row
+    const int64_t at = static_cast<int64_t>(blk) * rn.outer + static_cast<int64_t>(h) * rn.head;
+    return blk == rn.none ? Place{rn.count, 0} : Place{static_cast<int>(at / UNITS) + row, static_cast<int>(at % UNITS)};
   } else {
-    constexpr int COLS = D / 64, CH = D / 8;
-    const bool paged = p.rows.paged();
-    const char* base = static_cast<const char*>(pool) + p.rows.slice_base(slice_of(p, seq, h));
-#pragma unroll 4
-    for (int i = lane; i < TROWS * CH; i += 32) {
-      const int u = i / CH, ch = i % CH, row = k0 + u;
-      const int blk = __shfl_sync(FULL_MASK, place, u / rn.box_rows * COLS);  // (from the lane of row u's box)
-      const bool live = paged ? blk < p.rows.num_blocks : row < p.n_cap;
-      const int64_t off = paged ? blk * p.rows.block_bytes + static_cast<int64_t>(row & (p.rows.block_size - 1)) * p.rows.row_bytes
-                                : static_cast<int64_t>(row) * p.rows.row_bytes;
-      cp_async16(dst + (ch >> 3) * TCOL + u * 128 + (((ch & 7) ^ (u & 7)) << 4), base + (live ? off + ch * 16 : 0), live);
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
+    return {blk == rn.none ? rn.count : blk * rn.outer + h * rn.head + row, 0};
   }
+}
+// A tile's cached rows of K or V into the tile at `dst`, by one warp, arriving once on `bar`.
+// Rows past the slice are zeros or another slice's rows.
+template <int D, bool ODD>
+__device__ __forceinline__ void load_tile(uint32_t dst, const RowMaps<ODD>& maps, const LaneBox<D>& box, Place at, uint64_t* bar, int lane) {
+  if (lane == 0) mbar_arrive_expect_tx(bar, D * 256);
+  __syncwarp();
+  if (box.live) tma_load2(dst + box.off, &maps.m[ODD ? at.map : 0], box.x, at.row, bar);
 }
 
 // Packed query rows of one tile (row u: token tok0 + u / group, head u % group;

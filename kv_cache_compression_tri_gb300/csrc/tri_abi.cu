@@ -634,6 +634,10 @@ tri_status prepare_attn(const tri_kv* kv, const tri_queries* q, AttnParams& p) {
   return TRI_OK;
 }
 
+tri_status attn_status(cudaError_t e) {
+  return e == cudaSuccess ? TRI_OK : e == cudaErrorNotSupported ? TRI_ERR_UNSUPPORTED : TRI_ERR_CUDA;
+}
+
 // Rows one new token can see at most: the launch's bound, the row counts being on the device.
 int max_visible(const tri_kv* kv, int32_t n_sink, int32_t window) {
   if (window == 0) return kv->n_cap;
@@ -703,7 +707,7 @@ tri_status tri_attn_prefill(const tri_kv* kv, const tri_queries* q, void* out, f
   if (!out || !aligned(out, 16) || (lse && !aligned(lse, 4))) return TRI_ERR_INVALID_ARG;
   p.out = out;
   p.lse = lse;
-  return launch_attn_prefill(p, kv->dtype, kv->head_dim, stream) == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
+  return attn_status(launch_attn_prefill(p, kv->dtype, kv->head_dim, stream));
 }
 
 tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* lse, int64_t lse_seq_stride, float* mass,
@@ -717,7 +721,7 @@ tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* ls
   p.lse_in = lse;
   p.lse_seq = lse_seq_stride;
   p.mass = mass;
-  return launch_attn_mass(p, kv->dtype, kv->head_dim, stream) == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
+  return attn_status(launch_attn_mass(p, kv->dtype, kv->head_dim, stream));
 }
 
 tri_status tri_mass_evict(const float* mass, float* mass_out, const tri_kv* kv, int32_t n_prompt, int32_t n_recent,

@@ -146,3 +146,12 @@ def test_weights_are_derivatives_of_the_log_sum():
         k2 = k.copy()
         k2[j] += e * q / (0.5 * (q @ q))  # moves logit j by e
         assert np.isclose((attend(q, k2, v, 5, 0.5, 1, 3)[1] - l) / e, w[j], atol=1e-5)
+
+
+def test_prompts_and_masses_refuse_more_rows_than_a_coordinate_numbers(lib):  # noqa: F811
+    rows = dict(PAGED, num_blocks=1 << 27, block_stride=16 * 64, head_stride=(1 << 27) * 16 * 64, layer_stride=0)
+    far = dict(slice_stride=((1 << 31) - 128) * 64)
+    for over in (rows, far):
+        kp, qp = ctypes.byref(_post(**over)), ctypes.byref(_q())
+        assert lib.tri_attn_prefill(kp, qp, 0x30000, None, None) == UNSUPPORTED
+        assert lib.tri_attn_mass(kp, qp, 0x50000, 16, 0x60000, None) == UNSUPPORTED
