@@ -57,11 +57,11 @@ struct RowMaps {
 struct RowNumbers {
   int box_rows;          // rows of a box: 128, or a smaller block
   int odd;               // whether strides are not whole rows
-  int head, outer;       // from head to head, from block (or sequence) to the next: rows, if odd 16-byte units
+  int64_t head, outer;   // from head to head, from block (or sequence) to the next: rows (int), if odd 16-byte units
   int none, row_mask;    // the number of no block (or sequence); row & row_mask is its place in the block
   int count;             // rows of the (first) map; one past its last row reads as zeros
 };
-// false: more rows, or 16-byte units between slices, than a coordinate can number.
+// false: more rows than a coordinate can number.
 inline bool row_numbers(const AttnParams& p, RowNumbers& r) {
   const RowMap& m = p.rows;
   const bool paged = m.table != nullptr;
@@ -71,12 +71,12 @@ inline bool row_numbers(const AttnParams& p, RowNumbers& r) {
   const int64_t count = ((p.n_kv_heads - 1) * head + (n_outer - 1) * outer) / m.row_bytes + (paged ? m.block_size : p.n_cap);
   r.odd = head % m.row_bytes != 0 || outer % m.row_bytes != 0;
   const int64_t unit = r.odd ? 16 : m.row_bytes;
-  if (count > 0x7fffffff - 2 * TROWS || head / unit > 0x7fffffff || outer / unit > 0x7fffffff) return false;
+  if (count > 0x7fffffff - 2 * TROWS) return false;
   r.none = paged ? m.num_blocks : -1;
   r.row_mask = paged ? m.block_size - 1 : 0x7fffffff;
   r.box_rows = paged && m.block_size < TROWS ? m.block_size : TROWS;
-  r.head = static_cast<int>(head / unit);
-  r.outer = static_cast<int>(outer / unit);
+  r.head = head / unit;
+  r.outer = outer / unit;
   r.count = static_cast<int>(count);
   return true;
 }
@@ -102,7 +102,7 @@ inline bool encode_rows(RowMaps<ODD>& maps, const void* pool, const AttnParams& 
   const RowMap& m = p.rows;
   const int64_t base = p.layer * (m.table ? m.layer_bytes : p.n_kv_heads * m.slice_bytes);
   const int64_t n_outer = m.table ? m.num_blocks : p.n_seq, unit = ODD ? 16 : m.row_bytes;
-  const int64_t bytes = ((p.n_kv_heads - 1) * static_cast<int64_t>(r.head) + (n_outer - 1) * r.outer) * unit +
+  const int64_t bytes = ((p.n_kv_heads - 1) * r.head + (n_outer - 1) * r.outer) * unit +
                         static_cast<int64_t>(m.table ? m.block_size : p.n_cap) * m.row_bytes;
   return encode_row_maps(maps, static_cast<const char*>(pool) + base, bytes, head_dim, r.box_rows, encode);
 }
@@ -157,10 +157,10 @@ __device__ __forceinline__ Place box_place(const RowNumbers& rn, const LaneBox<D
   const int row = (k0 + box.row) & rn.row_mask;
   if constexpr (ODD) {
     constexpr int UNITS = D / 8;  // 16-byte units of a row
-    const int64_t at = static_cast<int64_t>(blk) * rn.outer + static_cast<int64_t>(h) * rn.head;
+    const int64_t at = blk * rn.outer + h * rn.head;
     return blk == rn.none ? Place{rn.count, 0} : Place{static_cast<int>(at / UNITS) + row, static_cast<int>(at % UNITS)};
   } else {
-    return {blk == rn.none ? rn.count : blk * rn.outer + h * rn.head + row, 0};
+    return {blk == rn.none ? rn.count : blk * static_cast<int>(rn.outer) + h * static_cast<int>(rn.head) + row, 0};
   }
 }
 // A tile's cached rows of K or V into the tile at `dst`, by one warp, arriving once on `bar`.

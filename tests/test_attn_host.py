@@ -155,3 +155,6 @@ def test_prompts_and_masses_refuse_more_rows_than_a_coordinate_numbers(lib):  # 
         kp, qp = ctypes.byref(_post(**over)), ctypes.byref(_q())
         assert lib.tri_attn_prefill(kp, qp, 0x30000, None, None) == UNSUPPORTED
         assert lib.tri_attn_mass(kp, qp, 0x50000, 16, 0x60000, None) == UNSUPPORTED
+    # queries too, where no map of theirs fits their strides
+    q = _q(n_q=3, token_stride=(1 << 36) + 8, seq_stride=0)
+    assert lib.tri_attn_mass(ctypes.byref(_post()), ctypes.byref(q), 0x50000, 16, 0x60000, None) == UNSUPPORTED

@@ -429,3 +429,13 @@ def test_offsets_past_32_bits(block, dtype):
         res.append((out, lse, mass[-H:], dec))
     for x, y in zip(*res):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("what", ["nan", -1, 1 << 20])
+def test_decode_blocks_out_of_sight(dtype, block, what):
+    for lens, n_sink, window in (([[333, 700], [64, 200]], 4, 90), ([[9000]], 0, 33), ([[3000, 2900]], 130, 65)):
+        c = Case(lens, 128, dtype, L=1, block=block)
+        assert hide(c, [1] * c.B, n_sink, window, what) > 0
+        check_decode(c, 4, layer=0, n_sink=n_sink, window=window, with_mass=True)
