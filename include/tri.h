@@ -421,7 +421,7 @@ typedef struct {
   int64_t token_stride;  /* size a multiple of 16 bytes                               */
   const int32_t* n_new;  /* device [n_seq]: tokens of each sequence, 0 .. n_q, or NULL:
                             n_q each. Outputs of tokens >= n_new are left as they were */
-  int32_t n_q;           /* tokens a sequence may have in this call, >= 1             */
+  int32_t n_q;           /* tokens a sequence may have in this call, 1 .. 2^31 - 257  */
   int32_t group;         /* query heads per KV head, 1 .. 8                           */
   int32_t layer;
   int32_t n_sink;        /* first rows that stay visible next to a window, >= 0       */

@@ -600,7 +600,7 @@ tri_status prepare_attn(const tri_kv* kv, const tri_queries* q, AttnParams& p) {
   if (st != TRI_OK) return st;
   if (kv->key_layout != TRI_KEYS_POST_ROPE) return TRI_ERR_UNSUPPORTED;
   if (!q || !q->q || !aligned(q->q, 16)) return TRI_ERR_INVALID_ARG;
-  if (q->n_q < 1 || q->group < 1 || q->group > MAX_GROUP) return TRI_ERR_INVALID_ARG;
+  if (q->n_q < 1 || q->n_q > 0x7fffffff - 256 || q->group < 1 || q->group > MAX_GROUP) return TRI_ERR_INVALID_ARG;
   if (q->layer < 0 || q->layer >= kv->n_layers) return TRI_ERR_INVALID_ARG;
   if (q->n_sink < 0 || q->window < 0) return TRI_ERR_INVALID_ARG;
   if (!(q->scale > 0.f) || !std::isfinite(q->scale)) return TRI_ERR_INVALID_ARG;

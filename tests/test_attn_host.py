@@ -158,3 +158,8 @@ def test_prompts_and_masses_refuse_more_rows_than_a_coordinate_numbers(lib):  # 
     # queries too, where no map of theirs fits their strides
     q = _q(n_q=3, token_stride=(1 << 36) + 8, seq_stride=0)
     assert lib.tri_attn_mass(ctypes.byref(_post()), ctypes.byref(q), 0x50000, 16, 0x60000, None) == UNSUPPORTED
+
+
+def test_more_tokens_than_tiles_can_count(lib):  # noqa: F811
+    for n_q in ((1 << 31) - 1, (1 << 31) - 256):  # (rounding up to tiles would leave the int range)
+        assert list(_calls(lib, _post(), _q(n_q=n_q))) == [INVALID] * 3
