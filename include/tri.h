@@ -66,7 +66,29 @@ typedef enum {
 #define TRI_DEV_BAD_BLOCK 6       /* a block table entry is outside [0, num_blocks) */
 #define TRI_DEV_BAD_QUERY 7       /* a sequence's n_new is outside [0, n_q]       */
 
-typedef enum { TRI_F32 = 0, TRI_BF16 = 1 } tri_dtype;
+/* TRI_Q4: cache rows in 4 bits. A row of head_dim d is d / 2 + 16 bytes: d / 2
+ * bytes of codes, then for each quarter of the row (d / 4 elements) its scale
+ * and minimum, fp16 each; element e of quarter j stands for
+ *   minimum_j + scale_j * code_e,  code_e in 0 .. 15.
+ * With i = e mod (d / 4), the code of element e is nibble n of the row (nibble n:
+ * bits 4 (n mod 2) .. of byte n / 2):
+ *   d = 128: n = 8 (4 (i / 8) + j) + i mod 8,
+ *   d = 64:  n = 8 (2 (i / 4) + j / 2) + 4 (i mod 4 / 2) + 2 (j mod 2) + i mod 2
+ * (the attention kernels read a row by four lanes; a lane's codes of all four
+ * quarters are next to each other). tri_append writes such rows, with min and max
+ * of a quarter over its elements x (magnitudes above 30656, infinite ones too,
+ * count as 30656):
+ *   minimum = fp16(min), scale = fp16(max(0, max - minimum) / 15),
+ *   code = (x - minimum) / scale to the nearest whole number, ties to even, within
+ *   0 .. 15 (0 where scale is 0),
+ * decided as in 64-bit arithmetic. A quarter that holds a NaN reads back as NaN. A
+ * cache written by other means keeps its scales, if not NaN, within 0 .. 4090.
+ * Taken by tri_append, tri_read_rows, tri_attn_decode, tri_attn_prefill_q4, the
+ * compactions (tri_compact_kv, tri_select_compact, rand_evict_compact,
+ * tri_mass_evict), tri_paged_blocks_used and what reads row counts only; other
+ * calls return TRI_ERR_UNSUPPORTED. Queries and results of the attention over such
+ * a cache are bf16. */
+typedef enum { TRI_F32 = 0, TRI_BF16 = 1, TRI_Q4 = 2 } tri_dtype;
 
 /* How band f pairs two coordinates of a head vector into one complex number:
  * interleaved (x[2f], x[2f+1]) as [TA] "RoPE in complex form" writes it, or
@@ -91,7 +113,8 @@ typedef enum { TRI_KEYS_PRE_ROPE = 0, TRI_KEYS_POST_ROPE = 1 } tri_key_layout;
 /* The cache. K and V rows are head_dim elements, contiguous; slice s starts
  * at element s * slice_stride of k (and of v); row i of the slice at element
  * s * slice_stride + i * head_dim. k and v: device, 16-byte aligned,
- * slice_stride * element size a multiple of 16 bytes. */
+ * slice_stride * element size a multiple of 16 bytes. For TRI_Q4 an element is a
+ * byte, and a row head_dim / 2 + 16 of them, wherever offsets and strides count. */
 typedef struct {
   void* k;               /* [n_slices][n_cap][head_dim] keys (see key_layout)    */
   void* v;               /* [n_slices][n_cap][head_dim] values                   */
@@ -464,6 +487,74 @@ tri_status tri_attn_prefill(const tri_kv* kv, const tri_queries* q, void* out, f
  * fault (row count, n_new, a block that some query sees) is skipped. */
 tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* lse, int64_t lse_seq_stride, float* mass,
                          tri_stream_t stream);
+
+/* tri_attn_prefill_q4 -- tri_attn_prefill over a 4-bit cache (TRI_Q4 only;
+ * TRI_ERR_UNSUPPORTED otherwise). The rows that some query may see are first
+ * written to ws as bf16 values, rounded once; the bf16 kernel then reads those.
+ * ws: device scratch of tri_attn_prefill_q4_workspace_bytes(kv) bytes (one layer's
+ * rows in bf16), 16-byte aligned, no initial contents needed; calls that may
+ * overlap need one each. A sequence with a fault in n_new, or in the table entry
+ * of a block that one of its queries sees (in any head), is skipped as a whole, one
+ * with a bad row count as tri_attn_prefill skips it. */
+size_t tri_attn_prefill_q4_workspace_bytes(const tri_kv* kv);
+tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out, float* lse, void* ws, size_t ws_bytes,
+                               tri_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * tri_append -- new tokens into one layer of the cache, rotated on the way.
+ * (No counterpart on the pages, whose engines fill their caches themselves.)
+ * Token i of the n_new of a sequence becomes row n_valid + i of each of the layer's
+ * slices of that sequence: V as it is, K rotated at the token's position when the cache
+ * holds TRI_KEYS_POST_ROPE, as it is otherwise, each rounded once to the cache's
+ * type. pos[slice][row] (if kv->pos is not NULL) gets the token's first position.
+ * n_valid of those slices grows by n_new. q, if given, is rotated into q_out the
+ * same way in either case.
+ * Rotation: band f of a head vector (pairs as `style` says) is multiplied by
+ * e^{i w_f p}, w_f = rope_theta^(-2f/d), with p = positions[seq][i][band_axis[f]]:
+ * one axis for text; several (time, height, width) for images and video, each
+ * band belonging to one. Angles are exact to 2^-52 turns or so at any position.
+ * A query at a text position p has all axes equal to p, so tri_score of the
+ * post-RoPE keys (which needs no positions) stays what it is for keys of several
+ * axes; pre-RoPE caches carry one position per row, so n_axes > 1 is refused there
+ * (TRI_ERR_UNSUPPORTED), and so are 4-bit caches of pre-RoPE keys.
+ * A slice with a fault (a row count, or too many rows for n_cap:
+ * TRI_DEV_NVALID_OVER_CAP; n_new: TRI_DEV_BAD_QUERY; the table entry of a block that
+ * a new row falls into: TRI_DEV_BAD_BLOCK) keeps its row count and its valid rows;
+ * rows from n_valid on may have been written.
+ * kv->pos_out is not used. Rows of one call must not coincide (no block in two
+ * sequences' tables at rows that the call writes).
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  const void* k;             /* device [n_seq][n_q][n_kv_heads][head_dim], 16-byte aligned, of the
+                                cache's type (TRI_Q4: bf16); a token's heads are contiguous   */
+  const void* v;             /* likewise                                                  */
+  int64_t k_seq_stride, k_token_stride; /* elements between sequences, and between tokens; */
+  int64_t v_seq_stride, v_token_stride; /* x element size a multiple of 16 bytes           */
+  const void* q;             /* NULL, or device [n_seq][n_q][n_kv_heads * group][head_dim]  */
+  void* q_out;               /* rotated queries, the same shape; q itself (with q's strides), or apart
+                                from it; tokens >= n_new are left as they were              */
+  int64_t q_seq_stride, q_token_stride;
+  int64_t q_out_seq_stride, q_out_token_stride;
+  const int32_t* positions;  /* device [n_seq][n_q][n_axes]                                */
+  const uint8_t* band_axis;  /* HOST [head_dim / 2], each below n_axes, or NULL when n_axes is 1 */
+  const int32_t* n_new;      /* device [n_seq]: tokens of each sequence, 0 .. n_q, or NULL: n_q each */
+  double rope_theta;
+  tri_rope_style style;
+  int32_t n_axes;            /* 1 .. 4                                                     */
+  int32_t n_q;               /* tokens a sequence may have in this call                    */
+  int32_t group;             /* query heads per KV head, 1 .. 8 (read with q only)         */
+  int32_t layer;
+} tri_tokens;
+
+tri_status tri_append(const tri_kv* kv, const tri_tokens* tokens, tri_stream_t stream);
+
+/* tri_read_rows -- the values that one layer's rows of a 4-bit cache stand for
+ * (TRI_Q4 only): k_out, v_out (either may be NULL): device bf16
+ * [n_seq][n_kv_heads][n_cap][head_dim], 16-byte aligned; rows below n_valid get
+ * minimum + scale * code, rounded to fp32 and then to bf16, others are left as they
+ * were. A slice with a bad row count, and rows in a block with a bad table entry,
+ * are left out. */
+tri_status tri_read_rows(const tri_kv* kv, int32_t layer, void* k_out, void* v_out, tri_stream_t stream);
 
 /* tri_mass_evict -- eviction by accumulated weight: exactly tri_select_compact
  * with scores = mass, and the masses moved with their rows: for j < n_keep,

@@ -26,15 +26,23 @@ __all__ = [
     "launch_count", "ROPE_INTERLEAVED", "ROPE_HALF", "NORM_WEIGHTED", "NORM_UNWEIGHTED",
     "DEV_OK", "DEV_NVALID_OVER_CAP", "DEV_NAN_SCORE", "DEV_BAD_KEEP", "DEV_BAD_QUERY",
     "attn_decode", "attn_decode_workspace_bytes", "attn_prefill", "attn_mass", "mass_evict",
+    "append", "read_rows", "attn_prefill_workspace_bytes", "q4_row_bytes",
 ]
 
 ROPE_INTERLEAVED, ROPE_HALF = 0, 1
 NORM_WEIGHTED, NORM_UNWEIGHTED = 0, 1
-F32, BF16 = 0, 1
+F32, BF16, Q4 = 0, 1, 2
 (DEV_OK, DEV_NVALID_OVER_CAP, DEV_NAN_SCORE, DEV_BAD_KEEP, DEV_TIMEOUT, DEV_GROUP_NVALID, DEV_BAD_BLOCK,
  DEV_BAD_QUERY) = (0, 1, 2, 3, 4, 5, 6, 7)
 
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+_KV_DTYPES = {**_DTYPES, torch.uint8: Q4}
+_Q4_DIMS = {48: 64, 80: 128}  # head dimension of a 4-bit row of so many bytes
+
+
+def q4_row_bytes(head_dim: int) -> int:
+    """Bytes of a 4-bit row (TRI_Q4): codes, and scale and minimum of each quarter."""
+    return head_dim // 2 + 16
 
 
 class TriError(RuntimeError):
@@ -59,6 +67,20 @@ class _TriKV(ctypes.Structure):
 class _TriCenters(ctypes.Structure):
     _fields_ = [("center", ctypes.c_void_p), ("mean_norm", ctypes.c_void_p),
                 ("mrl", ctypes.c_void_p)]
+
+
+class _TriTokens(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_seq_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64),
+        ("v_seq_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64),
+        ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+        ("q_seq_stride", ctypes.c_int64), ("q_token_stride", ctypes.c_int64),
+        ("q_out_seq_stride", ctypes.c_int64), ("q_out_token_stride", ctypes.c_int64),
+        ("positions", ctypes.c_void_p), ("band_axis", ctypes.c_char_p), ("n_new", ctypes.c_void_p),
+        ("rope_theta", ctypes.c_double), ("style", ctypes.c_int), ("n_axes", ctypes.c_int32),
+        ("n_q", ctypes.c_int32), ("group", ctypes.c_int32), ("layer", ctypes.c_int32),
+    ]
 
 
 class _TriQueries(ctypes.Structure):
@@ -139,6 +161,14 @@ def load_library():
         lib.tri_attn_decode.restype = ctypes.c_int
         lib.tri_attn_prefill.argtypes = [kvp, qp, vp, vp, vp]
         lib.tri_attn_prefill.restype = ctypes.c_int
+        lib.tri_attn_prefill_q4_workspace_bytes.argtypes = [kvp]
+        lib.tri_attn_prefill_q4_workspace_bytes.restype = ctypes.c_size_t
+        lib.tri_attn_prefill_q4.argtypes = [kvp, qp, vp, vp, vp, ctypes.c_size_t, vp]
+        lib.tri_attn_prefill_q4.restype = ctypes.c_int
+        lib.tri_append.argtypes = [kvp, ctypes.POINTER(_TriTokens), vp]
+        lib.tri_append.restype = ctypes.c_int
+        lib.tri_read_rows.argtypes = [kvp, i32, vp, vp, vp]
+        lib.tri_read_rows.restype = ctypes.c_int
         lib.tri_attn_mass.argtypes = [kvp, qp, vp, i64, vp, vp]
         lib.tri_attn_mass.restype = ctypes.c_int
         lib.tri_mass_evict.argtypes = [vp, vp, kvp, i32, i32, i32, vp, vp]
@@ -206,7 +236,9 @@ class KVCache:
     """A batch of caches: k, v [n_seq, n_layers, n_kv_heads, n_cap, head_dim]
     (bf16 or fp32, device); n_valid [S] int32; pos / pos_out [S, n_cap] int32
     (pos may be None: position = slot index); dev_status [1] int32.
-    post_rope: k holds RoPE-rotated keys (the score then ignores pos)."""
+    post_rope: k holds RoPE-rotated keys (the score then ignores pos).
+    4-bit rows (post_rope only): k, v uint8 with q4_row_bytes(head_dim) in place
+    of head_dim."""
     k: torch.Tensor
     v: torch.Tensor
     n_valid: torch.Tensor
@@ -236,7 +268,8 @@ class KVCache:
         k, v = self.k, self.v
         shape, strides, dtype = k.shape, k.stride(), k.dtype
         n_seq, L, H, n_cap, d = shape
-        assert k.is_cuda and dtype in _DTYPES
+        assert k.is_cuda and dtype in _KV_DTYPES
+        assert dtype != torch.uint8 or d in _Q4_DIMS
         assert v.shape == shape and v.dtype == dtype
         # rows contiguous, slices evenly strided
         stride = strides[2]
@@ -247,7 +280,7 @@ class KVCache:
             if t is not None:
                 assert t.dtype == torch.int32 and t.is_contiguous() and t.numel() == n_seq * L * H * n_cap
         return _TriKV(k.data_ptr(), v.data_ptr(), _ptr(self.pos), _ptr(self.pos_out),
-                      self.n_valid.data_ptr(), stride, n_seq, L, H, n_cap, d, _DTYPES[dtype],
+                      self.n_valid.data_ptr(), stride, n_seq, L, H, n_cap, _Q4_DIMS[d] if dtype == torch.uint8 else d, _KV_DTYPES[dtype],
                       _ptr(self.dev_status), 1 if self.post_rope else 0, None, 0, 0, 0, 0, 0)
 
 
@@ -258,7 +291,8 @@ class PagedKVCache:
     (block, layer, head) run of block_size rows contiguous); block_table
     [n_seq, blocks per sequence] int32 (physical block of each logical block,
     shared by the sequence's layers and heads); n_valid [S] int32; pos /
-    pos_out [S, n_cap] int32 with n_cap = blocks per sequence * block_size."""
+    pos_out [S, n_cap] int32 with n_cap = blocks per sequence * block_size.
+    4-bit rows as in KVCache: uint8 pools, q4_row_bytes(head_dim) per row."""
     k: torch.Tensor
     v: torch.Tensor
     block_table: torch.Tensor
@@ -288,7 +322,8 @@ class PagedKVCache:
         k, v, table = self.k, self.v, self.block_table
         shape, strides, dtype = k.shape, k.stride(), k.dtype
         nb, L, H, bs, d = shape
-        assert k.is_cuda and dtype in _DTYPES
+        assert k.is_cuda and dtype in _KV_DTYPES
+        assert dtype != torch.uint8 or d in _Q4_DIMS
         assert v.shape == shape and v.dtype == dtype
         assert v.stride() == strides
         assert strides[4] == 1 and strides[3] == d
@@ -300,7 +335,7 @@ class PagedKVCache:
             if t is not None:
                 assert t.dtype == torch.int32 and t.is_contiguous() and t.numel() == S * n_cap
         return _TriKV(k.data_ptr(), v.data_ptr(), _ptr(self.pos), _ptr(self.pos_out),
-                      self.n_valid.data_ptr(), 0, n_seq, L, H, n_cap, d, _DTYPES[dtype],
+                      self.n_valid.data_ptr(), 0, n_seq, L, H, n_cap, _Q4_DIMS[d] if dtype == torch.uint8 else d, _KV_DTYPES[dtype],
                       _ptr(self.dev_status), 1 if self.post_rope else 0, table.data_ptr(), bs, nb,
                       strides[0], strides[1], strides[2])
 
@@ -541,17 +576,94 @@ def select_union(scores: torch.Tensor, kv: KVCache, n_prompt: int, n_recent: int
 
 def _queries(kvs: _TriKV, kv, layer: int, q: torch.Tensor, shape, strides, n_new: torch.Tensor | None,
              scale: float | None, n_sink: int, window: int) -> _TriQueries:
-    """Queries of shape [n_seq, n_q, Hq, d] (any sequence and token strides) of the cache's type and device."""
+    """Queries of shape [n_seq, n_q, Hq, d] (any sequence and token strides) of the cache's type (bf16 for one in 4
+    bits) and device."""
     n_seq, n_q, Hq, d = shape
     dev = q.get_device()
     assert dev == kv.k.get_device() == torch.cuda.current_device(), "cache and queries on the current device"
-    assert q.dtype == kv.k.dtype and d == kvs.head_dim and n_seq == kvs.n_seq and Hq % kvs.n_kv_heads == 0
+    assert q.dtype == _token_dtype(kv) and d == kvs.head_dim and n_seq == kvs.n_seq and Hq % kvs.n_kv_heads == 0
     assert strides[3] == 1 and (strides[2] == d or Hq == 1)
     if n_new is not None:
         assert n_new.is_cuda and n_new.dtype == torch.int32 and n_new.is_contiguous() and n_new.numel() == n_seq
     # (the stride of a dimension of one may be anything)
     return _TriQueries(q.data_ptr(), strides[0] if n_seq > 1 else 0, strides[1] if n_q > 1 else Hq * d, _ptr(n_new), n_q,
                        Hq // kvs.n_kv_heads, layer, n_sink, window, d ** -0.5 if scale is None else scale)
+
+
+def _token_dtype(kv) -> torch.dtype:
+    """Type of queries, new rows and attention results: the cache's, bf16 for one in 4 bits."""
+    return torch.bfloat16 if kv.k.dtype == torch.uint8 else kv.k.dtype
+
+
+def _token_strides(t: torch.Tensor, shape, dtype: torch.dtype, device: int):
+    """Sequence and token strides of rows [n_seq, n_q, heads, d] whose heads are contiguous."""
+    assert t.get_device() == device and t.dtype == dtype and t.shape == shape
+    n_seq, n_q, heads, d = shape
+    st = t.stride()
+    assert st[3] == 1 and (st[2] == d or heads == 1)
+    # (the stride of a dimension of one may be anything)
+    return st[0] if n_seq > 1 else 0, st[1] if n_q > 1 else heads * d
+
+
+def append(kv, layer: int, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, rope_theta: float,
+           q: torch.Tensor | None = None, q_out: torch.Tensor | None = None, n_new: torch.Tensor | None = None,
+           band_axis=None, style: int = ROPE_INTERLEAVED, stream=None) -> torch.Tensor | None:
+    """New tokens into one layer of the cache (tri_append): k, v [n_seq, n_q, H, d]
+    (any sequence and token strides: views of a fused projection's output) go
+    behind the rows of the layer's slices, k rotated at the tokens' positions
+    [n_seq, n_q] or [n_seq, n_q, axes] int32 if the cache is post-RoPE; n_valid
+    grows by n_new [n_seq] int32 (None: n_q each), kv.pos gets the first axis. q
+    [n_seq, n_q, Hq, d] is rotated into q_out (q itself, or apart from it; None: a
+    new tensor), which is returned. band_axis: the axis of each of the d / 2 bands.
+    A 4-bit cache takes bf16 tokens."""
+    lib = load_library()
+    kvs = kv._abi()
+    dev, dtype, d, H = kv.k.get_device(), _token_dtype(kv), kvs.head_dim, kvs.n_kv_heads
+    assert dev == torch.cuda.current_device(), "cache and tokens on the current device"
+    n_seq, n_q = k.shape[:2]
+    assert n_seq == kvs.n_seq
+    ks, vs = (_token_strides(t, (n_seq, n_q, H, d), dtype, dev) for t in (k, v))
+    assert positions.get_device() == dev and positions.dtype == torch.int32 and positions.is_contiguous()
+    n_axes = positions.shape[2] if positions.dim() == 3 else 1
+    assert positions.shape[:2] == (n_seq, n_q) and positions.numel() == n_seq * n_q * n_axes
+    if n_new is not None:
+        assert n_new.get_device() == dev and n_new.dtype == torch.int32 and n_new.is_contiguous() and n_new.numel() == n_seq
+    axes = None
+    if band_axis is not None:
+        axes = bytes(int(a) for a in band_axis)
+        assert len(axes) == d // 2
+    qs = qos = (0, 0)
+    group = 0
+    if q is not None:
+        Hq = q.shape[2]
+        assert Hq % H == 0
+        group = Hq // H
+        qs = _token_strides(q, (n_seq, n_q, Hq, d), dtype, dev)
+        if q_out is None:
+            q_out = _empty((n_seq, n_q, Hq, d), dtype, q.device, stream)
+            if stream is not None:  # read on the current stream later on
+                q_out.record_stream(torch.cuda.current_stream())
+        qos = _token_strides(q_out, (n_seq, n_q, Hq, d), dtype, dev)
+    else:
+        assert q_out is None
+    tok = _TriTokens(k.data_ptr(), v.data_ptr(), *ks, *vs, _ptr(q), _ptr(q_out), *qs, *qos, positions.data_ptr(), axes,
+                     _ptr(n_new), float(rope_theta), style, n_axes, n_q, group, layer)
+    _check("tri_append", lib.tri_append(ctypes.byref(kvs), ctypes.byref(tok), _stream(stream)))
+    return q_out
+
+
+def read_rows(kv, layer: int, k_out: torch.Tensor | None, v_out: torch.Tensor | None, stream=None) -> None:
+    """The values that one layer's rows of a 4-bit cache stand for (tri_read_rows):
+    k_out, v_out [n_seq, H, n_cap, d] bf16 (either may be None); rows from n_valid
+    on are left as they were."""
+    lib = load_library()
+    kvs = kv._abi()
+    assert kv.k.get_device() == torch.cuda.current_device()
+    for t in (k_out, v_out):
+        if t is not None:
+            assert t.get_device() == kv.k.get_device() and t.dtype == torch.bfloat16 and t.is_contiguous()
+            assert t.shape == (kvs.n_seq, kvs.n_kv_heads, kvs.n_cap, kvs.head_dim)
+    _check("tri_read_rows", lib.tri_read_rows(ctypes.byref(kvs), layer, _ptr(k_out), _ptr(v_out), _stream(stream)))
 
 
 def _check_mass(kvs: _TriKV, mass: torch.Tensor):
@@ -592,14 +704,21 @@ def attn_decode(kv, layer: int, q: torch.Tensor, out: torch.Tensor, n_new: torch
     return out
 
 
+def attn_prefill_workspace_bytes(kv) -> int:
+    """Scratch of attn_prefill: one layer's rows in bf16 for a 4-bit cache, none otherwise."""
+    kvs = kv._abi()
+    return int(load_library().tri_attn_prefill_q4_workspace_bytes(ctypes.byref(kvs)))
+
+
 def attn_prefill(kv, layer: int, q: torch.Tensor, out: torch.Tensor, n_new: torch.Tensor | None = None,
                  scale: float | None = None, n_sink: int = 0, window: int = 0, lse: torch.Tensor | None = None,
-                 stream=None) -> torch.Tensor:
+                 stream=None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Causal attention of a chunk of new tokens, q [n_seq, n_q, Hq, d] (any
     sequence and token strides), over one layer of a post-RoPE cache whose
     newest rows they are (tri_attn_prefill): out [n_seq, n_q, Hq, d]; lse
     [n_seq, n_q, Hq] fp32. n_new [n_seq] int32: tokens of each sequence (rows of
-    out past them stay as they were)."""
+    out past them stay as they were). A 4-bit cache (tri_attn_prefill_q4) needs
+    attn_prefill_workspace_bytes(kv) of workspace."""
     lib = load_library()
     kvs = kv._abi()
     shape = q.shape
@@ -607,6 +726,13 @@ def attn_prefill(kv, layer: int, q: torch.Tensor, out: torch.Tensor, n_new: torc
     assert out.is_cuda and out.is_contiguous() and out.shape == shape and out.dtype == q.dtype
     if lse is not None:
         assert lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == shape[:3]
+    if kvs.dtype == Q4:
+        if workspace is None:
+            workspace = _scratch(int(lib.tri_attn_prefill_q4_workspace_bytes(ctypes.byref(kvs))), kv.device, stream)
+        assert workspace.is_cuda and workspace.is_contiguous()
+        _check("tri_attn_prefill_q4", lib.tri_attn_prefill_q4(ctypes.byref(kvs), ctypes.byref(qs), out.data_ptr(), _ptr(lse),
+                                                              workspace.data_ptr(), workspace.nbytes, _stream(stream)))
+        return out
     _check("tri_attn_prefill", lib.tri_attn_prefill(ctypes.byref(kvs), ctypes.byref(qs), out.data_ptr(), _ptr(lse),
                                                     _stream(stream)))
     return out

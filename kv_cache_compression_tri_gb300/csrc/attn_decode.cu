@@ -269,6 +269,51 @@ __device__ __forceinline__ void fetch_tile(const AttnParams& p, const Run& r, co
   }
 }
 
+// The warps' sums of a run in shared memory, [NW][8 heads][HS], and past them the run's.
+template <int D>
+struct RunSums {
+  static constexpr int HS = D + 4;  // floats between heads: the four lt of a store hit different banks
+};
+// The end of a run: its sums over the warps (so; m and l in sm_m, sm_l), then joined in the cluster or
+// left for the join. bad: a block (or copy) that a visible row needs is missing.
+template <class Tag, int D>
+__device__ __forceinline__ void finish_run(const AttnParams& p, const Run& r, const Tiles<Tag, D>& tl, int ls, int split, int64_t pi, bool bad,
+                                           float* so, const float (&sm_m)[NW][8], const float (&sm_l)[NW][8], float2* run_ml) {
+  constexpr int HS = RunSums<D>::HS;
+  const int t = threadIdx.x;
+  __syncthreads();
+  if (bad && t == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
+  float* tot = so + NW * 8 * HS;
+  for (int i = t; i < p.group * D; i += NW * 32) {
+    const int g = i / D, e = i % D;
+    float m = NEG_INF;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) m = fmaxf(m, sm_m[k][g]);
+    const float mu = m == NEG_INF ? 0.f : m;
+    float l = 0.f, acc = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const float a = fast_exp2(sm_m[k][g] - mu);
+      l = fmaf(sm_l[k][g], a, l);
+      acc = fmaf(so[(k * 8 + g) * HS + e], a, acc);
+    }
+    if (bad) l = -1.f;
+    if (p.join) {
+      tot[i] = acc;
+      if (e == 0) run_ml[g] = make_float2(m, l);
+    } else {
+      p.part_o[(pi + g) * D + e] = acc;
+      if (e == 0) p.part_ml[pi + g] = make_float2(m, l);
+    }
+  }
+  constexpr int TK = TileGeo<Tag, D>::TK;
+  if (p.join)
+    join_cluster<__nv_bfloat16, D>(p, r, ls, split, tot, run_ml, tl.u0 * TK, tl.u1 * TK, [&](int i) {
+      const int j = tl.row(i / TK) + i % TK;
+      return j < r.n && (j < r.vis.s1 || j >= r.vis.w0) ? j : -1;
+    });
+}
+
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_constant__ AttnParams p) {
   using T = __nv_bfloat16;
@@ -412,43 +457,20 @@ __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_cons
   // every ring is idle: the warps' vector sums go there
   const bool bad = __syncthreads_or(PAGED && !blocks_ok);
   float* so = reinterpret_cast<float*>(smem);
-  constexpr int HS = D + 4;  // floats between heads: the four lt of a store hit different banks
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) so[(w * 8 + 2 * lt + (c & 1)) * HS + 16 * i + lg + (c >> 1) * 8] = o[i][c];
-  __syncthreads();
-  if (PAGED && bad && t == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
-  // the run's sums: over the warps, into `tot` (past them in shared memory)
-  float* tot = so + NW * 8 * HS;
-  for (int i = t; i < p.group * D; i += NW * 32) {
-    const int g = i / D, e = i % D;
-    float m = NEG_INF;
-#pragma unroll
-    for (int k = 0; k < NW; ++k) m = fmaxf(m, sm_m[k][g]);
-    const float mu = m == NEG_INF ? 0.f : m;
-    float l = 0.f, acc = 0.f;
-#pragma unroll
-    for (int k = 0; k < NW; ++k) {
-      const float a = fast_exp2(sm_m[k][g] - mu);
-      l = fmaf(sm_l[k][g], a, l);
-      acc = fmaf(so[(k * 8 + g) * HS + e], a, acc);
-    }
-    if (PAGED && bad) l = -1.f;
-    if (p.join) {
-      tot[i] = acc;
-      if (e == 0) run_ml[g] = make_float2(m, l);
-    } else {
-      p.part_o[(pi + g) * D + e] = acc;
-      if (e == 0) p.part_ml[pi + g] = make_float2(m, l);
-    }
-  }
-  if (p.join)
-    join_cluster<__nv_bfloat16, D>(p, r, ls, split, tot, run_ml, tl.u0 * G::TK, tl.u1 * G::TK, [&](int i) {
-      const int j = tl.row(i / G::TK) + i % G::TK;
-      return j < r.n && (j < r.vis.s1 || j >= r.vis.w0) ? j : -1;
-    });
+    for (int c = 0; c < 4; ++c) so[(w * 8 + 2 * lt + (c & 1)) * RunSums<D>::HS + 16 * i + lg + (c >> 1) * 8] = o[i][c];
+  finish_run<T, D>(p, r, tl, ls, split, pi, PAGED && bad, so, sm_m, sm_l, run_ml);
 }
+
+}  // namespace
+}  // namespace tri
+
+#include "attn_decode_q4.cuh"
+
+namespace tri {
+namespace {
 
 // ---------------------------------------------------------------------------
 // fp32 rows
@@ -737,6 +759,13 @@ cudaError_t launch_bf16(const AttnParams& p, int max_rows, cudaStream_t st) {
   return e != cudaSuccess || p.join ? e : launch_join<__nv_bfloat16, D>(p, max_rows, st);
 }
 
+template <int D>
+cudaError_t launch_q4(const AttnParams& p, int max_rows, cudaStream_t st) {
+  const cudaError_t e =
+      launch_runs(p.rows.table ? decode_q4_kernel<D, true> : decode_q4_kernel<D, false>, TileGeo<Q4Tag, D>::SMEM, p, st);
+  return e != cudaSuccess || p.join ? e : launch_join<__nv_bfloat16, D>(p, max_rows, st);
+}
+
 template <int D, int GP>
 cudaError_t launch_fp32_group(const AttnParams& p, cudaStream_t st) {
   return launch_runs(p.rows.table ? decode_rows_kernel<D, GP, true> : decode_rows_kernel<D, GP, false>, TileGeo<float, D>::SMEM, p, st);
@@ -790,6 +819,7 @@ DecodePlan attn_decode_plan(int n_slices, int max_rows) {
 }
 
 cudaError_t launch_attn_decode(const AttnParams& p, int max_rows, tri_dtype dt, int head_dim, cudaStream_t st) {
+  if (dt == TRI_Q4) return head_dim == 64 ? launch_q4<64>(p, max_rows, st) : launch_q4<128>(p, max_rows, st);
   if (dt == TRI_BF16) return head_dim == 64 ? launch_bf16<64>(p, max_rows, st) : launch_bf16<128>(p, max_rows, st);
   return head_dim == 64 ? launch_fp32<64>(p, max_rows, st) : launch_fp32<128>(p, max_rows, st);
 }

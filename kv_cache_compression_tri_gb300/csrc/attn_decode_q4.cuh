@@ -1,0 +1,421 @@
+// attn_decode_q4.cuh -- the decode kernel over rows in 4 bits (included by
+// attn_decode.cu, whose runs, joins and masses it shares).
+//
+// A row is codes c and per quarter j of its elements a scale s_j and a minimum m_j:
+//   q . k = sum_j (s_j sum_e q_e c_e + m_j sum_e q_e),
+//   sum_r p_r v_r = sum_r (p_r s_rj) c_re + sum_r p_r m_rj   (e in quarter j),
+// so the products run on the codes, and scales and minima enter outside of them.
+//
+// Bound: 2 (d / 2 + 16) bytes a row pair, 160 instead of 512 at d 128. At the copy rate
+// that is 35 elements per clock and SM, so what it takes to bring 4 bits to an
+// operand decides: an fp16 whose exponent is 0 and whose low bits are c is the number
+// c 2^-24 (the tensor cores take subnormals as they are), four bits higher it
+// is c 2^-20. A word of eight codes is then four ANDs and one shift: pairs
+// (0, 4), (1, 5) << 4, (2, 6), (3, 7) << 4, with no offset to take off again; the
+// powers of two go into q and into the final scaling.
+//   S = K Q^T: A = 16 rows' codes. Lane (g, t) reads 16 (d 64: 8) bytes of rows g and g + 8,
+//   its elements of all four quarters (the row's order of codes is made for
+//   that); per quarter one or two MMAs whose sums are scaled per row in fp32.
+//   q as fp16, scaled by a power of two so that the head's largest is below 2^15: exact
+//   for every element down to 2^-25 of it. Minima: one MMA against the quarters' sums of
+//   q as fp16 pairs.
+//   O^T += V^T P^T: A = V transposed, 16 elements of a quarter x 16 rows. Two rows' codes of
+//   an element come together by a byte permute of their words, before they are
+//   spread. B = p s_j in fp16, p up to 2^4 (a scale is below 2^12): two
+//   roundings of 2^-11 of its weight, where results are rounded to 2^-9.
+// Each warp owns a ring of NST tiles of 32 rows, K and V, a bulk copy each (two in
+// pools of 16-row blocks); table entries are read a tile ahead. Rows out of sight are
+// copied but not used: their weight and their pairs (any bits) are set to zero.
+#pragma once
+
+#include "q4_common.cuh"
+
+namespace tri {
+namespace {
+
+struct Q4Tag {};
+template <int D>
+struct TileGeo<Q4Tag, D> {
+  static constexpr int ROW = Q4Row<D>::BYTES;
+  static constexpr int TK = 32;
+  static constexpr int TILE = TK * ROW;
+  static constexpr int NST = 3;
+  static constexpr int WARP_RING = NST * 2 * TILE;
+  static constexpr int SMEM = NW * WARP_RING;
+};
+
+__device__ __forceinline__ void mma16816h(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float scale_of(uint32_t pair) { return __half2float(__ushort_as_half(static_cast<unsigned short>(pair & 0xffff))); }
+// A lane's words of a row of codes.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a) : "memory");
+  else
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t x;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
+  return x;
+}
+
+// A head's query as B fragments for the codes (see the file comment), by the four
+// lanes of the head: f[mma][2], the sums of its quarters as an fp16 pair (lane t: quarter t), and
+// log2 of the power of two in them.
+template <int D>
+__device__ __forceinline__ void query_fragments(const __nv_bfloat16* q, bool live, int t, uint32_t (&f)[D / 16][2], uint32_t& sums, int& shift) {
+  float x[4][D / 16];  // [quarter][the lane's elements]
+  float most = 0.f, sum[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat16* at = q + j * (D / 4) + t * (D / 16);
+    uint32_t w[D / 32];
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) w[k] = live ? __ldg(reinterpret_cast<const uint32_t*>(at) + k) : 0u;
+    sum[j] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+      x[j][2 * k] = bf16_lo(w[k]);
+      x[j][2 * k + 1] = bf16_hi(w[k]);
+      most = fmaxf(most, fmaxf(fabsf(x[j][2 * k]), fabsf(x[j][2 * k + 1])));
+      sum[j] += x[j][2 * k] + x[j][2 * k + 1];
+    }
+  }
+#pragma unroll
+  for (int k = 1; k <= 2; k <<= 1) {
+    most = fmaxf(most, __shfl_xor_sync(FULL_MASK, most, k));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] += __shfl_xor_sync(FULL_MASK, sum[j], k);
+  }
+  // most 2^shift in [2^14, 2^15)
+  const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;
+  shift = most == 0.f ? 0 : min(max(14 - e, -100), 100);
+  const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) x[j][k] *= up;
+  if constexpr (D == 128) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f[2 * j + h][0] = pack_half(x[j][2 * h], x[j][2 * h + 4]);
+        f[2 * j + h][1] = pack_half(x[j][2 * h + 1] * 0.0625f, x[j][2 * h + 5] * 0.0625f);
+      }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j][0] = pack_half(x[j][0], x[j][2]);
+      f[j][1] = pack_half(x[j][1] * 0.0625f, x[j][3] * 0.0625f);
+    }
+  }
+  const float s = (t == 0 ? sum[0] : t == 1 ? sum[1] : t == 2 ? sum[2] : sum[3]) * up * 0.03125f;
+  const float hi = __half2float(__float2half_rn(s));
+  sums = pack_half(hi, s - hi);
+}
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(NW * 32, 3) decode_q4_kernel(const __grid_constant__ AttnParams p) {
+  using G = TileGeo<Q4Tag, D>;
+  constexpr int NWD = Q4Row<D>::WORDS, CODES = Q4Row<D>::CODES, LANE = 4 * NWD;  // bytes of a lane's codes
+  constexpr float LIFT = 4.f;  // log2 of the largest weight
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float sm_m[NW][8], sm_l[NW][8];
+  __shared__ float2 run_ml[MAX_GROUP];
+  __shared__ uint64_t bars[NW][G::NST];
+  const int ls = blockIdx.x / p.n_split, split = blockIdx.x % p.n_split;
+  const int t = threadIdx.x, w = t >> 5, lane = t & 31, lg = lane >> 2, lt = lane & 3;
+  const int64_t pi = static_cast<int64_t>(blockIdx.x) * p.group;
+  pdl_launch();
+  Run r;
+  if (!slice_run(p, ls, r)) {
+    if (!p.join && t < p.group) p.part_ml[pi + t] = make_float2(NEG_INF, -1.f);
+    return;  // (every run of the slice does)
+  }
+  const Tiles<Q4Tag, D> tl(p, r, split);
+
+  // The warp's ring. A tile's rows lie in `parts` runs of 16 or 32 rows; their blocks (or -1)
+  // are looked up a tile before the copies.
+  const uint32_t ring = smem_addr(smem) + w * G::WARP_RING;
+  unsigned char* ring_p = smem + w * G::WARP_RING;
+  bool blocks_ok = true;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < G::NST; ++i) mbar_init(&bars[w][i], 1);
+    mbar_init_fence();
+  }
+  __syncwarp();
+  const int run_rows = PAGED ? min(G::TK, p.rows.block_size) : G::TK;
+  struct Blocks {
+    int b[2];
+  };
+  auto look_up = [&](int u) {
+    Blocks b{{0, 0}};
+    if (PAGED && lane == 0 && u < tl.u1) {
+      const int r0 = tl.row(u);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int rs = r0 + 16 * k;
+        if (k == 1 && run_rows > 16) continue;
+        b.b[k] = rs < r.n ? __ldg(tl.trow + (rs >> p.rows.block_shift)) : -1;
+      }
+    }
+    return b;
+  };
+  auto fetch = [&](int u, int st, const Blocks& b) {
+    if (lane != 0) return;
+    const int r0 = tl.row(u);
+    int64_t off[2];
+    int bytes[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int rs = r0 + k * run_rows;
+      if ((PAGED ? k * run_rows >= G::TK : k == 1) || rs >= r.n) continue;
+      off[k] = tl.base + static_cast<int64_t>(rs) * G::ROW;
+      if (PAGED) {
+        const int blk = b.b[k];
+        if (blk < 0 || blk >= p.rows.num_blocks) {
+          // rows that nobody sees may have no block any more
+          if (rs < r.vis.s1 || rs + run_rows - 1 >= r.vis.w0) blocks_ok = false;
+          continue;
+        }
+        off[k] = tl.base + blk * p.rows.block_bytes + static_cast<int64_t>(rs & (p.rows.block_size - 1)) * G::ROW;
+      }
+      bytes[k] = min(run_rows, r.n - rs) * G::ROW;
+    }
+    mbar_arrive_expect_tx(&bars[w][st], static_cast<uint32_t>(2 * (bytes[0] + bytes[1])));
+    unsigned char* dst = ring_p + st * 2 * G::TILE;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (bytes[k] == 0) continue;
+      bulk_g2s(dst + k * 16 * G::ROW, static_cast<const char*>(p.k) + off[k], bytes[k], &bars[w][st]);
+      bulk_g2s(dst + G::TILE + k * 16 * G::ROW, static_cast<const char*>(p.v) + off[k], bytes[k], &bars[w][st]);
+    }
+  };
+  Blocks ahead{};
+#pragma unroll
+  for (int i = 0; i < G::NST - 1; ++i) {
+    const int u = tl.u0 + w + i * NW;
+    if (u < tl.u1) fetch(u, i, look_up(u));
+  }
+  ahead = look_up(tl.u0 + w + (G::NST - 1) * NW);
+
+  // the heads' B fragments, and what their products are to be multiplied with (heads 2 lt, 2 lt + 1)
+  uint32_t qf[D / 16][2], qsum;
+  float f0, f1;
+  {
+    int shift;
+    query_fragments<D>(static_cast<const __nv_bfloat16*>(p.q) + r.seq * p.q_seq + (static_cast<int64_t>(r.h) * p.group + lg) * D,
+                       lg < p.group, lt, qf, qsum, shift);
+    const int s0 = __shfl_sync(FULL_MASK, shift, 8 * lt), s1 = __shfl_sync(FULL_MASK, shift, 8 * lt + 4);
+    const float sl = p.scale * LOG2E;
+    f0 = sl * __uint_as_float(static_cast<uint32_t>(127 + 24 - s0) << 23);
+    f1 = sl * __uint_as_float(static_cast<uint32_t>(127 + 24 - s1) << 23);
+  }
+
+  float o[D / 16][4], om[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
+  // heads 2 lt, 2 lt + 1: weights are 2^(x - m), m at least the largest x minus LIFT
+  float m0 = NEG_INF, m1 = NEG_INF, l0 = 0.f, l1 = 0.f;
+  float* logits = p.logits ? p.logits + static_cast<int64_t>(ls) * p.n_cap * p.group : nullptr;
+  const uint32_t half_sel = lg >= 4 ? 0x7632 : 0x5410;
+  int st = 0;
+  uint32_t phase = 0;
+  bool landed = true;
+  for (int u = tl.u0 + w; u < tl.u1; u += NW) {
+    {
+      const int nx = u + (G::NST - 1) * NW, ns = st == 0 ? G::NST - 1 : st - 1;
+      if (nx < tl.u1) fetch(nx, ns, ahead);
+      ahead = look_up(nx + NW);
+    }
+    landed = mbar_wait_bounded(&bars[w][st], phase);
+    landed = __all_sync(FULL_MASK, landed);
+    if (!landed) break;
+    const int r0 = tl.row(u);
+    const bool inner = r0 + G::TK <= r.n && (r0 >= r.vis.w0 || r0 + G::TK <= r.vis.s1);
+    const uint32_t tk = ring + st * 2 * G::TILE, tv = tk + G::TILE;
+    float x[2][4];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t ra = tk + (16 * s + lg) * G::ROW, rb = ra + 8 * G::ROW;
+      uint32_t wa[NWD], wb[NWD], pa[4], pb[4];
+      lds_words(ra + LANE * lt, wa);
+      lds_words(rb + LANE * lt, wb);
+      lds_words(ra + CODES, pa);
+      lds_words(rb + CODES, pb);
+      {
+        const uint32_t ma = lds32(ra + CODES + 4 * lt), mb = lds32(rb + CODES + 4 * lt);
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816h(y, __byte_perm(ma, ma, 0x3232), __byte_perm(mb, mb, 0x3232), 0u, 0u, qsum, 0u);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[s][c] = y[c] * 0x1p-19f;
+      }
+#pragma unroll
+      for (int k = 0; k < NWD; ++k) {
+        const uint32_t a8 = wa[k] >> 8, b8 = wb[k] >> 8;
+        constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u;
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816h(y, wa[k] & LO, wb[k] & LO, wa[k] & HI, wb[k] & HI, qf[2 * k][0], qf[2 * k][1]);
+        if constexpr (D == 64) {
+          const float sa = scale_of(pa[2 * k]), sb = scale_of(pb[2 * k]);
+          x[s][0] = fmaf(y[0], sa, x[s][0]);
+          x[s][1] = fmaf(y[1], sa, x[s][1]);
+          x[s][2] = fmaf(y[2], sb, x[s][2]);
+          x[s][3] = fmaf(y[3], sb, x[s][3]);
+          y[0] = y[1] = y[2] = y[3] = 0.f;
+        }
+        mma16816h(y, a8 & LO, b8 & LO, a8 & HI, b8 & HI, qf[2 * k + 1][0], qf[2 * k + 1][1]);
+        constexpr int QS = D == 64 ? 2 : 1;
+        const float sa = scale_of(pa[QS * k + QS - 1]), sb = scale_of(pb[QS * k + QS - 1]);
+        x[s][0] = fmaf(y[0], sa, x[s][0]);
+        x[s][1] = fmaf(y[1], sa, x[s][1]);
+        x[s][2] = fmaf(y[2], sb, x[s][2]);
+        x[s][3] = fmaf(y[3], sb, x[s][3]);
+      }
+      x[s][0] *= f0;
+      x[s][1] *= f1;
+      x[s][2] *= f0;
+      x[s][3] *= f1;
+      const int ja = r0 + 16 * s + lg, jb = ja + 8;
+      if (!inner) {
+        if (!(ja < r.n && (ja < r.vis.s1 || ja >= r.vis.w0))) x[s][0] = x[s][1] = NEG_INF;
+        if (!(jb < r.n && (jb < r.vis.s1 || jb >= r.vis.w0))) x[s][2] = x[s][3] = NEG_INF;
+      }
+      if (logits) {  // (rows out of sight: their entries are not read)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int j = c < 2 ? ja : jb, g = 2 * lt + (c & 1);
+          if (g < p.group && j < r.n) logits[static_cast<int64_t>(j) * p.group + g] = x[s][c];
+        }
+      }
+    }
+    float mx0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+    float mx1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+    if (__any_sync(FULL_MASK, mx0 - LIFT > m0 || mx1 - LIFT > m1)) {
+#pragma unroll
+      for (int k = 4; k <= 16; k <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(FULL_MASK, mx0, k));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(FULL_MASK, mx1, k));
+      }
+      const float n0 = fmaxf(m0, mx0 - LIFT), n1 = fmaxf(m1, mx1 - LIFT);
+      const float a0 = n0 == NEG_INF ? 1.f : fast_exp2(m0 - n0), a1 = n1 == NEG_INF ? 1.f : fast_exp2(m1 - n1);
+      m0 = n0;
+      m1 = n1;
+      l0 *= a0;
+      l1 *= a1;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        o[i][0] *= a0;
+        o[i][1] *= a1;
+        o[i][2] *= a0;
+        o[i][3] *= a1;
+      }
+      om[0] *= a0;
+      om[1] *= a1;
+    }
+    const float z0 = m0 == NEG_INF ? 0.f : m0, z1 = m1 == NEG_INF ? 0.f : m1;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const float e[4] = {fast_exp2(x[s][0] - z0), fast_exp2(x[s][1] - z1), fast_exp2(x[s][2] - z0), fast_exp2(x[s][3] - z1)};
+      l0 += e[0] + e[2];
+      l1 += e[1] + e[3];
+      const uint32_t p01 = transpose8(pack_half(e[0], e[1])), p89 = transpose8(pack_half(e[2], e[3]));  // rows 2 lt, + 1, + 8, + 9; head lg
+      uint32_t vw[4][NWD], vp[4][4], vm[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int row = 16 * s + 2 * lt + (k & 1) + 8 * (k >> 1);
+        const uint32_t a = tv + row * G::ROW;
+        lds_words(a + LANE * (lg & 3), vw[k]);
+        lds_words(a + CODES, vp[k]);
+        vm[k] = lds32(a + CODES + 4 * (lg & 3));
+        if (!inner) {
+          const int j = r0 + row;
+          if (!(j < r.n && (j < r.vis.s1 || j >= r.vis.w0))) {
+            vm[k] = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vp[k][i] = 0u;
+          }
+        }
+      }
+      mma16816h(om, __byte_perm(vm[0], vm[1], 0x7632), 0u, __byte_perm(vm[2], vm[3], 0x7632), 0u, p01, p89);
+      uint32_t b0[4], b1[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        b0[j] = mul_half2(p01, __byte_perm(vp[0][j], vp[1][j], 0x5410));
+        b1[j] = mul_half2(p89, __byte_perm(vp[2][j], vp[3][j], 0x5410));
+      }
+#pragma unroll
+      for (int k = 0; k < NWD; ++k) {
+        const uint32_t y01 = __byte_perm(vw[0][k], vw[1][k], half_sel), y89 = __byte_perm(vw[2][k], vw[3][k], half_sel);
+        const uint32_t z01 = y01 >> 8, z89 = y89 >> 8;
+        constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u;
+        const int ja = D == 64 ? 2 * k : k, jb = D == 64 ? 2 * k + 1 : k;
+        mma16816h(o[2 * k], y01 & LO, y01 & HI, y89 & LO, y89 & HI, b0[ja], b1[ja]);
+        mma16816h(o[2 * k + 1], z01 & LO, z01 & HI, z89 & LO, z89 & HI, b0[jb], b1[jb]);
+      }
+    }
+    __syncwarp();  // the stage may be refilled
+    if (lane == 0) fence_proxy_async_smem();
+    if (++st == G::NST) {
+      st = 0;
+      phase ^= 1;
+    }
+  }
+  if (!landed) {
+    // a copy never came: report it, skip the slice, and let the copies in flight end
+    set_status(p.dev_status, TRI_DEV_TIMEOUT);
+    blocks_ok = false;
+    for (int k = 0; k < G::NST; ++k) (void)mbar_wait_bounded(&bars[w][(st + k) % G::NST], st + k >= G::NST ? phase ^ 1 : phase);
+  }
+#pragma unroll
+  for (int k = 4; k <= 16; k <<= 1) {
+    l0 += __shfl_xor_sync(FULL_MASK, l0, k);
+    l1 += __shfl_xor_sync(FULL_MASK, l1, k);
+  }
+  if (lg == 0) {
+    sm_m[w][2 * lt] = m0;
+    sm_m[w][2 * lt + 1] = m1;
+    sm_l[w][2 * lt] = l0;
+    sm_l[w][2 * lt + 1] = l1;
+  }
+  // every ring is idle: the warps' vector sums go there
+  const bool bad = __syncthreads_or(!blocks_ok);
+  float* so = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float a0 = __shfl_sync(FULL_MASK, om[0], 4 * j + lt), a1 = __shfl_sync(FULL_MASK, om[1], 4 * j + lt);
+    // the quarter's elements of this lane: d 128, two MMAs of two; d 64, one
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const int e = j * (D / 4) + (lg & 3) * (D / 16) + (lg >> 2) * (D / 32) + 2 * i;
+      const float(&y)[4] = o[j * (D / 64) + i];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        so[(w * 8 + 2 * lt + (c & 1)) * RunSums<D>::HS + e + (c >> 1)] = fmaf(y[c], c < 2 ? 0x1p24f : 0x1p20f, (c & 1) ? a1 : a0);
+    }
+  }
+  finish_run<Q4Tag, D>(p, r, tl, ls, split, pi, bad, so, sm_m, sm_l, run_ml);
+}
+
+}  // namespace
+}  // namespace tri

@@ -36,7 +36,7 @@ cudaError_t launch_blocks_used(const RowMap& rows, const int32_t* n_valid, int32
 }
 
 cudaError_t launch_compact(const CompactParams& p, int n_slices, cudaStream_t st) {
-  if (p.row_bytes % 16 != 0 || p.row_bytes < 128 || p.row_bytes > CTILE) return cudaErrorInvalidValue;
+  if (p.row_bytes % 16 != 0 || p.row_bytes < 48 || p.row_bytes > CTILE) return cudaErrorInvalidValue;
   const bool paged = p.rows.table != nullptr;
   auto kern = paged ? compact_kernel<true> : compact_kernel<false>;
   const size_t smem = COMPACT_SMEM + (paged ? CTAB * sizeof(int32_t) : 0);

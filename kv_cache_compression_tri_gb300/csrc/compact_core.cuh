@@ -87,7 +87,8 @@ __device__ __forceinline__ void move_rows(char* pool, const RowMap& rows, int64_
     const int64_t blk = (i < CTAB) ? ctab[i] : __ldg(trow + (r >> rows.block_shift));
     return sbase + blk * rows.block_bytes + static_cast<int64_t>(r & (rows.block_size - 1)) * rows.row_bytes;
   };
-  const int TR = TB / rb;  // rows per tile
+  constexpr int RPL = TB / 128 / 32;  // most rows a lane copies per tile (2)
+  const int TR = min(TB / rb, 32 * RPL);  // rows per tile (4-bit rows leave part of it unused)
   const int u_first = first / TR;
   const int ntiles = (n_keep - 1) / TR - u_first + 1;
   if (lane == 0) {
@@ -105,7 +106,6 @@ __device__ __forceinline__ void move_rows(char* pool, const RowMap& rows, int64_
   // Each lane copies rows lo_j + lane + 32 r of a tile (r < RPL); the byte
   // offsets of their sources (keep entry, and block for a paged cache) are
   // resolved one tile ahead so no gather waits on them.
-  constexpr int RPL = TB / 128 / 32;  // most rows a lane copies per tile (2)
   int64_t knext[RPL];
   auto load_keep = [&](int k, int64_t (&kv)[RPL]) {
     int lo_j, hi_j, t0;

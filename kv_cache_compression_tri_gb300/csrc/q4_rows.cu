@@ -1,0 +1,138 @@
+// q4_rows.cu -- one layer's rows of a 4-bit cache written out as bf16: for the
+// caller (tri_read_rows), or for a chunk's attention, which then runs on them
+// (tri_attn_prefill_q4).
+//
+// A thread writes 16 bytes: eight elements of one quarter, minimum + scale * code. Bound:
+// HBM, d / 2 + 16 bytes in and 2 d out per row (a prompt's rows stay in L2 for the
+// attention that follows).
+//
+// For a chunk: rows out of every query's sight are zero where a 128-row tile holds rows in
+// sight (the attention's weights there are 0, which a NaN would survive) and not
+// written elsewhere; and the first CTA of a sequence checks every table entry that
+// its queries need, so that the attention leaves the sequence out when one is bad.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "attn_common.cuh"
+#include "q4_common.cuh"
+
+namespace tri {
+namespace {
+
+constexpr int RT = 256;    // threads per CTA
+constexpr int CHUNK = 64;  // rows of a CTA, K and V
+constexpr int SIGHT = 128; // rows that an attention tile reads together
+
+// Eight elements, number 8 c .. 8 c + 7, of the 4-bit row at `row`.
+template <int D>
+__device__ __forceinline__ uint4 unpack8(const char* row, int c) {
+  const int j = c / (D / 32);  // quarter
+  const uint32_t pair = __ldg(reinterpret_cast<const uint32_t*>(row + Q4Row<D>::CODES) + j);
+  const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(pair & 0xffff)));
+  const float m = __half2float(__ushort_as_half(static_cast<unsigned short>(pair >> 16)));
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(row);
+  uint32_t n;  // the eight codes, in order
+  if constexpr (D == 128) {
+    n = __ldg(words + 4 * (c & 3) + j);
+  } else {
+    // lanes 2 (c & 1) and the next: four codes each, two and two in bytes (j & 1) and 2 + (j & 1) of a word
+    const int t = 2 * (c & 1);
+    const uint32_t a = __ldg(words + 2 * t + (j >> 1)) >> (8 * (j & 1)), b = __ldg(words + 2 * t + 2 + (j >> 1)) >> (8 * (j & 1));
+    n = (a & 0xff) | (a >> 8 & 0xff00) | ((b & 0xff) | (b >> 8 & 0xff00)) << 16;
+  }
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = fmaf(static_cast<float>(n >> (4 * e) & 15u), s, m);
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+
+// Rows of a slice of n that some of its nn newest queries see: [0, s1) and [w0, n).
+__device__ __forceinline__ Visible chunk_sight(const Q4RowsParams& p, int n, int nn) {
+  return {visible_rows(n - 1, p.n_sink, p.window).s1, visible_rows(max(n - nn, 0), p.n_sink, p.window).w0};
+}
+
+template <int D, bool CHUNKED>
+__global__ void __launch_bounds__(RT) q4_rows_kernel(const __grid_constant__ Q4RowsParams p, int tiles) {
+  constexpr int LPR = D / 8;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tile = blockIdx.x % tiles, ls = blockIdx.x / tiles;
+  const int seq = ls / p.n_kv_heads, h = ls % p.n_kv_heads;
+  const int64_t s0 = (static_cast<int64_t>(seq) * p.n_layers + p.layer) * p.n_kv_heads, s = s0 + h;
+  const int n = p.n_valid[s], nn = !CHUNKED ? 0 : p.n_new ? __ldg(p.n_new + seq) : p.n_q;
+  const int32_t* trow = p.rows.seq_table(s);
+  if (CHUNKED && tile == 0) {
+    if (threadIdx.x == 0) p.n_valid_out[ls] = n;
+    if (h == 0) {
+      bool bad = nn < 0 || nn > p.n_q;
+      if (bad && threadIdx.x == 0) set_status(p.dev_status, TRI_DEV_BAD_QUERY);
+      if (trow && !bad && nn > 0) {
+        int last = -1;
+        for (int k = 0; k < p.n_kv_heads; ++k) {
+          const int nk = p.n_valid[s0 + k];
+          if (nk == last || nk <= 0 || nk > p.n_cap) continue;  // (a bad count is the attention's to report)
+          last = nk;
+          const Visible vis = chunk_sight(p, nk, nn);
+          const int b1 = (nk - 1) >> p.rows.block_shift, bw = vis.w0 >> p.rows.block_shift;
+          const int bs = vis.s1 > 0 ? (vis.s1 - 1) >> p.rows.block_shift : -1;
+          for (int b = threadIdx.x; b <= b1; b += RT) {
+            if (b > bs && b < bw) continue;
+            const int blk = __ldg(trow + b);
+            bad |= blk < 0 || blk >= p.rows.num_blocks;
+          }
+        }
+        bad = __syncthreads_or(bad);
+        if (bad && threadIdx.x == 0) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
+      }
+      if (threadIdx.x == 0) p.n_new_out[seq] = bad ? 0 : nn;
+    }
+  }
+  if (n < 0 || n > p.n_cap) {
+    if (!CHUNKED && threadIdx.x == 0) set_status(p.dev_status, TRI_DEV_NVALID_OVER_CAP);
+    return;
+  }
+  const int r0 = tile * CHUNK, r1 = min(r0 + CHUNK, n);
+  if (r0 >= r1 || (CHUNKED && nn <= 0)) return;
+  Visible vis{0, 0};
+  if constexpr (CHUNKED) {
+    vis = chunk_sight(p, n, nn);
+    if (r0 >= (vis.s1 + SIGHT - 1) / SIGHT * SIGHT && r1 <= vis.w0 / SIGHT * SIGHT) return;
+  }
+  const int64_t base = p.rows.slice_base(s);
+  const int c = threadIdx.x % LPR;
+  const int64_t out = static_cast<int64_t>(ls) * p.n_cap;
+#pragma unroll
+  for (int i = 0; i < CHUNK * LPR / RT; ++i) {
+    const int r = r0 + i * (RT / LPR) + static_cast<int>(threadIdx.x) / LPR;
+    if (r >= r1) continue;
+    bool live = !CHUNKED || r < vis.s1 || r >= vis.w0;
+    int64_t off = base + static_cast<int64_t>(r) * p.rows.row_bytes;
+    if (trow && live) {
+      const int blk = __ldg(trow + (r >> p.rows.block_shift));
+      live = blk >= 0 && blk < p.rows.num_blocks;
+      if (!CHUNKED && !live) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
+      off = base + blk * p.rows.block_bytes + static_cast<int64_t>(r & (p.rows.block_size - 1)) * p.rows.row_bytes;
+    }
+    if (!CHUNKED && !live) continue;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+      if (p.dst[kv])
+        reinterpret_cast<uint4*>(p.dst[kv] + (out + r) * D)[c] = live ? unpack8<D>(p.src[kv] + off, c) : make_uint4(0, 0, 0, 0);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_q4_rows(const Q4RowsParams& p, int head_dim, cudaStream_t st) {
+  const int tiles = (p.n_cap + CHUNK - 1) / CHUNK;
+  const int64_t ctas = static_cast<int64_t>(p.n_seq) * p.n_kv_heads * tiles;
+  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  auto kern = head_dim == 64 ? (p.n_new_out ? q4_rows_kernel<64, true> : q4_rows_kernel<64, false>)
+                             : (p.n_new_out ? q4_rows_kernel<128, true> : q4_rows_kernel<128, false>);
+  kern<<<static_cast<unsigned>(ctas), RT, 0, st>>>(p, tiles);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace tri

@@ -54,13 +54,13 @@ cudaError_t launch_src_compact(const SelectParams& ps, const CompactParams& pc, 
 
 cudaError_t launch_select_compact(const SelectParams& ps, const CompactParams& pc, bool random, int n_slices,
                                   cudaStream_t st) {
-  if (pc.row_bytes % 16 != 0 || pc.row_bytes < 128 || pc.row_bytes > CTILE) return cudaErrorInvalidValue;
+  if (pc.row_bytes % 16 != 0 || pc.row_bytes < 48 || pc.row_bytes > CTILE) return cudaErrorInvalidValue;
   return random ? launch_src_compact<DrawKeys>(ps, pc, n_slices, st)
                 : launch_src_compact<ScoreKeys>(ps, pc, n_slices, st);
 }
 
 cudaError_t launch_mass_evict(const SelectParams& ps, const CompactParams& pc, int n_slices, cudaStream_t st) {
-  if (pc.row_bytes % 16 != 0 || pc.row_bytes < 128 || pc.row_bytes > CTILE) return cudaErrorInvalidValue;
+  if (pc.row_bytes % 16 != 0 || pc.row_bytes < 48 || pc.row_bytes > CTILE) return cudaErrorInvalidValue;
   // With at most one slice per SM the copies in flight are the bound, with more the CTAs per SM that hide a selection
   // (8192 -> 4096 rows, d 128: 152 slices 142 us with the large tiles, 185 without; 200 slices 257 and 200)
   return n_slices <= 152 ? launch_src_compact<ScoreKeys, true, 4 * CTILE>(ps, pc, n_slices, st)

@@ -23,12 +23,14 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-int elem_bytes(tri_dtype dt) { return dt == TRI_BF16 ? 2 : 4; }
+// Bytes of an element of the cache, and elements of a row (the header counts a 4-bit row in bytes).
+int elem_bytes(tri_dtype dt) { return dt == TRI_Q4 ? 1 : dt == TRI_BF16 ? 2 : 4; }
+int row_elems(const tri_kv* kv) { return kv->dtype == TRI_Q4 ? kv->head_dim / 2 + 16 : kv->head_dim; }
 
 // Shape checks shared by every call that takes a tri_kv.
-tri_status check_kv(const tri_kv* kv, bool need_v) {
+tri_status check_kv(const tri_kv* kv, bool need_v, bool q4_ok = false) {
   if (!kv) return TRI_ERR_INVALID_ARG;
-  if (kv->dtype != TRI_BF16 && kv->dtype != TRI_F32) return TRI_ERR_UNSUPPORTED;
+  if (kv->dtype != TRI_BF16 && kv->dtype != TRI_F32 && !(q4_ok && kv->dtype == TRI_Q4)) return TRI_ERR_UNSUPPORTED;
   if (kv->head_dim != 64 && kv->head_dim != 128) return TRI_ERR_UNSUPPORTED;
   if (kv->n_seq < 1 || kv->n_layers < 1 || kv->n_kv_heads < 1 || kv->n_cap < 1)
     return TRI_ERR_INVALID_ARG;
@@ -46,9 +48,9 @@ tri_status check_kv(const tri_kv* kv, bool need_v) {
     if (kv->num_blocks < 1) return TRI_ERR_INVALID_ARG;
     for (const int64_t st : {kv->block_stride, kv->layer_stride, kv->head_stride})
       if (st < 0 || (st * e) % 16 != 0) return TRI_ERR_INVALID_ARG;
-    if (kv->head_stride < static_cast<int64_t>(kv->block_size) * kv->head_dim) return TRI_ERR_INVALID_ARG;
+    if (kv->head_stride < static_cast<int64_t>(kv->block_size) * row_elems(kv)) return TRI_ERR_INVALID_ARG;
   } else {
-    if (kv->slice_stride < static_cast<int64_t>(kv->n_cap) * kv->head_dim) return TRI_ERR_INVALID_ARG;
+    if (kv->slice_stride < static_cast<int64_t>(kv->n_cap) * row_elems(kv)) return TRI_ERR_INVALID_ARG;
     if ((kv->slice_stride * e) % 16 != 0) return TRI_ERR_INVALID_ARG;
   }
   if (kv->pos && !aligned(kv->pos, 4)) return TRI_ERR_INVALID_ARG;
@@ -62,7 +64,7 @@ tri_status check_kv(const tri_kv* kv, bool need_v) {
 RowMap row_map(const tri_kv* kv) {
   RowMap m{};
   const int e = elem_bytes(kv->dtype);
-  m.row_bytes = kv->head_dim * e;
+  m.row_bytes = row_elems(kv) * e;
   m.lh_count = kv->n_layers * kv->n_kv_heads;
   m.n_kv_heads = kv->n_kv_heads;
   if (kv->block_table) {
@@ -248,7 +250,7 @@ CompactParams compact_params(const tri_kv* kv, const int32_t* keep_idx, int32_t 
   p.rows = row_map(kv);
   p.n_cap = kv->n_cap;
   p.budget = budget;
-  p.row_bytes = kv->head_dim * elem_bytes(kv->dtype);
+  p.row_bytes = p.rows.row_bytes;
   return p;
 }
 
@@ -334,7 +336,7 @@ tri_status tri_compress(const tri_kv* kv, const tri_centers* c, double rope_thet
 tri_status tri_select_compact(const float* scores, const tri_kv* kv, int32_t n_prompt, int32_t n_recent,
                               int32_t budget, int32_t* keep_idx, tri_stream_t stream) {
   TRI_CALL_RANGE();
-  tri_status st = check_kv(kv, true);
+  tri_status st = check_kv(kv, true, true);
   if (st != TRI_OK) return st;
   if (!kv->pos_out || !scores || !aligned(scores, 4) || !keep_idx || !aligned(keep_idx, 4)) return TRI_ERR_INVALID_ARG;
   st = check_protect(n_prompt, n_recent, budget, kv->n_cap);
@@ -349,7 +351,7 @@ tri_status rand_evict_compact(const tri_kv* kv, uint64_t seed, uint32_t round, t
                               int32_t n_prompt, int32_t n_recent, int32_t budget, int32_t* keep_idx,
                               tri_stream_t stream) {
   TRI_CALL_RANGE();
-  tri_status st = check_kv(kv, true);
+  tri_status st = check_kv(kv, true, true);
   if (st != TRI_OK) return st;
   if (kv->n_layers > 65535 || kv->n_kv_heads > 65536) return TRI_ERR_INVALID_ARG;
   if (scope != TRI_DRAW_PER_HEAD && scope != TRI_DRAW_PER_LAYER && scope != TRI_DRAW_PER_SEQUENCE)
@@ -412,7 +414,7 @@ tri_status rand_evict_scoped(const tri_kv* kv, uint64_t seed, uint32_t round, tr
 tri_status tri_compact_kv(const tri_kv* kv, const int32_t* keep_idx, int32_t budget,
                           tri_stream_t stream) {
   TRI_CALL_RANGE();
-  tri_status st = check_kv(kv, true);
+  tri_status st = check_kv(kv, true, true);
   if (st != TRI_OK) return st;
   if (!kv->pos_out) return TRI_ERR_INVALID_ARG;
   if (!keep_idx || !aligned(keep_idx, 4) || budget < 1 || budget > kv->n_cap) return TRI_ERR_INVALID_ARG;
@@ -595,8 +597,8 @@ namespace tri {
 namespace {
 
 // Checks shared by the attention calls, and their parameter block.
-tri_status prepare_attn(const tri_kv* kv, const tri_queries* q, AttnParams& p) {
-  const tri_status st = check_kv(kv, true);
+tri_status prepare_attn(const tri_kv* kv, const tri_queries* q, AttnParams& p, bool q4_ok = false) {
+  const tri_status st = check_kv(kv, true, q4_ok);
   if (st != TRI_OK) return st;
   if (kv->key_layout != TRI_KEYS_POST_ROPE) return TRI_ERR_UNSUPPORTED;
   if (!q || !q->q || !aligned(q->q, 16)) return TRI_ERR_INVALID_ARG;
@@ -605,7 +607,7 @@ tri_status prepare_attn(const tri_kv* kv, const tri_queries* q, AttnParams& p) {
   if (q->n_sink < 0 || q->window < 0) return TRI_ERR_INVALID_ARG;
   if (!(q->scale > 0.f) || !std::isfinite(q->scale)) return TRI_ERR_INVALID_ARG;
   if (q->n_new && !aligned(q->n_new, 4)) return TRI_ERR_INVALID_ARG;
-  const int e = elem_bytes(kv->dtype);
+  const int e = kv->dtype == TRI_F32 ? 4 : 2;  // (queries of a 4-bit cache are bf16)
   const int64_t token = static_cast<int64_t>(kv->n_kv_heads) * q->group * kv->head_dim;
   if (q->seq_stride < 0 || (q->seq_stride * e) % 16 != 0 || (q->token_stride * e) % 16 != 0) return TRI_ERR_INVALID_ARG;
   if (q->n_q > 1 && q->token_stride < token) return TRI_ERR_INVALID_ARG;
@@ -660,13 +662,43 @@ DecodeWs decode_ws(const tri_kv* kv, int32_t group, int32_t n_split, bool with_m
   return w;
 }
 
+// Workspace of tri_attn_prefill_q4: one layer's rows in bf16, [n_seq][n_kv_heads][n_cap][d] K, then V,
+// its row counts [n_seq][n_kv_heads] and new tokens [n_seq] (each part 16-byte aligned).
+struct Q4Ws {
+  size_t v_off, valid_off, new_off, total;
+};
+Q4Ws q4_ws(const tri_kv* kv) {
+  const size_t n = static_cast<size_t>(kv->n_seq) * kv->n_kv_heads;
+  Q4Ws w{};
+  w.v_off = n * kv->n_cap * kv->head_dim * 2;
+  w.valid_off = 2 * w.v_off;
+  w.new_off = w.valid_off + align16(n * sizeof(int32_t));
+  w.total = w.new_off + align16(kv->n_seq * sizeof(int32_t));
+  return w;
+}
+
+Q4RowsParams q4_rows_params(const tri_kv* kv, int32_t layer) {
+  Q4RowsParams r{};
+  r.src[0] = static_cast<const char*>(kv->k);
+  r.src[1] = static_cast<const char*>(kv->v);
+  r.n_valid = kv->n_valid;
+  r.dev_status = kv->dev_status;
+  r.rows = row_map(kv);
+  r.n_cap = kv->n_cap;
+  r.n_seq = kv->n_seq;
+  r.n_layers = kv->n_layers;
+  r.n_kv_heads = kv->n_kv_heads;
+  r.layer = layer;
+  return r;
+}
+
 }  // namespace
 }  // namespace tri
 
 extern "C" {
 
 size_t tri_attn_decode_workspace_bytes(const tri_kv* kv, int32_t group, int32_t with_mass) {
-  if (check_kv(kv, true) != TRI_OK || group < 1 || group > MAX_GROUP) return 0;
+  if (check_kv(kv, true, true) != TRI_OK || group < 1 || group > MAX_GROUP) return 0;
   const int n = kv->n_seq * kv->n_kv_heads;
   return decode_ws(kv, group, attn_decode_max_splits(n, kv->n_cap), with_mass != 0).total;
 }
@@ -675,7 +707,7 @@ tri_status tri_attn_decode(const tri_kv* kv, const tri_queries* q, void* out, fl
                            size_t ws_bytes, tri_stream_t stream) {
   TRI_CALL_RANGE();
   AttnParams p;
-  const tri_status st = prepare_attn(kv, q, p);
+  const tri_status st = prepare_attn(kv, q, p, true);
   if (st != TRI_OK) return st;
   if (q->n_q != 1 || !out || !aligned(out, 16)) return TRI_ERR_INVALID_ARG;
   if ((lse && !aligned(lse, 4)) || (mass && !aligned(mass, 4))) return TRI_ERR_INVALID_ARG;
@@ -710,6 +742,135 @@ tri_status tri_attn_prefill(const tri_kv* kv, const tri_queries* q, void* out, f
   return attn_status(launch_attn_prefill(p, kv->dtype, kv->head_dim, stream));
 }
 
+size_t tri_attn_prefill_q4_workspace_bytes(const tri_kv* kv) {
+  if (check_kv(kv, true, true) != TRI_OK || kv->dtype != TRI_Q4) return 0;
+  return q4_ws(kv).total;
+}
+
+tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out, float* lse, void* ws, size_t ws_bytes,
+                               tri_stream_t stream) {
+  TRI_CALL_RANGE();
+  AttnParams p;
+  const tri_status st = prepare_attn(kv, q, p, true);
+  if (st != TRI_OK) return st;
+  if (kv->dtype != TRI_Q4) return TRI_ERR_UNSUPPORTED;
+  if (!out || !aligned(out, 16) || (lse && !aligned(lse, 4))) return TRI_ERR_INVALID_ARG;
+  const Q4Ws w = q4_ws(kv);
+  if (!ws || !aligned(ws, 16) || ws_bytes < w.total) return TRI_ERR_INVALID_ARG;
+  // more rows than the attention's copies can number are refused before anything is enqueued
+  if (static_cast<int64_t>(kv->n_seq) * kv->n_kv_heads * kv->n_cap > 0x7fffffff - 256) return TRI_ERR_UNSUPPORTED;
+  char* base = static_cast<char*>(ws);
+  Q4RowsParams r = q4_rows_params(kv, q->layer);
+  r.dst[0] = reinterpret_cast<__nv_bfloat16*>(base);
+  r.dst[1] = reinterpret_cast<__nv_bfloat16*>(base + w.v_off);
+  r.n_new = p.n_new;
+  r.n_q = p.n_q;
+  r.n_sink = p.n_sink;
+  r.window = p.window;
+  r.n_valid_out = reinterpret_cast<int32_t*>(base + w.valid_off);
+  r.n_new_out = reinterpret_cast<int32_t*>(base + w.new_off);
+  const cudaError_t e = launch_q4_rows(r, kv->head_dim, stream);
+  if (e != cudaSuccess) return TRI_ERR_CUDA;
+  // the rows as a bf16 cache of one layer
+  p.k = r.dst[0];
+  p.v = r.dst[1];
+  p.n_valid = r.n_valid_out;
+  p.n_new = r.n_new_out;
+  p.n_layers = 1;
+  p.layer = 0;
+  p.rows = RowMap{};
+  p.rows.row_bytes = kv->head_dim * 2;
+  p.rows.lh_count = p.rows.n_kv_heads = kv->n_kv_heads;
+  p.rows.slice_bytes = static_cast<int64_t>(kv->n_cap) * p.rows.row_bytes;
+  p.out = out;
+  p.lse = lse;
+  return attn_status(launch_attn_prefill(p, TRI_BF16, kv->head_dim, stream));
+}
+
+tri_status tri_read_rows(const tri_kv* kv, int32_t layer, void* k_out, void* v_out, tri_stream_t stream) {
+  TRI_CALL_RANGE();
+  const tri_status st = check_kv(kv, true, true);
+  if (st != TRI_OK) return st;
+  if (kv->dtype != TRI_Q4) return TRI_ERR_UNSUPPORTED;
+  if (layer < 0 || layer >= kv->n_layers) return TRI_ERR_INVALID_ARG;
+  if ((!k_out && !v_out) || !aligned(k_out, 16) || !aligned(v_out, 16)) return TRI_ERR_INVALID_ARG;
+  Q4RowsParams r = q4_rows_params(kv, layer);
+  r.dst[0] = static_cast<__nv_bfloat16*>(k_out);
+  r.dst[1] = static_cast<__nv_bfloat16*>(v_out);
+  return launch_q4_rows(r, kv->head_dim, stream) == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
+}
+
+tri_status tri_append(const tri_kv* kv, const tri_tokens* t, tri_stream_t stream) {
+  TRI_CALL_RANGE();
+  const tri_status st = check_kv(kv, true, true);
+  if (st != TRI_OK) return st;
+  if (!t || !t->k || !aligned(t->k, 16) || !t->v || !aligned(t->v, 16)) return TRI_ERR_INVALID_ARG;
+  if (!t->positions || !aligned(t->positions, 4) || (t->n_new && !aligned(t->n_new, 4))) return TRI_ERR_INVALID_ARG;
+  if (t->n_q < 1 || t->n_q > 0x7fffffff - 256 || t->layer < 0 || t->layer >= kv->n_layers) return TRI_ERR_INVALID_ARG;
+  if (t->n_axes < 1 || t->n_axes > 4 || (t->n_axes > 1 && !t->band_axis)) return TRI_ERR_INVALID_ARG;
+  if (t->style != TRI_ROPE_INTERLEAVED && t->style != TRI_ROPE_HALF) return TRI_ERR_INVALID_ARG;
+  if (!(t->rope_theta > 1.0) || !std::isfinite(t->rope_theta)) return TRI_ERR_INVALID_ARG;
+  const bool post = kv->key_layout == TRI_KEYS_POST_ROPE;
+  if (!post && (t->n_axes > 1 || kv->dtype == TRI_Q4)) return TRI_ERR_UNSUPPORTED;
+  AppendParams p{};
+  const int64_t e = kv->dtype == TRI_F32 ? 4 : 2, d = kv->head_dim;
+  auto strides_ok = [&](int64_t seq, int64_t token, int64_t heads) {
+    return seq >= 0 && token >= 0 && (seq * e) % 16 == 0 && (token * e) % 16 == 0 && (t->n_q == 1 || token >= heads * d);
+  };
+  if (!strides_ok(t->k_seq_stride, t->k_token_stride, kv->n_kv_heads) ||
+      !strides_ok(t->v_seq_stride, t->v_token_stride, kv->n_kv_heads))
+    return TRI_ERR_INVALID_ARG;
+  if (t->q) {
+    if (!aligned(t->q, 16) || !t->q_out || !aligned(t->q_out, 16) || t->group < 1 || t->group > MAX_GROUP) return TRI_ERR_INVALID_ARG;
+    const int64_t hq = static_cast<int64_t>(kv->n_kv_heads) * t->group;
+    if (!strides_ok(t->q_seq_stride, t->q_token_stride, hq) || !strides_ok(t->q_out_seq_stride, t->q_out_token_stride, hq))
+      return TRI_ERR_INVALID_ARG;
+    // the results' rows are apart: whole sequences, or whole tokens, behind one another
+    using wide = __int128;
+    const wide row = hq * d, seq = t->q_out_seq_stride, token = t->q_out_token_stride;
+    if (kv->n_seq > 1 && seq < (t->n_q - 1) * token + row && (seq < row || token < (kv->n_seq - 1) * seq + row)) return TRI_ERR_INVALID_ARG;
+    if (t->q == t->q_out && ((kv->n_seq > 1 && t->q_seq_stride != t->q_out_seq_stride) ||
+                             (t->n_q > 1 && t->q_token_stride != t->q_out_token_stride)))
+      return TRI_ERR_INVALID_ARG;
+  }
+  for (int f = 0; f < kv->head_dim / 2; ++f) {
+    const int a = t->band_axis ? t->band_axis[f] : 0;
+    if (a >= t->n_axes) return TRI_ERR_INVALID_ARG;
+    p.axis_bits[f / 16] |= static_cast<uint32_t>(a) << (2 * (f % 16));
+    p.nu[f] = nu_fixed(std::pow(t->rope_theta, -2.0 * f / kv->head_dim));
+  }
+  p.k = static_cast<char*>(kv->k);
+  p.v = static_cast<char*>(kv->v);
+  p.pos = kv->pos;
+  p.n_valid = kv->n_valid;
+  p.dev_status = kv->dev_status;
+  p.rows = row_map(kv);
+  p.n_cap = kv->n_cap;
+  p.n_seq = kv->n_seq;
+  p.n_layers = kv->n_layers;
+  p.n_kv_heads = kv->n_kv_heads;
+  p.layer = t->layer;
+  p.kn = t->k;
+  p.vn = t->v;
+  p.k_seq = t->k_seq_stride;
+  p.k_token = t->k_token_stride;
+  p.v_seq = t->v_seq_stride;
+  p.v_token = t->v_token_stride;
+  p.q = t->q;
+  p.q_out = t->q_out;
+  p.q_seq = t->q_seq_stride;
+  p.q_token = t->q_token_stride;
+  p.qo_seq = t->q_out_seq_stride;
+  p.qo_token = t->q_out_token_stride;
+  p.positions = t->positions;
+  p.n_new = t->n_new;
+  p.n_axes = t->n_axes;
+  p.n_q = t->n_q;
+  p.group = t->q ? t->group : 0;
+  p.rotate_k = post;
+  return launch_append(p, kv->dtype, kv->head_dim, t->style, stream) == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
+}
+
 tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* lse, int64_t lse_seq_stride, float* mass,
                          tri_stream_t stream) {
   TRI_CALL_RANGE();
@@ -727,7 +888,7 @@ tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* ls
 tri_status tri_mass_evict(const float* mass, float* mass_out, const tri_kv* kv, int32_t n_prompt, int32_t n_recent,
                           int32_t budget, int32_t* keep_idx, tri_stream_t stream) {
   TRI_CALL_RANGE();
-  tri_status st = check_kv(kv, true);
+  tri_status st = check_kv(kv, true, true);
   if (st != TRI_OK) return st;
   if (!kv->pos_out || !mass || !aligned(mass, 4) || !mass_out || !aligned(mass_out, 4)) return TRI_ERR_INVALID_ARG;
   if (!keep_idx || !aligned(keep_idx, 4)) return TRI_ERR_INVALID_ARG;
@@ -747,7 +908,7 @@ tri_status tri_mass_evict(const float* mass, float* mass_out, const tri_kv* kv, 
 
 tri_status tri_paged_blocks_used(const tri_kv* kv, int32_t* blocks_used, tri_stream_t stream) {
   TRI_CALL_RANGE();
-  tri_status st = check_kv(kv, false);
+  tri_status st = check_kv(kv, false, true);
   if (st != TRI_OK) return st;
   if (!kv->block_table || !blocks_used || !aligned(blocks_used, 4)) return TRI_ERR_INVALID_ARG;
   const cudaError_t e = launch_blocks_used(row_map(kv), kv->n_valid, blocks_used, kv->n_seq, stream);

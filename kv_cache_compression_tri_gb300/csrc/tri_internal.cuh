@@ -2,6 +2,7 @@
 // kernels of libtri (GPU side only; the oracle has its own code).
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 #include <stdint.h>
@@ -362,6 +363,47 @@ struct AttnParams {
   float* logits;                   // [layer slices][n_cap][group], visible rows (mass only)
 };
 
+// New tokens into one layer's slices (append.cu).
+struct AppendParams {
+  char* k;
+  char* v;
+  int32_t* pos;            // [S][n_cap], or NULL
+  int32_t* n_valid;        // [S]
+  int32_t* dev_status;
+  RowMap rows;
+  int32_t n_cap, n_seq, n_layers, n_kv_heads, layer;
+  const void* kn;          // the tokens' rows; strides in elements
+  const void* vn;
+  int64_t k_seq, k_token, v_seq, v_token;
+  const void* q;           // or NULL
+  void* q_out;
+  int64_t q_seq, q_token, qo_seq, qo_token;
+  const int32_t* positions;  // [n_seq][n_q][n_axes]
+  const int32_t* n_new;    // [n_seq], or NULL: n_q
+  int32_t n_axes, n_q, group;
+  int32_t rotate_k;        // the cache holds rotated keys
+  // launch shape (append_plan): a warp takes a token and heads_per_warp KV heads; a CTA
+  // token_ways tokens, and as many runs of heads as that leaves warps for
+  int32_t heads_per_warp, token_ways, token_tiles, head_tiles;
+  uint64_t nu[MAX_BANDS];  // turns per position, 0.64 fixed point
+  uint32_t axis_bits[MAX_BANDS / 16];  // two bits per band
+};
+
+// One layer's rows of a 4-bit cache as bf16 values (q4_rows.cu).
+struct Q4RowsParams {
+  const char* src[2];      // K, V
+  __nv_bfloat16* dst[2];   // [n_seq][n_kv_heads][n_cap][d] each, or NULL
+  const int32_t* n_valid;
+  int32_t* dev_status;
+  RowMap rows;
+  int32_t n_cap, n_seq, n_layers, n_kv_heads, layer;
+  // for a chunk of queries: rows that none of them sees are left out or zero, and
+  const int32_t* n_new;    // [n_seq], or NULL: n_q
+  int32_t n_q, n_sink, window;
+  int32_t* n_new_out;      // [n_seq]: n_new, or 0 for a sequence with a fault; NULL: all rows, for the caller
+  int32_t* n_valid_out;    // [n_seq][n_kv_heads]: the layer's row counts
+};
+
 struct CalibParams {
   const void* q;
   float* ws;
@@ -446,6 +488,10 @@ cudaError_t launch_attn_decode(const AttnParams& p, int max_rows, tri_dtype dt, 
 cudaError_t launch_attn_prefill(const AttnParams& p, tri_dtype dt, int head_dim, cudaStream_t st);
 // The weights a chunk of queries gives every row, added to the rows' masses.
 cudaError_t launch_attn_mass(const AttnParams& p, tri_dtype dt, int head_dim, cudaStream_t st);
+// New tokens into one layer of the cache: the rows, then (in the same launch where
+// one CTA has all of a slice's tokens) the row counts. dt: the cache's type.
+cudaError_t launch_append(AppendParams& p, tri_dtype dt, int head_dim, tri_rope_style style, cudaStream_t st);
+cudaError_t launch_q4_rows(const Q4RowsParams& p, int head_dim, cudaStream_t st);
 // Selection by mass, then compaction of K, V, positions and masses.
 cudaError_t launch_mass_evict(const SelectParams& ps, const CompactParams& pc, int n_slices, cudaStream_t st);
 
