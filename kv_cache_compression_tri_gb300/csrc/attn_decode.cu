@@ -785,6 +785,32 @@ int attn_decode_max_splits(int n_slices, int max_rows) {
   return max(1, min(min(MAX_SPLIT, fill), most));
 }
 
+// Runs per slice of a 4-bit cache, for slices of max_rows. Measured (us; back to back; c: joined in a
+// cluster, k: by a second kernel; d 128, group 4, the last line d 64, group 1):
+//   slices x rows   1c    2c    4c    8c    2k    4k    7k    8k    14k   19k   38k
+//     8 x 2113     20.8  15.9  12.6  10.8  14.6  12.6  12.4  10.6  12.6  12.6   -
+//     8 x 32768   174.8  92.7  51.7  31.2  92.7  51.7  35.1  31.2  23.1  21.2  21.0
+//    32 x 8192     51.7  31.2  21.0  16.9  31.2  21.0  20.8  18.8  19.0  19.0  24.3
+//   128 x 8192     55.6  43.7  41.7  45.8  43.9  41.7  42.1  41.7  45.8  50.1   -
+//   128 x 32768   203.9 144.1 131.2 134.5 144.9 131.8 121.1 121.1 123.6 126.5   -
+//   256 x 2048     25.5  25.5  28.0  38.6  25.5  26.9  31.7  31.7  41.9   -     -
+//   512 x 2176     29.2  32.1  41.9   -    30.2  33.9  41.7   -     -     -     -
+// Four CTAs fit an SM. A cluster of the largest power of two whose runs are there at once; few slices of long
+// rows need more runs than a cluster holds, two CTAs per SM of them (each has its start and its sums to join);
+// runs of 4096 rows and more are cut in two, so that what an SM lacks at the end is shorter; and where a
+// cluster's runs would leave a fifth of the last wave empty, more runs that fill it.
+static DecodePlan attn_decode_plan_q4(int n_slices, int max_rows) {
+  const int64_t n = n_slices, slots = 4 * 152;
+  int s = 1;
+  while (2 * s <= MAX_CLUSTER && n * 2 * s <= slots && max_rows >= 64 * 2 * s) s *= 2;
+  const int64_t few = min(slots / 2 / n, static_cast<int64_t>(max_rows / 384));
+  if (few > s) return {static_cast<int>(min(few, static_cast<int64_t>(MAX_SPLIT))), false};
+  if (max_rows / s >= 4096) return {2 * s, false};
+  for (int k = s; k <= 4 * s && max_rows >= 512 * k; ++k)
+    if (n * k * 5 >= (n * k + slots - 1) / slots * slots * 4) return {k, k == s};
+  return {s, true};
+}
+
 // Runs per slice, for slices of max_rows. Measured (us; bf16, d 128, group 4;
 // c: joined in a cluster, k: by a second kernel):
 //   slices x rows   1c    2c    4c    8c    16c   3k    6k    12k   19k   38k   76k
@@ -802,7 +828,8 @@ int attn_decode_max_splits(int n_slices, int max_rows) {
 // cluster holds; more slices than slots that leave the last wave part empty are
 // cut into a few runs (512 slices of 2048 rows, d 64, group 1, masses: 1c 62.9,
 // 3k 54.4).
-DecodePlan attn_decode_plan(int n_slices, int max_rows) {
+DecodePlan attn_decode_plan(int n_slices, int max_rows, tri_dtype dt) {
+  if (dt == TRI_Q4) return attn_decode_plan_q4(n_slices, max_rows);
   const int64_t n = n_slices, slots = 2 * 152;
   int s = 1;
   while (2 * s <= MAX_CLUSTER && n * 2 * s <= slots && max_rows >= 64 * 2 * s) s *= 2;

@@ -23,9 +23,10 @@
 //   an element come together by a byte permute of their words, before they are
 //   spread. B = p s_j in fp16, p up to 2^4 (a scale is below 2^12): two
 //   roundings of 2^-11 of its weight, where results are rounded to 2^-9.
-// Each warp owns a ring of NST tiles of 32 rows, K and V, a bulk copy each (two in
-// pools of 16-row blocks); table entries are read a tile ahead. Rows out of sight are
-// copied but not used: their weight and their pairs (any bits) are set to zero.
+// Each warp owns a ring of NST tiles of 32 rows, K and V, filled by 16-byte asynchronous copies
+// of whole contiguous tiles (bulk copies by lanes of a warp took 20 instructions more per 16 rows
+// than these); table entries are read a tile ahead. Rows out of sight are copied but not
+// used: their weight and their pairs (any bits) are set to zero.
 #pragma once
 
 #include "q4_common.cuh"
@@ -39,7 +40,7 @@ struct TileGeo<Q4Tag, D> {
   static constexpr int ROW = Q4Row<D>::BYTES;
   static constexpr int TK = 32;
   static constexpr int TILE = TK * ROW;
-  static constexpr int NST = 3;
+  static constexpr int NST = 2;
   static constexpr int WARP_RING = NST * 2 * TILE;
   static constexpr int SMEM = NW * WARP_RING;
 };
@@ -49,6 +50,16 @@ __device__ __forceinline__ void mma16816h(float (&c)[4], uint32_t a0, uint32_t a
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The first product of a sum.
+__device__ __forceinline__ void mma16816h_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void cp_async16_all(uint32_t dst, const char* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   uint32_t r;
@@ -60,7 +71,7 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ float scale_of(uint32_t pair) { return __half2float(__ushort_as_half(static_cast<unsigned short>(pair & 0xffff))); }
+__device__ __forceinline__ float scale_of(uint32_t pair) { return __low2float(*reinterpret_cast<const __half2*>(&pair)); }
 // A lane's words of a row of codes.
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
@@ -132,14 +143,13 @@ __device__ __forceinline__ void query_fragments(const __nv_bfloat16* q, bool liv
 }
 
 template <int D, bool PAGED>
-__global__ void __launch_bounds__(NW * 32, 3) decode_q4_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_constant__ AttnParams p) {
   using G = TileGeo<Q4Tag, D>;
   constexpr int NWD = Q4Row<D>::WORDS, CODES = Q4Row<D>::CODES, LANE = 4 * NWD;  // bytes of a lane's codes
   constexpr float LIFT = 4.f;  // log2 of the largest weight
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float sm_m[NW][8], sm_l[NW][8];
   __shared__ float2 run_ml[MAX_GROUP];
-  __shared__ uint64_t bars[NW][G::NST];
   const int ls = blockIdx.x / p.n_split, split = blockIdx.x % p.n_split;
   const int t = threadIdx.x, w = t >> 5, lane = t & 31, lg = lane >> 2, lt = lane & 3;
   const int64_t pi = static_cast<int64_t>(blockIdx.x) * p.group;
@@ -151,62 +161,58 @@ __global__ void __launch_bounds__(NW * 32, 3) decode_q4_kernel(const __grid_cons
   }
   const Tiles<Q4Tag, D> tl(p, r, split);
 
-  // The warp's ring. A tile's rows lie in `parts` runs of 16 or 32 rows; their blocks (or -1)
-  // are looked up a tile before the copies.
+  // The warp's ring. A tile's rows lie in one run, or in two of 16-row blocks, whose table
+  // entries (-1: no row there) are read a tile before the copies.
+  constexpr int CHUNKS = G::TILE / 16, PER_LANE = CHUNKS / 32;  // 16-byte chunks of one tensor's tile
+  static_assert(CHUNKS % 32 == 0, "a tile in whole copies of a warp");
   const uint32_t ring = smem_addr(smem) + w * G::WARP_RING;
-  unsigned char* ring_p = smem + w * G::WARP_RING;
   bool blocks_ok = true;
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < G::NST; ++i) mbar_init(&bars[w][i], 1);
-    mbar_init_fence();
-  }
-  __syncwarp();
-  const int run_rows = PAGED ? min(G::TK, p.rows.block_size) : G::TK;
+  const char *kbase = static_cast<const char*>(p.k) + tl.base, *vbase = static_cast<const char*>(p.v) + tl.base;
+  const bool half_runs = PAGED && p.rows.block_size < G::TK;
   struct Blocks {
     int b[2];
   };
   auto look_up = [&](int u) {
-    Blocks b{{0, 0}};
-    if (PAGED && lane == 0 && u < tl.u1) {
+    Blocks b{{-1, -1}};
+    if (PAGED && u < tl.u1) {
       const int r0 = tl.row(u);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int rs = r0 + 16 * k;
-        if (k == 1 && run_rows > 16) continue;
-        b.b[k] = rs < r.n ? __ldg(tl.trow + (rs >> p.rows.block_shift)) : -1;
-      }
+      b.b[0] = __ldg(tl.trow + (r0 >> p.rows.block_shift));
+      if (half_runs && r0 + 16 < r.n) b.b[1] = __ldg(tl.trow + (r0 >> p.rows.block_shift) + 1);
     }
     return b;
   };
   auto fetch = [&](int u, int st, const Blocks& b) {
-    if (lane != 0) return;
-    const int r0 = tl.row(u);
-    int64_t off[2];
-    int bytes[2] = {0, 0};
+    const int r0 = tl.row(u), at = PAGED ? r0 & (p.rows.block_size - 1) : r0;
+    const uint32_t dst = ring + 2 * st * G::TILE + 16 * lane;
+    if (r0 + G::TK <= r.n && !half_runs && (!PAGED || (b.b[0] >= 0 && b.b[0] < p.rows.num_blocks))) {
+      const int64_t off = (PAGED ? b.b[0] * p.rows.block_bytes : 0) + static_cast<int64_t>(at) * G::ROW + 16 * lane;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int rs = r0 + k * run_rows;
-      if ((PAGED ? k * run_rows >= G::TK : k == 1) || rs >= r.n) continue;
-      off[k] = tl.base + static_cast<int64_t>(rs) * G::ROW;
-      if (PAGED) {
-        const int blk = b.b[k];
-        if (blk < 0 || blk >= p.rows.num_blocks) {
-          // rows that nobody sees may have no block any more
-          if (rs < r.vis.s1 || rs + run_rows - 1 >= r.vis.w0) blocks_ok = false;
-          continue;
-        }
-        off[k] = tl.base + blk * p.rows.block_bytes + static_cast<int64_t>(rs & (p.rows.block_size - 1)) * G::ROW;
+      for (int i = 0; i < PER_LANE; ++i) {
+        cp_async16_all(dst + 512 * i, kbase + off + 512 * i);
+        cp_async16_all(dst + G::TILE + 512 * i, vbase + off + 512 * i);
       }
-      bytes[k] = min(run_rows, r.n - rs) * G::ROW;
+      return;
     }
-    mbar_arrive_expect_tx(&bars[w][st], static_cast<uint32_t>(2 * (bytes[0] + bytes[1])));
-    unsigned char* dst = ring_p + st * 2 * G::TILE;
+    bool ok[2] = {true, true};
+    if (PAGED) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (bytes[k] == 0) continue;
-      bulk_g2s(dst + k * 16 * G::ROW, static_cast<const char*>(p.k) + off[k], bytes[k], &bars[w][st]);
-      bulk_g2s(dst + G::TILE + k * 16 * G::ROW, static_cast<const char*>(p.v) + off[k], bytes[k], &bars[w][st]);
+      for (int k = 0; k < 2; ++k) {
+        const int rs = r0 + 16 * k;
+        if ((k == 1 && !half_runs) || rs >= r.n) continue;
+        ok[k] = b.b[k] >= 0 && b.b[k] < p.rows.num_blocks;
+        // rows that nobody sees may have no block any more
+        if (!ok[k] && (rs < r.vis.s1 || rs + (half_runs ? 16 : G::TK) - 1 >= r.vis.w0)) blocks_ok = false;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < PER_LANE; ++i) {  // rows that are not there: zeros
+      const int c = lane + 32 * i, row = c / (G::ROW / 16);
+      const bool second = half_runs && row >= 16;
+      const bool live = r0 + row < r.n && (second ? ok[1] : ok[0]);
+      const int64_t off = (PAGED ? (second ? b.b[1] : b.b[0]) * p.rows.block_bytes : 0) + static_cast<int64_t>(at) * G::ROW +
+                          16 * (second ? c - G::ROW : c);
+      cp_async16(dst + 512 * i, kbase + (live ? off : 0), live);
+      cp_async16(dst + G::TILE + 512 * i, vbase + (live ? off : 0), live);
     }
   };
   Blocks ahead{};
@@ -214,6 +220,7 @@ __global__ void __launch_bounds__(NW * 32, 3) decode_q4_kernel(const __grid_cons
   for (int i = 0; i < G::NST - 1; ++i) {
     const int u = tl.u0 + w + i * NW;
     if (u < tl.u1) fetch(u, i, look_up(u));
+    cp_async_commit();
   }
   ahead = look_up(tl.u0 + w + (G::NST - 1) * NW);
 
@@ -226,8 +233,9 @@ __global__ void __launch_bounds__(NW * 32, 3) decode_q4_kernel(const __grid_cons
                        lg < p.group, lt, qf, qsum, shift);
     const int s0 = __shfl_sync(FULL_MASK, shift, 8 * lt), s1 = __shfl_sync(FULL_MASK, shift, 8 * lt + 4);
     const float sl = p.scale * LOG2E;
-    f0 = sl * __uint_as_float(static_cast<uint32_t>(127 + 24 - s0) << 23);
-    f1 = sl * __uint_as_float(static_cast<uint32_t>(127 + 24 - s1) << 23);
+    // (not 0, which an invisible row's -inf would not survive)
+    f0 = fmaxf(sl * __uint_as_float(static_cast<uint32_t>(127 + 24 - s0) << 23), 0x1p-126f);
+    f1 = fmaxf(sl * __uint_as_float(static_cast<uint32_t>(127 + 24 - s1) << 23), 0x1p-126f);
   }
 
   float o[D / 16][4], om[4] = {0.f, 0.f, 0.f, 0.f};
@@ -239,21 +247,10 @@ __global__ void __launch_bounds__(NW * 32, 3) decode_q4_kernel(const __grid_cons
   float m0 = NEG_INF, m1 = NEG_INF, l0 = 0.f, l1 = 0.f;
   float* logits = p.logits ? p.logits + static_cast<int64_t>(ls) * p.n_cap * p.group : nullptr;
   const uint32_t half_sel = lg >= 4 ? 0x7632 : 0x5410;
-  int st = 0;
-  uint32_t phase = 0;
-  bool landed = true;
-  for (int u = tl.u0 + w; u < tl.u1; u += NW) {
-    {
-      const int nx = u + (G::NST - 1) * NW, ns = st == 0 ? G::NST - 1 : st - 1;
-      if (nx < tl.u1) fetch(nx, ns, ahead);
-      ahead = look_up(nx + NW);
-    }
-    landed = mbar_wait_bounded(&bars[w][st], phase);
-    landed = __all_sync(FULL_MASK, landed);
-    if (!landed) break;
-    const int r0 = tl.row(u);
-    const bool inner = r0 + G::TK <= r.n && (r0 >= r.vis.w0 || r0 + G::TK <= r.vis.s1);
-    const uint32_t tk = ring + st * 2 * G::TILE, tv = tk + G::TILE;
+  // A tile's rows r0 .. from `tk`; all: every one of them is in sight.
+  auto tile = [&](auto all, int r0, uint32_t tk) {
+    constexpr bool INNER = decltype(all)::value;
+    const uint32_t tv = tk + G::TILE;
     float x[2][4];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -265,8 +262,8 @@ __global__ void __launch_bounds__(NW * 32, 3) decode_q4_kernel(const __grid_cons
       lds_words(rb + CODES, pb);
       {
         const uint32_t ma = lds32(ra + CODES + 4 * lt), mb = lds32(rb + CODES + 4 * lt);
-        float y[4] = {0.f, 0.f, 0.f, 0.f};
-        mma16816h(y, __byte_perm(ma, ma, 0x3232), __byte_perm(mb, mb, 0x3232), 0u, 0u, qsum, 0u);
+        float y[4];
+        mma16816h_first(y, __byte_perm(ma, ma, 0x3232), __byte_perm(mb, mb, 0x3232), 0u, 0u, qsum, 0u);
 #pragma unroll
         for (int c = 0; c < 4; ++c) x[s][c] = y[c] * 0x1p-19f;
       }
@@ -274,17 +271,18 @@ __global__ void __launch_bounds__(NW * 32, 3) decode_q4_kernel(const __grid_cons
       for (int k = 0; k < NWD; ++k) {
         const uint32_t a8 = wa[k] >> 8, b8 = wb[k] >> 8;
         constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u;
-        float y[4] = {0.f, 0.f, 0.f, 0.f};
-        mma16816h(y, wa[k] & LO, wb[k] & LO, wa[k] & HI, wb[k] & HI, qf[2 * k][0], qf[2 * k][1]);
+        float y[4];
+        mma16816h_first(y, wa[k] & LO, wb[k] & LO, wa[k] & HI, wb[k] & HI, qf[2 * k][0], qf[2 * k][1]);
         if constexpr (D == 64) {
           const float sa = scale_of(pa[2 * k]), sb = scale_of(pb[2 * k]);
           x[s][0] = fmaf(y[0], sa, x[s][0]);
           x[s][1] = fmaf(y[1], sa, x[s][1]);
           x[s][2] = fmaf(y[2], sb, x[s][2]);
           x[s][3] = fmaf(y[3], sb, x[s][3]);
-          y[0] = y[1] = y[2] = y[3] = 0.f;
+          mma16816h_first(y, a8 & LO, b8 & LO, a8 & HI, b8 & HI, qf[2 * k + 1][0], qf[2 * k + 1][1]);
+        } else {
+          mma16816h(y, a8 & LO, b8 & LO, a8 & HI, b8 & HI, qf[2 * k + 1][0], qf[2 * k + 1][1]);
         }
-        mma16816h(y, a8 & LO, b8 & LO, a8 & HI, b8 & HI, qf[2 * k + 1][0], qf[2 * k + 1][1]);
         constexpr int QS = D == 64 ? 2 : 1;
         const float sa = scale_of(pa[QS * k + QS - 1]), sb = scale_of(pb[QS * k + QS - 1]);
         x[s][0] = fmaf(y[0], sa, x[s][0]);
@@ -292,12 +290,8 @@ __global__ void __launch_bounds__(NW * 32, 3) decode_q4_kernel(const __grid_cons
         x[s][2] = fmaf(y[2], sb, x[s][2]);
         x[s][3] = fmaf(y[3], sb, x[s][3]);
       }
-      x[s][0] *= f0;
-      x[s][1] *= f1;
-      x[s][2] *= f0;
-      x[s][3] *= f1;
       const int ja = r0 + 16 * s + lg, jb = ja + 8;
-      if (!inner) {
+      if (!INNER) {
         if (!(ja < r.n && (ja < r.vis.s1 || ja >= r.vis.w0))) x[s][0] = x[s][1] = NEG_INF;
         if (!(jb < r.n && (jb < r.vis.s1 || jb >= r.vis.w0))) x[s][2] = x[s][3] = NEG_INF;
       }
@@ -305,19 +299,19 @@ __global__ void __launch_bounds__(NW * 32, 3) decode_q4_kernel(const __grid_cons
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int j = c < 2 ? ja : jb, g = 2 * lt + (c & 1);
-          if (g < p.group && j < r.n) logits[static_cast<int64_t>(j) * p.group + g] = x[s][c];
+          if (g < p.group && j < r.n) logits[static_cast<int64_t>(j) * p.group + g] = x[s][c] * (c & 1 ? f1 : f0);
         }
       }
     }
-    float mx0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-    float mx1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
-    if (__any_sync(FULL_MASK, mx0 - LIFT > m0 || mx1 - LIFT > m1)) {
+    float mx0 = fmaf(fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2])), f0, -LIFT);
+    float mx1 = fmaf(fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3])), f1, -LIFT);
+    if (__any_sync(FULL_MASK, mx0 > m0 || mx1 > m1)) {
 #pragma unroll
       for (int k = 4; k <= 16; k <<= 1) {
         mx0 = fmaxf(mx0, __shfl_xor_sync(FULL_MASK, mx0, k));
         mx1 = fmaxf(mx1, __shfl_xor_sync(FULL_MASK, mx1, k));
       }
-      const float n0 = fmaxf(m0, mx0 - LIFT), n1 = fmaxf(m1, mx1 - LIFT);
+      const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
       const float a0 = n0 == NEG_INF ? 1.f : fast_exp2(m0 - n0), a1 = n1 == NEG_INF ? 1.f : fast_exp2(m1 - n1);
       m0 = n0;
       m1 = n1;
@@ -333,10 +327,11 @@ __global__ void __launch_bounds__(NW * 32, 3) decode_q4_kernel(const __grid_cons
       om[0] *= a0;
       om[1] *= a1;
     }
-    const float z0 = m0 == NEG_INF ? 0.f : m0, z1 = m1 == NEG_INF ? 0.f : m1;
+    const float z0 = !INNER && m0 == NEG_INF ? 0.f : m0, z1 = !INNER && m1 == NEG_INF ? 0.f : m1;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const float e[4] = {fast_exp2(x[s][0] - z0), fast_exp2(x[s][1] - z1), fast_exp2(x[s][2] - z0), fast_exp2(x[s][3] - z1)};
+      const float e[4] = {fast_exp2(fmaf(x[s][0], f0, -z0)), fast_exp2(fmaf(x[s][1], f1, -z1)), fast_exp2(fmaf(x[s][2], f0, -z0)),
+                          fast_exp2(fmaf(x[s][3], f1, -z1))};
       l0 += e[0] + e[2];
       l1 += e[1] + e[3];
       const uint32_t p01 = transpose8(pack_half(e[0], e[1])), p89 = transpose8(pack_half(e[2], e[3]));  // rows 2 lt, + 1, + 8, + 9; head lg
@@ -348,7 +343,7 @@ __global__ void __launch_bounds__(NW * 32, 3) decode_q4_kernel(const __grid_cons
         lds_words(a + LANE * (lg & 3), vw[k]);
         lds_words(a + CODES, vp[k]);
         vm[k] = lds32(a + CODES + 4 * (lg & 3));
-        if (!inner) {
+        if (!INNER) {
           const int j = r0 + row;
           if (!(j < r.n && (j < r.vis.s1 || j >= r.vis.w0))) {
             vm[k] = 0u;
@@ -374,19 +369,27 @@ __global__ void __launch_bounds__(NW * 32, 3) decode_q4_kernel(const __grid_cons
         mma16816h(o[2 * k + 1], z01 & LO, z01 & HI, z89 & LO, z89 & HI, b0[jb], b1[jb]);
       }
     }
-    __syncwarp();  // the stage may be refilled
-    if (lane == 0) fence_proxy_async_smem();
-    if (++st == G::NST) {
-      st = 0;
-      phase ^= 1;
+  };
+  int st = 0;
+  for (int u = tl.u0 + w; u < tl.u1; u += NW) {
+    {
+      const int nx = u + (G::NST - 1) * NW, ns = st == 0 ? G::NST - 1 : st - 1;
+      if (nx < tl.u1) fetch(nx, ns, ahead);
+      cp_async_commit();
+      ahead = look_up(nx + NW);
     }
+    cp_async_wait<G::NST - 1>();
+    __syncwarp();
+    const int r0 = tl.row(u);
+    const uint32_t tk = ring + st * 2 * G::TILE;
+    if (r0 + G::TK <= r.n && (r0 >= r.vis.w0 || r0 + G::TK <= r.vis.s1))
+      tile(std::true_type{}, r0, tk);
+    else
+      tile(std::false_type{}, r0, tk);
+    __syncwarp();  // the stage may be refilled
+    st = st + 1 == G::NST ? 0 : st + 1;
   }
-  if (!landed) {
-    // a copy never came: report it, skip the slice, and let the copies in flight end
-    set_status(p.dev_status, TRI_DEV_TIMEOUT);
-    blocks_ok = false;
-    for (int k = 0; k < G::NST; ++k) (void)mbar_wait_bounded(&bars[w][(st + k) % G::NST], st + k >= G::NST ? phase ^ 1 : phase);
-  }
+  cp_async_wait<0>();
 #pragma unroll
   for (int k = 4; k <= 16; k <<= 1) {
     l0 += __shfl_xor_sync(FULL_MASK, l0, k);
