@@ -25,26 +25,42 @@ constexpr int RT = 256;    // threads per CTA
 constexpr int CHUNK = 64;  // rows of a CTA, K and V
 constexpr int SIGHT = 128; // rows that an attention tile reads together
 
-// Eight elements, number 8 c .. 8 c + 7, of the 4-bit row at `row`.
+// Elements 8 c .. 8 c + 7 of a 4-bit row: their words, and their quarter's pair.
+struct Eight {
+  uint32_t a, b, pair;
+};
 template <int D>
-__device__ __forceinline__ uint4 unpack8(const char* row, int c) {
+__device__ __forceinline__ Eight load8(const char* row, int c) {
   const int j = c / (D / 32);  // quarter
-  const uint32_t pair = __ldg(reinterpret_cast<const uint32_t*>(row + Q4Row<D>::CODES) + j);
-  const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(pair & 0xffff)));
-  const float m = __half2float(__ushort_as_half(static_cast<unsigned short>(pair >> 16)));
   const uint32_t* words = reinterpret_cast<const uint32_t*>(row);
-  uint32_t n;  // the eight codes, in order
+  Eight x;
+  x.pair = __ldg(reinterpret_cast<const uint32_t*>(row + Q4Row<D>::CODES) + j);
   if constexpr (D == 128) {
-    n = __ldg(words + 4 * (c & 3) + j);
+    x.a = __ldg(words + 4 * (c & 3) + j);
+    x.b = 0;
   } else {
-    // lanes 2 (c & 1) and the next: four codes each, two and two in bytes (j & 1) and 2 + (j & 1) of a word
-    const int t = 2 * (c & 1);
-    const uint32_t a = __ldg(words + 2 * t + (j >> 1)) >> (8 * (j & 1)), b = __ldg(words + 2 * t + 2 + (j >> 1)) >> (8 * (j & 1));
-    n = (a & 0xff) | (a >> 8 & 0xff00) | ((b & 0xff) | (b >> 8 & 0xff00)) << 16;
+    // of lanes 2 (c & 1) and the next
+    x.a = __ldg(words + 4 * (c & 1) + (j >> 1));
+    x.b = __ldg(words + 4 * (c & 1) + 2 + (j >> 1));
   }
+  return x;
+}
+template <int D>
+__device__ __forceinline__ uint4 values8(const Eight& w, int c) {
+  const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w.pair));  // scale, minimum
+  uint32_t n = w.a;  // the eight codes, in order
+  // (d 64: four codes of a word each, in its bytes j & 1 and 2 + (j & 1))
+  if constexpr (D == 64) n = __byte_perm(w.a, w.b, (c >> 1) & 1 ? 0x7531 : 0x6420);
+  // (a half with exponent 0 and c in its low bits is c 2^-24, four bits higher c 2^-20: exact)
   float x[8];
+  const float s0 = p.x * 0x1p24f, s1 = p.x * 0x1p20f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = fmaf(static_cast<float>(n >> (4 * e) & 15u), s, m);
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t pair = (e & 2 ? n >> 8 : n) & (e & 1 ? 0x00f000f0u : 0x000f000fu);  // codes e and e + 4
+    const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&pair));
+    x[e] = fmaf(c.x, e & 1 ? s1 : s0, p.y);
+    x[e + 4] = fmaf(c.y, e & 1 ? s1 : s0, p.y);
+  }
   return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
@@ -102,23 +118,35 @@ __global__ void __launch_bounds__(RT) q4_rows_kernel(const __grid_constant__ Q4R
   const int64_t base = p.rows.slice_base(s);
   const int c = threadIdx.x % LPR;
   const int64_t out = static_cast<int64_t>(ls) * p.n_cap;
+  // all loads of the thread, then its stores
+  constexpr int N = CHUNK * LPR / RT;
+  Eight w[N][2];
+  uint32_t write = 0;
 #pragma unroll
-  for (int i = 0; i < CHUNK * LPR / RT; ++i) {
+  for (int i = 0; i < N; ++i) {
     const int r = r0 + i * (RT / LPR) + static_cast<int>(threadIdx.x) / LPR;
-    if (r >= r1) continue;
-    bool live = !CHUNKED || r < vis.s1 || r >= vis.w0;
+    bool ok = r < r1 && (!CHUNKED || r < vis.s1 || r >= vis.w0);
     int64_t off = base + static_cast<int64_t>(r) * p.rows.row_bytes;
-    if (trow && live) {
+    if (trow && ok) {
       const int blk = __ldg(trow + (r >> p.rows.block_shift));
-      live = blk >= 0 && blk < p.rows.num_blocks;
-      if (!CHUNKED && !live) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
+      ok = blk >= 0 && blk < p.rows.num_blocks;
+      if (!CHUNKED && !ok) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
       off = base + blk * p.rows.block_bytes + static_cast<int64_t>(r & (p.rows.block_size - 1)) * p.rows.row_bytes;
     }
-    if (!CHUNKED && !live) continue;
+    if (r < r1 && (CHUNKED || ok)) write |= 1u << i;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      w[i][kv] = {0, 0, 0};  // (reads as zeros)
+      if (ok && p.dst[kv]) w[i][kv] = load8<D>(p.src[kv] + off, c);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int r = r0 + i * (RT / LPR) + static_cast<int>(threadIdx.x) / LPR;
+    if (!(write >> i & 1)) continue;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv)
-      if (p.dst[kv])
-        reinterpret_cast<uint4*>(p.dst[kv] + (out + r) * D)[c] = live ? unpack8<D>(p.src[kv] + off, c) : make_uint4(0, 0, 0, 0);
+      if (p.dst[kv]) reinterpret_cast<uint4*>(p.dst[kv] + (out + r) * D)[c] = values8<D>(w[i][kv], c);
   }
 }
 

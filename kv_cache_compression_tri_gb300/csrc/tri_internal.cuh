@@ -382,9 +382,10 @@ struct AppendParams {
   const int32_t* n_new;    // [n_seq], or NULL: n_q
   int32_t n_axes, n_q, group;
   int32_t rotate_k;        // the cache holds rotated keys
-  // launch shape (append_plan): a warp takes a token and heads_per_warp KV heads; a CTA
-  // token_ways tokens, and as many runs of heads as that leaves warps for
-  int32_t heads_per_warp, token_ways, token_tiles, head_tiles;
+  // launch shape (append_plan): tokens and KV heads of a CTA, tiles of them, and what divides by the heads
+  int32_t tokens, heads, token_tiles, head_tiles;
+  uint32_t head_magic, q_magic;
+  int2 head_step, q_step;  // the rows of a CTA's warps in one go, as tokens and heads
   uint64_t nu[MAX_BANDS];  // turns per position, 0.64 fixed point
   uint32_t axis_bits[MAX_BANDS / 16];  // two bits per band
 };
