@@ -362,16 +362,23 @@ __device__ __forceinline__ void store_q4(const AppendParams& p, char* to, bool l
 // Rows (token, head) of `toks` tokens in steps of AW groups of RPW from group g on, the next one's loads in flight:
 // f(whether there is a row, token, head, source, its chunks), by whole warps. `per`: heads of a token in
 // the numbering, `live` of them there; magic and step (AW groups as tokens and heads) belong to `per`.
+// first: the chunks of group g's row, from first_row.
+template <typename T, int D>
+__device__ __forceinline__ Raw<T> first_row(const T* base, int64_t token, int toks, int per, int live, uint32_t magic, int g, int sub, int l) {
+  const int n = g * (32 / (D / 16)) + sub, tok = div_small(n, magic), head = n - tok * per;
+  Raw<T> r{};
+  if (n < toks * per && head < live) r.template load<D>(base + tok * token + head * D, l);
+  return r;
+}
 template <typename T, int D, class Fn>
 __device__ __forceinline__ void for_rows(const T* base, int64_t token, int toks, int per, int live, uint32_t magic, int2 step, int g, int sub,
-                                         int l, Fn f) {
+                                         int l, const Raw<T>& first, Fn f) {
   constexpr int RPW = 32 / (D / 16);
   int n = g * RPW, tok = div_small(n + sub, magic), head = n + sub - tok * per;
   const T* src = base + tok * token + head * D;
   const int rows = toks * per;
-  Raw<T> next{};
+  Raw<T> next = first;
   bool in = n + sub < rows && head < live;
-  if (in) next.template load<D>(src, l);
   while (n < rows) {
     Raw<T> cur = next;
     const bool in_now = in;
@@ -393,7 +400,7 @@ __device__ __forceinline__ void for_rows(const T* base, int64_t token, int toks,
 }
 
 template <typename T, int D, bool HALF, bool Q4>
-__global__ void __launch_bounds__(AW * 32, Q4 ? 4 : 5) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(AW * 32, 4) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LANES = D / 16, RPW = 32 / LANES, F = D / 2;  // lanes of a row, rows of a warp
   constexpr int MAX_TOKENS = AW * 32 / F;
   __shared__ float4 turns[MAX_TOKENS][F / 2];
@@ -408,6 +415,18 @@ __global__ void __launch_bounds__(AW * 32, Q4 ? 4 : 5) append_kernel(const __gri
   const int nn = append_tokens(p, seq), toks = min(p.tokens, nn - i0);
   const int32_t* positions = p.positions + (static_cast<int64_t>(seq) * p.n_q + i0) * p.n_axes;
   if (toks > 0) {
+    // Rows (token, head) in groups of RPW, a warp's groups AW apart: first those of K, then of V, then of the queries,
+    // whose first groups go to the warps behind the last of the kind before.
+    const int kv_groups = (toks * H + RPW - 1) / RPW;
+    const T* kn = static_cast<const T*>(p.kn) + seq * p.k_seq + i0 * p.k_token + static_cast<int64_t>(h0) * D;
+    const T* vn = static_cast<const T*>(p.vn) + seq * p.v_seq + i0 * p.v_token + static_cast<int64_t>(h0) * D;
+    const int64_t q0 = static_cast<int64_t>(h0) * p.group * D;
+    const T* q = static_cast<const T*>(p.q) + seq * p.q_seq + i0 * p.q_token + q0;
+    const int vg = (w - kv_groups) & (AW - 1), qg = (w - 2 * kv_groups) & (AW - 1);
+    // (their loads are on the way while the sines are computed)
+    const Raw<T> k_first = first_row<T, D>(kn, p.k_token, toks, H, hc, p.head_magic, w, sub, l);
+    const Raw<T> v_first = first_row<T, D>(vn, p.v_token, toks, H, hc, p.head_magic, vg, sub, l);
+    const Raw<T> q_first = first_row<T, D>(q, p.q_token, toks, H * p.group, hc * p.group, p.q_magic, qg, sub, l);
     if (t < toks * F) {
       const int tok = t / F, e = t % F, k = e / (2 * LANES), lk = e / 2 % LANES;
       const int f = band_of<D, HALF>(lk, k, e & 1);
@@ -439,12 +458,7 @@ __global__ void __launch_bounds__(AW * 32, Q4 ? 4 : 5) append_kernel(const __gri
       dst[t] = to;
     }
     __syncthreads();
-    // Rows (token, head) in groups of RPW, a warp's groups AW apart: first those of K, then of V, then of the queries,
-    // whose first groups go to the warps behind the last of the kind before.
-    const int kv_groups = (toks * H + RPW - 1) / RPW;
-    const T* kn = static_cast<const T*>(p.kn) + seq * p.k_seq + i0 * p.k_token + static_cast<int64_t>(h0) * D;
-    const T* vn = static_cast<const T*>(p.vn) + seq * p.v_seq + i0 * p.v_token + static_cast<int64_t>(h0) * D;
-    for_rows<T, D>(kn, p.k_token, toks, H, hc, p.head_magic, p.head_step, w, sub, l, [&](bool in, int tok, int head, const T* src, Raw<T>& cur) {
+    for_rows<T, D>(kn, p.k_token, toks, H, hc, p.head_magic, p.head_step, w, sub, l, k_first, [&](bool in, int tok, int head, const T* src, Raw<T>& cur) {
       const float4* cs = turns[tok] + l;
       const int64_t off = in ? dst[tok * H + head] : -1;
       char* to = p.k + (off >= 0 ? off : 0);
@@ -464,7 +478,7 @@ __global__ void __launch_bounds__(AW * 32, Q4 ? 4 : 5) append_kernel(const __gri
         if (off >= 0) cur.template store<D>(reinterpret_cast<T*>(to), l);
       }
     });
-    for_rows<T, D>(vn, p.v_token, toks, H, hc, p.head_magic, p.head_step, (w - kv_groups) & (AW - 1), sub, l,
+    for_rows<T, D>(vn, p.v_token, toks, H, hc, p.head_magic, p.head_step, vg, sub, l, v_first,
                    [&](bool in, int tok, int head, const T* src, Raw<T>& cur) {
       const int64_t off = in ? dst[tok * H + head] : -1;
       char* to = p.v + (off >= 0 ? off : 0);
@@ -477,10 +491,8 @@ __global__ void __launch_bounds__(AW * 32, Q4 ? 4 : 5) append_kernel(const __gri
       }
     });
     if (p.q) {
-      const int64_t q0 = static_cast<int64_t>(h0) * p.group * D;
-      const T* q = static_cast<const T*>(p.q) + seq * p.q_seq + i0 * p.q_token + q0;
       T* qo = static_cast<T*>(p.q_out) + seq * p.qo_seq + i0 * p.qo_token + q0;
-      for_rows<T, D>(q, p.q_token, toks, H * p.group, hc * p.group, p.q_magic, p.q_step, (w - 2 * kv_groups) & (AW - 1), sub, l,
+      for_rows<T, D>(q, p.q_token, toks, H * p.group, hc * p.group, p.q_magic, p.q_step, qg, sub, l, q_first,
                      [&](bool in, int tok, int head, const T*, Raw<T>& cur) {
         float x[8], y[8];
         cur.get(x, y);

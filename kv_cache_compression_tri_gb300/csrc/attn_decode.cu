@@ -722,7 +722,7 @@ cudaError_t launch_join(const AttnParams& p, int max_rows, cudaStream_t st) {
 template <class Kernel>
 cudaError_t launch_runs(Kernel kern, size_t smem, const AttnParams& p, cudaStream_t st) {
   cudaError_t e;
-  if (smem > 48 * 1024) {
+  if (smem > 46 * 1024) {  // (48 KB, static shared memory included, need no asking for)
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }

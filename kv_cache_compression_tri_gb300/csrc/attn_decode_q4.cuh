@@ -23,7 +23,7 @@
 //   an element come together by a byte permute of their words, before they are
 //   spread. B = p s_j in fp16, p up to 2^4 (a scale is below 2^12): two
 //   roundings of 2^-11 of its weight, where results are rounded to 2^-9.
-// Each warp owns a ring of NST tiles of 32 rows, K and V, filled by 16-byte asynchronous copies
+// Each warp owns a ring of NST tiles of 32 (d 64: 64) rows, K and V, filled by 16-byte asynchronous copies
 // of whole contiguous tiles (bulk copies by lanes of a warp took 20 instructions more per 16 rows
 // than these); table entries are read a tile ahead. Rows out of sight are copied but not
 // used: their weight and their pairs (any bits) are set to zero.
@@ -38,7 +38,7 @@ struct Q4Tag {};
 template <int D>
 struct TileGeo<Q4Tag, D> {
   static constexpr int ROW = Q4Row<D>::BYTES;
-  static constexpr int TK = 32;
+  static constexpr int TK = D == 64 ? 64 : 32;  // (3 and 2.5 KB of K: half the loop's overhead at d 64)
   static constexpr int TILE = TK * ROW;
   static constexpr int NST = 2;
   static constexpr int WARP_RING = NST * 2 * TILE;
@@ -161,30 +161,38 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
   }
   const Tiles<Q4Tag, D> tl(p, r, split);
 
-  // The warp's ring. A tile's rows lie in one run, or in two of 16-row blocks, whose table
+  // The warp's ring. A tile's rows lie in one run, or in several of smaller blocks, whose table
   // entries (-1: no row there) are read a tile before the copies.
+  constexpr int SUB = G::TK / 16;                       // MMAs' rows of a tile
   constexpr int CHUNKS = G::TILE / 16, PER_LANE = CHUNKS / 32;  // 16-byte chunks of one tensor's tile
   static_assert(CHUNKS % 32 == 0, "a tile in whole copies of a warp");
   const uint32_t ring = smem_addr(smem) + w * G::WARP_RING;
   bool blocks_ok = true;
   const char *kbase = static_cast<const char*>(p.k) + tl.base, *vbase = static_cast<const char*>(p.v) + tl.base;
-  const bool half_runs = PAGED && p.rows.block_size < G::TK;
+  const bool whole = !PAGED || p.rows.block_size >= G::TK;
   struct Blocks {
-    int b[2];
+    int b[SUB];  // of rows 16 k on; whole tiles: b[0]
   };
   auto look_up = [&](int u) {
-    Blocks b{{-1, -1}};
+    Blocks b;
+#pragma unroll
+    for (int k = 0; k < SUB; ++k) b.b[k] = -1;
     if (PAGED && u < tl.u1) {
       const int r0 = tl.row(u);
       b.b[0] = __ldg(tl.trow + (r0 >> p.rows.block_shift));
-      if (half_runs && r0 + 16 < r.n) b.b[1] = __ldg(tl.trow + (r0 >> p.rows.block_shift) + 1);
+      if (!whole) {
+#pragma unroll
+        for (int k = 1; k < SUB; ++k)
+          if (r0 + 16 * k < r.n) b.b[k] = __ldg(tl.trow + ((r0 + 16 * k) >> p.rows.block_shift));
+      }
     }
     return b;
   };
   auto fetch = [&](int u, int st, const Blocks& b) {
-    const int r0 = tl.row(u), at = PAGED ? r0 & (p.rows.block_size - 1) : r0;
+    const int r0 = tl.row(u);
     const uint32_t dst = ring + 2 * st * G::TILE + 16 * lane;
-    if (r0 + G::TK <= r.n && !half_runs && (!PAGED || (b.b[0] >= 0 && b.b[0] < p.rows.num_blocks))) {
+    if (r0 + G::TK <= r.n && whole && (!PAGED || (b.b[0] >= 0 && b.b[0] < p.rows.num_blocks))) {
+      const int at = PAGED ? r0 & (p.rows.block_size - 1) : r0;
       const int64_t off = (PAGED ? b.b[0] * p.rows.block_bytes : 0) + static_cast<int64_t>(at) * G::ROW + 16 * lane;
 #pragma unroll
       for (int i = 0; i < PER_LANE; ++i) {
@@ -193,24 +201,33 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
       }
       return;
     }
-    bool ok[2] = {true, true};
+    uint32_t bad = 0;  // bit k: rows 16 k on have no block
     if (PAGED) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int rs = r0 + 16 * k;
-        if ((k == 1 && !half_runs) || rs >= r.n) continue;
-        ok[k] = b.b[k] >= 0 && b.b[k] < p.rows.num_blocks;
+      for (int k = 0; k < SUB; ++k) {
+        const int blk = whole ? b.b[0] : b.b[k], rs = r0 + 16 * k;
+        if (rs >= r.n || (blk >= 0 && blk < p.rows.num_blocks)) continue;
+        bad |= 1u << k;
         // rows that nobody sees may have no block any more
-        if (!ok[k] && (rs < r.vis.s1 || rs + (half_runs ? 16 : G::TK) - 1 >= r.vis.w0)) blocks_ok = false;
+        if (rs < r.vis.s1 || rs + 15 >= r.vis.w0) blocks_ok = false;
       }
     }
 #pragma unroll
     for (int i = 0; i < PER_LANE; ++i) {  // rows that are not there: zeros
-      const int c = lane + 32 * i, row = c / (G::ROW / 16);
-      const bool second = half_runs && row >= 16;
-      const bool live = r0 + row < r.n && (second ? ok[1] : ok[0]);
-      const int64_t off = (PAGED ? (second ? b.b[1] : b.b[0]) * p.rows.block_bytes : 0) + static_cast<int64_t>(at) * G::ROW +
-                          16 * (second ? c - G::ROW : c);
+      const int c = lane + 32 * i, row = c / (G::ROW / 16), k = row / 16, j = r0 + row;
+      const bool live = j < r.n && !(bad >> k & 1);
+      int64_t off;
+      if (PAGED) {
+        int blk = b.b[0];
+        if (!whole) {
+#pragma unroll
+          for (int x = 1; x < SUB; ++x) blk = k == x ? b.b[x] : blk;
+        }
+        off = blk * p.rows.block_bytes + static_cast<int64_t>(j & (p.rows.block_size - 1)) * G::ROW;
+      } else {
+        off = static_cast<int64_t>(j) * G::ROW;
+      }
+      off += 16 * (c - row * (G::ROW / 16));
       cp_async16(dst + 512 * i, kbase + (live ? off : 0), live);
       cp_async16(dst + G::TILE + 512 * i, vbase + (live ? off : 0), live);
     }
@@ -251,9 +268,9 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
   auto tile = [&](auto all, int r0, uint32_t tk) {
     constexpr bool INNER = decltype(all)::value;
     const uint32_t tv = tk + G::TILE;
-    float x[2][4];
+    float x[SUB][4];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < SUB; ++s) {
       const uint32_t ra = tk + (16 * s + lg) * G::ROW, rb = ra + 8 * G::ROW;
       uint32_t wa[NWD], wb[NWD], pa[4], pb[4];
       lds_words(ra + LANE * lt, wa);
@@ -303,8 +320,14 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
         }
       }
     }
-    float mx0 = fmaf(fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2])), f0, -LIFT);
-    float mx1 = fmaf(fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3])), f1, -LIFT);
+    float mx0 = fmaxf(x[0][0], x[0][2]), mx1 = fmaxf(x[0][1], x[0][3]);
+#pragma unroll
+    for (int s = 1; s < SUB; ++s) {
+      mx0 = fmaxf(fmaxf(mx0, x[s][0]), x[s][2]);
+      mx1 = fmaxf(fmaxf(mx1, x[s][1]), x[s][3]);
+    }
+    mx0 = fmaf(mx0, f0, -LIFT);
+    mx1 = fmaf(mx1, f1, -LIFT);
     if (__any_sync(FULL_MASK, mx0 > m0 || mx1 > m1)) {
 #pragma unroll
       for (int k = 4; k <= 16; k <<= 1) {
@@ -329,7 +352,7 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
     }
     const float z0 = !INNER && m0 == NEG_INF ? 0.f : m0, z1 = !INNER && m1 == NEG_INF ? 0.f : m1;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < SUB; ++s) {
       const float e[4] = {fast_exp2(fmaf(x[s][0], f0, -z0)), fast_exp2(fmaf(x[s][1], f1, -z1)), fast_exp2(fmaf(x[s][2], f0, -z0)),
                           fast_exp2(fmaf(x[s][3], f1, -z1))};
       l0 += e[0] + e[2];

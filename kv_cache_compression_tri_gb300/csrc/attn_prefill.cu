@@ -133,6 +133,7 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
                       const __grid_constant__ RowMaps<ODD> vmap, const __grid_constant__ RowNumbers rn, int n_tiles, int cluster) {
   using L = TcSmem<D, NQ>;
   const int splits = FEW_CTAS ? cluster : 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (for what writes a 4-bit cache's rows out; nothing otherwise)
   extern __shared__ __align__(1024) unsigned char smem[];  // (the swizzle goes by address)
   TcCtl& ctl = *reinterpret_cast<TcCtl*>(smem + L::CTRL);
   // (values that the MMA warps use come through a shuffle, so that the compiler
@@ -563,12 +564,19 @@ cudaError_t launch_tc(const AttnParams& p, const RowNumbers& rn, cudaStream_t st
   cfg.blockDim = dim3(TcSmem<D, NQ>::THREADS);
   cfg.dynamicSmemBytes = TcSmem<D, NQ>::BYTES;
   cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = static_cast<unsigned>(splits);
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = splits > 1;
+  cudaLaunchAttribute at[2]{};
+  if (splits > 1) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs].val.clusterDim.x = static_cast<unsigned>(splits);
+    at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (p.early) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
+  cfg.attrs = at;
   const cudaError_t r = cudaLaunchKernelEx(&cfg, kern, p, kmap, vmap, rn, n_tiles, splits);
   if (r == cudaSuccess) note_launch();
   return r;

@@ -772,6 +772,7 @@ tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out
   const cudaError_t e = launch_q4_rows(r, kv->head_dim, stream);
   if (e != cudaSuccess) return TRI_ERR_CUDA;
   // the rows as a bf16 cache of one layer
+  p.early = 1;
   p.k = r.dst[0];
   p.v = r.dst[1];
   p.n_valid = r.n_valid_out;

@@ -350,6 +350,7 @@ struct AttnParams {
   int32_t n_q, group;
   int32_t n_sink, window;
   float scale;                     // of q . k
+  int32_t early;                   // launched while the kernel before, which it waits for, still runs
   void* out;                       // [n_seq][n_q][n_kv_heads * group][head_dim]
   float* lse;                      // [n_seq][n_q][n_kv_heads * group], or NULL
   const float* lse_in;             // the weights' log-sums (attn_mass)
