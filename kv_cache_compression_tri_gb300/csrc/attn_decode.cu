@@ -761,8 +761,11 @@ cudaError_t launch_bf16(const AttnParams& p, int max_rows, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_q4(const AttnParams& p, int max_rows, cudaStream_t st) {
-  const cudaError_t e =
-      launch_runs(p.rows.table ? decode_q4_kernel<D, true> : decode_q4_kernel<D, false>, TileGeo<Q4Tag, D>::SMEM, p, st);
+  using G = TileGeo<Q4Tag, D>;
+  auto kern = !p.rows.table                  ? decode_q4_kernel<D, SLICES>
+              : p.rows.block_size >= G::TK ? decode_q4_kernel<D, WHOLE_TILES>
+                                             : decode_q4_kernel<D, SMALL_BLOCKS>;
+  const cudaError_t e = launch_runs(kern, G::SMEM, p, st);
   return e != cudaSuccess || p.join ? e : launch_join<__nv_bfloat16, D>(p, max_rows, st);
 }
 

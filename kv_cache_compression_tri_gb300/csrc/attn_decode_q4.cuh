@@ -142,9 +142,12 @@ __device__ __forceinline__ void query_fragments(const __nv_bfloat16* q, bool liv
   sums = pack_half(hi, s - hi);
 }
 
-template <int D, bool PAGED>
+// BLOCKS: how the cache's rows lie.
+enum Q4Blocks { SLICES, WHOLE_TILES, SMALL_BLOCKS };  // slices; pools whose blocks hold whole tiles, or not
+template <int D, Q4Blocks BLOCKS>
 __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_constant__ AttnParams p) {
   using G = TileGeo<Q4Tag, D>;
+  constexpr bool PAGED = BLOCKS != SLICES, whole = BLOCKS != SMALL_BLOCKS;
   constexpr int NWD = Q4Row<D>::WORDS, CODES = Q4Row<D>::CODES, LANE = 4 * NWD;  // bytes of a lane's codes
   constexpr float LIFT = 4.f;  // log2 of the largest weight
   extern __shared__ __align__(128) unsigned char smem[];
@@ -169,23 +172,15 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
   const uint32_t ring = smem_addr(smem) + w * G::WARP_RING;
   bool blocks_ok = true;
   const char *kbase = static_cast<const char*>(p.k) + tl.base, *vbase = static_cast<const char*>(p.v) + tl.base;
-  const bool whole = !PAGED || p.rows.block_size >= G::TK;
   struct Blocks {
-    int b[SUB];  // of rows 16 k on; whole tiles: b[0]
+    int b[whole ? 1 : SUB];  // of rows 16 k on; whole tiles: of all
   };
   auto look_up = [&](int u) {
     Blocks b;
+    const int r0 = tl.row(u);
 #pragma unroll
-    for (int k = 0; k < SUB; ++k) b.b[k] = -1;
-    if (PAGED && u < tl.u1) {
-      const int r0 = tl.row(u);
-      b.b[0] = __ldg(tl.trow + (r0 >> p.rows.block_shift));
-      if (!whole) {
-#pragma unroll
-        for (int k = 1; k < SUB; ++k)
-          if (r0 + 16 * k < r.n) b.b[k] = __ldg(tl.trow + ((r0 + 16 * k) >> p.rows.block_shift));
-      }
-    }
+    for (int k = 0; k < (whole ? 1 : SUB); ++k)
+      b.b[k] = PAGED && u < tl.u1 && r0 + 16 * k < r.n ? __ldg(tl.trow + ((r0 + 16 * k) >> p.rows.block_shift)) : -1;
     return b;
   };
   auto fetch = [&](int u, int st, const Blocks& b) {
@@ -201,11 +196,34 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
       }
       return;
     }
+    if (!whole) {
+      // (a tile holds whole blocks, so a chunk's place in its block is the same in every tile)
+      int64_t at[SUB];
+      bool all = r0 + G::TK <= r.n;
+#pragma unroll
+      for (int k = 0; k < SUB; ++k) {
+        at[k] = b.b[whole ? 0 : k] * p.rows.block_bytes;
+        all &= b.b[whole ? 0 : k] >= 0 && b.b[whole ? 0 : k] < p.rows.num_blocks;
+      }
+      if (all) {
+#pragma unroll
+        for (int i = 0; i < PER_LANE; ++i) {
+          const int c = lane + 32 * i, row = c / (G::ROW / 16), k = row / 16;
+          int64_t off = at[0];
+#pragma unroll
+          for (int x = 1; x < SUB; ++x) off = k == x ? at[x] : off;
+          off += (row & (p.rows.block_size - 1)) * G::ROW + 16 * (c - row * (G::ROW / 16));
+          cp_async16_all(dst + 512 * i, kbase + off);
+          cp_async16_all(dst + G::TILE + 512 * i, vbase + off);
+        }
+        return;
+      }
+    }
     uint32_t bad = 0;  // bit k: rows 16 k on have no block
     if (PAGED) {
 #pragma unroll
       for (int k = 0; k < SUB; ++k) {
-        const int blk = whole ? b.b[0] : b.b[k], rs = r0 + 16 * k;
+        const int blk = b.b[whole ? 0 : k], rs = r0 + 16 * k;
         if (rs >= r.n || (blk >= 0 && blk < p.rows.num_blocks)) continue;
         bad |= 1u << k;
         // rows that nobody sees may have no block any more
@@ -219,10 +237,8 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
       int64_t off;
       if (PAGED) {
         int blk = b.b[0];
-        if (!whole) {
 #pragma unroll
-          for (int x = 1; x < SUB; ++x) blk = k == x ? b.b[x] : blk;
-        }
+        for (int x = 1; x < (whole ? 1 : SUB); ++x) blk = k == x ? b.b[x] : blk;
         off = blk * p.rows.block_bytes + static_cast<int64_t>(j & (p.rows.block_size - 1)) * G::ROW;
       } else {
         off = static_cast<int64_t>(j) * G::ROW;

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(RT) q4_rows_kernel(const __grid_constant__ Q4R
     if (!CHUNKED && threadIdx.x == 0) set_status(p.dev_status, TRI_DEV_NVALID_OVER_CAP);
     return;
   }
-  const int r0 = tile * CHUNK, r1 = min(r0 + CHUNK, n);
+  const int r0 = tile * CHUNK, r1 = n - r0 > CHUNK ? r0 + CHUNK : n;
   if (r0 >= r1 || (CHUNKED && nn <= 0)) return;
   Visible vis{0, 0};
   if constexpr (CHUNKED) {
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(RT) q4_rows_kernel(const __grid_constant__ Q4R
 }  // namespace
 
 cudaError_t launch_q4_rows(const Q4RowsParams& p, int head_dim, cudaStream_t st) {
-  const int tiles = (p.n_cap + CHUNK - 1) / CHUNK;
+  const int tiles = (p.n_cap - 1) / CHUNK + 1;
   const int64_t ctas = static_cast<int64_t>(p.n_seq) * p.n_kv_heads * tiles;
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
   auto kern = head_dim == 64 ? (p.n_new_out ? q4_rows_kernel<64, true> : q4_rows_kernel<64, false>)
