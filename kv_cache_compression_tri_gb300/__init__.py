@@ -597,12 +597,10 @@ def _token_dtype(kv) -> torch.dtype:
 
 def _token_strides(t: torch.Tensor, shape, dtype: torch.dtype, device: int):
     """Sequence and token strides of rows [n_seq, n_q, heads, d] whose heads are contiguous."""
-    assert t.get_device() == device and t.dtype == dtype and t.shape == shape
-    n_seq, n_q, heads, d = shape
-    st = t.stride()
-    assert st[3] == 1 and (st[2] == d or heads == 1)
+    a, b, c, e = t.stride()
+    assert t.shape == shape and t.dtype == dtype and t.get_device() == device and e == 1 and (c == shape[3] or shape[2] == 1)
     # (the stride of a dimension of one may be anything)
-    return st[0] if n_seq > 1 else 0, st[1] if n_q > 1 else heads * d
+    return a if shape[0] > 1 else 0, b if shape[1] > 1 else shape[2] * shape[3]
 
 
 def append(kv, layer: int, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, rope_theta: float,
@@ -618,37 +616,38 @@ def append(kv, layer: int, k: torch.Tensor, v: torch.Tensor, positions: torch.Te
     A 4-bit cache takes bf16 tokens."""
     lib = load_library()
     kvs = kv._abi()
-    dev, dtype, d, H = kv.k.get_device(), _token_dtype(kv), kvs.head_dim, kvs.n_kv_heads
+    dev, dtype, d, H, n_seq = kv.k.get_device(), _token_dtype(kv), kvs.head_dim, kvs.n_kv_heads, kvs.n_seq
     assert dev == torch.cuda.current_device(), "cache and tokens on the current device"
-    n_seq, n_q = k.shape[:2]
-    assert n_seq == kvs.n_seq
-    ks, vs = (_token_strides(t, (n_seq, n_q, H, d), dtype, dev) for t in (k, v))
+    n_q = k.shape[1]
+    shape = (n_seq, n_q, H, d)
+    ks, vs = _token_strides(k, shape, dtype, dev), _token_strides(v, shape, dtype, dev)
+    at = positions.shape
+    n_axes = at[2] if len(at) == 3 else 1
+    assert at[0] == n_seq and at[1] == n_q and len(at) <= 3
     assert positions.get_device() == dev and positions.dtype == torch.int32 and positions.is_contiguous()
-    n_axes = positions.shape[2] if positions.dim() == 3 else 1
-    assert positions.shape[:2] == (n_seq, n_q) and positions.numel() == n_seq * n_q * n_axes
     if n_new is not None:
         assert n_new.get_device() == dev and n_new.dtype == torch.int32 and n_new.is_contiguous() and n_new.numel() == n_seq
     axes = None
     if band_axis is not None:
-        axes = bytes(int(a) for a in band_axis)
+        axes = bytes(band_axis)
         assert len(axes) == d // 2
-    qs = qos = (0, 0)
-    group = 0
+    qs, qos, group = (0, 0), (0, 0), 0
     if q is not None:
         Hq = q.shape[2]
         assert Hq % H == 0
-        group = Hq // H
-        qs = _token_strides(q, (n_seq, n_q, Hq, d), dtype, dev)
+        group, shape = Hq // H, (n_seq, n_q, Hq, d)
+        qs = _token_strides(q, shape, dtype, dev)
         if q_out is None:
-            q_out = _empty((n_seq, n_q, Hq, d), dtype, q.device, stream)
+            q_out = _empty(shape, dtype, q.device, stream)
             if stream is not None:  # read on the current stream later on
                 q_out.record_stream(torch.cuda.current_stream())
-        qos = _token_strides(q_out, (n_seq, n_q, Hq, d), dtype, dev)
+        qos = qs if q_out is q else _token_strides(q_out, shape, dtype, dev)
     else:
         assert q_out is None
     tok = _TriTokens(k.data_ptr(), v.data_ptr(), *ks, *vs, _ptr(q), _ptr(q_out), *qs, *qos, positions.data_ptr(), axes,
-                     _ptr(n_new), float(rope_theta), style, n_axes, n_q, group, layer)
-    _check("tri_append", lib.tri_append(ctypes.byref(kvs), ctypes.byref(tok), _stream(stream)))
+                     _ptr(n_new), rope_theta, style, n_axes, n_q, group, layer)
+    _check("tri_append", lib.tri_append(ctypes.byref(kvs), ctypes.byref(tok),
+                                        stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)))
     return q_out
 
 

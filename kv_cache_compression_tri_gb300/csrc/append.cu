@@ -30,8 +30,7 @@
 namespace tri {
 namespace {
 
-constexpr int AW = 8;  // warps per CTA
-constexpr int MAX_ROWS = 128;  // (token, KV head) rows of a CTA
+constexpr int AW = 4;  // warps per CTA (8192 tokens in 4 bits and read back: 58.6 us, with eight 60.8)
 constexpr int MAX_HEADS = 16;  // KV heads of a CTA
 
 // cos and sin of 2 pi frac(x nu): sincospi of the phase rounded to fp32 (within one step), and
@@ -400,11 +399,12 @@ __device__ __forceinline__ void for_rows(const T* base, int64_t token, int toks,
 }
 
 template <typename T, int D, bool HALF, bool Q4>
-__global__ void __launch_bounds__(AW * 32, 4) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(AW * 32, 8) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LANES = D / 16, RPW = 32 / LANES, F = D / 2;  // lanes of a row, rows of a warp
   constexpr int MAX_TOKENS = AW * 32 / F;
   __shared__ float4 turns[MAX_TOKENS][F / 2];
-  __shared__ int64_t dst[MAX_ROWS];  // byte offset of each (token, head) row in K and V, -1: none
+  static_assert(MAX_TOKENS * MAX_HEADS <= AW * 32, "a thread per row");
+  __shared__ int64_t dst[MAX_TOKENS * MAX_HEADS];  // byte offset of each (token, head) row in K and V, -1: none
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t = threadIdx.x, w = t >> 5, lane = t & 31, sub = lane / LANES, l = lane % LANES;
   int b = blockIdx.x;
@@ -547,7 +547,7 @@ template <typename T, int D, bool Q4>
 cudaError_t launch_style(const AppendParams& p, tri_rope_style style, cudaStream_t st) {
   auto kern = style == TRI_ROPE_HALF ? append_kernel<T, D, true, Q4> : append_kernel<T, D, false, Q4>;
   const int64_t ctas = static_cast<int64_t>(p.n_seq) * p.token_tiles * p.head_tiles;
-  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  if (ctas > 0x7fffffff) return cudaErrorNotSupported;  // (more than a launch counts)
   kern<<<static_cast<unsigned>(ctas), AW * 32, 0, st>>>(p);
   note_launch();
   cudaError_t e = cudaGetLastError();

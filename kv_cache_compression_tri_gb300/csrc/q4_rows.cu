@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(RT) q4_rows_kernel(const __grid_constant__ Q4R
 cudaError_t launch_q4_rows(const Q4RowsParams& p, int head_dim, cudaStream_t st) {
   const int tiles = (p.n_cap - 1) / CHUNK + 1;
   const int64_t ctas = static_cast<int64_t>(p.n_seq) * p.n_kv_heads * tiles;
-  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  if (ctas > 0x7fffffff) return cudaErrorNotSupported;  // (more than a launch counts)
   auto kern = head_dim == 64 ? (p.n_new_out ? q4_rows_kernel<64, true> : q4_rows_kernel<64, false>)
                              : (p.n_new_out ? q4_rows_kernel<128, true> : q4_rows_kernel<128, false>);
   kern<<<static_cast<unsigned>(ctas), RT, 0, st>>>(p, tiles);

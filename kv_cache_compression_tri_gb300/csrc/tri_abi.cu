@@ -770,7 +770,7 @@ tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out
   r.n_valid_out = reinterpret_cast<int32_t*>(base + w.valid_off);
   r.n_new_out = reinterpret_cast<int32_t*>(base + w.new_off);
   const cudaError_t e = launch_q4_rows(r, kv->head_dim, stream);
-  if (e != cudaSuccess) return TRI_ERR_CUDA;
+  if (e != cudaSuccess) return attn_status(e);
   // the rows as a bf16 cache of one layer
   p.early = 1;
   p.k = r.dst[0];
@@ -798,7 +798,7 @@ tri_status tri_read_rows(const tri_kv* kv, int32_t layer, void* k_out, void* v_o
   Q4RowsParams r = q4_rows_params(kv, layer);
   r.dst[0] = static_cast<__nv_bfloat16*>(k_out);
   r.dst[1] = static_cast<__nv_bfloat16*>(v_out);
-  return launch_q4_rows(r, kv->head_dim, stream) == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
+  return attn_status(launch_q4_rows(r, kv->head_dim, stream));
 }
 
 tri_status tri_append(const tri_kv* kv, const tri_tokens* t, tri_stream_t stream) {
@@ -869,7 +869,7 @@ tri_status tri_append(const tri_kv* kv, const tri_tokens* t, tri_stream_t stream
   p.n_q = t->n_q;
   p.group = t->q ? t->group : 0;
   p.rotate_k = post;
-  return launch_append(p, kv->dtype, kv->head_dim, t->style, stream) == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
+  return attn_status(launch_append(p, kv->dtype, kv->head_dim, t->style, stream));
 }
 
 tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* lse, int64_t lse_seq_stride, float* mass,

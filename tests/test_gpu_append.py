@@ -183,6 +183,14 @@ def test_several_axes(dtype, kind, half):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+def test_more_heads_than_a_cta_takes(dtype):
+    c = Cache([[(5 * h) % 23 for h in range(20)]], 64 if dtype == torch.float32 else 128, dtype, 64)
+    check(c, 3, 2)
+    check(c, 1, 2, seed=4)
+    assert int(c.status) == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_in_place_queries(dtype):
     check(Cache([[3, 0]], 64, dtype, 48), 5, 2, half=True, in_place=True)
 

@@ -174,6 +174,52 @@ def test_decode_long_rows_sampled():
     check_decode(Case([[8192]], 128, L=1, block=256), 1, layer=0, with_mass=True)
 
 
+def test_offsets_past_32_bits():
+    # a pool of which every block but the last ones lies past 2^31 bytes; slices too
+    nb, block = 30000, 256
+    k = torch.zeros(nb, 1, 4, block, 80, dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    small = Case([[600, 500, 1, 300]], 128, L=1, block=block)
+    per = small.table.shape[1]
+    table = torch.arange(nb - per, nb, dtype=torch.int32, device="cuda").view(1, per)
+    for big, pool in ((k, small.pools[0]), (v, small.pools[1])):
+        big[nb - per:] = pool[small.table[0].long()]
+    q = torch.randn(1, 16, 128, device="cuda").bfloat16()
+    outs = []
+    for kv in (small.kv, tri.PagedKVCache(k, v, table, small.kv.n_valid, None, None, small.status, post_rope=True)):
+        out, rows = torch.zeros_like(q), torch.zeros(1, 4, small.cap, 128, dtype=torch.bfloat16, device="cuda")
+        chunk, x = torch.zeros(1, 2, 16, 128, dtype=torch.bfloat16, device="cuda"), q.view(1, 1, 16, 128).expand(1, 2, 16, 128).contiguous()
+        tri.attn_decode(kv, 0, q, out)
+        tri.read_rows(kv, 0, rows, None)
+        tri.attn_prefill(kv, 0, x, chunk)
+        outs.append((out, rows, chunk))
+    small.ok()
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+@pytest.mark.parametrize("order", [(0, 1, 2), (2, 0, 1), (1, 2, 0)])
+@pytest.mark.parametrize("pad", [0, 1, 3])
+def test_pools_in_any_order(order, pad):
+    """Blocks, layers and heads in any order in memory, with rows of 16 bytes between."""
+    c = Case([[70, 33], [5, 64]], 64, block=16)
+    nb, L, H, bs, w = c.pools[0].shape
+    dims = (nb, L, H)
+    views = []
+    for p in c.pools:
+        flat = torch.full([dims[i] for i in order] + [bs * w + 16 * pad], 0xFF, dtype=torch.uint8, device="cuda")
+        rows = flat[..., :bs * w].view(*[dims[i] for i in order], bs, w) if pad == 0 else flat[..., :bs * w].unflatten(-1, (bs, w))
+        view = rows.permute(*[order.index(i) for i in range(3)], 3, 4)
+        view.copy_(p)
+        views.append(view)
+    kv = tri.PagedKVCache(*views, c.kv.block_table, c.kv.n_valid, None, None, c.status, post_rope=True)
+    q = torch.randn(2, 4, 64, device="cuda").bfloat16()
+    a, b = torch.zeros_like(q), torch.zeros_like(q)
+    tri.attn_decode(c.kv, 1, q, a)
+    tri.attn_decode(kv, 1, q, b)
+    c.ok()
+    assert torch.equal(a, b)
+
+
 def test_decode_repeats_bit_for_bit():
     c = Case([[700, 40], [2, 333]], 128, block=16)
     a, b = check_decode(c, 4, with_mass=True), check_decode(c, 4, with_mass=True)

@@ -165,3 +165,11 @@ def test_rotation_by_hand():
     rng = np.random.default_rng(1)
     a, b = rng.normal(size=64), rng.normal(size=64)
     assert np.isclose(rotate(a, [1000], 1e4) @ rotate(b, [993], 1e4), rotate(a, [7], 1e4) @ b)
+
+
+def test_more_than_a_launch_counts(lib):  # noqa: F811
+    many = dict(key_layout=1, n_seq=1 << 24, n_kv_heads=64)
+    tok = _tok(n_q=1 << 20, k_seq_stride=0, v_seq_stride=0, k_token_stride=64 * 64, v_token_stride=64 * 64, q=None)
+    assert _append(lib, _kv(**many), tok) == UNSUPPORTED
+    assert lib.tri_read_rows(ctypes.byref(_kv(**dict(Q4, n_seq=1 << 24, n_kv_heads=64, n_cap=1 << 20, slice_stride=48 << 20))), 0, 0x30000, None,
+                             None) == UNSUPPORTED
