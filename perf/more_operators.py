@@ -478,7 +478,9 @@ def _own(st):
         if c["mass"]:
             out["mass"] = st["mass"]
         return out
-    tri.attn_prefill(kv, 0, st["q"], st["out"], n_new=st["n_new"], n_sink=c["n_sink"], window=c["window"], lse=st["lse"], workspace=st["scratch"])
+    if "chunk_scratch" not in st:  # (a size that the library tells; kept like the other)
+        st["chunk_scratch"] = torch.empty(tri.attn_prefill_workspace_bytes(kv), dtype=torch.uint8, device="cuda")
+    tri.attn_prefill(kv, 0, st["q"], st["out"], n_new=st["n_new"], n_sink=c["n_sink"], window=c["window"], lse=st["lse"], workspace=st["chunk_scratch"])
     return {"out": st["out"], "lse": st["lse"]}
 
 
