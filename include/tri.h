@@ -82,7 +82,8 @@ typedef enum {
  *   code = (x - minimum) / scale to the nearest whole number, ties to even, within
  *   0 .. 15 (0 where scale is 0),
  * decided as in 64-bit arithmetic. A quarter that holds a NaN reads back as NaN. A
- * cache written by other means keeps its scales, if not NaN, within 0 .. 4090.
+ * cache written by other means keeps its scales, if not NaN, within 0 .. 4090, and
+ * its values within +-65504.
  * Taken by tri_append, tri_read_rows, tri_attn_decode, tri_attn_prefill_q4, the
  * compactions (tri_compact_kv, tri_select_compact, rand_evict_compact,
  * tri_mass_evict), tri_paged_blocks_used and what reads row counts only; other
@@ -461,6 +462,8 @@ typedef struct {
  * ranks by; other entries are left as they were. ws: device scratch of
  * tri_attn_decode_workspace_bytes(kv, group, mass != NULL) bytes, 16-byte
  * aligned, no initial contents needed; calls that may overlap need one each.
+ * 4-bit caches: products of the codes are exact; weights are rounded to fp16, and
+ * again with V's scales, for their product with V.
  * A slice with a fault (row count, block table, n_new) is skipped. */
 size_t tri_attn_decode_workspace_bytes(const tri_kv* kv, int32_t group, int32_t with_mass);
 tri_status tri_attn_decode(const tri_kv* kv, const tri_queries* q, void* out, float* lse, float* mass, void* ws,
@@ -490,10 +493,11 @@ tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* ls
 
 /* tri_attn_prefill_q4 -- tri_attn_prefill over a 4-bit cache (TRI_Q4 only;
  * TRI_ERR_UNSUPPORTED otherwise). The rows that some query may see are first
- * written to ws as bf16 values, rounded once; the bf16 kernel then reads those.
- * ws: device scratch of tri_attn_prefill_q4_workspace_bytes(kv) bytes (one layer's
- * rows in bf16), 16-byte aligned, no initial contents needed; calls that may
- * overlap need one each. A sequence with a fault in n_new, or in the table entry
+ * written to ws, the values of K as a pair of bf16, those of V in fp16; the kernel
+ * then reads those. Weights are rounded to fp16 for their product with V (their sum
+ * is not). ws: device scratch of tri_attn_prefill_q4_workspace_bytes(kv) bytes (one
+ * layer's rows, 6 head_dim bytes each), 16-byte aligned, no initial contents
+ * needed; calls that may overlap need one each. A sequence with a fault in n_new, or in the table entry
  * of a block that one of its queries sees (in any head), is skipped as a whole, one
  * with a bad row count as tri_attn_prefill skips it. */
 size_t tri_attn_prefill_q4_workspace_bytes(const tri_kv* kv);

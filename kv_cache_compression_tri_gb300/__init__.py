@@ -704,7 +704,7 @@ def attn_decode(kv, layer: int, q: torch.Tensor, out: torch.Tensor, n_new: torch
 
 
 def attn_prefill_workspace_bytes(kv) -> int:
-    """Scratch of attn_prefill: one layer's rows in bf16 for a 4-bit cache, none otherwise."""
+    """Scratch of attn_prefill: one layer's rows written out for a 4-bit cache, none otherwise."""
     kvs = kv._abi()
     return int(load_library().tri_attn_prefill_q4_workspace_bytes(ctypes.byref(kvs)))
 

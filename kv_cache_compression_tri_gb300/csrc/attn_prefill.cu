@@ -101,9 +101,9 @@ __device__ __forceinline__ void scale_o(uint32_t to, float a) {
     tmem_st16(to + k * 16, o);
   }
 }
-// Weights 2^(x sl - mu) of 32 columns, rounded to bf16 (hi), with PAIR also what the
-// rounding left (lo); returns their fp32 sum.
-template <bool PAIR>
+// Weights 2^(x sl - mu) of 32 columns, rounded to bf16 (fp16 with HALF) in hi, with PAIR
+// also what the rounding left (lo); returns their fp32 sum.
+template <bool PAIR, bool HALF>
 __device__ __forceinline__ float weights_of(const uint32_t (&x)[32], float sl, float mu, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
   float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
@@ -117,8 +117,8 @@ __device__ __forceinline__ float weights_of(const uint32_t (&x)[32], float sl, f
     e3 = fast_exp2(e3);
     add2(l0, l1, e0, e1);
     add2(l2, l3, e2, e3);
-    hi[k] = pack_bf16(e0, e1);
-    hi[k + 1] = pack_bf16(e2, e3);
+    hi[k] = HALF ? pack_half(e0, e1) : pack_bf16(e0, e1);
+    hi[k + 1] = HALF ? pack_half(e2, e3) : pack_bf16(e2, e3);
     if constexpr (PAIR) {
       lo[k] = pack_bf16(e0 - bf16_lo(hi[k]), e1 - bf16_hi(hi[k]));
       lo[k + 1] = pack_bf16(e2 - bf16_lo(hi[k + 1]), e3 - bf16_hi(hi[k + 1]));
@@ -127,11 +127,18 @@ __device__ __forceinline__ float weights_of(const uint32_t (&x)[32], float sl, f
   return (l0 + l1) + (l2 + l3);
 }
 
-template <int D, int NQ, bool FEW_CTAS, bool ODD>
+// Q4: the rows of a 4-bit cache, written out before. K as a bf16 pair (kmap; lmap: what the first rounding left),
+// two tiles of the ring and two products: 16 bits of its values. V and the weights in fp16, the latter up to 2^14 (no
+// further pair): 2^-11 of a weight, and 2^-25 of the smallest that counts.
+template <int D, int NQ, bool FEW_CTAS, bool ODD, bool Q4>
 __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
     prefill_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ RowMaps<ODD> kmap,
-                      const __grid_constant__ RowMaps<ODD> vmap, const __grid_constant__ RowNumbers rn, int n_tiles, int cluster) {
+                      const __grid_constant__ RowMaps<ODD> vmap, const __grid_constant__ RowMaps<Q4 ? ODD : false> lmap,
+                      const __grid_constant__ RowNumbers rn, int n_tiles, int cluster) {
   using L = TcSmem<D, NQ>;
+  constexpr int PER = Q4 ? 3 : 2;               // ring stages of a tile of rows: K (twice), V
+  constexpr bool PAIR = FEW_CTAS && !Q4;        // the weights as a pair
+  constexpr float LIFT = Q4 ? 6.f : 0.f;        // log2 of the weight of a row's running maximum
   const int splits = FEW_CTAS ? cluster : 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // (for what writes a 4-bit cache's rows out; nothing otherwise)
   extern __shared__ __align__(1024) unsigned char smem[];  // (the swizzle goes by address)
@@ -230,20 +237,23 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
     auto place_of = [&](int blk, int k0) { return box_place<D, ODD>(rn, box, blk, c.h, k0); };
     int blk_next = n_list ? block_of(tile_row(0)) : 0;
     Place place = n_list ? place_of(blk_next, tile_row(0)) : Place{0, 0};
-    for (; cnt < 2 * n_list && ok; ++cnt) {
-      const int st = cnt % L::NST, k0 = tile_row(cnt >> 1);
-      if (!(cnt & 1) && cnt + 2 < 2 * n_list)  // (on its way while this tile waits for its stage)
-        blk_next = block_of(tile_row((cnt >> 1) + 1));
+    for (; cnt < PER * n_list && ok; ++cnt) {
+      const int i = cnt / PER, part = cnt % PER, st = cnt % L::NST, k0 = tile_row(i);
+      if (part == 0 && i + 1 < n_list)  // (on its way while this tile waits for its stage)
+        blk_next = block_of(tile_row(i + 1));
       if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
       if (!ok) break;
-      const bool is_v = cnt & 1;
+      const bool is_v = part == PER - 1;
       const bool fix = is_v && k0 + TROWS - 1 > r_hi;
       uint64_t* bar = fix ? &ctl.v_fix : &ctl.full[st];
       if (bad & 1) ctl.flag[0] = 1;
       if (bad & 2) ctl.flag[1] = 1;
       __syncwarp();
-      load_tile<D, ODD>(ring + st * L::TILE, is_v ? vmap : kmap, box, place, bar, lane);
-      if (is_v && cnt + 1 < 2 * n_list) place = place_of(blk_next, tile_row((cnt >> 1) + 1));
+      if (Q4 && part == 1)
+        load_tile<D, Q4 ? ODD : false>(ring + st * L::TILE, lmap, box, place, bar, lane);
+      else
+        load_tile<D, ODD>(ring + st * L::TILE, is_v ? vmap : kmap, box, place, bar, lane);
+      if (is_v && i + 1 < n_list) place = place_of(blk_next, tile_row(i + 1));
       if (fix) {
         ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.v_fix, 0));
         if (!ok) break;
@@ -267,7 +277,7 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
     const int q = w - 1;
     const Steps need = steps_of(q);
     if (q < nq && elect_one()) {
-      constexpr uint32_t IQK = bf16_idesc(TROWS, STEP, false), IPV = bf16_idesc(TROWS, D, true);
+      constexpr uint32_t IQK = bf16_idesc(TROWS, STEP, false), IPV = Q4 ? f16_idesc(TROWS, D) | 1u << 16 : bf16_idesc(TROWS, D, true);
       constexpr uint64_t STAGE = L::TILE >> 4;  // (descriptors count 16 bytes)
       const uint64_t dq = sw128_desc(qa + q * L::TILE), dk = sw128_desc(ring), dv = sw128_desc_mn(ring);
       const uint32_t to = o_col(q);
@@ -278,6 +288,14 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
           const uint64_t off = (k >> 2) * (TCOL >> 4) + (k & 3) * 2;
           umma_f16(s_col(q, b), dq + off, ds + off, IQK, k > 0);
         }
+        if constexpr (Q4) {  // the pair's second half, in the stage behind
+          const uint64_t dl = dk + (at + 1 == L::NST ? 0 : at + 1) * STAGE + b * (STEP * 8);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = (k >> 2) * (TCOL >> 4) + (k & 3) * 2;
+            umma_f16(s_col(q, b), dq + off, dl + off, IQK, true);
+          }
+        }
         umma_commit(&ctl.s_full[q][b]);
       };
       uint32_t use[2] = {0, 0};  // products of each buffer
@@ -285,18 +303,21 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
       ok = mbar_wait_bounded(&ctl.q_ready[q], 0);
       if (n_list > 0 && ok) {
         ok = mbar_wait_bounded(&ctl.full[0], 0);
+        if (Q4 && ok) ok = mbar_wait_bounded(&ctl.full[1], 0);
         tc_fence_after();
 #pragma unroll
         for (int b = 0; b < 2; ++b)
           if (ok && need.has(step_of(0) + b)) issue_s(0, b);
         umma_commit(&ctl.empty[0]);
+        if (Q4) umma_commit(&ctl.empty[1]);
       }
       for (int i = 0; i < n_list && ok; ++i) {
         const bool more = i + 1 < n_list;
         const int x = step_of(i), xn = more ? step_of(i + 1) : need.e;
-        const uint32_t cv = 2 * i + 1, sv = cv % L::NST, sk = (cv + 1) % L::NST;
+        const uint32_t cv = PER * i + PER - 1, sv = cv % L::NST, sk = (cv + 1) % L::NST, sl = (cv + 2) % L::NST;
         ok = mbar_wait_bounded(&ctl.full[sv], (cv / L::NST) & 1);
         if (ok && more) ok = mbar_wait_bounded(&ctl.full[sk], ((cv + 1) / L::NST) & 1);
+        if (Q4 && ok && more) ok = mbar_wait_bounded(&ctl.full[sl], ((cv + 2) / L::NST) & 1);
         if (!ok) break;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -308,7 +329,7 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
             umma_ts(to, s_col(q, b), ds, IPV, use[0] + use[1] > 0);
 #pragma unroll
             for (int j = 1; j < STEP / 16; ++j) umma_ts(to, s_col(q, b) + (j >> 1) * 32 + (j & 1) * 8, ds + j * 128, IPV, true);
-            if constexpr (FEW_CTAS) {  // the pair's second half, 16 columns on
+            if constexpr (PAIR) {  // the pair's second half, 16 columns on
 #pragma unroll
               for (int j = 0; j < STEP / 16; ++j) umma_ts(to, s_col(q, b) + 16 + (j >> 1) * 32 + (j & 1) * 8, ds + j * 128, IPV, true);
             }
@@ -319,6 +340,7 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
         }
         umma_commit(&ctl.empty[sv]);
         if (more) umma_commit(&ctl.empty[sk]);
+        if (Q4 && more) umma_commit(&ctl.empty[sl]);
       }
       if (!ok) set_status(p.dev_status, TRI_DEV_TIMEOUT);
     }
@@ -379,11 +401,11 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
         wait_products();
         scale_o<D / 2>(to, a);
       }
-      const float mu = m == NEG_INF ? 0.f : m;
+      const float mu = (m == NEG_INF ? 0.f : m) - LIFT;
       uint32_t hi[16], lo[16];
-      l += weights_of<FEW_CTAS>(x, sl, mu, hi, lo);
+      l += weights_of<PAIR, Q4>(x, sl, mu, hi, lo);
       tmem_st16(ts, hi);
-      if constexpr (FEW_CTAS) tmem_st16(ts + 16, lo);
+      if constexpr (PAIR) tmem_st16(ts + 16, lo);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -394,6 +416,7 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
       ++n;
     }
     wait_products();
+    m -= LIFT;  // (what the sums are of)
     // (without a step nothing has waited for the other warps' copies of the query tile)
     if (n == 0 && ok) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.q_ready[q], 0));
     ctl.mx[n & 1][q][half][u] = l;
@@ -538,11 +561,13 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
   if (w == 1) tmem_dealloc(tm, L::TMEM);
 }
 
-template <int D, bool ODD>
+template <int D, bool ODD, bool Q4 = false>
 cudaError_t launch_tc(const AttnParams& p, const RowNumbers& rn, cudaStream_t st) {
   RowMaps<ODD> kmap, vmap;
+  RowMaps<Q4 ? ODD : false> lmap{};
   const Encode encode = tensor_map_encode();
   if (!encode || !encode_rows(kmap, p.k, p, D, rn, encode) || !encode_rows(vmap, p.v, p, D, rn, encode)) return cudaErrorInvalidValue;
+  if (Q4 && !encode_rows(lmap, p.k_rest, p, D, rn, encode)) return cudaErrorInvalidValue;
   // one or two query tiles per CTA: at d 64 two CTAs with a tile each fit an SM, and one's
   // start and end hide behind the other's work (8 padded prompts of up to 4096 tokens, sinks
   // and a window of 1000: 189 us, with two tiles per CTA 199)
@@ -556,7 +581,7 @@ cudaError_t launch_tc(const AttnParams& p, const RowNumbers& rn, cudaStream_t st
   const bool few = units * 2 <= SMS;
   int splits = 1;
   while (few && splits < MAX_SPLITS && units * splits * 2 <= SMS && rows >= 2 * splits * 2 * TROWS) splits *= 2;
-  auto kern = few ? prefill_tc_kernel<D, NQ, true, ODD> : prefill_tc_kernel<D, NQ, false, ODD>;
+  auto kern = few ? prefill_tc_kernel<D, NQ, true, ODD, Q4> : prefill_tc_kernel<D, NQ, false, ODD, Q4>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D, NQ>::BYTES);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -571,13 +596,13 @@ cudaError_t launch_tc(const AttnParams& p, const RowNumbers& rn, cudaStream_t st
     at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
     ++cfg.numAttrs;
   }
-  if (p.early) {
+  if (Q4) {  // (while the kernel that writes the rows still runs)
     at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
     ++cfg.numAttrs;
   }
   cfg.attrs = at;
-  const cudaError_t r = cudaLaunchKernelEx(&cfg, kern, p, kmap, vmap, rn, n_tiles, splits);
+  const cudaError_t r = cudaLaunchKernelEx(&cfg, kern, p, kmap, vmap, lmap, rn, n_tiles, splits);
   if (r == cudaSuccess) note_launch();
   return r;
 }
@@ -698,6 +723,11 @@ cudaError_t launch_fp32(const AttnParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attn_prefill(const AttnParams& p, tri_dtype dt, int head_dim, cudaStream_t st) {
+  if (dt == TRI_Q4) {
+    RowNumbers rn{};
+    if (!row_numbers(p, rn)) return cudaErrorNotSupported;
+    return head_dim == 64 ? launch_tc<64, false, true>(p, rn, st) : launch_tc<128, false, true>(p, rn, st);
+  }
   if (dt == TRI_BF16) {
     RowNumbers rn{};
     if (!row_numbers(p, rn)) return cudaErrorNotSupported;

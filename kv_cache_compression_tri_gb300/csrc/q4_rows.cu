@@ -1,10 +1,12 @@
-// q4_rows.cu -- one layer's rows of a 4-bit cache written out as bf16: for the
-// caller (tri_read_rows), or for a chunk's attention, which then runs on them
-// (tri_attn_prefill_q4).
+// q4_rows.cu -- one layer's rows of a 4-bit cache written out: for the caller
+// (tri_read_rows, bf16), or for a chunk's attention, which then runs on them
+// (tri_attn_prefill_q4: K as a bf16 pair, V in fp16. With both rounded to bf16 once, log-sums
+// were off by 1e-5 to 7e-5 of themselves, and results by more than twice what their own
+// rounding leaves).
 //
-// A thread writes 16 bytes: eight elements of one quarter, minimum + scale * code. Bound:
-// HBM, d / 2 + 16 bytes in and 2 d out per row (a prompt's rows stay in L2 for the
-// attention that follows).
+// A thread writes 16 bytes of each: eight elements of one quarter, minimum + scale * code.
+// Bound: HBM, d / 2 + 16 bytes in and 2 d (4 d of a pair) out per row (a prompt's rows stay in
+// L2 for the attention that follows).
 //
 // For a chunk: rows out of every query's sight are zero where a 128-row tile holds rows in
 // sight (the attention's weights there are 0, which a NaN would survive) and not
@@ -46,13 +48,12 @@ __device__ __forceinline__ Eight load8(const char* row, int c) {
   return x;
 }
 template <int D>
-__device__ __forceinline__ uint4 values8(const Eight& w, int c) {
+__device__ __forceinline__ void values8(const Eight& w, int c, float (&x)[8]) {
   const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w.pair));  // scale, minimum
   uint32_t n = w.a;  // the eight codes, in order
   // (d 64: four codes of a word each, in its bytes j & 1 and 2 + (j & 1))
   if constexpr (D == 64) n = __byte_perm(w.a, w.b, (c >> 1) & 1 ? 0x7531 : 0x6420);
   // (a half with exponent 0 and c in its low bits is c 2^-24, four bits higher c 2^-20: exact)
-  float x[8];
   const float s0 = p.x * 0x1p24f, s1 = p.x * 0x1p20f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -61,7 +62,17 @@ __device__ __forceinline__ uint4 values8(const Eight& w, int c) {
     x[e] = fmaf(c.x, e & 1 ? s1 : s0, p.y);
     x[e + 4] = fmaf(c.y, e & 1 ? s1 : s0, p.y);
   }
+}
+__device__ __forceinline__ uint4 bf16_of(const float (&x)[8]) {
   return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+// What rounding to `hi` left.
+__device__ __forceinline__ uint4 rest_of(const float (&x)[8], uint4 hi) {
+  const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) r[k] = pack_bf16(x[2 * k] - bf16_lo(h[k]), x[2 * k + 1] - bf16_hi(h[k]));
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // Rows of a slice of n that some of its nn newest queries see: [0, s1) and [w0, n).
@@ -144,9 +155,19 @@ __global__ void __launch_bounds__(RT) q4_rows_kernel(const __grid_constant__ Q4R
   for (int i = 0; i < N; ++i) {
     const int r = r0 + i * (RT / LPR) + static_cast<int>(threadIdx.x) / LPR;
     if (!(write >> i & 1)) continue;
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv)
-      if (p.dst[kv]) reinterpret_cast<uint4*>(p.dst[kv] + (out + r) * D)[c] = values8<D>(w[i][kv], c);
+    const int64_t to = (out + r) * (D / 8) + c;
+    float x[8];
+    if (p.dst[0]) {
+      values8<D>(w[i][0], c, x);
+      const uint4 hi = bf16_of(x);
+      static_cast<uint4*>(p.dst[0])[to] = hi;
+      if (CHUNKED) static_cast<uint4*>(p.k_rest)[to] = rest_of(x, hi);
+    }
+    if (p.dst[1]) {
+      values8<D>(w[i][1], c, x);
+      static_cast<uint4*>(p.dst[1])[to] =
+          CHUNKED ? make_uint4(pack_half(x[0], x[1]), pack_half(x[2], x[3]), pack_half(x[4], x[5]), pack_half(x[6], x[7])) : bf16_of(x);
+    }
   }
 }
 

@@ -662,16 +662,16 @@ DecodeWs decode_ws(const tri_kv* kv, int32_t group, int32_t n_split, bool with_m
   return w;
 }
 
-// Workspace of tri_attn_prefill_q4: one layer's rows in bf16, [n_seq][n_kv_heads][n_cap][d] K, then V,
-// its row counts [n_seq][n_kv_heads] and new tokens [n_seq] (each part 16-byte aligned).
+// Workspace of tri_attn_prefill_q4: one layer's rows, [n_seq][n_kv_heads][n_cap][d] K, what its rounding left, and V
+// (16 bits each), its row counts [n_seq][n_kv_heads] and new tokens [n_seq] (each part 16-byte aligned).
 struct Q4Ws {
-  size_t v_off, valid_off, new_off, total;
+  size_t rows, valid_off, new_off, total;  // rows: bytes of one of the three
 };
 Q4Ws q4_ws(const tri_kv* kv) {
   const size_t n = static_cast<size_t>(kv->n_seq) * kv->n_kv_heads;
   Q4Ws w{};
-  w.v_off = n * kv->n_cap * kv->head_dim * 2;
-  w.valid_off = 2 * w.v_off;
+  w.rows = n * kv->n_cap * kv->head_dim * 2;
+  w.valid_off = 3 * w.rows;
   w.new_off = w.valid_off + align16(n * sizeof(int32_t));
   w.total = w.new_off + align16(kv->n_seq * sizeof(int32_t));
   return w;
@@ -761,8 +761,9 @@ tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out
   if (static_cast<int64_t>(kv->n_seq) * kv->n_kv_heads * kv->n_cap > 0x7fffffff - 256) return TRI_ERR_UNSUPPORTED;
   char* base = static_cast<char*>(ws);
   Q4RowsParams r = q4_rows_params(kv, q->layer);
-  r.dst[0] = reinterpret_cast<__nv_bfloat16*>(base);
-  r.dst[1] = reinterpret_cast<__nv_bfloat16*>(base + w.v_off);
+  r.dst[0] = base;
+  r.k_rest = base + w.rows;
+  r.dst[1] = base + 2 * w.rows;
   r.n_new = p.n_new;
   r.n_q = p.n_q;
   r.n_sink = p.n_sink;
@@ -771,8 +772,8 @@ tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out
   r.n_new_out = reinterpret_cast<int32_t*>(base + w.new_off);
   const cudaError_t e = launch_q4_rows(r, kv->head_dim, stream);
   if (e != cudaSuccess) return attn_status(e);
-  // the rows as a bf16 cache of one layer
-  p.early = 1;
+  // the rows as a cache of one layer, 16 bits an element
+  p.k_rest = r.k_rest;
   p.k = r.dst[0];
   p.v = r.dst[1];
   p.n_valid = r.n_valid_out;
@@ -785,7 +786,7 @@ tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out
   p.rows.slice_bytes = static_cast<int64_t>(kv->n_cap) * p.rows.row_bytes;
   p.out = out;
   p.lse = lse;
-  return attn_status(launch_attn_prefill(p, TRI_BF16, kv->head_dim, stream));
+  return attn_status(launch_attn_prefill(p, TRI_Q4, kv->head_dim, stream));
 }
 
 tri_status tri_read_rows(const tri_kv* kv, int32_t layer, void* k_out, void* v_out, tri_stream_t stream) {
@@ -796,8 +797,8 @@ tri_status tri_read_rows(const tri_kv* kv, int32_t layer, void* k_out, void* v_o
   if (layer < 0 || layer >= kv->n_layers) return TRI_ERR_INVALID_ARG;
   if ((!k_out && !v_out) || !aligned(k_out, 16) || !aligned(v_out, 16)) return TRI_ERR_INVALID_ARG;
   Q4RowsParams r = q4_rows_params(kv, layer);
-  r.dst[0] = static_cast<__nv_bfloat16*>(k_out);
-  r.dst[1] = static_cast<__nv_bfloat16*>(v_out);
+  r.dst[0] = k_out;
+  r.dst[1] = v_out;
   return attn_status(launch_q4_rows(r, kv->head_dim, stream));
 }
 

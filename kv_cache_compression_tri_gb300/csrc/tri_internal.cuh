@@ -350,7 +350,7 @@ struct AttnParams {
   int32_t n_q, group;
   int32_t n_sink, window;
   float scale;                     // of q . k
-  int32_t early;                   // launched while the kernel before, which it waits for, still runs
+  const void* k_rest;              // 4-bit rows written out: K is a bf16 pair, v is fp16 (attn_prefill.cu)
   void* out;                       // [n_seq][n_q][n_kv_heads * group][head_dim]
   float* lse;                      // [n_seq][n_q][n_kv_heads * group], or NULL
   const float* lse_in;             // the weights' log-sums (attn_mass)
@@ -391,10 +391,11 @@ struct AppendParams {
   uint32_t axis_bits[MAX_BANDS / 16];  // two bits per band
 };
 
-// One layer's rows of a 4-bit cache as bf16 values (q4_rows.cu).
+// One layer's rows of a 4-bit cache written out (q4_rows.cu).
 struct Q4RowsParams {
   const char* src[2];      // K, V
-  __nv_bfloat16* dst[2];   // [n_seq][n_kv_heads][n_cap][d] each, or NULL
+  void* dst[2];            // [n_seq][n_kv_heads][n_cap][d] each, or NULL: bf16; for a chunk K in bf16, V in fp16,
+  void* k_rest;            // and what K's rounding left, in bf16
   const int32_t* n_valid;
   int32_t* dev_status;
   RowMap rows;

@@ -13,8 +13,9 @@ Tolerances, for one query with weights w over rows j, c codes, s scales, m minim
            A = sum w (s c + |m|) at most, and where they are subnormal 2^-25 of 2^4 (the largest weight):
            n 2^-29 (15 + max (s c + |m|)). fp32 sums n 2^-24 A. Result rounded to bf16.
   lse, mass  as for bf16 caches.
-The chunk's rows are rounded to bf16 before they are used, so its reference takes the rounded values,
-and its tolerances are those of the bf16 prefill.
+For a chunk K is a bf16 pair, 2^-16 of a value (half a step of half a step) in every product, V and the
+weights are fp16, 2^-11 each: ex = (d + 10) 2^-23 scale sum |q k| + 2^-16 scale sum |q k|, p = 2^-10 of
+A = sum w |v|, and for the subnormal ones of weights up to 2^6 and more, and of V: n 2^-31 max |v| + 2^-25.
 """
 import numpy as np
 import pytest
@@ -304,7 +305,7 @@ def check_prefill(c, G, n_q, layer=1, n_new=None, n_sink=0, window=0, seed=1, ex
             continue
         assert (got_o[b, new:] == 9).all() and (got_l[b, new:] == 9).all()
         for h in range(H):
-            k, v = (bf16(values(x)) for x in c.slice_rows(b, layer, h))
+            k, v = (values(x) for x in c.slice_rows(b, layer, h))
             n = len(k)
             for i in range(new):
                 for hq in range(h * G, (h + 1) * G):
@@ -313,11 +314,11 @@ def check_prefill(c, G, n_q, layer=1, n_new=None, n_sink=0, window=0, seed=1, ex
                     if not seen.any():
                         assert (got_o[b, i, hq] == 0).all() and got_l[b, i, hq] == -np.inf
                         continue
-                    ex = (d + 10) * 2.0 ** -23 * sc * (np.abs(k[seen]) @ np.abs(qn[b, i, hq])).max()
+                    ex = ((d + 10) * 2.0 ** -23 + 2.0 ** -16) * sc * (np.abs(k[seen]) @ np.abs(qn[b, i, hq])).max()
                     x = sc * (k[seen] @ qn[b, i, hq])
                     ew = 2 * ex + 2.0 ** -20 + 2.0 ** -22 * np.abs(x).max()
                     A = w[seen] @ np.abs(v[seen])
-                    tol = A * (2 * ew + 2.0 ** -8 + n * 2.0 ** -24) + 2.0 ** -8 * np.abs(o) + 1e-30
+                    tol = A * (2 * ew + 2.0 ** -10 + n * 2.0 ** -24) + n * 2.0 ** -31 * np.abs(v[seen]).max() + 2.0 ** -25 + 2.0 ** -8 * np.abs(o)
                     assert (np.abs(got_o[b, i, hq] - o) <= tol).all()
                     assert abs(got_l[b, i, hq] - l) <= ex + ew + 2.0 ** -22 * max(1.0, abs(l))
 
@@ -496,9 +497,10 @@ def test_serving_run(block):
             k, v = (values(np.stack([r[part] for r in rows[h]])) for part in (0, 1))
             for i in range(n):
                 o, _, w = attend(f64(qr[0, i, h * G]), k, v, m - n + i, d ** -0.5)
-                # loose: rows rounded to bf16 for the chunk move a logit by 2^-8 sum |q k| scale at most
-                x = 2.0 ** -8 * d ** -0.5 * (np.abs(k) @ np.abs(f64(qr[0, i, h * G]))).max() if n > 1 else 2.0 ** -10
-                assert (np.abs(f64(out[0, i, h * G]) - o) <= (2 * x + 2.0 ** -6) * (w @ np.abs(v)) + 2.0 ** -8 * np.abs(o) + 2.0 ** -8).all()
+                # half a step of the result, 2^-10 of sum w |v| (weights and V in fp16), and K's 2^-16 in a logit, in both cases
+                x = 2.0 ** -15 * d ** -0.5 * (np.abs(k) @ np.abs(f64(qr[0, i, h * G]))).max()
+                A = w @ np.abs(v) if n > 1 else w @ sizes(np.stack([r[1] for r in rows[h]]))
+                assert (np.abs(f64(out[0, i, h * G]) - o) <= (2 * x + 2.0 ** -9) * A + 2.0 ** -8 * np.abs(o) + 2.0 ** -20).all()
 
     at = 0
     qr = step(n0, at)

@@ -103,7 +103,7 @@ def test_attention_over_4_bits_rejects_bad_buffers(lib):  # noqa: F811
     for o in (dict(out=None), dict(out=0x30004), dict(lse=0x50002), dict(ws=None), dict(ws=0x40008), dict(ws_bytes=0)):
         assert list(_q4_calls(lib, kv, _q(), **o)) == [INVALID] * 2
     need = lib.tri_attn_prefill_q4_workspace_bytes(ctypes.byref(kv))
-    assert need >= 2 * 2 * 128 * 64 * 2 and need % 16 == 0  # K and V of two heads in bf16
+    assert need >= 3 * 2 * 128 * 64 * 2 and need % 16 == 0  # K twice and V of two heads, 16 bits
     assert list(_q4_calls(lib, kv, _q(), ws_bytes=need - 1))[1] == INVALID
     assert lib.tri_attn_prefill_q4_workspace_bytes(None) == 0
     for other in (_kv(key_layout=1), _kv(key_layout=1, dtype=0)):  # bf16 and fp32 caches have their own call
