@@ -54,20 +54,22 @@ constexpr int STEP = 64;     // cached rows of a step
 constexpr float RAISE = 8.f;
 constexpr int MAX_SPLITS = 8;  // CTAs that share query tiles
 
-template <int D, int NQ>
+template <int D, int NQ, bool Q4 = false>
 struct TcSmem {
   static constexpr int TILE = D / 64 * TCOL;
   static constexpr int THREADS = 128 + NQ * 256;  // copy warp, two MMA warps, an idle one, two warpgroups per query tile
-  static constexpr int NST = D == 128 ? 4 : 5;
+  // (Q4: stages of a step's rows)
+  static constexpr int STAGE = Q4 ? TILE / 2 : TILE;
+  static constexpr int NST = Q4 ? (D == 128 ? 9 : 10) : D == 128 ? 4 : 5;
   static constexpr int RING = NQ * TILE;  // after the query tiles
   static constexpr int TMEM = NQ * 256;   // columns: per query tile 2 x 64 of S/P and up to 128 of O
-  static constexpr int CTRL = RING + NST * TILE;
+  static constexpr int CTRL = RING + NST * STAGE;
   static constexpr int BYTES = CTRL + 4608;
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
 struct TcCtl {
-  uint64_t full[8], empty[8];                           // ring stages
+  uint64_t full[10], empty[10];                         // ring stages
   uint64_t q_ready[2];                                  // the query tile is in shared memory
   uint64_t s_full[2][2], p_ready[2][2], o_ready[2][2];  // [query tile][half of a tile of rows]: S complete; P written; its product complete
   uint64_t v_fix;                                       // the last tile of V has landed, before its tail is cleared
@@ -128,15 +130,16 @@ __device__ __forceinline__ float weights_of(const uint32_t (&x)[32], float sl, f
 }
 
 // Q4: the rows of a 4-bit cache, written out before. K as a bf16 pair (kmap; lmap: what the first rounding left),
-// two tiles of the ring and two products: 16 bits of its values. V and the weights in fp16, the latter up to 2^14 (no
-// further pair): 2^-11 of a weight, and 2^-25 of the smallest that counts.
+// two products: 16 bits of its values. V and the weights in fp16, the latter up to 2^14 (no further pair): 2^-11 of
+// a weight, and 2^-25 of the smallest that counts. A tile of rows then is three tiles of shared memory, and a ring
+// of four left the next K on its way when its product was due (4096 tokens over 8192 rows 599 us): here a
+// stage has one step's rows, and they come in the order in which the MMA warps take them.
 template <int D, int NQ, bool FEW_CTAS, bool ODD, bool Q4>
-__global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
+__global__ void __launch_bounds__((TcSmem<D, NQ, Q4>::THREADS), 3 - NQ)
     prefill_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ RowMaps<ODD> kmap,
                       const __grid_constant__ RowMaps<ODD> vmap, const __grid_constant__ RowMaps<Q4 ? ODD : false> lmap,
                       const __grid_constant__ RowNumbers rn, int n_tiles, int cluster) {
-  using L = TcSmem<D, NQ>;
-  constexpr int PER = Q4 ? 3 : 2;               // ring stages of a tile of rows: K (twice), V
+  using L = TcSmem<D, NQ, Q4>;
   constexpr bool PAIR = FEW_CTAS && !Q4;        // the weights as a pair
   constexpr float LIFT = Q4 ? 6.f : 0.f;        // log2 of the weight of a row's running maximum
   const int splits = FEW_CTAS ? cluster : 1;
@@ -237,23 +240,20 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
     auto place_of = [&](int blk, int k0) { return box_place<D, ODD>(rn, box, blk, c.h, k0); };
     int blk_next = n_list ? block_of(tile_row(0)) : 0;
     Place place = n_list ? place_of(blk_next, tile_row(0)) : Place{0, 0};
-    for (; cnt < PER * n_list && ok; ++cnt) {
-      const int i = cnt / PER, part = cnt % PER, st = cnt % L::NST, k0 = tile_row(i);
-      if (part == 0 && i + 1 < n_list)  // (on its way while this tile waits for its stage)
-        blk_next = block_of(tile_row(i + 1));
+    for (; !Q4 && cnt < 2 * n_list && ok; ++cnt) {
+      const int st = cnt % L::NST, k0 = tile_row(cnt >> 1);
+      if (!(cnt & 1) && cnt + 2 < 2 * n_list)  // (on its way while this tile waits for its stage)
+        blk_next = block_of(tile_row((cnt >> 1) + 1));
       if (cnt >= L::NST) ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (cnt / L::NST - 1) & 1));
       if (!ok) break;
-      const bool is_v = part == PER - 1;
+      const bool is_v = cnt & 1;
       const bool fix = is_v && k0 + TROWS - 1 > r_hi;
       uint64_t* bar = fix ? &ctl.v_fix : &ctl.full[st];
       if (bad & 1) ctl.flag[0] = 1;
       if (bad & 2) ctl.flag[1] = 1;
       __syncwarp();
-      if (Q4 && part == 1)
-        load_tile<D, Q4 ? ODD : false>(ring + st * L::TILE, lmap, box, place, bar, lane);
-      else
-        load_tile<D, ODD>(ring + st * L::TILE, is_v ? vmap : kmap, box, place, bar, lane);
-      if (is_v && i + 1 < n_list) place = place_of(blk_next, tile_row(i + 1));
+      load_tile<D, ODD>(ring + st * L::TILE, is_v ? vmap : kmap, box, place, bar, lane);
+      if (is_v && cnt + 1 < 2 * n_list) place = place_of(blk_next, tile_row((cnt >> 1) + 1));
       if (fix) {
         ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.v_fix, 0));
         if (!ok) break;
@@ -264,6 +264,46 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.full[st]);
+      }
+    }
+    if constexpr (Q4) {
+      // steps in turn: K of the first two, then V of a step and K of the step after next (slices only: the rows written out)
+      const int slice = c.seq * static_cast<int>(rn.outer) + c.h * static_cast<int>(rn.head), steps = 2 * n_list;
+      int st = 0, round = 0;  // the next load's stage, and how often the ring has been round
+      auto load = [&](const CUtensorMap* map, int k0, bool fix) {
+        if (round > 0) ok = ok && __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.empty[st], (round - 1) & 1));
+        if (!ok) return;
+        uint64_t* bar = fix ? &ctl.v_fix : &ctl.full[st];
+        if (lane == 0) mbar_arrive_expect_tx(bar, L::STAGE);
+        __syncwarp();
+        if (lane < D / 64) tma_load2(ring + st * L::STAGE + lane * (TCOL / 2), map, lane * 64, slice + k0, bar);
+        ++cnt;
+        if (fix) {  // rows past the last query's: zeros
+          ok = __all_sync(FULL_MASK, mbar_wait_bounded(&ctl.v_fix, 0));
+          if (!ok) return;
+          unsigned char* v = smem + L::RING + st * L::STAGE;
+          for (int i = (r_hi + 1 - k0) * 8 + lane; i < STEP * 8; i += 32)
+#pragma unroll
+            for (int a = 0; a < D / 64; ++a) *reinterpret_cast<uint4*>(v + a * (TCOL / 2) + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.full[st]);
+        }
+        if (++st == L::NST) {
+          st = 0;
+          ++round;
+        }
+      };
+      auto row_of = [&](int y) { return tile_row(y >> 1) + (y & 1) * STEP; };
+      auto load_k = [&](int y) {
+        load(&kmap.m[0], row_of(y), false);
+        load(&lmap.m[0], row_of(y), false);
+      };
+      for (int y = 0; y < min(2, steps) && ok; ++y) load_k(y);
+      for (int y = 0; y < steps && ok; ++y) {
+        const int k0 = row_of(y);
+        load(&vmap.m[0], k0, k0 <= r_hi && k0 + STEP - 1 > r_hi);  // (a step past it is nobody's)
+        if (y + 2 < steps) load_k(y + 2);
       }
     }
     if (bad) set_status(p.dev_status, TRI_DEV_BAD_BLOCK);
@@ -288,36 +328,25 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
           const uint64_t off = (k >> 2) * (TCOL >> 4) + (k & 3) * 2;
           umma_f16(s_col(q, b), dq + off, ds + off, IQK, k > 0);
         }
-        if constexpr (Q4) {  // the pair's second half, in the stage behind
-          const uint64_t dl = dk + (at + 1 == L::NST ? 0 : at + 1) * STAGE + b * (STEP * 8);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t off = (k >> 2) * (TCOL >> 4) + (k & 3) * 2;
-            umma_f16(s_col(q, b), dq + off, dl + off, IQK, true);
-          }
-        }
         umma_commit(&ctl.s_full[q][b]);
       };
       uint32_t use[2] = {0, 0};  // products of each buffer
       auto step_of = [&](int i) { return 2 * list.at(first + i); };
       ok = mbar_wait_bounded(&ctl.q_ready[q], 0);
-      if (n_list > 0 && ok) {
+      if (!Q4 && n_list > 0 && ok) {
         ok = mbar_wait_bounded(&ctl.full[0], 0);
-        if (Q4 && ok) ok = mbar_wait_bounded(&ctl.full[1], 0);
         tc_fence_after();
 #pragma unroll
         for (int b = 0; b < 2; ++b)
           if (ok && need.has(step_of(0) + b)) issue_s(0, b);
         umma_commit(&ctl.empty[0]);
-        if (Q4) umma_commit(&ctl.empty[1]);
       }
-      for (int i = 0; i < n_list && ok; ++i) {
+      for (int i = 0; !Q4 && i < n_list && ok; ++i) {
         const bool more = i + 1 < n_list;
         const int x = step_of(i), xn = more ? step_of(i + 1) : need.e;
-        const uint32_t cv = PER * i + PER - 1, sv = cv % L::NST, sk = (cv + 1) % L::NST, sl = (cv + 2) % L::NST;
+        const uint32_t cv = 2 * i + 1, sv = cv % L::NST, sk = (cv + 1) % L::NST;
         ok = mbar_wait_bounded(&ctl.full[sv], (cv / L::NST) & 1);
         if (ok && more) ok = mbar_wait_bounded(&ctl.full[sk], ((cv + 1) / L::NST) & 1);
-        if (Q4 && ok && more) ok = mbar_wait_bounded(&ctl.full[sl], ((cv + 2) / L::NST) & 1);
         if (!ok) break;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -340,7 +369,57 @@ __global__ void __launch_bounds__((TcSmem<D, NQ>::THREADS), 3 - NQ)
         }
         umma_commit(&ctl.empty[sv]);
         if (more) umma_commit(&ctl.empty[sk]);
-        if (Q4 && more) umma_commit(&ctl.empty[sl]);
+      }
+      if constexpr (Q4) {
+        // the steps as the copy warp brings them
+        constexpr uint64_t COL = TCOL >> 5;  // a step's 64-element column, in 16 bytes
+        constexpr uint64_t QSTAGE = L::STAGE >> 4;
+        const uint64_t dvs = sw128_desc_mn(ring, TCOL / 2);
+        const int steps = 2 * n_list;
+        uint32_t st = 0, par = 0;
+        auto landed = [&] { ok = ok && mbar_wait_bounded(&ctl.full[st], par); };
+        auto done = [&] {  // the stage is free once what reads it has completed
+          umma_commit(&ctl.empty[st]);
+          if (++st == L::NST) {
+            st = 0;
+            par ^= 1;
+          }
+        };
+        auto id_of = [&](int y) { return 2 * list.at(first + (y >> 1)) + (y & 1); };
+        auto products_s = [&](int y) {
+          const int b = y & 1;
+          const bool seen = need.has(id_of(y));
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            landed();
+            tc_fence_after();
+            if (ok && seen) {
+              const uint64_t ds = dk + st * QSTAGE;
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                umma_f16(s_col(q, b), dq + (k >> 2) * (TCOL >> 4) + (k & 3) * 2, ds + (k >> 2) * COL + (k & 3) * 2, IQK, half > 0 || k > 0);
+              if (half) umma_commit(&ctl.s_full[q][b]);
+            }
+            done();
+          }
+        };
+        for (int y = 0; y < min(2, steps) && ok; ++y) products_s(y);
+        for (int y = 0; y < steps && ok; ++y) {
+          const int b = y & 1;
+          landed();
+          if (ok && need.has(id_of(y))) {
+            ok = mbar_wait_bounded(&ctl.p_ready[q][b], use[b] & 1);
+            tc_fence_after();
+            const uint64_t ds = dvs + st * QSTAGE;
+            umma_ts(to, s_col(q, b), ds, IPV, use[0] + use[1] > 0);
+#pragma unroll
+            for (int j = 1; j < STEP / 16; ++j) umma_ts(to, s_col(q, b) + (j >> 1) * 32 + (j & 1) * 8, ds + j * 128, IPV, true);
+            umma_commit(&ctl.o_ready[q][b]);
+            ++use[b];
+          }
+          done();
+          if (ok && y + 2 < steps) products_s(y + 2);
+        }
       }
       if (!ok) set_status(p.dev_status, TRI_DEV_TIMEOUT);
     }
@@ -582,12 +661,12 @@ cudaError_t launch_tc(const AttnParams& p, const RowNumbers& rn, cudaStream_t st
   int splits = 1;
   while (few && splits < MAX_SPLITS && units * splits * 2 <= SMS && rows >= 2 * splits * 2 * TROWS) splits *= 2;
   auto kern = few ? prefill_tc_kernel<D, NQ, true, ODD, Q4> : prefill_tc_kernel<D, NQ, false, ODD, Q4>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D, NQ>::BYTES);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<D, NQ, Q4>::BYTES);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(units * splits));
-  cfg.blockDim = dim3(TcSmem<D, NQ>::THREADS);
-  cfg.dynamicSmemBytes = TcSmem<D, NQ>::BYTES;
+  cfg.blockDim = dim3(TcSmem<D, NQ, Q4>::THREADS);
+  cfg.dynamicSmemBytes = TcSmem<D, NQ, Q4>::BYTES;
   cfg.stream = st;
   cudaLaunchAttribute at[2]{};
   if (splits > 1) {
@@ -726,6 +805,7 @@ cudaError_t launch_attn_prefill(const AttnParams& p, tri_dtype dt, int head_dim,
   if (dt == TRI_Q4) {
     RowNumbers rn{};
     if (!row_numbers(p, rn)) return cudaErrorNotSupported;
+    rn.box_rows = STEP;
     return head_dim == 64 ? launch_tc<64, false, true>(p, rn, st) : launch_tc<128, false, true>(p, rn, st);
   }
   if (dt == TRI_BF16) {

@@ -203,11 +203,11 @@ __device__ __forceinline__ void load_query_tile(uint32_t dst, const AttnParams& 
 constexpr uint32_t bf16_idesc(int m, int n, bool b_mn) {
   return f16_idesc(m, n) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u);
 }
-// Descriptor of an MN-major operand in the 128-byte swizzle: 16 KB between its
-// 64-element columns (leading offset), 1024 bytes between groups of eight rows.
-__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr) {
+// Descriptor of an MN-major operand in the 128-byte swizzle: `column` bytes between its
+// 64-element columns (leading offset; 16 KB in a tile), 1024 bytes between groups of eight rows.
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t column = TCOL) {
   uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(TCOL >> 4) << 16;
+  d |= static_cast<uint64_t>(column >> 4) << 16;
   d |= static_cast<uint64_t>(1024u >> 4) << 32;
   d |= static_cast<uint64_t>(1u) << 46;
   d |= static_cast<uint64_t>(2u) << 61;
