@@ -808,7 +808,7 @@ static DecodePlan attn_decode_plan_q4(int n_slices, int max_rows) {
   while (2 * s <= MAX_CLUSTER && n * 2 * s <= slots && max_rows >= 64 * 2 * s) s *= 2;
   const int64_t few = min(slots / 2 / n, static_cast<int64_t>(max_rows / 384));
   if (few > s) return {static_cast<int>(min(few, static_cast<int64_t>(MAX_SPLIT))), false};
-  if (max_rows / s >= 4096) return {2 * s, false};
+  if (max_rows / s >= 4096 && 2 * s <= attn_decode_max_splits(n_slices, max_rows)) return {2 * s, false};  // (as many as the workspace holds)
   for (int k = s; k <= 4 * s && max_rows >= 512 * k; ++k)
     if (n * k * 5 >= (n * k + slots - 1) / slots * slots * 4) return {k, k == s};
   return {s, true};

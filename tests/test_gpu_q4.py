@@ -221,6 +221,39 @@ def test_pools_in_any_order(order, pad):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("n_slices,rows", [(38, 65536), (19, 131072), (20, 65600), (60, 33000), (304, 8192), (400, 4096)])
+def test_runs_stay_within_the_workspace(n_slices, rows):
+    k = torch.randint(0, 256, (1, 1, n_slices, rows, 48), dtype=torch.uint8, device="cuda")
+    k[..., 32:] = torch.tensor([0.125, -1.0] * 4).half().view(torch.uint8).cuda()
+    nv = torch.full((n_slices,), rows, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kv = tri.KVCache(k, k, nv, None, None, status, post_rope=True)
+    q = torch.zeros(1, n_slices, 64, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros_like(q)
+    need = tri.attn_decode_workspace_bytes(kv, 1)
+    ws = torch.full((need + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    tri.attn_decode(kv, 0, q, out, workspace=ws[:need])
+    assert int(status) == 0 and bool((ws[need:] == 0xA5).all())
+    # equal weights: the mean of the rows. Weights are exact; 32-bit sums and the result's rounding
+    rows_out = torch.zeros(1, n_slices, rows, 64, dtype=torch.bfloat16, device="cuda")
+    tri.read_rows(kv, 0, None, rows_out)  # (codes / 8 - 1: exact in bf16)
+    want = rows_out.double().mean(2)
+    assert bool(((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + rows * 2.0 ** -24 * 2).all())
+
+
+def test_bad_row_counts():
+    c = Case([[40, 39], [60, 50]], 64)
+    c.kv.n_valid[4] = c.cap + 1  # sequence 1, layer 0, head 0
+    q = torch.randn(2, 4, 64, device="cuda").bfloat16()
+    out = torch.full((2, 4, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    tri.attn_decode(c.kv, 0, q, out)
+    assert int(c.status) == 1 and bool((out[1, :2] == 9).all()) and bool((out[1, 2:] != 9).any()) and bool((out[0] != 9).any())
+    c.status.zero_()
+    chunk, x = torch.full((2, 3, 4, 64), 9.0, dtype=torch.bfloat16, device="cuda"), torch.randn(2, 3, 4, 64, device="cuda").bfloat16()
+    tri.attn_prefill(c.kv, 0, x, chunk)
+    assert int(c.status) == 1 and bool((chunk[1, :, :2] == 9).all()) and bool((chunk[0] != 9).any())
+
+
 def test_decode_repeats_bit_for_bit():
     c = Case([[700, 40], [2, 333]], 128, block=16)
     a, b = check_decode(c, 4, with_mass=True), check_decode(c, 4, with_mass=True)
