@@ -516,7 +516,8 @@ tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out
  * Rotation: band f of a head vector (pairs as `style` says) is multiplied by
  * e^{i w_f p}, w_f = rope_theta^(-2f/d), with p = positions[seq][i][band_axis[f]]:
  * one axis for text; several (time, height, width) for images and video, each
- * band belonging to one. Angles are exact to 2^-52 turns or so at any position.
+ * band belonging to one. Phases are 64-bit fixed-point products: an angle is off by
+ * some 2^-55 turns for each position, and fp32 arithmetic adds 2^-21 of an element.
  * A query at a text position p has all axes equal to p, so tri_score of the
  * post-RoPE keys (which needs no positions) stays what it is for keys of several
  * axes; pre-RoPE caches carry one position per row, so n_axes > 1 is refused there
@@ -525,7 +526,8 @@ tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out
  * TRI_DEV_NVALID_OVER_CAP; n_new: TRI_DEV_BAD_QUERY; the table entry of a block that
  * a new row falls into: TRI_DEV_BAD_BLOCK) keeps its row count and its valid rows;
  * rows from n_valid on may have been written.
- * kv->pos_out is not used. Rows of one call must not coincide (no block in two
+ * kv->pos_out is not used; with kv->pos NULL nothing keeps the positions (pre-RoPE
+ * keys are then scored at their rows' numbers). Rows of one call must not coincide (no block in two
  * sequences' tables at rows that the call writes).
  * ------------------------------------------------------------------------ */
 typedef struct {

@@ -22,7 +22,7 @@
 //   O^T += V^T P^T: A = V transposed, 16 elements of a quarter x 16 rows. Two rows' codes of
 //   an element come together by a byte permute of their words, before they are
 //   spread. B = p s_j in fp16, p up to 2^4 (a scale is below 2^12): two
-//   roundings of 2^-11 of its weight, where results are rounded to 2^-9.
+//   roundings of 2^-11 of its weight, where results are rounded to 2^-8.
 // Each warp owns a ring of NST tiles of 32 (d 64: 64) rows, K and V, filled by 16-byte asynchronous copies
 // of whole contiguous tiles (bulk copies by lanes of a warp took 20 instructions more per 16 rows
 // than these); table entries are read a tile ahead. Rows out of sight are copied but not
