@@ -495,11 +495,14 @@ tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* ls
  * TRI_ERR_UNSUPPORTED otherwise). The rows that some query may see are first
  * written to ws, the values of K as a pair of bf16, those of V in fp16; the kernel
  * then reads those. Weights are rounded to fp16 for their product with V (their sum
- * is not). ws: device scratch of tri_attn_prefill_q4_workspace_bytes(kv) bytes (one
- * layer's rows, 6 head_dim bytes each), 16-byte aligned, no initial contents
- * needed; calls that may overlap need one each. A sequence with a fault in n_new, or in the table entry
- * of a block that one of its queries sees (in any head), is skipped as a whole, one
- * with a bad row count as tri_attn_prefill skips it. */
+ * is not). Calls of few tokens (n_q * group up to 8, as a draft's tokens have) read
+ * the 4-bit rows themselves, as tri_attn_decode does. ws: device scratch of
+ * tri_attn_prefill_q4_workspace_bytes(kv) bytes (one layer's rows, 6 head_dim bytes
+ * each, or what those calls need), 16-byte aligned, no initial contents needed;
+ * calls that may overlap need one each. A sequence with a fault in n_new is skipped;
+ * one with a bad table entry of a block that one of its queries sees is skipped as
+ * a whole, in calls of few tokens in the heads that see it; a bad row count leaves
+ * out its slice. */
 size_t tri_attn_prefill_q4_workspace_bytes(const tri_kv* kv);
 tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out, float* lse, void* ws, size_t ws_bytes,
                                tri_stream_t stream);

@@ -52,7 +52,8 @@ namespace {
 struct Run {
   int64_t s;       // slice of the cache
   int n, seq, h;   // valid rows, sequence, KV head
-  Visible vis;
+  int news;        // new tokens
+  Visible vis;     // (of a chunk: to some token of it)
   int count;       // visible rows
 };
 
@@ -67,7 +68,12 @@ __device__ __forceinline__ bool slice_run(const AttnParams& p, int ls, Run& r) {
     return false;
   }
   if (nn <= 0) return false;
+  r.news = nn;
   r.vis = visible_rows(r.n - 1, p.n_sink, p.window);
+  if (p.token_heads) {
+    r.vis.w0 = visible_rows(max(r.n - nn, 0), p.n_sink, p.window).w0;
+    r.vis.s1 = min(r.vis.s1, r.vis.w0);
+  }
   r.count = r.vis.s1 + r.n - r.vis.w0;
   return true;
 }
@@ -115,14 +121,21 @@ __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.laun
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The result of a head's element, or of its log-sum, from the sums of all its rows.
+// The row of out and lse that column g of a slice has, or -1 (a token that is not there).
+__device__ __forceinline__ int64_t row_of_column(const AttnParams& p, const Run& r, int g) {
+  if (!p.token_heads) return (static_cast<int64_t>(r.seq) * p.n_kv_heads + r.h) * p.group + g;
+  const int tok = g / p.token_heads;
+  if (tok >= r.news) return -1;
+  return ((static_cast<int64_t>(r.seq) * p.n_q + tok) * p.n_kv_heads + r.h) * p.token_heads + g - tok * p.token_heads;
+}
 template <typename T, int D>
 __device__ __forceinline__ void store_out(const AttnParams& p, const Run& r, int g, int e, float o, float l) {
-  const int64_t row = (static_cast<int64_t>(r.seq) * p.n_kv_heads + r.h) * p.group + g;
-  static_cast<T*>(p.out)[row * D + e] = from_f32<T>(l != 0.f ? o / l : 0.f);
+  const int64_t row = row_of_column(p, r, g);
+  if (row >= 0) static_cast<T*>(p.out)[row * D + e] = from_f32<T>(l != 0.f ? o / l : 0.f);
 }
 __device__ __forceinline__ void store_lse(const AttnParams& p, const Run& r, int g, float m, float l) {
-  const int64_t row = (static_cast<int64_t>(r.seq) * p.n_kv_heads + r.h) * p.group + g;
-  if (p.lse) p.lse[row] = l != 0.f ? LN2 * (m + log2f(l)) : NEG_INF;
+  const int64_t row = row_of_column(p, r, g);
+  if (p.lse && row >= 0) p.lse[row] = l != 0.f ? LN2 * (m + log2f(l)) : NEG_INF;
 }
 
 // mass[j] += sum over the heads of 2^(x_j - m) / l for rows j = row_at(i), i in
@@ -762,9 +775,13 @@ cudaError_t launch_bf16(const AttnParams& p, int max_rows, cudaStream_t st) {
 template <int D>
 cudaError_t launch_q4(const AttnParams& p, int max_rows, cudaStream_t st) {
   using G = TileGeo<Q4Tag, D>;
-  auto kern = !p.rows.table                  ? decode_q4_kernel<D, SLICES>
-              : p.rows.block_size >= G::TK ? decode_q4_kernel<D, WHOLE_TILES>
-                                             : decode_q4_kernel<D, SMALL_BLOCKS>;
+  const bool whole = p.rows.block_size >= G::TK;
+  auto kern = p.token_heads ? (!p.rows.table ? decode_q4_kernel<D, SLICES, true>
+                               : whole       ? decode_q4_kernel<D, WHOLE_TILES, true>
+                                             : decode_q4_kernel<D, SMALL_BLOCKS, true>)
+                            : (!p.rows.table ? decode_q4_kernel<D, SLICES, false>
+                               : whole       ? decode_q4_kernel<D, WHOLE_TILES, false>
+                                             : decode_q4_kernel<D, SMALL_BLOCKS, false>);
   const cudaError_t e = launch_runs(kern, G::SMEM, p, st);
   return e != cudaSuccess || p.join ? e : launch_join<__nv_bfloat16, D>(p, max_rows, st);
 }

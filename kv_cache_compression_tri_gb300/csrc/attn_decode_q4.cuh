@@ -137,9 +137,10 @@ __device__ __forceinline__ void query_fragments(const __nv_bfloat16* q, bool liv
   sums = pack_half(hi, s - hi);
 }
 
-// BLOCKS: how the cache's rows lie.
+// BLOCKS: how the cache's rows lie. CHUNK: the columns are the heads of a few tokens, each with its own last row (the
+// newest p.n_q rows are theirs); tiles at the edge of what some token sees are masked column by column.
 enum Q4Blocks { SLICES, WHOLE_TILES, SMALL_BLOCKS };  // slices; pools whose blocks hold whole tiles, or not
-template <int D, Q4Blocks BLOCKS>
+template <int D, Q4Blocks BLOCKS, bool CHUNK>
 __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_constant__ AttnParams p) {
   using G = TileGeo<Q4Tag, D>;
   constexpr bool PAGED = BLOCKS != SLICES, whole = BLOCKS != SMALL_BLOCKS;
@@ -257,8 +258,10 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
   float f0, f1;
   {
     int shift;
-    query_fragments<D>(static_cast<const __nv_bfloat16*>(p.q) + r.seq * p.q_seq + (static_cast<int64_t>(r.h) * p.group + lg) * D,
-                       lg < p.group, lt, qf, qsum, shift);
+    const int tok = CHUNK ? lg / p.token_heads : 0, heads = CHUNK ? p.token_heads : p.group;
+    query_fragments<D>(static_cast<const __nv_bfloat16*>(p.q) + r.seq * p.q_seq + tok * p.q_token +
+                           (static_cast<int64_t>(r.h) * heads + lg - tok * heads) * D,
+                       lg < p.group && tok < r.news, lt, qf, qsum, shift);
     const int s0 = __shfl_sync(FULL_MASK, shift, 8 * lt), s1 = __shfl_sync(FULL_MASK, shift, 8 * lt + 4);
     const float sl = p.scale * LOG2E;
     // (not 0, which an invisible row's -inf would not survive)
@@ -320,8 +323,17 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
       }
       const int ja = r0 + 16 * s + lg, jb = ja + 8;
       if (!INNER) {
-        if (!(ja < r.n && (ja < r.vis.s1 || ja >= r.vis.w0))) x[s][0] = x[s][1] = NEG_INF;
-        if (!(jb < r.n && (jb < r.vis.s1 || jb >= r.vis.w0))) x[s][2] = x[s][3] = NEG_INF;
+        if constexpr (CHUNK) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int j = c < 2 ? ja : jb, last = r.n - r.news + (2 * lt + (c & 1)) / p.token_heads;
+            const Visible v = visible_rows(last, p.n_sink, p.window);
+            if (!(j < r.n && j <= last && (j < v.s1 || j >= v.w0))) x[s][c] = NEG_INF;
+          }
+        } else {
+          if (!(ja < r.n && (ja < r.vis.s1 || ja >= r.vis.w0))) x[s][0] = x[s][1] = NEG_INF;
+          if (!(jb < r.n && (jb < r.vis.s1 || jb >= r.vis.w0))) x[s][2] = x[s][3] = NEG_INF;
+        }
       }
       if (logits) {  // (rows out of sight: their entries are not read)
 #pragma unroll
@@ -404,6 +416,13 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
       }
     }
   };
+  // rows below all_s1, and from all_w0 up to all_end, are in every column's sight
+  int all_end = r.n, all_w0 = r.vis.w0, all_s1 = r.vis.s1;
+  if constexpr (CHUNK) {
+    all_end = max(r.n - r.news + 1, 0);
+    all_w0 = visible_rows(r.n - 1, p.n_sink, p.window).w0;
+    all_s1 = visible_rows(max(r.n - r.news, 0), p.n_sink, p.window).s1;
+  }
   int st = 0;
   for (int u = tl.u0 + w; u < tl.u1; u += NW) {
     {
@@ -416,7 +435,7 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
     __syncwarp();
     const int r0 = tl.row(u);
     const uint32_t tk = ring + st * 2 * G::TILE;
-    if (r0 + G::TK <= r.n && (r0 >= r.vis.w0 || r0 + G::TK <= r.vis.s1))
+    if (r0 + G::TK <= all_end && (r0 >= all_w0 || r0 + G::TK <= all_s1))
       tile(std::true_type{}, r0, tk);
     else
       tile(std::false_type{}, r0, tk);

@@ -744,7 +744,8 @@ tri_status tri_attn_prefill(const tri_kv* kv, const tri_queries* q, void* out, f
 
 size_t tri_attn_prefill_q4_workspace_bytes(const tri_kv* kv) {
   if (check_kv(kv, true, true) != TRI_OK || kv->dtype != TRI_Q4) return 0;
-  return q4_ws(kv).total;
+  const int n = kv->n_seq * kv->n_kv_heads;
+  return std::max(q4_ws(kv).total, decode_ws(kv, MAX_GROUP, attn_decode_max_splits(n, kv->n_cap), false).total);
 }
 
 tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out, float* lse, void* ws, size_t ws_bytes,
@@ -755,8 +756,27 @@ tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out
   if (st != TRI_OK) return st;
   if (kv->dtype != TRI_Q4) return TRI_ERR_UNSUPPORTED;
   if (!out || !aligned(out, 16) || (lse && !aligned(lse, 4))) return TRI_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 16) || ws_bytes < tri_attn_prefill_q4_workspace_bytes(kv)) return TRI_ERR_INVALID_ARG;
+  const int64_t slices = static_cast<int64_t>(kv->n_seq) * kv->n_kv_heads;
+  if (static_cast<int64_t>(q->n_q) * q->group <= MAX_GROUP && slices * std::max<int64_t>(16, kv->n_cap / 1024 + 1) <= 0x7fffffff) {
+    // as many query rows as the decode kernel has columns: it reads the 4-bit rows once, where they would be
+    // written out and read again (2 tokens of 16 sequences over 8 x 32768 rows, group 4)
+    const int n = static_cast<int>(slices);
+    const int64_t seen = static_cast<int64_t>(q->n_sink) + q->window + q->n_q - 1;
+    const int rows = q->window == 0 ? kv->n_cap : static_cast<int>(std::min<int64_t>(kv->n_cap, seen));
+    const DecodePlan plan = attn_decode_plan(n, rows, kv->dtype);
+    p.token_heads = q->group;
+    p.group = q->n_q * q->group;
+    p.n_split = plan.n_split;
+    p.join = plan.join;
+    const DecodeWs d = decode_ws(kv, p.group, p.n_split, false);
+    p.part_o = static_cast<float*>(ws);
+    p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + d.ml_off);
+    p.out = out;
+    p.lse = lse;
+    return launch_attn_decode(p, rows, kv->dtype, kv->head_dim, stream) == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
+  }
   const Q4Ws w = q4_ws(kv);
-  if (!ws || !aligned(ws, 16) || ws_bytes < w.total) return TRI_ERR_INVALID_ARG;
   // more rows than the attention's copies can number are refused before anything is enqueued
   if (static_cast<int64_t>(kv->n_seq) * kv->n_kv_heads * kv->n_cap > 0x7fffffff - 256) return TRI_ERR_UNSUPPORTED;
   char* base = static_cast<char*>(ws);

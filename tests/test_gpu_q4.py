@@ -338,8 +338,10 @@ def check_prefill(c, G, n_q, layer=1, n_new=None, n_sink=0, window=0, seed=1, ex
             continue
         assert (got_o[b, new:] == 9).all() and (got_l[b, new:] == 9).all()
         for h in range(H):
-            k, v = (values(x) for x in c.slice_rows(b, layer, h))
+            kb, vb = c.slice_rows(b, layer, h)
+            k, v = values(kb), values(vb)
             n = len(k)
+            few = n_q * G <= 8
             for i in range(new):
                 for hq in range(h * G, (h + 1) * G):
                     o, l, w = attend(qn[b, i, hq], k, v, n - new + i, sc, n_sink, window) if n else (np.zeros(d), -np.inf, np.zeros(0))
@@ -347,11 +349,17 @@ def check_prefill(c, G, n_q, layer=1, n_new=None, n_sink=0, window=0, seed=1, ex
                     if not seen.any():
                         assert (got_o[b, i, hq] == 0).all() and got_l[b, i, hq] == -np.inf
                         continue
-                    ex = ((d + 10) * 2.0 ** -23 + 2.0 ** -16) * sc * (np.abs(k[seen]) @ np.abs(qn[b, i, hq])).max()
+                    if few:  # the decode's: codes, scales and minima apart
+                        ex = (d / 4 + 16) * 2.0 ** -23 * sc * (sizes(kb[seen]) @ np.abs(qn[b, i, hq])).max()
+                        sv = sizes(vb[seen])
+                        small = n * 2.0 ** -29 * (15 + sv.max())
+                    else:
+                        ex = ((d + 10) * 2.0 ** -23 + 2.0 ** -16) * sc * (np.abs(k[seen]) @ np.abs(qn[b, i, hq])).max()
+                        sv = np.abs(v[seen])
+                        small = n * 2.0 ** -31 * sv.max() + 2.0 ** -25
                     x = sc * (k[seen] @ qn[b, i, hq])
                     ew = 2 * ex + 2.0 ** -20 + 2.0 ** -22 * np.abs(x).max()
-                    A = w[seen] @ np.abs(v[seen])
-                    tol = A * (2 * ew + 2.0 ** -10 + n * 2.0 ** -24) + n * 2.0 ** -31 * np.abs(v[seen]).max() + 2.0 ** -25 + 2.0 ** -8 * np.abs(o)
+                    tol = (w[seen] @ sv) * (2 * ew + 2.0 ** -10 + n * 2.0 ** -24) + small + 2.0 ** -8 * np.abs(o)
                     assert (np.abs(got_o[b, i, hq] - o) <= tol).all()
                     assert abs(got_l[b, i, hq] - l) <= ex + ew + 2.0 ** -22 * max(1.0, abs(l))
 
@@ -369,6 +377,32 @@ def test_prefill_sinks_and_window(n_sink, window):
 
 def test_prefill_queries_before_the_first_row():
     check_prefill(Case([[3, 0], [9, 12]], 128), 2, 7, n_new=[7, 0])
+
+
+# Few tokens read the 4-bit rows themselves, with the decode's tolerances: a weight's two roundings are of its products with
+# scale * code and with the minimum, so they count on s c + |m|, which is more than |v| where the two nearly cancel.
+@pytest.mark.parametrize("n_q,group", [(1, 8), (2, 4), (2, 3), (3, 2), (4, 2), (5, 1), (8, 1), (7, 1)])
+@pytest.mark.parametrize("block,n_sink,window", [(0, 0, 0), (64, 0, 0), (16, 3, 20), (32, 40, 64)])
+def test_prefill_of_few_tokens(n_q, group, block, n_sink, window):
+    c = Case([[0, 1, 70], [33, 200, 64], [5, 129, 3]], 64 if n_q % 2 else 128, block=block)
+    check_prefill(c, group, n_q, n_new=[n_q, max(n_q - 1, 1), n_q // 2], n_sink=n_sink, window=window)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_of_few_tokens_over_many_rows(d):
+    check_prefill(Case([[5000, 4990]], d, L=1), 2, 3, layer=0)
+    check_prefill(Case([[5000, 4990]], d, L=1, block=64), 4, 2, layer=0, n_sink=7, window=3000)
+    check_prefill(Case([[3] * 3] * 100, d, L=1, cap=64), 1, 5, layer=0)  # (tokens before the first row)
+
+
+def test_prefill_of_few_tokens_with_faults():
+    c = Case([[400, 390], [60, 50]], 64, block=16)
+    for e in range(2, 10):  # rows 32 .. 159
+        c.kv.block_table[0, e] = -1
+    check_prefill(c, 2, 3, n_sink=5, window=100)
+    c.kv.block_table[0, 20] = 1 << 20
+    check_prefill(c, 2, 3, n_sink=5, window=100, expect=6, left_out=(0,))
+    check_prefill(Case([[40, 39], [60, 50]], 64), 2, 3, n_new=[4, 3], expect=7, left_out=(0,))
 
 
 @pytest.mark.parametrize("what", [-1, 1 << 20])
