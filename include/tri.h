@@ -495,8 +495,8 @@ tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* ls
  * TRI_ERR_UNSUPPORTED otherwise). The rows that some query may see are first
  * written to ws, the values of K as a pair of bf16, those of V in fp16; the kernel
  * then reads those. Weights are rounded to fp16 for their product with V (their sum
- * is not). Calls of few tokens (n_q * group up to 8, as a draft's tokens have) read
- * the 4-bit rows themselves, as tri_attn_decode does. ws: device scratch of
+ * is not). Calls of few tokens (n_q up to 8 times the whole part of 8 / group, a
+ * draft's tokens for instance) read the 4-bit rows themselves, as tri_attn_decode does. ws: device scratch of
  * tri_attn_prefill_q4_workspace_bytes(kv) bytes (one layer's rows, 6 head_dim bytes
  * each, or what those calls need), 16-byte aligned, no initial contents needed;
  * calls that may overlap need one each. A sequence with a fault in n_new is skipped;

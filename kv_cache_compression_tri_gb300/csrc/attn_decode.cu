@@ -52,12 +52,18 @@ namespace {
 struct Run {
   int64_t s;       // slice of the cache
   int n, seq, h;   // valid rows, sequence, KV head
-  int news;        // new tokens
-  Visible vis;     // (of a chunk: to some token of it)
+  int tok0, news;  // a chunk's pass: its tokens; n is then the rows that the last of them sees to,
+  int first;       // and the first one's row (may be negative)
+  Visible vis;     // (of a pass: to some token of it)
   int count;       // visible rows
 };
 
 __device__ __forceinline__ bool slice_run(const AttnParams& p, int ls, Run& r) {
+  int pass = 0;
+  if (p.token_heads) {
+    pass = ls % p.passes;
+    ls /= p.passes;
+  }
   r.seq = ls / p.n_kv_heads;
   r.h = ls - r.seq * p.n_kv_heads;
   r.s = slice_of(p, r.seq, r.h);
@@ -68,11 +74,17 @@ __device__ __forceinline__ bool slice_run(const AttnParams& p, int ls, Run& r) {
     return false;
   }
   if (nn <= 0) return false;
-  r.news = nn;
-  r.vis = visible_rows(r.n - 1, p.n_sink, p.window);
   if (p.token_heads) {
-    r.vis.w0 = visible_rows(max(r.n - nn, 0), p.n_sink, p.window).w0;
+    r.tok0 = pass * p.pass_tokens;
+    r.news = min(p.pass_tokens, nn - r.tok0);
+    if (r.news <= 0) return false;
+    r.first = r.n - nn + r.tok0;
+    r.n = max(r.first + r.news, 0);
+    r.vis = visible_rows(r.n - 1, p.n_sink, p.window);
+    r.vis.w0 = visible_rows(max(r.first, 0), p.n_sink, p.window).w0;
     r.vis.s1 = min(r.vis.s1, r.vis.w0);
+  } else {
+    r.vis = visible_rows(r.n - 1, p.n_sink, p.window);
   }
   r.count = r.vis.s1 + r.n - r.vis.w0;
   return true;
@@ -126,7 +138,7 @@ __device__ __forceinline__ int64_t row_of_column(const AttnParams& p, const Run&
   if (!p.token_heads) return (static_cast<int64_t>(r.seq) * p.n_kv_heads + r.h) * p.group + g;
   const int tok = g / p.token_heads;
   if (tok >= r.news) return -1;
-  return ((static_cast<int64_t>(r.seq) * p.n_q + tok) * p.n_kv_heads + r.h) * p.token_heads + g - tok * p.token_heads;
+  return ((static_cast<int64_t>(r.seq) * p.n_q + r.tok0 + tok) * p.n_kv_heads + r.h) * p.token_heads + g - tok * p.token_heads;
 }
 template <typename T, int D>
 __device__ __forceinline__ void store_out(const AttnParams& p, const Run& r, int g, int e, float o, float l) {
@@ -718,7 +730,7 @@ template <typename T, int D>
 cudaError_t launch_join(const AttnParams& p, int max_rows, cudaStream_t st) {
   const int chunks = p.mass ? max(p.group, (max_rows + JROWS - 1) / JROWS) : p.group;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.n_seq * p.n_kv_heads * chunks));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.n_seq * p.n_kv_heads * max(p.passes, 1) * chunks));
   cfg.blockDim = dim3(JT);
   cfg.stream = st;
   cudaLaunchAttribute at{};
@@ -739,7 +751,7 @@ cudaError_t launch_runs(Kernel kern, size_t smem, const AttnParams& p, cudaStrea
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  const unsigned ctas = static_cast<unsigned>(p.n_seq * p.n_kv_heads * p.n_split);
+  const unsigned ctas = static_cast<unsigned>(p.n_seq * p.n_kv_heads * max(p.passes, 1) * p.n_split);
   if (p.join && p.n_split > 1) {
     if (p.n_split > 8) {
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);

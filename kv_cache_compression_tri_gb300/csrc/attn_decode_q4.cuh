@@ -138,7 +138,7 @@ __device__ __forceinline__ void query_fragments(const __nv_bfloat16* q, bool liv
 }
 
 // BLOCKS: how the cache's rows lie. CHUNK: the columns are the heads of a few tokens, each with its own last row (the
-// newest p.n_q rows are theirs); tiles at the edge of what some token sees are masked column by column.
+// pass's tokens are some of the chunk's); tiles at the edge of what some token sees are masked column by column.
 enum Q4Blocks { SLICES, WHOLE_TILES, SMALL_BLOCKS };  // slices; pools whose blocks hold whole tiles, or not
 template <int D, Q4Blocks BLOCKS, bool CHUNK>
 __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_constant__ AttnParams p) {
@@ -259,9 +259,9 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
   {
     int shift;
     const int tok = CHUNK ? lg / p.token_heads : 0, heads = CHUNK ? p.token_heads : p.group;
-    query_fragments<D>(static_cast<const __nv_bfloat16*>(p.q) + r.seq * p.q_seq + tok * p.q_token +
+    query_fragments<D>(static_cast<const __nv_bfloat16*>(p.q) + r.seq * p.q_seq + (CHUNK ? (r.tok0 + tok) * p.q_token : 0) +
                            (static_cast<int64_t>(r.h) * heads + lg - tok * heads) * D,
-                       lg < p.group && tok < r.news, lt, qf, qsum, shift);
+                       lg < p.group && (!CHUNK || tok < r.news), lt, qf, qsum, shift);
     const int s0 = __shfl_sync(FULL_MASK, shift, 8 * lt), s1 = __shfl_sync(FULL_MASK, shift, 8 * lt + 4);
     const float sl = p.scale * LOG2E;
     // (not 0, which an invisible row's -inf would not survive)
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
         if constexpr (CHUNK) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int j = c < 2 ? ja : jb, last = r.n - r.news + (2 * lt + (c & 1)) / p.token_heads;
+            const int j = c < 2 ? ja : jb, last = r.first + (2 * lt + (c & 1)) / p.token_heads;
             const Visible v = visible_rows(last, p.n_sink, p.window);
             if (!(j < r.n && j <= last && (j < v.s1 || j >= v.w0))) x[s][c] = NEG_INF;
           }
@@ -419,9 +419,9 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
   // rows below all_s1, and from all_w0 up to all_end, are in every column's sight
   int all_end = r.n, all_w0 = r.vis.w0, all_s1 = r.vis.s1;
   if constexpr (CHUNK) {
-    all_end = max(r.n - r.news + 1, 0);
+    all_end = max(r.first + 1, 0);
     all_w0 = visible_rows(r.n - 1, p.n_sink, p.window).w0;
-    all_s1 = visible_rows(max(r.n - r.news, 0), p.n_sink, p.window).s1;
+    all_s1 = visible_rows(max(r.first, 0), p.n_sink, p.window).s1;
   }
   int st = 0;
   for (int u = tl.u0 + w; u < tl.u1; u += NW) {

@@ -650,17 +650,23 @@ int max_visible(const tri_kv* kv, int32_t n_sink, int32_t window) {
 // their (m, l) [slices][splits][group], and for the masses the logits
 // [slices][n_cap][group] f32 (each part 16-byte aligned). The query allows for
 // the most runs any window may lead to.
+size_t decode_parts(const tri_kv* kv, int32_t group, size_t parts) { return align16(parts * group * kv->head_dim * sizeof(float)); }
 struct DecodeWs {
   size_t ml_off, logits_off, total;
 };
 DecodeWs decode_ws(const tri_kv* kv, int32_t group, int32_t n_split, bool with_mass) {
   const size_t n = static_cast<size_t>(kv->n_seq) * kv->n_kv_heads;
   DecodeWs w{};
-  w.ml_off = align16(n * n_split * group * kv->head_dim * sizeof(float));
+  w.ml_off = decode_parts(kv, group, n * n_split);
   w.logits_off = align16(w.ml_off + n * n_split * group * sizeof(float2));
   w.total = w.logits_off + (with_mass ? align16(n * group * kv->n_cap * sizeof(float)) : 0);
   return w;
 }
+
+// A chunk over a 4-bit cache takes the decode kernel for up to so many passes of 8 columns over its rows. Passes against
+// rows written out (us): 16 x 8 x 32768 rows, d 128, group 4: 1 pass 120, 2 214, 4 408, 8 784, written out 1023; 8 x 2113
+// rows: 13, 15, 17, 17 and 20 to 22; 64 x 8 x 2176 rows, d 64, group 1: 34, 53, 95, 175 and 165.
+constexpr int MAX_PASSES = 8;
 
 // Workspace of tri_attn_prefill_q4: one layer's rows, [n_seq][n_kv_heads][n_cap][d] K, what its rounding left, and V
 // (16 bits each), its row counts [n_seq][n_kv_heads] and new tokens [n_seq] (each part 16-byte aligned).
@@ -744,8 +750,13 @@ tri_status tri_attn_prefill(const tri_kv* kv, const tri_queries* q, void* out, f
 
 size_t tri_attn_prefill_q4_workspace_bytes(const tri_kv* kv) {
   if (check_kv(kv, true, true) != TRI_OK || kv->dtype != TRI_Q4) return 0;
-  const int n = kv->n_seq * kv->n_kv_heads;
-  return std::max(q4_ws(kv).total, decode_ws(kv, MAX_GROUP, attn_decode_max_splits(n, kv->n_cap), false).total);
+  size_t most = q4_ws(kv).total;
+  const int64_t n = static_cast<int64_t>(kv->n_seq) * kv->n_kv_heads;
+  for (int64_t k = 1; k <= MAX_PASSES && n * k <= 0x7fffffff; ++k) {
+    const size_t parts = static_cast<size_t>(n * k) * attn_decode_max_splits(static_cast<int>(n * k), kv->n_cap);
+    most = std::max(most, decode_parts(kv, MAX_GROUP, parts) + align16(parts * MAX_GROUP * sizeof(float2)));
+  }
+  return most;
 }
 
 tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out, float* lse, void* ws, size_t ws_bytes,
@@ -757,21 +768,23 @@ tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out
   if (kv->dtype != TRI_Q4) return TRI_ERR_UNSUPPORTED;
   if (!out || !aligned(out, 16) || (lse && !aligned(lse, 4))) return TRI_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 16) || ws_bytes < tri_attn_prefill_q4_workspace_bytes(kv)) return TRI_ERR_INVALID_ARG;
-  const int64_t slices = static_cast<int64_t>(kv->n_seq) * kv->n_kv_heads;
-  if (static_cast<int64_t>(q->n_q) * q->group <= MAX_GROUP && slices * std::max<int64_t>(16, kv->n_cap / 1024 + 1) <= 0x7fffffff) {
-    // as many query rows as the decode kernel has columns: it reads the 4-bit rows once, where they would be
-    // written out and read again (2 tokens of 16 sequences over 8 x 32768 rows, group 4)
+  const int64_t passes = (q->n_q + MAX_GROUP / q->group - 1) / (MAX_GROUP / q->group);
+  const int64_t slices = static_cast<int64_t>(kv->n_seq) * kv->n_kv_heads * passes;
+  if (passes <= MAX_PASSES && slices * std::max<int64_t>(16, kv->n_cap / 1024 + 1) <= 0x7fffffff) {
+    // so few query rows that the decode kernel, which has 8 columns for them, reads the 4-bit rows in less time
+    // than writing them out and reading that takes
     const int n = static_cast<int>(slices);
     const int64_t seen = static_cast<int64_t>(q->n_sink) + q->window + q->n_q - 1;
     const int rows = q->window == 0 ? kv->n_cap : static_cast<int>(std::min<int64_t>(kv->n_cap, seen));
     const DecodePlan plan = attn_decode_plan(n, rows, kv->dtype);
     p.token_heads = q->group;
-    p.group = q->n_q * q->group;
+    p.pass_tokens = std::min(q->n_q, MAX_GROUP / q->group);
+    p.passes = static_cast<int32_t>(passes);
+    p.group = p.pass_tokens * q->group;
     p.n_split = plan.n_split;
     p.join = plan.join;
-    const DecodeWs d = decode_ws(kv, p.group, p.n_split, false);
     p.part_o = static_cast<float*>(ws);
-    p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + d.ml_off);
+    p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + decode_parts(kv, p.group, slices * p.n_split));
     p.out = out;
     p.lse = lse;
     return launch_attn_decode(p, rows, kv->dtype, kv->head_dim, stream) == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;

@@ -348,7 +348,9 @@ struct AttnParams {
   int64_t q_seq, q_token;          // elements between sequences and tokens
   const int32_t* n_new;            // [n_seq], or NULL: n_q
   int32_t n_q, group;
-  int32_t token_heads;             // decode kernels: 0, or `group` columns are n_q tokens of so many heads each
+  // decode kernels, a chunk of few tokens: the heads of a token (0: no chunk), the tokens of a pass (group = both), and
+  // how many passes there are, each like a slice of its own
+  int32_t token_heads, pass_tokens, passes;
   int32_t n_sink, window;
   float scale;                     // of q . k
   const void* k_rest;              // 4-bit rows written out: K is a bf16 pair, v is fp16 (attn_prefill.cu)

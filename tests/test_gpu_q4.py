@@ -189,11 +189,13 @@ def test_offsets_past_32_bits():
     outs = []
     for kv in (small.kv, tri.PagedKVCache(k, v, table, small.kv.n_valid, None, None, small.status, post_rope=True)):
         out, rows = torch.zeros_like(q), torch.zeros(1, 4, small.cap, 128, dtype=torch.bfloat16, device="cuda")
-        chunk, x = torch.zeros(1, 2, 16, 128, dtype=torch.bfloat16, device="cuda"), q.view(1, 1, 16, 128).expand(1, 2, 16, 128).contiguous()
+        chunks = []
         tri.attn_decode(kv, 0, q, out)
         tri.read_rows(kv, 0, rows, None)
-        tri.attn_prefill(kv, 0, x, chunk)
-        outs.append((out, rows, chunk))
+        for n in (2, 20):  # read, and written out
+            chunks.append(torch.zeros(1, n, 16, 128, dtype=torch.bfloat16, device="cuda"))
+            tri.attn_prefill(kv, 0, q.view(1, 1, 16, 128).expand(1, n, 16, 128).contiguous(), chunks[-1])
+        outs.append((out, rows, *chunks))
     small.ok()
     assert all(torch.equal(a, b) for a, b in zip(*outs))
 
@@ -249,9 +251,11 @@ def test_bad_row_counts():
     tri.attn_decode(c.kv, 0, q, out)
     assert int(c.status) == 1 and bool((out[1, :2] == 9).all()) and bool((out[1, 2:] != 9).any()) and bool((out[0] != 9).any())
     c.status.zero_()
-    chunk, x = torch.full((2, 3, 4, 64), 9.0, dtype=torch.bfloat16, device="cuda"), torch.randn(2, 3, 4, 64, device="cuda").bfloat16()
-    tri.attn_prefill(c.kv, 0, x, chunk)
-    assert int(c.status) == 1 and bool((chunk[1, :, :2] == 9).all()) and bool((chunk[0] != 9).any())
+    for n in (3, 41):
+        chunk, x = torch.full((2, n, 4, 64), 9.0, dtype=torch.bfloat16, device="cuda"), torch.randn(2, n, 4, 64, device="cuda").bfloat16()
+        tri.attn_prefill(c.kv, 0, x, chunk)
+        assert int(c.status) == 1 and bool((chunk[1, :, :2] == 9).all()) and bool((chunk[0] != 9).any())
+        c.status.zero_()
 
 
 def test_decode_repeats_bit_for_bit():
@@ -341,7 +345,7 @@ def check_prefill(c, G, n_q, layer=1, n_new=None, n_sink=0, window=0, seed=1, ex
             kb, vb = c.slice_rows(b, layer, h)
             k, v = values(kb), values(vb)
             n = len(k)
-            few = n_q * G <= 8
+            few = -(-n_q // (8 // G)) <= 8  # passes of the decode kernel
             for i in range(new):
                 for hq in range(h * G, (h + 1) * G):
                     o, l, w = attend(qn[b, i, hq], k, v, n - new + i, sc, n_sink, window) if n else (np.zeros(d), -np.inf, np.zeros(0))
@@ -367,21 +371,22 @@ def check_prefill(c, G, n_q, layer=1, n_new=None, n_sink=0, window=0, seed=1, ex
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("block", [0, 16, 64])
 def test_prefill_ragged(d, block):
-    check_prefill(Case([[40, 1, 131], [64, 33, 200]], d, block=block), 3, 33, n_new=[33, 20])
+    check_prefill(Case([[40, 1, 131], [64, 33, 200]], d, block=block), 3, 33, n_new=[33, 20])  # 17 passes: written out
 
 
 @pytest.mark.parametrize("n_sink,window", [(0, 1), (4, 30), (40, 100), (130, 64), (3, 4000)])
 def test_prefill_sinks_and_window(n_sink, window):
-    check_prefill(Case([[450, 301]], 64, block=16), 2, 40, n_sink=n_sink, window=window)
+    check_prefill(Case([[450, 301]], 64, block=16), 2, 40, n_sink=n_sink, window=window)  # 10
 
 
 def test_prefill_queries_before_the_first_row():
     check_prefill(Case([[3, 0], [9, 12]], 128), 2, 7, n_new=[7, 0])
+    check_prefill(Case([[3, 0], [9, 12]], 128), 2, 37, n_new=[37, 0])
 
 
 # Few tokens read the 4-bit rows themselves, with the decode's tolerances: a weight's two roundings are of its products with
 # scale * code and with the minimum, so they count on s c + |m|, which is more than |v| where the two nearly cancel.
-@pytest.mark.parametrize("n_q,group", [(1, 8), (2, 4), (2, 3), (3, 2), (4, 2), (5, 1), (8, 1), (7, 1)])
+@pytest.mark.parametrize("n_q,group", [(1, 8), (2, 4), (2, 3), (3, 2), (5, 1), (8, 1), (3, 4), (5, 3), (16, 4), (8, 5), (33, 1), (64, 1)])
 @pytest.mark.parametrize("block,n_sink,window", [(0, 0, 0), (64, 0, 0), (16, 3, 20), (32, 40, 64)])
 def test_prefill_of_few_tokens(n_q, group, block, n_sink, window):
     c = Case([[0, 1, 70], [33, 200, 64], [5, 129, 3]], 64 if n_q % 2 else 128, block=block)
@@ -393,6 +398,8 @@ def test_prefill_of_few_tokens_over_many_rows(d):
     check_prefill(Case([[5000, 4990]], d, L=1), 2, 3, layer=0)
     check_prefill(Case([[5000, 4990]], d, L=1, block=64), 4, 2, layer=0, n_sink=7, window=3000)
     check_prefill(Case([[3] * 3] * 100, d, L=1, cap=64), 1, 5, layer=0)  # (tokens before the first row)
+    check_prefill(Case([[5000, 4990]], d, L=1, block=64), 4, 7, layer=0, n_sink=7, window=3000)
+    check_prefill(Case([[3, 20] * 2] * 9, d, L=1, cap=64), 8, 6, layer=0, n_new=[6, 0, 1, 2, 3, 4, 5, 6, 6])
 
 
 def test_prefill_of_few_tokens_with_faults():
@@ -405,25 +412,28 @@ def test_prefill_of_few_tokens_with_faults():
     check_prefill(Case([[40, 39], [60, 50]], 64), 2, 3, n_new=[4, 3], expect=7, left_out=(0,))
 
 
+@pytest.mark.parametrize("n_q", [20, 41])  # read, and written out
 @pytest.mark.parametrize("what", [-1, 1 << 20])
-def test_prefill_blocks_out_of_sight_and_bad_ones(what):
+def test_prefill_blocks_out_of_sight_and_bad_ones(what, n_q):
     c = Case([[400, 390], [60, 50]], 64, block=16)
     for e in range(2, 10):  # rows 32 .. 159
         c.kv.block_table[0, e] = what
-    check_prefill(c, 2, 20, n_sink=5, window=100)  # (the first rows that a window sees: 271 and on)
+    check_prefill(c, 2, n_q, n_sink=5, window=100)  # (the first rows that a window sees: 250 and on)
     c.kv.block_table[0, 20] = what
-    check_prefill(c, 2, 20, n_sink=5, window=100, expect=6, left_out=(0,))
+    check_prefill(c, 2, n_q, n_sink=5, window=100, expect=6, left_out=(0,))
 
 
-def test_prefill_bad_counts():
+@pytest.mark.parametrize("n_q", [20, 41])
+def test_prefill_bad_counts(n_q):
     c = Case([[40, 39], [60, 50]], 64)
-    check_prefill(c, 2, 20, n_new=[21, 20], expect=7, left_out=(0,))
+    check_prefill(c, 2, n_q, n_new=[n_q + 1, n_q], expect=7, left_out=(0,))
 
 
-def test_captured_attention_follows_the_cache():
+@pytest.mark.parametrize("n_q", [5, 41])
+def test_captured_attention_follows_the_cache(n_q):
     c = Case([[100, 90]], 128, block=16)
-    q = torch.randn(1, 5, 4, 128, device="cuda").bfloat16()
-    out, lse = torch.zeros_like(q), torch.zeros(1, 5, 4, device="cuda")
+    q = torch.randn(1, n_q, 4, 128, device="cuda").bfloat16()
+    out, lse = torch.zeros_like(q), torch.zeros(1, n_q, 4, device="cuda")
     dout = torch.zeros(1, 4, 128, dtype=torch.bfloat16, device="cuda")
     ws = torch.empty(tri.attn_prefill_workspace_bytes(c.kv), dtype=torch.uint8, device="cuda")
     dws = torch.empty(tri.attn_decode_workspace_bytes(c.kv, 2), dtype=torch.uint8, device="cuda")

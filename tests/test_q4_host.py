@@ -110,7 +110,7 @@ def test_attention_over_4_bits_rejects_bad_buffers(lib):  # noqa: F811
         assert lib.tri_attn_prefill_q4_workspace_bytes(ctypes.byref(other)) == 0
         assert lib.tri_attn_prefill_q4(ctypes.byref(other), ctypes.byref(_q()), 0x30000, None, 0x40000, 1 << 40, None) == UNSUPPORTED
     far = _kv(**dict(Q4_PAGED, n_cap=1 << 30, num_blocks=64))  # more rows than a chunk's copies number
-    q = _q(n_q=9)
+    q = _q(n_q=100, token_stride=4 * 64)
     assert lib.tri_attn_prefill_q4(ctypes.byref(far), ctypes.byref(q), 0x30000, None, 0x40000, 1 << 60, None) == UNSUPPORTED
 
 
