@@ -424,7 +424,8 @@ tri_status tri_select_union(const float* scores, const tri_kv* kv, int32_t n_pro
  * a query that sees nothing (an empty slice, r < 0) gets out = 0, lse = -inf.
  * Query head h * group + g reads KV head h. Rows a query does not see may hold
  * anything, NaN and infinities included, except that V rows below n_valid
- * must be finite for tri_attn_prefill (a weight of 0 multiplies them there).
+ * must be finite for tri_attn_prefill (a weight of 0 multiplies them there), and
+ * those that some query of the chunk sees for tri_attn_prefill_q4.
  * A pool's blocks that no query of a sequence sees may be gone: their table
  * entries may be anything, and no row of such a block is read into a result.
  * An infinite V element of a row that a query sees gives infinity or NaN.
@@ -495,14 +496,15 @@ tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* ls
  * TRI_ERR_UNSUPPORTED otherwise). The rows that some query may see are first
  * written to ws, the values of K as a pair of bf16, those of V in fp16; the kernel
  * then reads those. Weights are rounded to fp16 for their product with V (their sum
- * is not). Calls of few tokens (n_q up to 8 times the whole part of 8 / group, a
- * draft's tokens for instance) read the 4-bit rows themselves, as tri_attn_decode does. ws: device scratch of
+ * is not). Calls of few tokens (n_q up to 8 t, t the whole part of 8 / group: a
+ * draft's tokens for instance) read the 4-bit rows themselves, as tri_attn_decode
+ * does, t tokens at a time. ws: device scratch of
  * tri_attn_prefill_q4_workspace_bytes(kv) bytes (one layer's rows, 6 head_dim bytes
  * each, or what those calls need), 16-byte aligned, no initial contents needed;
  * calls that may overlap need one each. A sequence with a fault in n_new is skipped;
  * one with a bad table entry of a block that one of its queries sees is skipped as
- * a whole, in calls of few tokens in the heads that see it; a bad row count leaves
- * out its slice. */
+ * a whole, in calls of few tokens each head's t tokens (from token 0 on) of which one
+ * sees it; a bad row count leaves out its slice. */
 size_t tri_attn_prefill_q4_workspace_bytes(const tri_kv* kv);
 tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out, float* lse, void* ws, size_t ws_bytes,
                                tri_stream_t stream);

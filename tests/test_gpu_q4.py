@@ -423,6 +423,22 @@ def test_prefill_blocks_out_of_sight_and_bad_ones(what, n_q):
     check_prefill(c, 2, n_q, n_sink=5, window=100, expect=6, left_out=(0,))
 
 
+def test_prefill_of_few_tokens_leaves_out_those_that_need_a_bad_block():
+    outs = []
+    for bad in (False, True):
+        c = Case([[400, 399, 350]], 64, block=16)
+        q = torch.randn(1, 20, 6, 64, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").bfloat16()
+        out, lse = torch.full_like(q, 9.0), torch.full((1, 20, 6), 9.0, device="cuda")
+        if bad:
+            c.kv.block_table[0, 17] = -1  # rows 272 .. 287: seen from rows up to 386
+        tri.attn_prefill(c.kv, 0, q, out, n_sink=5, window=100, lse=lse)
+        outs += [out[0].view(20, 3, 2, 64), lse[0].view(20, 3, 2)]
+    assert int(c.status) == 6
+    for want, got in zip(outs[:2], outs[2:]):
+        assert bool((got[:8, 0] == 9).all()) and bool((got[:8, 1] == 9).all())  # tokens 0 .. 6 and 0 .. 7, by fours
+        assert torch.equal(got[8:, :2], want[8:, :2]) and bool((got[:, 2] == 9).all())
+
+
 @pytest.mark.parametrize("n_q", [20, 41])
 def test_prefill_bad_counts(n_q):
     c = Case([[40, 39], [60, 50]], 64)
