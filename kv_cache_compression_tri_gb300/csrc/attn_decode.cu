@@ -58,9 +58,11 @@ struct Run {
   int count;       // visible rows
 };
 
+// CHUNK (4-bit rows): the slice numbers count a chunk's passes.
+template <bool CHUNK = false>
 __device__ __forceinline__ bool slice_run(const AttnParams& p, int ls, Run& r) {
   int pass = 0;
-  if (p.token_heads) {
+  if constexpr (CHUNK) {
     pass = ls % p.passes;
     ls /= p.passes;
   }
@@ -74,7 +76,7 @@ __device__ __forceinline__ bool slice_run(const AttnParams& p, int ls, Run& r) {
     return false;
   }
   if (nn <= 0) return false;
-  if (p.token_heads) {
+  if constexpr (CHUNK) {
     r.tok0 = pass * p.pass_tokens;
     r.news = min(p.pass_tokens, nn - r.tok0);
     if (r.news <= 0) return false;
@@ -132,22 +134,24 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// The result of a head's element, or of its log-sum, from the sums of all its rows.
 // The row of out and lse that column g of a slice has, or -1 (a token that is not there).
+template <bool CHUNK>
 __device__ __forceinline__ int64_t row_of_column(const AttnParams& p, const Run& r, int g) {
-  if (!p.token_heads) return (static_cast<int64_t>(r.seq) * p.n_kv_heads + r.h) * p.group + g;
+  if (!CHUNK) return (static_cast<int64_t>(r.seq) * p.n_kv_heads + r.h) * p.group + g;
   const int tok = g / p.token_heads;
   if (tok >= r.news) return -1;
   return ((static_cast<int64_t>(r.seq) * p.n_q + r.tok0 + tok) * p.n_kv_heads + r.h) * p.token_heads + g - tok * p.token_heads;
 }
-template <typename T, int D>
+// The result of a head's element, or of its log-sum, from the sums of all its rows.
+template <typename T, int D, bool CHUNK>
 __device__ __forceinline__ void store_out(const AttnParams& p, const Run& r, int g, int e, float o, float l) {
-  const int64_t row = row_of_column(p, r, g);
-  if (row >= 0) static_cast<T*>(p.out)[row * D + e] = from_f32<T>(l != 0.f ? o / l : 0.f);
+  const int64_t row = row_of_column<CHUNK>(p, r, g);
+  if (!CHUNK || row >= 0) static_cast<T*>(p.out)[row * D + e] = from_f32<T>(l != 0.f ? o / l : 0.f);
 }
+template <bool CHUNK>
 __device__ __forceinline__ void store_lse(const AttnParams& p, const Run& r, int g, float m, float l) {
-  const int64_t row = row_of_column(p, r, g);
-  if (p.lse && row >= 0) p.lse[row] = l != 0.f ? LN2 * (m + log2f(l)) : NEG_INF;
+  const int64_t row = row_of_column<CHUNK>(p, r, g);
+  if (p.lse && (!CHUNK || row >= 0)) p.lse[row] = l != 0.f ? LN2 * (m + log2f(l)) : NEG_INF;
 }
 
 // mass[j] += sum over the heads of 2^(x_j - m) / l for rows j = row_at(i), i in
@@ -192,7 +196,7 @@ __device__ __forceinline__ void add_masses(const AttnParams& p, const Run& r, in
 // ml [group] are each run's sums in its shared memory. This CTA's share of the
 // heads' elements is written, and the masses of its own rows: row_at(i), i in
 // [i0, i1), or -1.
-template <typename T, int D, class RowAt>
+template <typename T, int D, bool CHUNK, class RowAt>
 __device__ __forceinline__ void join_cluster(const AttnParams& p, const Run& r, int ls, int split, const float* tot,
                                              const float2* ml, int i0, int i1, RowAt row_at) {
   __shared__ float s_m[MAX_GROUP], s_l[MAX_GROUP], s_a[MAX_CLUSTER][MAX_GROUP];
@@ -225,8 +229,8 @@ __device__ __forceinline__ void join_cluster(const AttnParams& p, const Run& r, 
       const int g = i / D, e = i % D;
       float o = 0.f;
       for (int u = 0; u < ns; ++u) o = fmaf(cluster_ld(tot + i, u, ns), s_a[u][g], o);
-      store_out<T, D>(p, r, g, e, o, s_l[g]);
-      if (e == 0) store_lse(p, r, g, s_m[g], s_l[g]);
+      store_out<T, D, CHUNK>(p, r, g, e, o, s_l[g]);
+      if (e == 0) store_lse<CHUNK>(p, r, g, s_m[g], s_l[g]);
     }
     if (p.mass) {
       add_masses(p, r, ls, s_m, s_l, i0, i1, row_at);
@@ -301,7 +305,7 @@ struct RunSums {
 };
 // The end of a run: its sums over the warps (so; m and l in sm_m, sm_l), then joined in the cluster or
 // left for the join. bad: a block (or copy) that a visible row needs is missing.
-template <class Tag, int D>
+template <class Tag, int D, bool CHUNK>
 __device__ __forceinline__ void finish_run(const AttnParams& p, const Run& r, const Tiles<Tag, D>& tl, int ls, int split, int64_t pi, bool bad,
                                            float* so, const float (&sm_m)[NW][8], const float (&sm_l)[NW][8], float2* run_ml) {
   constexpr int HS = RunSums<D>::HS;
@@ -333,7 +337,7 @@ __device__ __forceinline__ void finish_run(const AttnParams& p, const Run& r, co
   }
   constexpr int TK = TileGeo<Tag, D>::TK;
   if (p.join)
-    join_cluster<__nv_bfloat16, D>(p, r, ls, split, tot, run_ml, tl.u0 * TK, tl.u1 * TK, [&](int i) {
+    join_cluster<__nv_bfloat16, D, CHUNK>(p, r, ls, split, tot, run_ml, tl.u0 * TK, tl.u1 * TK, [&](int i) {
       const int j = tl.row(i / TK) + i % TK;
       return j < r.n && (j < r.vis.s1 || j >= r.vis.w0) ? j : -1;
     });
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(NW * 32) decode_tiles_kernel(const __grid_cons
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
     for (int c = 0; c < 4; ++c) so[(w * 8 + 2 * lt + (c & 1)) * RunSums<D>::HS + 16 * i + lg + (c >> 1) * 8] = o[i][c];
-  finish_run<T, D>(p, r, tl, ls, split, pi, PAGED && bad, so, sm_m, sm_l, run_ml);
+  finish_run<T, D, false>(p, r, tl, ls, split, pi, PAGED && bad, so, sm_m, sm_l, run_ml);
 }
 
 }  // namespace
@@ -660,7 +664,7 @@ __global__ void __launch_bounds__(DT) decode_rows_kernel(const __grid_constant__
     }
   }
   if (p.join)
-    join_cluster<float, D>(p, r, ls, split, tot, run_ml, tl.u0 * Geo::TK, tl.u1 * Geo::TK, [&](int i) {
+    join_cluster<float, D, false>(p, r, ls, split, tot, run_ml, tl.u0 * Geo::TK, tl.u1 * Geo::TK, [&](int i) {
       const int j = tl.row(i / Geo::TK) + i % Geo::TK;
       return j < r.n && (j < r.vis.s1 || j >= r.vis.w0) ? j : -1;
     });
@@ -675,7 +679,7 @@ constexpr int JT = NW * 32;
 constexpr int JROWS = 1024;
 constexpr int MAX_SPLIT = 128;
 
-template <typename T, int D>
+template <typename T, int D, bool CHUNK>
 __global__ void __launch_bounds__(JT) decode_join_kernel(const __grid_constant__ AttnParams p, int chunks) {
   __shared__ float s_m[MAX_GROUP], s_l[MAX_GROUP];
   __shared__ int skip;
@@ -683,7 +687,7 @@ __global__ void __launch_bounds__(JT) decode_join_kernel(const __grid_constant__
   if (t == 0) skip = 0;
   pdl_wait();
   Run r;
-  if (!slice_run(p, ls, r)) return;
+  if (!slice_run<CHUNK>(p, ls, r)) return;
   __syncthreads();
   // (m, l) of the heads: a warp per head, lanes over the runs
   const float2* ml = p.part_ml + static_cast<int64_t>(ls) * p.n_split * G;
@@ -717,16 +721,16 @@ __global__ void __launch_bounds__(JT) decode_join_kernel(const __grid_constant__
       float o = 0.f;
 #pragma unroll 4
       for (int i = 0; i < p.n_split; ++i) o = fmaf(po[static_cast<int64_t>(i) * G * D + e], fast_exp2(ml[i * G + c].x - s_m[c]), o);
-      store_out<T, D>(p, r, c, e, o, s_l[c]);
+      store_out<T, D, CHUNK>(p, r, c, e, o, s_l[c]);
     }
-    if (t == 0) store_lse(p, r, c, s_m[c], s_l[c]);
+    if (t == 0) store_lse<CHUNK>(p, r, c, s_m[c], s_l[c]);
   }
   if (!p.mass) return;
   add_masses(p, r, ls, s_m, s_l, c * JROWS, min(r.count, (c + 1) * JROWS),
              [&](int i) { return i < r.vis.s1 ? i : i - r.vis.s1 + r.vis.w0; });
 }
 
-template <typename T, int D>
+template <typename T, int D, bool CHUNK = false>
 cudaError_t launch_join(const AttnParams& p, int max_rows, cudaStream_t st) {
   const int chunks = p.mass ? max(p.group, (max_rows + JROWS - 1) / JROWS) : p.group;
   cudaLaunchConfig_t cfg{};
@@ -738,7 +742,7 @@ cudaError_t launch_join(const AttnParams& p, int max_rows, cudaStream_t st) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D>, p, chunks);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D, CHUNK>, p, chunks);
   if (e == cudaSuccess) note_launch();
   return e;
 }
@@ -795,7 +799,8 @@ cudaError_t launch_q4(const AttnParams& p, int max_rows, cudaStream_t st) {
                                : whole       ? decode_q4_kernel<D, WHOLE_TILES, false>
                                              : decode_q4_kernel<D, SMALL_BLOCKS, false>);
   const cudaError_t e = launch_runs(kern, G::SMEM, p, st);
-  return e != cudaSuccess || p.join ? e : launch_join<__nv_bfloat16, D>(p, max_rows, st);
+  if (e != cudaSuccess || p.join) return e;
+  return p.token_heads ? launch_join<__nv_bfloat16, D, true>(p, max_rows, st) : launch_join<__nv_bfloat16, D>(p, max_rows, st);
 }
 
 template <int D, int GP>

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
   const int64_t pi = static_cast<int64_t>(blockIdx.x) * p.group;
   pdl_launch();
   Run r;
-  if (!slice_run(p, ls, r)) {
+  if (!slice_run<CHUNK>(p, ls, r)) {
     if (!p.join && t < p.group) p.part_ml[pi + t] = make_float2(NEG_INF, -1.f);
     return;  // (every run of the slice does)
   }
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
         so[(w * 8 + 2 * lt + (c & 1)) * RunSums<D>::HS + e + (c >> 1)] = fmaf(y[c], c < 2 ? 0x1p24f : 0x1p20f, (c & 1) ? a1 : a0);
     }
   }
-  finish_run<Q4Tag, D>(p, r, tl, ls, split, pi, bad, so, sm_m, sm_l, run_ml);
+  finish_run<Q4Tag, D, CHUNK>(p, r, tl, ls, split, pi, bad, so, sm_m, sm_l, run_ml);
 }
 
 }  // namespace

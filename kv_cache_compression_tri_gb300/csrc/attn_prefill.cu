@@ -41,6 +41,8 @@
 // fp32 rows (prefill_kernel): CUDA cores, 64 x 64 tiles in shared memory.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "attn_tc.cuh"
 #include "attn_tile.cuh"
 
@@ -129,6 +131,10 @@ __device__ __forceinline__ float weights_of(const uint32_t (&x)[32], float sl, f
   return (l0 + l1) + (l2 + l3);
 }
 
+struct NoMaps {};
+template <bool Q4>
+using RestMaps = std::conditional_t<Q4, RowMaps<false>, NoMaps>;
+
 // Q4: the rows of a 4-bit cache, written out before. K as a bf16 pair (kmap; lmap: what the first rounding left),
 // two products: 16 bits of its values. V and the weights in fp16, the latter up to 2^14 (no further pair): 2^-11 of
 // a weight, and 2^-25 of the smallest that counts. A tile of rows then is three tiles of shared memory, and a ring
@@ -137,13 +143,13 @@ __device__ __forceinline__ float weights_of(const uint32_t (&x)[32], float sl, f
 template <int D, int NQ, bool FEW_CTAS, bool ODD, bool Q4>
 __global__ void __launch_bounds__((TcSmem<D, NQ, Q4>::THREADS), 3 - NQ)
     prefill_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ RowMaps<ODD> kmap,
-                      const __grid_constant__ RowMaps<ODD> vmap, const __grid_constant__ RowMaps<Q4 ? ODD : false> lmap,
+                      const __grid_constant__ RowMaps<ODD> vmap, const __grid_constant__ RestMaps<Q4> lmap,
                       const __grid_constant__ RowNumbers rn, int n_tiles, int cluster) {
   using L = TcSmem<D, NQ, Q4>;
   constexpr bool PAIR = FEW_CTAS && !Q4;        // the weights as a pair
   constexpr float LIFT = Q4 ? 6.f : 0.f;        // log2 of the weight of a row's running maximum
   const int splits = FEW_CTAS ? cluster : 1;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // (for what writes a 4-bit cache's rows out; nothing otherwise)
+  if constexpr (Q4) asm volatile("griddepcontrol.wait;" ::: "memory");  // (for what writes the rows out)
   extern __shared__ __align__(1024) unsigned char smem[];  // (the swizzle goes by address)
   TcCtl& ctl = *reinterpret_cast<TcCtl*>(smem + L::CTRL);
   // (values that the MMA warps use come through a shuffle, so that the compiler
@@ -643,10 +649,11 @@ __global__ void __launch_bounds__((TcSmem<D, NQ, Q4>::THREADS), 3 - NQ)
 template <int D, bool ODD, bool Q4 = false>
 cudaError_t launch_tc(const AttnParams& p, const RowNumbers& rn, cudaStream_t st) {
   RowMaps<ODD> kmap, vmap;
-  RowMaps<Q4 ? ODD : false> lmap{};
+  RestMaps<Q4> lmap{};
   const Encode encode = tensor_map_encode();
   if (!encode || !encode_rows(kmap, p.k, p, D, rn, encode) || !encode_rows(vmap, p.v, p, D, rn, encode)) return cudaErrorInvalidValue;
-  if (Q4 && !encode_rows(lmap, p.k_rest, p, D, rn, encode)) return cudaErrorInvalidValue;
+  if constexpr (Q4)
+    if (!encode_rows(lmap, p.k_rest, p, D, rn, encode)) return cudaErrorInvalidValue;
   // one or two query tiles per CTA: at d 64 two CTAs with a tile each fit an SM, and one's
   // start and end hide behind the other's work (8 padded prompts of up to 4096 tokens, sinks
   // and a window of 1000: 189 us, with two tiles per CTA 199)
