@@ -349,8 +349,9 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
       mx0 = fmaxf(fmaxf(mx0, x[s][0]), x[s][2]);
       mx1 = fmaxf(fmaxf(mx1, x[s][1]), x[s][3]);
     }
-    mx0 = fmaf(mx0, f0, -LIFT);
-    mx1 = fmaf(mx1, f1, -LIFT);
+    // (rounded up: to the nearest, logits of 2^17 give weights of 2^(LIFT + 1/64), which times the largest scale is past fp16)
+    mx0 = __fmaf_ru(mx0, f0, -LIFT);
+    mx1 = __fmaf_ru(mx1, f1, -LIFT);
     if (__any_sync(FULL_MASK, mx0 > m0 || mx1 > m1)) {
 #pragma unroll
       for (int k = 4; k <= 16; k <<= 1) {
