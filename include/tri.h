@@ -464,7 +464,9 @@ typedef struct {
  * tri_attn_decode_workspace_bytes(kv, group, mass != NULL) bytes, 16-byte
  * aligned, no initial contents needed; calls that may overlap need one each.
  * 4-bit caches: products of the codes are exact; weights are rounded to fp16, and
- * again with V's scales, for their product with V.
+ * again with V's scales, for their product with V: each time by 2^-11 of themselves,
+ * or 2^-36 of the query's largest weight (times the largest value of V) where that is
+ * more. Elements of q stay below 2^115 in magnitude.
  * A slice with a fault (row count, block table, n_new) is skipped. */
 size_t tri_attn_decode_workspace_bytes(const tri_kv* kv, int32_t group, int32_t with_mass);
 tri_status tri_attn_decode(const tri_kv* kv, const tri_queries* q, void* out, float* lse, float* mass, void* ws,
@@ -496,7 +498,7 @@ tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* ls
  * TRI_ERR_UNSUPPORTED otherwise). The rows that some query may see are first
  * written to ws, the values of K as a pair of bf16, those of V in fp16; the kernel
  * then reads those. Weights are rounded to fp16 for their product with V (their sum
- * is not). Calls of few tokens (n_q up to 8 t, t the whole part of 8 / group: a
+ * is not): by 2^-11 of themselves, or 2^-31 of the query's largest where that is more. Calls of few tokens (n_q up to 8 t, t the whole part of 8 / group: a
  * draft's tokens for instance) read the 4-bit rows themselves, as tri_attn_decode
  * does, t tokens at a time. ws: device scratch of
  * tri_attn_prefill_q4_workspace_bytes(kv) bytes (one layer's rows, 6 head_dim bytes

@@ -21,8 +21,15 @@
 //   q as fp16 pairs.
 //   O^T += V^T P^T: A = V transposed, 16 elements of a quarter x 16 rows. Two rows' codes of
 //   an element come together by a byte permute of their words, before they are
-//   spread. B = p s_j in fp16, p up to 2^4 (a scale is below 2^12): two
-//   roundings of 2^-11 of its weight, where results are rounded to 2^-8.
+//   spread. B = p (2^k s_j) in fp16: two roundings of 2^-11 of its weight, where results are
+//   rounded to 2^-8. p is up to 2^11 and 2^k s_j up to 2^5, k from the warp's largest scale so far (a
+//   larger one lowers it, and the sums so far with it), so that what falls to fp16's subnormal numbers
+//   and below is 2^-35 of the largest weight times the largest value. (With k 0 and p up to
+//   2^4, a row 14 above the others in the logit left these without their codes where V's
+//   elements were about 2^-10.) For this a lane per row reads the row's pairs in shared memory and puts
+//   them back as the products take them: two rows' scales, times 2^k, then two rows' minima. The
+//   quarter of the loads that this saves pays for it (16 x 8 x 32768 rows 119.8 us, without k 119.7, with the
+//   pairs left in their order 123.8).
 // Each warp owns a ring of NST tiles of 32 (d 64: 64) rows, K and V, filled by 16-byte asynchronous copies
 // of whole contiguous tiles (bulk copies by lanes of a warp took 20 instructions more per 16 rows
 // than these); table entries are read a tile ahead. Rows out of sight are copied but not
@@ -66,6 +73,11 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));  // (the number, where one is a NaN)
+  return r;
+}
 __device__ __forceinline__ float scale_of(uint32_t pair) { return __low2float(*reinterpret_cast<const __half2*>(&pair)); }
 // A lane's words of a row of codes.
 template <int N>
@@ -79,6 +91,10 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t x;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
   return x;
+}
+
+__device__ __forceinline__ void sts4(uint32_t a, const uint32_t (&w)[4]) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
 
 // A head's query as B fragments for the codes (see the file comment), by the four
@@ -145,7 +161,7 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
   using G = TileGeo<Q4Tag, D>;
   constexpr bool PAGED = BLOCKS != SLICES, whole = BLOCKS != SMALL_BLOCKS;
   constexpr int NWD = Q4Row<D>::WORDS, CODES = Q4Row<D>::CODES, LANE = 4 * NWD;  // bytes of a lane's codes
-  constexpr float LIFT = 4.f;  // log2 of the largest weight
+  constexpr float LIFT = 11.f;  // log2 of the largest weight
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float sm_m[NW][8], sm_l[NW][8];
   __shared__ float2 run_ml[MAX_GROUP];
@@ -276,6 +292,8 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
     for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
   // heads 2 lt, 2 lt + 1: weights are 2^(x - m), m at least the largest x minus LIFT
   float m0 = NEG_INF, m1 = NEG_INF, l0 = 0.f, l1 = 0.f;
+  // V's scales, and so o, are times 2^k, k <= 15 so that 2^k is an fp16 number: 2^(5 - k), which scales stay below, as fp16
+  uint32_t lim = (20 - 15) << 10;
   float* logits = p.logits ? p.logits + static_cast<int64_t>(ls) * p.n_cap * p.group : nullptr;
   const uint32_t half_sel = lg >= 4 ? 0x7632 : 0x5410;
   // A tile's rows r0 .. from `tk`; all: every one of them is in sight.
@@ -343,6 +361,10 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
         }
       }
     }
+    // V's pairs, a lane per row: zeros for rows out of sight (any bits), the scales of others times 2^k
+    uint32_t pv[G::TK / 32][4], most = 0;
+#pragma unroll
+    for (int i = 0; i < G::TK / 32; ++i) lds_words(tv + (lane + 32 * i) * G::ROW + CODES, pv[i]);
     float mx0 = fmaxf(x[0][0], x[0][2]), mx1 = fmaxf(x[0][1], x[0][3]);
 #pragma unroll
     for (int s = 1; s < SUB; ++s) {
@@ -352,18 +374,32 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
     // (rounded up: to the nearest, logits of 2^17 give weights of 2^(LIFT + 1/64), which times the largest scale is past fp16)
     mx0 = __fmaf_ru(mx0, f0, -LIFT);
     mx1 = __fmaf_ru(mx1, f1, -LIFT);
-    if (__any_sync(FULL_MASK, mx0 > m0 || mx1 > m1)) {
+#pragma unroll
+    for (int i = 0; i < G::TK / 32; ++i) {
+      const int j = r0 + lane + 32 * i;
+      if (!INNER && !(j < r.n && (j < r.vis.s1 || j >= r.vis.w0))) pv[i][0] = pv[i][1] = pv[i][2] = pv[i][3] = 0u;
+      most = max_half2(most, max_half2(max_half2(pv[i][0], pv[i][1]), max_half2(pv[i][2], pv[i][3])));
+    }
+    most &= 0xffffu;
+    if (__any_sync(FULL_MASK, mx0 > m0 || mx1 > m1 || most >= lim)) {
 #pragma unroll
       for (int k = 4; k <= 16; k <<= 1) {
         mx0 = fmaxf(mx0, __shfl_xor_sync(FULL_MASK, mx0, k));
         mx1 = fmaxf(mx1, __shfl_xor_sync(FULL_MASK, mx1, k));
       }
-      const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-      const float a0 = n0 == NEG_INF ? 1.f : fast_exp2(m0 - n0), a1 = n1 == NEG_INF ? 1.f : fast_exp2(m1 - n1);
+      // (a scale that is new is 2^-10 at least; infinite ones stay as they are)
+      const uint32_t next = max(lim, (min(__reduce_max_sync(FULL_MASK, most) >> 10, 30u) + 1) << 10);
+      const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1), ak = __uint_as_float((127 + (lim >> 10) - (next >> 10)) << 23);
+      float a0 = n0 == NEG_INF ? 1.f : fast_exp2(m0 - n0), a1 = n1 == NEG_INF ? 1.f : fast_exp2(m1 - n1);
       m0 = n0;
       m1 = n1;
+      lim = next;
       l0 *= a0;
       l1 *= a1;
+      om[0] *= a0;
+      om[1] *= a1;
+      a0 *= ak;
+      a1 *= ak;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         o[i][0] *= a0;
@@ -371,9 +407,23 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
         o[i][2] *= a0;
         o[i][3] *= a1;
       }
-      om[0] *= a0;
-      om[1] *= a1;
     }
+    // two rows' words of scales go to the pairs of the even row, those of minima to the odd one's
+    const bool odd = lane & 1;
+    const uint32_t up = odd ? 0x3c003c00u : __byte_perm((35u << 10) - lim, 0, 0x1010);  // 2^k, minima as they are
+#pragma unroll
+    for (int i = 0; i < G::TK / 32; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t own = __byte_perm(pv[i][2 * k], pv[i][2 * k + 1], odd ? 0x7632 : 0x5410);
+        const uint32_t other = __shfl_xor_sync(FULL_MASK, __byte_perm(pv[i][2 * k], pv[i][2 * k + 1], odd ? 0x5410 : 0x7632), 1);
+        w[2 * k] = mul_half2(__byte_perm(own, other, odd ? 0x1054 : 0x5410), up);
+        w[2 * k + 1] = mul_half2(__byte_perm(own, other, odd ? 0x3276 : 0x7632), up);
+      }
+      sts4(tv + (lane + 32 * i) * G::ROW + CODES, w);
+    }
+    __syncwarp();  // (the pairs)
     const float z0 = !INNER && m0 == NEG_INF ? 0.f : m0, z1 = !INNER && m1 == NEG_INF ? 0.f : m1;
 #pragma unroll
     for (int s = 0; s < SUB; ++s) {
@@ -382,29 +432,17 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
       l0 += e[0] + e[2];
       l1 += e[1] + e[3];
       const uint32_t p01 = transpose8(pack_half(e[0], e[1])), p89 = transpose8(pack_half(e[2], e[3]));  // rows 2 lt, + 1, + 8, + 9; head lg
-      uint32_t vw[4][NWD], vp[4][4], vm[4];
+      uint32_t vw[4][NWD], b0[4], b1[4];
+      const uint32_t ra = tv + (16 * s + 2 * lt) * G::ROW;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int row = 16 * s + 2 * lt + (k & 1) + 8 * (k >> 1);
-        const uint32_t a = tv + row * G::ROW;
-        lds_words(a + LANE * (lg & 3), vw[k]);
-        lds_words(a + CODES, vp[k]);
-        vm[k] = lds32(a + CODES + 4 * (lg & 3));
-        if (!INNER) {
-          const int j = r0 + row;
-          if (!(j < r.n && (j < r.vis.s1 || j >= r.vis.w0))) {
-            vm[k] = 0u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) vp[k][i] = 0u;
-          }
-        }
-      }
-      mma16816h(om, __byte_perm(vm[0], vm[1], 0x7632), 0u, __byte_perm(vm[2], vm[3], 0x7632), 0u, p01, p89);
-      uint32_t b0[4], b1[4];
+      for (int k = 0; k < 4; ++k) lds_words(ra + ((k & 1) + 8 * (k >> 1)) * G::ROW + LANE * (lg & 3), vw[k]);
+      lds_words(ra + CODES, b0);
+      lds_words(ra + 8 * G::ROW + CODES, b1);
+      mma16816h(om, lds32(ra + G::ROW + CODES + 4 * (lg & 3)), 0u, lds32(ra + 9 * G::ROW + CODES + 4 * (lg & 3)), 0u, p01, p89);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        b0[j] = mul_half2(p01, __byte_perm(vp[0][j], vp[1][j], 0x5410));
-        b1[j] = mul_half2(p89, __byte_perm(vp[2][j], vp[3][j], 0x5410));
+        b0[j] = mul_half2(p01, b0[j]);
+        b1[j] = mul_half2(p89, b1[j]);
       }
 #pragma unroll
       for (int k = 0; k < NWD; ++k) {
@@ -457,6 +495,7 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
   }
   // every ring is idle: the warps' vector sums go there
   const bool bad = __syncthreads_or(!blocks_ok);
+  const float down = __uint_as_float((127 - 20 + (lim >> 10)) << 23);  // 2^-k
   float* so = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -468,7 +507,7 @@ __global__ void __launch_bounds__(NW * 32, 4) decode_q4_kernel(const __grid_cons
       const float(&y)[4] = o[j * (D / 64) + i];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        so[(w * 8 + 2 * lt + (c & 1)) * RunSums<D>::HS + e + (c >> 1)] = fmaf(y[c], c < 2 ? 0x1p24f : 0x1p20f, (c & 1) ? a1 : a0);
+        so[(w * 8 + 2 * lt + (c & 1)) * RunSums<D>::HS + e + (c >> 1)] = fmaf(y[c], (c < 2 ? 0x1p24f : 0x1p20f) * down, (c & 1) ? a1 : a0);
     }
   }
   finish_run<Q4Tag, D, CHUNK>(p, r, tl, ls, split, pi, bad, so, sm_m, sm_l, run_ml);

@@ -1,5 +1,6 @@
 """Attention over 4-bit caches (tri_attn_decode, and chunks of few tokens) at sizes of V and of the
-logits where numbers of few bits could lose it: logits of 2^17 with the largest scales.
+logits where numbers of few bits could lose it: small V under a row that dominates, scales of very
+different sizes, logits of 2^17 with the largest scales.
 
 Tolerances as in test_gpu_q4.py: A = sum w (s c + |m|); 2^-10 of A for the weights' two roundings to fp16, 2 ew of it for
 the logits, n 2^-24 of it for fp32 sums, half a step of the result. Without that file's term for fp16's subnormal
@@ -69,6 +70,63 @@ def check(c, q, sc, n_q):
 
 def queries(rng, n_q, heads, d):
     return f64(torch.from_numpy(rng.normal(size=(max(n_q, 1), heads, d))).bfloat16())
+
+
+def dominated(rng, q, lens, gap, small):
+    """K with a first row `gap` above the rest in the logit of every query of the slice (which are one vector), V with a
+    first row `small` times the others; scale d^-1/2."""
+    H, d = len(lens), q.shape[-1]
+    k = [rng.normal(size=(n, d)) for n in lens]
+    v = [rng.normal(size=(n, d)) for n in lens]
+    for h in range(H):
+        u = q[0, h * (q.shape[1] // H)]
+        k[h][0] = u * gap * d ** 0.5 / (u @ u)
+        v[h][0] *= small
+    return k, v
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n_q", [0, 3])  # one new token; a chunk
+@pytest.mark.parametrize("size,gap,small", [(1e-2, 14, 1e-2), (1e-3, 14, 1e-3), (1e-4, 12, 1.0), (1e-4, 12, 1e-3), (1.0, 20, 1e-3), (1e-4, 0, 1.0),
+                                            (300.0, 14, 1e-2)])
+def test_a_row_that_dominates(d, n_q, size, gap, small):
+    rng = np.random.default_rng(int(gap) + d)
+    lens, G = [64, 700], 2
+    q = queries(rng, 1, 2, d)[:, [0, 0, 1, 1]]
+    q = np.repeat(q, max(n_q, 1), 0)
+    k, v = dominated(rng, q, lens, gap, small)
+    check(Values(k, [x * size for x in v], d, block=16 if n_q else 0), q, d ** -0.5, n_q)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n_q", [0, 2])
+@pytest.mark.parametrize("order", [1, -1])
+def test_scales_that_grow_and_shrink(d, n_q, order):
+    # V from 2^-12 to 2^7 along the rows, or the other way round; logits that make up for it, so that every size counts
+    rng = np.random.default_rng(d)
+    n, H = 600, 2
+    q = queries(rng, 1, H, d)
+    q = np.repeat(q, max(n_q, 1), 0)
+    e = np.linspace(-12, 7, n)[::order]
+    k, v = [], []
+    for h in range(H):
+        u = q[0, h]
+        x = rng.normal(size=(n, d)) * 0.3
+        k.append(x + np.outer(-e * np.log(2.0) * d ** 0.5 / (u @ u), u))
+        v.append(rng.normal(size=(n, d)) * 2.0 ** e[:, None])
+    check(Values(k, v, d), q, d ** -0.5, n_q)
+
+
+@pytest.mark.parametrize("n_q", [0, 3])
+def test_zero_and_missing_scales(n_q):
+    # constant quarters (scale 0), and rows of zeros between others
+    rng = np.random.default_rng(3)
+    d, n = 64, 200
+    q = queries(rng, n_q, 2, d)
+    k = [rng.normal(size=(n, d)) for _ in range(2)]
+    v = [np.repeat(rng.normal(size=(n, 4)), d // 4, 1), np.where(np.arange(n)[:, None] % 3 == 0, 0.0, 1e-5 * rng.normal(size=(n, d)))]
+    check(Values(k, v, d), q, d ** -0.5, n_q)
+    check(Values(k, [v[0], 0 * v[1]], d), q, d ** -0.5, n_q)
 
 
 @pytest.mark.parametrize("d", [64, 128])
