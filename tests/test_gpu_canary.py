@@ -312,3 +312,101 @@ def test_canary_paged_blocks_used():
     go.check(torch.ones(n_seq, dtype=torch.bool, device="cuda"), "tri_paged_blocks_used")
     most = nv.view(n_seq, -1).max(dim=1).values
     assert torch.equal(go.t, (most + bs - 1) // bs)
+
+
+def _rows4(shape, d, g):
+    """4-bit rows of random codes with small scales and minima."""
+    x = torch.randint(0, 256, (*shape, tri.q4_row_bytes(d)), generator=g, device="cuda", dtype=torch.uint8)
+    pairs = torch.rand(*shape, 4, 2, generator=g, device="cuda")
+    pairs[..., 1] -= 4
+    x[..., d // 2:] = pairs.half().view(*shape, 8).view(torch.uint8)
+    return x
+
+
+def _token_cache(dtype, d, seed, n_cap=150, lens=(0, 1, 33, 90, 110, 64)):
+    """2 sequences, 2 layers, 3 heads; the row counts of a layer's slices."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    shape = (2, 2, 3, n_cap)
+    k, v = (_rows4(shape, d, g) if dtype == torch.uint8 else torch.randn(*shape, d, generator=g, device="cuda").to(dtype) for _ in range(2))
+    nv = torch.tensor([*lens[:3], *lens[:3], *lens[3:], *lens[3:]], dtype=torch.int32)
+    pos = torch.arange(n_cap).expand(12, -1).int()
+    return GuardedCache(k, v, nv, pos=pos, post_rope=True), g
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32, torch.uint8])
+@pytest.mark.parametrize("d,n_q", [(64, 1), (64, 4), (128, 37)])
+def test_canary_append(dtype, d, n_q):
+    c, g = _token_cache(dtype, d, n_q)
+    H, Hq, layer, news = 3, 6, 1, [n_q, n_q // 2]
+    dt = torch.bfloat16 if dtype == torch.uint8 else dtype
+    gx = Guarded((2, n_q, (Hq + 2 * H) * d), dt, torch.randn(2, n_q, (Hq + 2 * H) * d, generator=g, device="cuda"))
+    q, k, v = (x.unflatten(-1, (-1, d)) for x in gx.t.split((Hq * d, H * d, H * d), dim=-1))
+    go = Guarded((2, n_q, Hq, d), dt)
+    gp = Guarded((2, n_q), torch.int32, torch.randint(0, 1000, (2, n_q)).int())
+    gnew = Guarded((2,), torch.int32, torch.tensor(news, dtype=torch.int32))
+    tri.append(c.kv, layer, k, v, gp.t, 1e4, q=q, q_out=go.t, n_new=gnew.t)
+    for x, what in ((gx, "projection"), (gp, "positions"), (gnew, "n_new")):
+        x.check(None, f"tri_append {what}")
+    live = torch.arange(n_q, device="cuda") < torch.tensor(news, device="cuda")[:, None]
+    go.check(live[:, :, None, None].expand(go.shape), "tri_append q_out")
+    # the new rows of the layer's slices, their positions and row counts
+    n0 = torch.from_numpy(c.nv0).cuda()[:, None]
+    s = torch.arange(12, device="cuda")
+    more = torch.where(s // 3 % 2 == layer, torch.tensor(news, device="cuda")[s // 6], 0)[:, None]
+    j = torch.arange(c.n_cap + GAP, device="cuda")[None]
+    new = (j >= n0) & (j < n0 + more)
+    for x in (c.gk, c.gv):
+        x.check(new.view(2, 2, 3, -1, 1).expand(x.shape), "tri_append rows")
+    c.gpos.check(new[:, :c.n_cap], "tri_append pos")
+    c.gn.check(more[:, 0] > 0, "tri_append n_valid")
+    c.gpo.check(None, "tri_append pos_out")
+    assert int(c.gst.t.item()) == 0 and torch.equal(c.gn.t, (n0 + more)[:, 0].int())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_canary_read_rows(d):
+    c, _ = _token_cache(torch.uint8, d, d)
+    gk, gv = Guarded((2, 3, c.n_cap, d), torch.bfloat16), Guarded((2, 3, c.n_cap, d), torch.bfloat16)
+    tri.read_rows(c.kv, 0, gk.t, gv.t)
+    n = torch.from_numpy(c.nv0).cuda().view(2, 2, 3)[:, 0]
+    live = torch.arange(c.n_cap, device="cuda") < n[..., None]
+    for x in (gk, gv):
+        x.check(live[..., None].expand(x.shape), "tri_read_rows")
+    c.check_untouched("tri_read_rows")
+
+
+@pytest.mark.parametrize("d,group,n_q", [(64, 2, 1), (128, 4, 5), (64, 3, 40), (128, 4, 70)])  # rows read, and written out
+def test_canary_chunks_over_4_bits(d, group, n_q):
+    c, g = _token_cache(torch.uint8, d, n_q)
+    Hq, news = 3 * group, [n_q, (n_q + 1) // 2]
+    gq = Guarded((2, n_q, Hq, d), torch.bfloat16, torch.randn(2, n_q, Hq, d, generator=g, device="cuda"))
+    go, gl = Guarded((2, n_q, Hq, d), torch.bfloat16), Guarded((2, n_q, Hq), torch.float32)
+    gnew = Guarded((2,), torch.int32, torch.tensor(news, dtype=torch.int32))
+    gw = Guarded((tri.attn_prefill_workspace_bytes(c.kv),), torch.uint8)
+    tri.attn_prefill(c.kv, 1, gq.t, go.t, n_new=gnew.t, lse=gl.t, workspace=gw.t)
+    gq.check(None, "tri_attn_prefill_q4 queries")
+    gnew.check(None, "tri_attn_prefill_q4 n_new")
+    gw.check(torch.ones(gw.shape, dtype=torch.bool, device="cuda"), "tri_attn_prefill_q4 workspace")
+    live = torch.arange(n_q, device="cuda") < torch.tensor(news, device="cuda")[:, None]
+    go.check(live[:, :, None, None].expand(go.shape), "tri_attn_prefill_q4 out")
+    gl.check(live[:, :, None].expand(gl.shape), "tri_attn_prefill_q4 lse")
+    c.check_untouched("tri_attn_prefill_q4")
+
+
+@pytest.mark.parametrize("d,group", [(64, 1), (128, 4), (128, 7)])
+def test_canary_decode_over_4_bits(d, group):
+    c, g = _token_cache(torch.uint8, d, group)
+    Hq = 3 * group
+    gq = Guarded((2, Hq, d), torch.bfloat16, torch.randn(2, Hq, d, generator=g, device="cuda"))
+    go, gl = Guarded((2, Hq, d), torch.bfloat16), Guarded((2, Hq), torch.float32)
+    gm = Guarded((12, c.n_cap), torch.float32, torch.zeros(12, c.n_cap))
+    gw = Guarded((tri.attn_decode_workspace_bytes(c.kv, group, True),), torch.uint8)
+    tri.attn_decode(c.kv, 1, gq.t, go.t, n_sink=2, window=20, lse=gl.t, mass=gm.t, workspace=gw.t)
+    gq.check(None, "tri_attn_decode queries")
+    for x, what in ((gw, "workspace"), (go, "out"), (gl, "lse")):
+        x.check(torch.ones(x.shape, dtype=torch.bool, device="cuda"), f"tri_attn_decode {what}")
+    n = torch.from_numpy(c.nv0).cuda()[:, None]
+    j = torch.arange(c.n_cap, device="cuda")[None]
+    seen = (j < n) & ((j < 2) | (j >= n - 20)) & (torch.arange(12, device="cuda")[:, None] // 3 % 2 == 1)
+    gm.check(seen, "tri_attn_decode mass")
+    c.check_untouched("tri_attn_decode")
