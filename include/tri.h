@@ -465,8 +465,8 @@ typedef struct {
  * aligned, no initial contents needed; calls that may overlap need one each.
  * 4-bit caches: products of the codes are exact; weights are rounded to fp16, and
  * again with V's scales, for their product with V: each time by 2^-11 of themselves,
- * or 2^-36 of the query's largest weight (times the largest value of V) where that is
- * more. Elements of q stay below 2^115 in magnitude.
+ * or 2^-36 of the query's largest weight (times the largest value of V, 2^-11 at
+ * least) where that is more. Elements of q stay below 2^115 in magnitude.
  * A slice with a fault (row count, block table, n_new) is skipped. */
 size_t tri_attn_decode_workspace_bytes(const tri_kv* kv, int32_t group, int32_t with_mass);
 tri_status tri_attn_decode(const tri_kv* kv, const tri_queries* q, void* out, float* lse, float* mass, void* ws,
@@ -498,18 +498,25 @@ tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* ls
  * TRI_ERR_UNSUPPORTED otherwise). The rows that some query may see are first
  * written to ws, the values of K as a pair of bf16, those of V in fp16; the kernel
  * then reads those. Weights are rounded to fp16 for their product with V (their sum
- * is not): by 2^-11 of themselves, or 2^-31 of the query's largest where that is more. Calls of few tokens (n_q up to 8 t, t the whole part of 8 / group: a
- * draft's tokens for instance) read the 4-bit rows themselves, as tri_attn_decode
- * does, t tokens at a time. ws: device scratch of
- * tri_attn_prefill_q4_workspace_bytes(kv) bytes (one layer's rows, 6 head_dim bytes
- * each, or what those calls need), 16-byte aligned, no initial contents needed;
- * calls that may overlap need one each. A sequence with a fault in n_new is skipped;
- * one with a bad table entry of a block that one of its queries sees is skipped as
- * a whole, in calls of few tokens each head's t tokens (from token 0 on) of which one
- * sees it; a bad row count leaves out its slice. */
+ * is not): by 2^-11 of themselves, or 2^-31 of the query's largest where that is more.
+ * Calls of few tokens (n_q up to 8 t, t the whole part of 8 / group: a draft's tokens
+ * for instance) read the 4-bit rows themselves, as tri_attn_decode does, t tokens at
+ * a time. ws: device scratch of tri_attn_prefill_q4_workspace_bytes(kv) bytes (one
+ * layer's rows, 6 head_dim bytes each, or what those calls need), 16-byte aligned, no
+ * initial contents needed; calls that may overlap need one each. A sequence with a
+ * fault in n_new is skipped; one with a bad table entry of a block that one of its
+ * queries sees is skipped as a whole, in calls of few tokens each head's t tokens
+ * (from token 0 on) of which one sees it; a bad row count leaves out its slice.
+ * tri_attn_prefill_q4_few -- the same for calls of few tokens alone (other ones:
+ * TRI_ERR_UNSUPPORTED), with the scratch that such a call needs, which does not grow
+ * with the cache: tri_attn_prefill_q4_few_workspace_bytes(kv, q) bytes, 0 if the call
+ * is none of few tokens (or not a call: a bad argument). */
 size_t tri_attn_prefill_q4_workspace_bytes(const tri_kv* kv);
 tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out, float* lse, void* ws, size_t ws_bytes,
                                tri_stream_t stream);
+size_t tri_attn_prefill_q4_few_workspace_bytes(const tri_kv* kv, const tri_queries* q);
+tri_status tri_attn_prefill_q4_few(const tri_kv* kv, const tri_queries* q, void* out, float* lse, void* ws, size_t ws_bytes,
+                                   tri_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * tri_append -- new tokens into one layer of the cache, rotated on the way.

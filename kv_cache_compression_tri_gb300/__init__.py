@@ -165,6 +165,10 @@ def load_library():
         lib.tri_attn_prefill_q4_workspace_bytes.restype = ctypes.c_size_t
         lib.tri_attn_prefill_q4.argtypes = [kvp, qp, vp, vp, vp, ctypes.c_size_t, vp]
         lib.tri_attn_prefill_q4.restype = ctypes.c_int
+        lib.tri_attn_prefill_q4_few_workspace_bytes.argtypes = [kvp, qp]
+        lib.tri_attn_prefill_q4_few_workspace_bytes.restype = ctypes.c_size_t
+        lib.tri_attn_prefill_q4_few.argtypes = [kvp, qp, vp, vp, vp, ctypes.c_size_t, vp]
+        lib.tri_attn_prefill_q4_few.restype = ctypes.c_int
         lib.tri_append.argtypes = [kvp, ctypes.POINTER(_TriTokens), vp]
         lib.tri_append.restype = ctypes.c_int
         lib.tri_read_rows.argtypes = [kvp, i32, vp, vp, vp]
@@ -703,10 +707,16 @@ def attn_decode(kv, layer: int, q: torch.Tensor, out: torch.Tensor, n_new: torch
     return out
 
 
-def attn_prefill_workspace_bytes(kv) -> int:
-    """Scratch of attn_prefill: one layer's rows written out for a 4-bit cache, none otherwise."""
-    kvs = kv._abi()
-    return int(load_library().tri_attn_prefill_q4_workspace_bytes(ctypes.byref(kvs)))
+def attn_prefill_workspace_bytes(kv, q: torch.Tensor | None = None, n_sink: int = 0, window: int = 0) -> int:
+    """Scratch of attn_prefill: one layer's rows written out for a 4-bit cache, none otherwise. q (with the call's n_sink
+    and window): what a call with these queries needs, much less where they are few tokens."""
+    lib, kvs = load_library(), kv._abi()
+    if q is not None and kvs.dtype == Q4:
+        few = lib.tri_attn_prefill_q4_few_workspace_bytes(
+            ctypes.byref(kvs), ctypes.byref(_queries(kvs, kv, 0, q, q.shape, q.stride(), None, None, n_sink, window)))
+        if few:
+            return int(few)
+    return int(lib.tri_attn_prefill_q4_workspace_bytes(ctypes.byref(kvs)))
 
 
 def attn_prefill(kv, layer: int, q: torch.Tensor, out: torch.Tensor, n_new: torch.Tensor | None = None,
@@ -717,7 +727,7 @@ def attn_prefill(kv, layer: int, q: torch.Tensor, out: torch.Tensor, n_new: torc
     newest rows they are (tri_attn_prefill): out [n_seq, n_q, Hq, d]; lse
     [n_seq, n_q, Hq] fp32. n_new [n_seq] int32: tokens of each sequence (rows of
     out past them stay as they were). A 4-bit cache (tri_attn_prefill_q4) needs
-    attn_prefill_workspace_bytes(kv) of workspace."""
+    attn_prefill_workspace_bytes(kv, q, n_sink, window) of workspace."""
     lib = load_library()
     kvs = kv._abi()
     shape = q.shape
@@ -726,11 +736,13 @@ def attn_prefill(kv, layer: int, q: torch.Tensor, out: torch.Tensor, n_new: torc
     if lse is not None:
         assert lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == shape[:3]
     if kvs.dtype == Q4:
+        few = lib.tri_attn_prefill_q4_few_workspace_bytes(ctypes.byref(kvs), ctypes.byref(qs))
         if workspace is None:
-            workspace = _scratch(int(lib.tri_attn_prefill_q4_workspace_bytes(ctypes.byref(kvs))), kv.device, stream)
+            workspace = _scratch(int(few or lib.tri_attn_prefill_q4_workspace_bytes(ctypes.byref(kvs))), kv.device, stream)
         assert workspace.is_cuda and workspace.is_contiguous()
-        _check("tri_attn_prefill_q4", lib.tri_attn_prefill_q4(ctypes.byref(kvs), ctypes.byref(qs), out.data_ptr(), _ptr(lse),
-                                                              workspace.data_ptr(), workspace.nbytes, _stream(stream)))
+        call = lib.tri_attn_prefill_q4_few if few else lib.tri_attn_prefill_q4
+        _check("tri_attn_prefill_q4", call(ctypes.byref(kvs), ctypes.byref(qs), out.data_ptr(), _ptr(lse), workspace.data_ptr(),
+                                           workspace.nbytes, _stream(stream)))
         return out
     _check("tri_attn_prefill", lib.tri_attn_prefill(ctypes.byref(kvs), ctypes.byref(qs), out.data_ptr(), _ptr(lse),
                                                     _stream(stream)))

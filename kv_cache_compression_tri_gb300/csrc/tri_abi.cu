@@ -663,9 +663,8 @@ DecodeWs decode_ws(const tri_kv* kv, int32_t group, int32_t n_split, bool with_m
   return w;
 }
 
-// A chunk over a 4-bit cache takes the decode kernel for up to so many passes of 8 columns over its rows. Passes against
-// rows written out (us): 16 x 8 x 32768 rows, d 128, group 4: 1 pass 120, 2 214, 4 408, 8 784, written out 1023; 8 x 2113
-// rows: 13, 15, 17, 17 and 20 to 22; 64 x 8 x 2176 rows, d 64, group 1: 34, 53, 95, 175 and 165.
+// A chunk of few tokens over a 4-bit cache takes the decode kernel, which has 8 columns for query rows, in passes over
+// the 4-bit rows: at most so many.
 constexpr int MAX_PASSES = 8;
 
 // Workspace of tri_attn_prefill_q4: one layer's rows, [n_seq][n_kv_heads][n_cap][d] K, what its rounding left, and V
@@ -696,6 +695,34 @@ Q4RowsParams q4_rows_params(const tri_kv* kv, int32_t layer) {
   r.n_kv_heads = kv->n_kv_heads;
   r.layer = layer;
   return r;
+}
+
+// A chunk's passes of the decode kernel (p's fields of a chunk and of the runs), and the rows that one of them sees at most;
+// false if the rows are to be written out.
+bool few_tokens(const tri_kv* kv, const tri_queries* q, AttnParams& p, int& rows) {
+  const int per = MAX_GROUP / q->group;
+  const int64_t passes = (static_cast<int64_t>(q->n_q) + per - 1) / per;
+  const int64_t slices = static_cast<int64_t>(kv->n_seq) * kv->n_kv_heads * passes;
+  if (passes > MAX_PASSES || slices * std::max<int64_t>(16, kv->n_cap / 1024 + 1) > 0x7fffffff) return false;
+  const int64_t seen = static_cast<int64_t>(q->n_sink) + q->window + q->n_q - 1;
+  rows = q->window == 0 ? kv->n_cap : static_cast<int>(std::min<int64_t>(kv->n_cap, seen));
+  const DecodePlan plan = attn_decode_plan(static_cast<int>(slices), rows, kv->dtype);
+  p.token_heads = q->group;
+  p.pass_tokens = std::min(q->n_q, per);
+  p.passes = static_cast<int32_t>(passes);
+  p.group = p.pass_tokens * q->group;
+  p.n_split = plan.n_split;
+  p.join = plan.join;
+  return true;
+}
+
+tri_status run_few_tokens(const tri_kv* kv, AttnParams& p, int rows, void* out, float* lse, void* ws, tri_stream_t stream) {
+  const size_t parts = static_cast<size_t>(kv->n_seq) * kv->n_kv_heads * p.passes * p.n_split;
+  p.part_o = static_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + decode_parts(kv, p.group, parts));
+  p.out = out;
+  p.lse = lse;
+  return launch_attn_decode(p, rows, kv->dtype, kv->head_dim, stream) == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
 }
 
 }  // namespace
@@ -768,27 +795,8 @@ tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out
   if (kv->dtype != TRI_Q4) return TRI_ERR_UNSUPPORTED;
   if (!out || !aligned(out, 16) || (lse && !aligned(lse, 4))) return TRI_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 16) || ws_bytes < tri_attn_prefill_q4_workspace_bytes(kv)) return TRI_ERR_INVALID_ARG;
-  const int64_t passes = (q->n_q + MAX_GROUP / q->group - 1) / (MAX_GROUP / q->group);
-  const int64_t slices = static_cast<int64_t>(kv->n_seq) * kv->n_kv_heads * passes;
-  if (passes <= MAX_PASSES && slices * std::max<int64_t>(16, kv->n_cap / 1024 + 1) <= 0x7fffffff) {
-    // so few query rows that the decode kernel, which has 8 columns for them, reads the 4-bit rows in less time
-    // than writing them out and reading that takes
-    const int n = static_cast<int>(slices);
-    const int64_t seen = static_cast<int64_t>(q->n_sink) + q->window + q->n_q - 1;
-    const int rows = q->window == 0 ? kv->n_cap : static_cast<int>(std::min<int64_t>(kv->n_cap, seen));
-    const DecodePlan plan = attn_decode_plan(n, rows, kv->dtype);
-    p.token_heads = q->group;
-    p.pass_tokens = std::min(q->n_q, MAX_GROUP / q->group);
-    p.passes = static_cast<int32_t>(passes);
-    p.group = p.pass_tokens * q->group;
-    p.n_split = plan.n_split;
-    p.join = plan.join;
-    p.part_o = static_cast<float*>(ws);
-    p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + decode_parts(kv, p.group, slices * p.n_split));
-    p.out = out;
-    p.lse = lse;
-    return launch_attn_decode(p, rows, kv->dtype, kv->head_dim, stream) == cudaSuccess ? TRI_OK : TRI_ERR_CUDA;
-  }
+  int rows;
+  if (few_tokens(kv, q, p, rows)) return run_few_tokens(kv, p, rows, out, lse, ws, stream);
   const Q4Ws w = q4_ws(kv);
   // more rows than the attention's copies can number are refused before anything is enqueued
   if (static_cast<int64_t>(kv->n_seq) * kv->n_kv_heads * kv->n_cap > 0x7fffffff - 256) return TRI_ERR_UNSUPPORTED;
@@ -820,6 +828,27 @@ tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out
   p.out = out;
   p.lse = lse;
   return attn_status(launch_attn_prefill(p, TRI_Q4, kv->head_dim, stream));
+}
+
+size_t tri_attn_prefill_q4_few_workspace_bytes(const tri_kv* kv, const tri_queries* q) {
+  AttnParams p;
+  int rows;
+  if (prepare_attn(kv, q, p, true) != TRI_OK || kv->dtype != TRI_Q4 || !few_tokens(kv, q, p, rows)) return 0;
+  const size_t parts = p.join ? 0 : static_cast<size_t>(kv->n_seq) * kv->n_kv_heads * p.passes * p.n_split;
+  return std::max<size_t>(16, decode_parts(kv, p.group, parts) + align16(parts * p.group * sizeof(float2)));
+}
+
+tri_status tri_attn_prefill_q4_few(const tri_kv* kv, const tri_queries* q, void* out, float* lse, void* ws, size_t ws_bytes,
+                                   tri_stream_t stream) {
+  TRI_CALL_RANGE();
+  AttnParams p;
+  const tri_status st = prepare_attn(kv, q, p, true);
+  if (st != TRI_OK) return st;
+  int rows;
+  if (kv->dtype != TRI_Q4 || !few_tokens(kv, q, p, rows)) return TRI_ERR_UNSUPPORTED;
+  if (!out || !aligned(out, 16) || (lse && !aligned(lse, 4))) return TRI_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 16) || ws_bytes < tri_attn_prefill_q4_few_workspace_bytes(kv, q)) return TRI_ERR_INVALID_ARG;
+  return run_few_tokens(kv, p, rows, out, lse, ws, stream);
 }
 
 tri_status tri_read_rows(const tri_kv* kv, int32_t layer, void* k_out, void* v_out, tri_stream_t stream) {

@@ -112,3 +112,38 @@ def test_append_several_tokens_and_head_tiles_per_cta():
     c = Cache([[3 * h for h in range(20)]], 64, Q4, 704, L=1)  # 16 heads, and 4
     check(c, 613, 1, layer=0, n_new=[611])
     assert int(c.status) == 0
+
+
+@pytest.mark.parametrize("lens,d,group,n_q,n_sink,window", [([[700, 33]], 64, 4, 3, 0, 0), ([[20000]], 128, 2, 9, 0, 0), ([[9000, 8800]] * 8, 64, 1, 30, 0, 0),
+                                                            ([[5000, 4990]], 128, 4, 16, 7, 3000), ([[200] * 6] * 9, 64, 8, 5, 0, 50)])
+def test_scratch_of_few_tokens(lens, d, group, n_q, n_sink, window):
+    c = Case(lens, d, L=1, block=64)
+    q = torch.randn(c.B, n_q, c.H * group, d, device="cuda").bfloat16()
+    need, full = tri.attn_prefill_workspace_bytes(c.kv, q, n_sink, window), tri.attn_prefill_workspace_bytes(c.kv)
+    assert 16 <= need <= full
+    outs = []
+    for size in (need, full, None):
+        out, lse = torch.full_like(q, 9.0), torch.full(q.shape[:3], 9.0, device="cuda")
+        ws = None if size is None else torch.full((size + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+        tri.attn_prefill(c.kv, 0, q, out, n_sink=n_sink, window=window, lse=lse, workspace=None if size is None else ws[:size])
+        c.ok()
+        assert size is None or bool((ws[size:] == 0xA5).all())
+        outs.append((out, lse))
+    assert all(torch.equal(a, b) for o in outs[1:] for a, b in zip(outs[0], o))
+
+
+def test_few_tokens_over_a_large_cache_need_little_memory():
+    n_cap = 1 << 17  # 1.3 GB of rows, 6.4 GB if they were written out
+    k = torch.zeros(8, 1, 8, n_cap, 80, dtype=torch.uint8, device="cuda")
+    nv = torch.full((64,), 100, dtype=torch.int32, device="cuda")
+    kv = tri.KVCache(k, k, nv, None, None, torch.zeros(1, dtype=torch.int32, device="cuda"), post_rope=True)
+    q = torch.randn(8, 2, 32, 128, device="cuda").bfloat16()
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    tri.attn_prefill(kv, 0, q, out)
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() - before < 16 << 20
+    assert not bool(out.any())

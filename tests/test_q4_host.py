@@ -174,3 +174,46 @@ def test_more_than_a_launch_counts(lib):  # noqa: F811
     assert _append(lib, _kv(**many), tok) == UNSUPPORTED
     assert lib.tri_read_rows(ctypes.byref(_kv(**dict(Q4, n_seq=1 << 24, n_kv_heads=64, n_cap=1 << 20, slice_stride=48 << 20))), 0, 0x30000, None,
                              None) == UNSUPPORTED
+
+
+def _few(lib, kv, q):  # noqa: F811
+    return lib.tri_attn_prefill_q4_few_workspace_bytes(ctypes.byref(kv), ctypes.byref(q))
+
+
+def _few_call(lib, kv, q, **o):  # noqa: F811
+    return lib.tri_attn_prefill_q4_few(ctypes.byref(kv), ctypes.byref(q), o.get("out", 0x30000), o.get("lse"), o.get("ws", 0x40000),
+                                       o.get("ws_bytes", 1 << 40), None)
+
+
+def test_scratch_of_few_tokens_does_not_grow_with_the_cache(lib):  # noqa: F811
+    q = lambda n, group=4: _q(n_q=n, group=group, seq_stride=n * 8 * group * 128, token_stride=8 * group * 128)
+    sizes = []
+    for n_cap in (4096, 32768, 1 << 20):
+        kv = _kv(dtype=2, key_layout=1, head_dim=128, n_seq=16, n_kv_heads=8, n_cap=n_cap, slice_stride=n_cap * 80)
+        few = [_few(lib, kv, q(n)) for n in (1, 2, 5, 16)]
+        # sums and (m, l) of at most 16 runs of 8 columns for each of the passes
+        assert all(0 < b <= 128 * passes * 16 * 8 * (128 * 4 + 8) for b, passes in zip(few, (1, 1, 3, 8))), few
+        full = lib.tri_attn_prefill_q4_workspace_bytes(ctypes.byref(kv))
+        assert full >= 6 * 128 * n_cap * 128 and max(few) <= full
+        assert _few(lib, kv, q(17)) == 0  # nine passes: written out
+        sizes.append(few[1])
+    assert sizes[1] == sizes[2] and sizes[1] <= 8 << 20, sizes
+
+
+@pytest.mark.parametrize("over,code", BAD_Q)
+def test_few_tokens_reject_bad_queries(lib, over, code):  # noqa: F811
+    kv, q = _kv(**Q4), _q(**over)
+    assert _few_call(lib, kv, q) == code and _few(lib, kv, q) == 0
+
+
+def test_few_tokens_reject_bad_buffers_and_other_calls(lib):  # noqa: F811
+    kv, q = _kv(**Q4), _q()
+    need = _few(lib, kv, q)
+    assert 16 <= need <= lib.tri_attn_prefill_q4_workspace_bytes(ctypes.byref(kv)) and need % 16 == 0
+    for o in (dict(out=None), dict(out=0x30004), dict(lse=0x50002), dict(ws=None), dict(ws=0x40008), dict(ws_bytes=need - 1)):
+        assert _few_call(lib, kv, q, **o) == INVALID
+    many = _q(n_q=100, token_stride=4 * 64)
+    assert _few(lib, kv, many) == 0 and _few_call(lib, kv, many) == UNSUPPORTED
+    for other in (_kv(key_layout=1), _kv(**dict(Q4, key_layout=0))):
+        assert _few(lib, other, q) == 0 and _few_call(lib, other, q) == UNSUPPORTED
+    assert lib.tri_attn_prefill_q4_few_workspace_bytes(None, None) == 0 and _few(lib, _kv(**dict(Q4, n_valid=None)), q) == 0
