@@ -499,9 +499,9 @@ tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* ls
  * written to ws, the values of K as a pair of bf16, those of V in fp16; the kernel
  * then reads those. Weights are rounded to fp16 for their product with V (their sum
  * is not): by 2^-11 of themselves, or 2^-31 of the query's largest where that is more.
- * Calls of few tokens (n_q up to 8 t, t the whole part of 8 / group: a draft's tokens
- * for instance) read the 4-bit rows themselves, as tri_attn_decode does, t tokens at
- * a time. ws: device scratch of tri_attn_prefill_q4_workspace_bytes(kv) bytes (one
+ * Calls of few tokens (a draft's for instance: n_q up to 8 t, t the whole part of
+ * 8 / group, of many sequences fewer where their slices are short) read the 4-bit
+ * rows themselves, as tri_attn_decode does, t tokens at a time. ws: device scratch of tri_attn_prefill_q4_workspace_bytes(kv) bytes (one
  * layer's rows, 6 head_dim bytes each, or what those calls need), 16-byte aligned, no
  * initial contents needed; calls that may overlap need one each. A sequence with a
  * fault in n_new is skipped; one with a bad table entry of a block that one of its
@@ -510,7 +510,8 @@ tri_status tri_attn_mass(const tri_kv* kv, const tri_queries* q, const float* ls
  * tri_attn_prefill_q4_few -- the same for calls of few tokens alone (other ones:
  * TRI_ERR_UNSUPPORTED), with the scratch that such a call needs, which does not grow
  * with the cache: tri_attn_prefill_q4_few_workspace_bytes(kv, q) bytes, 0 if the call
- * is none of few tokens (or not a call: a bad argument). */
+ * is none of few tokens (or not a call: a bad argument). Which calls are of few
+ * tokens follows from kv's sizes and q's n_q and group alone. */
 size_t tri_attn_prefill_q4_workspace_bytes(const tri_kv* kv);
 tri_status tri_attn_prefill_q4(const tri_kv* kv, const tri_queries* q, void* out, float* lse, void* ws, size_t ws_bytes,
                                tri_stream_t stream);

@@ -664,8 +664,29 @@ DecodeWs decode_ws(const tri_kv* kv, int32_t group, int32_t n_split, bool with_m
 }
 
 // A chunk of few tokens over a 4-bit cache takes the decode kernel, which has 8 columns for query rows, in passes over
-// the 4-bit rows: at most so many.
+// the 4-bit rows: at most so many. Passes that are all on the GPU at once cost little more than one; of many slices of
+// short rows a pass takes much of what writing the rows out does. Measured (us, group 1, so that a pass has 8 tokens; |: the rule
+// below goes no further; out: rows written out):
+//   d, slices x rows     2     3     4     5     6     7     8    out
+//    64,   64 x 1400    15    19    17    19    29    21    24     25
+//    64,  512 x  200    21 |  31    39    47    54    57    65     30
+//    64,  128 x  700    15    16    17 |  25    25    25    28     23
+//    64,  512 x 1400    39    57    72    89 | 105   119   134    113
+//    64,  256 x 2176    31    56    50    86    73    80 |  93     85
+//    64,  512 x 2176    52    75    93   113   134   152 | 171    164
+//    64,  512 x 4096    99   142   181   224   267 | 309   349    289
+//    64,  512 x 8192   154   225   287   357   427   497   560    548
+//   128,  512 x  200    31    41 |  54    66    76    82    94     56
+//   128,  256 x  700    26    37    41    54 |  62    66    76     64
+//   128,  256 x 1400    35    62    58    93    87 |  93   107    113
+//   128,  128 x 2176    31    45    47    71    76    83    76     83
+//   128, 1024 x 4096   271   402   527   658   783   914  1039   1036
 constexpr int MAX_PASSES = 8;
+int most_passes(int64_t slices, int n_cap, int head_dim) {
+  if (slices * MAX_PASSES <= 2 * 152) return MAX_PASSES;
+  if (head_dim == 128) return n_cap < 512 ? 3 : n_cap < 1024 ? 5 : n_cap < 2048 ? 6 : MAX_PASSES;
+  return n_cap < 512 ? 2 : n_cap < 1024 ? 4 : n_cap < 2048 ? 5 : n_cap < 4096 ? 7 : n_cap < 8192 ? 6 : MAX_PASSES;
+}
 
 // Workspace of tri_attn_prefill_q4: one layer's rows, [n_seq][n_kv_heads][n_cap][d] K, what its rounding left, and V
 // (16 bits each), its row counts [n_seq][n_kv_heads] and new tokens [n_seq] (each part 16-byte aligned).
@@ -702,8 +723,8 @@ Q4RowsParams q4_rows_params(const tri_kv* kv, int32_t layer) {
 bool few_tokens(const tri_kv* kv, const tri_queries* q, AttnParams& p, int& rows) {
   const int per = MAX_GROUP / q->group;
   const int64_t passes = (static_cast<int64_t>(q->n_q) + per - 1) / per;
-  const int64_t slices = static_cast<int64_t>(kv->n_seq) * kv->n_kv_heads * passes;
-  if (passes > MAX_PASSES || slices * std::max<int64_t>(16, kv->n_cap / 1024 + 1) > 0x7fffffff) return false;
+  const int64_t layer = static_cast<int64_t>(kv->n_seq) * kv->n_kv_heads, slices = layer * passes;
+  if (passes > most_passes(layer, kv->n_cap, kv->head_dim) || slices * std::max<int64_t>(16, kv->n_cap / 1024 + 1) > 0x7fffffff) return false;
   const int64_t seen = static_cast<int64_t>(q->n_sink) + q->window + q->n_q - 1;
   rows = q->window == 0 ? kv->n_cap : static_cast<int>(std::min<int64_t>(kv->n_cap, seen));
   const DecodePlan plan = attn_decode_plan(static_cast<int>(slices), rows, kv->dtype);

@@ -217,3 +217,14 @@ def test_few_tokens_reject_bad_buffers_and_other_calls(lib):  # noqa: F811
     for other in (_kv(key_layout=1), _kv(**dict(Q4, key_layout=0))):
         assert _few(lib, other, q) == 0 and _few_call(lib, other, q) == UNSUPPORTED
     assert lib.tri_attn_prefill_q4_few_workspace_bytes(None, None) == 0 and _few(lib, _kv(**dict(Q4, n_valid=None)), q) == 0
+
+
+@pytest.mark.parametrize("d,n_seq,n_cap,passes", [(64, 4, 200, 8), (64, 64, 200, 2), (64, 16, 700, 4), (64, 64, 1400, 5), (64, 64, 2176, 7), (64, 32, 4096, 6), (64, 64, 8192, 8),
+                                                  (128, 4, 200, 8), (128, 64, 200, 3), (128, 32, 700, 5), (128, 32, 1400, 6), (128, 16, 2176, 8)])
+def test_passes_that_are_of_few_tokens(lib, d, n_seq, n_cap, passes):  # noqa: F811
+    # 8 heads: slices and rows of which more passes were measured to take longer than rows written out
+    kv = _kv(dtype=2, key_layout=1, head_dim=d, n_seq=n_seq, n_kv_heads=8, n_cap=n_cap, slice_stride=n_cap * (d // 2 + 16))
+    for group, t in ((1, 8), (2, 4), (3, 2), (8, 1)):
+        q = lambda n: _q(n_q=n, group=group, seq_stride=n * 8 * group * d, token_stride=8 * group * d)
+        few = [n for n in range(1, 80) if _few(lib, kv, q(n)) > 0]
+        assert few == list(range(1, passes * t + 1))
