@@ -348,12 +348,8 @@ struct AttnParams {
   int64_t q_seq, q_token;          // elements between sequences and tokens
   const int32_t* n_new;            // [n_seq], or NULL: n_q
   int32_t n_q, group;
-  // decode kernels, a chunk of few tokens: the heads of a token (0: no chunk), the tokens of a pass (group = both), and
-  // how many passes there are, each like a slice of its own
-  int32_t token_heads, pass_tokens, passes;
   int32_t n_sink, window;
   float scale;                     // of q . k
-  const void* k_rest;              // 4-bit rows written out: K is a bf16 pair, v is fp16 (attn_prefill.cu)
   void* out;                       // [n_seq][n_q][n_kv_heads * group][head_dim]
   float* lse;                      // [n_seq][n_q][n_kv_heads * group], or NULL
   const float* lse_in;             // the weights' log-sums (attn_mass)
@@ -365,6 +361,12 @@ struct AttnParams {
   float* part_o;                   // [layer slices][n_split][group][head_dim]: sums of 2^(x - m) v
   float2* part_ml;                 // [layer slices][n_split][group]: m and sum of 2^(x - m); sum -1: skipped
   float* logits;                   // [layer slices][n_cap][group], visible rows (mass only)
+  // 4-bit caches (behind the rest: between, they moved fields that the bf16 prompt's kernel reads, and 8192
+  // tokens took 344.2 us for 342.3)
+  const void* k_rest;              // 4-bit rows written out: K is a bf16 pair, v is fp16 (attn_prefill.cu)
+  // a chunk of few tokens in the decode kernels: the heads of a token (0: no chunk), the tokens of a pass (group = both), and
+  // how many passes there are, each like a slice of its own
+  int32_t token_heads, pass_tokens, passes;
 };
 
 // New tokens into one layer's slices (append.cu).
