@@ -601,6 +601,7 @@ tri_status prepare_attn(const tri_kv* kv, const tri_queries* q, AttnParams& p, b
   const tri_status st = check_kv(kv, true, q4_ok);
   if (st != TRI_OK) return st;
   if (kv->key_layout != TRI_KEYS_POST_ROPE) return TRI_ERR_UNSUPPORTED;
+  if (kv->n_cap > 0x7fffffff - 256) return TRI_ERR_UNSUPPORTED;  // (the kernels add a tile's rows to a row)
   if (!q || !q->q || !aligned(q->q, 16)) return TRI_ERR_INVALID_ARG;
   if (q->n_q < 1 || q->n_q > 0x7fffffff - 256 || q->group < 1 || q->group > MAX_GROUP) return TRI_ERR_INVALID_ARG;
   if (q->layer < 0 || q->layer >= kv->n_layers) return TRI_ERR_INVALID_ARG;

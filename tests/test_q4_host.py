@@ -228,3 +228,11 @@ def test_passes_that_are_of_few_tokens(lib, d, n_seq, n_cap, passes):  # noqa: F
         q = lambda n: _q(n_q=n, group=group, seq_stride=n * 8 * group * d, token_stride=8 * group * d)
         few = [n for n in range(1, 80) if _few(lib, kv, q(n)) > 0]
         assert few == list(range(1, passes * t + 1))
+
+
+def test_attention_refuses_more_rows_than_it_counts(lib):  # noqa: F811
+    from test_attn_host import _calls
+    for n_cap in ((1 << 31) - 1, (1 << 31) - 64, (1 << 31) - 256):
+        kv = _kv(**dict(Q4, n_cap=n_cap, slice_stride=n_cap * 48))
+        assert list(_q4_calls(lib, kv, _q(), ws_bytes=1 << 62)) == [UNSUPPORTED] * 2 and _few(lib, kv, _q()) == 0
+        assert list(_calls(lib, _kv(key_layout=1, n_cap=n_cap, slice_stride=n_cap * 64), _q())) == [UNSUPPORTED] * 3
