@@ -431,9 +431,10 @@ tri_status tri_select_union(const float* scores, const tri_kv* kv, int32_t n_pro
  * An infinite V element of a row that a query sees gives infinity or NaN.
  *
  * n_cap is at most 2^31 - 257 (TRI_ERR_UNSUPPORTED otherwise). Pools, slices and
- * queries may be in any order and at any strides of whole 16 bytes; for tri_attn_prefill and tri_attn_mass of bf16 caches a layer's rows,
- * and for the latter the queries, lie within 2^31 - 256 rows (of head_dim) of
- * the first (TRI_ERR_UNSUPPORTED otherwise).
+ * queries may be in any order and at any strides of whole 16 bytes; for
+ * tri_attn_prefill and tri_attn_mass of bf16 caches a layer's rows, and for the
+ * latter the queries, lie within 2^31 - 256 rows (of head_dim) of the first
+ * (TRI_ERR_UNSUPPORTED otherwise).
  *
  * Keys are taken as cached, so they must be TRI_KEYS_POST_ROPE and q rotated
  * in the same way (TRI_ERR_UNSUPPORTED otherwise). Sums, maxima and lse are
