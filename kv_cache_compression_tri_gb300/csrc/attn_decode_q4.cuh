@@ -24,12 +24,12 @@
 //   spread. B = p (2^k s_j) in fp16: two roundings of 2^-11 of its weight, where results are
 //   rounded to 2^-8. p is up to 2^11 and 2^k s_j up to 2^5, k from the warp's largest scale so far (a
 //   larger one lowers it, and the sums so far with it), so that what falls to fp16's subnormal numbers
-//   and below is 2^-35 of the largest weight times the largest value. (With k 0 and p up to
-//   2^4, a row 14 above the others in the logit left these without their codes where V's
-//   elements were about 2^-10.) For this a lane per row reads the row's pairs in shared memory and puts
-//   them back as the products take them: two rows' scales, times 2^k, then two rows' minima. The
-//   quarter of the loads that this saves pays for it (16 x 8 x 32768 rows 119.8 us, without k 119.7, with the
-//   pairs left in their order 123.8).
+//   and below is 2^-36 of the largest weight times the largest value (2^-11 at least, as 2^k is an
+//   fp16 number too). (With k 0 and p up to 2^4, a row 14 above the others in the logit left these
+//   without their codes where V's elements were about 2^-10.) For this a lane per row reads the row's
+//   pairs in shared memory and puts them back as the products take them: two rows' scales, times
+//   2^k, then two rows' minima. The quarter of the loads that this saves pays for it (16 x 8 x 32768
+//   rows 119.8 us, without k 119.7, with the pairs left in their order 123.8).
 // Each warp owns a ring of NST tiles of 32 (d 64: 64) rows, K and V, filled by 16-byte asynchronous copies
 // of whole contiguous tiles (bulk copies by lanes of a warp took 20 instructions more per 16 rows
 // than these); table entries are read a tile ahead. Rows out of sight are copied but not

@@ -4,7 +4,8 @@ different sizes, logits of 2^17 with the largest scales.
 
 Tolerances as in test_gpu_q4.py: A = sum w (s c + |m|); 2^-10 of A for the weights' two roundings to fp16, 2 ew of it for
 the logits, n 2^-24 of it for fp32 sums, half a step of the result. Without that file's term for fp16's subnormal
-numbers: what falls among them is below 2^-35 of the largest weight times the largest s c + |m|, n 2^-35 of that in all.
+numbers: what falls among them is below 2^-35 of the largest weight times the largest s c + |m| (of 2^-11 and more: 2^k
+is at most 2^15), n 2^-35 of that in all.
 """
 import numpy as np
 import pytest
